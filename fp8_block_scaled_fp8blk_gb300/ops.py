@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -54,6 +55,17 @@ _lib.nvfp4_expert_gemv.restype = _INT
 _lib.nvfp4_expert_gemv.argtypes = [_P, _P, _P, _INT, _P, _INT, _P, _P, _I64, _I64, _P]
 _lib.mxfp4_expert_gemv.restype = _INT
 _lib.mxfp4_expert_gemv.argtypes = [_P, _P, _INT, _P, _INT, _P, _P, _I64, _I64, _P]
+_lib.fp8blk_kv_map.restype = _INT
+_lib.fp8blk_kv_map.argtypes = [_P] * 10 + [_INT] * 4 + [_I64, _P]
+_lib.fp8blk_kv_append.restype = _INT
+_lib.fp8blk_kv_append.argtypes = [_P, _P, _INT, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _INT, _INT, _INT, _P]
+_lib.fp8blk_kv_attn_ws_bytes.restype = ctypes.c_size_t
+_lib.fp8blk_kv_attn_ws_bytes.argtypes = [_INT] * 5
+_lib.fp8blk_kv_attn.restype = _INT
+_lib.fp8blk_kv_attn.argtypes = [_P, _INT] + [_P] * 10 + [ctypes.c_size_t, _INT, _INT, _I64, _INT, _INT, _INT, _INT, _I64,
+                                                       _INT, _I64, _I64, ctypes.c_float, _P]
+_lib.fp8blk_token_logprobs.restype = _INT
+_lib.fp8blk_token_logprobs.argtypes = [_P, _INT] + [_P] * 6 + [_I64, _I64, _I64, _INT, _P]
 _lib.fp8blk_set_launch_tuning.restype = _INT
 _lib.fp8blk_set_launch_tuning.argtypes = [_INT, _INT, _INT, _INT, _INT]
 _lib.fp8blk_set_m1_kernel.restype = _INT
@@ -73,6 +85,10 @@ _lib.fp8blk_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), _INT]
 OK, EINVAL, EALIGN, ESCALE, EWS, ECUDA, ERANGE = 0, 1, 2, 3, 4, 5, 6
 STATUS_WAIT_TIMEOUT = 1
 STATUS_BAD_EXPERT = 2
+STATUS_BAD_KV = 4
+STATUS_KV_EXHAUSTED = 8
+STATUS_BAD_TARGET = 16
+MAX_M, MAX_HEAD_DIM, MAX_TOP, MAX_VOCAB = 8, 256, 32, 262144
 
 
 class Fp8BlkError(RuntimeError):
@@ -267,6 +283,191 @@ def mxfp4_expert_gemv(codes: torch.Tensor, scales: torch.Tensor, ids: torch.Tens
     _check(_lib.mxfp4_expert_gemv(_ptr(codes), _ptr(scales), n_experts, _ptr(ids), n_active, _ptr(x), _ptr(y),
                                   rows, cols, _stream(x)), "mxfp4_expert_gemv")
     return y
+
+
+# ---------------------------------------------------------------- paged cache
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _dtype(t: torch.Tensor, what: str) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{what} must be float32 or bfloat16, not {t.dtype}")
+    return code
+
+
+def _typed(t: torch.Tensor, dtype: torch.dtype, what: str) -> int:
+    """Data pointer of a contiguous tensor of exactly this type."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows3(t: torch.Tensor, what: str) -> int:
+    """Row stride of a [rows, heads, head_dim] tensor whose rows are dense."""
+    if t.dim() != 3:
+        raise ValueError(f"{what} must have 3 dimensions [rows, heads, head_dim]")
+    s0, s1, s2 = t.stride()
+    heads, dim = t.shape[1], t.shape[2]
+    if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
+        raise ValueError(f"{what}: heads and head_dim must be contiguous inside a row")
+    return s0 if t.shape[0] > 1 else heads * dim
+
+
+def _cache_shape(k_codes, k_scales, v_codes, v_scales):
+    shape = k_codes.shape
+    if len(shape) != 4 or v_codes.shape != shape:
+        raise ValueError("k_codes and v_codes must both be [n_blocks, kv_heads, block_tokens, head_dim]")
+    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
+        raise ValueError("k_scales and v_scales must both be [n_blocks, kv_heads]")
+    return shape
+
+
+class KvMap(NamedTuple):
+    """What fp8blk_kv_map writes beside the block table."""
+    seq_lens: torch.Tensor    # int32 [n]
+    q_starts: torch.Tensor    # int32 [n + 1]
+    slots: torch.Tensor       # int64 [max_tokens], -1 past the last new token
+    positions: torch.Tensor   # int32 [max_tokens], -1 past the last new token
+    free_head: torch.Tensor   # int32 [1], the next call's free_head
+
+
+def kv_map_buffers(n: int, max_tokens: int, device) -> KvMap:
+    """Output buffers of fp8blk_kv_map, for callers that keep them from step to step."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return KvMap(torch.empty(n, **i32), torch.empty(n + 1, **i32),
+                 torch.empty(max_tokens, dtype=torch.int64, device=device), torch.empty(max_tokens, **i32),
+                 torch.empty(1, **i32))
+
+
+def fp8blk_kv_map(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_blocks: torch.Tensor,
+                  free_head: torch.Tensor, block_tokens: int, max_tokens: int, out: KvMap | None = None) -> KvMap:
+    """Block tables (updated in place), slots and positions of one step, from the requests' lengths on the device."""
+    n, width = block_table.shape
+    if out is None:
+        out = kv_map_buffers(n, max_tokens, block_table.device)
+    if ctx_lens.numel() != n or new_lens.numel() != n or free_head.numel() != 1:
+        raise ValueError("ctx_lens and new_lens must have one entry per row of block_table, free_head one")
+    if (out.seq_lens.numel() != n or out.q_starts.numel() != n + 1 or out.slots.numel() != max_tokens
+            or out.positions.numel() != max_tokens or out.free_head.numel() != 1):
+        raise ValueError("out does not fit (see kv_map_buffers)")
+    i32 = torch.int32
+    _check(_lib.fp8blk_kv_map(_typed(ctx_lens, i32, "ctx_lens"), _typed(new_lens, i32, "new_lens"),
+                              _typed(block_table, i32, "block_table"), _typed(free_blocks, i32, "free_blocks"),
+                              _typed(free_head, i32, "free_head"), _typed(out.seq_lens, i32, "out.seq_lens"),
+                              _typed(out.q_starts, i32, "out.q_starts"), _typed(out.slots, torch.int64, "out.slots"),
+                              _typed(out.positions, i32, "out.positions"), _typed(out.free_head, i32, "out.free_head"),
+                              n, width, free_blocks.numel(), block_tokens, max_tokens, _stream(block_table)),
+           "fp8blk_kv_map")
+    return out
+
+
+def fp8blk_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                     v_codes: torch.Tensor, v_scales: torch.Tensor) -> None:
+    """Write keys and values [n, kv_heads, head_dim] (float32 or bfloat16; rows may be strided) into the cache at `slots`."""
+    blocks, heads, block, dim = _cache_shape(k_codes, k_scales, v_codes, v_scales)
+    n = slots.numel()
+    if k.shape != (n, heads, dim) or v.shape != k.shape:
+        raise ValueError("k and v must both be [len(slots), kv_heads, head_dim] of the cache")
+    if v.dtype is not k.dtype:
+        raise TypeError("k and v must have the same type")
+    if n == 0:
+        return
+    u8, f32 = torch.uint8, torch.float32
+    _check(_lib.fp8blk_kv_append(k.data_ptr(), v.data_ptr(), _dtype(k, "k"), _typed(slots, torch.int64, "slots"),
+                                 _typed(k_codes, u8, "k_codes"), _typed(k_scales, f32, "k_scales"),
+                                 _typed(v_codes, u8, "v_codes"), _typed(v_scales, f32, "v_scales"), n,
+                                 _rows3(k, "k"), _rows3(v, "v"), blocks, heads, block, dim, _stream(k_codes)),
+           "fp8blk_kv_append")
+
+
+def fp8blk_kv_attn_ws_bytes(n_seqs: int, max_m: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(_lib.fp8blk_kv_attn_ws_bytes(n_seqs, max_m, q_heads, kv_heads, head_dim))
+
+
+def kv_attn_workspace(n_seqs: int, max_m: int, q_heads: int, kv_heads: int, head_dim: int, device) -> torch.Tensor:
+    """A zero-filled workspace of the size fp8blk_kv_attn needs."""
+    n = fp8blk_kv_attn_ws_bytes(n_seqs, max_m, q_heads, kv_heads, head_dim)
+    if n == 0:
+        raise Fp8BlkError(EINVAL, "fp8blk_kv_attn_ws_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def fp8blk_kv_attn(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                   v_scales: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, q_starts: torch.Tensor,
+                   max_m: int, sm_scale: float, ws: torch.Tensor, out: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of q [rows, q_heads, head_dim] (float32 or bfloat16; rows may be strided) over the paged cache; up to
+    max_m rows per request.  `lse` (float32 [rows, q_heads]) is written when given."""
+    blocks, kv_heads, block, dim = _cache_shape(k_codes, k_scales, v_codes, v_scales)
+    n, width = block_table.shape
+    rows, q_heads = q.shape[0], q.shape[1]
+    if q.dim() != 3 or q.shape[2] != dim:
+        raise ValueError("q must be [rows, q_heads, head_dim] of the cache")
+    if out is None:
+        out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype is not q.dtype:
+        raise ValueError("out must have q's shape and type")
+    if seq_lens.numel() != n or q_starts.numel() != n + 1:
+        raise ValueError("seq_lens must have one entry per row of block_table, q_starts one more")
+    if lse is not None and lse.shape != (rows, q_heads):
+        raise ValueError("lse must be [rows, q_heads]")
+    if rows == 0:
+        return out
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    _check(_lib.fp8blk_kv_attn(q.data_ptr(), _dtype(q, "q"), _typed(k_codes, u8, "k_codes"),
+                               _typed(k_scales, f32, "k_scales"), _typed(v_codes, u8, "v_codes"),
+                               _typed(v_scales, f32, "v_scales"), _typed(block_table, i32, "block_table"),
+                               _typed(seq_lens, i32, "seq_lens"), _typed(q_starts, i32, "q_starts"), out.data_ptr(),
+                               None if lse is None else _typed(lse, f32, "lse"), ws.data_ptr(),
+                               ws.numel() * ws.element_size(), n, max_m, rows, q_heads, kv_heads, dim, block, blocks,
+                               width, _rows3(q, "q"), _rows3(out, "out"), sm_scale, _stream(q)), "fp8blk_kv_attn")
+    return out
+
+
+# ---------------------------------------------------------------- scoring
+class TokenLogprobs(NamedTuple):
+    """What fp8blk_token_logprobs writes."""
+    logprob: torch.Tensor       # float32 [n]
+    rank: torch.Tensor          # int32 [n]
+    entropy: torch.Tensor       # float32 [n]
+    top_ids: torch.Tensor       # int32 [n, top]
+    top_logprobs: torch.Tensor  # float32 [n, top]
+
+
+def token_logprobs_buffers(n: int, top: int, device) -> TokenLogprobs:
+    """Output buffers of fp8blk_token_logprobs, for callers that keep them from step to step."""
+    i32, f32 = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
+    return TokenLogprobs(torch.empty(n, **f32), torch.empty(n, **i32), torch.empty(n, **f32),
+                         torch.empty((n, top), **i32), torch.empty((n, top), **f32))
+
+
+def fp8blk_token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0,
+                          out: TokenLogprobs | None = None) -> TokenLogprobs:
+    """Log probability, rank and entropy of `targets` [n] under logits [n, vocab] (float32 or bfloat16; rows may be
+    strided), with the `top` most likely tokens."""
+    if logits.dim() != 2 or targets.numel() != logits.shape[0]:
+        raise ValueError("logits must be [n, vocab], targets [n]")
+    n, vocab = logits.shape
+    if logits.stride(1) != 1 and vocab > 1:
+        raise ValueError("logits must be contiguous inside a row")
+    if out is None:
+        out = token_logprobs_buffers(n, top, logits.device)
+    if out.logprob.numel() != n or out.rank.numel() != n or out.entropy.numel() != n or \
+            out.top_ids.shape != (n, top) or out.top_logprobs.shape != (n, top):
+        raise ValueError("out does not fit (see token_logprobs_buffers)")
+    if n == 0:
+        return out
+    f32, i32 = torch.float32, torch.int32
+    _check(_lib.fp8blk_token_logprobs(logits.data_ptr(), _dtype(logits, "logits"), _typed(targets, i32, "targets"),
+                                      _typed(out.logprob, f32, "out.logprob"), _typed(out.rank, i32, "out.rank"),
+                                      _typed(out.entropy, f32, "out.entropy"), _typed(out.top_ids, i32, "out.top_ids"),
+                                      _typed(out.top_logprobs, f32, "out.top_logprobs"), n, vocab,
+                                      logits.stride(0) if n > 1 else vocab, top, _stream(logits)),
+           "fp8blk_token_logprobs")
+    return out
 
 
 # ---------------------------------------------------------------- control

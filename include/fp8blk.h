@@ -54,6 +54,13 @@ extern "C" {
 
 #define FP8BLK_MAX_M 8      /* activation rows per call: 1 (decode) .. 8 (batched verify) */
 #define FP8BLK_BLOCK 128    /* side of a square scale block */
+#define FP8BLK_MAX_HEAD_DIM 256  /* widest attention head of the paged cache */
+#define FP8BLK_MAX_TOP 32        /* most alternatives per row of fp8blk_token_logprobs */
+#define FP8BLK_MAX_VOCAB 262144  /* most logits per row of fp8blk_token_logprobs */
+
+/* Element types of activations and logits (the `dtype` arguments). */
+#define FP8BLK_F32 0
+#define FP8BLK_BF16 1
 
 /* Bits of the device status word (see fp8blk_device_status). */
 #define FP8BLK_STATUS_WAIT_TIMEOUT 1u /* a kernel gave up waiting for a weight tile (bounded
@@ -61,6 +68,10 @@ extern "C" {
 #define FP8BLK_STATUS_BAD_EXPERT 2u   /* an expert GEMV met a device-side expert id outside
                                          [0, n_experts) or a global scale that is not a power
                                          of two in [2^-100, 2^100]; that slot's outputs are NaN */
+#define FP8BLK_STATUS_BAD_KV 4u          /* a cache call met a negative or too long length, a block id or
+                                            slot outside the pool, or row starts outside the rows */
+#define FP8BLK_STATUS_KV_EXHAUSTED 8u    /* fp8blk_kv_map ran out of free blocks */
+#define FP8BLK_STATUS_BAD_TARGET 16u     /* fp8blk_token_logprobs met a target outside [-1, vocab) */
 
 /* Version of this ABI; bumped on any incompatible change. */
 int fp8blk_abi_version(void);
@@ -270,6 +281,156 @@ int nvfp4_expert_gemv(const uint8_t *codes, const uint8_t *scales, const float *
  */
 int mxfp4_expert_gemv(const uint8_t *codes, const uint8_t *scales, int n_experts, const int32_t *ids,
                       int n_active, const float *x, float *y, int64_t rows, int64_t cols, void *stream);
+
+/*
+ * The paged e4m3 cache (fp8blk_kv_map, fp8blk_kv_append, fp8blk_kv_attn).
+ * Keys and values of past tokens are kept in blocks of block_tokens tokens
+ * (16, 32, 64 or 128) out of two pools, with one scale for each (block, head):
+ *   k_codes, v_codes    device, uint8 e4m3 [n_blocks, kv_heads, block_tokens,
+ *                       head_dim], 16-byte aligned
+ *   k_scales, v_scales  device, f32 [n_blocks, kv_heads]; value = e4m3(code) *
+ *                       scale.  fp8blk_kv_append writes powers of two;
+ *                       fp8blk_kv_attn takes any f32.
+ *   block_table         device, int32 [n_seqs, max_blocks]: token p of request
+ *                       s is row p % block_tokens of block
+ *                       block_table[s][p / block_tokens].
+ *   q_starts            device, int32 [n_seqs + 1]: the rows of this step that
+ *                       belong to request s are q_starts[s] .. q_starts[s+1].
+ * A block belongs to one request.  n_blocks * kv_heads * block_tokens < 2^31;
+ * head_dim a multiple of 16 up to FP8BLK_MAX_HEAD_DIM.  Lengths, tables and
+ * slots stay on the device, so the host checks none of them: the kernels check
+ * each before use, skip what is out of range, and set FP8BLK_STATUS_BAD_KV.
+ * No counterpart on the pages (their engine keeps its caches elsewhere); these
+ * calls serve the same decode step and verify batch, m = 1..8 rows a request
+ * ("Struct Dsv4Gpu" page, decode_step_greedy and verify_batch_dev).
+ */
+
+/*
+ * fp8blk_kv_map -- block tables, slots and positions of one step, from the
+ * requests' lengths.  For request s with ctx_lens[s] cached tokens and
+ * new_lens[s] new ones (either may be 0):
+ *   seq_lens[s] = ctx_lens[s] + new_lens[s];
+ *   q_starts    = exclusive prefix sum of new_lens;
+ *   table entries [ceil(ctx / B), ceil((ctx + new) / B)) are filled, requests in
+ *   order, with the next ids of free_blocks from *free_head on; entries below
+ *   are read and kept, entries above are left alone;
+ *   positions[i] = the position of new token i in its request, and
+ *   slots[i] = block_table[s][p / B] * B + p % B;
+ *   *free_head_out = *free_head + the number of ids taken.
+ * Entries i of slots and positions past the last new token are -1, so a step
+ * captured once with max_tokens rows serves every batch that fits.
+ * A pass that only appends needs no copy between calls: *free_head_out is the
+ * next call's *free_head (the two must not be the same address).
+ * When the free list runs out, the missing blocks' table entries and slots are
+ * -1 and FP8BLK_STATUS_KV_EXHAUSTED is set.  Tokens beyond the table's width
+ * get slot -1, starts beyond max_tokens stop there, negative lengths count as
+ * 0; each sets FP8BLK_STATUS_BAD_KV.
+ *   ctx_lens, new_lens   device, int32 [n_seqs]
+ *   block_table          device, int32 [n_seqs, max_blocks], updated in place
+ *   free_blocks          device, int32 [n_free]: ids in the order they are taken
+ *   free_head            device, int32 [1]: ids of free_blocks already taken
+ *   seq_lens, q_starts   device, int32 [n_seqs], [n_seqs + 1]
+ *   slots                device, int64 [max_tokens], 16-byte aligned
+ *   positions            device, int32 [max_tokens], 16-byte aligned
+ *   free_head_out        device, int32 [1]
+ *   n_seqs 1 .. 65536; max_tokens 1 .. 2^31 - 1.
+ * Outputs other than block_table must not overlap any input.
+ * Errors: EINVAL, EALIGN, ERANGE, ECUDA.
+ */
+int fp8blk_kv_map(const int32_t *ctx_lens, const int32_t *new_lens, int32_t *block_table, const int32_t *free_blocks,
+                  const int32_t *free_head, int32_t *seq_lens, int32_t *q_starts, int64_t *slots, int32_t *positions,
+                  int32_t *free_head_out, int n_seqs, int max_blocks, int n_free, int block_tokens, int64_t max_tokens,
+                  void *stream);
+
+/*
+ * fp8blk_kv_append -- write new keys and values into the cache.  A run is a
+ * maximal group of consecutive tokens whose slots are consecutive inside one
+ * block; for each run and head
+ *   s = the smallest power of two, at least 2^-126, with max|x| <= 448 s over
+ *       the run (values that are not finite do not count); if the block holds
+ *       earlier tokens (the run does not start at row 0), s = max(s, old scale);
+ *   code = e4m3(x / s), nearest even; NaN and infinities become the NaN code;
+ *   if s is larger than the old scale, the codes of the block's earlier rows
+ *   become e4m3(e4m3(code) * old / s).
+ * So a block's scale never shrinks while it fills, and row 0 starts it afresh
+ * (a block that is reused, or rolled back to empty, needs no clearing).
+ *   k, v       device, f32 or bf16 [n_tokens, kv_heads, head_dim], tokens
+ *              k_stride / v_stride elements apart (for instance slices of one
+ *              fused projection), 16-byte aligned rows
+ *   dtype      FP8BLK_F32 or FP8BLK_BF16, of k and v
+ *   slots      device, int64 [n_tokens]; negative = skip the token
+ * In one call, no two runs may lie in the same block.
+ * A slot at or past n_blocks * block_tokens is skipped and sets
+ * FP8BLK_STATUS_BAD_KV.
+ * Errors: EINVAL (also a stride that is no multiple of 16 bytes, or shorter
+ * than a token), EALIGN, ERANGE, ECUDA.
+ */
+int fp8blk_kv_append(const void *k, const void *v, int dtype, const int64_t *slots, uint8_t *k_codes, float *k_scales,
+                     uint8_t *v_codes, float *v_scales, int64_t n_tokens, int64_t k_stride, int64_t v_stride,
+                     int64_t n_blocks, int kv_heads, int block_tokens, int head_dim, void *stream);
+
+/* Workspace size (bytes) of fp8blk_kv_attn; 0 for invalid shapes. */
+size_t fp8blk_kv_attn_ws_bytes(int n_seqs, int max_m, int q_heads, int kv_heads, int head_dim);
+
+/*
+ * fp8blk_kv_attn -- attention of each request's new rows over its cache.
+ * Row i of the r = q_starts[s+1] - q_starts[s] rows of request s sits at
+ * position p = seq_lens[s] - r + i and sees the positions 0 .. p; query head h
+ * reads cache head h / (q_heads / kv_heads):
+ *   a_t   = sm_scale * sum_d q[d] * k[t][d],       t = 0 .. p
+ *   lse   = log sum_t exp(a_t),   out[d] = sum_t exp(a_t - lse) * v[t][d].
+ * A row that sees nothing (p < 0) gives out = 0 and lse = -inf.  What a row
+ * does not see has no part in it, whatever codes and scales are there.
+ * Scores, softmax statistics and sums are f32; the codes go to the tensor
+ * cores as stored.
+ *   q, out     device, f32 or bf16 (`dtype`) [total_rows, q_heads, head_dim],
+ *              rows q_stride / out_stride elements apart, 16-byte aligned rows;
+ *              rows outside q_starts are left alone
+ *   lse        device, optional (NULL = not written): f32 [total_rows, q_heads]
+ *   seq_lens   device, int32 [n_seqs]: tokens in the cache, this step's included
+ *   max_m      most rows of one request, 1 .. FP8BLK_MAX_M
+ *   q_heads    a multiple of kv_heads
+ *   ws         device workspace of at least fp8blk_kv_attn_ws_bytes() bytes,
+ *              16-byte aligned; zero-filled once before its first use, left
+ *              ready by every call.  Calls that share it must be ordered.
+ * A block id outside the pool (or a length past max_blocks) makes the rows
+ * that see it NaN; a request with more than max_m rows, or rows outside
+ * total_rows, is skipped; each sets FP8BLK_STATUS_BAD_KV.
+ * Errors: EINVAL, EALIGN, EWS, ERANGE, ECUDA.
+ */
+int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, const float *k_scales, const uint8_t *v_codes,
+                   const float *v_scales, const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_starts,
+                   void *out, float *lse, void *ws, size_t ws_bytes, int n_seqs, int max_m, int64_t total_rows,
+                   int q_heads, int kv_heads, int head_dim, int block_tokens, int64_t n_blocks, int max_blocks,
+                   int64_t q_stride, int64_t out_stride, float sm_scale, void *stream);
+
+/*
+ * fp8blk_token_logprobs -- score given tokens under rows of logits: for row i
+ * with x = logits[i], t = targets[i], lse = log sum_v exp(x_v)
+ *   logprob[i] = x_t - lse
+ *   rank[i]    = number of v that come before t in the order below
+ *   entropy[i] = -sum_v p_v log p_v,  p = exp(x - lse)
+ *   top_ids[i], top_logprobs[i] = the first `top` tokens of that order
+ * Order: larger logits first, the lowest index first among equal ones (-0 and
+ * +0 are equal), NaN last -- the order of fp8blk_gemv_argmax, so top_ids[i][0]
+ * is its token.  Sums are f32.  The logits are read from memory once.
+ * A row with a NaN or +inf, or with -inf alone, has NaN logprob, entropy and
+ * top_logprobs; -inf among finite logits has probability 0.  Target -1 means
+ * none: logprob NaN, rank -1; any other target outside [0, vocab) gives the
+ * same and sets FP8BLK_STATUS_BAD_TARGET.
+ *   logits   device, f32 or bf16 (`dtype`) [n_rows, vocab], rows `stride`
+ *            elements apart (any stride >= vocab), aligned to one element
+ *   targets  device, int32 [n_rows]
+ *   logprob, entropy  device, f32 [n_rows];  rank  device, int32 [n_rows]
+ *   top      0 .. FP8BLK_MAX_TOP, at most vocab; with 0, top_ids and
+ *            top_logprobs may be NULL
+ *   top_ids, top_logprobs  device, int32 / f32 [n_rows, top]
+ *   vocab    1 .. FP8BLK_MAX_VOCAB
+ * Errors: EINVAL, EALIGN, ERANGE, ECUDA.
+ */
+int fp8blk_token_logprobs(const void *logits, int dtype, const int32_t *targets, float *logprob, int32_t *rank,
+                          float *entropy, int32_t *top_ids, float *top_logprobs, int64_t n_rows, int64_t vocab,
+                          int64_t stride, int top, void *stream);
 
 /*
  * fp8blk_set_launch_tuning -- process-wide launch-shape knobs for the
