@@ -1,100 +1,61 @@
 // kv_attn.cu -- attention of 1..8 new rows per request over the paged e4m3
-// cache (fp8blk_kv_attn): entry point and launch.
+// cache (fp8blk_kv_attn): entry point, choice of the row group, launch.
+#include "kv_attn.cuh"
 #include "step.h"
+
+#include <algorithm>
 
 namespace fp8blk {
 
-struct AttnArgs {
-    const void *q;
-    void *out;
-    float *lse;
-    const uint8_t *k_codes, *v_codes;
-    const float *k_scales, *v_scales;
-    const int32_t *table, *seq_lens, *q_starts;
-    unsigned int *status;
-    int64_t q_stride, out_stride, n_blocks;
-    int n_seqs, max_m, total_rows, q_heads, kv_heads, head_dim, block_log2, width;
-    float scale_log2;
-};
+// Rows of one MMA group: the smallest of 8, 16, 32, 64 that holds all query
+// rows of a request and cache head, as far as tensor memory and shared memory
+// go; more rows take more groups, which read the cache again (out of L2).
+static int attn_rows(int rows, int planes, int halves) {
+    const int most = (halves == 1 ? 128 : 64) / planes;
+    int r = 8;
+    while (r < rows && r < most) r *= 2;
+    return r;
+}
 
-template <typename T>
-__device__ __forceinline__ float attn_load(const T *p) { return static_cast<float>(*p); }
+// Partial sums are sized for the largest row group of either type.
+static size_t attn_ws_bytes(int rows, int head_dim) {
+    const int halves = head_dim > 128 ? 2 : 1;
+    const size_t r = static_cast<size_t>(attn_rows(rows, 2, halves));
+    return kAtHeaderBytes + static_cast<size_t>(kAtMaxGrid) * 2 * (r * halves * 128 + 2 * r) * sizeof(float);
+}
 
-// One CTA per (row, head); each warp takes every fourth token, online softmax
-// per warp, the four joined at the end.
-template <typename T>
-__global__ void __launch_bounds__(128) kv_attn_simple_kernel(const AttnArgs a) {
-    __shared__ float s_o[4][FP8BLK_MAX_HEAD_DIM], s_m[4], s_l[4];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int s = blockIdx.x / a.max_m, i = blockIdx.x - s * a.max_m, h = blockIdx.y;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int first = a.q_starts[s];
-    const int64_t rows64 = static_cast<int64_t>(a.q_starts[s + 1]) - first;
-    const int len = max(a.seq_lens[s], 0);
-    const bool bad = first < 0 || rows64 < 0 || rows64 > a.max_m || first + rows64 > a.total_rows;
-    if (i == 0 && h == 0 && threadIdx.x == 0 && (bad || a.seq_lens[s] < 0)) atomicOr(a.status, FP8BLK_STATUS_BAD_KV);
-    if (bad || i >= rows64) return;
-    const int rows = static_cast<int>(rows64), row = first + i;
-    const int last = len - rows + i;
-    const int kvh = h / (a.q_heads / a.kv_heads), D = a.head_dim, block = 1 << a.block_log2;
-    const T *q = static_cast<const T *>(a.q) + row * a.q_stride + static_cast<int64_t>(h) * D;
-    float qv[8], o[8], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        qv[j] = lane + 32 * j < D ? attn_load(q + lane + 32 * j) * a.scale_log2 : 0.f;
-        o[j] = 0.f;
-    }
-    for (int t = warp; t <= last; t += 4) {
-        const int page = t >> a.block_log2;
-        const int id = page < a.width ? a.table[static_cast<int64_t>(s) * a.width + page] : -1;
-        const bool ok = id >= 0 && id < a.n_blocks;
-        if (!ok && lane == 0) atomicOr(a.status, FP8BLK_STATUS_BAD_KV);
-        const int64_t bh = static_cast<int64_t>(ok ? id : 0) * a.kv_heads + kvh;
-        const int64_t at = (bh * block + (t & (block - 1))) * D;
-        float d = 0.f, vv[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int c = lane + 32 * j;
-            vv[j] = 0.f;
-            if (c < D) {
-                d = fmaf(qv[j], e4m3x2_to_f32(a.k_codes[at + c]).x, d);
-                vv[j] = e4m3x2_to_f32(a.v_codes[at + c]).x;
-            }
+template <typename T, int PL, int R, int ND>
+static cudaError_t launch_attn(const AttnArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap, int64_t grid,
+                               cudaStream_t stream) {
+    const size_t smem = AttnShape<PL, R, ND>::kSmem;
+    const auto kernel = kv_attn_kernel<T, PL, R, ND>;
+    int per_sm = 0;
+    cudaError_t err = kernel_occupancy(reinterpret_cast<const void *>(kernel), kAtThreads, smem, &per_sm);
+    if (err != cudaSuccess) return err;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    return step_launch(kernel, dim3(static_cast<unsigned>(grid)), kAtThreads, smem, stream, kmap, vmap, a);
+}
+
+template <typename T, int PL>
+static cudaError_t launch_attn_rows(const AttnArgs &a, int rows, const CUtensorMap &kmap, const CUtensorMap &vmap,
+                                    int64_t grid, cudaStream_t s) {
+    if (a.head_dim > 128) {
+        switch (rows) {
+            case 8: return launch_attn<T, PL, 8, 2>(a, kmap, vmap, grid, s);
+            case 16: return launch_attn<T, PL, 16, 2>(a, kmap, vmap, grid, s);
+            default:
+                if constexpr (PL == 2) return launch_attn<T, PL, 32, 2>(a, kmap, vmap, grid, s);
+                else return cudaErrorInvalidValue;
         }
-#pragma unroll
-        for (int x = 16; x; x >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, x);
-        d *= ok ? a.k_scales[bh] : __int_as_float(0x7FC00000);
-        const float nm = fmaxf(m, d), c = exp2f(m - nm), p = exp2f(d - nm);
-        l = l * c + p;
-        const float pv = p * a.v_scales[bh];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = fmaf(o[j], c, pv * vv[j]);
-        m = nm;
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (lane + 32 * j < D) s_o[warp][lane + 32 * j] = o[j];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
+    switch (rows) {
+        case 8: return launch_attn<T, PL, 8, 1>(a, kmap, vmap, grid, s);
+        case 16: return launch_attn<T, PL, 16, 1>(a, kmap, vmap, grid, s);
+        case 32: return launch_attn<T, PL, 32, 1>(a, kmap, vmap, grid, s);
+        default:
+            if constexpr (PL == 2) return launch_attn<T, PL, 64, 1>(a, kmap, vmap, grid, s);
+            else return cudaErrorInvalidValue;
     }
-    __syncthreads();
-    const float mm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    float w[4], tl = 0.f;
-    for (int i = 0; i < 4; ++i) {
-        w[i] = s_m[i] == -INFINITY ? 0.f : exp2f(s_m[i] - mm);
-        tl += w[i] * s_l[i];
-    }
-    const float inv = last >= 0 ? 1.f / tl : 0.f;
-    T *out = static_cast<T *>(a.out) + row * a.out_stride + static_cast<int64_t>(h) * D;
-    for (int c = threadIdx.x; c < D; c += 128) {
-        float v = 0.f;
-        for (int i = 0; i < 4; ++i) v += s_m[i] == -INFINITY ? 0.f : w[i] * s_o[i][c];
-        out[c] = static_cast<T>(v * inv);
-    }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[static_cast<int64_t>(row) * a.q_heads + h] = last >= 0 ? (mm + log2f(tl)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace fp8blk
@@ -109,7 +70,7 @@ static bool attn_shape_ok(int n_seqs, int max_m, int q_heads, int kv_heads, int 
 
 extern "C" size_t fp8blk_kv_attn_ws_bytes(int n_seqs, int max_m, int q_heads, int kv_heads, int head_dim) {
     if (!attn_shape_ok(n_seqs, max_m, q_heads, kv_heads, head_dim)) return 0;
-    return 16;
+    return attn_ws_bytes(max_m * (q_heads / kv_heads), head_dim);
 }
 
 extern "C" int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, const float *k_scales,
@@ -136,17 +97,19 @@ extern "C" int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, 
     if (!step_aligned(ws, 16)) return FP8BLK_EALIGN;
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
+    const int planes = dtype == FP8BLK_F32 ? 4 : 2, halves = head_dim > 128 ? 2 : 1, group = q_heads / kv_heads;
+    const int rows = attn_rows(max_m * group, planes, halves);
     AttnArgs a = {};
     a.q = q;
     a.out = out;
     a.lse = lse;
-    a.k_codes = k_codes;
-    a.v_codes = v_codes;
     a.k_scales = k_scales;
     a.v_scales = v_scales;
     a.table = block_table;
     a.seq_lens = seq_lens;
     a.q_starts = q_starts;
+    a.counters = static_cast<uint32_t *>(ws);
+    a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kAtHeaderBytes);
     a.status = dev.status;
     a.q_stride = q_stride;
     a.out_stride = out_stride;
@@ -154,14 +117,27 @@ extern "C" int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, 
     a.n_seqs = n_seqs;
     a.max_m = max_m;
     a.total_rows = static_cast<int>(total_rows);
-    a.q_heads = q_heads;
     a.kv_heads = kv_heads;
+    a.group = group;
     a.head_dim = head_dim;
     a.block_log2 = step_log2(block_tokens);
     a.width = max_blocks;
     a.scale_log2 = sm_scale * 1.4426950408889634f;
-    const dim3 grid(static_cast<unsigned>(n_seqs) * max_m, static_cast<unsigned>(q_heads));
+    // The pools as [(block, head, token), head_dim]: a box is one head's tokens of one block, 128 elements wide (zeros
+    // past head_dim).
+    CUtensorMap kmap, vmap;
+    const int64_t pool_rows = n_blocks * kv_heads * block_tokens;
+    cudaError_t err = encode_map_2d(k_codes, pool_rows, head_dim, head_dim, CU_TENSOR_MAP_DATA_TYPE_UINT8, block_tokens, 128,
+                                    CU_TENSOR_MAP_SWIZZLE_128B, &kmap);
+    if (err == cudaSuccess)
+        err = encode_map_2d(v_codes, pool_rows, head_dim, head_dim, CU_TENSOR_MAP_DATA_TYPE_UINT8, block_tokens, 128,
+                            CU_TENSOR_MAP_SWIZZLE_128B, &vmap);
+    if (err != cudaSuccess) return step_from_cuda(err);
+    // One CTA per SM, and no more than the longest possible list has entries.
+    const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(max_blocks) * block_tokens + kAtTile - 1) / kAtTile);
+    const int64_t entries = static_cast<int64_t>(n_seqs) * kv_heads * ((max_m * group + rows - 1) / rows) * tiles;
+    const int64_t grid = std::min<int64_t>(std::min(dev.sms, kAtMaxGrid), entries);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return step_from_cuda(dtype == FP8BLK_F32 ? step_launch(kv_attn_simple_kernel<float>, grid, 128, 0, s, a)
-                                              : step_launch(kv_attn_simple_kernel<__nv_bfloat16>, grid, 128, 0, s, a));
+    return step_from_cuda(dtype == FP8BLK_F32 ? launch_attn_rows<float, 4>(a, rows, kmap, vmap, grid, s)
+                                              : launch_attn_rows<__nv_bfloat16, 2>(a, rows, kmap, vmap, grid, s));
 }

@@ -1,0 +1,940 @@
+// kv_attn.cuh -- attention of 1..8 new rows per request over the paged e4m3
+// cache, on the fifth-generation tensor cores, with the cached codes fed to
+// the MMAs exactly as stored.
+//
+// For one request and cache head, with R query rows (row r = query head x new
+// position) against a tile of 128 tokens:
+//   S[t][r] = sum_d k[t][d] q[r][d]            (first MMA,  M = 128 tokens)
+//   p[t][r] = 2^(S[t][r] s_k(t) c_r - m_r)     (c_r: softmax scale in base 2, m_r: the tile's maximum)
+//   O[d][r] = sum_t v[t][d] p[t][r] s_v(t)     (second MMA, M = 128 of head_dim)
+// K's tile is the first MMA's A operand as TMA lands it (K-major, 128-byte
+// swizzle), V's tile the second's (the same landing, read M-major), so the
+// CUDA cores never touch a code.  q and p s_v are the B operands: each value
+// is carried as PL e4m3 planes, t_0 = value * 2^e, plane_p = e4m3(t_p), t_{p+1}
+// = 16 (t_p - plane_p), all subtractions exact.  Plane p is a column group of
+// its own, and sums are recombined as sum_p 16^-p D_p in f32.
+//   f32 queries and outputs: PL = 4, a value keeps 2^-16 of itself at worst
+//     (rms 5e-7), which leaves the result at the error of an f32 computation.
+//   bf16: PL = 2.  bf16's 8 bits fit two planes, so q is exact; p keeps 2^-8 at
+//     worst (rms 5e-4), a third of the rounding of the bf16 output.
+// Scores, statistics and output sums are f32; the softmax denominator is
+// summed from the f32 weights.
+//
+// p is relative to the maximum over its own tile and row, not to the running
+// one, and p s_v to the tile's largest |s_v|, times 2^8: every tile's weights
+// fill e4m3's range, so what a weight loses is 2^-22 (bf16) or 2^-30 (f32) of
+// its own tile's largest at worst, and a long tail of small weights keeps its
+// share.  Each tile's product is read back and added to f32 sums in registers
+// with its factor 2^(m_r - running maximum) max|s_v| 2^-8, so nothing in
+// tensor memory is ever rescaled.
+//
+// Work: all (request, cache head, row group, tile) quadruples in one list, cut
+// into one contiguous range per CTA, so ragged lengths balance.  A unit
+// (request, head, row group) that lies across CTAs is joined by the CTA that
+// finishes last, over the partial sums in CTA order (deterministic).
+//
+// Roles (384 threads, one CTA per SM): warps 0-3 softmax (TMEM lane = token),
+// warps 4-7 output sums (TMEM lane = element of head_dim), warp 8 TMA producer
+// (a lane per block), warp 9 first MMA, warp 10 second MMA, warp 11 query
+// planes of the next unit.  Every wait is bounded; a timeout raises a CTA-wide
+// flag, the outputs become NaN, the join still counts, copies and MMAs in
+// flight are waited for, and the status word records it.
+#pragma once
+
+#include "tc8_gemv.cuh"
+
+namespace fp8blk {
+
+constexpr int kAtThreads = 384;
+constexpr int kAtTile = 128;            // tokens per tile
+constexpr int kAtMaxGrid = 256;         // bound on CTAs: arrival counters and partial sums in the workspace
+constexpr size_t kAtHeaderBytes = kAtMaxGrid * sizeof(uint32_t);
+constexpr float kAtNoRef = -3.0e38f;    // maximum of a row that has seen nothing
+constexpr float kAtPeak = 256.0f;       // a tile's largest weight as the planes hold it (e4m3 ends at 448)
+
+struct AttnArgs {
+    const void *q;
+    void *out;
+    float *lse;                       // or null
+    const float *k_scales, *v_scales;
+    const int32_t *table, *seq_lens, *q_starts;
+    uint32_t *counters;               // [kAtMaxGrid], zero between calls
+    float *partials;                  // [grid][2][R x (ND * 128) sums | R references | R denominators]
+    unsigned int *status;
+    int64_t q_stride, out_stride, n_blocks;
+    int n_seqs, max_m, total_rows, kv_heads, group, head_dim, block_log2, width;
+    float scale_log2;                 // softmax scale x log2 e
+};
+
+__device__ float g_attn_nan = __builtin_nanf("");  // what a block outside the pool has for a scale
+
+template <int PL, int R, int ND>
+struct AttnShape {
+    static constexpr int N = PL * R;                          // columns of both B operands
+    static constexpr int kTileBytes = ND * kAtTile * 128;     // K or V codes of a tile
+    static constexpr int kQBytes = ND * N * 128;              // query planes of a unit
+    static constexpr int kPBytes = kAtTile * N;               // weight planes of a tile
+    static constexpr int kFixed = 1024 + 2 * kQBytes + 2 * kPBytes;
+    static constexpr int kRoom = 227 * 1024 - 12 * 1024;      // dynamic shared memory beside the static arrays
+    static constexpr int kStages0 = (kRoom - kFixed) / (2 * kTileBytes);
+    static constexpr int kStages = kStages0 > 6 ? 6 : kStages0;
+    static constexpr size_t kSmem = kFixed + static_cast<size_t>(kStages) * 2 * kTileBytes;
+    static constexpr int kTmemUsed = N * (2 + 2 * ND);        // S and O, both double buffered
+    static constexpr int kTmem = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+    static constexpr int kPartial = R * (ND * 128) + 2 * R;   // floats of one partial
+    static_assert(kStages >= 2 && kTmemUsed <= 512 && N % 16 == 0 && N <= 128, "shape");
+};
+
+// Shared-memory descriptor of an operand tile whose rows are `row_bytes` (128,
+// 64, 32 or 16) long under the swizzle of that width, in groups of 8 rows.
+// K-major operands have rows along M or N; MN-major ones along K.
+template <int ROW_BYTES>
+__device__ __forceinline__ uint64_t at_desc(uint32_t saddr) {
+    constexpr uint64_t layout = ROW_BYTES == 128 ? 2 : ROW_BYTES == 64 ? 4 : ROW_BYTES == 32 ? 6 : 0;
+    constexpr uint64_t group = 8 * ROW_BYTES;
+    uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= (ROW_BYTES == 16 ? group >> 4 : 1ull) << 16;  // without a swizzle the 8-row groups step by the leading offset
+    d |= (group >> 4) << 32;
+    d |= 1ull << 46;
+    d |= layout << 61;
+    return d;
+}
+__host__ __device__ constexpr uint32_t at_idesc(int n, bool mn_major) {
+    return t8_idesc(128, n) | (mn_major ? (1u << 15) | (1u << 16) : 0u);
+}
+// Byte offset `a` inside a tile under the swizzle of ROW_BYTES-long rows.
+template <int ROW_BYTES>
+__device__ __forceinline__ uint32_t at_swizzle(uint32_t a) {
+    constexpr uint32_t mask = ROW_BYTES / 16 - 1;
+    return a ^ (((a >> 7) & mask) << 4);
+}
+
+__device__ __forceinline__ void at_ld8(uint32_t taddr, float *v) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[j]);
+}
+template <int C>
+__device__ __forceinline__ void at_ld(uint32_t taddr, float *v) {
+    static_assert(C == 8 || C == 16, "columns");
+    if constexpr (C == 8) at_ld8(taddr, v);
+    else t8_ld16(taddr, v);
+}
+__device__ __forceinline__ void at_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float at_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Named barrier over the 128 threads of one role, and the same with an OR.
+__device__ __forceinline__ void at_bar(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool at_bar_or(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v)), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
+// Maximum over the warp (NaN ignored; NaN if there is nothing else).
+__device__ __forceinline__ float at_warp_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// One request as the kernel takes it.
+struct AttnSeq {
+    int first, rows, len;  // rows 0: nothing to do
+    int tiles;             // per unit; 1 for an empty cache (which has no pipeline tile)
+    int groups;            // row groups
+    bool bad;
+};
+template <int R>
+__device__ __forceinline__ AttnSeq at_seq(const AttnArgs &a, int s) {
+    AttnSeq q;
+    q.first = a.q_starts[s];
+    const int64_t rows = static_cast<int64_t>(a.q_starts[s + 1]) - q.first;
+    const int len = a.seq_lens[s];
+    const bool off = q.first < 0 || rows < 0 || rows > a.max_m || q.first + rows > a.total_rows;
+    q.bad = off || len < 0;
+    q.rows = off ? 0 : static_cast<int>(rows);
+    q.len = max(len, 0);
+    q.tiles = max(1, (q.len >> 7) + ((q.len & 127) != 0));
+    q.groups = (q.rows * a.group + R - 1) / R;
+    return q;
+}
+
+// A position in the CTA's range of the list: request, unit of the request,
+// tiles [j0, j1) of the unit, and how many list entries are left after them.
+template <int R>
+struct AttnWalk {
+    const AttnArgs &a;
+    AttnSeq q;
+    int s, unit, j0, j1;
+    int64_t left;
+    __device__ __forceinline__ AttnWalk(const AttnArgs &args, int s0, int64_t offset, int64_t count)
+        : a(args), s(s0), left(count) {
+        q = at_seq<R>(a, s);
+        unit = static_cast<int>(offset / q.tiles);
+        j0 = static_cast<int>(offset - static_cast<int64_t>(unit) * q.tiles);
+        clip();
+    }
+    __device__ __forceinline__ void clip() {
+        j1 = static_cast<int>(min(static_cast<int64_t>(q.tiles), j0 + left));
+        left -= j1 - j0;
+    }
+    // The next unit; false at the end of the range.
+    __device__ __forceinline__ bool next() {
+        if (left <= 0) return false;
+        if (++unit == a.kv_heads * q.groups) {
+            unit = 0;
+            do q = at_seq<R>(a, ++s);
+            while (q.rows == 0);
+        }
+        j0 = 0;
+        clip();
+        return true;
+    }
+    __device__ __forceinline__ int head() const { return unit / q.groups; }
+    __device__ __forceinline__ int row0() const { return (unit % q.groups) * R; }
+};
+
+template <typename T>
+__device__ __forceinline__ float4 at_load4(const T *p);
+template <>
+__device__ __forceinline__ float4 at_load4<float>(const float *p) {
+    return *reinterpret_cast<const float4 *>(p);
+}
+template <>
+__device__ __forceinline__ float4 at_load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(p);
+    const float2 lo = bf16x2_to_f32(w.x), hi = bf16x2_to_f32(w.y);
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+__device__ __forceinline__ void at_store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void at_store4(__nv_bfloat16 *p, float4 v) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+
+template <typename T, int PL, int R, int ND>
+__global__ void __launch_bounds__(kAtThreads, 1)
+    kv_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
+    using Sh = AttnShape<PL, R, ND>;
+    constexpr int N = Sh::N, S = Sh::kStages, CH = R < 16 ? R : 16;
+    extern __shared__ __align__(1024) uint8_t at_smem[];
+    __shared__ __align__(8) uint64_t k_full[S], k_free[S], v_full[S], v_free[S], sc_full[S];
+    __shared__ __align__(8) uint64_t s_full[2], s_free[2], p_full[2], o_full[2], o_free[2];
+    __shared__ __align__(8) uint64_t q_full[2], ml_full[2], ml_free[2], qk_done, pv_done;
+    __shared__ float sc[S][2][8];                       // k and v scales of a tile's blocks
+    __shared__ __align__(16) float s_qs[2][R];          // per query row: 2^-e x scale x log2 e (NaN: the row is not finite)
+    __shared__ int s_lim[2][R];                         // last position each row sees
+    __shared__ __align__(16) float s_tref[R], s_lf[R];       // the tile's maximum, and 2^(it - running maximum)
+    __shared__ __align__(16) float s_corr[2][R], s_of[2][R]; // per tile: factor of the sums so far, and of the tile's product
+    __shared__ float s_wmax[4][R];
+    __shared__ int s_moved[2];
+    __shared__ float s_l[2][4][R], s_mref[2][R];
+    __shared__ int s_vnan[2][ND * 128];                 // first position whose value code is NaN, per element
+    __shared__ int64_t s_scan[kAtThreads / 32];
+    __shared__ int64_t s_total, s_off;
+    __shared__ int s_first, s_abort, s_last;
+    __shared__ uint32_t tmem_slot;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint8_t *sQ = at_smem + ((1024u - (smem_addr(at_smem) & 1023u)) & 1023u);
+    uint8_t *sP = sQ + 2 * Sh::kQBytes;
+    uint8_t *sK = sP + 2 * Sh::kPBytes;                 // S tiles of K, then S of V
+    uint8_t *sV = sK + static_cast<size_t>(S) * Sh::kTileBytes;
+
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(smem_addr(&k_full[i]), 1);
+            mbar_init(smem_addr(&k_free[i]), 1);
+            mbar_init(smem_addr(&v_full[i]), 1);
+            mbar_init(smem_addr(&v_free[i]), 1);
+            mbar_init(smem_addr(&sc_full[i]), 32);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&s_full[i]), 1);
+            mbar_init(smem_addr(&s_free[i]), 4);
+            mbar_init(smem_addr(&p_full[i]), 4);
+            mbar_init(smem_addr(&o_full[i]), 1);
+            mbar_init(smem_addr(&o_free[i]), 4);
+            mbar_init(smem_addr(&q_full[i]), 1);
+            mbar_init(smem_addr(&ml_full[i]), 4);
+            mbar_init(smem_addr(&ml_free[i]), 4);
+        }
+        mbar_init(smem_addr(&qk_done), 1);
+        mbar_init(smem_addr(&pv_done), 1);
+        mbar_init_fence();
+        s_abort = 0;
+    }
+    for (int i = tid; i < 2 * ND * 128; i += kAtThreads) (&s_vnan[0][0])[i] = 0x7FFFFFFF;
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
+                     "r"(Sh::kTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    // ---- the list: tiles of every request, scanned by every CTA (thread i sums
+    // requests [i per, (i + 1) per)).
+    {
+        const int per = (a.n_seqs + kAtThreads - 1) / kAtThreads;
+        const int r0 = min(tid * per, a.n_seqs), r1 = min(r0 + per, a.n_seqs);
+        int64_t mine = 0;
+        bool bad = false;
+        for (int s = r0; s < r1; ++s) {
+            const AttnSeq q = at_seq<R>(a, s);
+            mine += static_cast<int64_t>(a.kv_heads) * q.groups * q.tiles;
+            bad |= q.bad;
+        }
+        if (bad && blockIdx.x == 0) atomicOr(a.status, 4u);
+        int64_t pre = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, pre, d);
+            if (lane >= d) pre += u;
+        }
+        if (lane == 31) s_scan[warp] = pre;
+        t8_fence_before();
+        __syncthreads();
+        t8_fence_after();
+        int64_t base = 0, total = 0;
+        for (int w = 0; w < kAtThreads / 32; ++w) {
+            if (w == warp) base = total;
+            total += s_scan[w];
+        }
+        const int64_t grid = min(static_cast<int64_t>(gridDim.x), total);
+        int64_t at = base + pre - mine;  // this thread's first entry
+        if (blockIdx.x < grid) {
+            const int64_t t0 = static_cast<int64_t>(blockIdx.x) * total / grid;
+            if (at <= t0 && t0 < at + mine) {
+                for (int s = r0;; ++s) {
+                    const AttnSeq q = at_seq<R>(a, s);
+                    const int64_t here = static_cast<int64_t>(a.kv_heads) * q.groups * q.tiles;
+                    if (t0 < at + here) {
+                        s_first = s;
+                        s_off = t0 - at;
+                        break;
+                    }
+                    at += here;
+                }
+            }
+        }
+        if (tid == 0) s_total = total;
+        __syncthreads();
+    }
+    const uint32_t tmem = tmem_slot;
+    const int64_t total = s_total;
+    const int64_t grid = min(static_cast<int64_t>(gridDim.x), total);
+    const bool busy = blockIdx.x < grid;
+    const int64_t t_begin = busy ? static_cast<int64_t>(blockIdx.x) * total / grid : 0;
+    const int64_t t_count = busy ? (static_cast<int64_t>(blockIdx.x) + 1) * total / grid - t_begin : 0;
+
+    if (busy) {
+        AttnWalk<R> w(a, s_first, s_off, t_count);
+        if (warp == 8) {
+            // ---------------- TMA producer: lane p copies the tile's p-th block
+            const int np = kAtTile >> a.block_log2, block = 1 << a.block_log2;
+            const uint64_t pol = l2_policy_evict_first();
+            int st = 0;
+            uint32_t ph = 0;
+            int64_t it = 0;
+            struct Tile {
+                int id, head, pages;  // pages that the request has in this tile
+                bool mine;
+            };
+            AttnWalk<R> f(w);  // runs one tile ahead: the block id is a register by the time it is used
+            int fj = f.j0;
+            bool more = true;
+            auto fetch = [&](Tile &t) -> bool {
+                while (more && (f.q.len == 0 || fj >= f.j1)) {
+                    more = f.next();
+                    fj = f.j0;
+                }
+                if (!more) return false;
+                const int page = fj * np + lane;
+                t.pages = min(np, ((f.q.len + block - 1) >> a.block_log2) - fj * np);
+                t.mine = lane < t.pages;
+                t.head = f.head();
+                t.id = t.mine && page < a.width ? a.table[static_cast<int64_t>(f.s) * a.width + page] : -1;
+                ++fj;
+                return true;
+            };
+            Tile cur = {}, nxt = {};
+            bool have = fetch(nxt);
+            while (have) {
+                cur = nxt;
+                have = fetch(nxt);
+                const bool ok = cur.id >= 0 && cur.id < a.n_blocks;
+                if (cur.mine && !ok) atomicOr(a.status, 4u);
+                const int64_t bh = static_cast<int64_t>(ok ? cur.id : 0) * a.kv_heads + cur.head;
+                const int row = static_cast<int>(bh << a.block_log2);
+                const uint32_t bytes = static_cast<uint32_t>(cur.pages) * block * 128 * ND;
+                if (it >= S && !t8_warp_wait(smem_addr(&k_free[st]), ph ^ 1u, &s_abort, lane)) break;
+                if (lane == 0) mbar_arrive_expect_tx(smem_addr(&k_full[st]), bytes);
+                __syncwarp();
+                if (cur.mine) {
+#pragma unroll
+                    for (int h = 0; h < ND; ++h)
+                        t8_tma_2d(smem_addr(sK + static_cast<size_t>(st) * Sh::kTileBytes + h * kAtTile * 128 + lane * block * 128),
+                                  &kmap, h * 128, row, smem_addr(&k_full[st]), pol);
+                }
+                if (it >= S && !t8_warp_wait(smem_addr(&v_free[st]), ph ^ 1u, &s_abort, lane)) {
+                    (void)mbar_wait_bounded(smem_addr(&k_full[st]), ph);  // K of this tile is on its way
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(smem_addr(&v_full[st]), bytes);
+                __syncwarp();
+                if (cur.mine) {
+#pragma unroll
+                    for (int h = 0; h < ND; ++h)
+                        t8_tma_2d(smem_addr(sV + static_cast<size_t>(st) * Sh::kTileBytes + h * kAtTile * 128 + lane * block * 128),
+                                  &vmap, h * 128, row, smem_addr(&v_full[st]), pol);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[st][0][lane])),
+                                 "l"(ok ? a.k_scales + bh : &g_attn_nan)
+                                 : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[st][1][lane])),
+                                 "l"(ok ? a.v_scales + bh : &g_attn_nan)
+                                 : "memory");
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sc_full[st])) : "memory");
+                ++it;
+                if (++st == S) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            // What is still in flight lands before the CTA's shared memory is released.
+            for (int64_t v = it > S ? it - S : 0; v < it; ++v) {
+                const uint32_t par = static_cast<uint32_t>((v / S) & 1);
+                (void)mbar_wait_bounded(smem_addr(&k_full[v % S]), par);
+                (void)mbar_wait_bounded(smem_addr(&v_full[v % S]), par);
+                (void)mbar_wait_bounded(smem_addr(&sc_full[v % S]), par);
+            }
+        } else if (warp == 9) {
+            // ---------------- first MMA: S = K q
+            if (lane == 0) {
+                constexpr uint32_t idesc = at_idesc(N, false);
+                int st = 0, b = 0, ub = 0;
+                uint32_t ph = 0, uph = 0;
+                int64_t it = 0;
+                bool ok = true;
+                do {
+                    if (w.q.len == 0) continue;
+                    ok = t8_wait(smem_addr(&q_full[ub]), uph, &s_abort);
+                    for (int j = w.j0; ok && j < w.j1; ++j) {
+                        if (!t8_wait(smem_addr(&k_full[st]), ph, &s_abort) ||
+                            (it >= 2 && !t8_wait(smem_addr(&s_free[b]), static_cast<uint32_t>(((it >> 1) - 1) & 1), &s_abort))) {
+                            ok = false;
+                            break;
+                        }
+                        t8_fence_after();
+                        const uint32_t ka = smem_addr(sK + static_cast<size_t>(st) * Sh::kTileBytes);
+                        const uint32_t qa = smem_addr(sQ + ub * Sh::kQBytes);
+                        const uint32_t d = tmem + static_cast<uint32_t>(b * N);
+#pragma unroll
+                        for (int h = 0; h < ND; ++h)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (h * 128 + c * 32 < a.head_dim)  // columns past head_dim are zeros on both sides
+                                    t8_mma(d, at_desc<128>(ka + h * kAtTile * 128 + c * 32), at_desc<128>(qa + h * N * 128 + c * 32),
+                                           idesc, h + c > 0);
+                        t8_commit(smem_addr(&k_free[st]));
+                        t8_commit(smem_addr(&s_full[b]));
+                        ++it;
+                        b ^= 1;
+                        if (++st == S) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                    ub ^= 1;
+                    if (ub == 0) uph ^= 1u;
+                } while (ok && w.next());
+                t8_commit(smem_addr(&qk_done));
+                (void)mbar_wait_bounded(smem_addr(&qk_done), 0u);
+            }
+        } else if (warp == 10) {
+            // ---------------- second MMA: O = V^T p
+            if (lane == 0) {
+                constexpr uint32_t idesc = at_idesc(N, true);
+                int st = 0, b = 0;
+                uint32_t ph = 0;
+                int64_t it = 0;
+                bool ok = true;
+                do {
+                    if (w.q.len == 0) continue;
+                    for (int j = w.j0; j < w.j1; ++j) {
+                        const uint32_t bp = static_cast<uint32_t>((it >> 1) & 1);
+                        if (!t8_wait(smem_addr(&v_full[st]), ph, &s_abort) || !t8_wait(smem_addr(&p_full[b]), bp, &s_abort) ||
+                            (it >= 2 && !t8_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort))) {
+                            ok = false;
+                            break;
+                        }
+                        t8_fence_after();
+                        const uint32_t va = smem_addr(sV + static_cast<size_t>(st) * Sh::kTileBytes);
+                        const uint32_t pa = smem_addr(sP + b * Sh::kPBytes);
+#pragma unroll
+                        for (int h = 0; h < ND; ++h) {
+                            const uint32_t d = tmem + static_cast<uint32_t>(2 * N + (b * ND + h) * N);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                t8_mma(d, at_desc<128>(va + h * kAtTile * 128 + c * 32 * 128), at_desc<N>(pa + c * 32 * N), idesc, c > 0);
+                        }
+                        t8_commit(smem_addr(&v_free[st]));
+                        t8_commit(smem_addr(&o_full[b]));
+                        ++it;
+                        b ^= 1;
+                        if (++st == S) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                } while (ok && w.next());
+                t8_commit(smem_addr(&pv_done));
+                (void)mbar_wait_bounded(smem_addr(&pv_done), 0u);
+            }
+        } else if (warp == 11) {
+            // ---------------- query planes: lane l encodes elements 4l .. 4l+3 (+128) of each row
+            int ub = 0;
+            int64_t iu = 0;
+            do {
+                if (w.q.len == 0) continue;
+                // The unit before last is written out: nothing reads this buffer, its scales or its limits any more.
+                if (iu >= 2 && !t8_warp_wait(smem_addr(&ml_free[ub]), static_cast<uint32_t>(((iu >> 1) - 1) & 1), &s_abort, lane)) break;
+                uint8_t *dst = sQ + ub * Sh::kQBytes;
+                const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0);
+                const T *q = static_cast<const T *>(a.q) + w.q.first * a.q_stride + static_cast<int64_t>(w.head()) * a.group * a.head_dim;
+                for (int r4 = 0; r4 < R; r4 += 4) {
+                    float4 v[4][ND];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int h = 0; h < ND; ++h) {
+                            const int r = r4 + x, i = (row0 + r) / a.group, c = row0 + r - i * a.group, d = h * 128 + 4 * lane;
+                            v[x][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (r < valid && d < a.head_dim) v[x][h] = at_load4<T>(q + i * a.q_stride + c * a.head_dim + d);
+                        }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int r = r4 + x;
+                        uint32_t g = 0;
+#pragma unroll
+                        for (int h = 0; h < ND; ++h) {
+                            const float4 f = v[x][h];
+                            g = max(g, max(max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))),
+                                           max(__float_as_uint(fabsf(f.z)), __float_as_uint(fabsf(f.w)))));
+                        }
+                        const int ex = t8_plane_exponent(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, g)));
+                        float f1, f2;
+                        t8_pow2_split(ex == kT8Poison ? 0 : ex, f1, f2);
+                        if (lane == 0) {
+                            float g1, g2;
+                            t8_pow2_split(ex == kT8Poison ? 0 : -ex, g1, g2);
+                            s_qs[ub][r] = ex == kT8Poison ? __int_as_float(0x7FC00000) : a.scale_log2 * g1 * g2;
+                            s_lim[ub][r] = r < valid ? w.q.len - w.q.rows + (row0 + r) / a.group : w.q.len - 1;
+                        }
+#pragma unroll
+                        for (int h = 0; h < ND; ++h) {
+                            float t0 = v[x][h].x * f1 * f2, t1 = v[x][h].y * f1 * f2, t2 = v[x][h].z * f1 * f2, t3 = v[x][h].w * f1 * f2;
+#pragma unroll
+                            for (int p = 0; p < PL; ++p) {
+                                const uint32_t lo = t8_to_e4m3x2(t0, t1), hi = t8_to_e4m3x2(t2, t3);
+                                const int n = p * R + r;
+                                *reinterpret_cast<uint32_t *>(dst + h * N * 128 + at_swizzle<128>(n * 128 + 4 * lane)) = lo | (hi << 16);
+                                if (p + 1 < PL) {
+                                    const float2 qlo = e4m3x2_to_f32(lo), qhi = e4m3x2_to_f32(hi);
+                                    t0 = (t0 - qlo.x) * 16.f;
+                                    t1 = (t1 - qlo.y) * 16.f;
+                                    t2 = (t2 - qhi.x) * 16.f;
+                                    t3 = (t3 - qhi.y) * 16.f;
+                                }
+                            }
+                        }
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic stores -> the MMA
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&q_full[ub]));
+                ++iu;
+                ub ^= 1;
+            } while (w.next());
+        } else if (warp < 4) {
+            // ---------------- softmax: thread = token of the tile
+            const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+            int st = 0, b = 0, ub = 0;
+            uint32_t ph = 0;
+            int64_t it = 0, iu = 0;
+            bool ok = true;
+            do {
+                if (w.q.len == 0) continue;
+                const uint32_t uph = static_cast<uint32_t>((iu >> 1) & 1);
+                ok = t8_warp_wait(smem_addr(&q_full[ub]), uph, &s_abort, lane) &&
+                     (iu < 2 || t8_warp_wait(smem_addr(&ml_free[ub]), uph ^ 1u, &s_abort, lane));
+                float ref = kAtNoRef;  // running maximum of row `tid` (threads below R)
+                float l[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) l[r] = 0.f;
+                const int seen_by_all = w.q.len - w.q.rows;  // positions up to here are seen by every row
+                for (int j = w.j0; j < w.j1; ++j) {
+                    const uint32_t bp = static_cast<uint32_t>((it >> 1) & 1);
+                    ok = ok && t8_warp_wait(smem_addr(&sc_full[st]), ph, &s_abort, lane) &&
+                         t8_warp_wait(smem_addr(&s_full[b]), bp, &s_abort, lane) &&
+                         (it < 2 || t8_warp_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort, lane));
+                    const int pos = j * kAtTile + tid;
+                    const bool edge = (j + 1) * kAtTile - 1 > seen_by_all;  // some row does not see the whole tile
+                    const int page = tid >> a.block_log2;
+                    const float ks = sc[st][0][page];
+                    float s[R];
+                    if (ok) t8_fence_after();
+#pragma unroll
+                    for (int c = 0; c < R; c += CH) {
+                        float d[PL][CH];
+#pragma unroll
+                        for (int p = 0; p < PL; ++p) at_ld<CH>(tmem + lanes + static_cast<uint32_t>(b * N + p * R + c), d[p]);
+                        at_wait_ld();
+#pragma unroll
+                        for (int r = 0; r < CH; ++r) {
+                            float u = d[PL - 1][r];
+#pragma unroll
+                            for (int p = PL - 2; p >= 0; --p) u = fmaf(u, 0.0625f, d[p][r]);
+                            s[c + r] = u * (s_qs[ub][c + r] * ks);
+                        }
+                    }
+                    t8_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&s_free[b]));
+                    if (edge) {
+#pragma unroll
+                        for (int r = 0; r < R; ++r) s[r] = pos > s_lim[ub][r] ? -INFINITY : s[r];
+                    }
+                    // The tile's value scales, relative to the largest.
+                    float vref = 0.f;
+                    for (int p = 0; p < kAtTile >> a.block_log2; ++p) {
+                        const float x = fabsf(sc[st][1][p]);
+                        if ((j * kAtTile + (p << a.block_log2)) < w.q.len && x < INFINITY) vref = fmaxf(vref, x);
+                    }
+                    if (vref == 0.f) vref = 1.f;
+                    const float vs = sc[st][1][page] / vref * kAtPeak;
+                    // Each row's maximum over the tile.
+                    {
+                        float mine[(R + 31) / 32];
+#pragma unroll
+                        for (int r = 0; r < R; ++r) {
+                            const float m = at_warp_max(s[r]);
+                            if (r % 32 == 0 || lane == r % 32) mine[r / 32] = m;
+                        }
+#pragma unroll
+                        for (int x = 0; x < (R + 31) / 32; ++x)
+                            if (32 * x + lane < R) s_wmax[warp][32 * x + lane] = mine[x];
+                    }
+                    at_bar(1);
+                    bool raised = false;
+                    if (tid < R) {
+                        const float m = fmaxf(fmaxf(s_wmax[0][tid], s_wmax[1][tid]), fmaxf(s_wmax[2][tid], s_wmax[3][tid]));
+                        const float tref = fmaxf(m, kAtNoRef), now = fmaxf(ref, tref);
+                        const float f = at_exp2(tref - now);
+                        raised = now > ref;
+                        s_tref[tid] = tref;
+                        s_lf[tid] = f;
+                        s_corr[b][tid] = at_exp2(ref - now);
+                        s_of[b][tid] = f * (vref * (1.0f / kAtPeak));
+                        ref = now;
+                    }
+                    const bool moved = at_bar_or(1, raised);
+                    if (moved) {
+#pragma unroll
+                        for (int r = 0; r < R; ++r) l[r] *= s_corr[b][r];
+                    }
+                    uint8_t *pb = sP + b * Sh::kPBytes;
+#pragma unroll
+                    for (int c = 0; c < R; c += CH) {
+                        float t[CH];
+#pragma unroll
+                        for (int r = 0; r < CH; ++r) {
+                            const float e = at_exp2(s[c + r] - s_tref[c + r]);
+                            l[c + r] = fmaf(e, s_lf[c + r], l[c + r]);
+                            t[r] = e * vs;
+                            if (edge && pos > s_lim[ub][c + r]) t[r] = 0.f;  // whatever the scale
+                        }
+#pragma unroll
+                        for (int p = 0; p < PL; ++p) {
+                            uint32_t word[CH / 4];
+#pragma unroll
+                            for (int r = 0; r < CH; r += 4) {
+                                const uint32_t lo = t8_to_e4m3x2(t[r], t[r + 1]), hi = t8_to_e4m3x2(t[r + 2], t[r + 3]);
+                                word[r / 4] = lo | (hi << 16);
+                                if (p + 1 < PL) {
+                                    const float2 qlo = e4m3x2_to_f32(lo), qhi = e4m3x2_to_f32(hi);
+                                    t[r] = (t[r] - qlo.x) * 16.f;
+                                    t[r + 1] = (t[r + 1] - qlo.y) * 16.f;
+                                    t[r + 2] = (t[r + 2] - qhi.x) * 16.f;
+                                    t[r + 3] = (t[r + 3] - qhi.y) * 16.f;
+                                }
+                            }
+                            uint8_t *at = pb + at_swizzle<N>(tid * N + p * R + c);
+                            if constexpr (CH == 16) *reinterpret_cast<uint4 *>(at) = make_uint4(word[0], word[1], word[2], word[3]);
+                            else *reinterpret_cast<uint2 *>(at) = make_uint2(word[0], word[1]);
+                        }
+                    }
+                    if (edge) {
+                        // This token's row of V: zeros where the request ends (what is there is no token's), and NaN
+                        // codes that only later rows see leave the tile and mark the element for those rows.
+                        ok = ok && t8_warp_wait(smem_addr(&v_full[st]), ph, &s_abort, lane);
+                        if (ok && pos > seen_by_all) {
+#pragma unroll
+                            for (int h = 0; h < ND; ++h) {
+                                uint8_t *row = sV + static_cast<size_t>(st) * Sh::kTileBytes + h * kAtTile * 128;
+                                for (int c = 0; c < 8; ++c) {
+                                    uint4 *at = reinterpret_cast<uint4 *>(row + at_swizzle<128>(tid * 128 + c * 16));
+                                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                                    if (pos < w.q.len) {
+                                        x = *at;
+                                        uint32_t *xs = &x.x;
+                                        for (int y = 0; y < 16; ++y) {
+                                            const uint32_t code = (xs[y >> 2] >> (8 * (y & 3))) & 0x7Fu;
+                                            if (code == 0x7Fu) {
+                                                xs[y >> 2] &= ~(0xFFu << (8 * (y & 3)));
+                                                atomicMin(&s_vnan[ub][h * 128 + c * 16 + y], pos);
+                                            }
+                                        }
+                                    }
+                                    *at = x;
+                                }
+                            }
+                        }
+                    }
+                    if (tid == 0) s_moved[b] = moved;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic stores -> the MMA
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
+                    ++it;
+                    b ^= 1;
+                    if (++st == S) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                // Denominators over this warp's tokens, and the references.
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float x = l[r];
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+                    if (lane == 0) s_l[ub][warp][r] = x;
+                }
+                if (tid < R) s_mref[ub][tid] = ref;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ml_full[ub]));
+                ++iu;
+                ub ^= 1;
+            } while (w.next());
+        } else {
+            // ---------------- output sums: thread = element d (and d + 128) of head_dim
+            const int dt = tid - 128, ow = warp - 4;
+            const uint32_t lanes = static_cast<uint32_t>(ow * 32) << 16;
+            int b = 0, ub = 0;
+            int64_t it = 0, iu = 0, done = t_begin;
+            bool ok = true, first_unit = true;
+            const float nanf = __int_as_float(0x7FC00000);
+            T *out = static_cast<T *>(a.out);
+            do {
+                const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0), kvh = w.head();
+                const bool whole = w.j0 == 0 && w.j1 == w.q.tiles;
+                const int64_t unit_begin = done - w.j0;  // list entry of the unit's first tile
+                done += w.j1 - w.j0;
+                auto out_row = [&](int r) {  // (row, query head) of the unit's row r
+                    const int i = (row0 + r) / a.group;
+                    return static_cast<int64_t>(w.q.first + i) * a.out_stride +
+                           static_cast<int64_t>(kvh * a.group + (row0 + r - i * a.group)) * a.head_dim;
+                };
+                auto lse_at = [&](int r) {
+                    const int i = (row0 + r) / a.group;
+                    return static_cast<int64_t>(w.q.first + i) * (a.kv_heads * a.group) + kvh * a.group + (row0 + r - i * a.group);
+                };
+                if (w.q.len == 0) {  // nothing cached: zeros, and no part in the pipeline
+                    for (int r = 0; r < valid; ++r) {
+#pragma unroll
+                        for (int h = 0; h < ND; ++h)
+                            if (dt + h * 128 < a.head_dim) out[out_row(r) + dt + h * 128] = static_cast<T>(0.f);
+                        if (a.lse && dt == 0) a.lse[lse_at(r)] = -INFINITY;
+                    }
+                    first_unit = false;
+                    continue;
+                }
+                float acc[ND][R];
+#pragma unroll
+                for (int h = 0; h < ND; ++h)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) acc[h][r] = 0.f;
+                for (int j = w.j0; j < w.j1; ++j) {
+                    const uint32_t bp = static_cast<uint32_t>((it >> 1) & 1);
+                    ok = ok && t8_warp_wait(smem_addr(&o_full[b]), bp, &s_abort, lane) &&
+                         t8_warp_wait(smem_addr(&p_full[b]), bp, &s_abort, lane);  // long complete: orders the softmax's words
+                    if (!ok) break;
+                    t8_fence_after();
+                    if (s_moved[b]) {
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int h = 0; h < ND; ++h) acc[h][r] *= s_corr[b][r];
+                    }
+#pragma unroll
+                    for (int h = 0; h < ND; ++h)
+#pragma unroll
+                        for (int c = 0; c < R; c += CH) {
+                            float d[PL][CH];
+#pragma unroll
+                            for (int p = 0; p < PL; ++p)
+                                at_ld<CH>(tmem + lanes + static_cast<uint32_t>(2 * N + (b * ND + h) * N + p * R + c), d[p]);
+                            at_wait_ld();
+#pragma unroll
+                            for (int r = 0; r < CH; ++r) {
+                                float u = d[PL - 1][r];
+#pragma unroll
+                                for (int p = PL - 2; p >= 0; --p) u = fmaf(u, 0.0625f, d[p][r]);
+                                acc[h][c + r] = fmaf(u, s_of[b][c + r], acc[h][c + r]);
+                            }
+                        }
+                    t8_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&o_free[b]));
+                    ++it;
+                    b ^= 1;
+                }
+                ok = ok && t8_warp_wait(smem_addr(&ml_full[ub]), static_cast<uint32_t>((iu >> 1) & 1), &s_abort, lane);
+                if (!ok) {
+#pragma unroll
+                    for (int h = 0; h < ND; ++h)
+#pragma unroll
+                        for (int r = 0; r < R; ++r) acc[h][r] = nanf;
+                }
+#pragma unroll
+                for (int h = 0; h < ND; ++h) {
+                    const int p = s_vnan[ub][h * 128 + dt];
+                    if (p != 0x7FFFFFFF) {  // a NaN value code: the rows that see it
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            if (s_lim[ub][r] >= p) acc[h][r] = nanf;
+                        s_vnan[ub][h * 128 + dt] = 0x7FFFFFFF;
+                    }
+                }
+                auto denom = [&](int r) { return (s_l[ub][0][r] + s_l[ub][1][r]) + (s_l[ub][2][r] + s_l[ub][3][r]); };
+                if (whole) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        if (r < valid) {
+                            const float l = denom(r), inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                            for (int h = 0; h < ND; ++h)
+                                if (dt + h * 128 < a.head_dim) out[out_row(r) + dt + h * 128] = static_cast<T>(acc[h][r] * inv);
+                            if (a.lse && dt == r % 128)
+                                a.lse[lse_at(r)] = l == 0.f ? -INFINITY : (s_mref[ub][r] + log2f(l)) * 0.6931471805599453f;
+                        }
+                    }
+                } else {
+                    // A part of a unit: its sums go to the workspace, and the part that arrives last joins them all.
+                    float *mine = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (first_unit ? 0 : 1)) * Sh::kPartial;
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int h = 0; h < ND; ++h) __stcg(mine + r * (ND * 128) + h * 128 + dt, acc[h][r]);
+                    if (dt < R) {
+                        __stcg(mine + R * ND * 128 + dt, s_mref[ub][dt]);
+                        __stcg(mine + R * ND * 128 + R + dt, denom(dt));
+                    }
+                    const int64_t unit_end = unit_begin + w.q.tiles;
+                    const int b0 = static_cast<int>(((unit_begin + 1) * grid - 1) / total);
+                    const int b1 = static_cast<int>((unit_end * grid - 1) / total);
+                    const int parts = b1 - b0 + 1;
+                    const bool b0_first = static_cast<int64_t>(b0) * total / grid == unit_begin;
+                    __threadfence();
+                    at_bar(2);
+                    if (dt == 0) {
+                        s_last = atomicInc(a.counters + b0, static_cast<unsigned>(parts - 1)) == static_cast<unsigned>(parts - 1);
+                        __threadfence();
+                    }
+                    at_bar(2);
+                    if (s_last) {
+                        for (int r = ow; r < valid; r += 4) {
+                            float m = kAtNoRef, l = 0.f;
+                            float4 o[ND];
+#pragma unroll
+                            for (int h = 0; h < ND; ++h) o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            for (int c0 = 0; c0 < parts; c0 += 32) {
+                                const int p = c0 + lane, cn = min(32, parts - c0);
+                                // Part p lies in CTA b0 + p: its first unit, but for a unit that starts inside CTA b0.
+                                auto part = [&](int q) {
+                                    return a.partials + (static_cast<int64_t>(b0 + q) * 2 + (q == 0 && !b0_first ? 1 : 0)) * Sh::kPartial;
+                                };
+                                const float pm = p < parts ? __ldcg(part(p) + R * ND * 128 + r) : kAtNoRef;
+                                const float pl = p < parts ? __ldcg(part(p) + R * ND * 128 + R + r) : 0.f;
+                                float top = fmaxf(m, pm);
+#pragma unroll
+                                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                                const float keep = at_exp2(m - top), wgt = p < parts ? at_exp2(pm - top) : 0.f;
+                                float lw = pl * wgt;
+#pragma unroll
+                                for (int d = 16; d; d >>= 1) lw += __shfl_xor_sync(0xFFFFFFFFu, lw, d);
+                                l = l * keep + lw;
+#pragma unroll
+                                for (int h = 0; h < ND; ++h) {
+                                    o[h].x *= keep;
+                                    o[h].y *= keep;
+                                    o[h].z *= keep;
+                                    o[h].w *= keep;
+                                }
+                                m = top;
+#pragma unroll 8
+                                for (int q = 0; q < cn; ++q) {
+                                    const float g = __shfl_sync(0xFFFFFFFFu, wgt, q);
+                                    const float4 *src = reinterpret_cast<const float4 *>(part(c0 + q) + r * (ND * 128)) + lane;
+#pragma unroll
+                                    for (int h = 0; h < ND; ++h) {
+                                        const float4 x = __ldcg(src + h * 32);
+                                        o[h].x = fmaf(x.x, g, o[h].x);
+                                        o[h].y = fmaf(x.y, g, o[h].y);
+                                        o[h].z = fmaf(x.z, g, o[h].z);
+                                        o[h].w = fmaf(x.w, g, o[h].w);
+                                    }
+                                }
+                            }
+                            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                            for (int h = 0; h < ND; ++h)
+                                if (4 * lane + h * 128 < a.head_dim)
+                                    at_store4(out + out_row(r) + 4 * lane + h * 128,
+                                              make_float4(o[h].x * inv, o[h].y * inv, o[h].z * inv, o[h].w * inv));
+                            if (a.lse && lane == 0) a.lse[lse_at(r)] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&ml_free[ub]));
+                first_unit = false;
+                ++iu;
+                ub ^= 1;
+            } while (w.next());
+        }
+    }
+
+    t8_fence_before();
+    __syncthreads();
+    if (tid == 0 && *reinterpret_cast<volatile int *>(&s_abort)) atomicOr(a.status, 1u);
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(Sh::kTmem) : "memory");
+}
+
+}  // namespace fp8blk
