@@ -7,11 +7,11 @@
 
 namespace fp8blk {
 
-// Rows of one MMA group: the smallest of 8, 16, 32, 64 that holds all query
-// rows of a request and cache head, as far as tensor memory and shared memory
-// go; more rows take more groups, which read the cache again (out of L2).
+// Rows of one MMA group: the smallest of 8, 16, 32 that holds all query rows of
+// a request and cache head, as far as tensor memory and registers go; more rows
+// take more groups, which read the cache again (out of L2).
 static int attn_rows(int rows, int planes, int halves) {
-    const int most = (halves == 1 ? 128 : 64) / planes;
+    const int most = halves == 2 && planes == 4 ? 16 : 32;
     int r = 8;
     while (r < rows && r < most) r *= 2;
     return r;
@@ -51,10 +51,7 @@ static cudaError_t launch_attn_rows(const AttnArgs &a, int rows, const CUtensorM
     switch (rows) {
         case 8: return launch_attn<T, PL, 8, 1>(a, kmap, vmap, grid, s);
         case 16: return launch_attn<T, PL, 16, 1>(a, kmap, vmap, grid, s);
-        case 32: return launch_attn<T, PL, 32, 1>(a, kmap, vmap, grid, s);
-        default:
-            if constexpr (PL == 2) return launch_attn<T, PL, 64, 1>(a, kmap, vmap, grid, s);
-            else return cudaErrorInvalidValue;
+        default: return launch_attn<T, PL, 32, 1>(a, kmap, vmap, grid, s);
     }
 }
 

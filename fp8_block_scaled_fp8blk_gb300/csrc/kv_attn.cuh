@@ -33,24 +33,25 @@
 // (request, head, row group) that lies across CTAs is joined by the CTA that
 // finishes last, over the partial sums in CTA order (deterministic).
 //
-// Roles (384 threads, one CTA per SM): warps 0-3 softmax (TMEM lane = token),
-// warps 4-7 output sums (TMEM lane = element of head_dim), warp 8 TMA producer
-// (a lane per block), warp 9 first MMA, warp 10 second MMA, warp 11 query
-// planes of the next unit.  Every wait is bounded; a timeout raises a CTA-wide
-// flag, the outputs become NaN, the join still counts, copies and MMAs in
-// flight are waited for, and the status word records it.
+// Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax of even and odd
+// tiles (TMEM lane = token), warps 8-11 output sums (TMEM lane = element of
+// head_dim), warp 12 TMA producer (a lane per block), warp 13 first MMA, warp 14
+// second MMA, warp 15 query planes of the next unit.  Every wait is bounded; a
+// timeout raises a CTA-wide flag, the outputs become NaN, the join still counts,
+// copies and MMAs in flight are waited for, and the status word records it.
 #pragma once
 
 #include "tc8_gemv.cuh"
 
 namespace fp8blk {
 
-constexpr int kAtThreads = 384;
+constexpr int kAtThreads = 512;
+constexpr int kAtOutWarp = 8, kAtProducerWarp = 12, kAtQkWarp = 13, kAtPvWarp = 14, kAtQueryWarp = 15;
 constexpr int kAtTile = 128;            // tokens per tile
 constexpr int kAtMaxGrid = 256;         // bound on CTAs: arrival counters and partial sums in the workspace
 constexpr size_t kAtHeaderBytes = kAtMaxGrid * sizeof(uint32_t);
 constexpr float kAtNoRef = -3.0e38f;    // maximum of a row that has seen nothing
-constexpr float kAtPeak = 256.0f;       // a tile's largest weight as the planes hold it (e4m3 ends at 448)
+constexpr int kAtPeakLog2 = 7;          // a tile's largest weight in the planes is in [2^7, 2^8) (e4m3 ends at 448)
 
 struct AttnArgs {
     const void *q;
@@ -131,6 +132,27 @@ __device__ __forceinline__ float at_exp2(float x) {
     return y;
 }
 
+// Waits of the roles in the tile loop: no suspend hint, every lane polls.  Same
+// bound and abort flag as t8_wait.
+__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, int *abort_flag) {
+    if (mbar_try_wait_short(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait_short(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int *>(abort_flag)) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *reinterpret_cast<volatile int *>(abort_flag) = 1;
+            return false;
+        }
+    }
+}
+// The same for a whole warp: one outcome for all lanes.
+__device__ __forceinline__ bool at_warp_wait(uint32_t bar, uint32_t parity, int *abort_flag) {
+    const bool ok = at_wait(bar, parity, abort_flag);
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+
 // Named barrier over the 128 threads of one role, and the same with an OR.
 __device__ __forceinline__ void at_bar(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ bool at_bar_or(int id, bool v) {
@@ -144,11 +166,45 @@ __device__ __forceinline__ bool at_bar_or(int id, bool v) {
     return r != 0;
 }
 
-// Maximum over the warp (NaN ignored; NaN if there is nothing else).
-__device__ __forceinline__ float at_warp_max(float v) {
-    float m;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
-    return m;
+// Maximum of each of R values over the warp (NaN ignored), as a butterfly that
+// halves the values a lane holds at each step: 31 shuffles for 32 values, 9 for
+// 8 (one redux.sync per value measured about 50 cycles each, one after another).
+// Lane l ends with value at_owned<R>(l).
+template <int R>
+__device__ __forceinline__ int at_owned(int lane) {
+    int r = 0;
+#pragma unroll
+    for (int h = 16, n = R; h; h >>= 1)
+        if (n > 1) {
+            n >>= 1;
+            if (lane & h) r += n;
+        }
+    return r;
+}
+template <int R, typename F>
+__device__ __forceinline__ float at_butterfly(const float (&x)[R], int lane, F op) {
+    static_assert(R == 8 || R == 16 || R == 32, "values");
+    float v[R / 2];
+#pragma unroll
+    for (int i = 0; i < R / 2; ++i) {
+        const bool up = lane & 16;
+        v[i] = op(up ? x[i + R / 2] : x[i], __shfl_xor_sync(0xFFFFFFFFu, up ? x[i] : x[i + R / 2], 16));
+    }
+#pragma unroll
+    for (int h = 8, n = R / 4; h; h >>= 1, n >>= 1) {
+        if (n >= 1) {
+            const bool up = lane & h;
+#pragma unroll
+            for (int i = 0; i < R / 4; ++i)
+                if (i < n) {
+                    const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                    v[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, h));
+                }
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], h));
+        }
+    }
+    return v[0];
 }
 
 // One request as the kernel takes it.
@@ -225,23 +281,88 @@ __device__ __forceinline__ void at_store4(__nv_bfloat16 *p, float4 v) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
+// Query planes of one unit: a warp takes four rows at a time, eight lanes a row.
+// A lane holds four quarters of 4 elements, 32 elements apart, per 128-wide half.
+// The row's exponent, scale and last visible position ride along.
+template <typename T, int PL, int R, int ND>
+__device__ __forceinline__ void at_build_queries(const AttnArgs &a, const AttnWalk<R> &w, uint8_t *dst, float *qs, int *lim, int part,
+                                                 int parts, int lane) {
+    constexpr int N = PL * R;
+    const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0);
+    const T *q = static_cast<const T *>(a.q) + w.q.first * a.q_stride + static_cast<int64_t>(w.head()) * a.group * a.head_dim;
+    const int sub = lane >> 3, l8 = lane & 7;
+    for (int r = 4 * part + sub; r < R; r += 4 * parts) {
+        const int i = (row0 + r) / a.group, c = row0 + r - i * a.group;
+        const T *x = q + i * a.q_stride + c * a.head_dim;
+        float4 v[ND][4];
+#pragma unroll
+        for (int h = 0; h < ND; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int d = h * 128 + k * 32 + 4 * l8;
+                v[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < valid && d < a.head_dim) v[h][k] = at_load4<T>(x + d);
+            }
+        uint32_t g = 0;  // largest |x| as bits; a NaN sorts above infinity
+#pragma unroll
+        for (int h = 0; h < ND; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float4 f = v[h][k];
+                g = max(g, max(max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))),
+                               max(__float_as_uint(fabsf(f.z)), __float_as_uint(fabsf(f.w)))));
+            }
+#pragma unroll
+        for (int d = 4; d; d >>= 1) g = max(g, __shfl_xor_sync(0xFFFFFFFFu, g, d));
+        const int ex = t8_plane_exponent(__uint_as_float(g));
+        float f1, f2;
+        t8_pow2_split(ex == kT8Poison ? 0 : ex, f1, f2);
+        if (l8 == 0) {
+            float g1, g2;
+            t8_pow2_split(ex == kT8Poison ? 0 : -ex, g1, g2);
+            qs[r] = ex == kT8Poison ? __int_as_float(0x7FC00000) : a.scale_log2 * g1 * g2;
+            lim[r] = r < valid ? w.q.len - w.q.rows + i : w.q.len - 1;
+        }
+#pragma unroll
+        for (int h = 0; h < ND; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float t0 = v[h][k].x * f1 * f2, t1 = v[h][k].y * f1 * f2, t2 = v[h][k].z * f1 * f2, t3 = v[h][k].w * f1 * f2;
+#pragma unroll
+                for (int p = 0; p < PL; ++p) {
+                    const uint32_t lo = t8_to_e4m3x2(t0, t1), hi = t8_to_e4m3x2(t2, t3);
+                    *reinterpret_cast<uint32_t *>(dst + h * N * 128 + at_swizzle<128>((p * R + r) * 128 + k * 32 + 4 * l8)) =
+                        lo | (hi << 16);
+                    if (p + 1 < PL) {
+                        const float2 qlo = e4m3x2_to_f32(lo), qhi = e4m3x2_to_f32(hi);
+                        t0 = (t0 - qlo.x) * 16.f;
+                        t1 = (t1 - qlo.y) * 16.f;
+                        t2 = (t2 - qhi.x) * 16.f;
+                        t3 = (t3 - qhi.y) * 16.f;
+                    }
+                }
+            }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic stores -> the MMA
+}
+
 template <typename T, int PL, int R, int ND>
 __global__ void __launch_bounds__(kAtThreads, 1)
     kv_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
     using Sh = AttnShape<PL, R, ND>;
-    constexpr int N = Sh::N, S = Sh::kStages, CH = R < 16 ? R : 16;
+    constexpr int N = Sh::N, S = Sh::kStages, CH = R < 16 || PL > 2 || ND > 1 ? 8 : 16;
     extern __shared__ __align__(1024) uint8_t at_smem[];
-    __shared__ __align__(8) uint64_t k_full[S], k_free[S], v_full[S], v_free[S], sc_full[S];
+    __shared__ __align__(8) uint64_t k_full[S], v_full[S], v_free[S], sc_full[S];
     __shared__ __align__(8) uint64_t s_full[2], s_free[2], p_full[2], o_full[2], o_free[2];
     __shared__ __align__(8) uint64_t q_full[2], ml_full[2], ml_free[2], qk_done, pv_done;
     __shared__ float sc[S][2][8];                       // k and v scales of a tile's blocks
     __shared__ __align__(16) float s_qs[2][R];          // per query row: 2^-e x scale x log2 e (NaN: the row is not finite)
-    __shared__ int s_lim[2][R];                         // last position each row sees
-    __shared__ __align__(16) float s_tref[R], s_lf[R];       // the tile's maximum, and 2^(it - running maximum)
-    __shared__ __align__(16) float s_corr[2][R], s_of[2][R]; // per tile: factor of the sums so far, and of the tile's product
-    __shared__ float s_wmax[4][R];
-    __shared__ int s_moved[2];
-    __shared__ float s_l[2][4][R], s_mref[2][R];
+    __shared__ __align__(16) int s_lim[2][R];           // last position each row sees
+    __shared__ __align__(16) float s_wmax[2][4][R];     // per softmax group: its warps' maxima over the tile
+    __shared__ __align__(16) float s_tref[2][R], s_lf[2][R], s_lc[2][R];  // tile maximum; factors into and of the group's denominator
+    __shared__ float s_vf[2];                           // factor of the tile's product from its value scales
+    __shared__ __align__(16) float s_corr[R], s_of[R];  // output sums: factor of the sums so far, and of the tile's product
+    __shared__ float s_l[2][8][R], s_mref[2][2][R], s_inv[R];
     __shared__ int s_vnan[2][ND * 128];                 // first position whose value code is NaN, per element
     __shared__ int64_t s_scan[kAtThreads / 32];
     __shared__ int64_t s_total, s_off;
@@ -257,7 +378,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(smem_addr(&k_full[i]), 1);
-            mbar_init(smem_addr(&k_free[i]), 1);
             mbar_init(smem_addr(&v_full[i]), 1);
             mbar_init(smem_addr(&v_free[i]), 1);
             mbar_init(smem_addr(&sc_full[i]), 32);
@@ -269,7 +389,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             mbar_init(smem_addr(&o_full[i]), 1);
             mbar_init(smem_addr(&o_free[i]), 4);
             mbar_init(smem_addr(&q_full[i]), 1);
-            mbar_init(smem_addr(&ml_full[i]), 4);
+            mbar_init(smem_addr(&ml_full[i]), 8);
             mbar_init(smem_addr(&ml_free[i]), 4);
         }
         mbar_init(smem_addr(&qk_done), 1);
@@ -344,64 +464,64 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
     if (busy) {
         AttnWalk<R> w(a, s_first, s_off, t_count);
-        if (warp == 8) {
+        const bool built = w.q.len > 0;  // the first unit's query planes are built by every warp
+        if (built) at_build_queries<T, PL, R, ND>(a, w, sQ, s_qs[0], s_lim[0], warp, kAtThreads / 32, lane);
+        __syncthreads();
+        if (warp == kAtProducerWarp) {
             // ---------------- TMA producer: lane p copies the tile's p-th block
             const int np = kAtTile >> a.block_log2, block = 1 << a.block_log2;
             const uint64_t pol = l2_policy_evict_first();
             int st = 0;
             uint32_t ph = 0;
             int64_t it = 0;
-            struct Tile {
-                int id, head, pages;  // pages that the request has in this tile
-                bool mine;
-            };
-            AttnWalk<R> f(w);  // runs one tile ahead: the block id is a register by the time it is used
+            AttnWalk<R> f(w);
             int fj = f.j0;
             bool more = true;
-            auto fetch = [&](Tile &t) -> bool {
+            // Block ids: a window of 32 table entries in the lanes' registers, and the next window on its way.
+            int win = -1, ids = -1, ids_next = -1, win_unit = -1;
+            int64_t win_seq = -1;
+            auto load_ids = [&](int page0) {
+                const int page = page0 + lane;
+                return page < a.width ? a.table[static_cast<int64_t>(f.s) * a.width + page] : -1;
+            };
+            while (true) {
                 while (more && (f.q.len == 0 || fj >= f.j1)) {
                     more = f.next();
                     fj = f.j0;
                 }
-                if (!more) return false;
-                const int page = fj * np + lane;
-                t.pages = min(np, ((f.q.len + block - 1) >> a.block_log2) - fj * np);
-                t.mine = lane < t.pages;
-                t.head = f.head();
-                t.id = t.mine && page < a.width ? a.table[static_cast<int64_t>(f.s) * a.width + page] : -1;
-                ++fj;
-                return true;
-            };
-            Tile cur = {}, nxt = {};
-            bool have = fetch(nxt);
-            while (have) {
-                cur = nxt;
-                have = fetch(nxt);
-                const bool ok = cur.id >= 0 && cur.id < a.n_blocks;
-                if (cur.mine && !ok) atomicOr(a.status, 4u);
-                const int64_t bh = static_cast<int64_t>(ok ? cur.id : 0) * a.kv_heads + cur.head;
+                if (!more) break;
+                const int page0 = fj * np;
+                if (f.s != win_seq || f.unit != win_unit || page0 >= win + 32) {
+                    const bool follows = f.s == win_seq && f.unit == win_unit;
+                    ids = follows ? ids_next : load_ids(page0);
+                    win = page0;
+                    win_seq = f.s;
+                    win_unit = f.unit;
+                    ids_next = load_ids(page0 + 32);
+                }
+                const int pages = min(np, ((f.q.len + block - 1) >> a.block_log2) - page0);
+                const int id = __shfl_sync(0xFFFFFFFFu, ids, (page0 - win + lane) & 31);
+                const bool mine = lane < pages, ok = id >= 0 && id < a.n_blocks;
+                if (mine && !ok) atomicOr(a.status, 4u);
+                const int64_t bh = static_cast<int64_t>(ok ? id : 0) * a.kv_heads + f.head();
                 const int row = static_cast<int>(bh << a.block_log2);
-                const uint32_t bytes = static_cast<uint32_t>(cur.pages) * block * 128 * ND;
-                if (it >= S && !t8_warp_wait(smem_addr(&k_free[st]), ph ^ 1u, &s_abort, lane)) break;
-                if (lane == 0) mbar_arrive_expect_tx(smem_addr(&k_full[st]), bytes);
+                const uint32_t bytes = static_cast<uint32_t>(pages) * block * 128 * ND;
+                ++fj;
+                // V's slot is the last of the stage's to be read.
+                if (it >= S && !at_warp_wait(smem_addr(&v_free[st]), ph ^ 1u, &s_abort)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(smem_addr(&k_full[st]), bytes);
+                    mbar_arrive_expect_tx(smem_addr(&v_full[st]), bytes);
+                }
                 __syncwarp();
-                if (cur.mine) {
+                if (mine) {
+                    const uint32_t at = static_cast<uint32_t>(st) * Sh::kTileBytes + lane * block * 128;
 #pragma unroll
                     for (int h = 0; h < ND; ++h)
-                        t8_tma_2d(smem_addr(sK + static_cast<size_t>(st) * Sh::kTileBytes + h * kAtTile * 128 + lane * block * 128),
-                                  &kmap, h * 128, row, smem_addr(&k_full[st]), pol);
-                }
-                if (it >= S && !t8_warp_wait(smem_addr(&v_free[st]), ph ^ 1u, &s_abort, lane)) {
-                    (void)mbar_wait_bounded(smem_addr(&k_full[st]), ph);  // K of this tile is on its way
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(smem_addr(&v_full[st]), bytes);
-                __syncwarp();
-                if (cur.mine) {
+                        t8_tma_2d(smem_addr(sK) + at + h * kAtTile * 128, &kmap, h * 128, row, smem_addr(&k_full[st]), pol);
 #pragma unroll
                     for (int h = 0; h < ND; ++h)
-                        t8_tma_2d(smem_addr(sV + static_cast<size_t>(st) * Sh::kTileBytes + h * kAtTile * 128 + lane * block * 128),
-                                  &vmap, h * 128, row, smem_addr(&v_full[st]), pol);
+                        t8_tma_2d(smem_addr(sV) + at + h * kAtTile * 128, &vmap, h * 128, row, smem_addr(&v_full[st]), pol);
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[st][0][lane])),
                                  "l"(ok ? a.k_scales + bh : &g_attn_nan)
                                  : "memory");
@@ -423,7 +543,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 (void)mbar_wait_bounded(smem_addr(&v_full[v % S]), par);
                 (void)mbar_wait_bounded(smem_addr(&sc_full[v % S]), par);
             }
-        } else if (warp == 9) {
+        } else if (warp == kAtQkWarp) {
             // ---------------- first MMA: S = K q
             if (lane == 0) {
                 constexpr uint32_t idesc = at_idesc(N, false);
@@ -433,10 +553,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 bool ok = true;
                 do {
                     if (w.q.len == 0) continue;
-                    ok = t8_wait(smem_addr(&q_full[ub]), uph, &s_abort);
+                    ok = at_wait(smem_addr(&q_full[ub]), uph, &s_abort);
                     for (int j = w.j0; ok && j < w.j1; ++j) {
-                        if (!t8_wait(smem_addr(&k_full[st]), ph, &s_abort) ||
-                            (it >= 2 && !t8_wait(smem_addr(&s_free[b]), static_cast<uint32_t>(((it >> 1) - 1) & 1), &s_abort))) {
+                        if (!at_wait(smem_addr(&k_full[st]), ph, &s_abort) ||
+                            (it >= 2 && !at_wait(smem_addr(&s_free[b]), static_cast<uint32_t>(((it >> 1) - 1) & 1), &s_abort))) {
                             ok = false;
                             break;
                         }
@@ -451,7 +571,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                                 if (h * 128 + c * 32 < a.head_dim)  // columns past head_dim are zeros on both sides
                                     t8_mma(d, at_desc<128>(ka + h * kAtTile * 128 + c * 32), at_desc<128>(qa + h * N * 128 + c * 32),
                                            idesc, h + c > 0);
-                        t8_commit(smem_addr(&k_free[st]));
                         t8_commit(smem_addr(&s_full[b]));
                         ++it;
                         b ^= 1;
@@ -466,7 +585,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 t8_commit(smem_addr(&qk_done));
                 (void)mbar_wait_bounded(smem_addr(&qk_done), 0u);
             }
-        } else if (warp == 10) {
+        } else if (warp == kAtPvWarp) {
             // ---------------- second MMA: O = V^T p
             if (lane == 0) {
                 constexpr uint32_t idesc = at_idesc(N, true);
@@ -478,8 +597,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     if (w.q.len == 0) continue;
                     for (int j = w.j0; j < w.j1; ++j) {
                         const uint32_t bp = static_cast<uint32_t>((it >> 1) & 1);
-                        if (!t8_wait(smem_addr(&v_full[st]), ph, &s_abort) || !t8_wait(smem_addr(&p_full[b]), bp, &s_abort) ||
-                            (it >= 2 && !t8_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort))) {
+                        if (!at_wait(smem_addr(&v_full[st]), ph, &s_abort) || !at_wait(smem_addr(&p_full[b]), bp, &s_abort) ||
+                            (it >= 2 && !at_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort))) {
                             ok = false;
                             break;
                         }
@@ -506,104 +625,58 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 t8_commit(smem_addr(&pv_done));
                 (void)mbar_wait_bounded(smem_addr(&pv_done), 0u);
             }
-        } else if (warp == 11) {
-            // ---------------- query planes: lane l encodes elements 4l .. 4l+3 (+128) of each row
+        } else if (warp == kAtQueryWarp) {
+            // ---------------- query planes of the units after the first
             int ub = 0;
             int64_t iu = 0;
             do {
                 if (w.q.len == 0) continue;
                 // The unit before last is written out: nothing reads this buffer, its scales or its limits any more.
-                if (iu >= 2 && !t8_warp_wait(smem_addr(&ml_free[ub]), static_cast<uint32_t>(((iu >> 1) - 1) & 1), &s_abort, lane)) break;
-                uint8_t *dst = sQ + ub * Sh::kQBytes;
-                const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0);
-                const T *q = static_cast<const T *>(a.q) + w.q.first * a.q_stride + static_cast<int64_t>(w.head()) * a.group * a.head_dim;
-                for (int r4 = 0; r4 < R; r4 += 4) {
-                    float4 v[4][ND];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-#pragma unroll
-                        for (int h = 0; h < ND; ++h) {
-                            const int r = r4 + x, i = (row0 + r) / a.group, c = row0 + r - i * a.group, d = h * 128 + 4 * lane;
-                            v[x][h] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (r < valid && d < a.head_dim) v[x][h] = at_load4<T>(q + i * a.q_stride + c * a.head_dim + d);
-                        }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int r = r4 + x;
-                        uint32_t g = 0;
-#pragma unroll
-                        for (int h = 0; h < ND; ++h) {
-                            const float4 f = v[x][h];
-                            g = max(g, max(max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))),
-                                           max(__float_as_uint(fabsf(f.z)), __float_as_uint(fabsf(f.w)))));
-                        }
-                        const int ex = t8_plane_exponent(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, g)));
-                        float f1, f2;
-                        t8_pow2_split(ex == kT8Poison ? 0 : ex, f1, f2);
-                        if (lane == 0) {
-                            float g1, g2;
-                            t8_pow2_split(ex == kT8Poison ? 0 : -ex, g1, g2);
-                            s_qs[ub][r] = ex == kT8Poison ? __int_as_float(0x7FC00000) : a.scale_log2 * g1 * g2;
-                            s_lim[ub][r] = r < valid ? w.q.len - w.q.rows + (row0 + r) / a.group : w.q.len - 1;
-                        }
-#pragma unroll
-                        for (int h = 0; h < ND; ++h) {
-                            float t0 = v[x][h].x * f1 * f2, t1 = v[x][h].y * f1 * f2, t2 = v[x][h].z * f1 * f2, t3 = v[x][h].w * f1 * f2;
-#pragma unroll
-                            for (int p = 0; p < PL; ++p) {
-                                const uint32_t lo = t8_to_e4m3x2(t0, t1), hi = t8_to_e4m3x2(t2, t3);
-                                const int n = p * R + r;
-                                *reinterpret_cast<uint32_t *>(dst + h * N * 128 + at_swizzle<128>(n * 128 + 4 * lane)) = lo | (hi << 16);
-                                if (p + 1 < PL) {
-                                    const float2 qlo = e4m3x2_to_f32(lo), qhi = e4m3x2_to_f32(hi);
-                                    t0 = (t0 - qlo.x) * 16.f;
-                                    t1 = (t1 - qlo.y) * 16.f;
-                                    t2 = (t2 - qhi.x) * 16.f;
-                                    t3 = (t3 - qhi.y) * 16.f;
-                                }
-                            }
-                        }
-                    }
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic stores -> the MMA
+                if (iu >= 2 && !at_warp_wait(smem_addr(&ml_free[ub]), static_cast<uint32_t>(((iu >> 1) - 1) & 1), &s_abort)) break;
+                if (iu > 0 || !built) at_build_queries<T, PL, R, ND>(a, w, sQ + ub * Sh::kQBytes, s_qs[ub], s_lim[ub], 0, 1, lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&q_full[ub]));
                 ++iu;
                 ub ^= 1;
             } while (w.next());
-        } else if (warp < 4) {
-            // ---------------- softmax: thread = token of the tile
-            const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-            int st = 0, b = 0, ub = 0;
+        } else if (warp < kAtOutWarp) {
+            // ---------------- softmax: group g takes the tiles g, g + 2, ...; thread = token of the tile
+            const int g = warp >> 2, wg = warp & 3, tg = tid & 127, bar = 1 + g;
+            const uint32_t lanes = static_cast<uint32_t>(wg * 32) << 16;
+            int st = 0, ub = 0;
             uint32_t ph = 0;
             int64_t it = 0, iu = 0;
             bool ok = true;
             do {
                 if (w.q.len == 0) continue;
                 const uint32_t uph = static_cast<uint32_t>((iu >> 1) & 1);
-                ok = t8_warp_wait(smem_addr(&q_full[ub]), uph, &s_abort, lane) &&
-                     (iu < 2 || t8_warp_wait(smem_addr(&ml_free[ub]), uph ^ 1u, &s_abort, lane));
-                float ref = kAtNoRef;  // running maximum of row `tid` (threads below R)
+                ok = ok && at_warp_wait(smem_addr(&q_full[ub]), uph, &s_abort) &&
+                     (iu < 2 || at_warp_wait(smem_addr(&ml_free[ub]), uph ^ 1u, &s_abort));
+                float ref = kAtNoRef;  // running maximum of row `tg` (threads below R)
                 float l[R];
 #pragma unroll
                 for (int r = 0; r < R; ++r) l[r] = 0.f;
                 const int seen_by_all = w.q.len - w.q.rows;  // positions up to here are seen by every row
-                for (int j = w.j0; j < w.j1; ++j) {
+                for (int j = w.j0; j < w.j1; ++j, ++it) {
+                    const int cs = st;
+                    const uint32_t cph = ph;
+                    if (++st == S) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                    if ((it & 1) != g) continue;
                     const uint32_t bp = static_cast<uint32_t>((it >> 1) & 1);
-                    ok = ok && t8_warp_wait(smem_addr(&sc_full[st]), ph, &s_abort, lane) &&
-                         t8_warp_wait(smem_addr(&s_full[b]), bp, &s_abort, lane) &&
-                         (it < 2 || t8_warp_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort, lane));
-                    const int pos = j * kAtTile + tid;
+                    ok = ok && at_warp_wait(smem_addr(&sc_full[cs]), cph, &s_abort) && at_warp_wait(smem_addr(&s_full[g]), bp, &s_abort);
+                    const int pos = j * kAtTile + tg;
                     const bool edge = (j + 1) * kAtTile - 1 > seen_by_all;  // some row does not see the whole tile
-                    const int page = tid >> a.block_log2;
-                    const float ks = sc[st][0][page];
+                    const float ks = sc[cs][0][tg >> a.block_log2];
                     float s[R];
-                    if (ok) t8_fence_after();
+                    t8_fence_after();
 #pragma unroll
                     for (int c = 0; c < R; c += CH) {
                         float d[PL][CH];
 #pragma unroll
-                        for (int p = 0; p < PL; ++p) at_ld<CH>(tmem + lanes + static_cast<uint32_t>(b * N + p * R + c), d[p]);
+                        for (int p = 0; p < PL; ++p) at_ld<CH>(tmem + lanes + static_cast<uint32_t>(g * N + p * R + c), d[p]);
                         at_wait_ld();
 #pragma unroll
                         for (int r = 0; r < CH; ++r) {
@@ -615,57 +688,54 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     }
                     t8_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&s_free[b]));
+                    if (lane == 0) mbar_arrive(smem_addr(&s_free[g]));
                     if (edge) {
 #pragma unroll
                         for (int r = 0; r < R; ++r) s[r] = pos > s_lim[ub][r] ? -INFINITY : s[r];
                     }
-                    // The tile's value scales, relative to the largest.
-                    float vref = 0.f;
-                    for (int p = 0; p < kAtTile >> a.block_log2; ++p) {
-                        const float x = fabsf(sc[st][1][p]);
-                        if ((j * kAtTile + (p << a.block_log2)) < w.q.len && x < INFINITY) vref = fmaxf(vref, x);
-                    }
-                    if (vref == 0.f) vref = 1.f;
-                    const float vs = sc[st][1][page] / vref * kAtPeak;
                     // Each row's maximum over the tile.
                     {
-                        float mine[(R + 31) / 32];
-#pragma unroll
-                        for (int r = 0; r < R; ++r) {
-                            const float m = at_warp_max(s[r]);
-                            if (r % 32 == 0 || lane == r % 32) mine[r / 32] = m;
-                        }
-#pragma unroll
-                        for (int x = 0; x < (R + 31) / 32; ++x)
-                            if (32 * x + lane < R) s_wmax[warp][32 * x + lane] = mine[x];
+                        const float top = at_butterfly<R>(s, lane, [](float x, float y) { return fmaxf(x, y); });
+                        if ((lane & (32 / R - 1)) == 0) s_wmax[g][wg][at_owned<R>(lane)] = top;
                     }
-                    at_bar(1);
+                    // The tile's value scales, relative to the power of two under the largest.
+                    float vtop = 0.f;
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        const float x = fabsf(sc[cs][1][p]);
+                        if (p < (kAtTile >> a.block_log2) && (j * kAtTile + (p << a.block_log2)) < w.q.len && x < INFINITY) vtop = fmaxf(vtop, x);
+                    }
+                    const int ve = max(__float_as_int(vtop) >> 23, 8);  // biased exponent; 2^-119 and below count as 2^-119
+                    const float vs = sc[cs][1][tg >> a.block_log2] * __int_as_float(ve == 254 ? 0x00400000 : (254 - ve) << 23) * (1 << kAtPeakLog2);
+                    at_bar(bar);
                     bool raised = false;
-                    if (tid < R) {
-                        const float m = fmaxf(fmaxf(s_wmax[0][tid], s_wmax[1][tid]), fmaxf(s_wmax[2][tid], s_wmax[3][tid]));
+                    if (tg < R) {
+                        const float m = fmaxf(fmaxf(s_wmax[g][0][tg], s_wmax[g][1][tg]), fmaxf(s_wmax[g][2][tg], s_wmax[g][3][tg]));
                         const float tref = fmaxf(m, kAtNoRef), now = fmaxf(ref, tref);
-                        const float f = at_exp2(tref - now);
                         raised = now > ref;
-                        s_tref[tid] = tref;
-                        s_lf[tid] = f;
-                        s_corr[b][tid] = at_exp2(ref - now);
-                        s_of[b][tid] = f * (vref * (1.0f / kAtPeak));
+                        s_lf[g][tg] = at_exp2(tref - now);
+                        s_lc[g][tg] = at_exp2(ref - now);
                         ref = now;
+                        // The output sums have read what the tile before last left here.
+                        if (it >= 2) ok = at_wait(smem_addr(&o_free[g]), bp ^ 1u, &s_abort) && ok;
+                        s_tref[g][tg] = tref;
+                        if (tg == 0) s_vf[g] = __int_as_float((ve - kAtPeakLog2) << 23);
                     }
-                    const bool moved = at_bar_or(1, raised);
+                    const bool moved = at_bar_or(bar, raised);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    // P's buffer: the second MMA of the tile before last has read it (o_free says so to the threads above).
                     if (moved) {
 #pragma unroll
-                        for (int r = 0; r < R; ++r) l[r] *= s_corr[b][r];
+                        for (int r = 0; r < R; ++r) l[r] *= s_lc[g][r];
                     }
-                    uint8_t *pb = sP + b * Sh::kPBytes;
+                    uint8_t *pb = sP + g * Sh::kPBytes;
 #pragma unroll
                     for (int c = 0; c < R; c += CH) {
                         float t[CH];
 #pragma unroll
                         for (int r = 0; r < CH; ++r) {
-                            const float e = at_exp2(s[c + r] - s_tref[c + r]);
-                            l[c + r] = fmaf(e, s_lf[c + r], l[c + r]);
+                            const float e = at_exp2(s[c + r] - s_tref[g][c + r]);
+                            l[c + r] = fmaf(e, s_lf[g][c + r], l[c + r]);
                             t[r] = e * vs;
                             if (edge && pos > s_lim[ub][c + r]) t[r] = 0.f;  // whatever the scale
                         }
@@ -684,7 +754,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                                     t[r + 3] = (t[r + 3] - qhi.y) * 16.f;
                                 }
                             }
-                            uint8_t *at = pb + at_swizzle<N>(tid * N + p * R + c);
+                            uint8_t *at = pb + at_swizzle<N>(tg * N + p * R + c);
                             if constexpr (CH == 16) *reinterpret_cast<uint4 *>(at) = make_uint4(word[0], word[1], word[2], word[3]);
                             else *reinterpret_cast<uint2 *>(at) = make_uint2(word[0], word[1]);
                         }
@@ -692,17 +762,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     if (edge) {
                         // This token's row of V: zeros where the request ends (what is there is no token's), and NaN
                         // codes that only later rows see leave the tile and mark the element for those rows.
-                        ok = ok && t8_warp_wait(smem_addr(&v_full[st]), ph, &s_abort, lane);
+                        ok = ok && at_warp_wait(smem_addr(&v_full[cs]), cph, &s_abort);
                         if (ok && pos > seen_by_all) {
 #pragma unroll
                             for (int h = 0; h < ND; ++h) {
-                                uint8_t *row = sV + static_cast<size_t>(st) * Sh::kTileBytes + h * kAtTile * 128;
+                                uint8_t *row = sV + static_cast<size_t>(cs) * Sh::kTileBytes + h * kAtTile * 128;
                                 for (int c = 0; c < 8; ++c) {
-                                    uint4 *at = reinterpret_cast<uint4 *>(row + at_swizzle<128>(tid * 128 + c * 16));
+                                    uint4 *at = reinterpret_cast<uint4 *>(row + at_swizzle<128>(tg * 128 + c * 16));
                                     uint4 x = make_uint4(0u, 0u, 0u, 0u);
                                     if (pos < w.q.len) {
                                         x = *at;
                                         uint32_t *xs = &x.x;
+#pragma unroll
                                         for (int y = 0; y < 16; ++y) {
                                             const uint32_t code = (xs[y >> 2] >> (8 * (y & 3))) & 0x7Fu;
                                             if (code == 0x7Fu) {
@@ -716,26 +787,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                             }
                         }
                     }
-                    if (tid == 0) s_moved[b] = moved;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic stores -> the MMA
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
-                    ++it;
-                    b ^= 1;
-                    if (++st == S) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
+                    if (lane == 0) mbar_arrive(smem_addr(&p_full[g]));
                 }
-                // Denominators over this warp's tokens, and the references.
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    float x = l[r];
-#pragma unroll
-                    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-                    if (lane == 0) s_l[ub][warp][r] = x;
+                // Denominators over this warp's tokens, and the group's maxima.
+                {
+                    const float x = at_butterfly<R>(l, lane, [](float p, float q) { return p + q; });
+                    if ((lane & (32 / R - 1)) == 0) s_l[ub][warp][at_owned<R>(lane)] = x;
                 }
-                if (tid < R) s_mref[ub][tid] = ref;
+                if (tg < R) s_mref[ub][g][tg] = ref;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ml_full[ub]));
                 ++iu;
@@ -743,7 +804,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             } while (w.next());
         } else {
             // ---------------- output sums: thread = element d (and d + 128) of head_dim
-            const int dt = tid - 128, ow = warp - 4;
+            const int dt = tid - kAtOutWarp * 32, ow = warp - kAtOutWarp;
             const uint32_t lanes = static_cast<uint32_t>(ow * 32) << 16;
             int b = 0, ub = 0;
             int64_t it = 0, iu = 0, done = t_begin;
@@ -774,6 +835,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     first_unit = false;
                     continue;
                 }
+                float ref = kAtNoRef;  // running maximum of row `dt` (threads below R)
                 float acc[ND][R];
 #pragma unroll
                 for (int h = 0; h < ND; ++h)
@@ -781,15 +843,23 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     for (int r = 0; r < R; ++r) acc[h][r] = 0.f;
                 for (int j = w.j0; j < w.j1; ++j) {
                     const uint32_t bp = static_cast<uint32_t>((it >> 1) & 1);
-                    ok = ok && t8_warp_wait(smem_addr(&o_full[b]), bp, &s_abort, lane) &&
-                         t8_warp_wait(smem_addr(&p_full[b]), bp, &s_abort, lane);  // long complete: orders the softmax's words
-                    if (!ok) break;
+                    ok = ok && at_warp_wait(smem_addr(&o_full[b]), bp, &s_abort) &&
+                         at_warp_wait(smem_addr(&p_full[b]), bp, &s_abort);  // long complete: orders the softmax's words
                     t8_fence_after();
-                    if (s_moved[b]) {
+                    bool raised = false;
+                    at_bar(3);  // every warp has read the last tile's factors
+                    if (dt < R) {
+                        const float tref = s_tref[b][dt], now = fmaxf(ref, tref);
+                        raised = now > ref;
+                        s_corr[dt] = at_exp2(ref - now);
+                        s_of[dt] = at_exp2(tref - now) * s_vf[b];
+                        ref = now;
+                    }
+                    if (at_bar_or(3, raised)) {
 #pragma unroll
                         for (int r = 0; r < R; ++r)
 #pragma unroll
-                            for (int h = 0; h < ND; ++h) acc[h][r] *= s_corr[b][r];
+                            for (int h = 0; h < ND; ++h) acc[h][r] *= s_corr[r];
                     }
 #pragma unroll
                     for (int h = 0; h < ND; ++h)
@@ -805,7 +875,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                                 float u = d[PL - 1][r];
 #pragma unroll
                                 for (int p = PL - 2; p >= 0; --p) u = fmaf(u, 0.0625f, d[p][r]);
-                                acc[h][c + r] = fmaf(u, s_of[b][c + r], acc[h][c + r]);
+                                acc[h][c + r] = fmaf(u, s_of[c + r], acc[h][c + r]);
                             }
                         }
                     t8_fence_before();
@@ -814,7 +884,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     ++it;
                     b ^= 1;
                 }
-                ok = ok && t8_warp_wait(smem_addr(&ml_full[ub]), static_cast<uint32_t>((iu >> 1) & 1), &s_abort, lane);
+                ok = ok && at_warp_wait(smem_addr(&ml_full[ub]), static_cast<uint32_t>((iu >> 1) & 1), &s_abort);
                 if (!ok) {
 #pragma unroll
                     for (int h = 0; h < ND; ++h)
@@ -831,19 +901,35 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         s_vnan[ub][h * 128 + dt] = 0x7FFFFFFF;
                     }
                 }
-                auto denom = [&](int r) { return (s_l[ub][0][r] + s_l[ub][1][r]) + (s_l[ub][2][r] + s_l[ub][3][r]); };
+                float l = 0.f;  // denominator of row `dt` at the maximum `ref`
+                if (dt < R) {
+#pragma unroll
+                    for (int g = 0; g < 2; ++g)
+                        l += at_exp2(s_mref[ub][g][dt] - ref) * ((s_l[ub][4 * g][dt] + s_l[ub][4 * g + 1][dt]) +
+                                                                 (s_l[ub][4 * g + 2][dt] + s_l[ub][4 * g + 3][dt]));
+                }
                 if (whole) {
+                    if (dt < R) {
+                        s_inv[dt] = l == 0.f ? 0.f : 1.f / l;
+                        if (a.lse && dt < valid) a.lse[lse_at(dt)] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+                    }
+                    at_bar(3);
+                    int64_t at = out_row(0);
+                    int c = row0 % a.group;
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         if (r < valid) {
-                            const float l = denom(r), inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
                             for (int h = 0; h < ND; ++h)
-                                if (dt + h * 128 < a.head_dim) out[out_row(r) + dt + h * 128] = static_cast<T>(acc[h][r] * inv);
-                            if (a.lse && dt == r % 128)
-                                a.lse[lse_at(r)] = l == 0.f ? -INFINITY : (s_mref[ub][r] + log2f(l)) * 0.6931471805599453f;
+                                if (dt + h * 128 < a.head_dim) out[at + dt + h * 128] = static_cast<T>(acc[h][r] * s_inv[r]);
+                        }
+                        at += a.head_dim;
+                        if (++c == a.group) {
+                            c = 0;
+                            at += a.out_stride - static_cast<int64_t>(a.group) * a.head_dim;
                         }
                     }
+                    at_bar(3);  // s_inv is free again
                 } else {
                     // A part of a unit: its sums go to the workspace, and the part that arrives last joins them all.
                     float *mine = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (first_unit ? 0 : 1)) * Sh::kPartial;
@@ -852,8 +938,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                         for (int h = 0; h < ND; ++h) __stcg(mine + r * (ND * 128) + h * 128 + dt, acc[h][r]);
                     if (dt < R) {
-                        __stcg(mine + R * ND * 128 + dt, s_mref[ub][dt]);
-                        __stcg(mine + R * ND * 128 + R + dt, denom(dt));
+                        __stcg(mine + R * ND * 128 + dt, ref);
+                        __stcg(mine + R * ND * 128 + R + dt, l);
                     }
                     const int64_t unit_end = unit_begin + w.q.tiles;
                     const int b0 = static_cast<int>(((unit_begin + 1) * grid - 1) / total);
@@ -861,12 +947,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const int parts = b1 - b0 + 1;
                     const bool b0_first = static_cast<int64_t>(b0) * total / grid == unit_begin;
                     __threadfence();
-                    at_bar(2);
+                    at_bar(3);
                     if (dt == 0) {
                         s_last = atomicInc(a.counters + b0, static_cast<unsigned>(parts - 1)) == static_cast<unsigned>(parts - 1);
                         __threadfence();
                     }
-                    at_bar(2);
+                    at_bar(3);
                     if (s_last) {
                         for (int r = ow; r < valid; r += 4) {
                             float m = kAtNoRef, l = 0.f;
