@@ -35,8 +35,8 @@
 //
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax of even and odd
 // tiles (TMEM lane = token), warps 8-11 output sums (TMEM lane = element of
-// head_dim), warp 12 TMA producer (a lane per block), warp 13 first MMA, warp 14
-// second MMA, warp 15 query planes of the next unit.  Every wait is bounded; a
+// head_dim), warp 12 TMA producer (a lane per block), warps 13 and 14 the MMAs of
+// even and odd tiles, warp 15 query planes of the next unit.  Every wait is bounded; a
 // timeout raises a CTA-wide flag, the outputs become NaN, the join still counts,
 // copies and MMAs in flight are waited for, and the status word records it.
 #pragma once
@@ -46,7 +46,7 @@
 namespace fp8blk {
 
 constexpr int kAtThreads = 512;
-constexpr int kAtOutWarp = 8, kAtProducerWarp = 12, kAtQkWarp = 13, kAtPvWarp = 14, kAtQueryWarp = 15;
+constexpr int kAtOutWarp = 8, kAtProducerWarp = 12, kAtMmaWarp = 13, kAtQueryWarp = 15;
 constexpr int kAtTile = 128;            // tokens per tile
 constexpr int kAtMaxGrid = 256;         // bound on CTAs: arrival counters and partial sums in the workspace
 constexpr size_t kAtHeaderBytes = kAtMaxGrid * sizeof(uint32_t);
@@ -229,23 +229,33 @@ __device__ __forceinline__ AttnSeq at_seq(const AttnArgs &a, int s) {
     return q;
 }
 
+// CTA b's range of a list of `total` entries over `grid` <= total CTAs: the first
+// total % grid CTAs take one entry more.
+struct AttnSplit {
+    int each, more;
+    __device__ __forceinline__ AttnSplit(int total, int grid) : each(total / grid), more(total - each * grid) {}
+    __device__ __forceinline__ int begin(int b) const { return b * each + min(b, more); }
+    __device__ __forceinline__ int owner(int x) const {
+        const int head = more * (each + 1);
+        return x < head ? x / (each + 1) : more + (x - head) / each;
+    }
+};
+
 // A position in the CTA's range of the list: request, unit of the request,
 // tiles [j0, j1) of the unit, and how many list entries are left after them.
 template <int R>
 struct AttnWalk {
     const AttnArgs &a;
     AttnSeq q;
-    int s, unit, j0, j1;
-    int64_t left;
-    __device__ __forceinline__ AttnWalk(const AttnArgs &args, int s0, int64_t offset, int64_t count)
-        : a(args), s(s0), left(count) {
-        q = at_seq<R>(a, s);
-        unit = static_cast<int>(offset / q.tiles);
-        j0 = static_cast<int>(offset - static_cast<int64_t>(unit) * q.tiles);
+    int s, unit, j0, j1, left;
+    __device__ __forceinline__ AttnWalk(const AttnArgs &args, const AttnSeq &seq, int s0, int offset, int count)
+        : a(args), q(seq), s(s0), left(count) {
+        unit = offset / q.tiles;
+        j0 = offset - unit * q.tiles;
         clip();
     }
     __device__ __forceinline__ void clip() {
-        j1 = static_cast<int>(min(static_cast<int64_t>(q.tiles), j0 + left));
+        j1 = min(q.tiles, j0 + left);
         left -= j1 - j0;
     }
     // The next unit; false at the end of the range.
@@ -354,7 +364,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     extern __shared__ __align__(1024) uint8_t at_smem[];
     __shared__ __align__(8) uint64_t k_full[S], v_full[S], v_free[S], sc_full[S];
     __shared__ __align__(8) uint64_t s_full[2], s_free[2], p_full[2], o_full[2], o_free[2];
-    __shared__ __align__(8) uint64_t q_full[2], ml_full[2], ml_free[2], qk_done, pv_done;
+    __shared__ __align__(8) uint64_t q_full[2], ml_full[2], ml_free[2], mma_done[2];
     __shared__ float sc[S][2][8];                       // k and v scales of a tile's blocks
     __shared__ __align__(16) float s_qs[2][R];          // per query row: 2^-e x scale x log2 e (NaN: the row is not finite)
     __shared__ __align__(16) int s_lim[2][R];           // last position each row sees
@@ -364,9 +374,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     __shared__ __align__(16) float s_corr[R], s_of[R];  // output sums: factor of the sums so far, and of the tile's product
     __shared__ float s_l[2][8][R], s_mref[2][2][R], s_inv[R];
     __shared__ int s_vnan[2][ND * 128];                 // first position whose value code is NaN, per element
-    __shared__ int64_t s_scan[kAtThreads / 32];
-    __shared__ int64_t s_total, s_off;
-    __shared__ int s_first, s_abort, s_last;
+    __shared__ int s_scan[kAtThreads / 32];
+    __shared__ AttnSeq s_seq;
+    __shared__ int s_first, s_off, s_abort, s_last;
     __shared__ uint32_t tmem_slot;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -391,9 +401,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             mbar_init(smem_addr(&q_full[i]), 1);
             mbar_init(smem_addr(&ml_full[i]), 8);
             mbar_init(smem_addr(&ml_free[i]), 4);
+            mbar_init(smem_addr(&mma_done[i]), 1);
         }
-        mbar_init(smem_addr(&qk_done), 1);
-        mbar_init(smem_addr(&pv_done), 1);
         mbar_init_fence();
         s_abort = 0;
     }
@@ -408,65 +417,65 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     grid_launch_dependents();
 
     // ---- the list: tiles of every request, scanned by every CTA (thread i sums
-    // requests [i per, (i + 1) per)).
+    // requests [i per, (i + 1) per)).  The host keeps the total below 2^31.
+    int total = 0, grid = 0, t_begin = 0;
     {
         const int per = (a.n_seqs + kAtThreads - 1) / kAtThreads;
         const int r0 = min(tid * per, a.n_seqs), r1 = min(r0 + per, a.n_seqs);
-        int64_t mine = 0;
+        int mine = 0;
         bool bad = false;
+        AttnSeq q = {};
         for (int s = r0; s < r1; ++s) {
-            const AttnSeq q = at_seq<R>(a, s);
-            mine += static_cast<int64_t>(a.kv_heads) * q.groups * q.tiles;
+            q = at_seq<R>(a, s);
+            mine += a.kv_heads * q.groups * q.tiles;
             bad |= q.bad;
         }
         if (bad && blockIdx.x == 0) atomicOr(a.status, 4u);
-        int64_t pre = mine;
+        int pre = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, pre, d);
+            const int u = __shfl_up_sync(0xFFFFFFFFu, pre, d);
             if (lane >= d) pre += u;
         }
         if (lane == 31) s_scan[warp] = pre;
         t8_fence_before();
         __syncthreads();
         t8_fence_after();
-        int64_t base = 0, total = 0;
-        for (int w = 0; w < kAtThreads / 32; ++w) {
-            if (w == warp) base = total;
-            total += s_scan[w];
-        }
-        const int64_t grid = min(static_cast<int64_t>(gridDim.x), total);
-        int64_t at = base + pre - mine;  // this thread's first entry
-        if (blockIdx.x < grid) {
-            const int64_t t0 = static_cast<int64_t>(blockIdx.x) * total / grid;
-            if (at <= t0 && t0 < at + mine) {
-                for (int s = r0;; ++s) {
-                    const AttnSeq q = at_seq<R>(a, s);
-                    const int64_t here = static_cast<int64_t>(a.kv_heads) * q.groups * q.tiles;
-                    if (t0 < at + here) {
-                        s_first = s;
-                        s_off = t0 - at;
-                        break;
+        const int sum = s_scan[lane & (kAtThreads / 32 - 1)];  // each warp's sum, in lanes 0..15
+        total = __reduce_add_sync(0xFFFFFFFFu, lane < kAtThreads / 32 ? sum : 0);
+        const int base = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sum : 0);
+        grid = min(static_cast<int>(gridDim.x), total);
+        int at = base + pre - mine;  // this thread's first entry
+        if (static_cast<int>(blockIdx.x) < grid) {
+            t_begin = AttnSplit(total, grid).begin(blockIdx.x);
+            if (at <= t_begin && t_begin < at + mine) {
+                int s = r0;
+                if (per > 1)
+                    for (;; ++s) {
+                        q = at_seq<R>(a, s);
+                        const int here = a.kv_heads * q.groups * q.tiles;
+                        if (t_begin < at + here) break;
+                        at += here;
                     }
-                    at += here;
-                }
+                s_seq = q;
+                s_first = s;
+                s_off = t_begin - at;
             }
         }
-        if (tid == 0) s_total = total;
         __syncthreads();
     }
     const uint32_t tmem = tmem_slot;
-    const int64_t total = s_total;
-    const int64_t grid = min(static_cast<int64_t>(gridDim.x), total);
-    const bool busy = blockIdx.x < grid;
-    const int64_t t_begin = busy ? static_cast<int64_t>(blockIdx.x) * total / grid : 0;
-    const int64_t t_count = busy ? (static_cast<int64_t>(blockIdx.x) + 1) * total / grid - t_begin : 0;
 
-    if (busy) {
-        AttnWalk<R> w(a, s_first, s_off, t_count);
-        const bool built = w.q.len > 0;  // the first unit's query planes are built by every warp
-        if (built) at_build_queries<T, PL, R, ND>(a, w, sQ, s_qs[0], s_lim[0], warp, kAtThreads / 32, lane);
-        __syncthreads();
+    if (static_cast<int>(blockIdx.x) < grid) {
+        const AttnSplit split(total, grid);
+        AttnWalk<R> w(a, s_seq, s_first, s_off, split.begin(blockIdx.x + 1) - t_begin);
+        // The first unit's query planes are built by the warps that have nothing to do yet.
+        const bool built = w.q.len > 0;
+        if (warp < kAtProducerWarp || warp == kAtQueryWarp) {
+            if (built && warp < kAtProducerWarp)
+                at_build_queries<T, PL, R, ND>(a, w, sQ, s_qs[0], s_lim[0], warp, kAtProducerWarp, lane);
+            asm volatile("bar.sync 4, %0;" ::"n"((kAtProducerWarp + 1) * 32) : "memory");
+        }
         if (warp == kAtProducerWarp) {
             // ---------------- TMA producer: lane p copies the tile's p-th block
             const int np = kAtTile >> a.block_log2, block = 1 << a.block_log2;
@@ -478,8 +487,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             int fj = f.j0;
             bool more = true;
             // Block ids: a window of 32 table entries in the lanes' registers, and the next window on its way.
-            int win = -1, ids = -1, ids_next = -1, win_unit = -1;
-            int64_t win_seq = -1;
+            int win = -1, ids = -1, ids_next = -1, win_unit = -1, win_seq = -1, win_head = 0;
             auto load_ids = [&](int page0) {
                 const int page = page0 + lane;
                 return page < a.width ? a.table[static_cast<int64_t>(f.s) * a.width + page] : -1;
@@ -497,36 +505,29 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     win = page0;
                     win_seq = f.s;
                     win_unit = f.unit;
+                    win_head = f.head();
                     ids_next = load_ids(page0 + 32);
                 }
                 const int pages = min(np, ((f.q.len + block - 1) >> a.block_log2) - page0);
-                const int id = __shfl_sync(0xFFFFFFFFu, ids, (page0 - win + lane) & 31);
-                const bool mine = lane < pages, ok = id >= 0 && id < a.n_blocks;
+                // Lanes 0.. copy the tile's blocks of K, lanes 16.. those of V, each with its scale.
+                const int p = lane & 15, id = __shfl_sync(0xFFFFFFFFu, ids, (page0 - win + p) & 31);
+                const bool mine = p < pages, ok = id >= 0 && id < a.n_blocks;
                 if (mine && !ok) atomicOr(a.status, 4u);
-                const int64_t bh = static_cast<int64_t>(ok ? id : 0) * a.kv_heads + f.head();
+                const int64_t bh = static_cast<int64_t>(ok ? id : 0) * a.kv_heads + win_head;
                 const int row = static_cast<int>(bh << a.block_log2);
-                const uint32_t bytes = static_cast<uint32_t>(pages) * block * 128 * ND;
                 ++fj;
                 // V's slot is the last of the stage's to be read.
                 if (it >= S && !at_warp_wait(smem_addr(&v_free[st]), ph ^ 1u, &s_abort)) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(smem_addr(&k_full[st]), bytes);
-                    mbar_arrive_expect_tx(smem_addr(&v_full[st]), bytes);
-                }
+                const uint32_t full = smem_addr(lane < 16 ? &k_full[st] : &v_full[st]);
+                if (p == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(pages) * block * 128 * ND);
                 __syncwarp();
                 if (mine) {
-                    const uint32_t at = static_cast<uint32_t>(st) * Sh::kTileBytes + lane * block * 128;
+                    const uint32_t at = smem_addr(lane < 16 ? sK : sV) + static_cast<uint32_t>(st) * Sh::kTileBytes + p * block * 128;
 #pragma unroll
                     for (int h = 0; h < ND; ++h)
-                        t8_tma_2d(smem_addr(sK) + at + h * kAtTile * 128, &kmap, h * 128, row, smem_addr(&k_full[st]), pol);
-#pragma unroll
-                    for (int h = 0; h < ND; ++h)
-                        t8_tma_2d(smem_addr(sV) + at + h * kAtTile * 128, &vmap, h * 128, row, smem_addr(&v_full[st]), pol);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[st][0][lane])),
-                                 "l"(ok ? a.k_scales + bh : &g_attn_nan)
-                                 : "memory");
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[st][1][lane])),
-                                 "l"(ok ? a.v_scales + bh : &g_attn_nan)
+                        t8_tma_2d(at + h * kAtTile * 128, lane < 16 ? &kmap : &vmap, h * 128, row, full, pol);
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[st][lane >> 4][p])),
+                                 "l"(ok ? (lane < 16 ? a.k_scales : a.v_scales) + bh : &g_attn_nan)
                                  : "memory");
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sc_full[st])) : "memory");
@@ -543,87 +544,84 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 (void)mbar_wait_bounded(smem_addr(&v_full[v % S]), par);
                 (void)mbar_wait_bounded(smem_addr(&sc_full[v % S]), par);
             }
-        } else if (warp == kAtQkWarp) {
-            // ---------------- first MMA: S = K q
+        } else if (warp == kAtMmaWarp || warp == kAtMmaWarp + 1) {
+            // ---------------- MMA issuers: warp g issues both products of the tiles g, g + 2, ...  Whichever of the two
+            // can go next goes, the second product first (it frees a stage).
             if (lane == 0) {
-                constexpr uint32_t idesc = at_idesc(N, false);
-                int st = 0, b = 0, ub = 0;
-                uint32_t ph = 0, uph = 0;
-                int64_t it = 0;
-                bool ok = true;
-                do {
-                    if (w.q.len == 0) continue;
-                    ok = at_wait(smem_addr(&q_full[ub]), uph, &s_abort);
-                    for (int j = w.j0; ok && j < w.j1; ++j) {
-                        if (!at_wait(smem_addr(&k_full[st]), ph, &s_abort) ||
-                            (it >= 2 && !at_wait(smem_addr(&s_free[b]), static_cast<uint32_t>(((it >> 1) - 1) & 1), &s_abort))) {
-                            ok = false;
-                            break;
-                        }
-                        t8_fence_after();
-                        const uint32_t ka = smem_addr(sK + static_cast<size_t>(st) * Sh::kTileBytes);
-                        const uint32_t qa = smem_addr(sQ + ub * Sh::kQBytes);
-                        const uint32_t d = tmem + static_cast<uint32_t>(b * N);
+                const int g = warp - kAtMmaWarp;
+                constexpr uint32_t qk_idesc = at_idesc(N, false), pv_idesc = at_idesc(N, true);
+                int qt = g, pt = g;         // next tile of each product
+                int iu = -1, unit_end = 0;  // the first product's unit, and the tile after its last
+                bool more = true;           // false: unit_end is the end of the range
+                uint64_t t0 = 0;
+                int spins = 0;
+                while (more || pt < unit_end) {
+                    bool went = false;
+                    {
+                        const int st = pt % S;
+                        const uint32_t ph = static_cast<uint32_t>(pt / S) & 1u, bp = static_cast<uint32_t>(pt >> 1) & 1u;
+                        if (pt < qt && mbar_test_wait(smem_addr(&p_full[g]), bp) && mbar_test_wait(smem_addr(&v_full[st]), ph) &&
+                            (pt < 2 || mbar_test_wait(smem_addr(&o_free[g]), bp ^ 1u))) {
+                            t8_fence_after();
+                            const uint32_t va = smem_addr(sV) + static_cast<uint32_t>(st) * Sh::kTileBytes;
+                            const uint32_t pa = smem_addr(sP + g * Sh::kPBytes);
 #pragma unroll
-                        for (int h = 0; h < ND; ++h)
+                            for (int h = 0; h < ND; ++h) {
+                                const uint32_t d = tmem + static_cast<uint32_t>(2 * N + (g * ND + h) * N);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                if (h * 128 + c * 32 < a.head_dim)  // columns past head_dim are zeros on both sides
-                                    t8_mma(d, at_desc<128>(ka + h * kAtTile * 128 + c * 32), at_desc<128>(qa + h * N * 128 + c * 32),
-                                           idesc, h + c > 0);
-                        t8_commit(smem_addr(&s_full[b]));
-                        ++it;
-                        b ^= 1;
-                        if (++st == S) {
-                            st = 0;
-                            ph ^= 1u;
+                                for (int c = 0; c < 4; ++c)
+                                    t8_mma(d, at_desc<128>(va + h * kAtTile * 128 + c * 32 * 128), at_desc<N>(pa + c * 32 * N), pv_idesc,
+                                           c > 0);
+                            }
+                            t8_commit(smem_addr(&o_full[g]));
+                            t8_commit(smem_addr(&v_free[st]));
+                            pt += 2;
+                            went = true;
                         }
                     }
-                    ub ^= 1;
-                    if (ub == 0) uph ^= 1u;
-                } while (ok && w.next());
-                t8_commit(smem_addr(&qk_done));
-                (void)mbar_wait_bounded(smem_addr(&qk_done), 0u);
-            }
-        } else if (warp == kAtPvWarp) {
-            // ---------------- second MMA: O = V^T p
-            if (lane == 0) {
-                constexpr uint32_t idesc = at_idesc(N, true);
-                int st = 0, b = 0;
-                uint32_t ph = 0;
-                int64_t it = 0;
-                bool ok = true;
-                do {
-                    if (w.q.len == 0) continue;
-                    for (int j = w.j0; j < w.j1; ++j) {
-                        const uint32_t bp = static_cast<uint32_t>((it >> 1) & 1);
-                        if (!at_wait(smem_addr(&v_full[st]), ph, &s_abort) || !at_wait(smem_addr(&p_full[b]), bp, &s_abort) ||
-                            (it >= 2 && !at_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort))) {
-                            ok = false;
-                            break;
-                        }
-                        t8_fence_after();
-                        const uint32_t va = smem_addr(sV + static_cast<size_t>(st) * Sh::kTileBytes);
-                        const uint32_t pa = smem_addr(sP + b * Sh::kPBytes);
-#pragma unroll
-                        for (int h = 0; h < ND; ++h) {
-                            const uint32_t d = tmem + static_cast<uint32_t>(2 * N + (b * ND + h) * N);
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                t8_mma(d, at_desc<128>(va + h * kAtTile * 128 + c * 32 * 128), at_desc<N>(pa + c * 32 * N), idesc, c > 0);
-                        }
-                        t8_commit(smem_addr(&v_free[st]));
-                        t8_commit(smem_addr(&o_full[b]));
-                        ++it;
-                        b ^= 1;
-                        if (++st == S) {
-                            st = 0;
-                            ph ^= 1u;
+                    while (more && qt >= unit_end) {  // on to the unit that tile qt belongs to
+                        if (iu >= 0 || w.q.len == 0) more = w.next();
+                        while (more && w.q.len == 0) more = w.next();
+                        if (more) {
+                            ++iu;
+                            unit_end += w.j1 - w.j0;
                         }
                     }
-                } while (ok && w.next());
-                t8_commit(smem_addr(&pv_done));
-                (void)mbar_wait_bounded(smem_addr(&pv_done), 0u);
+                    if (qt < unit_end) {
+                        const int st = qt % S;
+                        const uint32_t ph = static_cast<uint32_t>(qt / S) & 1u, bp = static_cast<uint32_t>(qt >> 1) & 1u;
+                        if (mbar_test_wait(smem_addr(&k_full[st]), ph) && (qt < 2 || mbar_test_wait(smem_addr(&s_free[g]), bp ^ 1u)) &&
+                            mbar_test_wait(smem_addr(&q_full[iu & 1]), static_cast<uint32_t>(iu >> 1) & 1u)) {
+                            t8_fence_after();
+                            const uint32_t ka = smem_addr(sK) + static_cast<uint32_t>(st) * Sh::kTileBytes;
+                            const uint32_t qa = smem_addr(sQ + (iu & 1) * Sh::kQBytes);
+                            const uint32_t d = tmem + static_cast<uint32_t>(g * N);
+#pragma unroll
+                            for (int h = 0; h < ND; ++h)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    if (h * 128 + c * 32 < a.head_dim)  // columns past head_dim are zeros on both sides
+                                        t8_mma(d, at_desc<128>(ka + h * kAtTile * 128 + c * 32), at_desc<128>(qa + h * N * 128 + c * 32),
+                                               qk_idesc, h + c > 0);
+                            t8_commit(smem_addr(&s_full[g]));
+                            qt += 2;
+                            went = true;
+                        }
+                    }
+                    if (went) {
+                        spins = 0;
+                    } else if ((++spins & 31) == 0) {  // bounded, as at_wait
+                        if (*reinterpret_cast<volatile int *>(&s_abort)) break;
+                        const uint64_t now = global_timer_ns();
+                        if (spins == 32) t0 = now;
+                        else if (now - t0 > kWaitLimitNs) {
+                            *reinterpret_cast<volatile int *>(&s_abort) = 1;
+                            break;
+                        }
+                    }
+                }
+                t8_commit(smem_addr(&mma_done[g]));
+                (void)mbar_wait_bounded(smem_addr(&mma_done[g]), 0u);
             }
         } else if (warp == kAtQueryWarp) {
             // ---------------- query planes of the units after the first
@@ -807,14 +805,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const int dt = tid - kAtOutWarp * 32, ow = warp - kAtOutWarp;
             const uint32_t lanes = static_cast<uint32_t>(ow * 32) << 16;
             int b = 0, ub = 0;
-            int64_t it = 0, iu = 0, done = t_begin;
+            int64_t it = 0, iu = 0;
+            int done = t_begin;
             bool ok = true, first_unit = true;
             const float nanf = __int_as_float(0x7FC00000);
             T *out = static_cast<T *>(a.out);
             do {
                 const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0), kvh = w.head();
                 const bool whole = w.j0 == 0 && w.j1 == w.q.tiles;
-                const int64_t unit_begin = done - w.j0;  // list entry of the unit's first tile
+                const int unit_begin = done - w.j0;  // list entry of the unit's first tile
                 done += w.j1 - w.j0;
                 auto out_row = [&](int r) {  // (row, query head) of the unit's row r
                     const int i = (row0 + r) / a.group;
@@ -941,69 +940,87 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         __stcg(mine + R * ND * 128 + dt, ref);
                         __stcg(mine + R * ND * 128 + R + dt, l);
                     }
-                    const int64_t unit_end = unit_begin + w.q.tiles;
-                    const int b0 = static_cast<int>(((unit_begin + 1) * grid - 1) / total);
-                    const int b1 = static_cast<int>((unit_end * grid - 1) / total);
-                    const int parts = b1 - b0 + 1;
-                    const bool b0_first = static_cast<int64_t>(b0) * total / grid == unit_begin;
-                    __threadfence();
+                    const int b0 = split.owner(unit_begin), parts = split.owner(unit_begin + w.q.tiles - 1) - b0 + 1;
+                    const bool b0_first = split.begin(b0) == unit_begin;
                     at_bar(3);
-                    if (dt == 0) {
-                        s_last = atomicInc(a.counters + b0, static_cast<unsigned>(parts - 1)) == static_cast<unsigned>(parts - 1);
-                        __threadfence();
+                    if (dt == 0) {  // the barrier and this release order every thread's sums before the count
+                        uint32_t old;
+                        asm volatile("fence.acq_rel.gpu;\n\tatom.inc.relaxed.gpu.global.u32 %0, [%1], %2;\n\tfence.acq_rel.gpu;"
+                                     : "=r"(old)
+                                     : "l"(a.counters + b0), "r"(static_cast<uint32_t>(parts - 1))
+                                     : "memory");
+                        s_last = old == static_cast<uint32_t>(parts - 1);
                     }
                     at_bar(3);
                     if (s_last) {
-                        for (int r = ow; r < valid; r += 4) {
-                            float m = kAtNoRef, l = 0.f;
-                            float4 o[ND];
+                        // Warp ow joins the rows ow, ow + 4, ...: lane = part for the weights, four elements for the sums.
+                        constexpr int RW = R / 4;
+                        auto part = [&](int p) {  // part p lies in CTA b0 + p: its first unit, but for a unit that starts inside CTA b0
+                            return a.partials + (static_cast<int64_t>(b0 + p) * 2 + (p == 0 && !b0_first ? 1 : 0)) * Sh::kPartial;
+                        };
+                        float m[RW], den[RW];
+                        float4 o[RW][ND];
 #pragma unroll
-                            for (int h = 0; h < ND; ++h) o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            for (int c0 = 0; c0 < parts; c0 += 32) {
-                                const int p = c0 + lane, cn = min(32, parts - c0);
-                                // Part p lies in CTA b0 + p: its first unit, but for a unit that starts inside CTA b0.
-                                auto part = [&](int q) {
-                                    return a.partials + (static_cast<int64_t>(b0 + q) * 2 + (q == 0 && !b0_first ? 1 : 0)) * Sh::kPartial;
-                                };
-                                const float pm = p < parts ? __ldcg(part(p) + R * ND * 128 + r) : kAtNoRef;
-                                const float pl = p < parts ? __ldcg(part(p) + R * ND * 128 + R + r) : 0.f;
-                                float top = fmaxf(m, pm);
+                        for (int k = 0; k < RW; ++k) {
+                            m[k] = kAtNoRef;
+                            den[k] = 0.f;
+#pragma unroll
+                            for (int h = 0; h < ND; ++h) o[k][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                        for (int c0 = 0; c0 < parts; c0 += 32) {
+                            const int cn = min(32, parts - c0);
+                            float pm[RW], pl[RW], wgt[RW];
+#pragma unroll
+                            for (int k = 0; k < RW; ++k) {
+                                const float *src = part(c0 + min(lane, cn - 1)) + R * ND * 128 + ow + 4 * k;
+                                pm[k] = __ldcg(src);
+                                pl[k] = __ldcg(src + R);
+                            }
+#pragma unroll
+                            for (int k = 0; k < RW; ++k) {
+                                float top = fmaxf(m[k], pm[k]);
 #pragma unroll
                                 for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                                const float keep = at_exp2(m - top), wgt = p < parts ? at_exp2(pm - top) : 0.f;
-                                float lw = pl * wgt;
+                                const float keep = at_exp2(m[k] - top);
+                                wgt[k] = lane < cn ? at_exp2(pm[k] - top) : 0.f;
+                                float x = lane < cn ? pl[k] * wgt[k] : 0.f;
 #pragma unroll
-                                for (int d = 16; d; d >>= 1) lw += __shfl_xor_sync(0xFFFFFFFFu, lw, d);
-                                l = l * keep + lw;
+                                for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+                                den[k] = den[k] * keep + x;
+                                m[k] = top;
 #pragma unroll
-                                for (int h = 0; h < ND; ++h) {
-                                    o[h].x *= keep;
-                                    o[h].y *= keep;
-                                    o[h].z *= keep;
-                                    o[h].w *= keep;
-                                }
-                                m = top;
-#pragma unroll 8
-                                for (int q = 0; q < cn; ++q) {
-                                    const float g = __shfl_sync(0xFFFFFFFFu, wgt, q);
-                                    const float4 *src = reinterpret_cast<const float4 *>(part(c0 + q) + r * (ND * 128)) + lane;
+                                for (int h = 0; h < ND; ++h)
+                                    o[k][h] = make_float4(o[k][h].x * keep, o[k][h].y * keep, o[k][h].z * keep, o[k][h].w * keep);
+                            }
+#pragma unroll 4
+                            for (int p = 0; p < cn; ++p) {
+                                const float4 *src = reinterpret_cast<const float4 *>(part(c0 + p) + ow * (ND * 128)) + lane;
+#pragma unroll
+                                for (int k = 0; k < RW; ++k) {
+                                    const float f = __shfl_sync(0xFFFFFFFFu, wgt[k], p);
 #pragma unroll
                                     for (int h = 0; h < ND; ++h) {
-                                        const float4 x = __ldcg(src + h * 32);
-                                        o[h].x = fmaf(x.x, g, o[h].x);
-                                        o[h].y = fmaf(x.y, g, o[h].y);
-                                        o[h].z = fmaf(x.z, g, o[h].z);
-                                        o[h].w = fmaf(x.w, g, o[h].w);
+                                        const float4 x = __ldcg(src + k * (4 * ND * 32) + h * 32);
+                                        o[k][h].x = fmaf(x.x, f, o[k][h].x);
+                                        o[k][h].y = fmaf(x.y, f, o[k][h].y);
+                                        o[k][h].z = fmaf(x.z, f, o[k][h].z);
+                                        o[k][h].w = fmaf(x.w, f, o[k][h].w);
                                     }
                                 }
                             }
-                            const float inv = l == 0.f ? 0.f : 1.f / l;
+                        }
+#pragma unroll
+                        for (int k = 0; k < RW; ++k) {
+                            const int r = ow + 4 * k;
+                            if (r >= valid) continue;
+                            const float inv = den[k] == 0.f ? 0.f : 1.f / den[k];
+                            const int64_t at = out_row(r) + 4 * lane;
 #pragma unroll
                             for (int h = 0; h < ND; ++h)
                                 if (4 * lane + h * 128 < a.head_dim)
-                                    at_store4(out + out_row(r) + 4 * lane + h * 128,
-                                              make_float4(o[h].x * inv, o[h].y * inv, o[h].z * inv, o[h].w * inv));
-                            if (a.lse && lane == 0) a.lse[lse_at(r)] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                                    at_store4(out + at + h * 128,
+                                              make_float4(o[k][h].x * inv, o[k][h].y * inv, o[k][h].z * inv, o[k][h].w * inv));
+                            if (a.lse && lane == 0) a.lse[lse_at(r)] = den[k] == 0.f ? -INFINITY : (m[k] + log2f(den[k])) * 0.6931471805599453f;
                         }
                     }
                 }
