@@ -18,212 +18,388 @@ struct LogprobArgs {
     unsigned int *status;
     int64_t stride;
     int vocab, top;
-    int slice;  // elements per CTA of a row's cluster (a multiple of 16)
+    int cluster;  // CTAs of a row
+    int words;    // 16-byte words of a row's slice
 };
 
 constexpr int kLpThreads = 512;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpGroups = 128;             // thread groups whose maxima bound the k-th largest
-constexpr int kLpGroupSize = kLpThreads / kLpGroups;
+constexpr int kLpGroups = 128;                           // thread groups whose maxima bound the k-th largest
+constexpr int kLpGroupSize = kLpThreads / kLpGroups;     // 4 lanes
 constexpr int kLpMaxTop = FP8BLK_MAX_TOP;
+constexpr int kLpCandidates = 1024;                      // room for what reaches the bound; more takes the slow selection
+constexpr int kLpMaxCluster = 8;
+constexpr float kLpLog2e = 1.4426950408889634f;
+constexpr float kLpFloor = -3.402823466e38f;             // reference of a thread that has seen nothing finite
+constexpr float kLpSlack = 20.0f;                        // a value may pass its thread's reference by this much
 
-// Order key of a logit: larger value first, -0 and +0 alike, NaN below all;
-// 0 is no logit's key but NaN's.
-__device__ __forceinline__ uint32_t value_key(float v) {
-    if (v != v) return 0u;
-    const uint32_t u = __float_as_uint(v + 0.0f);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-// Unique order of (value, index): the lowest index first among equal values.
+// Unique order of (value, index): larger values first, -0 and +0 alike, the
+// lowest index first among equal values, NaN below everything.
 __device__ __forceinline__ uint64_t full_key(float v, uint32_t index) {
-    return (static_cast<uint64_t>(value_key(v)) << 32) | (0xFFFFFFFFu - index);
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    const uint32_t key = v != v ? 0u : ((u & 0x80000000u) ? ~u : (u | 0x80000000u));
+    return (static_cast<uint64_t>(key) << 32) | (0xFFFFFFFFu - index);
+}
+// The next f32 above v (NaN above +inf and for NaN).
+__device__ __forceinline__ float next_up(float v) {
+    const int u = __float_as_int(v + 0.0f);
+    return __int_as_float(u >= 0 ? u + 1 : u - 1);
 }
 
+// 16 bytes of logits as f32.
 template <typename T>
-__device__ __forceinline__ float logit(const T *p) { return static_cast<float>(*p); }
+struct LpVec;
+template <>
+struct LpVec<float> {
+    static constexpr int kN = 4;
+    static __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[4]) {
+        x[0] = __uint_as_float(w.x);
+        x[1] = __uint_as_float(w.y);
+        x[2] = __uint_as_float(w.z);
+        x[3] = __uint_as_float(w.w);
+    }
+};
+template <>
+struct LpVec<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    static __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[8]) {
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = bf16x2_to_f32(v[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+};
 
-// What a CTA of the cluster tells the others.
+// What a CTA of the cluster tells the first.
 struct LpShare {
-    float max;
-    float sum, weighted;  // sum of e, sum of e * (x - max)
+    float max;            // largest value, NaN left out
+    float sum, weighted;  // of 2^y and of y 2^y, y = (x - max) log2 e; NaN if there is a NaN or +inf
     int rank;
     int n_top;
     uint64_t top[kLpMaxTop];
 };
 
-// One cluster per row, one slice of the row per CTA, held in shared memory as
-// f32: the row is read from global memory once, and the maximum, the sums and
-// the candidates each take a sweep of shared memory.
+// A whole word of a row, issued where it stands.
+__device__ __forceinline__ uint4 lp_load(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ float lp_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One cluster per row, one slice of the row per CTA, one pass over memory:
+// thread t takes the slice's 16-byte words t, t + 512, ... and keeps its own
+// reference, sum, weighted sum, maximum and rank count; what is joined, is
+// joined at the end.  The reference moves only when a value passes it by more
+// than 20, so the pass has no serial rescaling.
+//   The top: the k-th largest of 128 group maxima bounds the k-th largest of the
+// slice from below, so only threads whose own maximum reaches it hold
+// candidates; a warp each reads those threads' words again (out of L2: some 20
+// threads' worth), and the few candidates are ranked by counting.  Rows where too
+// many values tie with the bound are selected one by one.
+//   Bound: HBM (4 or 2 bytes a logit).  Per f32 logit about 9 instructions, a
+// third of the issue rate at full bandwidth.
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(const LogprobArgs a) {
-    extern __shared__ __align__(16) float s_x[];
-    __shared__ LpShare share;
-    __shared__ float w_f[kLpWarps], w_g[kLpWarps];
-    __shared__ int w_i[kLpWarps];
-    __shared__ uint64_t s_group[kLpGroups];
-    __shared__ uint64_t s_tau;
-    __shared__ int s_count;
+__global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_kernel(const LogprobArgs a) {
+    constexpr int V = LpVec<T>::kN, UN = 4;
+    __shared__ LpShare s_all[kLpMaxCluster];  // of every CTA, in the cluster's first
+    __shared__ uint64_t s_top[kLpMaxTop];
+    __shared__ float w_max[kLpWarps], w_sum[kLpWarps], w_wgt[kLpWarps];
+    __shared__ int w_rank[kLpWarps];
+    __shared__ __align__(16) float s_group[kLpGroups];
+    __shared__ float s_bound;
+    __shared__ int s_hot[kLpThreads], s_hots, s_count;
+    __shared__ uint64_t s_cand[kLpCandidates], w_best[kLpWarps];
     cg::cluster_group cluster = cg::this_cluster();
-    const int c = static_cast<int>(cluster.block_rank()), nc = static_cast<int>(cluster.num_blocks());
+    const int nc = a.cluster, c = nc > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+    // The first CTA's shared memory is written to below: it has to have started.
+    if (nc > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / nc;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int base = c * a.slice;
-    const int count = max(0, min(a.slice, a.vocab - base));
-    const T *x = static_cast<const T *>(a.logits) + row * a.stride + base;
-    uint64_t *cand = reinterpret_cast<uint64_t *>(s_x + a.slice);
+    const T *x = static_cast<const T *>(a.logits) + row * a.stride;
+    // The row as 16-byte words: word w holds elements [w V - off, w V - off + V); the first and last may be partial.
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    const uint4 *words = reinterpret_cast<const uint4 *>(x - off);
+    const int n_words = (a.vocab + off + V - 1) / V;
+    const int w0 = c * a.words, w1 = min(w0 + a.words, n_words);
 
-    // Sweep 1: the slice into shared memory, its maximum, and each thread's best key.
-    float mx = -INFINITY;
-    bool nan = false;
-    uint64_t best = 0;
-    for (int i = tid; i < count; i += kLpThreads) {
-        const float v = logit(x + i);
-        s_x[i] = v;
-        mx = fmaxf(mx, v);
-        nan |= v != v;
-        if (a.top > 0) {
-            const uint64_t k = full_key(v, base + i);
-            best = k > best ? k : best;
-        }
-    }
-    mx = nan ? __int_as_float(0x7FC00000) : mx;
-    // Maximum over the CTA; a NaN anywhere wins.
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const float o = __shfl_xor_sync(0xFFFFFFFFu, mx, d);
-        mx = (mx != mx || o != o) ? __int_as_float(0x7FC00000) : fmaxf(mx, o);
-    }
-    if (lane == 0) w_f[warp] = mx;
-#pragma unroll
-    for (int d = 1; d < kLpGroupSize; d <<= 1) {
-        const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, best, d);
-        best = o > best ? o : best;
-    }
-    if (tid % kLpGroupSize == 0) s_group[tid / kLpGroupSize] = best;
-    if (tid == 0) {
-        s_count = 0;
-        s_tau = 0;
-    }
-    __syncthreads();
-    if (tid == 0) {
-        float m = w_f[0];
-        for (int w = 1; w < kLpWarps; ++w) m = (m != m || w_f[w] != w_f[w]) ? __int_as_float(0x7FC00000) : fmaxf(m, w_f[w]);
-        share.max = m;
-    }
-    // tau = the k-th largest group maximum: at least k elements reach it, and
-    // only elements of k groups can.
-    if (a.top > 0 && tid < kLpGroups) {
-        const uint64_t mine = s_group[tid];
-        int above = 0;
-        for (int g = 0; g < kLpGroups; ++g) above += s_group[g] > mine;
-        if (above == a.top - 1) s_tau = mine;
-    }
-    cluster.sync();
-    float m = -INFINITY;
-    for (int r = 0; r < nc; ++r) {
-        const float o = cluster.map_shared_rank(&share, r)->max;
-        m = (m != m || o != o) ? __int_as_float(0x7FC00000) : fmaxf(m, o);
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
+    const int g0 = off == 0 ? w0 : max(w0, 1), g1 = min(w1, (a.vocab + off) / V);  // whole words of the slice
 
-    // Sweep 2: sums, rank and candidates.
+    // The first words are on their way before the target's logit is asked for.
+    int w = w0 + tid;
+    const bool leads = w < g0 && w < w1;  // the row's first word, partial
+    if (leads) w += kLpThreads;
+    const int w_first = w;
+    uint4 next[UN];
+    auto fetch = [&](int at) {
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            if (at + u * kLpThreads < g1) next[u] = lp_load(words + at + u * kLpThreads);
+    };
+    fetch(w);
     const int target = a.targets[row];
     const bool has_target = target >= 0 && target < a.vocab;
-    const uint64_t tkey = has_target ? full_key(logit(static_cast<const T *>(a.logits) + row * a.stride + target), target) : ~0ull;
-    const uint64_t tau = s_tau;
-    float sum = 0.f, weighted = 0.f;
+    const float t = has_target ? static_cast<float>(x[target]) : __int_as_float(0x7FC00000);
+
+    float ref = kLpFloor, top = -INFINITY, sum = 0.f, weighted = 0.f;
     int rank = 0;
-    for (int i = tid; i < count; i += kLpThreads) {
-        const float v = s_x[i];
-        const float d = v - ref, e = __expf(d);
+    auto raise = [&](float m) {  // a new reference; m > ref
+        const float d = (ref - m) * kLpLog2e, f = lp_exp2(d);
+        weighted = f == 0.f ? 0.f : f * fmaf(sum, d, weighted);
+        sum *= f;
+        ref = m;
+    };
+    auto add = [&](float v) {
+        const float y = (v - ref) * kLpLog2e, e = lp_exp2(y);
         sum += e;
-        if (e > 0.f) weighted = fmaf(e, d, weighted);
-        const uint64_t k = full_key(v, base + i);
-        rank += k > tkey;
-        if (a.top > 0 && k >= tau) cand[atomicAdd(&s_count, 1)] = k;
-    }
+        weighted = fmaf(e, fmaxf(y, kLpFloor), weighted);
+    };
+    auto word = [&](int w, const uint4 &bits) {  // a whole word
+        float v[V];
+        LpVec<T>::unpack(bits, v);
+        float m = v[0];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        weighted += __shfl_xor_sync(0xFFFFFFFFu, weighted, d);
-        rank += __shfl_xor_sync(0xFFFFFFFFu, rank, d);
+        for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
+        if (m > ref + kLpSlack) raise(m);
+        top = fmaxf(top, m);
+#pragma unroll
+        for (int i = 0; i < V; ++i) add(v[i]);
+        if (m >= t) {  // some may come before the target
+            const int e0 = w * V - off;
+            const float bar = e0 + V <= target ? t : next_up(t);
+#pragma unroll
+            for (int i = 0; i < V; ++i) rank += v[i] >= bar;
+            if (e0 <= target && target < e0 + V) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) rank += e0 + i < target && v[i] == t;
+            }
+        }
+    };
+    auto element = [&](int i, float v) {  // one of a partial word
+        if (v > ref + kLpSlack) raise(v);
+        top = fmaxf(top, v);
+        add(v);
+        rank += v > t || (v == t && i < target);
+    };
+    auto partial = [&](int w) {
+        for (int i = max(0, w * V - off); i < min(a.vocab, w * V - off + V); ++i) element(i, static_cast<float>(x[i]));
+    };
+    if (leads) partial(w_first - kLpThreads);
+    while (w < g1) {
+        uint4 bits[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) bits[u] = next[u];
+        fetch(w + UN * kLpThreads);
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            if (w + u * kLpThreads < g1) word(w + u * kLpThreads, bits[u]);
+        w += UN * kLpThreads;
     }
-    if (lane == 0) {
-        w_f[warp] = sum;
-        w_g[warp] = weighted;
-        w_i[warp] = rank;
+    if (g1 < w1 && g1 >= g0 && (g1 - w0) % kLpThreads == tid) partial(g1);  // the row's last word, partial
+    if (has_target && t != t) {  // a NaN target: every number comes before it, and the NaNs of lower index
+        rank = 0;
+        for (int w = w0 + tid; w < w1; w += kLpThreads)
+            for (int i = max(0, w * V - off); i < min(a.vocab, w * V - off + V); ++i) {
+                const float v = static_cast<float>(x[i]);
+                rank += v == v || i < target;
+            }
+    }
+
+    // ---- the slice's maximum and the bound on its k-th largest
+    float m = top;
+#pragma unroll
+    for (int d = 1; d < kLpGroupSize; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    if ((tid & (kLpGroupSize - 1)) == 0) s_group[tid / kLpGroupSize] = m;
+#pragma unroll
+    for (int d = kLpGroupSize; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    if (lane == 0) w_max[warp] = m;
+    if (tid == 0) {
+        s_hots = 0;
+        s_count = 0;
     }
     __syncthreads();
-    if (tid == 0) {
-        float fs = 0.f, gs = 0.f;
-        int is = 0;
-        for (int w = 0; w < kLpWarps; ++w) {
-            fs += w_f[w];
-            gs += w_g[w];
-            is += w_i[w];
+    m = w_max[lane & (kLpWarps - 1)];
+#pragma unroll
+    for (int d = 1; d < kLpWarps; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    const float slice_max = m, base = fmaxf(m, kLpFloor);
+    if (a.top > 0 && tid < kLpGroups) {
+        const float mine = s_group[tid];
+        int above = 0, level = 0;
+#pragma unroll 8
+        for (int g = 0; g < kLpGroups; g += 4) {
+            const float4 o = *reinterpret_cast<const float4 *>(s_group + g);
+            above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+            level += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
         }
-        share.sum = fs;
-        share.weighted = gs;
-        share.rank = is;
-        share.n_top = min(s_count, a.top);
+        if (above < a.top && above + level >= a.top) s_bound = mine;
     }
-    // The slice's top: each candidate's place is the number of larger ones.
-    if (a.top > 0) {
-        const int n = s_count;
-        for (int i = tid; i < n; i += kLpThreads) {
-            const uint64_t k = cand[i];
-            int above = 0;
-            for (int j = 0; j < n; ++j) above += cand[j] > k;
-            if (above < a.top) share.top[above] = k;
+    // ---- the slice's sums, at its own maximum
+    {
+        const float d = (ref - base) * kLpLog2e, f = lp_exp2(d);
+        float ws = f == 0.f && sum == sum ? 0.f : f * fmaf(sum, d, weighted), ss = sum * f;
+        int rr = rank;
+#pragma unroll
+        for (int k = 16; k; k >>= 1) {
+            ss += __shfl_xor_sync(0xFFFFFFFFu, ss, k);
+            ws += __shfl_xor_sync(0xFFFFFFFFu, ws, k);
+            rr += __shfl_xor_sync(0xFFFFFFFFu, rr, k);
+        }
+        if (lane == 0) {
+            w_sum[warp] = ss;
+            w_wgt[warp] = ws;
+            w_rank[warp] = rr;
         }
     }
-    cluster.sync();
-    if (c == 0) {
-        float total = 0.f, wsum = 0.f;
-        int rk = 0;
-        for (int r = 0; r < nc; ++r) {
-            const LpShare *o = cluster.map_shared_rank(&share, r);
-            total += o->sum;
-            wsum += o->weighted;
-            rk += o->rank;
+    __syncthreads();
+    if (warp == 0) {
+        float ss = lane < kLpWarps ? w_sum[lane] : 0.f, ws = lane < kLpWarps ? w_wgt[lane] : 0.f;
+        int rr = lane < kLpWarps ? w_rank[lane] : 0;
+#pragma unroll
+        for (int k = kLpWarps / 2; k; k >>= 1) {
+            ss += __shfl_xor_sync(0xFFFFFFFFu, ss, k);
+            ws += __shfl_xor_sync(0xFFFFFFFFu, ws, k);
+            rr += __shfl_xor_sync(0xFFFFFFFFu, rr, k);
         }
-        const float logz = logf(total);
-        if (tid == 0) {
-            const float nanf = __int_as_float(0x7FC00000);
-            if (has_target) {
-                const float t = logit(static_cast<const T *>(a.logits) + row * a.stride + target);
-                a.logprob[row] = m == -INFINITY ? nanf : (t - m) - logz;
-                a.rank[row] = rk;
-            } else {
-                a.logprob[row] = nanf;
-                a.rank[row] = -1;
-                if (target != -1) atomicOr(a.status, FP8BLK_STATUS_BAD_TARGET);
+        __syncwarp();
+        if (lane == 0) {
+            w_sum[0] = ss;
+            w_wgt[0] = ws;
+            w_rank[0] = rr;
+        }
+    }
+
+    // ---- the slice's top: candidates out of the hot threads' words, ranked by counting
+    const int elements = max(0, min(a.vocab, w1 * V - off) - max(0, w0 * V - off));
+    const int want = min(a.top, elements);
+    if (want > 0) {
+        const float bound = s_bound;
+        if (w0 + tid < w1 && !(top < bound)) s_hot[atomicAdd(&s_hots, 1)] = tid;
+        __syncthreads();
+        const int hots = s_hots;
+        for (int h = warp; h < hots; h += kLpWarps)
+            for (int w = w0 + s_hot[h] + lane * kLpThreads; w < w1; w += 32 * kLpThreads) {
+                float v[V];
+                const int e0 = w * V - off;
+                const bool full = w >= g0 && w < g1;
+                if (full) LpVec<T>::unpack(lp_load(words + w), v);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if (!full) {
+                        if (e0 + i < 0 || e0 + i >= a.vocab) continue;
+                        v[i] = static_cast<float>(x[e0 + i]);
+                    }
+                    if (v[i] < bound || (v[i] != v[i] && bound != -INFINITY)) continue;
+                    const int at = atomicAdd(&s_count, 1);
+                    if (at < kLpCandidates) s_cand[at] = full_key(v[i], e0 + i);
+                }
             }
-            a.entropy[row] = m == -INFINITY ? nanf : logz - wsum / total;
+        __syncthreads();
+        const int n = s_count;
+        if (n <= kLpCandidates) {
+            for (int i = tid; i < n; i += kLpThreads) {
+                const uint64_t k = s_cand[i];
+                int above = 0;
+                for (int j = 0; j < n; ++j) above += s_cand[j] > k;
+                if (above < want) s_top[above] = k;
+            }
+        } else {  // too many at the bound: the next largest key, `want` times
+            uint64_t last = ~0ull;
+            for (int k = 0; k < want; ++k) {
+                uint64_t best = 0;
+                for (int w = w0 + tid; w < w1; w += kLpThreads)
+                    for (int i = max(0, w * V - off); i < min(a.vocab, w * V - off + V); ++i) {
+                        const uint64_t key = full_key(static_cast<float>(x[i]), i);
+                        if (key < last && key > best) best = key;
+                    }
+#pragma unroll
+                for (int d = 16; d; d >>= 1) {
+                    const uint64_t o = __shfl_xor_sync(0xFFFFFFFFu, best, d);
+                    best = o > best ? o : best;
+                }
+                if (lane == 0) w_best[warp] = best;
+                __syncthreads();
+                for (int w = 0; w < kLpWarps; ++w) best = w_best[w] > best ? w_best[w] : best;
+                last = best;
+                if (tid == 0) s_top[k] = best;
+                __syncthreads();
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- into the first CTA's shared memory (no CTA waits for it but the first), and the row
+    {
+        if (nc > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        LpShare *to = nc > 1 ? cluster.map_shared_rank(&s_all[c], 0) : &s_all[0];
+        if (tid < want) to->top[tid] = s_top[tid];
+        if (tid == 0) {
+            to->max = slice_max;
+            to->sum = w_sum[0];
+            to->weighted = w_wgt[0];
+            to->rank = w_rank[0];
+            to->n_top = want;
+        }
+        if (nc > 1) {
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+            if (c != 0) return;
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        } else {
+            __syncthreads();
+        }
+    }
+    {
+        float peak = -INFINITY;
+        for (int r = 0; r < nc; ++r) peak = fmaxf(peak, s_all[r].max);
+        const float ground = fmaxf(peak, kLpFloor);
+        float total = 0.f, wsum = 0.f;
+        int before = 0;
+        for (int r = 0; r < nc; ++r) {
+            const LpShare &o = s_all[r];
+            const float d = (fmaxf(o.max, kLpFloor) - ground) * kLpLog2e, f = lp_exp2(d), s = o.sum;
+            total += s * f;
+            if (f != 0.f || s != s) wsum += f * fmaf(s, d, o.weighted);
+            before += o.rank;
+        }
+        const float nanf = __int_as_float(0x7FC00000);
+        const float logz = peak == -INFINITY ? nanf : logf(total);
+        if (tid == 0) {
+            a.logprob[row] = has_target ? (t - ground) - logz : nanf;
+            a.rank[row] = has_target ? before : -1;
+            a.entropy[row] = logz - wsum / total * 0.6931471805599453f;
+            if (!has_target && target != -1) atomicOr(a.status, FP8BLK_STATUS_BAD_TARGET);
         }
         // Merge the slices' sorted lists: a key's place is the sum of its places.
         for (int i = tid; i < nc * a.top; i += kLpThreads) {
             const int r = i / a.top, j = i - r * a.top;
-            const LpShare *o = cluster.map_shared_rank(&share, r);
-            if (j >= o->n_top) continue;
-            const uint64_t k = o->top[j];
+            if (j >= s_all[r].n_top) continue;
+            const uint64_t k = s_all[r].top[j];
             int place = j;
-            for (int s = 0; s < nc && place < a.top; ++s) {
+            for (int s = 0; s < nc; ++s) {
                 if (s == r) continue;
-                const LpShare *p = cluster.map_shared_rank(&share, s);
-                for (int y = 0; y < p->n_top && p->top[y] > k; ++y) ++place;
+                int lo = 0, hi = s_all[s].n_top;  // the first entry that is not above k
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_all[s].top[mid] > k) lo = mid + 1;
+                    else hi = mid;
+                }
+                place += lo;
             }
             if (place < a.top) {
                 const uint32_t id = 0xFFFFFFFFu - static_cast<uint32_t>(k);
-                const float t = logit(static_cast<const T *>(a.logits) + row * a.stride + id);
                 a.top_ids[row * a.top + place] = static_cast<int32_t>(id);
-                a.top_logprobs[row * a.top + place] = m == -INFINITY ? __int_as_float(0x7FC00000) : (t - m) - logz;
+                a.top_logprobs[row * a.top + place] = (static_cast<float>(x[id]) - ground) - logz;
             }
         }
     }
-    cluster.sync();  // the others' shared memory is read above
 }
 
 }  // namespace fp8blk
@@ -244,23 +420,17 @@ extern "C" int fp8blk_token_logprobs(const void *logits, int dtype, const int32_
         return FP8BLK_EALIGN;
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
-    LogprobArgs a = {logits, targets, logprob, entropy, rank, top_ids, top_logprobs, dev.status, stride,
-                     static_cast<int>(vocab), top, 0};
-    // Slices of at most 32768 elements; more CTAs per row while there are fewer than one per SM.
+    // CTAs of a row: more while a call has fewer than two per SM and slices stay above 8 KiB.  Two CTAs fit on an SM;
+    // the one that streams covers the other's reductions, so one CTA per row is best when there are rows enough.
+    const int64_t bytes = vocab * es;
     int nc = 1;
-    while (nc < 8 && ((vocab + nc - 1) / nc > 32768 || (n_rows * nc < dev.sms && vocab / nc > 4096))) nc *= 2;
-    a.slice = static_cast<int>(((vocab + nc - 1) / nc + 15) / 16 * 16);
-    const size_t cand = top > 0 ? static_cast<size_t>(top) * kLpGroupSize * ((a.slice + kLpThreads - 1) / kLpThreads) * 8 : 0;
-    const size_t smem = static_cast<size_t>(a.slice) * 4 + cand;
-    const void *kernel = dtype == FP8BLK_F32 ? reinterpret_cast<const void *>(token_logprobs_kernel<float>)
-                                             : reinterpret_cast<const void *>(token_logprobs_kernel<__nv_bfloat16>);
-    int per_sm = 0;
-    cudaError_t err = kernel_occupancy(kernel, kLpThreads, smem, &per_sm);
-    if (err != cudaSuccess || per_sm < 1) return step_from_cuda(err != cudaSuccess ? err : cudaErrorInvalidConfiguration);
+    while (nc < kLpMaxCluster && n_rows * nc < 2 * dev.sms && bytes / nc > 16384) nc *= 2;
+    const int64_t words = (bytes + 15) / 16 + 1;  // a row that starts inside a word reaches into one more
+    LogprobArgs a = {logits, targets, logprob, entropy, rank, top_ids, top_logprobs, dev.status, stride,
+                     static_cast<int>(vocab), top, nc, static_cast<int>((words + nc - 1) / nc)};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n_rows * nc));
     cfg.blockDim = dim3(kLpThreads);
-    cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
