@@ -57,6 +57,7 @@ __device__ __forceinline__ MapRequest map_request(const MapArgs &a, int r) {
 __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const MapArgs a) {
     __shared__ int64_t s_tok[kMapThreads + 1], s_blk[kMapThreads + 1];  // exclusive prefixes per thread
     __shared__ int64_t w_tok[kMapThreads / 32], w_blk[kMapThreads / 32];
+    __shared__ MapRequest s_req[kMapThreads];  // the requests themselves, when each thread scans at most one
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
     grid_launch_dependents();
@@ -66,6 +67,7 @@ __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const MapArgs a) {
     bool bad = false;
     for (int r = r0; r < r1; ++r) {
         const MapRequest m = map_request(a, r);
+        s_req[tid] = m;
         tok += m.fresh;
         blk += m.wanted - m.held;
         bad |= m.bad;
@@ -117,6 +119,7 @@ __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const MapArgs a) {
         if (bad) atomicOr(a.status, FP8BLK_STATUS_BAD_KV);
     }
 
+    auto request = [&](int r) { return q == 1 ? s_req[r] : map_request(a, r); };
     // The thread whose prefix range holds `at` (< the last entry): the last
     // one with prefix <= at, so threads without a share are passed over.
     auto find = [&](const int64_t *s, int64_t at) {
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const MapArgs a) {
         const int t = find(s_blk, e);
         int64_t at = s_blk[t];
         for (int r = t * q; r < a.n; ++r) {
-            const MapRequest m = map_request(a, r);
+            const MapRequest m = request(r);
             const int32_t need = m.wanted - m.held;
             if (e < at + need) {
                 a.table[static_cast<int64_t>(r) * a.width + m.held + (e - at)] = fresh_block(head + e);
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const MapArgs a) {
             if (r < 0) {
                 const int i = find(s_tok, t);
                 r = i * q;
-                m = map_request(a, r);
+                m = request(r);
                 start = s_tok[i];
                 end = start + m.fresh;
                 first = s_blk[i];
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const MapArgs a) {
             while (t >= end) {
                 first += m.wanted - m.held;
                 start = end;
-                m = map_request(a, ++r);
+                m = request(++r);
                 end = start + m.fresh;
             }
             pos[j] = static_cast<int32_t>(m.ctx + (t - start));
@@ -210,21 +213,8 @@ struct AppendArgs {
     int64_t n_tokens, k_stride, v_stride;  // strides in elements
     int64_t n_slots;                       // n_blocks * block_tokens
     int kv_heads, head_dim, block_log2;
+    int chunk;                             // tokens a CTA looks after
 };
-
-// Four consecutive values as f32.
-template <typename T>
-__device__ __forceinline__ float4 load4(const T *p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float *p) {
-    return *reinterpret_cast<const float4 *>(p);
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    const float2 lo = bf16x2_to_f32(w.x), hi = bf16x2_to_f32(w.y);
-    return make_float4(lo.x, lo.y, hi.x, hi.y);
-}
 
 // |v| for a block's maximum: what is not finite does not count.
 __device__ __forceinline__ uint32_t finite_abs_bits(float v) {
@@ -248,67 +238,91 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
     return r;
 }
 __device__ __forceinline__ float poison_inf(float v) { return isfinite(v) ? v : __int_as_float(0x7FC00000); }
-__device__ __forceinline__ uint32_t encode4(float4 x, float inv) {
-    const uint32_t lo = to_e4m3x2(poison_inf(x.x) * inv, poison_inf(x.y) * inv);
-    const uint32_t hi = to_e4m3x2(poison_inf(x.z) * inv, poison_inf(x.w) * inv);
-    return lo | (hi << 16);
-}
 
-constexpr int kAppendWarps = 4;
-
-// A run is a maximal group of consecutive tokens with consecutive slots of one
-// block; its first token leads it.  One warp per (run, head, K or V): maximum,
-// then encode (the second read of the run comes from L1).
+// Eight consecutive values as they lie in memory: two or one 16-byte words.
 template <typename T>
-__global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const AppendArgs a) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.y;
-    const bool is_v = blockIdx.z != 0;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp;
-    if (t >= a.n_tokens) return;
-    const int64_t slot = a.slots[t];
-    if (slot < 0) return;
-    if (slot >= a.n_slots) {
-        if (lane == 0) atomicOr(a.status, FP8BLK_STATUS_BAD_KV);
-        return;
+struct Eight;
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = *reinterpret_cast<const float4 *>(p);
+        b = *reinterpret_cast<const float4 *>(p + 4);
     }
-    const int block = 1 << a.block_log2;
-    const int off = static_cast<int>(slot & (block - 1));
-    if (off != 0 && t > 0 && a.slots[t - 1] == slot - 1) return;  // another token leads this run
-    // The run's length: consecutive slots up to the block's end.
-    int run = 1;
-    for (int base = 1; base < block - off; base += 32) {
-        const int j = base + lane;
-        const bool follows = j < block - off && t + j < a.n_tokens && a.slots[t + j] == slot + j;
-        const unsigned stop = __ballot_sync(0xFFFFFFFFu, !follows);
-        if (stop) {
-            run += __ffs(stop) - 1;
-            break;
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = bf16x2_to_f32(w[i]);
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
         }
-        run += 32;
     }
-    const int D = a.head_dim;
+};
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kAppendHeld = 4;       // groups of eight values a thread keeps between its two passes
+constexpr int kAppendMaxChunk = 64;  // tokens a CTA looks after
+
+// One run for one head of K or V: maximum, scale, codes.  THREADS threads (a
+// warp, or the CTA) take the run's groups of eight in turn; the first
+// kAppendHeld groups of a thread stay in registers, so that runs of up to 8192
+// values (a CTA) or 1024 (a warp) are read once, and the rest comes from L1.
+// red: a word per warp (CTA only).
+template <typename T, int THREADS>
+__device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64_t slot, int run, int h, bool is_v, int tid,
+                                           uint32_t *red) {
+    const int D = a.head_dim, block = 1 << a.block_log2, off = static_cast<int>(slot & (block - 1));
     const int64_t stride = is_v ? a.v_stride : a.k_stride;
     const T *x = static_cast<const T *>(is_v ? a.v : a.k) + t * stride + static_cast<int64_t>(h) * D;
     const int64_t bh = (slot >> a.block_log2) * a.kv_heads + h;
     uint8_t *codes = (is_v ? a.v_codes : a.k_codes) + bh * block * D;
     float *scale = (is_v ? a.v_scales : a.k_scales) + bh;
-    const int per = D / 4, total = run * per;
-    uint32_t amax = 0;
-    for (int i = lane; i < total; i += 32) {
+    const int per = D / 8, total = run * per;
+    auto at = [&](int i) {
         const int row = i / per;
-        const float4 f = load4<T>(x + row * stride + 4 * (i - row * per));
-        amax = max(amax, max(max(finite_abs_bits(f.x), finite_abs_bits(f.y)), max(finite_abs_bits(f.z), finite_abs_bits(f.w))));
+        return x + row * stride + 8 * (i - row * per);
+    };
+    Eight<T> held[kAppendHeld];
+#pragma unroll
+    for (int k = 0; k < kAppendHeld; ++k)
+        if (tid + k * THREADS < total) held[k].load(at(tid + k * THREADS));
+    const float old = off > 0 ? *scale : 0.f;
+    uint32_t amax = 0;
+    auto peak = [&](const Eight<T> &e) {
+        float f[8];
+        e.get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = max(amax, finite_abs_bits(f[j]));
+    };
+#pragma unroll
+    for (int k = 0; k < kAppendHeld; ++k)
+        if (tid + k * THREADS < total) peak(held[k]);
+    for (int i = tid + kAppendHeld * THREADS; i < total; i += THREADS) {
+        Eight<T> e;
+        e.load(at(i));
+        peak(e);
     }
-    float s = __uint_as_float(static_cast<uint32_t>(scale_exponent(__reduce_max_sync(0xFFFFFFFFu, amax))) << 23);
+    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+    if constexpr (THREADS > 32) {
+        if ((tid & 31) == 0) red[tid >> 5] = amax;
+        __syncthreads();
+        amax = __reduce_max_sync(0xFFFFFFFFu, red[tid & (THREADS / 32 - 1)]);
+    }
+    float s = __uint_as_float(static_cast<uint32_t>(scale_exponent(amax)) << 23);
     if (off > 0) {
-        const float old = *scale;
         if (old < s) {  // the codes that were there follow the larger scale: a product by a power of two, rounded once
             const float ratio = old / s;
             uint32_t *w = reinterpret_cast<uint32_t *>(codes);
-            for (int i = lane; i < off * per; i += 32) {
+            for (int i = tid; i < off * per * 2; i += THREADS) {
                 float2 lo, hi;
                 e4m3x4_to_f32(w[i], lo, hi);
                 w[i] = to_e4m3x2(lo.x * ratio, lo.y * ratio) | (to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16);
@@ -318,13 +332,85 @@ __global__ void __launch_bounds__(kAppendWarps * 32) kv_append_kernel(const Appe
         }
     }
     const float inv = 1.0f / s;
-    uint32_t *w = reinterpret_cast<uint32_t *>(codes + static_cast<int64_t>(off) * D);
-    for (int i = lane; i < total; i += 32) {
-        const int row = i / per;
-        w[i] = encode4(load4<T>(x + row * stride + 4 * (i - row * per)), inv);
+    uint2 *w = reinterpret_cast<uint2 *>(codes + static_cast<int64_t>(off) * D);
+    auto encode = [&](const Eight<T> &e, int i) {
+        float f[8];
+        e.get(f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = poison_inf(f[j]) * inv;
+        w[i] = make_uint2(to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16), to_e4m3x2(f[4], f[5]) | (to_e4m3x2(f[6], f[7]) << 16));
+    };
+#pragma unroll
+    for (int k = 0; k < kAppendHeld; ++k)
+        if (tid + k * THREADS < total) encode(held[k], tid + k * THREADS);
+    for (int i = tid + kAppendHeld * THREADS; i < total; i += THREADS) {
+        Eight<T> e;
+        e.load(at(i));
+        encode(e, i);
     }
-    __syncwarp();
-    if (lane == 0) *scale = s;
+    if constexpr (THREADS > 32) __syncthreads();  // red and the old scale have been read
+    else __syncwarp();
+    if (tid == 0) *scale = s;
+}
+
+// A run is a maximal group of consecutive tokens with consecutive slots of one
+// block; its first token leads it, and the CTA whose chunk holds that token
+// writes it.  Chunks with few leaders (prompts) take one run at a time with the
+// whole CTA, chunks with many (decode) a warp per run.
+//   Bound: HBM for prompts (es bytes in, 1 out per value), latency for decode.
+template <typename T>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
+    __shared__ int s_lead[kAppendMaxChunk], s_leads, s_run;
+    __shared__ uint32_t red[kAppendWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.y;
+    const bool is_v = blockIdx.z != 0;
+    const int block = 1 << a.block_log2;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
+    const int here = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.n_tokens - t0));
+    if (tid == 0) {
+        s_leads = 0;
+        s_run = block;
+    }
+    __syncthreads();
+    if (tid < here) {
+        const int64_t slot = a.slots[t0 + tid], before = t0 + tid > 0 ? a.slots[t0 + tid - 1] : -1;
+        if (slot >= a.n_slots) atomicOr(a.status, FP8BLK_STATUS_BAD_KV);
+        else if (slot >= 0 && ((slot & (block - 1)) == 0 || before != slot - 1)) s_lead[atomicAdd(&s_leads, 1)] = tid;
+    }
+    __syncthreads();
+    const int leads = s_leads;
+    if (leads >= kAppendWarps / 2 || (here <= 32 && leads * 8 >= here)) {
+        for (int i = warp; i < leads; i += kAppendWarps) {
+            const int64_t t = t0 + s_lead[i], slot = a.slots[t];
+            const int most = block - static_cast<int>(slot & (block - 1));
+            int run = 1;
+            for (int base = 1; base < most; base += 32) {
+                const int j = base + lane;
+                const bool follows = j < most && t + j < a.n_tokens && a.slots[t + j] == slot + j;
+                const unsigned stop = __ballot_sync(0xFFFFFFFFu, !follows);
+                if (stop) {
+                    run += __ffs(stop) - 1;
+                    break;
+                }
+                run += 32;
+            }
+            append_run<T, 32>(a, t, slot, run, h, is_v, lane, nullptr);
+        }
+    } else {
+        for (int i = 0; i < leads; ++i) {
+            const int64_t t = t0 + s_lead[i], slot = a.slots[t];
+            const int most = block - static_cast<int>(slot & (block - 1));
+            if (tid > 0 && tid < most && !(t + tid < a.n_tokens && a.slots[t + tid] == slot + tid)) atomicMin(&s_run, tid);
+            __syncthreads();
+            const int run = min(s_run, most);
+            append_run<T, kAppendThreads>(a, t, slot, run, h, is_v, tid, red);
+            if (tid == 0) s_run = block;
+            __syncthreads();
+        }
+    }
 }
 
 }  // namespace fp8blk
@@ -351,7 +437,7 @@ extern "C" int fp8blk_kv_map(const int32_t *ctx_lens, const int32_t *new_lens, i
     MapArgs a = {ctx_lens, new_lens, block_table, free_blocks, free_head, seq_lens, q_starts, slots, positions,
                  free_head_out, dev.status, n_seqs, max_blocks, n_free, step_log2(block_tokens), max_tokens};
     int64_t grid = (max_tokens + kMapThreads * kMapPerThread - 1) / (kMapThreads * kMapPerThread);
-    if (grid > dev.sms) grid = dev.sms;
+    if (grid > 3 * dev.sms) grid = 3 * dev.sms;
     return step_from_cuda(step_launch(kv_map_kernel, dim3(static_cast<unsigned>(grid)), kMapThreads, 0,
                                       static_cast<cudaStream_t>(stream), a));
 }
@@ -371,10 +457,13 @@ extern "C" int fp8blk_kv_append(const void *k, const void *v, int dtype, const i
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
     AppendArgs a = {k, v, slots, k_codes, v_codes, k_scales, v_scales, dev.status, n_tokens, k_stride, v_stride,
-                    n_blocks * block_tokens, kv_heads, head_dim, step_log2(block_tokens)};
-    const dim3 grid(static_cast<unsigned>((n_tokens + kAppendWarps - 1) / kAppendWarps), static_cast<unsigned>(kv_heads), 2);
+                    n_blocks * block_tokens, kv_heads, head_dim, step_log2(block_tokens), 4};
+    // Tokens per CTA: about one run of a prompt when there are tokens enough to fill the SMs, down to a few tokens (a
+    // warp each) for a decode step.
+    while (a.chunk < kAppendMaxChunk && n_tokens * kv_heads * 2 / (2 * a.chunk) >= 8 * dev.sms) a.chunk *= 2;
+    const dim3 grid(static_cast<unsigned>((n_tokens + a.chunk - 1) / a.chunk), static_cast<unsigned>(kv_heads), 2);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return step_from_cuda(dtype == FP8BLK_F32
-                              ? step_launch(kv_append_kernel<float>, grid, kAppendWarps * 32, 0, s, a)
-                              : step_launch(kv_append_kernel<__nv_bfloat16>, grid, kAppendWarps * 32, 0, s, a));
+                              ? step_launch(kv_append_kernel<float>, grid, kAppendThreads, 0, s, a)
+                              : step_launch(kv_append_kernel<__nv_bfloat16>, grid, kAppendThreads, 0, s, a));
 }
