@@ -110,10 +110,13 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return t.data_ptr()
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object around it
+
+
 def _stream(t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError("tensor must be on a CUDA device")
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(t.get_device())
 
 
 def abi_version() -> int:
