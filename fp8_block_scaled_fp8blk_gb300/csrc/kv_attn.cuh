@@ -126,6 +126,15 @@ __device__ __forceinline__ void at_ld(uint32_t taddr, float *v) {
 }
 __device__ __forceinline__ void at_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// v rounded to four significant bits, no finer than e4m3's subnormal step 2^-9:
+// exactly an e4m3 value for |v| < 2^8, so a plane's residual needs no decoding
+// (conversions out of e4m3 run at an eighth of the rate of these).  Halves go
+// away from zero; the next plane takes what is left either way.  NaN stays NaN.
+__device__ __forceinline__ float at_plane(float v) {
+    const float h = __int_as_float((__float_as_int(v) + 0x80000) & 0xFFF00000);
+    return __fadd_rn(__fadd_rn(h, 24576.0f), -24576.0f);  // 1.5 x 2^14: an ulp of 2^-9
+}
+
 __device__ __forceinline__ float at_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -210,7 +219,7 @@ __device__ __forceinline__ float at_butterfly(const float (&x)[R], int lane, F o
 // One request as the kernel takes it.
 struct AttnSeq {
     int first, rows, len;  // rows 0: nothing to do
-    int tiles;             // per unit; 1 for an empty cache (which has no pipeline tile)
+    int tiles;             // per unit; 0 for an empty cache
     int groups;            // row groups
     bool bad;
 };
@@ -224,7 +233,7 @@ __device__ __forceinline__ AttnSeq at_seq(const AttnArgs &a, int s) {
     q.bad = off || len < 0;
     q.rows = off ? 0 : static_cast<int>(rows);
     q.len = max(len, 0);
-    q.tiles = max(1, (q.len >> 7) + ((q.len & 127) != 0));
+    q.tiles = (q.len >> 7) + ((q.len & 127) != 0);
     q.groups = (q.rows * a.group + R - 1) / R;
     return q;
 }
@@ -241,23 +250,31 @@ struct AttnSplit {
     }
 };
 
-// A position in the CTA's range of the list: request, unit of the request,
-// tiles [j0, j1) of the unit, and how many list entries are left after them.
+// A unit's entries in the list: one for its set-up, then its tiles.  A unit of at
+// most kAtSmall tiles is never cut: a cut inside it moves to its start (joining
+// two parts costs more than the tiles).
+constexpr int kAtSmall = 4;
+
+// A position in the CTA's range of the list: request, unit of the request, its
+// entries from e0 on and tiles [j0, j1), and the list entries left after them.
 template <int R>
 struct AttnWalk {
     const AttnArgs &a;
     AttnSeq q;
-    int s, unit, j0, j1, left;
+    int s, unit, e0, j0, j1, left;
     __device__ __forceinline__ AttnWalk(const AttnArgs &args, const AttnSeq &seq, int s0, int offset, int count)
         : a(args), q(seq), s(s0), left(count) {
-        unit = offset / q.tiles;
-        j0 = offset - unit * q.tiles;
+        unit = offset / (q.tiles + 1);
+        e0 = offset - unit * (q.tiles + 1);
         clip();
     }
     __device__ __forceinline__ void clip() {
-        j1 = min(q.tiles, j0 + left);
-        left -= j1 - j0;
+        const int e1 = min(q.tiles + 1, e0 + left);
+        left -= e1 - e0;
+        j0 = max(e0 - 1, 0);
+        j1 = e1 - 1;
     }
+    __device__ __forceinline__ bool none() const { return j1 <= j0; }  // no tile here
     // The next unit; false at the end of the range.
     __device__ __forceinline__ bool next() {
         if (left <= 0) return false;
@@ -266,7 +283,7 @@ struct AttnWalk {
             do q = at_seq<R>(a, ++s);
             while (q.rows == 0);
         }
-        j0 = 0;
+        e0 = 0;
         clip();
         return true;
     }
@@ -301,18 +318,29 @@ __device__ __forceinline__ void at_build_queries(const AttnArgs &a, const AttnWa
     const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0);
     const T *q = static_cast<const T *>(a.q) + w.q.first * a.q_stride + static_cast<int64_t>(w.head()) * a.group * a.head_dim;
     const int sub = lane >> 3, l8 = lane & 7;
-    for (int r = 4 * part + sub; r < R; r += 4 * parts) {
-        const int i = (row0 + r) / a.group, c = row0 + r - i * a.group;
-        const T *x = q + i * a.q_stride + c * a.head_dim;
-        float4 v[ND][4];
+    float4 next[ND][4];
+    int i = 0;
+    auto fetch = [&](int r) {
+        i = (row0 + r) / a.group;
+        const T *x = q + i * a.q_stride + (row0 + r - i * a.group) * a.head_dim;
 #pragma unroll
         for (int h = 0; h < ND; ++h)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int d = h * 128 + k * 32 + 4 * l8;
-                v[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < valid && d < a.head_dim) v[h][k] = at_load4<T>(x + d);
+                next[h][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < valid && d < a.head_dim) next[h][k] = at_load4<T>(x + d);
             }
+    };
+    if (4 * part < R) fetch(4 * part + sub);
+    for (int r = 4 * part + sub; r < R; r += 4 * parts) {
+        float4 v[ND][4];
+#pragma unroll
+        for (int h = 0; h < ND; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[h][k] = next[h][k];
+        const int token = i;
+        if (r + 4 * parts < R) fetch(r + 4 * parts);  // on their way while these rows are encoded
         uint32_t g = 0;  // largest |x| as bits; a NaN sorts above infinity
 #pragma unroll
         for (int h = 0; h < ND; ++h)
@@ -331,7 +359,7 @@ __device__ __forceinline__ void at_build_queries(const AttnArgs &a, const AttnWa
             float g1, g2;
             t8_pow2_split(ex == kT8Poison ? 0 : -ex, g1, g2);
             qs[r] = ex == kT8Poison ? __int_as_float(0x7FC00000) : a.scale_log2 * g1 * g2;
-            lim[r] = r < valid ? w.q.len - w.q.rows + i : w.q.len - 1;
+            lim[r] = r < valid ? w.q.len - w.q.rows + token : w.q.len - 1;
         }
 #pragma unroll
         for (int h = 0; h < ND; ++h)
@@ -340,16 +368,13 @@ __device__ __forceinline__ void at_build_queries(const AttnArgs &a, const AttnWa
                 float t0 = v[h][k].x * f1 * f2, t1 = v[h][k].y * f1 * f2, t2 = v[h][k].z * f1 * f2, t3 = v[h][k].w * f1 * f2;
 #pragma unroll
                 for (int p = 0; p < PL; ++p) {
-                    const uint32_t lo = t8_to_e4m3x2(t0, t1), hi = t8_to_e4m3x2(t2, t3);
-                    *reinterpret_cast<uint32_t *>(dst + h * N * 128 + at_swizzle<128>((p * R + r) * 128 + k * 32 + 4 * l8)) =
-                        lo | (hi << 16);
+                    float h0 = t0, h1 = t1, h2 = t2, h3 = t3;
                     if (p + 1 < PL) {
-                        const float2 qlo = e4m3x2_to_f32(lo), qhi = e4m3x2_to_f32(hi);
-                        t0 = (t0 - qlo.x) * 16.f;
-                        t1 = (t1 - qlo.y) * 16.f;
-                        t2 = (t2 - qhi.x) * 16.f;
-                        t3 = (t3 - qhi.y) * 16.f;
+                        h0 = at_plane(t0), h1 = at_plane(t1), h2 = at_plane(t2), h3 = at_plane(t3);
+                        t0 = (t0 - h0) * 16.f, t1 = (t1 - h1) * 16.f, t2 = (t2 - h2) * 16.f, t3 = (t3 - h3) * 16.f;
                     }
+                    *reinterpret_cast<uint32_t *>(dst + h * N * 128 + at_swizzle<128>((p * R + r) * 128 + k * 32 + 4 * l8)) =
+                        t8_to_e4m3x2(h0, h1) | (t8_to_e4m3x2(h2, h3) << 16);
                 }
             }
     }
@@ -376,7 +401,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     __shared__ int s_vnan[2][ND * 128];                 // first position whose value code is NaN, per element
     __shared__ int s_scan[kAtThreads / 32];
     __shared__ AttnSeq s_seq;
-    __shared__ int s_first, s_off, s_abort, s_last;
+    __shared__ int s_first, s_off, s_begin, s_end, s_abort, s_last;
     __shared__ uint32_t tmem_slot;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -418,7 +443,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
     // ---- the list: tiles of every request, scanned by every CTA (thread i sums
     // requests [i per, (i + 1) per)).  The host keeps the total below 2^31.
-    int total = 0, grid = 0, t_begin = 0;
+    int total = 0, grid = 0;
     {
         const int per = (a.n_seqs + kAtThreads - 1) / kAtThreads;
         const int r0 = min(tid * per, a.n_seqs), r1 = min(r0 + per, a.n_seqs);
@@ -427,7 +452,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         AttnSeq q = {};
         for (int s = r0; s < r1; ++s) {
             q = at_seq<R>(a, s);
-            mine += a.kv_heads * q.groups * q.tiles;
+            mine += a.kv_heads * q.groups * (q.tiles + 1);
             bad |= q.bad;
         }
         if (bad && blockIdx.x == 0) atomicOr(a.status, 4u);
@@ -445,32 +470,44 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         total = __reduce_add_sync(0xFFFFFFFFu, lane < kAtThreads / 32 ? sum : 0);
         const int base = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sum : 0);
         grid = min(static_cast<int>(gridDim.x), total);
-        int at = base + pre - mine;  // this thread's first entry
+        const int at = base + pre - mine;  // this thread's first entry
         if (static_cast<int>(blockIdx.x) < grid) {
-            t_begin = AttnSplit(total, grid).begin(blockIdx.x);
-            if (at <= t_begin && t_begin < at + mine) {
-                int s = r0;
-                if (per > 1)
-                    for (;; ++s) {
-                        q = at_seq<R>(a, s);
-                        const int here = a.kv_heads * q.groups * q.tiles;
-                        if (t_begin < at + here) break;
-                        at += here;
-                    }
+            const AttnSplit split(total, grid);
+            // Entry x, if it lies in one of this thread's requests: the request, the entry within it, and its list
+            // position, all moved to the unit's start where the unit is small.
+            auto locate = [&](int x, int &r, int &off) {
+                int here = at;
+                r = r0;
+                if (per > 1) q = at_seq<R>(a, r);
+                for (;;) {
+                    const int size = a.kv_heads * q.groups * (q.tiles + 1);
+                    if (x < here + size) break;
+                    here += size;
+                    q = at_seq<R>(a, ++r);
+                }
+                off = x - here;
+                if (q.tiles <= kAtSmall) off -= off % (q.tiles + 1);
+                return here + off;
+            };
+            const int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
+            int r, off;
+            if (at <= x1 && x1 < at + mine) s_end = locate(x1, r, off);
+            else if (tid == 0 && x1 == total) s_end = total;
+            if (at <= x0 && x0 < at + mine) {
+                s_begin = locate(x0, r, off);
                 s_seq = q;
-                s_first = s;
-                s_off = t_begin - at;
+                s_first = r;
+                s_off = off;
             }
         }
         __syncthreads();
     }
     const uint32_t tmem = tmem_slot;
 
-    if (static_cast<int>(blockIdx.x) < grid) {
+    if (static_cast<int>(blockIdx.x) < grid && s_begin < s_end) {
         const AttnSplit split(total, grid);
-        AttnWalk<R> w(a, s_seq, s_first, s_off, split.begin(blockIdx.x + 1) - t_begin);
-        // The first unit's query planes are built by the warps that have nothing to do yet.
-        const bool built = w.q.len > 0;
+        AttnWalk<R> w(a, s_seq, s_first, s_off, s_end - s_begin);
+        const bool built = !w.none();
         if (warp < kAtProducerWarp || warp == kAtQueryWarp) {
             if (built && warp < kAtProducerWarp)
                 at_build_queries<T, PL, R, ND>(a, w, sQ, s_qs[0], s_lim[0], warp, kAtProducerWarp, lane);
@@ -493,7 +530,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 return page < a.width ? a.table[static_cast<int64_t>(f.s) * a.width + page] : -1;
             };
             while (true) {
-                while (more && (f.q.len == 0 || fj >= f.j1)) {
+                while (more && fj >= f.j1) {
                     more = f.next();
                     fj = f.j0;
                 }
@@ -580,8 +617,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         }
                     }
                     while (more && qt >= unit_end) {  // on to the unit that tile qt belongs to
-                        if (iu >= 0 || w.q.len == 0) more = w.next();
-                        while (more && w.q.len == 0) more = w.next();
+                        if (iu >= 0 || w.none()) more = w.next();
+                        while (more && w.none()) more = w.next();
                         if (more) {
                             ++iu;
                             unit_end += w.j1 - w.j0;
@@ -628,7 +665,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             int ub = 0;
             int64_t iu = 0;
             do {
-                if (w.q.len == 0) continue;
+                if (w.none()) continue;
                 // The unit before last is written out: nothing reads this buffer, its scales or its limits any more.
                 if (iu >= 2 && !at_warp_wait(smem_addr(&ml_free[ub]), static_cast<uint32_t>(((iu >> 1) - 1) & 1), &s_abort)) break;
                 if (iu > 0 || !built) at_build_queries<T, PL, R, ND>(a, w, sQ + ub * Sh::kQBytes, s_qs[ub], s_lim[ub], 0, 1, lane);
@@ -646,7 +683,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             int64_t it = 0, iu = 0;
             bool ok = true;
             do {
-                if (w.q.len == 0) continue;
+                if (w.none()) continue;
                 const uint32_t uph = static_cast<uint32_t>((iu >> 1) & 1);
                 ok = ok && at_warp_wait(smem_addr(&q_full[ub]), uph, &s_abort) &&
                      (iu < 2 || at_warp_wait(smem_addr(&ml_free[ub]), uph ^ 1u, &s_abort));
@@ -742,15 +779,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                             uint32_t word[CH / 4];
 #pragma unroll
                             for (int r = 0; r < CH; r += 4) {
-                                const uint32_t lo = t8_to_e4m3x2(t[r], t[r + 1]), hi = t8_to_e4m3x2(t[r + 2], t[r + 3]);
-                                word[r / 4] = lo | (hi << 16);
-                                if (p + 1 < PL) {
-                                    const float2 qlo = e4m3x2_to_f32(lo), qhi = e4m3x2_to_f32(hi);
-                                    t[r] = (t[r] - qlo.x) * 16.f;
-                                    t[r + 1] = (t[r + 1] - qlo.y) * 16.f;
-                                    t[r + 2] = (t[r + 2] - qhi.x) * 16.f;
-                                    t[r + 3] = (t[r + 3] - qhi.y) * 16.f;
+                                float h[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    h[y] = p + 1 < PL ? at_plane(t[r + y]) : t[r + y];
+                                    if (p + 1 < PL) t[r + y] = (t[r + y] - h[y]) * 16.f;
                                 }
+                                word[r / 4] = t8_to_e4m3x2(h[0], h[1]) | (t8_to_e4m3x2(h[2], h[3]) << 16);
                             }
                             uint8_t *at = pb + at_swizzle<N>(tg * N + p * R + c);
                             if constexpr (CH == 16) *reinterpret_cast<uint4 *>(at) = make_uint4(word[0], word[1], word[2], word[3]);
@@ -806,15 +841,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const uint32_t lanes = static_cast<uint32_t>(ow * 32) << 16;
             int b = 0, ub = 0;
             int64_t it = 0, iu = 0;
-            int done = t_begin;
-            bool ok = true, first_unit = true;
+            int done = s_begin;
+            bool ok = true;
             const float nanf = __int_as_float(0x7FC00000);
             T *out = static_cast<T *>(a.out);
             do {
                 const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0), kvh = w.head();
                 const bool whole = w.j0 == 0 && w.j1 == w.q.tiles;
-                const int unit_begin = done - w.j0;  // list entry of the unit's first tile
-                done += w.j1 - w.j0;
+                const int unit_begin = done - w.e0;  // list position of the unit
+                done += w.j1 + 1 - w.e0;
                 auto out_row = [&](int r) {  // (row, query head) of the unit's row r
                     const int i = (row0 + r) / a.group;
                     return static_cast<int64_t>(w.q.first + i) * a.out_stride +
@@ -831,9 +866,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                             if (dt + h * 128 < a.head_dim) out[out_row(r) + dt + h * 128] = static_cast<T>(0.f);
                         if (a.lse && dt == 0) a.lse[lse_at(r)] = -INFINITY;
                     }
-                    first_unit = false;
                     continue;
                 }
+                if (w.none()) continue;
                 float ref = kAtNoRef;  // running maximum of row `dt` (threads below R)
                 float acc[ND][R];
 #pragma unroll
@@ -931,7 +966,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     at_bar(3);  // s_inv is free again
                 } else {
                     // A part of a unit: its sums go to the workspace, and the part that arrives last joins them all.
-                    float *mine = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (first_unit ? 0 : 1)) * Sh::kPartial;
+                    float *mine = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (w.j0 == 0)) * Sh::kPartial;
 #pragma unroll
                     for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -940,8 +975,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         __stcg(mine + R * ND * 128 + dt, ref);
                         __stcg(mine + R * ND * 128 + R + dt, l);
                     }
-                    const int b0 = split.owner(unit_begin), parts = split.owner(unit_begin + w.q.tiles - 1) - b0 + 1;
-                    const bool b0_first = split.begin(b0) == unit_begin;
+                    const int b0 = split.owner(unit_begin + 1), parts = split.owner(unit_begin + w.q.tiles) - b0 + 1;
                     at_bar(3);
                     if (dt == 0) {  // the barrier and this release order every thread's sums before the count
                         uint32_t old;
@@ -955,8 +989,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     if (s_last) {
                         // Warp ow joins the rows ow, ow + 4, ...: lane = part for the weights, four elements for the sums.
                         constexpr int RW = R / 4;
-                        auto part = [&](int p) {  // part p lies in CTA b0 + p: its first unit, but for a unit that starts inside CTA b0
-                            return a.partials + (static_cast<int64_t>(b0 + p) * 2 + (p == 0 && !b0_first ? 1 : 0)) * Sh::kPartial;
+                        auto part = [&](int p) {  // part p lies in CTA b0 + p, which holds one that begins a unit and one that does not
+                            return a.partials + (static_cast<int64_t>(b0 + p) * 2 + (p == 0)) * Sh::kPartial;
                         };
                         float m[RW], den[RW];
                         float4 o[RW][ND];
@@ -1026,7 +1060,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ml_free[ub]));
-                first_unit = false;
                 ++iu;
                 ub ^= 1;
             } while (w.next());
