@@ -35,10 +35,14 @@
 //
 // Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax of even and odd
 // tiles (TMEM lane = token), warps 8-11 output sums (TMEM lane = element of
-// head_dim), warp 12 TMA producer (a lane per block), warps 13 and 14 the MMAs of
-// even and odd tiles, warp 15 query planes of the next unit.  Every wait is bounded; a
-// timeout raises a CTA-wide flag, the outputs become NaN, the join still counts,
-// copies and MMAs in flight are waited for, and the status word records it.
+// head_dim) and the query planes of the next unit, warps 12 and 15 TMA producers
+// of K and V (a lane per block), warps 13 and 14 the MMAs of even and odd tiles.
+// Rows go through the softmax eight at a time in a loop, and scores are read
+// from tensor memory twice rather than kept: unrolled over 32 rows, the roles'
+// code did not fit the instruction caches, and that was the largest stall.
+//   Every wait is bounded; a timeout raises a CTA-wide flag, the outputs become
+// NaN, the join still counts, copies and MMAs in flight are waited for, and the
+// status word records it.
 #pragma once
 
 #include "tc8_gemv.cuh"
@@ -46,7 +50,7 @@
 namespace fp8blk {
 
 constexpr int kAtThreads = 512;
-constexpr int kAtOutWarp = 8, kAtProducerWarp = 12, kAtMmaWarp = 13, kAtQueryWarp = 15;
+constexpr int kAtOutWarp = 8, kAtKWarp = 12, kAtMmaWarp = 13, kAtVWarp = 15;
 constexpr int kAtTile = 128;            // tokens per tile
 constexpr int kAtMaxGrid = 256;         // bound on CTAs: arrival counters and partial sums in the workspace
 constexpr size_t kAtHeaderBytes = kAtMaxGrid * sizeof(uint32_t);
@@ -118,21 +122,21 @@ __device__ __forceinline__ void at_ld8(uint32_t taddr, float *v) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[j]);
 }
-template <int C>
-__device__ __forceinline__ void at_ld(uint32_t taddr, float *v) {
-    static_assert(C == 8 || C == 16, "columns");
-    if constexpr (C == 8) at_ld8(taddr, v);
-    else t8_ld16(taddr, v);
-}
 __device__ __forceinline__ void at_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// v rounded to four significant bits, no finer than e4m3's subnormal step 2^-9:
-// exactly an e4m3 value for |v| < 2^8, so a plane's residual needs no decoding
-// (conversions out of e4m3 run at an eighth of the rate of these).  Halves go
-// away from zero; the next plane takes what is left either way.  NaN stays NaN.
-__device__ __forceinline__ float at_plane(float v) {
-    const float h = __int_as_float((__float_as_int(v) + 0x80000) & 0xFFF00000);
-    return __fadd_rn(__fadd_rn(h, 24576.0f), -24576.0f);  // 1.5 x 2^14: an ulp of 2^-9
+// The four values' next e4m3 plane as a word of codes; unless it is the last
+// plane, the values become 16 times what it leaves (exact).
+template <bool LAST>
+__device__ __forceinline__ uint32_t at_plane(float &a, float &b, float &c, float &d) {
+    const uint32_t lo = t8_to_e4m3x2(a, b), hi = t8_to_e4m3x2(c, d);
+    if constexpr (!LAST) {
+        const float2 x = e4m3x2_to_f32(lo), y = e4m3x2_to_f32(hi);
+        a = (a - x.x) * 16.f;
+        b = (b - x.y) * 16.f;
+        c = (c - y.x) * 16.f;
+        d = (d - y.y) * 16.f;
+    }
+    return lo | (hi << 16);
 }
 
 __device__ __forceinline__ float at_exp2(float x) {
@@ -368,13 +372,8 @@ __device__ __forceinline__ void at_build_queries(const AttnArgs &a, const AttnWa
                 float t0 = v[h][k].x * f1 * f2, t1 = v[h][k].y * f1 * f2, t2 = v[h][k].z * f1 * f2, t3 = v[h][k].w * f1 * f2;
 #pragma unroll
                 for (int p = 0; p < PL; ++p) {
-                    float h0 = t0, h1 = t1, h2 = t2, h3 = t3;
-                    if (p + 1 < PL) {
-                        h0 = at_plane(t0), h1 = at_plane(t1), h2 = at_plane(t2), h3 = at_plane(t3);
-                        t0 = (t0 - h0) * 16.f, t1 = (t1 - h1) * 16.f, t2 = (t2 - h2) * 16.f, t3 = (t3 - h3) * 16.f;
-                    }
                     *reinterpret_cast<uint32_t *>(dst + h * N * 128 + at_swizzle<128>((p * R + r) * 128 + k * 32 + 4 * l8)) =
-                        t8_to_e4m3x2(h0, h1) | (t8_to_e4m3x2(h2, h3) << 16);
+                        p + 1 < PL ? at_plane<false>(t0, t1, t2, t3) : at_plane<true>(t0, t1, t2, t3);
                 }
             }
     }
@@ -385,7 +384,7 @@ template <typename T, int PL, int R, int ND>
 __global__ void __launch_bounds__(kAtThreads, 1)
     kv_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
     using Sh = AttnShape<PL, R, ND>;
-    constexpr int N = Sh::N, S = Sh::kStages, CH = R < 16 || PL > 2 || ND > 1 ? 8 : 16;
+    constexpr int N = Sh::N, S = Sh::kStages;
     extern __shared__ __align__(1024) uint8_t at_smem[];
     __shared__ __align__(8) uint64_t k_full[S], v_full[S], v_free[S], sc_full[S];
     __shared__ __align__(8) uint64_t s_full[2], s_free[2], p_full[2], o_full[2], o_free[2];
@@ -415,7 +414,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             mbar_init(smem_addr(&k_full[i]), 1);
             mbar_init(smem_addr(&v_full[i]), 1);
             mbar_init(smem_addr(&v_free[i]), 1);
-            mbar_init(smem_addr(&sc_full[i]), 32);
+            mbar_init(smem_addr(&sc_full[i]), 64);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&s_full[i]), 1);
@@ -423,7 +422,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             mbar_init(smem_addr(&p_full[i]), 4);
             mbar_init(smem_addr(&o_full[i]), 1);
             mbar_init(smem_addr(&o_free[i]), 4);
-            mbar_init(smem_addr(&q_full[i]), 1);
+            mbar_init(smem_addr(&q_full[i]), 4);
             mbar_init(smem_addr(&ml_full[i]), 8);
             mbar_init(smem_addr(&ml_free[i]), 4);
             mbar_init(smem_addr(&mma_done[i]), 1);
@@ -508,79 +507,88 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const AttnSplit split(total, grid);
         AttnWalk<R> w(a, s_seq, s_first, s_off, s_end - s_begin);
         const bool built = !w.none();
-        if (warp < kAtProducerWarp || warp == kAtQueryWarp) {
-            if (built && warp < kAtProducerWarp)
-                at_build_queries<T, PL, R, ND>(a, w, sQ, s_qs[0], s_lim[0], warp, kAtProducerWarp, lane);
-            asm volatile("bar.sync 4, %0;" ::"n"((kAtProducerWarp + 1) * 32) : "memory");
+        if (built && warp < kAtKWarp) {
+            at_build_queries<T, PL, R, ND>(a, w, sQ, s_qs[0], s_lim[0], warp, kAtKWarp, lane);
+            asm volatile("bar.sync 4, %0;" ::"n"(kAtKWarp * 32) : "memory");
         }
-        if (warp == kAtProducerWarp) {
-            // ---------------- TMA producer: lane p copies the tile's p-th block
+        if (warp == kAtKWarp || warp == kAtVWarp) {
+            // ---------------- TMA producers: lane p copies the tile's p-th block of K (or V), with its scale
+            const bool is_v = warp == kAtVWarp;
             const int np = kAtTile >> a.block_log2, block = 1 << a.block_log2;
             const uint64_t pol = l2_policy_evict_first();
+            const CUtensorMap *map = is_v ? &vmap : &kmap;
+            const float *scales = is_v ? a.v_scales : a.k_scales;
+            const uint32_t ring = smem_addr(is_v ? sV : sK);
+            uint64_t *full = is_v ? v_full : k_full;
             int st = 0;
             uint32_t ph = 0;
             int64_t it = 0;
-            AttnWalk<R> f(w);
-            int fj = f.j0;
-            bool more = true;
-            // Block ids: a window of 32 table entries in the lanes' registers, and the next window on its way.
-            int win = -1, ids = -1, ids_next = -1, win_unit = -1, win_seq = -1, win_head = 0;
+            // Block ids, 32 table entries at a time in the lanes' registers: the window in use, the one after it, and
+            // the first one of the next unit, each asked for long before its use.
+            AttnWalk<R> n(w);
+            bool more = !n.none();
+            auto skip = [&] {
+                do more = n.next();
+                while (more && n.none());
+            };
+            if (!more) skip();
             auto load_ids = [&](int page0) {
                 const int page = page0 + lane;
-                return page < a.width ? a.table[static_cast<int64_t>(f.s) * a.width + page] : -1;
+                return more && page < a.width ? a.table[static_cast<int64_t>(n.s) * a.width + page] : -1;
             };
-            while (true) {
-                while (more && fj >= f.j1) {
-                    more = f.next();
-                    fj = f.j0;
-                }
-                if (!more) break;
-                const int page0 = fj * np;
-                if (f.s != win_seq || f.unit != win_unit || page0 >= win + 32) {
-                    const bool follows = f.s == win_seq && f.unit == win_unit;
-                    ids = follows ? ids_next : load_ids(page0);
-                    win = page0;
-                    win_seq = f.s;
-                    win_unit = f.unit;
-                    win_head = f.head();
-                    ids_next = load_ids(page0 + 32);
-                }
-                const int pages = min(np, ((f.q.len + block - 1) >> a.block_log2) - page0);
-                // Lanes 0.. copy the tile's blocks of K, lanes 16.. those of V, each with its scale.
-                const int p = lane & 15, id = __shfl_sync(0xFFFFFFFFu, ids, (page0 - win + p) & 31);
-                const bool mine = p < pages, ok = id >= 0 && id < a.n_blocks;
-                if (mine && !ok) atomicOr(a.status, 4u);
-                const int64_t bh = static_cast<int64_t>(ok ? id : 0) * a.kv_heads + win_head;
-                const int row = static_cast<int>(bh << a.block_log2);
-                ++fj;
-                // V's slot is the last of the stage's to be read.
-                if (it >= S && !at_warp_wait(smem_addr(&v_free[st]), ph ^ 1u, &s_abort)) break;
-                const uint32_t full = smem_addr(lane < 16 ? &k_full[st] : &v_full[st]);
-                if (p == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(pages) * block * 128 * ND);
-                __syncwarp();
-                if (mine) {
-                    const uint32_t at = smem_addr(lane < 16 ? sK : sV) + static_cast<uint32_t>(st) * Sh::kTileBytes + p * block * 128;
+            int ids_unit = load_ids(n.j0 * np);
+            bool ok = true;
+            while (ok && more) {
+                const int j1 = n.j1, len = n.q.len, head = n.head(), page_end = j1 * np;
+                const int32_t *row = a.table + static_cast<int64_t>(n.s) * a.width;
+                int j = n.j0, win = j * np, ids = ids_unit;
+                auto window = [&](int page0) {
+                    const int page = page0 + lane;
+                    return page0 < page_end && page < a.width ? row[page] : -1;
+                };
+                int ids_next = window(win + 32);
+                skip();
+                ids_unit = load_ids(n.j0 * np);
+                for (; j < j1; ++j) {
+                    const int page0 = j * np;
+                    if (page0 >= win + 32) {
+                        win += 32;
+                        ids = ids_next;
+                        ids_next = window(win + 32);
+                    }
+                    const int pages = min(np, ((len + block - 1) >> a.block_log2) - page0);
+                    const int id = __shfl_sync(0xFFFFFFFFu, ids, (page0 - win + lane) & 31);
+                    const bool mine = lane < pages, good = id >= 0 && id < a.n_blocks;
+                    if (mine && !good) atomicOr(a.status, 4u);
+                    const int64_t bh = static_cast<int64_t>(good ? id : 0) * a.kv_heads + head;
+                    // V's slot is the last of the stage's to be read.
+                    if (it >= S && !at_warp_wait(smem_addr(&v_free[st]), ph ^ 1u, &s_abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_addr(&full[st]);
+                    if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(pages) * block * 128 * ND);
+                    __syncwarp();
+                    if (mine) {
+                        const uint32_t at = ring + static_cast<uint32_t>(st) * Sh::kTileBytes + lane * block * 128;
 #pragma unroll
-                    for (int h = 0; h < ND; ++h)
-                        t8_tma_2d(at + h * kAtTile * 128, lane < 16 ? &kmap : &vmap, h * 128, row, full, pol);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[st][lane >> 4][p])),
-                                 "l"(ok ? (lane < 16 ? a.k_scales : a.v_scales) + bh : &g_attn_nan)
-                                 : "memory");
-                }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sc_full[st])) : "memory");
-                ++it;
-                if (++st == S) {
-                    st = 0;
-                    ph ^= 1u;
+                        for (int h = 0; h < ND; ++h)
+                            t8_tma_2d(at + h * kAtTile * 128, map, h * 128, static_cast<int>(bh << a.block_log2), bar, pol);
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[st][is_v][lane])),
+                                     "l"(good ? scales + bh : &g_attn_nan)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sc_full[st])) : "memory");
+                    ++it;
+                    if (++st == S) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
             // What is still in flight lands before the CTA's shared memory is released.
-            for (int64_t v = it > S ? it - S : 0; v < it; ++v) {
-                const uint32_t par = static_cast<uint32_t>((v / S) & 1);
-                (void)mbar_wait_bounded(smem_addr(&k_full[v % S]), par);
-                (void)mbar_wait_bounded(smem_addr(&v_full[v % S]), par);
-                (void)mbar_wait_bounded(smem_addr(&sc_full[v % S]), par);
-            }
+            for (int64_t v = it > S ? it - S : 0; v < it; ++v) (void)mbar_wait_bounded(smem_addr(&full[v % S]), static_cast<uint32_t>((v / S) & 1));
+            asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp == kAtMmaWarp || warp == kAtMmaWarp + 1) {
             // ---------------- MMA issuers: warp g issues both products of the tiles g, g + 2, ...  Whichever of the two
             // can go next goes, the second product first (it frees a stage).
@@ -660,20 +668,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 t8_commit(smem_addr(&mma_done[g]));
                 (void)mbar_wait_bounded(smem_addr(&mma_done[g]), 0u);
             }
-        } else if (warp == kAtQueryWarp) {
-            // ---------------- query planes of the units after the first
-            int ub = 0;
-            int64_t iu = 0;
-            do {
-                if (w.none()) continue;
-                // The unit before last is written out: nothing reads this buffer, its scales or its limits any more.
-                if (iu >= 2 && !at_warp_wait(smem_addr(&ml_free[ub]), static_cast<uint32_t>(((iu >> 1) - 1) & 1), &s_abort)) break;
-                if (iu > 0 || !built) at_build_queries<T, PL, R, ND>(a, w, sQ + ub * Sh::kQBytes, s_qs[ub], s_lim[ub], 0, 1, lane);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&q_full[ub]));
-                ++iu;
-                ub ^= 1;
-            } while (w.next());
         } else if (warp < kAtOutWarp) {
             // ---------------- softmax: group g takes the tiles g, g + 2, ...; thread = token of the tile
             const int g = warp >> 2, wg = warp & 3, tg = tid & 127, bar = 1 + g;
@@ -688,9 +682,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 ok = ok && at_warp_wait(smem_addr(&q_full[ub]), uph, &s_abort) &&
                      (iu < 2 || at_warp_wait(smem_addr(&ml_free[ub]), uph ^ 1u, &s_abort));
                 float ref = kAtNoRef;  // running maximum of row `tg` (threads below R)
-                float l[R];
+                float *den = s_l[ub][warp];  // this warp's denominators; lane l looks after its own of every eight rows
+                const int own = at_owned<8>(lane);
+                const bool owner = (lane & 3) == 0;
+                if (owner) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) l[r] = 0.f;
+                    for (int c = 0; c < R; c += 8) den[c + own] = 0.f;
+                }
                 const int seen_by_all = w.q.len - w.q.rows;  // positions up to here are seen by every row
                 for (int j = w.j0; j < w.j1; ++j, ++it) {
                     const int cs = st;
@@ -705,34 +703,39 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const int pos = j * kAtTile + tg;
                     const bool edge = (j + 1) * kAtTile - 1 > seen_by_all;  // some row does not see the whole tile
                     const float ks = sc[cs][0][tg >> a.block_log2];
-                    float s[R];
-                    t8_fence_after();
+                    // Scores of rows c .. c + 7, in base 2; what a row does not see is -inf.
+                    auto scores = [&](int c, float (&s)[8]) {
+                        float d[PL][8];
 #pragma unroll
-                    for (int c = 0; c < R; c += CH) {
-                        float d[PL][CH];
-#pragma unroll
-                        for (int p = 0; p < PL; ++p) at_ld<CH>(tmem + lanes + static_cast<uint32_t>(g * N + p * R + c), d[p]);
+                        for (int p = 0; p < PL; ++p) at_ld8(tmem + lanes + static_cast<uint32_t>(g * N + p * R + c), d[p]);
                         at_wait_ld();
 #pragma unroll
-                        for (int r = 0; r < CH; ++r) {
+                        for (int r = 0; r < 8; ++r) {
                             float u = d[PL - 1][r];
 #pragma unroll
                             for (int p = PL - 2; p >= 0; --p) u = fmaf(u, 0.0625f, d[p][r]);
-                            s[c + r] = u * (s_qs[ub][c + r] * ks);
+                            s[r] = u * (s_qs[ub][c + r] * ks);
                         }
-                    }
-                    t8_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&s_free[g]));
-                    if (edge) {
+                        if (edge) {
 #pragma unroll
-                        for (int r = 0; r < R; ++r) s[r] = pos > s_lim[ub][r] ? -INFINITY : s[r];
-                    }
+                            for (int r = 0; r < 8; ++r) s[r] = pos > s_lim[ub][c + r] ? -INFINITY : s[r];
+                        }
+                    };
+                    auto release = [&] {  // the scores' columns may be overwritten
+                        t8_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&s_free[g]));
+                    };
+                    t8_fence_after();
+                    float s[8];
                     // Each row's maximum over the tile.
-                    {
-                        const float top = at_butterfly<R>(s, lane, [](float x, float y) { return fmaxf(x, y); });
-                        if ((lane & (32 / R - 1)) == 0) s_wmax[g][wg][at_owned<R>(lane)] = top;
+#pragma unroll 1
+                    for (int c = 0; c < R; c += 8) {
+                        scores(c, s);
+                        const float top = at_butterfly<8>(s, lane, [](float x, float y) { return fmaxf(x, y); });
+                        if (owner) s_wmax[g][wg][c + own] = top;
                     }
+                    if constexpr (R == 8) release();
                     // The tile's value scales, relative to the power of two under the largest.
                     float vtop = 0.f;
 #pragma unroll
@@ -743,55 +746,41 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const int ve = max(__float_as_int(vtop) >> 23, 8);  // biased exponent; 2^-119 and below count as 2^-119
                     const float vs = sc[cs][1][tg >> a.block_log2] * __int_as_float(ve == 254 ? 0x00400000 : (254 - ve) << 23) * (1 << kAtPeakLog2);
                     at_bar(bar);
-                    bool raised = false;
                     if (tg < R) {
                         const float m = fmaxf(fmaxf(s_wmax[g][0][tg], s_wmax[g][1][tg]), fmaxf(s_wmax[g][2][tg], s_wmax[g][3][tg]));
                         const float tref = fmaxf(m, kAtNoRef), now = fmaxf(ref, tref);
-                        raised = now > ref;
                         s_lf[g][tg] = at_exp2(tref - now);
                         s_lc[g][tg] = at_exp2(ref - now);
                         ref = now;
-                        // The output sums have read what the tile before last left here.
+                        // The output sums have read what the tile before last left here, and the second MMA its weights.
                         if (it >= 2) ok = at_wait(smem_addr(&o_free[g]), bp ^ 1u, &s_abort) && ok;
                         s_tref[g][tg] = tref;
                         if (tg == 0) s_vf[g] = __int_as_float((ve - kAtPeakLog2) << 23);
                     }
-                    const bool moved = at_bar_or(bar, raised);
+                    at_bar(bar);
                     ok = __all_sync(0xFFFFFFFFu, ok);
-                    // P's buffer: the second MMA of the tile before last has read it (o_free says so to the threads above).
-                    if (moved) {
-#pragma unroll
-                        for (int r = 0; r < R; ++r) l[r] *= s_lc[g][r];
-                    }
                     uint8_t *pb = sP + g * Sh::kPBytes;
+#pragma unroll 1
+                    for (int c = 0; c < R; c += 8) {
+                        if constexpr (R > 8) scores(c, s);
+                        float t[8];
 #pragma unroll
-                    for (int c = 0; c < R; c += CH) {
-                        float t[CH];
-#pragma unroll
-                        for (int r = 0; r < CH; ++r) {
-                            const float e = at_exp2(s[c + r] - s_tref[g][c + r]);
-                            l[c + r] = fmaf(e, s_lf[g][c + r], l[c + r]);
-                            t[r] = e * vs;
+                        for (int r = 0; r < 8; ++r) {
+                            s[r] = at_exp2(s[r] - s_tref[g][c + r]);
+                            t[r] = s[r] * vs;
                             if (edge && pos > s_lim[ub][c + r]) t[r] = 0.f;  // whatever the scale
                         }
 #pragma unroll
                         for (int p = 0; p < PL; ++p) {
-                            uint32_t word[CH / 4];
-#pragma unroll
-                            for (int r = 0; r < CH; r += 4) {
-                                float h[4];
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    h[y] = p + 1 < PL ? at_plane(t[r + y]) : t[r + y];
-                                    if (p + 1 < PL) t[r + y] = (t[r + y] - h[y]) * 16.f;
-                                }
-                                word[r / 4] = t8_to_e4m3x2(h[0], h[1]) | (t8_to_e4m3x2(h[2], h[3]) << 16);
-                            }
-                            uint8_t *at = pb + at_swizzle<N>(tg * N + p * R + c);
-                            if constexpr (CH == 16) *reinterpret_cast<uint4 *>(at) = make_uint4(word[0], word[1], word[2], word[3]);
-                            else *reinterpret_cast<uint2 *>(at) = make_uint2(word[0], word[1]);
+                            uint2 word;
+                            word.x = p + 1 < PL ? at_plane<false>(t[0], t[1], t[2], t[3]) : at_plane<true>(t[0], t[1], t[2], t[3]);
+                            word.y = p + 1 < PL ? at_plane<false>(t[4], t[5], t[6], t[7]) : at_plane<true>(t[4], t[5], t[6], t[7]);
+                            *reinterpret_cast<uint2 *>(pb + at_swizzle<N>(tg * N + p * R + c)) = word;
                         }
+                        const float sum = at_butterfly<8>(s, lane, [](float x, float y) { return x + y; });
+                        if (owner) den[c + own] = fmaf(den[c + own], s_lc[g][c + own], sum * s_lf[g][c + own]);
                     }
+                    if constexpr (R > 8) release();
                     if (edge) {
                         // This token's row of V: zeros where the request ends (what is there is no token's), and NaN
                         // codes that only later rows see leave the tile and mark the element for those rows.
@@ -824,11 +813,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&p_full[g]));
                 }
-                // Denominators over this warp's tokens, and the group's maxima.
-                {
-                    const float x = at_butterfly<R>(l, lane, [](float p, float q) { return p + q; });
-                    if ((lane & (32 / R - 1)) == 0) s_l[ub][warp][at_owned<R>(lane)] = x;
-                }
                 if (tg < R) s_mref[ub][g][tg] = ref;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ml_full[ub]));
@@ -845,6 +829,26 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             bool ok = true;
             const float nanf = __int_as_float(0x7FC00000);
             T *out = static_cast<T *>(a.out);
+            // Query planes: the first unit's are built above; here each unit starts with the next one's, into the
+            // buffers of the unit before it, which this group has finished.
+            AttnWalk<R> n(w);
+            bool more = true;
+            auto skip = [&] {
+                do more = n.next();
+                while (more && n.none());
+            };
+            auto build = [&](int to) {
+                if (!more) return;
+                at_build_queries<T, PL, R, ND>(a, n, sQ + to * Sh::kQBytes, s_qs[to], s_lim[to], ow, 4, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&q_full[to]));
+            };
+            if (built) {
+                if (lane == 0) mbar_arrive(smem_addr(&q_full[0]));
+            } else {
+                skip();
+                build(0);
+            }
             do {
                 const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0), kvh = w.head();
                 const bool whole = w.j0 == 0 && w.j1 == w.q.tiles;
@@ -869,6 +873,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     continue;
                 }
                 if (w.none()) continue;
+                skip();
+                build(ub ^ 1);
                 float ref = kAtNoRef;  // running maximum of row `dt` (threads below R)
                 float acc[ND][R];
 #pragma unroll
@@ -898,14 +904,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                     for (int h = 0; h < ND; ++h)
 #pragma unroll
-                        for (int c = 0; c < R; c += CH) {
-                            float d[PL][CH];
+                        for (int c = 0; c < R; c += 8) {
+                            float d[PL][8];
 #pragma unroll
                             for (int p = 0; p < PL; ++p)
-                                at_ld<CH>(tmem + lanes + static_cast<uint32_t>(2 * N + (b * ND + h) * N + p * R + c), d[p]);
+                                at_ld8(tmem + lanes + static_cast<uint32_t>(2 * N + (b * ND + h) * N + p * R + c), d[p]);
                             at_wait_ld();
 #pragma unroll
-                            for (int r = 0; r < CH; ++r) {
+                            for (int r = 0; r < 8; ++r) {
                                 float u = d[PL - 1][r];
 #pragma unroll
                                 for (int p = PL - 2; p >= 0; --p) u = fmaf(u, 0.0625f, d[p][r]);
