@@ -10,8 +10,8 @@ namespace fp8blk {
 // Rows of one MMA group: the smallest of 8, 16, 32 that holds all query rows of
 // a request and cache head, as far as tensor memory and registers go; more rows
 // take more groups, which read the cache again (out of L2).
-static int attn_rows(int rows, int planes, int halves) {
-    const int most = halves == 2 && planes == 4 ? 16 : 32;
+static int attn_rows(int rows, int halves) {
+    const int most = halves == 2 ? 16 : 32;
     int r = 8;
     while (r < rows && r < most) r *= 2;
     return r;
@@ -20,7 +20,7 @@ static int attn_rows(int rows, int planes, int halves) {
 // Partial sums are sized for the largest row group of either type.
 static size_t attn_ws_bytes(int rows, int head_dim) {
     const int halves = head_dim > 128 ? 2 : 1;
-    const size_t r = static_cast<size_t>(attn_rows(rows, 2, halves));
+    const size_t r = static_cast<size_t>(attn_rows(rows, halves));
     return kAtHeaderBytes + static_cast<size_t>(kAtMaxGrid) * 2 * (r * halves * 128 + 2 * r) * sizeof(float);
 }
 
@@ -40,13 +40,7 @@ template <typename T, int PL>
 static cudaError_t launch_attn_rows(const AttnArgs &a, int rows, const CUtensorMap &kmap, const CUtensorMap &vmap,
                                     int64_t grid, cudaStream_t s) {
     if (a.head_dim > 128) {
-        switch (rows) {
-            case 8: return launch_attn<T, PL, 8, 2>(a, kmap, vmap, grid, s);
-            case 16: return launch_attn<T, PL, 16, 2>(a, kmap, vmap, grid, s);
-            default:
-                if constexpr (PL == 2) return launch_attn<T, PL, 32, 2>(a, kmap, vmap, grid, s);
-                else return cudaErrorInvalidValue;
-        }
+        return rows == 8 ? launch_attn<T, PL, 8, 2>(a, kmap, vmap, grid, s) : launch_attn<T, PL, 16, 2>(a, kmap, vmap, grid, s);
     }
     switch (rows) {
         case 8: return launch_attn<T, PL, 8, 1>(a, kmap, vmap, grid, s);
@@ -94,8 +88,8 @@ extern "C" int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, 
     if (!step_aligned(ws, 16)) return FP8BLK_EALIGN;
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
-    const int planes = dtype == FP8BLK_F32 ? 4 : 2, halves = head_dim > 128 ? 2 : 1, group = q_heads / kv_heads;
-    const int rows = attn_rows(max_m * group, planes, halves);
+    const int halves = head_dim > 128 ? 2 : 1, group = q_heads / kv_heads;
+    const int rows = attn_rows(max_m * group, halves);
     AttnArgs a = {};
     a.q = q;
     a.out = out;

@@ -33,10 +33,11 @@
 // (request, head, row group) that lies across CTAs is joined by the CTA that
 // finishes last, over the partial sums in CTA order (deterministic).
 //
-// Roles (512 threads, one CTA per SM): warps 0-3 and 4-7 softmax of even and odd
+// Roles (640 threads, one CTA per SM): warps 0-3 and 4-7 softmax of even and odd
 // tiles (TMEM lane = token), warps 8-11 output sums (TMEM lane = element of
-// head_dim) and the query planes of the next unit, warps 12 and 15 TMA producers
-// of K and V (a lane per block), warps 13 and 14 the MMAs of even and odd tiles.
+// head_dim), warps 12-15 query planes of the units to come, warps 16 and 19 TMA
+// producers of K and V (a lane per block), warps 17 and 18 the MMAs of even and
+// odd tiles.
 // Rows go through the softmax eight at a time in a loop, and scores are read
 // from tensor memory twice rather than kept: unrolled over 32 rows, the roles'
 // code did not fit the instruction caches, and that was the largest stall.
@@ -49,8 +50,8 @@
 
 namespace fp8blk {
 
-constexpr int kAtThreads = 512;
-constexpr int kAtOutWarp = 8, kAtKWarp = 12, kAtMmaWarp = 13, kAtVWarp = 15;
+constexpr int kAtThreads = 640;
+constexpr int kAtOutWarp = 8, kAtQueryWarp = 12, kAtKWarp = 16, kAtMmaWarp = 17, kAtVWarp = 19;
 constexpr int kAtTile = 128;            // tokens per tile
 constexpr int kAtMaxGrid = 256;         // bound on CTAs: arrival counters and partial sums in the workspace
 constexpr size_t kAtHeaderBytes = kAtMaxGrid * sizeof(uint32_t);
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         t8_fence_before();
         __syncthreads();
         t8_fence_after();
-        const int sum = s_scan[lane & (kAtThreads / 32 - 1)];  // each warp's sum, in lanes 0..15
+        const int sum = s_scan[min(lane, kAtThreads / 32 - 1)];  // each warp's sum, in the lanes of its number
         total = __reduce_add_sync(0xFFFFFFFFu, lane < kAtThreads / 32 ? sum : 0);
         const int base = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sum : 0);
         grid = min(static_cast<int>(gridDim.x), total);
@@ -668,6 +669,21 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 t8_commit(smem_addr(&mma_done[g]));
                 (void)mbar_wait_bounded(smem_addr(&mma_done[g]), 0u);
             }
+        } else if (warp >= kAtQueryWarp) {
+            // ---------------- query planes of the units after the first
+            int ub = 0;
+            int64_t iu = 0;
+            do {
+                if (w.none()) continue;
+                // The unit before last is written out: nothing reads this buffer, its scales or its limits any more.
+                if (iu >= 2 && !at_warp_wait(smem_addr(&ml_free[ub]), static_cast<uint32_t>(((iu >> 1) - 1) & 1), &s_abort)) break;
+                if (iu > 0 || !built)
+                    at_build_queries<T, PL, R, ND>(a, w, sQ + ub * Sh::kQBytes, s_qs[ub], s_lim[ub], warp - kAtQueryWarp, 4, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&q_full[ub]));
+                ++iu;
+                ub ^= 1;
+            } while (w.next());
         } else if (warp < kAtOutWarp) {
             // ---------------- softmax: group g takes the tiles g, g + 2, ...; thread = token of the tile
             const int g = warp >> 2, wg = warp & 3, tg = tid & 127, bar = 1 + g;
@@ -789,21 +805,21 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                             for (int h = 0; h < ND; ++h) {
                                 uint8_t *row = sV + static_cast<size_t>(cs) * Sh::kTileBytes + h * kAtTile * 128;
-                                for (int c = 0; c < 8; ++c) {
-                                    uint4 *at = reinterpret_cast<uint4 *>(row + at_swizzle<128>(tg * 128 + c * 16));
-                                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                                    if (pos < w.q.len) {
-                                        x = *at;
-                                        uint32_t *xs = &x.x;
+                                if (pos >= w.q.len) {
 #pragma unroll
-                                        for (int y = 0; y < 16; ++y) {
-                                            const uint32_t code = (xs[y >> 2] >> (8 * (y & 3))) & 0x7Fu;
-                                            if (code == 0x7Fu) {
-                                                xs[y >> 2] &= ~(0xFFu << (8 * (y & 3)));
-                                                atomicMin(&s_vnan[ub][h * 128 + c * 16 + y], pos);
-                                            }
+                                    for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row + tg * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+                                    continue;
+                                }
+#pragma unroll 1
+                                for (int c = 0; c < 32; ++c) {
+                                    uint32_t *at = reinterpret_cast<uint32_t *>(row + at_swizzle<128>(tg * 128 + c * 4));
+                                    uint32_t x = *at;
+                                    if ((((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) == 0u) continue;  // no NaN code among the four
+                                    for (int y = 0; y < 4; ++y)
+                                        if (((x >> (8 * y)) & 0x7Fu) == 0x7Fu) {
+                                            x &= ~(0xFFu << (8 * y));
+                                            atomicMin(&s_vnan[ub][h * 128 + c * 4 + y], pos);
                                         }
-                                    }
                                     *at = x;
                                 }
                             }
@@ -829,26 +845,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             bool ok = true;
             const float nanf = __int_as_float(0x7FC00000);
             T *out = static_cast<T *>(a.out);
-            // Query planes: the first unit's are built above; here each unit starts with the next one's, into the
-            // buffers of the unit before it, which this group has finished.
-            AttnWalk<R> n(w);
-            bool more = true;
-            auto skip = [&] {
-                do more = n.next();
-                while (more && n.none());
-            };
-            auto build = [&](int to) {
-                if (!more) return;
-                at_build_queries<T, PL, R, ND>(a, n, sQ + to * Sh::kQBytes, s_qs[to], s_lim[to], ow, 4, lane);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&q_full[to]));
-            };
-            if (built) {
-                if (lane == 0) mbar_arrive(smem_addr(&q_full[0]));
-            } else {
-                skip();
-                build(0);
-            }
             do {
                 const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0), kvh = w.head();
                 const bool whole = w.j0 == 0 && w.j1 == w.q.tiles;
@@ -873,8 +869,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     continue;
                 }
                 if (w.none()) continue;
-                skip();
-                build(ub ^ 1);
                 float ref = kAtNoRef;  // running maximum of row `dt` (threads below R)
                 float acc[ND][R];
 #pragma unroll
