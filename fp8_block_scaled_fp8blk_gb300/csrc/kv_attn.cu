@@ -127,7 +127,7 @@ extern "C" int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, 
     // One CTA per SM, and no more than the longest possible list has entries.
     const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(max_blocks) * block_tokens + kAtTile - 1) / kAtTile);
     const int64_t entries = static_cast<int64_t>(n_seqs) * kv_heads * ((max_m * group + rows - 1) / rows) * (tiles + 1);
-    if (entries > kStepMaxIndex) return FP8BLK_ERANGE;  // the kernel counts them in 32 bits
+    if (entries > kStepMaxIndex / at_max_weight(rows)) return FP8BLK_ERANGE;  // the kernel counts them in 32 bits
     const int64_t grid = std::min<int64_t>(std::min(dev.sms, kAtMaxGrid), entries);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return step_from_cuda(dtype == FP8BLK_F32 ? launch_attn_rows<float, 4>(a, rows, kmap, vmap, grid, s)

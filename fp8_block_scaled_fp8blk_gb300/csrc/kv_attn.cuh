@@ -10,9 +10,9 @@
 // K's tile is the first MMA's A operand as TMA lands it (K-major, 128-byte
 // swizzle), V's tile the second's (the same landing, read M-major), so the
 // CUDA cores never touch a code.  q and p s_v are the B operands: each value
-// is carried as PL e4m3 planes, t_0 = value * 2^e, plane_p = e4m3(t_p), t_{p+1}
-// = 16 (t_p - plane_p), all subtractions exact.  Plane p is a column group of
-// its own, and sums are recombined as sum_p 16^-p D_p in f32.
+// is carried as PL e4m3 planes, each the rounding of what the one before leaves
+// (all subtractions exact).  Plane p is a column group of its own, and the
+// products are weighed and summed in f32.
 //   f32 queries and outputs: PL = 4, a value keeps 2^-16 of itself at worst
 //     (rms 5e-7), which leaves the result at the error of an f32 computation.
 //   bf16: PL = 2.  bf16's 8 bits fit two planes, so q is exact; p keeps 2^-8 at
@@ -22,7 +22,7 @@
 //
 // p is relative to the maximum over its own tile and row, not to the running
 // one, and p s_v to the tile's largest |s_v|, times 2^8: every tile's weights
-// fill e4m3's range, so what a weight loses is 2^-22 (bf16) or 2^-30 (f32) of
+// fill e4m3's range, so what a weight loses is 2^-22 (bf16) or 2^-26 (f32) of
 // its own tile's largest at worst, and a long tail of small weights keeps its
 // share.  Each tile's product is read back and added to f32 sums in registers
 // with its factor 2^(m_r - running maximum) max|s_v| 2^-8, so nothing in
@@ -125,19 +125,51 @@ __device__ __forceinline__ void at_ld8(uint32_t taddr, float *v) {
 }
 __device__ __forceinline__ void at_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// The four values' next e4m3 plane as a word of codes; unless it is the last
-// plane, the values become 16 times what it leaves (exact).
-template <bool LAST>
-__device__ __forceinline__ uint32_t at_plane(float &a, float &b, float &c, float &d) {
+// e4m3x2 -> two f16, exactly.
+__device__ __forceinline__ uint32_t at_e4m3x2_f16x2(uint32_t codes) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(codes));
+    return h;
+}
+// a -= the low f16 of h, b -= the high one (exact here: a residual of rounding).
+__device__ __forceinline__ void at_minus(uint32_t h, float &a, float &b) {
+    asm("{\n\t.reg .b16 l, u, m;\n\tmov.b32 {l, u}, %2;\n\tmov.b16 m, 0xBC00;\n\t"
+        "fma.rn.f32.f16 %0, l, m, %0;\n\tfma.rn.f32.f16 %1, u, m, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(h));
+}
+// Planes.  p = 0 is the value's own e4m3 code, and each plane takes what the one
+// before leaves; what is left after plane 0 of two, or plane 1 of four, is scaled
+// up, so that it does not end in e4m3's subnormals: by 16, or by 256.  So the
+// planes weigh 1, 2^-4, or 1, 1, 2^-8, 2^-8.
+template <int PL>
+__device__ __forceinline__ constexpr float at_plane_gain(int p) { return PL == 2 ? 16.f : p == 1 ? 256.f : 1.f; }
+template <int PL>
+__device__ __forceinline__ float at_join(const float (&d)[PL]) {
+    if constexpr (PL == 2) return fmaf(d[1], 1.f / 16.f, d[0]);
+    else return fmaf(d[2] + d[3], 1.f / 256.f, d[0] + d[1]);
+}
+// The four values' plane p as a word of codes; the values become what it leaves.
+template <int PL>
+__device__ __forceinline__ uint32_t at_plane(int p, float &a, float &b, float &c, float &d) {
     const uint32_t lo = t8_to_e4m3x2(a, b), hi = t8_to_e4m3x2(c, d);
-    if constexpr (!LAST) {
-        const float2 x = e4m3x2_to_f32(lo), y = e4m3x2_to_f32(hi);
-        a = (a - x.x) * 16.f;
-        b = (b - x.y) * 16.f;
-        c = (c - y.x) * 16.f;
-        d = (d - y.y) * 16.f;
+    if (p + 1 < PL) {
+        at_minus(at_e4m3x2_f16x2(lo), a, b);
+        at_minus(at_e4m3x2_f16x2(hi), c, d);
+        const float gain = at_plane_gain<PL>(p);
+        if (gain != 1.f) {
+            a *= gain;
+            b *= gain;
+            c *= gain;
+            d *= gain;
+        }
     }
     return lo | (hi << 16);
+}
+// Eight consecutive words of shared memory (16-byte aligned).
+__device__ __forceinline__ void at_lds8(const float *p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
 __device__ __forceinline__ float at_exp2(float x) {
@@ -226,7 +258,10 @@ struct AttnSeq {
     int first, rows, len;  // rows 0: nothing to do
     int tiles;             // per unit; 0 for an empty cache
     int groups;            // row groups
+    int weight;            // list entries of a tile
     bool bad;
+    // List entries of all its units: each has one tile's worth for its set-up, then its tiles.
+    __device__ __forceinline__ int entries(int kv_heads) const { return kv_heads * groups * (tiles + 1) * weight; }
 };
 template <int R>
 __device__ __forceinline__ AttnSeq at_seq(const AttnArgs &a, int s) {
@@ -240,6 +275,8 @@ __device__ __forceinline__ AttnSeq at_seq(const AttnArgs &a, int s) {
     q.len = max(len, 0);
     q.tiles = (q.len >> 7) + ((q.len & 127) != 0);
     q.groups = (q.rows * a.group + R - 1) / R;
+    // A tile of eight rows is paced by its codes' way from memory; each further eight add about half of that.
+    q.weight = R == 8 ? 1 : 1 + min(R, q.rows * a.group + 7) / 8;
     return q;
 }
 
@@ -255,27 +292,31 @@ struct AttnSplit {
     }
 };
 
-// A unit's entries in the list: one for its set-up, then its tiles.  A unit of at
-// most kAtSmall tiles is never cut: a cut inside it moves to its start (joining
-// two parts costs more than the tiles).
+// The largest weight of a tile.
+__host__ __device__ constexpr int at_max_weight(int rows) { return rows == 8 ? 1 : 1 + rows / 8; }
+
+// A unit of at most kAtSmall tiles is never cut: a cut inside it moves to its
+// start (joining two parts costs more than the tiles).  Other cuts move to the
+// start of a tile.
 constexpr int kAtSmall = 4;
 
 // A position in the CTA's range of the list: request, unit of the request, its
-// entries from e0 on and tiles [j0, j1), and the list entries left after them.
+// tiles from slot e0 on (slot 0 is the set-up, slot j + 1 tile j), tiles
+// [j0, j1), and the list entries left after them.
 template <int R>
 struct AttnWalk {
     const AttnArgs &a;
     AttnSeq q;
     int s, unit, e0, j0, j1, left;
-    __device__ __forceinline__ AttnWalk(const AttnArgs &args, const AttnSeq &seq, int s0, int offset, int count)
+    __device__ __forceinline__ AttnWalk(const AttnArgs &args, const AttnSeq &seq, int s0, int slot, int count)
         : a(args), q(seq), s(s0), left(count) {
-        unit = offset / (q.tiles + 1);
-        e0 = offset - unit * (q.tiles + 1);
+        unit = slot / (q.tiles + 1);
+        e0 = slot - unit * (q.tiles + 1);
         clip();
     }
     __device__ __forceinline__ void clip() {
-        const int e1 = min(q.tiles + 1, e0 + left);
-        left -= e1 - e0;
+        const int e1 = min(q.tiles + 1, e0 + left / q.weight);
+        left -= (e1 - e0) * q.weight;
         j0 = max(e0 - 1, 0);
         j1 = e1 - 1;
     }
@@ -294,6 +335,8 @@ struct AttnWalk {
     }
     __device__ __forceinline__ int head() const { return unit / q.groups; }
     __device__ __forceinline__ int row0() const { return (unit % q.groups) * R; }
+    // The unit's rows, up to a multiple of eight.
+    __device__ __forceinline__ int rows() const { return R == 8 ? 8 : min(R, (q.rows * a.group - row0() + 7) & ~7); }
 };
 
 template <typename T>
@@ -374,7 +417,7 @@ __device__ __forceinline__ void at_build_queries(const AttnArgs &a, const AttnWa
 #pragma unroll
                 for (int p = 0; p < PL; ++p) {
                     *reinterpret_cast<uint32_t *>(dst + h * N * 128 + at_swizzle<128>((p * R + r) * 128 + k * 32 + 4 * l8)) =
-                        p + 1 < PL ? at_plane<false>(t0, t1, t2, t3) : at_plane<true>(t0, t1, t2, t3);
+                        at_plane<PL>(p, t0, t1, t2, t3);
                 }
             }
     }
@@ -401,7 +444,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     __shared__ int s_vnan[2][ND * 128];                 // first position whose value code is NaN, per element
     __shared__ int s_scan[kAtThreads / 32];
     __shared__ AttnSeq s_seq;
-    __shared__ int s_first, s_off, s_begin, s_end, s_abort, s_last;
+    __shared__ int s_first, s_slot, s_begin, s_end, s_abort, s_last;
     __shared__ uint32_t tmem_slot;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -452,7 +495,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         AttnSeq q = {};
         for (int s = r0; s < r1; ++s) {
             q = at_seq<R>(a, s);
-            mine += a.kv_heads * q.groups * (q.tiles + 1);
+            mine += q.entries(a.kv_heads);
             bad |= q.bad;
         }
         if (bad && blockIdx.x == 0) atomicOr(a.status, 4u);
@@ -469,35 +512,34 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const int sum = s_scan[min(lane, kAtThreads / 32 - 1)];  // each warp's sum, in the lanes of its number
         total = __reduce_add_sync(0xFFFFFFFFu, lane < kAtThreads / 32 ? sum : 0);
         const int base = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sum : 0);
-        grid = min(static_cast<int>(gridDim.x), total);
+        // Every CTA's share is at least a tile, so no two cuts move to the same place inside a unit.
+        grid = min(static_cast<int>(gridDim.x), max(total / at_max_weight(R), min(total, 1)));
         const int at = base + pre - mine;  // this thread's first entry
         if (static_cast<int>(blockIdx.x) < grid) {
             const AttnSplit split(total, grid);
-            // Entry x, if it lies in one of this thread's requests: the request, the entry within it, and its list
-            // position, all moved to the unit's start where the unit is small.
-            auto locate = [&](int x, int &r, int &off) {
+            // Entry x, which lies in one of this thread's requests: the request, the slot within it, and its list
+            // position, moved to the slot's start, or to the unit's where the unit is small.
+            auto locate = [&](int x, int &r, int &slot) {
                 int here = at;
                 r = r0;
                 if (per > 1) q = at_seq<R>(a, r);
-                for (;;) {
-                    const int size = a.kv_heads * q.groups * (q.tiles + 1);
-                    if (x < here + size) break;
-                    here += size;
+                while (x >= here + q.entries(a.kv_heads)) {
+                    here += q.entries(a.kv_heads);
                     q = at_seq<R>(a, ++r);
                 }
-                off = x - here;
-                if (q.tiles <= kAtSmall) off -= off % (q.tiles + 1);
-                return here + off;
+                slot = (x - here) / q.weight;
+                if (q.tiles <= kAtSmall) slot -= slot % (q.tiles + 1);
+                return here + slot * q.weight;
             };
             const int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
-            int r, off;
-            if (at <= x1 && x1 < at + mine) s_end = locate(x1, r, off);
+            int r, slot;
+            if (at <= x1 && x1 < at + mine) s_end = locate(x1, r, slot);
             else if (tid == 0 && x1 == total) s_end = total;
             if (at <= x0 && x0 < at + mine) {
-                s_begin = locate(x0, r, off);
+                s_begin = locate(x0, r, slot);
                 s_seq = q;
                 s_first = r;
-                s_off = off;
+                s_slot = slot;
             }
         }
         __syncthreads();
@@ -506,7 +548,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 
     if (static_cast<int>(blockIdx.x) < grid && s_begin < s_end) {
         const AttnSplit split(total, grid);
-        AttnWalk<R> w(a, s_seq, s_first, s_off, s_end - s_begin);
+        AttnWalk<R> w(a, s_seq, s_first, s_slot, s_end - s_begin);
         const bool built = !w.none();
         if (built && warp < kAtKWarp) {
             at_build_queries<T, PL, R, ND>(a, w, sQ, s_qs[0], s_lim[0], warp, kAtKWarp, lane);
@@ -706,6 +748,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     for (int c = 0; c < R; c += 8) den[c + own] = 0.f;
                 }
                 const int seen_by_all = w.q.len - w.q.rows;  // positions up to here are seen by every row
+                const int rows = w.rows();                   // columns past the unit's rows hold what they may
                 for (int j = w.j0; j < w.j1; ++j, ++it) {
                     const int cs = st;
                     const uint32_t cph = ph;
@@ -721,16 +764,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const float ks = sc[cs][0][tg >> a.block_log2];
                     // Scores of rows c .. c + 7, in base 2; what a row does not see is -inf.
                     auto scores = [&](int c, float (&s)[8]) {
-                        float d[PL][8];
+                        float d[PL][8], qs[8];
 #pragma unroll
                         for (int p = 0; p < PL; ++p) at_ld8(tmem + lanes + static_cast<uint32_t>(g * N + p * R + c), d[p]);
+                        at_lds8(s_qs[ub] + c, qs);
                         at_wait_ld();
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
-                            float u = d[PL - 1][r];
+                            float x[PL];
 #pragma unroll
-                            for (int p = PL - 2; p >= 0; --p) u = fmaf(u, 0.0625f, d[p][r]);
-                            s[r] = u * (s_qs[ub][c + r] * ks);
+                            for (int p = 0; p < PL; ++p) x[p] = d[p][r];
+                            s[r] = at_join<PL>(x) * (qs[r] * ks);
                         }
                         if (edge) {
 #pragma unroll
@@ -746,7 +790,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     float s[8];
                     // Each row's maximum over the tile.
 #pragma unroll 1
-                    for (int c = 0; c < R; c += 8) {
+                    for (int c = 0; c < rows; c += 8) {
                         scores(c, s);
                         const float top = at_butterfly<8>(s, lane, [](float x, float y) { return fmaxf(x, y); });
                         if (owner) s_wmax[g][wg][c + own] = top;
@@ -762,7 +806,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const int ve = max(__float_as_int(vtop) >> 23, 8);  // biased exponent; 2^-119 and below count as 2^-119
                     const float vs = sc[cs][1][tg >> a.block_log2] * __int_as_float(ve == 254 ? 0x00400000 : (254 - ve) << 23) * (1 << kAtPeakLog2);
                     at_bar(bar);
-                    if (tg < R) {
+                    if (tg < rows) {
                         const float m = fmaxf(fmaxf(s_wmax[g][0][tg], s_wmax[g][1][tg]), fmaxf(s_wmax[g][2][tg], s_wmax[g][3][tg]));
                         const float tref = fmaxf(m, kAtNoRef), now = fmaxf(ref, tref);
                         s_lf[g][tg] = at_exp2(tref - now);
@@ -777,20 +821,21 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     uint8_t *pb = sP + g * Sh::kPBytes;
 #pragma unroll 1
-                    for (int c = 0; c < R; c += 8) {
+                    for (int c = 0; c < rows; c += 8) {
                         if constexpr (R > 8) scores(c, s);
-                        float t[8];
+                        float t[8], tref[8];
+                        at_lds8(s_tref[g] + c, tref);
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
-                            s[r] = at_exp2(s[r] - s_tref[g][c + r]);
+                            s[r] = at_exp2(s[r] - tref[r]);
                             t[r] = s[r] * vs;
                             if (edge && pos > s_lim[ub][c + r]) t[r] = 0.f;  // whatever the scale
                         }
 #pragma unroll
                         for (int p = 0; p < PL; ++p) {
                             uint2 word;
-                            word.x = p + 1 < PL ? at_plane<false>(t[0], t[1], t[2], t[3]) : at_plane<true>(t[0], t[1], t[2], t[3]);
-                            word.y = p + 1 < PL ? at_plane<false>(t[4], t[5], t[6], t[7]) : at_plane<true>(t[4], t[5], t[6], t[7]);
+                            word.x = at_plane<PL>(p, t[0], t[1], t[2], t[3]);
+                            word.y = at_plane<PL>(p, t[4], t[5], t[6], t[7]);
                             *reinterpret_cast<uint2 *>(pb + at_swizzle<N>(tg * N + p * R + c)) = word;
                         }
                         const float sum = at_butterfly<8>(s, lane, [](float x, float y) { return x + y; });
@@ -810,17 +855,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                                     for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row + tg * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
                                     continue;
                                 }
+                                uint32_t nan = 0;
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const uint4 x = *reinterpret_cast<const uint4 *>(row + tg * 128 + c * 16);
+                                    nan |= ((x.x & 0x7F7F7F7Fu) + 0x01010101u) | ((x.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                                           ((x.z & 0x7F7F7F7Fu) + 0x01010101u) | ((x.w & 0x7F7F7F7Fu) + 0x01010101u);
+                                }
+                                if ((nan & 0x80808080u) == 0u) continue;  // no NaN code in the row
 #pragma unroll 1
-                                for (int c = 0; c < 32; ++c) {
-                                    uint32_t *at = reinterpret_cast<uint32_t *>(row + at_swizzle<128>(tg * 128 + c * 4));
-                                    uint32_t x = *at;
-                                    if ((((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) == 0u) continue;  // no NaN code among the four
-                                    for (int y = 0; y < 4; ++y)
-                                        if (((x >> (8 * y)) & 0x7Fu) == 0x7Fu) {
-                                            x &= ~(0xFFu << (8 * y));
-                                            atomicMin(&s_vnan[ub][h * 128 + c * 4 + y], pos);
-                                        }
-                                    *at = x;
+                                for (int c = 0; c < 128; ++c) {
+                                    uint8_t *at = row + at_swizzle<128>(tg * 128 + c);
+                                    if ((*at & 0x7Fu) != 0x7Fu) continue;
+                                    *at = 0;
+                                    atomicMin(&s_vnan[ub][h * 128 + c], pos);
                                 }
                             }
                         }
@@ -829,7 +877,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&p_full[g]));
                 }
-                if (tg < R) s_mref[ub][g][tg] = ref;
+                if (tg < rows) s_mref[ub][g][tg] = ref;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&ml_full[ub]));
                 ++iu;
@@ -847,9 +895,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             T *out = static_cast<T *>(a.out);
             do {
                 const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0), kvh = w.head();
+                const int rows = w.rows();
                 const bool whole = w.j0 == 0 && w.j1 == w.q.tiles;
-                const int unit_begin = done - w.e0;  // list position of the unit
-                done += w.j1 + 1 - w.e0;
+                const int unit_begin = done - w.e0 * w.q.weight;  // list position of the unit
+                done += (w.j1 + 1 - w.e0) * w.q.weight;
                 auto out_row = [&](int r) {  // (row, query head) of the unit's row r
                     const int i = (row0 + r) / a.group;
                     return static_cast<int64_t>(w.q.first + i) * a.out_stride +
@@ -882,36 +931,43 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     t8_fence_after();
                     bool raised = false;
                     at_bar(3);  // every warp has read the last tile's factors
-                    if (dt < R) {
+                    if (dt < rows) {
                         const float tref = s_tref[b][dt], now = fmaxf(ref, tref);
                         raised = now > ref;
                         s_corr[dt] = at_exp2(ref - now);
                         s_of[dt] = at_exp2(tref - now) * s_vf[b];
                         ref = now;
                     }
-                    if (at_bar_or(3, raised)) {
+                    const bool moved = at_bar_or(3, raised);
 #pragma unroll
-                        for (int r = 0; r < R; ++r)
+                    for (int c = 0; c < R; c += 8) {
+                        if (c < rows) {
+                            float f[8];
+                            if (moved) {
+                                at_lds8(s_corr + c, f);
 #pragma unroll
-                            for (int h = 0; h < ND; ++h) acc[h][r] *= s_corr[r];
-                    }
+                                for (int h = 0; h < ND; ++h)
 #pragma unroll
-                    for (int h = 0; h < ND; ++h)
+                                    for (int r = 0; r < 8; ++r) acc[h][c + r] *= f[r];
+                            }
+                            at_lds8(s_of + c, f);
 #pragma unroll
-                        for (int c = 0; c < R; c += 8) {
-                            float d[PL][8];
+                            for (int h = 0; h < ND; ++h) {
+                                float d[PL][8];
 #pragma unroll
-                            for (int p = 0; p < PL; ++p)
-                                at_ld8(tmem + lanes + static_cast<uint32_t>(2 * N + (b * ND + h) * N + p * R + c), d[p]);
-                            at_wait_ld();
+                                for (int p = 0; p < PL; ++p)
+                                    at_ld8(tmem + lanes + static_cast<uint32_t>(2 * N + (b * ND + h) * N + p * R + c), d[p]);
+                                at_wait_ld();
 #pragma unroll
-                            for (int r = 0; r < 8; ++r) {
-                                float u = d[PL - 1][r];
+                                for (int r = 0; r < 8; ++r) {
+                                    float x[PL];
 #pragma unroll
-                                for (int p = PL - 2; p >= 0; --p) u = fmaf(u, 0.0625f, d[p][r]);
-                                acc[h][c + r] = fmaf(u, s_of[c + r], acc[h][c + r]);
+                                    for (int p = 0; p < PL; ++p) x[p] = d[p][r];
+                                    acc[h][c + r] = fmaf(at_join<PL>(x), f[r], acc[h][c + r]);
+                                }
                             }
                         }
+                    }
                     t8_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&o_free[b]));
@@ -936,14 +992,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     }
                 }
                 float l = 0.f;  // denominator of row `dt` at the maximum `ref`
-                if (dt < R) {
+                if (dt < rows) {
 #pragma unroll
                     for (int g = 0; g < 2; ++g)
                         l += at_exp2(s_mref[ub][g][dt] - ref) * ((s_l[ub][4 * g][dt] + s_l[ub][4 * g + 1][dt]) +
                                                                  (s_l[ub][4 * g + 2][dt] + s_l[ub][4 * g + 3][dt]));
                 }
                 if (whole) {
-                    if (dt < R) {
+                    if (dt < rows) {
                         s_inv[dt] = l == 0.f ? 0.f : 1.f / l;
                         if (a.lse && dt < valid) a.lse[lse_at(dt)] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
                     }
@@ -975,7 +1031,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         __stcg(mine + R * ND * 128 + dt, ref);
                         __stcg(mine + R * ND * 128 + R + dt, l);
                     }
-                    const int b0 = split.owner(unit_begin + 1), parts = split.owner(unit_begin + w.q.tiles) - b0 + 1;
+                    // The CTAs of the unit's first and last tile: a tile belongs to the last CTA whose range begins in it or
+                    // before it.
+                    const int b0 = split.owner(unit_begin + 2 * w.q.weight - 1);
+                    const int parts = split.owner(unit_begin + (w.q.tiles + 1) * w.q.weight - 1) - b0 + 1;
                     at_bar(3);
                     if (dt == 0) {  // the barrier and this release order every thread's sums before the count
                         uint32_t old;
