@@ -11,18 +11,21 @@
 // swizzle), V's tile the second's (the same landing, read M-major), so the
 // CUDA cores never touch a code.  q and p s_v are the B operands: each value
 // is carried as PL e4m3 planes, each the rounding of what the one before leaves
-// (all subtractions exact).  Plane p is a column group of its own, and the
-// products are weighed and summed in f32.
-//   f32 queries and outputs: PL = 4, a value keeps 2^-16 of itself at worst
-//     (rms 5e-7), which leaves the result at the error of an f32 computation.
-//   bf16: PL = 2.  bf16's 8 bits fit two planes, so q is exact; p keeps 2^-8 at
-//     worst (rms 5e-4), a third of the rounding of the bf16 output.
+// (all subtractions exact).  Planes of one weight add up in the same columns of
+// tensor memory (an MMA each), planes of another weight lie beside them.
+//   f32 queries and outputs: four planes of weight 1, 1, 2^-8, 2^-8; a value keeps
+//     2^-16 of itself at worst (rms 5e-7), which leaves the result at the error
+//     of an f32 computation.
+//   bf16: two planes of weight 1, 1 (eight rows: 1, 2^-4, as an MMA has 16 columns
+//     at least).  bf16's 8 bits fit two planes, so q is exact to 2^-18 of its
+//     row's largest; p keeps 2^-8 at worst (rms 5e-4), a third of the rounding
+//     of the bf16 output.
 // Scores, statistics and output sums are f32; the softmax denominator is
 // summed from the f32 weights.
 //
 // p is relative to the maximum over its own tile and row, not to the running
 // one, and p s_v to the tile's largest |s_v|, times 2^8: every tile's weights
-// fill e4m3's range, so what a weight loses is 2^-22 (bf16) or 2^-26 (f32) of
+// fill e4m3's range, so what a weight loses is 2^-18 (bf16) or 2^-26 (f32) of
 // its own tile's largest at worst, and a long tail of small weights keeps its
 // share.  Each tile's product is read back and added to f32 sums in registers
 // with its factor 2^(m_r - running maximum) max|s_v| 2^-8, so nothing in
@@ -53,6 +56,7 @@ namespace fp8blk {
 constexpr int kAtThreads = 640;
 constexpr int kAtOutWarp = 8, kAtQueryWarp = 12, kAtKWarp = 16, kAtMmaWarp = 17, kAtVWarp = 19;
 constexpr int kAtTile = 128;            // tokens per tile
+constexpr int kAtDeep = 4;              // tiles between the first product and the sums: scores, weights and products
 constexpr int kAtMaxGrid = 256;         // bound on CTAs: arrival counters and partial sums in the workspace
 constexpr size_t kAtHeaderBytes = kAtMaxGrid * sizeof(uint32_t);
 constexpr float kAtNoRef = -3.0e38f;    // maximum of a row that has seen nothing
@@ -76,19 +80,23 @@ __device__ float g_attn_nan = __builtin_nanf("");  // what a block outside the p
 
 template <int PL, int R, int ND>
 struct AttnShape {
-    static constexpr int N = PL * R;                          // columns of both B operands
+    static constexpr int kGroups = PL == 4 || R == 8 ? 2 : 1; // weights, each a group of R columns
+    static constexpr int kSteps = PL / kGroups;               // planes of one weight, an MMA each
+    static constexpr int N = kGroups * R;                     // columns of a product
     static constexpr int kTileBytes = ND * kAtTile * 128;     // K or V codes of a tile
-    static constexpr int kQBytes = ND * N * 128;              // query planes of a unit
-    static constexpr int kPBytes = kAtTile * N;               // weight planes of a tile
-    static constexpr int kFixed = 1024 + 2 * kQBytes + 2 * kPBytes;
+    static constexpr int kQStep = N * 128;                    // query planes of one step and half of head_dim
+    static constexpr int kQBytes = ND * kSteps * kQStep;      // query planes of a unit
+    static constexpr int kPStep = kAtTile * N;                // weight planes of one step
+    static constexpr int kPBytes = kSteps * kPStep;           // weight planes of a tile
+    static constexpr int kFixed = 1024 + 2 * kQBytes + kAtDeep * kPBytes;
     static constexpr int kRoom = 227 * 1024 - 12 * 1024;      // dynamic shared memory beside the static arrays
     static constexpr int kStages0 = (kRoom - kFixed) / (2 * kTileBytes);
     static constexpr int kStages = kStages0 > 6 ? 6 : kStages0;
     static constexpr size_t kSmem = kFixed + static_cast<size_t>(kStages) * 2 * kTileBytes;
-    static constexpr int kTmemUsed = N * (2 + 2 * ND);        // S and O, both double buffered
-    static constexpr int kTmem = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
+    static constexpr int kTmemUsed = N * kAtDeep * (1 + ND);  // scores and products
+    static constexpr int kTmem = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
     static constexpr int kPartial = R * (ND * 128) + 2 * R;   // floats of one partial
-    static_assert(kStages >= 2 && kTmemUsed <= 512 && N % 16 == 0 && N <= 128, "shape");
+    static_assert(kStages >= 2 && kTmemUsed <= 512 && N % 16 == 0 && N <= 64, "shape");
 };
 
 // Shared-memory descriptor of an operand tile whose rows are `row_bytes` (128,
@@ -138,26 +146,23 @@ __device__ __forceinline__ void at_minus(uint32_t h, float &a, float &b) {
         : "+f"(a), "+f"(b)
         : "r"(h));
 }
-// Planes.  p = 0 is the value's own e4m3 code, and each plane takes what the one
-// before leaves; what is left after plane 0 of two, or plane 1 of four, is scaled
-// up, so that it does not end in e4m3's subnormals: by 16, or by 256.  So the
-// planes weigh 1, 2^-4, or 1, 1, 2^-8, 2^-8.
-template <int PL>
-__device__ __forceinline__ constexpr float at_plane_gain(int p) { return PL == 2 ? 16.f : p == 1 ? 256.f : 1.f; }
-template <int PL>
-__device__ __forceinline__ float at_join(const float (&d)[PL]) {
-    if constexpr (PL == 2) return fmaf(d[1], 1.f / 16.f, d[0]);
-    else return fmaf(d[2] + d[3], 1.f / 256.f, d[0] + d[1]);
+// What is left after a plane is scaled up where the next one has another weight,
+// so that it does not end in e4m3's subnormals.  Plane p lies in step p % steps,
+// column group p / steps.
+template <int PL, int GROUPS>
+__device__ __forceinline__ float at_join(const float (&d)[GROUPS]) {
+    if constexpr (GROUPS == 1) return d[0];
+    else return fmaf(d[GROUPS - 1], PL == 2 ? 1.f / 16.f : 1.f / 256.f, d[0]);
 }
 // The four values' plane p as a word of codes; the values become what it leaves.
-template <int PL>
+template <int PL, int GROUPS>
 __device__ __forceinline__ uint32_t at_plane(int p, float &a, float &b, float &c, float &d) {
     const uint32_t lo = t8_to_e4m3x2(a, b), hi = t8_to_e4m3x2(c, d);
     if (p + 1 < PL) {
         at_minus(at_e4m3x2_f16x2(lo), a, b);
         at_minus(at_e4m3x2_f16x2(hi), c, d);
-        const float gain = at_plane_gain<PL>(p);
-        if (gain != 1.f) {
+        if (GROUPS == 2 && p + 1 == PL / 2) {
+            const float gain = PL == 2 ? 16.f : 256.f;
             a *= gain;
             b *= gain;
             c *= gain;
@@ -315,7 +320,7 @@ struct AttnWalk {
         clip();
     }
     __device__ __forceinline__ void clip() {
-        const int e1 = min(q.tiles + 1, e0 + left / q.weight);
+        const int e1 = min(q.tiles + 1, e0 + (R == 8 ? left : left / q.weight));
         left -= (e1 - e0) * q.weight;
         j0 = max(e0 - 1, 0);
         j1 = e1 - 1;
@@ -362,7 +367,7 @@ __device__ __forceinline__ void at_store4(__nv_bfloat16 *p, float4 v) {
 template <typename T, int PL, int R, int ND>
 __device__ __forceinline__ void at_build_queries(const AttnArgs &a, const AttnWalk<R> &w, uint8_t *dst, float *qs, int *lim, int part,
                                                  int parts, int lane) {
-    constexpr int N = PL * R;
+    using Sh = AttnShape<PL, R, ND>;
     const int row0 = w.row0(), valid = min(R, w.q.rows * a.group - row0);
     const T *q = static_cast<const T *>(a.q) + w.q.first * a.q_stride + static_cast<int64_t>(w.head()) * a.group * a.head_dim;
     const int sub = lane >> 3, l8 = lane & 7;
@@ -416,8 +421,9 @@ __device__ __forceinline__ void at_build_queries(const AttnArgs &a, const AttnWa
                 float t0 = v[h][k].x * f1 * f2, t1 = v[h][k].y * f1 * f2, t2 = v[h][k].z * f1 * f2, t3 = v[h][k].w * f1 * f2;
 #pragma unroll
                 for (int p = 0; p < PL; ++p) {
-                    *reinterpret_cast<uint32_t *>(dst + h * N * 128 + at_swizzle<128>((p * R + r) * 128 + k * 32 + 4 * l8)) =
-                        at_plane<PL>(p, t0, t1, t2, t3);
+                    const int n = p / Sh::kSteps * R + r;
+                    *reinterpret_cast<uint32_t *>(dst + (h * Sh::kSteps + p % Sh::kSteps) * Sh::kQStep + at_swizzle<128>(n * 128 + k * 32 + 4 * l8)) =
+                        at_plane<PL, Sh::kGroups>(p, t0, t1, t2, t3);
                 }
             }
     }
@@ -428,17 +434,17 @@ template <typename T, int PL, int R, int ND>
 __global__ void __launch_bounds__(kAtThreads, 1)
     kv_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
     using Sh = AttnShape<PL, R, ND>;
-    constexpr int N = Sh::N, S = Sh::kStages;
+    constexpr int N = Sh::N, S = Sh::kStages, G = Sh::kGroups;
     extern __shared__ __align__(1024) uint8_t at_smem[];
     __shared__ __align__(8) uint64_t k_full[S], v_full[S], v_free[S], sc_full[S];
-    __shared__ __align__(8) uint64_t s_full[2], s_free[2], p_full[2], o_full[2], o_free[2];
+    __shared__ __align__(8) uint64_t s_full[kAtDeep], s_free[kAtDeep], p_full[kAtDeep], o_full[kAtDeep], o_free[kAtDeep];
     __shared__ __align__(8) uint64_t q_full[2], ml_full[2], ml_free[2], mma_done[2];
     __shared__ float sc[S][2][8];                       // k and v scales of a tile's blocks
     __shared__ __align__(16) float s_qs[2][R];          // per query row: 2^-e x scale x log2 e (NaN: the row is not finite)
     __shared__ __align__(16) int s_lim[2][R];           // last position each row sees
     __shared__ __align__(16) float s_wmax[2][4][R];     // per softmax group: its warps' maxima over the tile
-    __shared__ __align__(16) float s_tref[2][R], s_lf[2][R], s_lc[2][R];  // tile maximum; factors into and of the group's denominator
-    __shared__ float s_vf[2];                           // factor of the tile's product from its value scales
+    __shared__ __align__(16) float s_tref[kAtDeep][R], s_lf[2][R], s_lc[2][R];  // tile maximum; factors into and of the group's denominator
+    __shared__ float s_vf[kAtDeep];                           // factor of the tile's product from its value scales
     __shared__ __align__(16) float s_corr[R], s_of[R];  // output sums: factor of the sums so far, and of the tile's product
     __shared__ float s_l[2][8][R], s_mref[2][2][R], s_inv[R];
     __shared__ int s_vnan[2][ND * 128];                 // first position whose value code is NaN, per element
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t *sQ = at_smem + ((1024u - (smem_addr(at_smem) & 1023u)) & 1023u);
     uint8_t *sP = sQ + 2 * Sh::kQBytes;
-    uint8_t *sK = sP + 2 * Sh::kPBytes;                 // S tiles of K, then S of V
+    uint8_t *sK = sP + kAtDeep * Sh::kPBytes;                 // S tiles of K, then S of V
     uint8_t *sV = sK + static_cast<size_t>(S) * Sh::kTileBytes;
 
     if (tid == 0) {
@@ -460,12 +466,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             mbar_init(smem_addr(&v_free[i]), 1);
             mbar_init(smem_addr(&sc_full[i]), 64);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kAtDeep; ++i) {
             mbar_init(smem_addr(&s_full[i]), 1);
             mbar_init(smem_addr(&s_free[i]), 4);
             mbar_init(smem_addr(&p_full[i]), 4);
             mbar_init(smem_addr(&o_full[i]), 1);
             mbar_init(smem_addr(&o_free[i]), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&q_full[i]), 4);
             mbar_init(smem_addr(&ml_full[i]), 8);
             mbar_init(smem_addr(&ml_free[i]), 4);
@@ -638,7 +646,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             if (lane == 0) {
                 const int g = warp - kAtMmaWarp;
                 constexpr uint32_t qk_idesc = at_idesc(N, false), pv_idesc = at_idesc(N, true);
+                // Descriptors of the rings' starts; an offset adds to the address field (16-byte units, 14 bits).
+                const uint64_t k_desc = at_desc<128>(smem_addr(sK)), q_desc = at_desc<128>(smem_addr(sQ));
+                const uint64_t v_desc = at_desc<128>(smem_addr(sV)), p_desc = at_desc<N>(smem_addr(sP));
                 int qt = g, pt = g;         // next tile of each product
+                int q_st = g % S, p_st = g % S;
+                uint32_t q_ph = 0, p_ph = 0;
                 int iu = -1, unit_end = 0;  // the first product's unit, and the tile after its last
                 bool more = true;           // false: unit_end is the end of the range
                 uint64_t t0 = 0;
@@ -646,24 +659,30 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 while (more || pt < unit_end) {
                     bool went = false;
                     {
-                        const int st = pt % S;
-                        const uint32_t ph = static_cast<uint32_t>(pt / S) & 1u, bp = static_cast<uint32_t>(pt >> 1) & 1u;
-                        if (pt < qt && mbar_test_wait(smem_addr(&p_full[g]), bp) && mbar_test_wait(smem_addr(&v_full[st]), ph) &&
-                            (pt < 2 || mbar_test_wait(smem_addr(&o_free[g]), bp ^ 1u))) {
+                        const int b = pt & (kAtDeep - 1);
+                        const uint32_t bp = static_cast<uint32_t>(pt / kAtDeep) & 1u;
+                        if (pt < qt && mbar_test_wait(smem_addr(&p_full[b]), bp) && mbar_test_wait(smem_addr(&v_full[p_st]), p_ph) &&
+                            (pt < kAtDeep || mbar_test_wait(smem_addr(&o_free[b]), bp ^ 1u))) {
                             t8_fence_after();
-                            const uint32_t va = smem_addr(sV) + static_cast<uint32_t>(st) * Sh::kTileBytes;
-                            const uint32_t pa = smem_addr(sP + g * Sh::kPBytes);
+                            const uint64_t va = v_desc + static_cast<uint32_t>(p_st) * (Sh::kTileBytes / 16);
+                            const uint64_t pa = p_desc + static_cast<uint32_t>(b) * (Sh::kPBytes / 16);
+                            const uint32_t d = tmem + static_cast<uint32_t>((kAtDeep + b * ND) * N);
 #pragma unroll
-                            for (int h = 0; h < ND; ++h) {
-                                const uint32_t d = tmem + static_cast<uint32_t>(2 * N + (g * ND + h) * N);
+                            for (int h = 0; h < ND; ++h)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    t8_mma(d, at_desc<128>(va + h * kAtTile * 128 + c * 32 * 128), at_desc<N>(pa + c * 32 * N), pv_idesc,
-                                           c > 0);
-                            }
-                            t8_commit(smem_addr(&o_full[g]));
-                            t8_commit(smem_addr(&v_free[st]));
+                                for (int x = 0; x < Sh::kSteps; ++x)
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c)
+                                        t8_mma(d + h * N, va + (h * kAtTile * 128 + c * 32 * 128) / 16,
+                                               pa + (x * Sh::kPStep + c * 32 * N) / 16, pv_idesc, x + c > 0);
+                            t8_commit(smem_addr(&o_full[b]));
+                            t8_commit(smem_addr(&v_free[p_st]));
                             pt += 2;
+                            p_st += 2;
+                            if (p_st >= S) {
+                                p_st -= S;
+                                p_ph ^= 1u;
+                            }
                             went = true;
                         }
                     }
@@ -676,23 +695,30 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         }
                     }
                     if (qt < unit_end) {
-                        const int st = qt % S;
-                        const uint32_t ph = static_cast<uint32_t>(qt / S) & 1u, bp = static_cast<uint32_t>(qt >> 1) & 1u;
-                        if (mbar_test_wait(smem_addr(&k_full[st]), ph) && (qt < 2 || mbar_test_wait(smem_addr(&s_free[g]), bp ^ 1u)) &&
+                        const int b = qt & (kAtDeep - 1);
+                        const uint32_t bp = static_cast<uint32_t>(qt / kAtDeep) & 1u;
+                        if (mbar_test_wait(smem_addr(&k_full[q_st]), q_ph) && (qt < kAtDeep || mbar_test_wait(smem_addr(&s_free[b]), bp ^ 1u)) &&
                             mbar_test_wait(smem_addr(&q_full[iu & 1]), static_cast<uint32_t>(iu >> 1) & 1u)) {
                             t8_fence_after();
-                            const uint32_t ka = smem_addr(sK) + static_cast<uint32_t>(st) * Sh::kTileBytes;
-                            const uint32_t qa = smem_addr(sQ + (iu & 1) * Sh::kQBytes);
-                            const uint32_t d = tmem + static_cast<uint32_t>(g * N);
+                            const uint64_t ka = k_desc + static_cast<uint32_t>(q_st) * (Sh::kTileBytes / 16);
+                            const uint64_t qa = q_desc + static_cast<uint32_t>(iu & 1) * (Sh::kQBytes / 16);
+                            const uint32_t d = tmem + static_cast<uint32_t>(b * N);
 #pragma unroll
                             for (int h = 0; h < ND; ++h)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    if (h * 128 + c * 32 < a.head_dim)  // columns past head_dim are zeros on both sides
-                                        t8_mma(d, at_desc<128>(ka + h * kAtTile * 128 + c * 32), at_desc<128>(qa + h * N * 128 + c * 32),
-                                               qk_idesc, h + c > 0);
-                            t8_commit(smem_addr(&s_full[g]));
+                                for (int x = 0; x < Sh::kSteps; ++x)
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c)
+                                        if (h * 128 + c * 32 < a.head_dim)  // columns past head_dim are zeros on both sides
+                                            t8_mma(d, ka + (h * kAtTile * 128 + c * 32) / 16,
+                                                   qa + ((h * Sh::kSteps + x) * Sh::kQStep + c * 32) / 16, qk_idesc, h + x + c > 0);
+                            t8_commit(smem_addr(&s_full[b]));
                             qt += 2;
+                            q_st += 2;
+                            if (q_st >= S) {
+                                q_st -= S;
+                                q_ph ^= 1u;
+                            }
                             went = true;
                         }
                     }
@@ -757,24 +783,26 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         ph ^= 1u;
                     }
                     if ((it & 1) != g) continue;
-                    const uint32_t bp = static_cast<uint32_t>((it >> 1) & 1);
-                    ok = ok && at_warp_wait(smem_addr(&sc_full[cs]), cph, &s_abort) && at_warp_wait(smem_addr(&s_full[g]), bp, &s_abort);
+                    const uint32_t bp = static_cast<uint32_t>(it / kAtDeep) & 1u;
+                    const int b = static_cast<int>(it & (kAtDeep - 1));
+                    ok = ok && at_warp_wait(smem_addr(&sc_full[cs]), cph, &s_abort) &&
+                         at_warp_wait(smem_addr(&s_full[b]), bp, &s_abort);
                     const int pos = j * kAtTile + tg;
                     const bool edge = (j + 1) * kAtTile - 1 > seen_by_all;  // some row does not see the whole tile
                     const float ks = sc[cs][0][tg >> a.block_log2];
                     // Scores of rows c .. c + 7, in base 2; what a row does not see is -inf.
                     auto scores = [&](int c, float (&s)[8]) {
-                        float d[PL][8], qs[8];
+                        float d[G][8], qs[8];
 #pragma unroll
-                        for (int p = 0; p < PL; ++p) at_ld8(tmem + lanes + static_cast<uint32_t>(g * N + p * R + c), d[p]);
+                        for (int x = 0; x < G; ++x) at_ld8(tmem + lanes + static_cast<uint32_t>(b * N + x * R + c), d[x]);
                         at_lds8(s_qs[ub] + c, qs);
                         at_wait_ld();
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
-                            float x[PL];
+                            float u[G];
 #pragma unroll
-                            for (int p = 0; p < PL; ++p) x[p] = d[p][r];
-                            s[r] = at_join<PL>(x) * (qs[r] * ks);
+                            for (int x = 0; x < G; ++x) u[x] = d[x][r];
+                            s[r] = at_join<PL>(u) * (qs[r] * ks);
                         }
                         if (edge) {
 #pragma unroll
@@ -784,7 +812,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     auto release = [&] {  // the scores' columns may be overwritten
                         t8_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_addr(&s_free[g]));
+                        if (lane == 0) mbar_arrive(smem_addr(&s_free[b]));
                     };
                     t8_fence_after();
                     float s[8];
@@ -812,19 +840,19 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         s_lf[g][tg] = at_exp2(tref - now);
                         s_lc[g][tg] = at_exp2(ref - now);
                         ref = now;
-                        // The output sums have read what the tile before last left here, and the second MMA its weights.
-                        if (it >= 2) ok = at_wait(smem_addr(&o_free[g]), bp ^ 1u, &s_abort) && ok;
-                        s_tref[g][tg] = tref;
-                        if (tg == 0) s_vf[g] = __int_as_float((ve - kAtPeakLog2) << 23);
+                        // The output sums have read what the tile kAtDeep ago left here, and the second MMA its weights.
+                        if (it >= kAtDeep) ok = at_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort) && ok;
+                        s_tref[b][tg] = tref;
+                        if (tg == 0) s_vf[b] = __int_as_float((ve - kAtPeakLog2) << 23);
                     }
                     at_bar(bar);
                     ok = __all_sync(0xFFFFFFFFu, ok);
-                    uint8_t *pb = sP + g * Sh::kPBytes;
+                    uint8_t *pb = sP + b * Sh::kPBytes;
 #pragma unroll 1
                     for (int c = 0; c < rows; c += 8) {
                         if constexpr (R > 8) scores(c, s);
                         float t[8], tref[8];
-                        at_lds8(s_tref[g] + c, tref);
+                        at_lds8(s_tref[b] + c, tref);
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
                             s[r] = at_exp2(s[r] - tref[r]);
@@ -834,9 +862,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                         for (int p = 0; p < PL; ++p) {
                             uint2 word;
-                            word.x = at_plane<PL>(p, t[0], t[1], t[2], t[3]);
-                            word.y = at_plane<PL>(p, t[4], t[5], t[6], t[7]);
-                            *reinterpret_cast<uint2 *>(pb + at_swizzle<N>(tg * N + p * R + c)) = word;
+                            word.x = at_plane<PL, G>(p, t[0], t[1], t[2], t[3]);
+                            word.y = at_plane<PL, G>(p, t[4], t[5], t[6], t[7]);
+                            *reinterpret_cast<uint2 *>(pb + p % Sh::kSteps * Sh::kPStep + at_swizzle<N>(tg * N + p / Sh::kSteps * R + c)) = word;
                         }
                         const float sum = at_butterfly<8>(s, lane, [](float x, float y) { return x + y; });
                         if (owner) den[c + own] = fmaf(den[c + own], s_lc[g][c + own], sum * s_lf[g][c + own]);
@@ -875,7 +903,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic stores -> the MMA
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&p_full[g]));
+                    if (lane == 0) mbar_arrive(smem_addr(&p_full[b]));
                 }
                 if (tg < rows) s_mref[ub][g][tg] = ref;
                 __syncwarp();
@@ -887,7 +915,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             // ---------------- output sums: thread = element d (and d + 128) of head_dim
             const int dt = tid - kAtOutWarp * 32, ow = warp - kAtOutWarp;
             const uint32_t lanes = static_cast<uint32_t>(ow * 32) << 16;
-            int b = 0, ub = 0;
+            int ub = 0;
             int64_t it = 0, iu = 0;
             int done = s_begin;
             bool ok = true;
@@ -925,7 +953,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                     for (int r = 0; r < R; ++r) acc[h][r] = 0.f;
                 for (int j = w.j0; j < w.j1; ++j) {
-                    const uint32_t bp = static_cast<uint32_t>((it >> 1) & 1);
+                    const int b = static_cast<int>(it & (kAtDeep - 1));
+                    const uint32_t bp = static_cast<uint32_t>(it / kAtDeep) & 1u;
                     ok = ok && at_warp_wait(smem_addr(&o_full[b]), bp, &s_abort) &&
                          at_warp_wait(smem_addr(&p_full[b]), bp, &s_abort);  // long complete: orders the softmax's words
                     t8_fence_after();
@@ -953,16 +982,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                             at_lds8(s_of + c, f);
 #pragma unroll
                             for (int h = 0; h < ND; ++h) {
-                                float d[PL][8];
+                                float d[G][8];
 #pragma unroll
-                                for (int p = 0; p < PL; ++p)
-                                    at_ld8(tmem + lanes + static_cast<uint32_t>(2 * N + (b * ND + h) * N + p * R + c), d[p]);
+                                for (int x = 0; x < G; ++x)
+                                    at_ld8(tmem + lanes + static_cast<uint32_t>((kAtDeep + b * ND + h) * N + x * R + c), d[x]);
                                 at_wait_ld();
 #pragma unroll
                                 for (int r = 0; r < 8; ++r) {
-                                    float x[PL];
+                                    float x[G];
 #pragma unroll
-                                    for (int p = 0; p < PL; ++p) x[p] = d[p][r];
+                                    for (int y = 0; y < G; ++y) x[y] = d[y][r];
                                     acc[h][c + r] = fmaf(at_join<PL>(x), f[r], acc[h][c + r]);
                                 }
                             }
@@ -972,7 +1001,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&o_free[b]));
                     ++it;
-                    b ^= 1;
                 }
                 ok = ok && at_warp_wait(smem_addr(&ml_full[ub]), static_cast<uint32_t>((iu >> 1) & 1), &s_abort);
                 if (!ok) {
