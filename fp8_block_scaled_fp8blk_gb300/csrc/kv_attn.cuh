@@ -57,6 +57,7 @@ constexpr int kAtThreads = 640;
 constexpr int kAtOutWarp = 8, kAtQueryWarp = 12, kAtKWarp = 16, kAtMmaWarp = 17, kAtVWarp = 19;
 constexpr int kAtTile = 128;            // tokens per tile
 constexpr int kAtDeep = 4;              // tiles between the first product and the sums: scores, weights and products
+constexpr int kAtScaleDeep = 16;        // tiles whose scales are held: more than K's ring and the scores can be ahead of the softmax
 constexpr int kAtMaxGrid = 256;         // bound on CTAs: arrival counters and partial sums in the workspace
 constexpr size_t kAtHeaderBytes = kAtMaxGrid * sizeof(uint32_t);
 constexpr float kAtNoRef = -3.0e38f;    // maximum of a row that has seen nothing
@@ -88,15 +89,18 @@ struct AttnShape {
     static constexpr int kQBytes = ND * kSteps * kQStep;      // query planes of a unit
     static constexpr int kPStep = kAtTile * N;                // weight planes of one step
     static constexpr int kPBytes = kSteps * kPStep;           // weight planes of a tile
-    static constexpr int kFixed = 1024 + 2 * kQBytes + kAtDeep * kPBytes;
-    static constexpr int kRoom = 227 * 1024 - 12 * 1024;      // dynamic shared memory beside the static arrays
-    static constexpr int kStages0 = (kRoom - kFixed) / (2 * kTileBytes);
-    static constexpr int kStages = kStages0 > 6 ? 6 : kStages0;
-    static constexpr size_t kSmem = kFixed + static_cast<size_t>(kStages) * 2 * kTileBytes;
+    static constexpr int kPDeep = N == 64 || ND == 2 ? 2 : kAtDeep;  // tiles whose weights are held
+    static constexpr int kFixed = 1024 + 2 * kQBytes + kPDeep * kPBytes;
+    static constexpr int kRoom = (227 - 9) * 1024;            // dynamic shared memory beside the static arrays
+    static constexpr int kTiles = (kRoom - kFixed) / kTileBytes;
+    // V's tiles are held longer than K's (until the weights are there).
+    static constexpr int kStagesV = (kTiles + 1) / 2 > 6 ? 6 : (kTiles + 1) / 2;
+    static constexpr int kStagesK = kTiles / 2 > 6 ? 6 : kTiles / 2;
+    static constexpr size_t kSmem = kFixed + static_cast<size_t>(kStagesK + kStagesV) * kTileBytes;
     static constexpr int kTmemUsed = N * kAtDeep * (1 + ND);  // scores and products
     static constexpr int kTmem = kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
     static constexpr int kPartial = R * (ND * 128) + 2 * R;   // floats of one partial
-    static_assert(kStages >= 2 && kTmemUsed <= 512 && N % 16 == 0 && N <= 64, "shape");
+    static_assert(kStagesK >= 2 && kStagesK + kAtDeep < kAtScaleDeep && kTmemUsed <= 512 && N % 16 == 0 && N <= 64, "shape");
 };
 
 // Shared-memory descriptor of an operand tile whose rows are `row_bytes` (128,
@@ -434,12 +438,12 @@ template <typename T, int PL, int R, int ND>
 __global__ void __launch_bounds__(kAtThreads, 1)
     kv_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
     using Sh = AttnShape<PL, R, ND>;
-    constexpr int N = Sh::N, S = Sh::kStages, G = Sh::kGroups;
+    constexpr int N = Sh::N, SK = Sh::kStagesK, SV = Sh::kStagesV, PD = Sh::kPDeep, G = Sh::kGroups;
     extern __shared__ __align__(1024) uint8_t at_smem[];
-    __shared__ __align__(8) uint64_t k_full[S], v_full[S], v_free[S], sc_full[S];
+    __shared__ __align__(8) uint64_t k_full[SK], k_free[SK], v_full[SV], v_free[SV], sc_full[kAtScaleDeep];
     __shared__ __align__(8) uint64_t s_full[kAtDeep], s_free[kAtDeep], p_full[kAtDeep], o_full[kAtDeep], o_free[kAtDeep];
     __shared__ __align__(8) uint64_t q_full[2], ml_full[2], ml_free[2], mma_done[2];
-    __shared__ float sc[S][2][8];                       // k and v scales of a tile's blocks
+    __shared__ float sc[kAtScaleDeep][2][8];                       // k and v scales of a tile's blocks
     __shared__ __align__(16) float s_qs[2][R];          // per query row: 2^-e x scale x log2 e (NaN: the row is not finite)
     __shared__ __align__(16) int s_lim[2][R];           // last position each row sees
     __shared__ __align__(16) float s_wmax[2][4][R];     // per softmax group: its warps' maxima over the tile
@@ -456,16 +460,19 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t *sQ = at_smem + ((1024u - (smem_addr(at_smem) & 1023u)) & 1023u);
     uint8_t *sP = sQ + 2 * Sh::kQBytes;
-    uint8_t *sK = sP + kAtDeep * Sh::kPBytes;                 // S tiles of K, then S of V
-    uint8_t *sV = sK + static_cast<size_t>(S) * Sh::kTileBytes;
+    uint8_t *sK = sP + PD * Sh::kPBytes;                // K's ring, then V's
+    uint8_t *sV = sK + static_cast<size_t>(SK) * Sh::kTileBytes;
 
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) {
+        for (int i = 0; i < SK; ++i) {
             mbar_init(smem_addr(&k_full[i]), 1);
+            mbar_init(smem_addr(&k_free[i]), 1);
+        }
+        for (int i = 0; i < SV; ++i) {
             mbar_init(smem_addr(&v_full[i]), 1);
             mbar_init(smem_addr(&v_free[i]), 1);
-            mbar_init(smem_addr(&sc_full[i]), 64);
         }
+        for (int i = 0; i < kAtScaleDeep; ++i) mbar_init(smem_addr(&sc_full[i]), 32);
         for (int i = 0; i < kAtDeep; ++i) {
             mbar_init(smem_addr(&s_full[i]), 1);
             mbar_init(smem_addr(&s_free[i]), 4);
@@ -558,19 +565,36 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const AttnSplit split(total, grid);
         AttnWalk<R> w(a, s_seq, s_first, s_slot, s_end - s_begin);
         const bool built = !w.none();
-        if (built && warp < kAtKWarp) {
-            at_build_queries<T, PL, R, ND>(a, w, sQ, s_qs[0], s_lim[0], warp, kAtKWarp, lane);
-            asm volatile("bar.sync 4, %0;" ::"n"(kAtKWarp * 32) : "memory");
+        if (warp < kAtKWarp && (built || warp >= kAtQueryWarp)) {
+            // ---------------- query planes: all these warps build the first unit's; the last four go on with the others.
+            // (One loop: the code is long, and a second copy of it would cost the other roles instruction cache.)
+            AttnWalk<R> n(w);
+            int ub = 0, iu = 0;
+            bool all = built;
+            do {
+                if (n.none()) continue;
+                // The unit before last is written out: nothing reads this buffer, its scales or its limits any more.
+                if (iu >= 2 && !at_warp_wait(smem_addr(&ml_free[ub]), static_cast<uint32_t>((iu >> 1) - 1) & 1u, &s_abort)) break;
+                at_build_queries<T, PL, R, ND>(a, n, sQ + ub * Sh::kQBytes, s_qs[ub], s_lim[ub], all ? warp : warp - kAtQueryWarp,
+                                               all ? kAtKWarp : 4, lane);
+                if (all) asm volatile("bar.sync 4, %0;" ::"n"(kAtKWarp * 32) : "memory");
+                if (warp < kAtQueryWarp) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&q_full[ub]));
+                all = false;
+                ++iu;
+                ub ^= 1;
+            } while (n.next());
         }
         if (warp == kAtKWarp || warp == kAtVWarp) {
-            // ---------------- TMA producers: lane p copies the tile's p-th block of K (or V), with its scale
+            // ---------------- TMA producers: lane p copies the tile's p-th block of K (or V); K's brings both scales
             const bool is_v = warp == kAtVWarp;
             const int np = kAtTile >> a.block_log2, block = 1 << a.block_log2;
             const uint64_t pol = l2_policy_evict_first();
             const CUtensorMap *map = is_v ? &vmap : &kmap;
-            const float *scales = is_v ? a.v_scales : a.k_scales;
             const uint32_t ring = smem_addr(is_v ? sV : sK);
-            uint64_t *full = is_v ? v_full : k_full;
+            uint64_t *full = is_v ? v_full : k_full, *free = is_v ? v_free : k_free;
+            const int S = is_v ? SV : SK;
             int st = 0;
             uint32_t ph = 0;
             int64_t it = 0;
@@ -612,24 +636,30 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const bool mine = lane < pages, good = id >= 0 && id < a.n_blocks;
                     if (mine && !good) atomicOr(a.status, 4u);
                     const int64_t bh = static_cast<int64_t>(good ? id : 0) * a.kv_heads + head;
-                    // V's slot is the last of the stage's to be read.
-                    if (it >= S && !at_warp_wait(smem_addr(&v_free[st]), ph ^ 1u, &s_abort)) {
+                    if (it >= S && !at_warp_wait(smem_addr(&free[st]), ph ^ 1u, &s_abort)) {
                         ok = false;
                         break;
                     }
                     const uint32_t bar = smem_addr(&full[st]);
                     if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(pages) * block * 128 * ND);
                     __syncwarp();
+                    const int slot = static_cast<int>(it & (kAtScaleDeep - 1));
                     if (mine) {
                         const uint32_t at = ring + static_cast<uint32_t>(st) * Sh::kTileBytes + lane * block * 128;
 #pragma unroll
                         for (int h = 0; h < ND; ++h)
                             t8_tma_2d(at + h * kAtTile * 128, map, h * 128, static_cast<int>(bh << a.block_log2), bar, pol);
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[st][is_v][lane])),
-                                     "l"(good ? scales + bh : &g_attn_nan)
-                                     : "memory");
+                        if (!is_v) {
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[slot][0][lane])),
+                                         "l"(good ? a.k_scales + bh : &g_attn_nan)
+                                         : "memory");
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(&sc[slot][1][lane])),
+                                         "l"(good ? a.v_scales + bh : &g_attn_nan)
+                                         : "memory");
+                        }
                     }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sc_full[st])) : "memory");
+                    if (!is_v)
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sc_full[slot])) : "memory");
                     ++it;
                     if (++st == S) {
                         st = 0;
@@ -650,7 +680,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 const uint64_t k_desc = at_desc<128>(smem_addr(sK)), q_desc = at_desc<128>(smem_addr(sQ));
                 const uint64_t v_desc = at_desc<128>(smem_addr(sV)), p_desc = at_desc<N>(smem_addr(sP));
                 int qt = g, pt = g;         // next tile of each product
-                int q_st = g % S, p_st = g % S;
+                int q_st = g, p_st = g;     // ... and its slot in K's, V's ring
                 uint32_t q_ph = 0, p_ph = 0;
                 int iu = -1, unit_end = 0;  // the first product's unit, and the tile after its last
                 bool more = true;           // false: unit_end is the end of the range
@@ -665,7 +695,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                             (pt < kAtDeep || mbar_test_wait(smem_addr(&o_free[b]), bp ^ 1u))) {
                             t8_fence_after();
                             const uint64_t va = v_desc + static_cast<uint32_t>(p_st) * (Sh::kTileBytes / 16);
-                            const uint64_t pa = p_desc + static_cast<uint32_t>(b) * (Sh::kPBytes / 16);
+                            const uint64_t pa = p_desc + static_cast<uint32_t>(b & (PD - 1)) * (Sh::kPBytes / 16);
                             const uint32_t d = tmem + static_cast<uint32_t>((kAtDeep + b * ND) * N);
 #pragma unroll
                             for (int h = 0; h < ND; ++h)
@@ -679,8 +709,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                             t8_commit(smem_addr(&v_free[p_st]));
                             pt += 2;
                             p_st += 2;
-                            if (p_st >= S) {
-                                p_st -= S;
+                            if (p_st >= SV) {
+                                p_st -= SV;
                                 p_ph ^= 1u;
                             }
                             went = true;
@@ -713,10 +743,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                                             t8_mma(d, ka + (h * kAtTile * 128 + c * 32) / 16,
                                                    qa + ((h * Sh::kSteps + x) * Sh::kQStep + c * 32) / 16, qk_idesc, h + x + c > 0);
                             t8_commit(smem_addr(&s_full[b]));
+                            t8_commit(smem_addr(&k_free[q_st]));
                             qt += 2;
                             q_st += 2;
-                            if (q_st >= S) {
-                                q_st -= S;
+                            if (q_st >= SK) {
+                                q_st -= SK;
                                 q_ph ^= 1u;
                             }
                             went = true;
@@ -737,21 +768,6 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 t8_commit(smem_addr(&mma_done[g]));
                 (void)mbar_wait_bounded(smem_addr(&mma_done[g]), 0u);
             }
-        } else if (warp >= kAtQueryWarp) {
-            // ---------------- query planes of the units after the first
-            int ub = 0;
-            int64_t iu = 0;
-            do {
-                if (w.none()) continue;
-                // The unit before last is written out: nothing reads this buffer, its scales or its limits any more.
-                if (iu >= 2 && !at_warp_wait(smem_addr(&ml_free[ub]), static_cast<uint32_t>(((iu >> 1) - 1) & 1), &s_abort)) break;
-                if (iu > 0 || !built)
-                    at_build_queries<T, PL, R, ND>(a, w, sQ + ub * Sh::kQBytes, s_qs[ub], s_lim[ub], warp - kAtQueryWarp, 4, lane);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&q_full[ub]));
-                ++iu;
-                ub ^= 1;
-            } while (w.next());
         } else if (warp < kAtOutWarp) {
             // ---------------- softmax: group g takes the tiles g, g + 2, ...; thread = token of the tile
             const int g = warp >> 2, wg = warp & 3, tg = tid & 127, bar = 1 + g;
@@ -776,16 +792,17 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 const int seen_by_all = w.q.len - w.q.rows;  // positions up to here are seen by every row
                 const int rows = w.rows();                   // columns past the unit's rows hold what they may
                 for (int j = w.j0; j < w.j1; ++j, ++it) {
-                    const int cs = st;
-                    const uint32_t cph = ph;
-                    if (++st == S) {
+                    const int vs_st = st;  // V's slot
+                    const uint32_t v_ph = ph;
+                    if (++st == SV) {
                         st = 0;
                         ph ^= 1u;
                     }
                     if ((it & 1) != g) continue;
                     const uint32_t bp = static_cast<uint32_t>(it / kAtDeep) & 1u;
                     const int b = static_cast<int>(it & (kAtDeep - 1));
-                    ok = ok && at_warp_wait(smem_addr(&sc_full[cs]), cph, &s_abort) &&
+                    const int cs = static_cast<int>(it & (kAtScaleDeep - 1));  // the scales' slot
+                    ok = ok && at_warp_wait(smem_addr(&sc_full[cs]), static_cast<uint32_t>(it / kAtScaleDeep) & 1u, &s_abort) &&
                          at_warp_wait(smem_addr(&s_full[b]), bp, &s_abort);
                     const int pos = j * kAtTile + tg;
                     const bool edge = (j + 1) * kAtTile - 1 > seen_by_all;  // some row does not see the whole tile
@@ -842,12 +859,14 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         ref = now;
                         // The output sums have read what the tile kAtDeep ago left here, and the second MMA its weights.
                         if (it >= kAtDeep) ok = at_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort) && ok;
+                        if (PD < kAtDeep && it >= PD)
+                            ok = at_wait(smem_addr(&o_full[(it - PD) & (kAtDeep - 1)]), static_cast<uint32_t>((it - PD) / kAtDeep) & 1u, &s_abort) && ok;
                         s_tref[b][tg] = tref;
                         if (tg == 0) s_vf[b] = __int_as_float((ve - kAtPeakLog2) << 23);
                     }
                     at_bar(bar);
                     ok = __all_sync(0xFFFFFFFFu, ok);
-                    uint8_t *pb = sP + b * Sh::kPBytes;
+                    uint8_t *pb = sP + (b & (PD - 1)) * Sh::kPBytes;
 #pragma unroll 1
                     for (int c = 0; c < rows; c += 8) {
                         if constexpr (R > 8) scores(c, s);
@@ -873,11 +892,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     if (edge) {
                         // This token's row of V: zeros where the request ends (what is there is no token's), and NaN
                         // codes that only later rows see leave the tile and mark the element for those rows.
-                        ok = ok && at_warp_wait(smem_addr(&v_full[cs]), cph, &s_abort);
+                        ok = ok && at_warp_wait(smem_addr(&v_full[vs_st]), v_ph, &s_abort);
                         if (ok && pos > seen_by_all) {
 #pragma unroll
                             for (int h = 0; h < ND; ++h) {
-                                uint8_t *row = sV + static_cast<size_t>(cs) * Sh::kTileBytes + h * kAtTile * 128;
+                                uint8_t *row = sV + static_cast<size_t>(vs_st) * Sh::kTileBytes + h * kAtTile * 128;
                                 if (pos >= w.q.len) {
 #pragma unroll
                                     for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(row + tg * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -911,7 +930,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 ++iu;
                 ub ^= 1;
             } while (w.next());
-        } else {
+        } else if (warp < kAtQueryWarp) {
             // ---------------- output sums: thread = element d (and d + 128) of head_dim
             const int dt = tid - kAtOutWarp * 32, ow = warp - kAtOutWarp;
             const uint32_t lanes = static_cast<uint32_t>(ow * 32) << 16;
