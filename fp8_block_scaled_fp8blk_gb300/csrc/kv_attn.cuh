@@ -496,18 +496,26 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    t8_fence_before();
+    __syncthreads();
+    t8_fence_after();
+    const uint32_t tmem = tmem_slot;
     grid_dependency_wait();
     grid_launch_dependents();
 
-    // ---- the list: tiles of every request, scanned by every CTA (thread i sums
-    // requests [i per, (i + 1) per)).  The host keeps the total below 2^31.
-    int total = 0, grid = 0;
+    // ---- the list: tiles of every request, scanned by every CTA -- by every warp for itself (lane = request) up to 32
+    // requests, else by all threads together (thread i sums requests [i per, (i + 1) per)).  The host keeps the total
+    // below 2^31.
+    int total, grid, begin = 0, end = 0, first = 0, slot = 0;  // this CTA's range, its first request and slot
+    AttnSeq seq = {};
     {
-        const int per = (a.n_seqs + kAtThreads - 1) / kAtThreads;
-        const int r0 = min(tid * per, a.n_seqs), r1 = min(r0 + per, a.n_seqs);
+        const bool alone = a.n_seqs <= 32;
+        const int per = alone ? 1 : (a.n_seqs + kAtThreads - 1) / kAtThreads;
+        const int r0 = min((alone ? lane : tid) * per, a.n_seqs), r1 = min(r0 + per, a.n_seqs);
         int mine = 0;
         bool bad = false;
         AttnSeq q = {};
+        q.weight = 1;
         for (int s = r0; s < r1; ++s) {
             q = at_seq<R>(a, s);
             mine += q.entries(a.kv_heads);
@@ -520,13 +528,15 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const int u = __shfl_up_sync(0xFFFFFFFFu, pre, d);
             if (lane >= d) pre += u;
         }
-        if (lane == 31) s_scan[warp] = pre;
-        t8_fence_before();
-        __syncthreads();
-        t8_fence_after();
-        const int sum = s_scan[min(lane, kAtThreads / 32 - 1)];  // each warp's sum, in the lanes of its number
-        total = __reduce_add_sync(0xFFFFFFFFu, lane < kAtThreads / 32 ? sum : 0);
-        const int base = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sum : 0);
+        int base = 0;
+        total = __shfl_sync(0xFFFFFFFFu, pre, 31);
+        if (!alone) {
+            if (lane == 31) s_scan[warp] = pre;
+            __syncthreads();
+            const int sum = s_scan[min(lane, kAtThreads / 32 - 1)];  // each warp's sum, in the lanes of its number
+            total = __reduce_add_sync(0xFFFFFFFFu, lane < kAtThreads / 32 ? sum : 0);
+            base = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sum : 0);
+        }
         // Every CTA's share is at least a tile, so no two cuts move to the same place inside a unit.
         grid = min(static_cast<int>(gridDim.x), max(total / at_max_weight(R), min(total, 1)));
         const int at = base + pre - mine;  // this thread's first entry
@@ -534,7 +544,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const AttnSplit split(total, grid);
             // Entry x, which lies in one of this thread's requests: the request, the slot within it, and its list
             // position, moved to the slot's start, or to the unit's where the unit is small.
-            auto locate = [&](int x, int &r, int &slot) {
+            auto locate = [&](int x, int &r, int &sl) {
                 int here = at;
                 r = r0;
                 if (per > 1) q = at_seq<R>(a, r);
@@ -542,28 +552,48 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     here += q.entries(a.kv_heads);
                     q = at_seq<R>(a, ++r);
                 }
-                slot = (x - here) / q.weight;
-                if (q.tiles <= kAtSmall) slot -= slot % (q.tiles + 1);
-                return here + slot * q.weight;
+                sl = (x - here) / q.weight;
+                if (q.tiles <= kAtSmall) sl -= sl % (q.tiles + 1);
+                return here + sl * q.weight;
             };
             const int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
-            int r, slot;
-            if (at <= x1 && x1 < at + mine) s_end = locate(x1, r, slot);
-            else if (tid == 0 && x1 == total) s_end = total;
-            if (at <= x0 && x0 < at + mine) {
-                s_begin = locate(x0, r, slot);
-                s_seq = q;
-                s_first = r;
-                s_slot = slot;
+            const bool has0 = at <= x0 && x0 < at + mine, has1 = at <= x1 && x1 < at + mine;
+            int r = 0, sl = 0, p0 = 0, p1 = total;
+            if (has1) p1 = locate(x1, r, sl);
+            if (has0) p0 = locate(x0, r, sl);
+            if (alone) {
+                const int from0 = __ffs(__ballot_sync(0xFFFFFFFFu, has0)) - 1, from1 = __ffs(__ballot_sync(0xFFFFFFFFu, has1)) - 1;
+                begin = __shfl_sync(0xFFFFFFFFu, p0, from0);
+                end = __shfl_sync(0xFFFFFFFFu, p1, max(from1, 0));
+                if (from1 < 0) end = total;
+                first = from0;
+                slot = __shfl_sync(0xFFFFFFFFu, sl, from0);
+                seq = at_seq<R>(a, first);
+            } else {
+                if (has1 || (tid == 0 && x1 == total)) s_end = p1;
+                if (has0) {
+                    s_begin = p0;
+                    s_seq = q;
+                    s_first = r;
+                    s_slot = sl;
+                }
             }
         }
-        __syncthreads();
+        if (!alone) {
+            __syncthreads();
+            if (static_cast<int>(blockIdx.x) < grid) {
+                begin = s_begin;
+                end = s_end;
+                first = s_first;
+                slot = s_slot;
+                seq = s_seq;
+            }
+        }
     }
-    const uint32_t tmem = tmem_slot;
 
-    if (static_cast<int>(blockIdx.x) < grid && s_begin < s_end) {
+    if (begin < end) {
         const AttnSplit split(total, grid);
-        AttnWalk<R> w(a, s_seq, s_first, s_slot, s_end - s_begin);
+        AttnWalk<R> w(a, seq, first, slot, end - begin);
         const bool built = !w.none();
         if (warp < kAtKWarp && (built || warp >= kAtQueryWarp)) {
             // ---------------- query planes: all these warps build the first unit's; the last four go on with the others.
@@ -943,7 +973,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             const uint32_t lanes = static_cast<uint32_t>(ow * 32) << 16;
             int ub = 0;
             int64_t it = 0, iu = 0;
-            int done = s_begin;
+            int done = begin;
             bool ok = true;
             const float nanf = __int_as_float(0x7FC00000);
             T *out = static_cast<T *>(a.out);
@@ -1139,7 +1169,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                                 for (int h = 0; h < ND; ++h)
                                     o[k][h] = make_float4(o[k][h].x * keep, o[k][h].y * keep, o[k][h].z * keep, o[k][h].w * keep);
                             }
-#pragma unroll 4
+#pragma unroll(16 / RW)
                             for (int p = 0; p < cn; ++p) {
                                 const float4 *src = reinterpret_cast<const float4 *>(part(c0 + p) + ow * (ND * 128)) + lane;
 #pragma unroll
