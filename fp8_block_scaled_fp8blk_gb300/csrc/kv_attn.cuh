@@ -463,31 +463,28 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     uint8_t *sK = sP + PD * Sh::kPBytes;                // K's ring, then V's
     uint8_t *sV = sK + static_cast<size_t>(SK) * Sh::kTileBytes;
 
-    if (tid == 0) {
-        for (int i = 0; i < SK; ++i) {
-            mbar_init(smem_addr(&k_full[i]), 1);
-            mbar_init(smem_addr(&k_free[i]), 1);
-        }
-        for (int i = 0; i < SV; ++i) {
-            mbar_init(smem_addr(&v_full[i]), 1);
-            mbar_init(smem_addr(&v_free[i]), 1);
-        }
-        for (int i = 0; i < kAtScaleDeep; ++i) mbar_init(smem_addr(&sc_full[i]), 32);
-        for (int i = 0; i < kAtDeep; ++i) {
-            mbar_init(smem_addr(&s_full[i]), 1);
-            mbar_init(smem_addr(&s_free[i]), 4);
-            mbar_init(smem_addr(&p_full[i]), 4);
-            mbar_init(smem_addr(&o_full[i]), 1);
-            mbar_init(smem_addr(&o_free[i]), 4);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&q_full[i]), 4);
-            mbar_init(smem_addr(&ml_full[i]), 8);
-            mbar_init(smem_addr(&ml_free[i]), 4);
-            mbar_init(smem_addr(&mma_done[i]), 1);
-        }
-        mbar_init_fence();
-        s_abort = 0;
+    // A thread per barrier.
+    {
+        auto init = [&](uint64_t *bars, int n, int first, int count) {
+            if (tid >= first && tid < first + n) mbar_init(smem_addr(bars + tid - first), static_cast<uint32_t>(count));
+            return first + n;
+        };
+        int at = init(sc_full, kAtScaleDeep, 0, 32);
+        at = init(k_full, SK, at, 1);
+        at = init(k_free, SK, at, 1);
+        at = init(v_full, SV, at, 1);
+        at = init(v_free, SV, at, 1);
+        at = init(s_full, kAtDeep, at, 1);
+        at = init(s_free, kAtDeep, at, 4);
+        at = init(p_full, kAtDeep, at, 4);
+        at = init(o_full, kAtDeep, at, 1);
+        at = init(o_free, kAtDeep, at, 4);
+        at = init(q_full, 2, at, 4);
+        at = init(ml_full, 2, at, 8);
+        at = init(ml_free, 2, at, 4);
+        at = init(mma_done, 2, at, 1);
+        if (tid < at) mbar_init_fence();
+        if (tid == 0) s_abort = 0;
     }
     for (int i = tid; i < 2 * ND * 128; i += kAtThreads) (&s_vnan[0][0])[i] = 0x7FFFFFFF;
     if (warp == 0) {
@@ -540,39 +537,50 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         // Every CTA's share is at least a tile, so no two cuts move to the same place inside a unit.
         grid = min(static_cast<int>(gridDim.x), max(total / at_max_weight(R), min(total, 1)));
         const int at = base + pre - mine;  // this thread's first entry
+        // A cut at entry x of a request that begins at `at`: its slot, and its list position once moved to the slot's
+        // start, or to the unit's where the unit is small.
+        auto cut = [](int x, int at, int tiles, int weight, int &sl) {
+            sl = R == 8 ? x - at : (x - at) / weight;
+            if (tiles <= kAtSmall) sl -= sl % (tiles + 1);
+            return at + sl * weight;
+        };
         if (static_cast<int>(blockIdx.x) < grid) {
             const AttnSplit split(total, grid);
-            // Entry x, which lies in one of this thread's requests: the request, the slot within it, and its list
-            // position, moved to the slot's start, or to the unit's where the unit is small.
-            auto locate = [&](int x, int &r, int &sl) {
-                int here = at;
-                r = r0;
-                if (per > 1) q = at_seq<R>(a, r);
-                while (x >= here + q.entries(a.kv_heads)) {
-                    here += q.entries(a.kv_heads);
-                    q = at_seq<R>(a, ++r);
-                }
-                sl = (x - here) / q.weight;
-                if (q.tiles <= kAtSmall) sl -= sl % (q.tiles + 1);
-                return here + sl * q.weight;
-            };
             const int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
-            const bool has0 = at <= x0 && x0 < at + mine, has1 = at <= x1 && x1 < at + mine;
-            int r = 0, sl = 0, p0 = 0, p1 = total;
-            if (has1) p1 = locate(x1, r, sl);
-            if (has0) p0 = locate(x0, r, sl);
             if (alone) {
-                const int from0 = __ffs(__ballot_sync(0xFFFFFFFFu, has0)) - 1, from1 = __ffs(__ballot_sync(0xFFFFFFFFu, has1)) - 1;
-                begin = __shfl_sync(0xFFFFFFFFu, p0, from0);
-                end = __shfl_sync(0xFFFFFFFFu, p1, max(from1, 0));
-                if (from1 < 0) end = total;
-                first = from0;
-                slot = __shfl_sync(0xFFFFFFFFu, sl, from0);
-                seq = at_seq<R>(a, first);
+                int sl;
+                const unsigned has1 = __ballot_sync(0xFFFFFFFFu, at <= x1 && x1 < at + mine);
+                if (has1 == 0) {
+                    end = total;
+                } else {
+                    const int from = __ffs(has1) - 1;
+                    end = cut(x1, __shfl_sync(0xFFFFFFFFu, at, from), __shfl_sync(0xFFFFFFFFu, q.tiles, from),
+                              __shfl_sync(0xFFFFFFFFu, q.weight, from), sl);
+                }
+                first = __ffs(__ballot_sync(0xFFFFFFFFu, at <= x0 && x0 < at + mine)) - 1;
+                seq.first = __shfl_sync(0xFFFFFFFFu, q.first, first);
+                seq.rows = __shfl_sync(0xFFFFFFFFu, q.rows, first);
+                seq.len = __shfl_sync(0xFFFFFFFFu, q.len, first);
+                seq.tiles = __shfl_sync(0xFFFFFFFFu, q.tiles, first);
+                seq.groups = __shfl_sync(0xFFFFFFFFu, q.groups, first);
+                seq.weight = __shfl_sync(0xFFFFFFFFu, q.weight, first);
+                begin = cut(x0, __shfl_sync(0xFFFFFFFFu, at, first), seq.tiles, seq.weight, slot);
             } else {
-                if (has1 || (tid == 0 && x1 == total)) s_end = p1;
-                if (has0) {
-                    s_begin = p0;
+                auto locate = [&](int x, int &r, int &sl) {  // among this thread's requests
+                    int here = at;
+                    r = r0;
+                    if (per > 1) q = at_seq<R>(a, r);
+                    while (x >= here + q.entries(a.kv_heads)) {
+                        here += q.entries(a.kv_heads);
+                        q = at_seq<R>(a, ++r);
+                    }
+                    return cut(x, here, q.tiles, q.weight, sl);
+                };
+                int r, sl;
+                if (at <= x1 && x1 < at + mine) s_end = locate(x1, r, sl);
+                else if (tid == 0 && x1 == total) s_end = total;
+                if (at <= x0 && x0 < at + mine) {
+                    s_begin = locate(x0, r, sl);
                     s_seq = q;
                     s_first = r;
                     s_slot = sl;
@@ -1130,74 +1138,65 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     }
                     at_bar(3);
                     if (s_last) {
-                        // Warp ow joins the rows ow, ow + 4, ...: lane = part for the weights, four elements for the sums.
-                        constexpr int RW = R / 4;
                         auto part = [&](int p) {  // part p lies in CTA b0 + p, which holds one that begins a unit and one that does not
                             return a.partials + (static_cast<int64_t>(b0 + p) * 2 + (p == 0)) * Sh::kPartial;
                         };
-                        float m[RW], den[RW];
-                        float4 o[RW][ND];
+                        // Maxima and denominators: 128 / R threads a row.  (Loops, not unrolled code: this runs once or
+                        // twice a launch, and fetching its instructions would take longer than the loads.)
+                        constexpr int L = 128 / R;
+                        {
+                            const int r = dt / L;
+                            float m = kAtNoRef, d = 0.f;
+#pragma unroll 4
+                            for (int p = dt % L; p < parts; p += L) {
+                                const float *src = part(p) + R * ND * 128 + r;
+                                const float pm = __ldcg(src), pl = __ldcg(src + R), top = fmaxf(m, pm);
+                                d = d * at_exp2(m - top) + pl * at_exp2(pm - top);
+                                m = top;
+                            }
 #pragma unroll
-                        for (int k = 0; k < RW; ++k) {
-                            m[k] = kAtNoRef;
-                            den[k] = 0.f;
-#pragma unroll
-                            for (int h = 0; h < ND; ++h) o[k][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            for (int x = L / 2; x; x >>= 1) {
+                                const float om = __shfl_xor_sync(0xFFFFFFFFu, m, x), od = __shfl_xor_sync(0xFFFFFFFFu, d, x), top = fmaxf(m, om);
+                                // The lower lane's share first on both sides: one order, one result.
+                                const float mine = d * at_exp2(m - top), other = od * at_exp2(om - top);
+                                d = dt & x ? other + mine : mine + other;
+                                m = top;
+                            }
+                            if (dt % L == 0) {
+                                s_corr[r] = m;
+                                s_inv[r] = d == 0.f ? 0.f : 1.f / d;
+                                if (a.lse && r < valid) a.lse[lse_at(r)] = d == 0.f ? -INFINITY : (m + log2f(d)) * 0.6931471805599453f;
+                            }
                         }
-                        for (int c0 = 0; c0 < parts; c0 += 32) {
-                            const int cn = min(32, parts - c0);
-                            float pm[RW], pl[RW], wgt[RW];
+                        at_bar(3);
+                        // Sums: a thread takes four elements of every 128th quadruple, kItems at a time over all parts.
+                        constexpr int kAll = R * ND / 4, kItems = kAll < 4 ? kAll : 4, kAhead = 16 / kItems;
+#pragma unroll 1
+                        for (int k0 = 0; k0 < kAll; k0 += kItems) {
+                            float4 o[kItems];
 #pragma unroll
-                            for (int k = 0; k < RW; ++k) {
-                                const float *src = part(c0 + min(lane, cn - 1)) + R * ND * 128 + ow + 4 * k;
-                                pm[k] = __ldcg(src);
-                                pl[k] = __ldcg(src + R);
-                            }
+                            for (int k = 0; k < kItems; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll kAhead
+                            for (int p = 0; p < parts; ++p) {
+                                const float *src = part(p);
 #pragma unroll
-                            for (int k = 0; k < RW; ++k) {
-                                float top = fmaxf(m[k], pm[k]);
-#pragma unroll
-                                for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                                const float keep = at_exp2(m[k] - top);
-                                wgt[k] = lane < cn ? at_exp2(pm[k] - top) : 0.f;
-                                float x = lane < cn ? pl[k] * wgt[k] : 0.f;
-#pragma unroll
-                                for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
-                                den[k] = den[k] * keep + x;
-                                m[k] = top;
-#pragma unroll
-                                for (int h = 0; h < ND; ++h)
-                                    o[k][h] = make_float4(o[k][h].x * keep, o[k][h].y * keep, o[k][h].z * keep, o[k][h].w * keep);
-                            }
-#pragma unroll(16 / RW)
-                            for (int p = 0; p < cn; ++p) {
-                                const float4 *src = reinterpret_cast<const float4 *>(part(c0 + p) + ow * (ND * 128)) + lane;
-#pragma unroll
-                                for (int k = 0; k < RW; ++k) {
-                                    const float f = __shfl_sync(0xFFFFFFFFu, wgt[k], p);
-#pragma unroll
-                                    for (int h = 0; h < ND; ++h) {
-                                        const float4 x = __ldcg(src + k * (4 * ND * 32) + h * 32);
-                                        o[k][h].x = fmaf(x.x, f, o[k][h].x);
-                                        o[k][h].y = fmaf(x.y, f, o[k][h].y);
-                                        o[k][h].z = fmaf(x.z, f, o[k][h].z);
-                                        o[k][h].w = fmaf(x.w, f, o[k][h].w);
-                                    }
+                                for (int k = 0; k < kItems; ++k) {
+                                    const int i = (k0 + k) * 128 + dt, r = i / (ND * 32);
+                                    const float f = at_exp2(__ldcg(src + R * ND * 128 + r) - s_corr[r]);
+                                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(src) + i);
+                                    o[k].x = fmaf(x.x, f, o[k].x);
+                                    o[k].y = fmaf(x.y, f, o[k].y);
+                                    o[k].z = fmaf(x.z, f, o[k].z);
+                                    o[k].w = fmaf(x.w, f, o[k].w);
                                 }
                             }
-                        }
 #pragma unroll
-                        for (int k = 0; k < RW; ++k) {
-                            const int r = ow + 4 * k;
-                            if (r >= valid) continue;
-                            const float inv = den[k] == 0.f ? 0.f : 1.f / den[k];
-                            const int64_t at = out_row(r) + 4 * lane;
-#pragma unroll
-                            for (int h = 0; h < ND; ++h)
-                                if (4 * lane + h * 128 < a.head_dim)
-                                    at_store4(out + at + h * 128,
-                                              make_float4(o[k][h].x * inv, o[k][h].y * inv, o[k][h].z * inv, o[k][h].w * inv));
-                            if (a.lse && lane == 0) a.lse[lse_at(r)] = den[k] == 0.f ? -INFINITY : (m[k] + log2f(den[k])) * 0.6931471805599453f;
+                            for (int k = 0; k < kItems; ++k) {
+                                const int i = (k0 + k) * 128 + dt, r = i / (ND * 32), d = (i & (ND * 32 - 1)) * 4;
+                                const float f = s_inv[r];
+                                if (r < valid && d < a.head_dim)
+                                    at_store4(out + out_row(r) + d, make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f));
+                            }
                         }
                     }
                 }
