@@ -2,6 +2,8 @@
 // the top alternatives, from rows of logits (fp8blk_token_logprobs).
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "step.h"
 
 namespace cg = cooperative_groups;
@@ -73,6 +75,12 @@ struct LpVec<__nv_bfloat16> {
     }
 };
 
+// A full key's value: -0 comes back as +0, and 0 for NaN as NaN.
+__device__ __forceinline__ float key_value(uint64_t key) {
+    const uint32_t k = static_cast<uint32_t>(key >> 32);
+    return k == 0 ? __int_as_float(0x7FC00000) : __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
 // What a CTA of the cluster tells the first.
 struct LpShare {
     float max;            // largest value, NaN left out
@@ -94,16 +102,43 @@ __device__ __forceinline__ float lp_exp2(float x) {
     return y;
 }
 
+// A CTA's slice of one row, as 16-byte words: word w holds the elements
+// [w V - off, w V - off + V) of the row, of which the row's first and last word
+// may hold fewer.  Words [w0, w1) are the slice's, [g0, g1) the whole ones.
+template <typename T>
+struct LpSlice {
+    static constexpr int V = LpVec<T>::kN;
+    const T *x;
+    const uint4 *words;
+    int off, w0, w1, g0, g1;
+    __device__ __forceinline__ LpSlice(const LogprobArgs &a, int64_t row, int c) {
+        x = static_cast<const T *>(a.logits) + row * a.stride;
+        off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+        words = reinterpret_cast<const uint4 *>(x - off);
+        w0 = c * a.words;
+        w1 = min(w0 + a.words, (a.vocab + off + V - 1) / V);
+        g0 = off == 0 ? w0 : max(w0, 1);
+        g1 = min(w1, (a.vocab + off) / V);
+    }
+    // Elements of word w: [first, last).
+    __device__ __forceinline__ int first(int w) const { return max(0, w * V - off); }
+    __device__ __forceinline__ int last(int w, int vocab) const { return min(vocab, w * V - off + V); }
+    // A thread's first whole word; the row's first word, if partial, is thread 0's before that.
+    __device__ __forceinline__ int start(int tid) const { return w0 + tid + (w0 + tid < g0 ? kLpThreads : 0); }
+};
+
 // One cluster per row, one slice of the row per CTA, one pass over memory:
 // thread t takes the slice's 16-byte words t, t + 512, ... and keeps its own
 // reference, sum, weighted sum, maximum and rank count; what is joined, is
 // joined at the end.  The reference moves only when a value passes it by more
-// than 20, so the pass has no serial rescaling.
+// than 20, so the pass has no serial rescaling.  (A resident grid that asks for
+// the next row's words before it joins a row measured 4% slower than a CTA per
+// row and its scheduling by the hardware; clusters of 16, 40% slower than of 8.)
 //   The top: the k-th largest of 128 group maxima bounds the k-th largest of the
 // slice from below, so only threads whose own maximum reaches it hold
-// candidates; a warp each reads those threads' words again (out of L2: some 20
-// threads' worth), and the few candidates are ranked by counting.  Rows where too
-// many values tie with the bound are selected one by one.
+// candidates; their words are read again (out of L2: some 20 threads' worth), and
+// the few candidates are ranked by counting.  Rows where too many values tie with the bound are
+// selected one by one.
 //   Bound: HBM (4 or 2 bytes a logit).  Per f32 logit about 9 instructions, a
 // third of the issue rate at full bandwidth.
 template <typename T>
@@ -122,30 +157,20 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
     // The first CTA's shared memory is written to below: it has to have started.
     if (nc > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / nc;
     grid_dependency_wait();
     grid_launch_dependents();
-    const T *x = static_cast<const T *>(a.logits) + row * a.stride;
-    // The row as 16-byte words: word w holds elements [w V - off, w V - off + V); the first and last may be partial.
-    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-    const uint4 *words = reinterpret_cast<const uint4 *>(x - off);
-    const int n_words = (a.vocab + off + V - 1) / V;
-    const int w0 = c * a.words, w1 = min(w0 + a.words, n_words);
-
-    const int g0 = off == 0 ? w0 : max(w0, 1), g1 = min(w1, (a.vocab + off) / V);  // whole words of the slice
-
+    const int64_t row = blockIdx.x / nc;
+    const LpSlice<T> r(a, row, c);
+    const int w0 = r.w0, w1 = r.w1, g0 = r.g0, g1 = r.g1, off = r.off;
+    const T *x = r.x;
     // The first words are on their way before the target's logit is asked for.
-    int w = w0 + tid;
-    const bool leads = w < g0 && w < w1;  // the row's first word, partial
-    if (leads) w += kLpThreads;
-    const int w_first = w;
     uint4 next[UN];
     auto fetch = [&](int at) {
 #pragma unroll
         for (int u = 0; u < UN; ++u)
-            if (at + u * kLpThreads < g1) next[u] = lp_load(words + at + u * kLpThreads);
+            if (at + u * kLpThreads < g1) next[u] = lp_load(r.words + at + u * kLpThreads);
     };
-    fetch(w);
+    fetch(r.start(tid));
     const int target = a.targets[row];
     const bool has_target = target >= 0 && target < a.vocab;
     const float t = has_target ? static_cast<float>(x[target]) : __int_as_float(0x7FC00000);
@@ -191,10 +216,13 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
         rank += v > t || (v == t && i < target);
     };
     auto partial = [&](int w) {
-        for (int i = max(0, w * V - off); i < min(a.vocab, w * V - off + V); ++i) element(i, static_cast<float>(x[i]));
+        for (int i = r.first(w); i < r.last(w, a.vocab); ++i) element(i, static_cast<float>(x[i]));
     };
-    if (leads) partial(w_first - kLpThreads);
-    while (w < g1) {
+    const int w_first = r.start(tid);
+    const bool leads = w0 + tid < g0 && w0 + tid < w1;                         // thread 0's: the row's first word, partial
+    const bool trails = g1 < w1 && g1 >= g0 && (g1 - w0) % kLpThreads == tid;  // the row's last word, partial
+    if (leads) partial(w0 + tid);
+    for (int w = w_first; w < g1; w += UN * kLpThreads) {
         uint4 bits[UN];
 #pragma unroll
         for (int u = 0; u < UN; ++u) bits[u] = next[u];
@@ -202,13 +230,12 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
 #pragma unroll
         for (int u = 0; u < UN; ++u)
             if (w + u * kLpThreads < g1) word(w + u * kLpThreads, bits[u]);
-        w += UN * kLpThreads;
     }
-    if (g1 < w1 && g1 >= g0 && (g1 - w0) % kLpThreads == tid) partial(g1);  // the row's last word, partial
+    if (trails) partial(g1);
     if (has_target && t != t) {  // a NaN target: every number comes before it, and the NaNs of lower index
         rank = 0;
         for (int w = w0 + tid; w < w1; w += kLpThreads)
-            for (int i = max(0, w * V - off); i < min(a.vocab, w * V - off + V); ++i) {
+            for (int i = r.first(w); i < r.last(w, a.vocab); ++i) {
                 const float v = static_cast<float>(x[i]);
                 rank += v == v || i < target;
             }
@@ -282,26 +309,30 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
     const int want = min(a.top, elements);
     if (want > 0) {
         const float bound = s_bound;
-        if (w0 + tid < w1 && !(top < bound)) s_hot[atomicAdd(&s_hots, 1)] = tid;
-        __syncthreads();
-        const int hots = s_hots;
-        for (int h = warp; h < hots; h += kLpWarps)
-            for (int w = w0 + s_hot[h] + lane * kLpThreads; w < w1; w += 32 * kLpThreads) {
+        auto consider = [&](float v, int i) {
+            if (v < bound || (v != v && bound != -INFINITY)) return;
+            const int at = atomicAdd(&s_count, 1);
+            if (at < kLpCandidates) s_cand[at] = full_key(v, i);
+        };
+        auto consider_word = [&](int w) {
+            if (w >= g0 && w < g1) {
                 float v[V];
-                const int e0 = w * V - off;
-                const bool full = w >= g0 && w < g1;
-                if (full) LpVec<T>::unpack(lp_load(words + w), v);
+                LpVec<T>::unpack(lp_load(r.words + w), v);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    if (!full) {
-                        if (e0 + i < 0 || e0 + i >= a.vocab) continue;
-                        v[i] = static_cast<float>(x[e0 + i]);
-                    }
-                    if (v[i] < bound || (v[i] != v[i] && bound != -INFINITY)) continue;
-                    const int at = atomicAdd(&s_count, 1);
-                    if (at < kLpCandidates) s_cand[at] = full_key(v[i], e0 + i);
-                }
+                for (int i = 0; i < V; ++i) consider(v[i], w * V - off + i);
+            } else {
+                for (int i = r.first(w); i < r.last(w, a.vocab); ++i) consider(static_cast<float>(x[i]), i);
             }
+        };
+        const bool hot = w0 + tid < w1 && !(top < bound);
+        // The hot threads' words, all at once.
+        if (hot) s_hot[atomicAdd(&s_hots, 1)] = tid;
+        __syncthreads();
+        const int each = (w1 - w0 + kLpThreads - 1) / kLpThreads, all = s_hots * each;
+        for (int i = tid; i < all; i += kLpThreads) {
+            const int h = i / each, w = w0 + s_hot[h] + (i - h * each) * kLpThreads;
+            if (w < w1) consider_word(w);
+        }
         __syncthreads();
         const int n = s_count;
         if (n <= kLpCandidates) {
@@ -316,7 +347,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
             for (int k = 0; k < want; ++k) {
                 uint64_t best = 0;
                 for (int w = w0 + tid; w < w1; w += kLpThreads)
-                    for (int i = max(0, w * V - off); i < min(a.vocab, w * V - off + V); ++i) {
+                    for (int i = r.first(w); i < r.last(w, a.vocab); ++i) {
                         const uint64_t key = full_key(static_cast<float>(x[i]), i);
                         if (key < last && key > best) best = key;
                     }
@@ -358,12 +389,12 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
     }
     {
         float peak = -INFINITY;
-        for (int r = 0; r < nc; ++r) peak = fmaxf(peak, s_all[r].max);
+        for (int q = 0; q < nc; ++q) peak = fmaxf(peak, s_all[q].max);
         const float ground = fmaxf(peak, kLpFloor);
         float total = 0.f, wsum = 0.f;
         int before = 0;
-        for (int r = 0; r < nc; ++r) {
-            const LpShare &o = s_all[r];
+        for (int q = 0; q < nc; ++q) {
+            const LpShare &o = s_all[q];
             const float d = (fmaxf(o.max, kLpFloor) - ground) * kLpLog2e, f = lp_exp2(d), s = o.sum;
             total += s * f;
             if (f != 0.f || s != s) wsum += f * fmaf(s, d, o.weighted);
@@ -379,16 +410,16 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
         }
         // Merge the slices' sorted lists: a key's place is the sum of its places.
         for (int i = tid; i < nc * a.top; i += kLpThreads) {
-            const int r = i / a.top, j = i - r * a.top;
-            if (j >= s_all[r].n_top) continue;
-            const uint64_t k = s_all[r].top[j];
+            const int q = i / a.top, j = i - q * a.top;
+            if (j >= s_all[q].n_top) continue;
+            const uint64_t k = s_all[q].top[j];
             int place = j;
-            for (int s = 0; s < nc; ++s) {
-                if (s == r) continue;
-                int lo = 0, hi = s_all[s].n_top;  // the first entry that is not above k
+            for (int y = 0; y < nc; ++y) {
+                if (y == q) continue;
+                int lo = 0, hi = s_all[y].n_top;  // the first entry that is not above k
                 while (lo < hi) {
                     const int mid = (lo + hi) >> 1;
-                    if (s_all[s].top[mid] > k) lo = mid + 1;
+                    if (s_all[y].top[mid] > k) lo = mid + 1;
                     else hi = mid;
                 }
                 place += lo;
@@ -396,7 +427,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
             if (place < a.top) {
                 const uint32_t id = 0xFFFFFFFFu - static_cast<uint32_t>(k);
                 a.top_ids[row * a.top + place] = static_cast<int32_t>(id);
-                a.top_logprobs[row * a.top + place] = (static_cast<float>(x[id]) - ground) - logz;
+                a.top_logprobs[row * a.top + place] = (key_value(k) - ground) - logz;
             }
         }
     }
@@ -420,11 +451,11 @@ extern "C" int fp8blk_token_logprobs(const void *logits, int dtype, const int32_
         return FP8BLK_EALIGN;
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
-    // CTAs of a row: more while a call has fewer than two per SM and slices stay above 8 KiB.  Two CTAs fit on an SM;
-    // the one that streams covers the other's reductions, so one CTA per row is best when there are rows enough.
-    const int64_t bytes = vocab * es;
-    int nc = 1;
-    while (nc < kLpMaxCluster && n_rows * nc < 2 * dev.sms && bytes / nc > 16384) nc *= 2;
+    // CTAs of a row: two per SM over the call, with slices of 8 KiB at least.  One CTA per row is best when there are
+    // rows enough: the other CTA of the SM streams while this one joins its row.
+    const int64_t bytes = vocab * es, slots = 2 * static_cast<int64_t>(dev.sms);
+    int nc = static_cast<int>(std::min<int64_t>(std::min<int64_t>(slots / n_rows, kLpMaxCluster), bytes / 8192));
+    if (nc < 1) nc = 1;
     const int64_t words = (bytes + 15) / 16 + 1;  // a row that starts inside a word reaches into one more
     LogprobArgs a = {logits, targets, logprob, entropy, rank, top_ids, top_logprobs, dev.status, stride,
                      static_cast<int>(vocab), top, nc, static_cast<int>((words + nc - 1) / nc)};
