@@ -8,6 +8,8 @@
 // under one scale.
 #include "step.h"
 
+#include <algorithm>
+
 namespace fp8blk {
 
 // ------------------------------------------------------------------ kv_map
@@ -214,6 +216,8 @@ struct AppendArgs {
     int64_t n_slots;                       // n_blocks * block_tokens
     int kv_heads, head_dim, block_log2;
     int chunk;                             // tokens a CTA looks after
+    int staged;                            // values of one run that shared memory holds (0: none)
+    uint32_t per_inverse;                  // ceil(2^32 / (head_dim / 8)): divides group numbers below 2^16
 };
 
 // |v| for a block's maximum: what is not finite does not count.
@@ -252,6 +256,14 @@ struct Eight<float> {
     __device__ __forceinline__ void get(float (&x)[8]) const {
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
+    // The largest magnitude, NaN left out.
+    __device__ __forceinline__ float peak(float m) const {
+        float x[8];
+        get(x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+        return m;
+    }
 };
 template <>
 struct Eight<__nv_bfloat16> {
@@ -265,6 +277,11 @@ struct Eight<__nv_bfloat16> {
             x[2 * i] = f.x, x[2 * i + 1] = f.y;
         }
     }
+    __device__ __forceinline__ float peak(float m) const {
+        const __nv_bfloat162 *w = reinterpret_cast<const __nv_bfloat162 *>(&a);
+        const __nv_bfloat162 h = __hmax2(__hmax2(__habs2(w[0]), __habs2(w[1])), __hmax2(__habs2(w[2]), __habs2(w[3])));
+        return fmaxf(m, fmaxf(__low2float(h), __high2float(h)));
+    }
 };
 
 constexpr int kAppendThreads = 256;
@@ -272,14 +289,21 @@ constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int kAppendHeld = 4;       // groups of eight values a thread keeps between its two passes
 constexpr int kAppendMaxChunk = 64;  // tokens a CTA looks after
 
+// The token of group i of a run (i < 128 x 32): i / (head_dim / 8) by its inverse,
+// exact (the excess, i x (head_dim / 8) / 2^32, is below one group).
+__device__ __forceinline__ int append_row(const AppendArgs &a, int i) {
+    return static_cast<int>(__umulhi(static_cast<uint32_t>(i), a.per_inverse));
+}
+
 // One run for one head of K or V: maximum, scale, codes.  THREADS threads (a
-// warp, or the CTA) take the run's groups of eight in turn; the first
-// kAppendHeld groups of a thread stay in registers, so that runs of up to 8192
-// values (a CTA) or 1024 (a warp) are read once, and the rest comes from L1.
-// red: a word per warp (CTA only).
-template <typename T, int THREADS>
+// warp, or the CTA) take the run's groups of eight in turn.  A warp keeps its
+// first kAppendHeld groups in registers between the two passes (1024 values; the
+// rest comes from L1 again); the CTA takes them from shared memory, where they
+// were copied for K and V at once, so that V's are on their way while K's are
+// encoded.  staged: null if the run does not fit there.  red: a word per warp.
+template <typename T, int THREADS, int kHeld>
 __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64_t slot, int run, int h, bool is_v, int tid,
-                                           uint32_t *red) {
+                                           const T *staged, uint32_t *red) {
     const int D = a.head_dim, block = 1 << a.block_log2, off = static_cast<int>(slot & (block - 1));
     const int64_t stride = is_v ? a.v_stride : a.k_stride;
     const T *x = static_cast<const T *>(is_v ? a.v : a.k) + t * stride + static_cast<int64_t>(h) * D;
@@ -288,40 +312,65 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
     float *scale = (is_v ? a.v_scales : a.k_scales) + bh;
     const int per = D / 8, total = run * per;
     auto at = [&](int i) {
-        const int row = i / per;
+        const int row = append_row(a, i);
         return x + row * stride + 8 * (i - row * per);
     };
-    Eight<T> held[kAppendHeld];
+    Eight<T> held[kHeld + 1];
 #pragma unroll
-    for (int k = 0; k < kAppendHeld; ++k)
+    for (int k = 0; k < kHeld; ++k)
         if (tid + k * THREADS < total) held[k].load(at(tid + k * THREADS));
     const float old = off > 0 ? *scale : 0.f;
-    uint32_t amax = 0;
-    auto peak = [&](const Eight<T> &e) {
-        float f[8];
-        e.get(f);
+    // Over all the run's groups, and over the threads.  (Magnitudes are not negative: their bits order as they do.)
+    auto over_run = [&](auto f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max(amax, finite_abs_bits(f[j]));
+        for (int k = 0; k < kHeld; ++k)
+            if (tid + k * THREADS < total) f(held[k], tid + k * THREADS);
+        if (THREADS > 32 && staged) {
+#pragma unroll 4
+            for (int i = tid; i < total; i += THREADS) {
+                Eight<T> e;
+                e.load(staged + 8 * i);
+                f(e, i);
+            }
+        } else {
+#pragma unroll 1
+            for (int i = tid + kHeld * THREADS; i < total; i += THREADS) {
+                Eight<T> e;
+                e.load(at(i));
+                f(e, i);
+            }
+        }
     };
+    auto over_threads = [&](uint32_t m) {
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if constexpr (THREADS > 32) {
+            if ((tid & 31) == 0) red[tid >> 5] = m;
+            __syncthreads();
+            m = __reduce_max_sync(0xFFFFFFFFu, red[tid & (THREADS / 32 - 1)]);
+        }
+        return m;
+    };
+    float peak = 0.f;
+    over_run([&](const Eight<T> &e, int) { peak = e.peak(peak); });
+    uint32_t amax = over_threads(__float_as_uint(peak));
+    const bool infinite = amax >= 0x7F800000u;
+    if (infinite) {  // not often: once more, infinities left out (NaN already are)
+        if constexpr (THREADS > 32) __syncthreads();
+        uint32_t m = 0;
+        over_run([&](const Eight<T> &e, int) {
+            float f[8];
+            e.get(f);
 #pragma unroll
-    for (int k = 0; k < kAppendHeld; ++k)
-        if (tid + k * THREADS < total) peak(held[k]);
-    for (int i = tid + kAppendHeld * THREADS; i < total; i += THREADS) {
-        Eight<T> e;
-        e.load(at(i));
-        peak(e);
-    }
-    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-    if constexpr (THREADS > 32) {
-        if ((tid & 31) == 0) red[tid >> 5] = amax;
-        __syncthreads();
-        amax = __reduce_max_sync(0xFFFFFFFFu, red[tid & (THREADS / 32 - 1)]);
+            for (int j = 0; j < 8; ++j) m = max(m, finite_abs_bits(f[j]));
+        });
+        amax = over_threads(m);
     }
     float s = __uint_as_float(static_cast<uint32_t>(scale_exponent(amax)) << 23);
     if (off > 0) {
         if (old < s) {  // the codes that were there follow the larger scale: a product by a power of two, rounded once
             const float ratio = old / s;
             uint32_t *w = reinterpret_cast<uint32_t *>(codes);
+#pragma unroll 1
             for (int i = tid; i < off * per * 2; i += THREADS) {
                 float2 lo, hi;
                 e4m3x4_to_f32(w[i], lo, hi);
@@ -333,22 +382,18 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
     }
     const float inv = 1.0f / s;
     uint2 *w = reinterpret_cast<uint2 *>(codes + static_cast<int64_t>(off) * D);
-    auto encode = [&](const Eight<T> &e, int i) {
+    over_run([&](const Eight<T> &e, int i) {
         float f[8];
         e.get(f);
+        if (infinite) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = poison_inf(f[j]) * inv;
+            for (int j = 0; j < 8; ++j) f[j] = poison_inf(f[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= inv;
         w[i] = make_uint2(to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16), to_e4m3x2(f[4], f[5]) | (to_e4m3x2(f[6], f[7]) << 16));
-    };
-#pragma unroll
-    for (int k = 0; k < kAppendHeld; ++k)
-        if (tid + k * THREADS < total) encode(held[k], tid + k * THREADS);
-    for (int i = tid + kAppendHeld * THREADS; i < total; i += THREADS) {
-        Eight<T> e;
-        e.load(at(i));
-        encode(e, i);
-    }
-    if constexpr (THREADS > 32) __syncthreads();  // red and the old scale have been read
+    });
+    if constexpr (THREADS > 32) __syncthreads();  // red, the staged values and the old scale have been read
     else __syncwarp();
     if (tid == 0) *scale = s;
 }
@@ -358,57 +403,72 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
 // writes it.  Chunks with few leaders (prompts) take one run at a time with the
 // whole CTA, chunks with many (decode) a warp per run.
 //   Bound: HBM for prompts (es bytes in, 1 out per value), latency for decode.
-template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
-    __shared__ int s_lead[kAppendMaxChunk], s_leads, s_run;
+template <typename T, bool WHOLE>
+__global__ void __launch_bounds__(kAppendThreads, WHOLE ? 6 : 2) kv_append_kernel(const AppendArgs a) {
+    extern __shared__ __align__(16) uint8_t append_smem[];  // a run's values, K's and V's
+    __shared__ uint32_t s_starts[kAppendWarps], s_leads[kAppendWarps];  // a bit per token from the chunk's first on
     __shared__ uint32_t red[kAppendWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.y;
-    const bool is_v = blockIdx.z != 0;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
     const int block = 1 << a.block_log2;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
-    const int here = static_cast<int>(min(static_cast<int64_t>(a.chunk), a.n_tokens - t0));
-    if (tid == 0) {
-        s_leads = 0;
-        s_run = block;
+    // Where runs start, in the chunk and as far past it as its last run can reach (chunk + block <= 192 tokens).
+    const int64_t mine = t0 + tid < a.n_tokens ? a.slots[t0 + tid] : -1;
+    const int64_t before = t0 + tid > 0 && t0 + tid < a.n_tokens ? a.slots[t0 + tid - 1] : -1;
+    const bool good = mine >= 0 && mine < a.n_slots, here = tid < a.chunk;
+    const bool starts = !good || (mine & (block - 1)) == 0 || before != mine - 1;
+    if (here && mine >= a.n_slots) atomicOr(a.status, FP8BLK_STATUS_BAD_KV);
+    const uint32_t sb = __ballot_sync(0xFFFFFFFFu, starts), lb = __ballot_sync(0xFFFFFFFFu, starts && good && here);
+    if (lane == 0) {
+        s_starts[warp] = sb;
+        s_leads[warp] = lb;
     }
     __syncthreads();
-    if (tid < here) {
-        const int64_t slot = a.slots[t0 + tid], before = t0 + tid > 0 ? a.slots[t0 + tid - 1] : -1;
-        if (slot >= a.n_slots) atomicOr(a.status, FP8BLK_STATUS_BAD_KV);
-        else if (slot >= 0 && ((slot & (block - 1)) == 0 || before != slot - 1)) s_lead[atomicAdd(&s_leads, 1)] = tid;
-    }
-    __syncthreads();
-    const int leads = s_leads;
-    if (leads >= kAppendWarps / 2 || (here <= 32 && leads * 8 >= here)) {
-        for (int i = warp; i < leads; i += kAppendWarps) {
-            const int64_t t = t0 + s_lead[i], slot = a.slots[t];
-            const int most = block - static_cast<int>(slot & (block - 1));
-            int run = 1;
-            for (int base = 1; base < most; base += 32) {
-                const int j = base + lane;
-                const bool follows = j < most && t + j < a.n_tokens && a.slots[t + j] == slot + j;
-                const unsigned stop = __ballot_sync(0xFFFFFFFFu, !follows);
-                if (stop) {
-                    run += __ffs(stop) - 1;
-                    break;
+    uint64_t leads = s_leads[0] | (static_cast<uint64_t>(s_leads[1]) << 32);
+    const bool whole = WHOLE && __popcll(leads) < kAppendWarps / 2;  // the CTA on one run at a time
+    for (int n = 0; leads != 0; ++n) {
+        const int i = __ffsll(static_cast<long long>(leads)) - 1;
+        leads &= leads - 1;
+        if (!whole && n % kAppendWarps != warp) continue;
+        int end = i + 1;  // the next start
+        while ((s_starts[end >> 5] >> (end & 31)) == 0) end = (end | 31) + 1;
+        end += __ffs(s_starts[end >> 5] >> (end & 31)) - 1;
+        const int64_t slot = a.slots[t0 + i];
+        if constexpr (WHOLE) if (whole) {
+            const int per = a.head_dim / 8, total = (end - i) * per;
+            const bool fits = total * 8 <= a.staged;
+            T *buffer = reinterpret_cast<T *>(append_smem);
+            if (fits) {
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    const int64_t stride = v ? a.v_stride : a.k_stride;
+                    const T *x = static_cast<const T *>(v ? a.v : a.k) + (t0 + i) * stride + static_cast<int64_t>(h) * a.head_dim;
+                    for (int g = tid; g < total; g += kAppendThreads) {
+                        const int row = append_row(a, g);
+                        const T *src = x + row * stride + 8 * (g - row * per);
+                        const uint32_t dst = smem_addr(buffer + v * a.staged + 8 * g);
+#pragma unroll
+                        for (int y = 0; y < static_cast<int>(sizeof(T)) / 2; ++y)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * y),
+                                         "l"(reinterpret_cast<const char *>(src) + 16 * y)
+                                         : "memory");
+                    }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
                 }
-                run += 32;
             }
-            append_run<T, 32>(a, t, slot, run, h, is_v, lane, nullptr);
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v) {
+                if (v == 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                else asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncthreads();
+                append_run<T, kAppendThreads, 0>(a, t0 + i, slot, end - i, h, v != 0, tid, fits ? buffer + v * a.staged : nullptr, red);
+            }
         }
-    } else {
-        for (int i = 0; i < leads; ++i) {
-            const int64_t t = t0 + s_lead[i], slot = a.slots[t];
-            const int most = block - static_cast<int>(slot & (block - 1));
-            if (tid > 0 && tid < most && !(t + tid < a.n_tokens && a.slots[t + tid] == slot + tid)) atomicMin(&s_run, tid);
-            __syncthreads();
-            const int run = min(s_run, most);
-            append_run<T, kAppendThreads>(a, t, slot, run, h, is_v, tid, red);
-            if (tid == 0) s_run = block;
-            __syncthreads();
+        if (!whole) {
+#pragma unroll 1
+            for (int v = blockIdx.z; v < 2; v += gridDim.z) append_run<T, 32, WHOLE ? 0 : kAppendHeld>(a, t0 + i, slot, end - i, h, v != 0, lane, nullptr, nullptr);
         }
     }
 }
@@ -457,13 +517,25 @@ extern "C" int fp8blk_kv_append(const void *k, const void *v, int dtype, const i
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
     AppendArgs a = {k, v, slots, k_codes, v_codes, k_scales, v_scales, dev.status, n_tokens, k_stride, v_stride,
-                    n_blocks * block_tokens, kv_heads, head_dim, step_log2(block_tokens), 4};
+                    n_blocks * block_tokens, kv_heads, head_dim, step_log2(block_tokens), 4, 0,
+                    static_cast<uint32_t>(((uint64_t(1) << 32) + head_dim / 8 - 1) / (head_dim / 8))};
     // Tokens per CTA: about one run of a prompt when there are tokens enough to fill the SMs, down to a few tokens (a
     // warp each) for a decode step.
     while (a.chunk < kAppendMaxChunk && n_tokens * kv_heads * 2 / (2 * a.chunk) >= 8 * dev.sms) a.chunk *= 2;
-    const dim3 grid(static_cast<unsigned>((n_tokens + a.chunk - 1) / a.chunk), static_cast<unsigned>(kv_heads), 2);
+    // K and V by the same CTA where it takes whole runs, by CTAs of their own where a warp does.  Runs are staged in
+    // shared memory up to 32 KiB (three CTAs per SM or more).
+    const bool whole = a.chunk > 8;
+    const dim3 grid(static_cast<unsigned>((n_tokens + a.chunk - 1) / a.chunk), static_cast<unsigned>(kv_heads), whole ? 1 : 2);
+    if (whole) a.staged = std::min(block_tokens * head_dim, 32768 / es);
+    const size_t smem = static_cast<size_t>(a.staged) * 2 * es;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return step_from_cuda(dtype == FP8BLK_F32
-                              ? step_launch(kv_append_kernel<float>, grid, kAppendThreads, 0, s, a)
-                              : step_launch(kv_append_kernel<__nv_bfloat16>, grid, kAppendThreads, 0, s, a));
+    auto launch = [&](auto kernel) {
+        int per_sm = 0;
+        const cudaError_t err = kernel_occupancy(reinterpret_cast<const void *>(kernel), kAppendThreads, smem, &per_sm);
+        if (err != cudaSuccess) return err;
+        if (per_sm < 1) return cudaErrorInvalidConfiguration;
+        return step_launch(kernel, grid, kAppendThreads, smem, s, a);
+    };
+    if (dtype == FP8BLK_F32) return step_from_cuda(whole ? launch(kv_append_kernel<float, true>) : launch(kv_append_kernel<float, false>));
+    return step_from_cuda(whole ? launch(kv_append_kernel<__nv_bfloat16, true>) : launch(kv_append_kernel<__nv_bfloat16, false>));
 }
