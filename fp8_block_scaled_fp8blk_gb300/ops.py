@@ -301,31 +301,41 @@ def _dtype(t: torch.Tensor, what: str) -> int:
 
 def _typed(t: torch.Tensor, dtype: torch.dtype, what: str) -> int:
     """Data pointer of a contiguous tensor of exactly this type."""
+    if t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, dtype, what)
+    return t.data_ptr()
+
+
+def _refuse(t: torch.Tensor, dtype: torch.dtype, what: str) -> None:
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{what} must be contiguous")
 
 
 def _rows3(t: torch.Tensor, what: str) -> int:
     """Row stride of a [rows, heads, head_dim] tensor whose rows are dense."""
     if t.dim() != 3:
         raise ValueError(f"{what} must have 3 dimensions [rows, heads, head_dim]")
+    rows, heads, dim = t.shape
     s0, s1, s2 = t.stride()
-    heads, dim = t.shape[1], t.shape[2]
     if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
         raise ValueError(f"{what}: heads and head_dim must be contiguous inside a row")
-    return s0 if t.shape[0] > 1 else heads * dim
+    return s0 if rows > 1 else heads * dim
 
 
-def _cache_shape(k_codes, k_scales, v_codes, v_scales):
+_U8, _F32, _I32, _I64T = torch.uint8, torch.float32, torch.int32, torch.int64
+
+
+def _cache(k_codes, k_scales, v_codes, v_scales):
+    """Shape and data pointers of a cache: (n_blocks, kv_heads, block_tokens, head_dim), (k_codes, k_scales, ...)."""
     shape = k_codes.shape
     if len(shape) != 4 or v_codes.shape != shape:
         raise ValueError("k_codes and v_codes must both be [n_blocks, kv_heads, block_tokens, head_dim]")
-    if k_scales.shape != shape[:2] or v_scales.shape != shape[:2]:
+    pairs = shape[:2]
+    if k_scales.shape != pairs or v_scales.shape != pairs:
         raise ValueError("k_scales and v_scales must both be [n_blocks, kv_heads]")
-    return shape
+    return shape, (_typed(k_codes, _U8, "k_codes"), _typed(k_scales, _F32, "k_scales"), _typed(v_codes, _U8, "v_codes"),
+                   _typed(v_scales, _F32, "v_scales"))
 
 
 class KvMap(NamedTuple):
@@ -370,20 +380,18 @@ def fp8blk_kv_map(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
 def fp8blk_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
                      v_codes: torch.Tensor, v_scales: torch.Tensor) -> None:
     """Write keys and values [n, kv_heads, head_dim] (float32 or bfloat16; rows may be strided) into the cache at `slots`."""
-    blocks, heads, block, dim = _cache_shape(k_codes, k_scales, v_codes, v_scales)
+    (blocks, heads, block, dim), cache = _cache(k_codes, k_scales, v_codes, v_scales)
     n = slots.numel()
-    if k.shape != (n, heads, dim) or v.shape != k.shape:
+    if k.shape != (n, heads, dim) or v.shape != (n, heads, dim):
         raise ValueError("k and v must both be [len(slots), kv_heads, head_dim] of the cache")
     if v.dtype is not k.dtype:
         raise TypeError("k and v must have the same type")
     if n == 0:
         return
-    u8, f32 = torch.uint8, torch.float32
-    _check(_lib.fp8blk_kv_append(k.data_ptr(), v.data_ptr(), _dtype(k, "k"), _typed(slots, torch.int64, "slots"),
-                                 _typed(k_codes, u8, "k_codes"), _typed(k_scales, f32, "k_scales"),
-                                 _typed(v_codes, u8, "v_codes"), _typed(v_scales, f32, "v_scales"), n,
-                                 _rows3(k, "k"), _rows3(v, "v"), blocks, heads, block, dim, _stream(k_codes)),
-           "fp8blk_kv_append")
+    rc = _lib.fp8blk_kv_append(k.data_ptr(), v.data_ptr(), _dtype(k, "k"), _typed(slots, _I64T, "slots"), *cache, n,
+                               _rows3(k, "k"), _rows3(v, "v"), blocks, heads, block, dim, _stream(k_codes))
+    if rc:
+        _check(rc, "fp8blk_kv_append")
 
 
 def fp8blk_kv_attn_ws_bytes(n_seqs: int, max_m: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -404,10 +412,11 @@ def fp8blk_kv_attn(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tenso
                    lse: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of q [rows, q_heads, head_dim] (float32 or bfloat16; rows may be strided) over the paged cache; up to
     max_m rows per request.  `lse` (float32 [rows, q_heads]) is written when given."""
-    blocks, kv_heads, block, dim = _cache_shape(k_codes, k_scales, v_codes, v_scales)
+    (blocks, kv_heads, block, dim), cache = _cache(k_codes, k_scales, v_codes, v_scales)
     n, width = block_table.shape
-    rows, q_heads = q.shape[0], q.shape[1]
-    if q.dim() != 3 or q.shape[2] != dim:
+    q_stride = _rows3(q, "q")
+    rows, q_heads, q_dim = q.shape
+    if q_dim != dim:
         raise ValueError("q must be [rows, q_heads, head_dim] of the cache")
     if out is None:
         out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
@@ -419,14 +428,12 @@ def fp8blk_kv_attn(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tenso
         raise ValueError("lse must be [rows, q_heads]")
     if rows == 0:
         return out
-    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
-    _check(_lib.fp8blk_kv_attn(q.data_ptr(), _dtype(q, "q"), _typed(k_codes, u8, "k_codes"),
-                               _typed(k_scales, f32, "k_scales"), _typed(v_codes, u8, "v_codes"),
-                               _typed(v_scales, f32, "v_scales"), _typed(block_table, i32, "block_table"),
-                               _typed(seq_lens, i32, "seq_lens"), _typed(q_starts, i32, "q_starts"), out.data_ptr(),
-                               None if lse is None else _typed(lse, f32, "lse"), ws.data_ptr(),
-                               ws.numel() * ws.element_size(), n, max_m, rows, q_heads, kv_heads, dim, block, blocks,
-                               width, _rows3(q, "q"), _rows3(out, "out"), sm_scale, _stream(q)), "fp8blk_kv_attn")
+    rc = _lib.fp8blk_kv_attn(q.data_ptr(), _dtype(q, "q"), *cache, _typed(block_table, _I32, "block_table"),
+                             _typed(seq_lens, _I32, "seq_lens"), _typed(q_starts, _I32, "q_starts"), out.data_ptr(),
+                             None if lse is None else _typed(lse, _F32, "lse"), ws.data_ptr(), ws.nbytes, n, max_m, rows,
+                             q_heads, kv_heads, dim, block, blocks, width, q_stride, _rows3(out, "out"), sm_scale, _stream(q))
+    if rc:
+        _check(rc, "fp8blk_kv_attn")
     return out
 
 
