@@ -110,6 +110,9 @@ SHAPES = [  # lens, rows, heads, kv, dim, block
     ([129], [7], 10, 2, 192, 128),
     ([390], [8], 8, 1, 144, 16),
     ([64] * 40, [1] * 40, 4, 2, 64, 64),
+    ([300, 77], [8, 5], 4, 2, 64, 32),   # sixteen query rows per cache head, and ten
+    ([600, 129], [4, 8], 4, 1, 112, 16),
+    ([257], [8], 4, 2, 208, 64),
 ]
 
 
@@ -117,6 +120,15 @@ SHAPES = [  # lens, rows, heads, kv, dim, block
 @pytest.mark.parametrize("lens,rows,heads,kv,dim,block", SHAPES)
 def test_matches_plain(ops, dtype, lens, rows, heads, kv, dim, block):
     check(ops, Case(lens, rows, heads, kv, dim, block, seed=sum(lens) + dim), dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_more_requests_than_threads(ops, dtype):
+    """Lists that each thread scans several requests of, with idle requests and empty caches among them."""
+    rng = np.random.default_rng(21)
+    lens, rows = rng.integers(0, 40, 1500), rng.integers(0, 3, 1500)
+    lens[7], rows[7] = 900, 2
+    check(ops, Case(lens, rows, 2, 1, 32, 16, seed=22), dtype)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
