@@ -33,7 +33,6 @@ constexpr int kLpCandidates = 1024;                      // room for what reache
 constexpr int kLpMaxCluster = 8;
 constexpr float kLpLog2e = 1.4426950408889634f;
 constexpr float kLpFloor = -3.402823466e38f;             // reference of a thread that has seen nothing finite
-constexpr float kLpSlack = 20.0f;                        // a value may pass its thread's reference by this much
 
 // Unique order of (value, index): larger values first, -0 and +0 alike, the
 // lowest index first among equal values, NaN below everything.
@@ -60,6 +59,10 @@ struct LpVec<float> {
         x[2] = __uint_as_float(w.z);
         x[3] = __uint_as_float(w.w);
     }
+    // The largest, NaN left out (-inf or NaN if there is nothing else).
+    static __device__ __forceinline__ float peak(const uint4 &w) {
+        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+    }
 };
 template <>
 struct LpVec<__nv_bfloat16> {
@@ -72,6 +75,11 @@ struct LpVec<__nv_bfloat16> {
             x[2 * i] = f.x;
             x[2 * i + 1] = f.y;
         }
+    }
+    static __device__ __forceinline__ float peak(const uint4 &w) {
+        const __nv_bfloat162 *p = reinterpret_cast<const __nv_bfloat162 *>(&w);
+        const __nv_bfloat162 m = __hmax2(__hmax2(p[0], p[1]), __hmax2(p[2], p[3]));
+        return fmaxf(__low2float(m), __high2float(m));
     }
 };
 
@@ -129,9 +137,9 @@ struct LpSlice {
 
 // One cluster per row, one slice of the row per CTA, one pass over memory:
 // thread t takes the slice's 16-byte words t, t + 512, ... and keeps its own
-// reference, sum, weighted sum, maximum and rank count; what is joined, is
-// joined at the end.  The reference moves only when a value passes it by more
-// than 20, so the pass has no serial rescaling.  (A resident grid that asks for
+// maximum, sum, weighted sum and rank count; what is joined, is joined at the
+// end.  The sums are relative to the maximum of the words so far (four at a
+// time), so the terms that matter have exponents near 0, where they are exact.  (A resident grid that asks for
 // the next row's words before it joins a row measured 4% slower than a CTA per
 // row and its scheduling by the hardware; clusters of 16, 40% slower than of 8.)
 //   The top: the k-th largest of 128 group maxima bounds the k-th largest of the
@@ -188,14 +196,9 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
         sum += e;
         weighted = fmaf(e, fmaxf(y, kLpFloor), weighted);
     };
-    auto word = [&](int w, const uint4 &bits) {  // a whole word
+    auto word = [&](int w, const uint4 &bits, float m) {  // a whole word, its maximum m
         float v[V];
         LpVec<T>::unpack(bits, v);
-        float m = v[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-        if (m > ref + kLpSlack) raise(m);
-        top = fmaxf(top, m);
 #pragma unroll
         for (int i = 0; i < V; ++i) add(v[i]);
         if (m >= t) {  // some may come before the target
@@ -210,7 +213,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
         }
     };
     auto element = [&](int i, float v) {  // one of a partial word
-        if (v > ref + kLpSlack) raise(v);
+        if (v > ref) raise(v);
         top = fmaxf(top, v);
         add(v);
         rank += v > t || (v == t && i < target);
@@ -227,9 +230,17 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
 #pragma unroll
         for (int u = 0; u < UN; ++u) bits[u] = next[u];
         fetch(w + UN * kLpThreads);
+        float m[UN], most = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            m[u] = w + u * kLpThreads < g1 ? LpVec<T>::peak(bits[u]) : -INFINITY;
+            most = fmaxf(most, m[u]);
+        }
+        if (most > ref) raise(most);
+        top = fmaxf(top, most);
 #pragma unroll
         for (int u = 0; u < UN; ++u)
-            if (w + u * kLpThreads < g1) word(w + u * kLpThreads, bits[u]);
+            if (w + u * kLpThreads < g1) word(w + u * kLpThreads, bits[u], m[u]);
     }
     if (trails) partial(g1);
     if (has_target && t != t) {  // a NaN target: every number comes before it, and the NaNs of lower index
