@@ -22,24 +22,34 @@ struct LogprobArgs {
     int vocab, top;
     int cluster;  // CTAs of a row
     int words;    // 16-byte words of a row's slice
+    int shift;    // a segment is kLpUnroll << shift words of a thread
 };
 
 constexpr int kLpThreads = 512;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpGroups = 128;                           // thread groups whose maxima bound the k-th largest
 constexpr int kLpGroupSize = kLpThreads / kLpGroups;     // 4 lanes
-constexpr int kLpMaxTop = FP8BLK_MAX_TOP;
+constexpr int kLpMaxTop = FP8BLK_MAX_TOP;  // a lane's each in the last merge
 constexpr int kLpCandidates = 1024;                      // room for what reaches the bound; more takes the slow selection
 constexpr int kLpMaxCluster = 8;
+constexpr int kLpUnrollLog2 = 2, kLpUnroll = 1 << kLpUnrollLog2;  // words of a thread in flight
+constexpr int kLpSegments = 16;                          // parts of a thread's words whose maxima are kept
 constexpr float kLpLog2e = 1.4426950408889634f;
 constexpr float kLpFloor = -3.402823466e38f;             // reference of a thread that has seen nothing finite
 
-// Unique order of (value, index): larger values first, -0 and +0 alike, the
-// lowest index first among equal values, NaN below everything.
-__device__ __forceinline__ uint64_t full_key(float v, uint32_t index) {
+// f32 values as ordered integers: -0 and +0 alike, NaN (0) below everything.
+__device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t u = __float_as_uint(v + 0.0f);
-    const uint32_t key = v != v ? 0u : ((u & 0x80000000u) ? ~u : (u | 0x80000000u));
-    return (static_cast<uint64_t>(key) << 32) | (0xFFFFFFFFu - index);
+    return v != v ? 0u : ((u & 0x80000000u) ? ~u : (u | 0x80000000u));
+}
+constexpr uint32_t kLpKeyInf = 0x007FFFFFu;  // of -inf
+// A key's value; 0's is NaN.
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return k == 0 ? __int_as_float(0x7FC00000) : __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+// Unique order of (value, index): larger values first, the lowest index first among equal ones.
+__device__ __forceinline__ uint64_t full_key(float v, uint32_t index) {
+    return (static_cast<uint64_t>(order_key(v)) << 32) | (0xFFFFFFFFu - index);
 }
 // The next f32 above v (NaN above +inf and for NaN).
 __device__ __forceinline__ float next_up(float v) {
@@ -82,12 +92,6 @@ struct LpVec<__nv_bfloat16> {
         return fmaxf(__low2float(m), __high2float(m));
     }
 };
-
-// A full key's value: -0 comes back as +0, and 0 for NaN as NaN.
-__device__ __forceinline__ float key_value(uint64_t key) {
-    const uint32_t k = static_cast<uint32_t>(key >> 32);
-    return k == 0 ? __int_as_float(0x7FC00000) : __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
-}
 
 // What a CTA of the cluster tells the first.
 struct LpShare {
@@ -151,13 +155,14 @@ struct LpSlice {
 // third of the issue rate at full bandwidth.
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_kernel(const LogprobArgs a) {
-    constexpr int V = LpVec<T>::kN, UN = 4;
+    constexpr int V = LpVec<T>::kN, UN = kLpUnroll;
     __shared__ LpShare s_all[kLpMaxCluster];  // of every CTA, in the cluster's first
     __shared__ uint64_t s_top[kLpMaxTop];
     __shared__ float w_max[kLpWarps], w_sum[kLpWarps], w_wgt[kLpWarps];
     __shared__ int w_rank[kLpWarps];
-    __shared__ __align__(16) float s_group[kLpGroups];
+    __shared__ __align__(16) uint32_t s_group[kLpGroups];
     __shared__ float s_bound;
+    __shared__ float s_seg[kLpSegments][kLpThreads];  // maxima of the threads' segments
     __shared__ int s_hot[kLpThreads], s_hots, s_count;
     __shared__ uint64_t s_cand[kLpCandidates], w_best[kLpWarps];
     cg::cluster_group cluster = cg::this_cluster();
@@ -225,12 +230,15 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
     const bool leads = w0 + tid < g0 && w0 + tid < w1;                         // thread 0's: the row's first word, partial
     const bool trails = g1 < w1 && g1 >= g0 && (g1 - w0) % kLpThreads == tid;  // the row's last word, partial
     if (leads) partial(w0 + tid);
-    for (int w = w_first; w < g1; w += UN * kLpThreads) {
+    int turn = 0;
+    float most = -INFINITY;  // of the segment
+    for (int w = w_first; w < g1; w += UN * kLpThreads, ++turn) {
         uint4 bits[UN];
 #pragma unroll
         for (int u = 0; u < UN; ++u) bits[u] = next[u];
         fetch(w + UN * kLpThreads);
-        float m[UN], most = -INFINITY;
+        float m[UN];
+        if ((turn & ((1 << a.shift) - 1)) == 0) most = -INFINITY;
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
             m[u] = w + u * kLpThreads < g1 ? LpVec<T>::peak(bits[u]) : -INFINITY;
@@ -238,6 +246,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
         }
         if (most > ref) raise(most);
         top = fmaxf(top, most);
+        s_seg[turn >> a.shift][tid] = most;
 #pragma unroll
         for (int u = 0; u < UN; ++u)
             if (w + u * kLpThreads < g1) word(w + u * kLpThreads, bits[u], m[u]);
@@ -256,7 +265,9 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
     float m = top;
 #pragma unroll
     for (int d = 1; d < kLpGroupSize; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    if ((tid & (kLpGroupSize - 1)) == 0) s_group[tid / kLpGroupSize] = m;
+    // The groups' maxima as keys that no two share: the last 7 bits give way to the group's number.
+    const uint32_t mine = (order_key(m) & ~(kLpGroups - 1u)) | (tid / kLpGroupSize);
+    if ((tid & (kLpGroupSize - 1)) == 0) s_group[tid / kLpGroupSize] = mine;
 #pragma unroll
     for (int d = kLpGroupSize; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
     if (lane == 0) w_max[warp] = m;
@@ -269,16 +280,17 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
 #pragma unroll
     for (int d = 1; d < kLpWarps; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
     const float slice_max = m, base = fmaxf(m, kLpFloor);
-    if (a.top > 0 && tid < kLpGroups) {
-        const float mine = s_group[tid];
-        int above = 0, level = 0;
-#pragma unroll 8
-        for (int g = 0; g < kLpGroups; g += 4) {
-            const float4 o = *reinterpret_cast<const float4 *>(s_group + g);
+    if (a.top > 0) {  // a group's four lanes count the keys above its own
+        int above = 0;
+#pragma unroll
+        for (int g = 0; g < kLpGroups / 4 / kLpGroupSize; ++g) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(s_group + (g * kLpGroupSize + (tid & (kLpGroupSize - 1))) * 4);
             above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
-            level += (o.x == mine) + (o.y == mine) + (o.z == mine) + (o.w == mine);
         }
-        if (above < a.top && above + level >= a.top) s_bound = mine;
+#pragma unroll
+        for (int d = 1; d < kLpGroupSize; d <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, d);
+        // Not above the k-th largest group maximum, by the bits left out.
+        if (above == a.top - 1) s_bound = key_value(max(mine & ~(kLpGroups - 1u), kLpKeyInf));
     }
     // ---- the slice's sums, at its own maximum
     {
@@ -335,23 +347,37 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
                 for (int i = r.first(w); i < r.last(w, a.vocab); ++i) consider(static_cast<float>(x[i]), i);
             }
         };
-        const bool hot = w0 + tid < w1 && !(top < bound);
-        // The hot threads' words, all at once.
-        if (hot) s_hot[atomicAdd(&s_hots, 1)] = tid;
+        const int lg = kLpUnrollLog2 + a.shift, span = 1 << lg;  // words of a segment
+        const bool hot = !(top < bound);
+        if (hot)
+            for (int g = 0; w_first + g * span * kLpThreads < g1; ++g)
+                if (!(s_seg[g][tid] < bound)) {
+                    const int at = atomicAdd(&s_hots, 1);
+                    if (at < kLpThreads) s_hot[at] = g * kLpThreads + tid;
+                }
+        if (leads && hot) consider_word(w0 + tid);
+        if (trails && hot) consider_word(g1);
         __syncthreads();
-        const int each = (w1 - w0 + kLpThreads - 1) / kLpThreads, all = s_hots * each;
-        for (int i = tid; i < all; i += kLpThreads) {
-            const int h = i / each, w = w0 + s_hot[h] + (i - h * each) * kLpThreads;
-            if (w < w1) consider_word(w);
+        const int hots = s_hots;
+        if (hots <= kLpThreads) {  // their words, all at once
+            for (int i = tid; i < hots * span; i += kLpThreads) {
+                const int h = s_hot[i >> lg], w = r.start(h & (kLpThreads - 1)) + ((h / kLpThreads << lg) + (i & (span - 1))) * kLpThreads;
+                if (w < g1) consider_word(w);
+            }
+        } else {
+            for (int w = w_first; w < g1; w += kLpThreads) consider_word(w);
         }
         __syncthreads();
         const int n = s_count;
         if (n <= kLpCandidates) {
-            for (int i = tid; i < n; i += kLpThreads) {
-                const uint64_t k = s_cand[i];
+            constexpr int kShare = 16;  // threads of a candidate
+            for (int i = tid / kShare; i - tid / kShare < n; i += kLpThreads / kShare) {
+                const uint64_t k = i < n ? s_cand[i] : 0;
                 int above = 0;
-                for (int j = 0; j < n; ++j) above += s_cand[j] > k;
-                if (above < want) s_top[above] = k;
+                for (int j = tid % kShare; j < n; j += kShare) above += s_cand[j] > k;
+#pragma unroll
+                for (int d = 1; d < kShare; d <<= 1) above += __shfl_xor_sync(0xFFFFFFFFu, above, d);
+                if (i < n && above < want) s_top[above] = k;
             }
         } else {  // too many at the bound: the next largest key, `want` times
             uint64_t last = ~0ull;
@@ -399,17 +425,26 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
         }
     }
     {
-        float peak = -INFINITY;
-        for (int q = 0; q < nc; ++q) peak = fmaxf(peak, s_all[q].max);
+        // Lane q of every eight has slice q.
+        const int q = lane & (kLpMaxCluster - 1);
+        const LpShare &o = s_all[q < nc ? q : 0];
+        float peak = o.max;
+#pragma unroll
+        for (int d = 1; d < kLpMaxCluster; d <<= 1) peak = fmaxf(peak, __shfl_xor_sync(0xFFFFFFFFu, peak, d));
         const float ground = fmaxf(peak, kLpFloor);
         float total = 0.f, wsum = 0.f;
         int before = 0;
-        for (int q = 0; q < nc; ++q) {
-            const LpShare &o = s_all[q];
+        if (q < nc) {
             const float d = (fmaxf(o.max, kLpFloor) - ground) * kLpLog2e, f = lp_exp2(d), s = o.sum;
-            total += s * f;
-            if (f != 0.f || s != s) wsum += f * fmaf(s, d, o.weighted);
-            before += o.rank;
+            total = s * f;
+            if (f != 0.f || s != s) wsum = f * fmaf(s, d, o.weighted);
+            before = o.rank;
+        }
+#pragma unroll
+        for (int d = 1; d < kLpMaxCluster; d <<= 1) {
+            total += __shfl_xor_sync(0xFFFFFFFFu, total, d);
+            wsum += __shfl_xor_sync(0xFFFFFFFFu, wsum, d);
+            before += __shfl_xor_sync(0xFFFFFFFFu, before, d);
         }
         const float nanf = __int_as_float(0x7FC00000);
         const float logz = peak == -INFINITY ? nanf : logf(total);
@@ -419,26 +454,29 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
             a.entropy[row] = logz - wsum / total * 0.6931471805599453f;
             if (!has_target && target != -1) atomicOr(a.status, FP8BLK_STATUS_BAD_TARGET);
         }
-        // Merge the slices' sorted lists: a key's place is the sum of its places.
-        for (int i = tid; i < nc * a.top; i += kLpThreads) {
-            const int q = i / a.top, j = i - q * a.top;
-            if (j >= s_all[q].n_top) continue;
-            const uint64_t k = s_all[q].top[j];
-            int place = j;
-            for (int y = 0; y < nc; ++y) {
-                if (y == q) continue;
-                int lo = 0, hi = s_all[y].n_top;  // the first entry that is not above k
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (s_all[y].top[mid] > k) lo = mid + 1;
-                    else hi = mid;
-                }
-                place += lo;
+        // Merge the slices' sorted lists: a key's place is the sum of its places in all.
+        if (warp < nc && lane < s_all[warp].n_top) {
+            const uint64_t k = s_all[warp].top[lane];
+            int place[kLpMaxCluster], room[kLpMaxCluster];
+#pragma unroll
+            for (int y = 0; y < kLpMaxCluster; ++y) {
+                place[y] = y == warp ? lane : 0;
+                room[y] = y < nc && y != warp ? s_all[y].n_top : 0;
             }
-            if (place < a.top) {
+            for (int step = kLpMaxTop; step; step >>= 1) {
+#pragma unroll
+                for (int y = 0; y < kLpMaxCluster; ++y) {
+                    const int to = place[y] + step;
+                    if (to <= room[y] && s_all[y].top[to - 1] > k) place[y] = to;
+                }
+            }
+            int at = 0;
+#pragma unroll
+            for (int y = 0; y < kLpMaxCluster; ++y) at += place[y];
+            if (at < a.top) {
                 const uint32_t id = 0xFFFFFFFFu - static_cast<uint32_t>(k);
-                a.top_ids[row * a.top + place] = static_cast<int32_t>(id);
-                a.top_logprobs[row * a.top + place] = (key_value(k) - ground) - logz;
+                a.top_ids[row * a.top + at] = static_cast<int32_t>(id);
+                a.top_logprobs[row * a.top + at] = (key_value(static_cast<uint32_t>(k >> 32)) - ground) - logz;
             }
         }
     }
@@ -469,7 +507,8 @@ extern "C" int fp8blk_token_logprobs(const void *logits, int dtype, const int32_
     if (nc < 1) nc = 1;
     const int64_t words = (bytes + 15) / 16 + 1;  // a row that starts inside a word reaches into one more
     LogprobArgs a = {logits, targets, logprob, entropy, rank, top_ids, top_logprobs, dev.status, stride,
-                     static_cast<int>(vocab), top, nc, static_cast<int>((words + nc - 1) / nc)};
+                     static_cast<int>(vocab), top, nc, static_cast<int>((words + nc - 1) / nc), 0};
+    while ((kLpSegments << a.shift) * kLpUnroll * kLpThreads < a.words) ++a.shift;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n_rows * nc));
     cfg.blockDim = dim3(kLpThreads);
