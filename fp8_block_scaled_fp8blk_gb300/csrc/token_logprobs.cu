@@ -25,10 +25,9 @@ struct LogprobArgs {
     int shift;    // a segment is kLpUnroll << shift words of a thread
 };
 
-constexpr int kLpThreads = 512;
-constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpWide = 512, kLpNarrow = 256;            // threads of a CTA: of several a row, of one a row
+constexpr int kLpResident = 1024;                        // threads of an SM
 constexpr int kLpGroups = 128;                           // thread groups whose maxima bound the k-th largest
-constexpr int kLpGroupSize = kLpThreads / kLpGroups;     // 4 lanes
 constexpr int kLpMaxTop = FP8BLK_MAX_TOP;  // a lane's each in the last merge
 constexpr int kLpCandidates = 1024;                      // room for what reaches the bound; more takes the slow selection
 constexpr int kLpMaxCluster = 8;
@@ -117,7 +116,7 @@ __device__ __forceinline__ float lp_exp2(float x) {
 // A CTA's slice of one row, as 16-byte words: word w holds the elements
 // [w V - off, w V - off + V) of the row, of which the row's first and last word
 // may hold fewer.  Words [w0, w1) are the slice's, [g0, g1) the whole ones.
-template <typename T>
+template <typename T, int TH>
 struct LpSlice {
     static constexpr int V = LpVec<T>::kN;
     const T *x;
@@ -136,34 +135,38 @@ struct LpSlice {
     __device__ __forceinline__ int first(int w) const { return max(0, w * V - off); }
     __device__ __forceinline__ int last(int w, int vocab) const { return min(vocab, w * V - off + V); }
     // A thread's first whole word; the row's first word, if partial, is thread 0's before that.
-    __device__ __forceinline__ int start(int tid) const { return w0 + tid + (w0 + tid < g0 ? kLpThreads : 0); }
+    __device__ __forceinline__ int start(int tid) const { return w0 + tid + (w0 + tid < g0 ? TH : 0); }
 };
 
 // One cluster per row, one slice of the row per CTA, one pass over memory:
-// thread t takes the slice's 16-byte words t, t + 512, ... and keeps its own
+// thread t takes the slice's 16-byte words t, t + TH, ... and keeps its own
 // maximum, sum, weighted sum and rank count; what is joined, is joined at the
 // end.  The sums are relative to the maximum of the words so far (four at a
-// time), so the terms that matter have exponents near 0, where they are exact.  (A resident grid that asks for
-// the next row's words before it joins a row measured 4% slower than a CTA per
-// row and its scheduling by the hardware; clusters of 16, 40% slower than of 8.)
+// time), so the terms that matter have exponents near 0, where they are exact;
+// a reference that lags by up to 20 saves a few instructions and costs 1e-6.
 //   The top: the k-th largest of 128 group maxima bounds the k-th largest of the
-// slice from below, so only threads whose own maximum reaches it hold
-// candidates; their words are read again (out of L2: some 20 threads' worth), and
-// the few candidates are ranked by counting.  Rows where too many values tie with the bound are
-// selected one by one.
-//   Bound: HBM (4 or 2 bytes a logit).  Per f32 logit about 9 instructions, a
-// third of the issue rate at full bandwidth.
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_kernel(const LogprobArgs a) {
-    constexpr int V = LpVec<T>::kN, UN = kLpUnroll;
+// slice from below.  Only segments (a thread's four words, or more in a long
+// row) whose own maximum reaches it hold candidates: some 20 segments are read
+// again, out of L2, and the few candidates are ranked by counting.  Rows where
+// too many values tie with the bound are selected one by one.
+//   Bound: HBM (4 or 2 bytes a logit) for many rows of f32, at about 9
+// instructions a logit; instructions for bf16; the chain of joins for few rows.
+// Measured, top 20 and 131072 logits: 2048 rows of f32 177 us (91% of the copy
+// rate; without the top 100%), of bf16 147 us (54%); top 5, 8 rows of f32 7.1 us.
+// (A resident grid that asks for the next row's words before it joins a row,
+// clusters of 16, and words staged by asynchronous copies, twice as many in
+// flight, each measured slower.)
+template <typename T, int TH>
+__global__ void __launch_bounds__(TH, kLpResident / TH) token_logprobs_kernel(const LogprobArgs a) {
+    constexpr int V = LpVec<T>::kN, UN = kLpUnroll, kLpWarps = TH / 32, kLpGroupSize = TH / kLpGroups;
     __shared__ LpShare s_all[kLpMaxCluster];  // of every CTA, in the cluster's first
     __shared__ uint64_t s_top[kLpMaxTop];
     __shared__ float w_max[kLpWarps], w_sum[kLpWarps], w_wgt[kLpWarps];
     __shared__ int w_rank[kLpWarps];
     __shared__ __align__(16) uint32_t s_group[kLpGroups];
     __shared__ float s_bound;
-    __shared__ float s_seg[kLpSegments][kLpThreads];  // maxima of the threads' segments
-    __shared__ int s_hot[kLpThreads], s_hots, s_count;
+    __shared__ float s_seg[kLpSegments][TH];  // maxima of the threads' segments
+    __shared__ int s_hot[TH], s_hots, s_count;
     __shared__ uint64_t s_cand[kLpCandidates], w_best[kLpWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = a.cluster, c = nc > 1 ? static_cast<int>(cluster.block_rank()) : 0;
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t row = blockIdx.x / nc;
-    const LpSlice<T> r(a, row, c);
+    const LpSlice<T, TH> r(a, row, c);
     const int w0 = r.w0, w1 = r.w1, g0 = r.g0, g1 = r.g1, off = r.off;
     const T *x = r.x;
     // The first words are on their way before the target's logit is asked for.
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
     auto fetch = [&](int at) {
 #pragma unroll
         for (int u = 0; u < UN; ++u)
-            if (at + u * kLpThreads < g1) next[u] = lp_load(r.words + at + u * kLpThreads);
+            if (at + u * TH < g1) next[u] = lp_load(r.words + at + u * TH);
     };
     fetch(r.start(tid));
     const int target = a.targets[row];
@@ -228,20 +231,20 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
     };
     const int w_first = r.start(tid);
     const bool leads = w0 + tid < g0 && w0 + tid < w1;                         // thread 0's: the row's first word, partial
-    const bool trails = g1 < w1 && g1 >= g0 && (g1 - w0) % kLpThreads == tid;  // the row's last word, partial
+    const bool trails = g1 < w1 && g1 >= g0 && (g1 - w0) % TH == tid;  // the row's last word, partial
     if (leads) partial(w0 + tid);
     int turn = 0;
     float most = -INFINITY;  // of the segment
-    for (int w = w_first; w < g1; w += UN * kLpThreads, ++turn) {
+    for (int w = w_first; w < g1; w += UN * TH, ++turn) {
         uint4 bits[UN];
 #pragma unroll
         for (int u = 0; u < UN; ++u) bits[u] = next[u];
-        fetch(w + UN * kLpThreads);
+        fetch(w + UN * TH);
         float m[UN];
         if ((turn & ((1 << a.shift) - 1)) == 0) most = -INFINITY;
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
-            m[u] = w + u * kLpThreads < g1 ? LpVec<T>::peak(bits[u]) : -INFINITY;
+            m[u] = w + u * TH < g1 ? LpVec<T>::peak(bits[u]) : -INFINITY;
             most = fmaxf(most, m[u]);
         }
         if (most > ref) raise(most);
@@ -249,12 +252,12 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
         s_seg[turn >> a.shift][tid] = most;
 #pragma unroll
         for (int u = 0; u < UN; ++u)
-            if (w + u * kLpThreads < g1) word(w + u * kLpThreads, bits[u], m[u]);
+            if (w + u * TH < g1) word(w + u * TH, bits[u], m[u]);
     }
     if (trails) partial(g1);
     if (has_target && t != t) {  // a NaN target: every number comes before it, and the NaNs of lower index
         rank = 0;
-        for (int w = w0 + tid; w < w1; w += kLpThreads)
+        for (int w = w0 + tid; w < w1; w += TH)
             for (int i = r.first(w); i < r.last(w, a.vocab); ++i) {
                 const float v = static_cast<float>(x[i]);
                 rank += v == v || i < target;
@@ -350,28 +353,28 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
         const int lg = kLpUnrollLog2 + a.shift, span = 1 << lg;  // words of a segment
         const bool hot = !(top < bound);
         if (hot)
-            for (int g = 0; w_first + g * span * kLpThreads < g1; ++g)
+            for (int g = 0; w_first + g * span * TH < g1; ++g)
                 if (!(s_seg[g][tid] < bound)) {
                     const int at = atomicAdd(&s_hots, 1);
-                    if (at < kLpThreads) s_hot[at] = g * kLpThreads + tid;
+                    if (at < TH) s_hot[at] = g * TH + tid;
                 }
         if (leads && hot) consider_word(w0 + tid);
         if (trails && hot) consider_word(g1);
         __syncthreads();
         const int hots = s_hots;
-        if (hots <= kLpThreads) {  // their words, all at once
-            for (int i = tid; i < hots * span; i += kLpThreads) {
-                const int h = s_hot[i >> lg], w = r.start(h & (kLpThreads - 1)) + ((h / kLpThreads << lg) + (i & (span - 1))) * kLpThreads;
+        if (hots <= TH) {  // their words, all at once
+            for (int i = tid; i < hots * span; i += TH) {
+                const int h = s_hot[i >> lg], w = r.start(h & (TH - 1)) + ((h / TH << lg) + (i & (span - 1))) * TH;
                 if (w < g1) consider_word(w);
             }
         } else {
-            for (int w = w_first; w < g1; w += kLpThreads) consider_word(w);
+            for (int w = w_first; w < g1; w += TH) consider_word(w);
         }
         __syncthreads();
         const int n = s_count;
         if (n <= kLpCandidates) {
             constexpr int kShare = 16;  // threads of a candidate
-            for (int i = tid / kShare; i - tid / kShare < n; i += kLpThreads / kShare) {
+            for (int i = tid / kShare; i - tid / kShare < n; i += TH / kShare) {
                 const uint64_t k = i < n ? s_cand[i] : 0;
                 int above = 0;
                 for (int j = tid % kShare; j < n; j += kShare) above += s_cand[j] > k;
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(kLpThreads, 1024 / kLpThreads) token_logprobs_
             uint64_t last = ~0ull;
             for (int k = 0; k < want; ++k) {
                 uint64_t best = 0;
-                for (int w = w0 + tid; w < w1; w += kLpThreads)
+                for (int w = w0 + tid; w < w1; w += TH)
                     for (int i = r.first(w); i < r.last(w, a.vocab); ++i) {
                         const uint64_t key = full_key(static_cast<float>(x[i]), i);
                         if (key < last && key > best) best = key;
@@ -500,18 +503,21 @@ extern "C" int fp8blk_token_logprobs(const void *logits, int dtype, const int32_
         return FP8BLK_EALIGN;
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
-    // CTAs of a row: two per SM over the call, with slices of 8 KiB at least.  One CTA per row is best when there are
-    // rows enough: the other CTA of the SM streams while this one joins its row.
-    const int64_t bytes = vocab * es, slots = 2 * static_cast<int64_t>(dev.sms);
-    int nc = static_cast<int>(std::min<int64_t>(std::min<int64_t>(slots / n_rows, kLpMaxCluster), bytes / 8192));
-    if (nc < 1) nc = 1;
+    // From three rows per SM on, a narrow CTA per row, four of them resident: they take turns at the end of a row, when
+    // nothing streams (4000 x 32000 f32: 112 us, with wide CTAs 139; 2048 x 131072: 177 and 187).  With fewer rows, wide
+    // CTAs and as many a row as fit at once, with slices of 8 KiB at least (380 x 131072 f32: 46 us, narrow 55).
+    const int64_t bytes = vocab * es, slots = kLpResident / kLpWide * static_cast<int64_t>(dev.sms);
+    const bool narrow = n_rows >= 3 * static_cast<int64_t>(dev.sms);
+    const int threads = narrow ? kLpNarrow : kLpWide;
+    const int nc = static_cast<int>(std::max<int64_t>(std::min<int64_t>({slots / n_rows, kLpMaxCluster, bytes / 8192}), 1));
     const int64_t words = (bytes + 15) / 16 + 1;  // a row that starts inside a word reaches into one more
     LogprobArgs a = {logits, targets, logprob, entropy, rank, top_ids, top_logprobs, dev.status, stride,
                      static_cast<int>(vocab), top, nc, static_cast<int>((words + nc - 1) / nc), 0};
-    while ((kLpSegments << a.shift) * kLpUnroll * kLpThreads < a.words) ++a.shift;
+    const int64_t whole = std::min<int64_t>(a.words, bytes / 16);  // words of a slice, at most
+    while (static_cast<int64_t>(kLpSegments << a.shift) * kLpUnroll * threads < whole) ++a.shift;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n_rows * nc));
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -522,6 +528,8 @@ extern "C" int fp8blk_token_logprobs(const void *logits, int dtype, const int32_
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = tuning().use_pdl ? 2 : 1;
-    return step_from_cuda(dtype == FP8BLK_F32 ? cudaLaunchKernelEx(&cfg, token_logprobs_kernel<float>, a)
-                                              : cudaLaunchKernelEx(&cfg, token_logprobs_kernel<__nv_bfloat16>, a));
+    auto kernel = dtype == FP8BLK_F32
+                      ? (narrow ? token_logprobs_kernel<float, kLpNarrow> : token_logprobs_kernel<float, kLpWide>)
+                      : (narrow ? token_logprobs_kernel<__nv_bfloat16, kLpNarrow> : token_logprobs_kernel<__nv_bfloat16, kLpWide>);
+    return step_from_cuda(cudaLaunchKernelEx(&cfg, kernel, a));
 }

@@ -131,6 +131,40 @@ def test_repeats_bit_for_bit_and_in_a_graph(ops):
         assert all(torch.equal(p, q) for p, q in zip(a, out))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab,start,top", [(1, 0, 1), (31, 1, 20), (1003, 3, 32), (70001, 1, 20), (262144, 0, 32)])
+@pytest.mark.parametrize("n", [310, 461])
+def test_many_rows_one_cta_each(ops, dtype, n, vocab, start, top):
+    """Rows enough that each is one CTA's, wide or narrow: every kind of row at many places, the same everywhere."""
+    rng = np.random.default_rng(vocab + n)
+    kinds = (2.5 * rng.standard_normal((9, vocab))).astype(np.float32)
+    kinds[1] = np.sort(kinds[1])
+    kinds[2] = np.sort(kinds[2])[::-1]
+    kinds[3] = rng.integers(-1, 2, vocab)      # ties
+    kinds[4] = 0.0                             # nothing but ties
+    kinds[5, vocab // 2:] = -np.inf
+    kinds[6] = -np.inf
+    kinds[7, vocab // 2] = np.nan
+    kinds[8, : vocab // 2] = np.finfo(np.float32).min / 2
+    buf = torch.zeros((9, start + vocab), dtype=dtype, device="cuda:0")
+    buf[:, start:] = to_dev(kinds).to(dtype)
+    targets = rng.integers(0, vocab, 9).astype(np.int32)
+    top = min(top, vocab)
+    check(ops, buf[:, start:], targets, top)
+    which = torch.arange(n, device="cuda:0") % 9
+    got = ops.fp8blk_token_logprobs(buf[which][:, start:], to_dev(targets)[which], top)
+    x = buf[:, start:].float().cpu().numpy().astype(np.float64)
+    logprob, rank, entropy, ids, tops = ref.token_logprobs(x, targets, top)
+    k = which.cpu().numpy()
+    assert np.array_equal(got.rank.cpu().numpy(), rank[k]) and np.array_equal(got.top_ids.cpu().numpy(), ids[k])
+    fin = np.where(np.isfinite(x), np.abs(x), 0.0).max(1)
+    tol = 2.0 ** -18 * (1.0 + fin)
+    for g, w, t in ((got.logprob, logprob, tol), (got.entropy, entropy, tol * 3), (got.top_logprobs, tops, tol[:, None])):
+        g = g.cpu().numpy().astype(np.float64)
+        ok = (g == w[k]) | (np.abs(g - w[k]) <= t[k]) | (np.isnan(w[k]) & np.isnan(g))
+        assert ok.all()
+
+
 def test_many_rows_far_offsets(ops):
     """Rows whose byte offset is past 2^32."""
     n, vocab = 9000, 131072
