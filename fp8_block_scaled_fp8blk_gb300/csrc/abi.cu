@@ -99,20 +99,6 @@ static EncodeTiledFn encode_tiled_fn(cudaError_t *err) {
     return fn;
 }
 
-cudaError_t encode_map_2d(const void *ptr, int64_t rows, int64_t cols, int64_t row_bytes, CUtensorMapDataType dtype,
-                          int box_rows, int box_cols, CUtensorMapSwizzle swizzle, CUtensorMap *out) {
-    cudaError_t err;
-    EncodeTiledFn fn = encode_tiled_fn(&err);
-    if (!fn) return err;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t estr[2] = {1u, 1u};
-    const CUresult r = fn(out, dtype, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 namespace {
 struct MapEntry {
     const void *ptr;
@@ -135,9 +121,17 @@ cudaError_t tensor_map_2d(const void *ptr, int64_t rows, int64_t cols, int64_t r
             *out = e.map;
             return cudaSuccess;
         }
+    cudaError_t err;
+    EncodeTiledFn fn = encode_tiled_fn(&err);
+    if (!fn) return err;
     CUtensorMap map;
-    const cudaError_t err = encode_map_2d(ptr, rows, cols, row_bytes, dtype, box_rows, box_cols, swizzle, &map);
-    if (err != cudaSuccess) return err;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1u, 1u};
+    const CUresult r = fn(&map, dtype, 2, const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
     g_maps[g_map_next] = MapEntry{ptr, rows, cols, box_rows, box_cols, static_cast<int>(dtype), static_cast<int>(swizzle), map};
     g_map_next = (g_map_next + 1) % 128;
     *out = map;

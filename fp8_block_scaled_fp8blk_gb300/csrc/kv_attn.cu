@@ -24,6 +24,29 @@ static size_t attn_ws_bytes(int rows, int head_dim) {
     return kAtHeaderBytes + static_cast<size_t>(kAtMaxGrid) * 2 * (r * halves * 128 + 2 * r) * sizeof(float);
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Tensor map of a pool of codes as [rows, head_dim]: boxes of box_rows rows x 128 codes.  Encoded anew by each call (bit
+// packing on the host): nothing is kept by a pool's address.
+static cudaError_t pool_map(const uint8_t *codes, int64_t rows, int head_dim, int box_rows, CUtensorMap *out) {
+    static const EncodeTiled encode = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiled>(f) : nullptr;
+    }();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim)};
+    const cuuint32_t box[2] = {128u, static_cast<cuuint32_t>(box_rows)}, steps[2] = {1u, 1u};
+    const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(codes), dims, strides, box, steps,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <typename T, int PL, int R, int ND>
 static cudaError_t launch_attn(const AttnArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap, int64_t grid,
                                cudaStream_t stream) {
@@ -118,16 +141,15 @@ extern "C" int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, 
     // past head_dim).
     CUtensorMap kmap, vmap;
     const int64_t pool_rows = n_blocks * kv_heads * block_tokens;
-    cudaError_t err = encode_map_2d(k_codes, pool_rows, head_dim, head_dim, CU_TENSOR_MAP_DATA_TYPE_UINT8, block_tokens, 128,
-                                    CU_TENSOR_MAP_SWIZZLE_128B, &kmap);
-    if (err == cudaSuccess)
-        err = encode_map_2d(v_codes, pool_rows, head_dim, head_dim, CU_TENSOR_MAP_DATA_TYPE_UINT8, block_tokens, 128,
-                            CU_TENSOR_MAP_SWIZZLE_128B, &vmap);
+    cudaError_t err = pool_map(k_codes, pool_rows, head_dim, block_tokens, &kmap);
+    if (err == cudaSuccess) err = pool_map(v_codes, pool_rows, head_dim, block_tokens, &vmap);
     if (err != cudaSuccess) return step_from_cuda(err);
-    // One CTA per SM, and no more than the longest possible list has entries.
+    // One CTA per SM, and no more than the longest possible list has entries (a unit: its set-up, its tiles, and one for a
+    // length past the table).
     const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(max_blocks) * block_tokens + kAtTile - 1) / kAtTile);
-    const int64_t entries = static_cast<int64_t>(n_seqs) * kv_heads * ((max_m * group + rows - 1) / rows) * (tiles + 1);
+    const int64_t entries = static_cast<int64_t>(n_seqs) * kv_heads * ((max_m * group + rows - 1) / rows) * (tiles + 2);
     if (entries > kStepMaxIndex / at_max_weight(rows)) return FP8BLK_ERANGE;  // the kernel counts them in 32 bits
+    a.max_tiles = static_cast<int>(tiles + 1);
     const int64_t grid = std::min<int64_t>(std::min(dev.sms, kAtMaxGrid), entries);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return step_from_cuda(dtype == FP8BLK_F32 ? launch_attn_rows<float, 4>(a, rows, kmap, vmap, grid, s)

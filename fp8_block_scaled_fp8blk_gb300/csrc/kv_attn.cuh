@@ -74,6 +74,7 @@ struct AttnArgs {
     unsigned int *status;
     int64_t q_stride, out_stride, n_blocks;
     int n_seqs, max_m, total_rows, kv_heads, group, head_dim, block_log2, width;
+    int max_tiles;                    // a table's tiles and one more
     float scale_log2;                 // softmax scale x log2 e
 };
 
@@ -282,7 +283,8 @@ __device__ __forceinline__ AttnSeq at_seq(const AttnArgs &a, int s) {
     q.bad = off || len < 0;
     q.rows = off ? 0 : static_cast<int>(rows);
     q.len = max(len, 0);
-    q.tiles = (q.len >> 7) + ((q.len & 127) != 0);
+    // A length past the table ends in a tile past it, whose scales are NaN: every row sees some of it.
+    q.tiles = min((q.len >> 7) + ((q.len & 127) != 0), a.max_tiles);
     q.groups = (q.rows * a.group + R - 1) / R;
     // Measured on f32 tiles of 8, 16 and 32 rows: 1.1, 1.5 and 1.9 us, about (3 + eighths) x 0.28.
     q.weight = R == 8 ? 1 : 3 + min(R, q.rows * a.group + 7) / 8;
@@ -669,7 +671,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         ids = ids_next;
                         ids_next = window(win + 32);
                     }
-                    const int pages = min(np, ((len + block - 1) >> a.block_log2) - page0);
+                    const int pages = min(np, (len >> a.block_log2) + ((len & (block - 1)) != 0) - page0);
                     const int id = __shfl_sync(0xFFFFFFFFu, ids, (page0 - win + lane) & 31);
                     const bool mine = lane < pages, good = id >= 0 && id < a.n_blocks;
                     if (mine && !good) atomicOr(a.status, 4u);

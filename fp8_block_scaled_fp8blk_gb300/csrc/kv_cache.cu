@@ -56,6 +56,9 @@ __device__ __forceinline__ MapRequest map_request(const MapArgs &a, int r) {
 // a second launch or a grid-wide wait) and then writes its share of the
 // outputs: tokens and fresh table entries, each found by a search in the scan.
 // Thread i scans requests [i q, (i + 1) q), q = ceil(n / 512).
+//   Bound: latency (the scan, then a search of nine dependent steps).  Measured
+// in a graph: 64 requests of one token 4.9 us; 512 requests with 2.1 M new
+// tokens 12.8 us, 3.9 of them what the bytes take.
 __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const MapArgs a) {
     __shared__ int64_t s_tok[kMapThreads + 1], s_blk[kMapThreads + 1];  // exclusive prefixes per thread
     __shared__ int64_t w_tok[kMapThreads / 32], w_blk[kMapThreads / 32];
@@ -403,6 +406,10 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
 // writes it.  Chunks with few leaders (prompts) take one run at a time with the
 // whole CTA, chunks with many (decode) a warp per run.
 //   Bound: HBM for prompts (es bytes in, 1 out per value), latency for decode.
+// Measured in a graph: 16.7 k bf16 tokens of 16 prompts, 8 heads of 128, 24.0 us
+// (64% of the copy rate; ncu: 52% of the ALU pipe's issue and 36% of DRAM's
+// cycles busy, so what is left is the two passes over a run one after the
+// other); 64 tokens of f32, one a request, 2.7 us.
 template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kAppendThreads, WHOLE ? 6 : 2) kv_append_kernel(const AppendArgs a) {
     extern __shared__ __align__(16) uint8_t append_smem[];  // a run's values, K's and V's

@@ -70,10 +70,6 @@ Plan make_plan(int m, int64_t rows, int64_t cols, int bpw, const DeviceInfo &dev
 // Fill GemvArgs geometry from a plan.
 void apply_plan(const Plan &p, GemvArgs *a);
 
-// A 2-D tensor map of a rows x cols row-major array whose rows are row_bytes
-// apart, encoded anew (a matter of bit packing on the host).
-cudaError_t encode_map_2d(const void *ptr, int64_t rows, int64_t cols, int64_t row_bytes, CUtensorMapDataType dtype,
-                          int box_rows, int box_cols, CUtensorMapSwizzle swizzle, CUtensorMap *out);
 // Tensor map of an e4m3 weight matrix for the tensor-core kernel: 2-D,
 // {cols, rows}, boxes of box_rows rows x 128 bytes, 128-byte swizzle, zeros
 // out of range.  Cached per (pointer, shape, box height).

@@ -396,7 +396,9 @@ size_t fp8blk_kv_attn_ws_bytes(int n_seqs, int max_m, int q_heads, int kv_heads,
  * A block id outside the pool (or a length past max_blocks) makes the rows
  * that see it NaN; a request with more than max_m rows, or rows outside
  * total_rows, is skipped; each sets FP8BLK_STATUS_BAD_KV.
- * Errors: EINVAL, EALIGN, EWS, ERANGE, ECUDA.
+ * Errors: EINVAL, EALIGN, EWS, ERANGE (a size past the limits above, or more
+ * than about 2^28 tiles of 128 tokens over all requests, heads and groups of 32
+ * rows at max_blocks each), ECUDA.
  */
 int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, const float *k_scales, const uint8_t *v_codes,
                    const float *v_scales, const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_starts,
@@ -413,7 +415,8 @@ int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, const float
  *   top_ids[i], top_logprobs[i] = the first `top` tokens of that order
  * Order: larger logits first, the lowest index first among equal ones (-0 and
  * +0 are equal), NaN last -- the order of fp8blk_gemv_argmax, so top_ids[i][0]
- * is its token.  Sums are f32.  The logits are read from memory once.
+ * is its token.  Sums are f32.  The logits are read once (the few words that
+ * can hold top tokens, twice).
  * A row with a NaN or +inf, or with -inf alone, has NaN logprob, entropy and
  * top_logprobs; -inf among finite logits has probability 0.  Target -1 means
  * none: logprob NaN, rank -1; any other target outside [0, vocab) gives the

@@ -241,6 +241,23 @@ def test_bad_ids_and_lengths_are_flagged(ops):
     assert (out[:2] == 0).all() and torch.equal(out[2:], clean[2:])
 
 
+@pytest.mark.parametrize("heads,kv,rows", [(32, 4, 4), (8, 8, 1)])
+@pytest.mark.parametrize("n", [20, 50])
+def test_lengths_far_past_the_table(ops, n, heads, kv, rows):
+    """They make their own rows NaN, whatever their sum, and take no longer than the table is wide."""
+    c = Case([40 + 7 * s for s in range(n)], [rows] * n, heads, kv, 64, 16, seed=15)
+    want, _, peak, spread = ref.kv_attn(c.q.astype(np.float64), c.kc, c.ks, c.vc, c.vs, c.table, c.lens, c.starts, c.scale)
+    u = 2.0 ** -16 + (c.dim + 16) * 2.0 ** -24  # check's bound for f32
+    tol = (2 * u * peak[:, :, None] + 2.0 ** -16 + 2.0 ** -19) * spread
+    c.lens[::2] = 2 ** 31 - 1
+    c.lens[0] = 16 * c.table.shape[1] + 129 + 128
+    out = run(ops, c, torch.float32)[0]
+    assert ops.fp8blk_device_status(clear=True) == ops.STATUS_BAD_KV
+    assert torch.isnan(out.view(n, -1)[::2]).all()
+    near = np.abs(out.cpu().numpy().astype(np.float64) - want) <= tol
+    assert near.reshape(n, -1)[1::2].all()
+
+
 def test_bad_row_starts_are_flagged(ops):
     c = Case([70, 40, 30], [2, 2, 2], 2, 1, 64, 16, seed=14)
     clean = run(ops, c, torch.float32)[0]
