@@ -44,6 +44,16 @@
 // Rows go through the softmax eight at a time in a loop, and scores are read
 // from tensor memory twice rather than kept: unrolled over 32 rows, the roles'
 // code did not fit the instruction caches, and that was the largest stall.
+//   Bound: HBM for few query rows, the softmax groups for many (a tile of 32
+// rows of f32 takes a group about 7100 cycles: 1500 for the maxima, 3500 for
+// weights, planes and sums, the rest waits and barriers; of eight rows of bf16,
+// 2400).  Measured in a graph, 8 cache heads of 128: 64 requests of 4.2 k tokens
+// on average, eight bf16 rows a head, 99.3 us (84% of the copy rate); one of
+// 131072 tokens 53 us (75%: start-up and join take the rest); 16 of 8.4 k with
+// 4..32 f32 rows a head 119 us (35%).
+//   Measured slower: 16 or 32 rows at a time (up to 141 us for the last), a third
+// softmax group (140 us), the planes as a loop over their weights (123 us),
+// redux.sync for the maxima, both products of a tile from one issuer in order.
 //   Every wait is bounded; a timeout raises a CTA-wide flag, the outputs become
 // NaN, the join still counts, copies and MMAs in flight are waited for, and the
 // status word records it.
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     __shared__ __align__(8) uint64_t k_full[SK], k_free[SK], v_full[SV], v_free[SV], sc_full[kAtScaleDeep];
     __shared__ __align__(8) uint64_t s_full[kAtDeep], s_free[kAtDeep], p_full[kAtDeep], o_full[kAtDeep], o_free[kAtDeep];
     __shared__ __align__(8) uint64_t q_full[2], ml_full[2], ml_free[2], mma_done[2];
-    __shared__ float sc[kAtScaleDeep][2][8];                       // k and v scales of a tile's blocks
+    __shared__ __align__(16) float sc[kAtScaleDeep][2][8];                       // k and v scales of a tile's blocks
     __shared__ __align__(16) float s_qs[2][R];          // per query row: 2^-e x scale x log2 e (NaN: the row is not finite)
     __shared__ __align__(16) int s_lim[2][R];           // last position each row sees
     __shared__ __align__(16) float s_wmax[2][4][R];     // per softmax group: its warps' maxima over the tile
@@ -842,9 +852,20 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const uint32_t bp = static_cast<uint32_t>(it / kAtDeep) & 1u;
                     const int b = static_cast<int>(it & (kAtDeep - 1));
                     const int cs = static_cast<int>(it & (kAtScaleDeep - 1));  // the scales' slot
-                    ok = ok && at_warp_wait(smem_addr(&sc_full[cs]), static_cast<uint32_t>(it / kAtScaleDeep) & 1u, &s_abort) &&
-                         at_warp_wait(smem_addr(&s_full[b]), bp, &s_abort);
                     const int pos = j * kAtTile + tg;
+                    ok = ok && at_warp_wait(smem_addr(&sc_full[cs]), static_cast<uint32_t>(it / kAtScaleDeep) & 1u, &s_abort);
+                    // The tile's value scales, relative to the power of two under the largest.
+                    const int blocks = (min(w.q.len - j * kAtTile, kAtTile) - 1) >> a.block_log2;  // the last one's number
+                    float vs[8], vtop = 0.f;
+                    at_lds8(sc[cs][1], vs);
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        const float x = fabsf(vs[p]);
+                        if (p <= blocks && x < INFINITY) vtop = fmaxf(vtop, x);
+                    }
+                    const int ve = max(__float_as_int(vtop) >> 23, 8);  // biased exponent; 2^-119 and below count as 2^-119
+                    const float vscale = sc[cs][1][tg >> a.block_log2] * __int_as_float(ve == 254 ? 0x00400000 : (254 - ve) << 23) * (1 << kAtPeakLog2);
+                    ok = ok && at_warp_wait(smem_addr(&s_full[b]), bp, &s_abort);
                     const bool edge = (j + 1) * kAtTile - 1 > seen_by_all;  // some row does not see the whole tile
                     const float ks = sc[cs][0][tg >> a.block_log2];
                     // Scores of rows c .. c + 7, in base 2; what a row does not see is -inf.
@@ -881,26 +902,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         if (owner) s_wmax[g][wg][c + own] = top;
                     }
                     if constexpr (R == 8) release();
-                    // The tile's value scales, relative to the power of two under the largest.
-                    float vtop = 0.f;
-#pragma unroll
-                    for (int p = 0; p < 8; ++p) {
-                        const float x = fabsf(sc[cs][1][p]);
-                        if (p < (kAtTile >> a.block_log2) && (j * kAtTile + (p << a.block_log2)) < w.q.len && x < INFINITY) vtop = fmaxf(vtop, x);
-                    }
-                    const int ve = max(__float_as_int(vtop) >> 23, 8);  // biased exponent; 2^-119 and below count as 2^-119
-                    const float vs = sc[cs][1][tg >> a.block_log2] * __int_as_float(ve == 254 ? 0x00400000 : (254 - ve) << 23) * (1 << kAtPeakLog2);
+                    // One warp waits until the output sums have read what the tile kAtDeep ago left in this slot, another until
+                    // the second MMA has read its weights.
+                    if (wg == 1 && it >= kAtDeep) ok = at_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort) && ok;
                     at_bar(bar);
+                    if (PD < kAtDeep && wg == 2 && it >= PD)
+                        ok = at_wait(smem_addr(&o_full[(it - PD) & (kAtDeep - 1)]), static_cast<uint32_t>((it - PD) / kAtDeep) & 1u, &s_abort) && ok;
                     if (tg < rows) {
                         const float m = fmaxf(fmaxf(s_wmax[g][0][tg], s_wmax[g][1][tg]), fmaxf(s_wmax[g][2][tg], s_wmax[g][3][tg]));
                         const float tref = fmaxf(m, kAtNoRef), now = fmaxf(ref, tref);
                         s_lf[g][tg] = at_exp2(tref - now);
                         s_lc[g][tg] = at_exp2(ref - now);
                         ref = now;
-                        // The output sums have read what the tile kAtDeep ago left here, and the second MMA its weights.
-                        if (it >= kAtDeep) ok = at_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort) && ok;
-                        if (PD < kAtDeep && it >= PD)
-                            ok = at_wait(smem_addr(&o_full[(it - PD) & (kAtDeep - 1)]), static_cast<uint32_t>((it - PD) / kAtDeep) & 1u, &s_abort) && ok;
                         s_tref[b][tg] = tref;
                         if (tg == 0) s_vf[b] = __int_as_float((ve - kAtPeakLog2) << 23);
                     }
@@ -918,7 +931,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
                             s[r] = at_exp2(s[r] - tref[r]);
-                            t[r] = s[r] * vs;
+                            t[r] = s[r] * vscale;
                         }
                         if (edge) {
 #pragma unroll
