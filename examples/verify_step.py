@@ -126,9 +126,10 @@ def main(seed: int = 0) -> dict:
         n = 0
         while first + n < end - 1 and accepted[first + n]:
             n += 1
+        draft = (f"log p of the first draft {float(scores.logprob[first]):.3f} (rank {int(scores.rank[first])}), "
+                 if end - first > 1 else "")
         print(f"request {s}: {end - first - 1} drafts, {n} accepted, next token {int(tokens[first + n])}, "
-              f"log p of the first draft {float(scores.logprob[first]):.3f} (rank {int(scores.rank[first])}), "
-              f"entropy {float(scores.entropy[first]):.3f}")
+              f"{draft}entropy {float(scores.entropy[first]):.3f}")
         first = end
     if ops.fp8blk_device_status(clear=True):
         raise RuntimeError("a kernel reported a problem")

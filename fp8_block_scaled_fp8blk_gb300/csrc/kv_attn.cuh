@@ -51,7 +51,7 @@
 // on average, eight bf16 rows a head, 99.3 us (84% of the copy rate); one of
 // 131072 tokens 53 us (75%: start-up and join take the rest); 16 of 8.4 k with
 // 4..32 f32 rows a head 119 us (35%).
-//   Measured slower: 16 or 32 rows at a time (up to 141 us for the last), a third
+//   Measured slower (the last case): 16 rows at a time (141 us), a third
 // softmax group (140 us), the planes as a loop over their weights (123 us),
 // redux.sync for the maxima, both products of a tile from one issuer in order.
 //   Every wait is bounded; a timeout raises a CTA-wide flag, the outputs become
