@@ -34,7 +34,9 @@
 // Work: all (request, cache head, row group, tile) quadruples in one list, cut
 // into one contiguous range per CTA, so ragged lengths balance.  A unit
 // (request, head, row group) that lies across CTAs is joined by the CTA that
-// finishes last, over the partial sums in CTA order (deterministic).
+// finishes last, over the partial sums in CTA order (deterministic); one in more
+// than 24 parts in two steps, eights first (one request of 53580 tokens, one
+// cache head of 256, in 140 parts: 36 us, in one step 103).
 //
 // Roles (640 threads, one CTA per SM): warps 0-3 and 4-7 softmax of even and odd
 // tiles (TMEM lane = token), warps 8-11 output sums (TMEM lane = element of
@@ -45,15 +47,16 @@
 // from tensor memory twice rather than kept: unrolled over 32 rows, the roles'
 // code did not fit the instruction caches, and that was the largest stall.
 //   Bound: HBM for few query rows, the softmax groups for many (a tile of 32
-// rows of f32 takes a group about 7100 cycles: 1500 for the maxima, 3500 for
+// rows of f32 takes a group about 7000 cycles: 1500 for the maxima, 3500 for
 // weights, planes and sums, the rest waits and barriers; of eight rows of bf16,
 // 2400).  Measured in a graph, 8 cache heads of 128: 64 requests of 4.2 k tokens
-// on average, eight bf16 rows a head, 99.3 us (84% of the copy rate); one of
-// 131072 tokens 53 us (75%: start-up and join take the rest); 16 of 8.4 k with
-// 4..32 f32 rows a head 119 us (35%).
-//   Measured slower (the last case): 16 rows at a time (141 us), a third
-// softmax group (140 us), the planes as a loop over their weights (123 us),
-// redux.sync for the maxima, both products of a tile from one issuer in order.
+// on average, eight bf16 rows a head, 101 us (82% of the copy rate); one of
+// 131072 tokens 54 us (74%: start-up and join take the rest); 16 of 8.4 k with
+// 4..32 f32 rows a head 107 us (39%).
+//   Measured slower (the last case, then at 119 us): 16 rows at a time (141), a
+// third softmax group (140), the planes as a loop over their weights (123);
+// redux.sync for the maxima, both products of a tile from one issuer in order,
+// the join as a function of its own (every case by 2 to 7 us).
 //   Every wait is bounded; a timeout raises a CTA-wide flag, the outputs become
 // NaN, the join still counts, copies and MMAs in flight are waited for, and the
 // status word records it.
@@ -69,7 +72,9 @@ constexpr int kAtTile = 128;            // tokens per tile
 constexpr int kAtDeep = 4;              // tiles between the first product and the sums: scores, weights and products
 constexpr int kAtScaleDeep = 16;        // tiles whose scales are held: more than K's ring and the scores can be ahead of the softmax
 constexpr int kAtMaxGrid = 256;         // bound on CTAs: arrival counters and partial sums in the workspace
-constexpr size_t kAtHeaderBytes = kAtMaxGrid * sizeof(uint32_t);
+constexpr int kAtJoin = 24;             // parts of a unit that one CTA joins by itself; more are joined in two steps,
+constexpr int kAtFanLog2 = 3;           // eights of them first
+constexpr size_t kAtHeaderBytes = 2 * kAtMaxGrid * sizeof(uint32_t);
 constexpr float kAtNoRef = -3.0e38f;    // maximum of a row that has seen nothing
 constexpr int kAtPeakLog2 = 7;          // a tile's largest weight in the planes is in [2^7, 2^8) (e4m3 ends at 448)
 
@@ -79,7 +84,7 @@ struct AttnArgs {
     float *lse;                       // or null
     const float *k_scales, *v_scales;
     const int32_t *table, *seq_lens, *q_starts;
-    uint32_t *counters;               // [kAtMaxGrid], zero between calls
+    uint32_t *counters;               // [2][kAtMaxGrid] of the joins' first and second steps, zero between calls
     float *partials;                  // [grid][2][R x (ND * 128) sums | R references | R denominators]
     unsigned int *status;
     int64_t q_stride, out_stride, n_blocks;
@@ -1142,46 +1147,66 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     // before it.
                     const int b0 = split.owner(unit_begin + 2 * w.q.weight - 1);
                     const int parts = split.owner(unit_begin + (w.q.tiles + 1) * w.q.weight - 1) - b0 + 1;
-                    at_bar(3);
-                    if (dt == 0) {  // the barrier and this release order every thread's sums before the count
-                        uint32_t old;
-                        asm volatile("fence.acq_rel.gpu;\n\tatom.inc.relaxed.gpu.global.u32 %0, [%1], %2;\n\tfence.acq_rel.gpu;"
-                                     : "=r"(old)
-                                     : "l"(a.counters + b0), "r"(static_cast<uint32_t>(parts - 1))
-                                     : "memory");
-                        s_last = old == static_cast<uint32_t>(parts - 1);
+                    // The CTA that arrives last joins the parts; of many parts, eights first, an eight's sums in place of its
+                    // first part's.  An eight of one part is joined already.  (That one lies in the unit's last CTA, which may
+                    // begin another unit and then counts that one's parts in its counter; the CTAs of the other eights' first
+                    // parts hold nothing else, or begin this unit.)
+                    auto part = [&](int p) {  // part p lies in CTA b0 + p, which holds one that begins a unit and one that does not
+                        return a.partials + (static_cast<int64_t>(b0 + p) * 2 + (p == 0)) * Sh::kPartial;
+                    };
+                    int lo = 0, shift = 0, count = parts;  // the parts lo + (p << shift), p < count
+                    uint32_t *counter = a.counters + b0;
+                    bool eights = false;
+                    if (parts > kAtJoin) {
+                        lo = (static_cast<int>(blockIdx.x) - b0) >> kAtFanLog2 << kAtFanLog2;
+                        count = min(parts - lo, 1 << kAtFanLog2);
+                        counter += lo;
+                        eights = true;
                     }
-                    at_bar(3);
-                    if (s_last) {
-                        auto part = [&](int p) {  // part p lies in CTA b0 + p, which holds one that begins a unit and one that does not
-                            return a.partials + (static_cast<int64_t>(b0 + p) * 2 + (p == 0)) * Sh::kPartial;
-                        };
+#pragma unroll 1
+                    while (true) {
+                        if (eights && count == 1) {
+                            lo = 0;
+                            shift = kAtFanLog2;
+                            count = (parts + (1 << kAtFanLog2) - 1) >> kAtFanLog2;
+                            counter = a.counters + kAtMaxGrid + b0;
+                            eights = false;
+                        }
+                        at_bar(3);
+                        if (dt == 0) {  // the barrier and this release order every thread's sums before the count
+                            uint32_t old;
+                            asm volatile("fence.acq_rel.gpu;\n\tatom.inc.relaxed.gpu.global.u32 %0, [%1], %2;\n\tfence.acq_rel.gpu;"
+                                         : "=r"(old)
+                                         : "l"(counter), "r"(static_cast<uint32_t>(count - 1))
+                                         : "memory");
+                            s_last = old == static_cast<uint32_t>(count - 1);
+                        }
+                        at_bar(3);
+                        if (!s_last) break;
                         // Maxima and denominators: 128 / R threads a row.  (Loops, not unrolled code: this runs once or
                         // twice a launch, and fetching its instructions would take longer than the loads.)
                         constexpr int L = 128 / R;
-                        {
-                            const int r = dt / L;
-                            float m = kAtNoRef, d = 0.f;
+                        const int row = dt / L;
+                        float m = kAtNoRef, d = 0.f;
 #pragma unroll 4
-                            for (int p = dt % L; p < parts; p += L) {
-                                const float *src = part(p) + R * ND * 128 + r;
-                                const float pm = __ldcg(src), pl = __ldcg(src + R), top = fmaxf(m, pm);
-                                d = d * at_exp2(m - top) + pl * at_exp2(pm - top);
-                                m = top;
-                            }
+                        for (int p = dt % L; p < count; p += L) {
+                            const float *src = part(lo + (p << shift)) + R * ND * 128 + row;
+                            const float pm = __ldcg(src), pl = __ldcg(src + R), top = fmaxf(m, pm);
+                            d = d * at_exp2(m - top) + pl * at_exp2(pm - top);
+                            m = top;
+                        }
 #pragma unroll
-                            for (int x = L / 2; x; x >>= 1) {
-                                const float om = __shfl_xor_sync(0xFFFFFFFFu, m, x), od = __shfl_xor_sync(0xFFFFFFFFu, d, x), top = fmaxf(m, om);
-                                // The lower lane's share first on both sides: one order, one result.
-                                const float mine = d * at_exp2(m - top), other = od * at_exp2(om - top);
-                                d = dt & x ? other + mine : mine + other;
-                                m = top;
-                            }
-                            if (dt % L == 0) {
-                                s_corr[r] = m;
-                                s_inv[r] = d == 0.f ? 0.f : 1.f / d;
-                                if (a.lse && r < valid) a.lse[lse_at(r)] = d == 0.f ? -INFINITY : (m + log2f(d)) * 0.6931471805599453f;
-                            }
+                        for (int x = L / 2; x; x >>= 1) {
+                            const float om = __shfl_xor_sync(0xFFFFFFFFu, m, x), od = __shfl_xor_sync(0xFFFFFFFFu, d, x), top = fmaxf(m, om);
+                            // The lower lane's share first on both sides: one order, one result.
+                            const float mine = d * at_exp2(m - top), other = od * at_exp2(om - top);
+                            d = dt & x ? other + mine : mine + other;
+                            m = top;
+                        }
+                        if (dt % L == 0) {
+                            s_corr[row] = m;
+                            s_inv[row] = d == 0.f ? 0.f : 1.f / d;
+                            if (!eights && a.lse && row < valid) a.lse[lse_at(row)] = d == 0.f ? -INFINITY : (m + log2f(d)) * 0.6931471805599453f;
                         }
                         at_bar(3);
                         // Sums: a thread takes four elements of every 128th quadruple, kItems at a time over all parts.
@@ -1192,8 +1217,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                             for (int k = 0; k < kItems; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll kAhead
-                            for (int p = 0; p < parts; ++p) {
-                                const float *src = part(p);
+                            for (int p = 0; p < count; ++p) {
+                                const float *src = part(lo + (p << shift));
 #pragma unroll
                                 for (int k = 0; k < kItems; ++k) {
                                     const int i = (k0 + k) * 128 + dt, r = i / (ND * 32);
@@ -1207,12 +1232,22 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                             }
 #pragma unroll
                             for (int k = 0; k < kItems; ++k) {
-                                const int i = (k0 + k) * 128 + dt, r = i / (ND * 32), d = (i & (ND * 32 - 1)) * 4;
-                                const float f = s_inv[r];
-                                if (r < valid && d < a.head_dim)
-                                    at_store4(out + out_row(r) + d, make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f));
+                                const int i = (k0 + k) * 128 + dt, r = i / (ND * 32), e = (i & (ND * 32 - 1)) * 4;
+                                if (eights) {
+                                    __stcg(reinterpret_cast<float4 *>(part(lo)) + i, o[k]);  // this thread alone reads it above
+                                } else if (r < valid && e < a.head_dim) {
+                                    const float f = s_inv[r];
+                                    at_store4(out + out_row(r) + e, make_float4(o[k].x * f, o[k].y * f, o[k].z * f, o[k].w * f));
+                                }
                             }
                         }
+                        if (!eights) break;
+                        at_bar(3);  // every thread has read the parts' maxima
+                        if (dt % L == 0) {
+                            __stcg(part(lo) + R * ND * 128 + row, m);
+                            __stcg(part(lo) + R * ND * 128 + R + row, d);
+                        }
+                        count = 1;  // its eight is joined
                     }
                 }
                 __syncwarp();

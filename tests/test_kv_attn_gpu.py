@@ -137,6 +137,25 @@ def test_one_long_request(ops, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens,rows,heads,kv,dim,block", [
+    ([20001], [1], 2, 1, 64, 128),       # one unit in as many parts as there are CTAs
+    ([9000, 12000, 7], [8, 5, 1], 4, 1, 128, 64),
+    ([3500, 3600, 3700, 3800], [2] * 4, 6, 1, 256, 32),
+    ([6000] * 3, [8] * 3, 8, 1, 64, 128),  # two row groups, parts of 32 rows
+])
+def test_units_in_many_parts(ops, dtype, lens, rows, heads, kv, dim, block):
+    """Joined in two steps; the counters are back at zero for the next call."""
+    c = Case(lens, rows, heads, kv, dim, block, seed=21)
+    check(ops, c, dtype)
+    dev, q = c.dev(), to_dev(c.q).to(dtype)
+    ws = ops.kv_attn_workspace(len(lens), max(rows), heads, kv, dim, DEV)
+    first = ops.fp8blk_kv_attn(q, *dev, max(rows), c.scale, ws)
+    head = ws[:2048].clone()
+    again = ops.fp8blk_kv_attn(q, *dev, max(rows), c.scale, ws)
+    assert torch.equal(first, again) and int(head.count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_rows_that_see_nothing(ops, dtype):
     """Requests with fewer tokens than rows, with none, and with no row at all."""
     check(ops, Case([3, 0, 200, 0, 1, 17], [5, 2, 0, 0, 1, 8], 6, 3, 48, 16, seed=4), dtype)
