@@ -56,7 +56,7 @@
 //   Measured slower (the last case, then at 119 us): 16 rows at a time (141), a
 // third softmax group (140), the planes as a loop over their weights (123);
 // redux.sync for the maxima, both products of a tile from one issuer in order,
-// the join as a function of its own (every case by 2 to 7 us).
+// the join as a function of its own (most cases by 1 to 7 us).
 //   Every wait is bounded; a timeout raises a CTA-wide flag, the outputs become
 // NaN, the join still counts, copies and MMAs in flight are waited for, and the
 // status word records it.
