@@ -151,8 +151,9 @@ struct LpSlice {
 // too many values tie with the bound are selected one by one.
 //   Bound: HBM (4 or 2 bytes a logit) for many rows of f32, at about 9
 // instructions a logit; instructions for bf16; the chain of joins for few rows.
-// Measured, top 20 and 131072 logits: 2048 rows of f32 177 us (91% of the copy
-// rate; without the top 100%), of bf16 147 us (54%); top 5, 8 rows of f32 7.1 us.
+// Measured, top 20 and 131072 logits: 2048 rows of f32 187 us (86% of the copy
+// rate; without the top about 100%), of bf16 148 us (54%); top 5, 8 rows of f32
+// 7.4 us.
 // (A resident grid that asks for the next row's words before it joins a row,
 // clusters of 16, and words staged by asynchronous copies, twice as many in
 // flight, each measured slower.)
@@ -504,7 +505,7 @@ extern "C" int fp8blk_token_logprobs(const void *logits, int dtype, const int32_
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
     // From three rows per SM on, a narrow CTA per row, four of them resident: they take turns at the end of a row, when
-    // nothing streams (4000 x 32000 f32: 112 us, with wide CTAs 139; 2048 x 131072: 177 and 187).  With fewer rows, wide
+    // nothing streams (4000 x 32000 f32: 112 us, with wide CTAs 139; 2048 x 131072: 4% less).  With fewer rows, wide
     // CTAs and as many a row as fit at once, with slices of 8 KiB at least (380 x 131072 f32: 46 us, narrow 55).
     const int64_t bytes = vocab * es, slots = kLpResident / kLpWide * static_cast<int64_t>(dev.sms);
     const bool narrow = n_rows >= 3 * static_cast<int64_t>(dev.sms);
