@@ -24,12 +24,15 @@
 // summed from the f32 weights.
 //
 // p is relative to the maximum over its own tile and row, not to the running
-// one, and p s_v to the tile's largest |s_v|, times 2^8: every tile's weights
-// fill e4m3's range, so what a weight loses is 2^-18 (bf16) or 2^-26 (f32) of
-// its own tile's largest at worst, and a long tail of small weights keeps its
-// share.  Each tile's product is read back and added to f32 sums in registers
-// with its factor 2^(m_r - running maximum) max|s_v| 2^-8, so nothing in
-// tensor memory is ever rescaled.
+// one, and p s_v is brought by a power of two of the row's own, 2^-k, under
+// the row's largest p |s_v| of the tile: every row's weights fill e4m3's range,
+// whatever the scales of blocks that the row does not attend to, so what a
+// weight loses is 2^-16 (bf16) or 2^-24 (f32) of its own row's largest in the
+// tile at worst, and a long tail of small weights keeps its share.  (k comes
+// from the maxima of sixteen tokens, which share a scale, and their scales'
+// exponents, so it costs no second maximum.)  Each tile's product is read back
+// and added to f32 sums in registers with its factor 2^(m_r - running maximum)
+// 2^k, so nothing in tensor memory is ever rescaled.
 //
 // Work: all (request, cache head, row group, tile) quadruples in one list, cut
 // into one contiguous range per CTA, so ragged lengths balance.  A unit
@@ -76,7 +79,10 @@ constexpr int kAtJoin = 24;             // parts of a unit that one CTA joins by
 constexpr int kAtFanLog2 = 3;           // eights of them first
 constexpr size_t kAtHeaderBytes = 2 * kAtMaxGrid * sizeof(uint32_t);
 constexpr float kAtNoRef = -3.0e38f;    // maximum of a row that has seen nothing
-constexpr int kAtPeakLog2 = 7;          // a tile's largest weight in the planes is in [2^7, 2^8) (e4m3 ends at 448)
+constexpr int kAtPeakLog2 = 7;          // a row's largest weight of a tile in the planes is in [2^6, 2^8) (e4m3 ends at 448)
+constexpr int kAtSpread = 120;          // a row's weights are lifted by up to 2^120: value scales further apart in a tile
+                                        // than that lose bits of what lies under the smaller one
+constexpr int kAtMinScale = -119;       // value scales below 2^-119 count as 2^-119 (with a smaller factor)
 
 struct AttnArgs {
     const void *q;
@@ -107,7 +113,7 @@ struct AttnShape {
     static constexpr int kPBytes = kSteps * kPStep;           // weight planes of a tile
     static constexpr int kPDeep = N == 64 || ND == 2 ? 2 : kAtDeep;  // tiles whose weights are held
     static constexpr int kFixed = 1024 + 2 * kQBytes + kPDeep * kPBytes;
-    static constexpr int kRoom = (227 - 9) * 1024;            // dynamic shared memory beside the static arrays
+    static constexpr int kRoom = (227 - 10) * 1024;           // dynamic shared memory beside the static arrays
     static constexpr int kTiles = (kRoom - kFixed) / kTileBytes;
     // V's tiles are held longer than K's (until the weights are there).
     static constexpr int kStagesV = (kTiles + 1) / 2 > 6 ? 6 : (kTiles + 1) / 2;
@@ -237,45 +243,30 @@ __device__ __forceinline__ bool at_bar_or(int id, bool v) {
     return r != 0;
 }
 
-// Maximum of each of R values over the warp (NaN ignored), as a butterfly that
-// halves the values a lane holds at each step: 31 shuffles for 32 values, 9 for
-// 8 (one redux.sync per value measured about 50 cycles each, one after another).
-// Lane l ends with value at_owned<R>(l).
-template <int R>
-__device__ __forceinline__ int at_owned(int lane) {
-    int r = 0;
+// One of eight values, folded by `op` over the sixteen lanes of each half of the
+// warp, as a butterfly that halves the values a lane holds at each step: eight
+// shuffles (one redux.sync per value measured about 50 cycles each, one after
+// another).  Lane l ends with value at_owned(l) of its half.
+__device__ __forceinline__ int at_owned(int lane) { return (lane & 8 ? 4 : 0) + (lane & 4 ? 2 : 0) + (lane & 2 ? 1 : 0); }
+template <typename F>
+__device__ __forceinline__ float at_butterfly(const float (&x)[8], int lane, F op) {
+    float v[4];
 #pragma unroll
-    for (int h = 16, n = R; h; h >>= 1)
-        if (n > 1) {
-            n >>= 1;
-            if (lane & h) r += n;
-        }
-    return r;
-}
-template <int R, typename F>
-__device__ __forceinline__ float at_butterfly(const float (&x)[R], int lane, F op) {
-    static_assert(R == 8 || R == 16 || R == 32, "values");
-    float v[R / 2];
-#pragma unroll
-    for (int i = 0; i < R / 2; ++i) {
-        const bool up = lane & 16;
-        v[i] = op(up ? x[i + R / 2] : x[i], __shfl_xor_sync(0xFFFFFFFFu, up ? x[i] : x[i + R / 2], 16));
+    for (int i = 0; i < 4; ++i) {
+        const bool up = lane & 8;
+        v[i] = op(up ? x[i + 4] : x[i], __shfl_xor_sync(0xFFFFFFFFu, up ? x[i] : x[i + 4], 8));
     }
 #pragma unroll
-    for (int h = 8, n = R / 4; h; h >>= 1, n >>= 1) {
-        if (n >= 1) {
-            const bool up = lane & h;
+    for (int h = 4, n = 2; n; h >>= 1, n >>= 1) {
+        const bool up = lane & h;
 #pragma unroll
-            for (int i = 0; i < R / 4; ++i)
-                if (i < n) {
-                    const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
-                    v[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, h));
-                }
-        } else {
-            v[0] = op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], h));
-        }
+        for (int i = 0; i < 2; ++i)
+            if (i < n) {
+                const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                v[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, h));
+            }
     }
-    return v[0];
+    return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
 }
 
 // One request as the kernel takes it.
@@ -463,9 +454,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     __shared__ __align__(16) float sc[kAtScaleDeep][2][8];                       // k and v scales of a tile's blocks
     __shared__ __align__(16) float s_qs[2][R];          // per query row: 2^-e x scale x log2 e (NaN: the row is not finite)
     __shared__ __align__(16) int s_lim[2][R];           // last position each row sees
-    __shared__ __align__(16) float s_wmax[2][4][R];     // per softmax group: its warps' maxima over the tile
+    __shared__ __align__(16) float s_wmax[2][8][R];     // per softmax group: maxima over sixteen tokens of the tile
+    __shared__ __align__(16) float s_ve[2][8];          // ... and the exponents of their value scales
     __shared__ __align__(16) float s_tref[kAtDeep][R], s_lf[2][R], s_lc[2][R];  // tile maximum; factors into and of the group's denominator
-    __shared__ float s_vf[kAtDeep];                           // factor of the tile's product from its value scales
+    __shared__ __align__(16) float s_lift[kAtDeep][R];  // per row: 2^(peak + the tile's top value scale's exponent - k)
+    __shared__ uint32_t s_top[kAtDeep];                 // less a lift's bits: the bits of that row's 2^(k - peak)
     __shared__ __align__(16) float s_corr[R], s_of[R];  // output sums: factor of the sums so far, and of the tile's product
     __shared__ float s_l[2][8][R], s_mref[2][2][R], s_inv[R];
     __shared__ int s_vnan[2][ND * 128];                 // first position whose value code is NaN, per element
@@ -838,8 +831,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                      (iu < 2 || at_warp_wait(smem_addr(&ml_free[ub]), uph ^ 1u, &s_abort));
                 float ref = kAtNoRef;  // running maximum of row `tg` (threads below R)
                 float *den = s_l[ub][warp];  // this warp's denominators; lane l looks after its own of every eight rows
-                const int own = at_owned<8>(lane);
-                const bool owner = (lane & 3) == 0;
+                const int own = at_owned(lane);
+                const bool owner = (lane & 17) == 0;
                 if (owner) {
 #pragma unroll
                     for (int c = 0; c < R; c += 8) den[c + own] = 0.f;
@@ -859,7 +852,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const int cs = static_cast<int>(it & (kAtScaleDeep - 1));  // the scales' slot
                     const int pos = j * kAtTile + tg;
                     ok = ok && at_warp_wait(smem_addr(&sc_full[cs]), static_cast<uint32_t>(it / kAtScaleDeep) & 1u, &s_abort);
-                    // The tile's value scales, relative to the power of two under the largest.
+                    // This token's value scale, relative to the power of two under the tile's largest.
                     const int blocks = (min(w.q.len - j * kAtTile, kAtTile) - 1) >> a.block_log2;  // the last one's number
                     float vs[8], vtop = 0.f;
                     at_lds8(sc[cs][1], vs);
@@ -868,8 +861,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         const float x = fabsf(vs[p]);
                         if (p <= blocks && x < INFINITY) vtop = fmaxf(vtop, x);
                     }
-                    const int ve = max(__float_as_int(vtop) >> 23, 8);  // biased exponent; 2^-119 and below count as 2^-119
-                    const float vscale = sc[cs][1][tg >> a.block_log2] * __int_as_float(ve == 254 ? 0x00400000 : (254 - ve) << 23) * (1 << kAtPeakLog2);
+                    const int ve = max(__float_as_int(vtop) >> 23, 127 + kAtMinScale);  // biased exponent
+                    const float vscale = sc[cs][1][tg >> a.block_log2] * __int_as_float(ve == 254 ? 0x00400000 : (254 - ve) << 23);
+                    if (tg < 8) {
+                        const float x = fabsf(sc[cs][1][tg * 16 >> a.block_log2]);
+                        s_ve[g][tg] = static_cast<float>(max((__float_as_int(x) >> 23) - 127, kAtMinScale));
+                    }
                     ok = ok && at_warp_wait(smem_addr(&s_full[b]), bp, &s_abort);
                     const bool edge = (j + 1) * kAtTile - 1 > seen_by_all;  // some row does not see the whole tile
                     const float ks = sc[cs][0][tg >> a.block_log2];
@@ -899,12 +896,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     };
                     t8_fence_after();
                     float s[8];
-                    // Each row's maximum over the tile.
+                    // Each row's maxima over sixteen tokens.
 #pragma unroll 1
                     for (int c = 0; c < rows; c += 8) {
                         scores(c, s);
-                        const float top = at_butterfly<8>(s, lane, [](float x, float y) { return fmaxf(x, y); });
-                        if (owner) s_wmax[g][wg][c + own] = top;
+                        const float top = at_butterfly(s, lane, [](float x, float y) { return fmaxf(x, y); });
+                        if ((lane & 1) == 0) s_wmax[g][2 * wg + (lane >> 4)][c + own] = top;
                     }
                     if constexpr (R == 8) release();
                     // One warp waits until the output sums have read what the tile kAtDeep ago left in this slot, another until
@@ -914,13 +911,23 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     if (PD < kAtDeep && wg == 2 && it >= PD)
                         ok = at_wait(smem_addr(&o_full[(it - PD) & (kAtDeep - 1)]), static_cast<uint32_t>((it - PD) / kAtDeep) & 1u, &s_abort) && ok;
                     if (tg < rows) {
-                        const float m = fmaxf(fmaxf(s_wmax[g][0][tg], s_wmax[g][1][tg]), fmaxf(s_wmax[g][2][tg], s_wmax[g][3][tg]));
-                        const float tref = fmaxf(m, kAtNoRef), now = fmaxf(ref, tref);
+                        float exps[8], tref = kAtNoRef, most = -INFINITY;
+                        at_lds8(s_ve[g], exps);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const float part = s_wmax[g][x][tg];
+                            tref = fmaxf(tref, part);
+                            most = fmaxf(most, part + exps[x]);
+                        }
+                        const float now = fmaxf(ref, tref);
+                        // k: the largest p |s_v| is below 2^(k + 1).
+                        const int k = min(max(__float2int_ru(most - tref), max(ve - 127 - kAtSpread, kAtMinScale)), ve - 127);
+                        s_lift[b][tg] = __int_as_float((kAtPeakLog2 + ve - k) << 23);
                         s_lf[g][tg] = at_exp2(tref - now);
                         s_lc[g][tg] = at_exp2(ref - now);
                         ref = now;
                         s_tref[b][tg] = tref;
-                        if (tg == 0) s_vf[b] = __int_as_float((ve - kAtPeakLog2) << 23);
+                        if (tg == 0) s_top[b] = static_cast<uint32_t>(ve + 127) << 23;
                     }
                     at_bar(bar);
                     ok = __all_sync(0xFFFFFFFFu, ok);
@@ -934,10 +941,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         float t[8], tref[8];
                         at_lds8(s_tref[b] + c, tref);
 #pragma unroll
-                        for (int r = 0; r < 8; ++r) {
-                            s[r] = at_exp2(s[r] - tref[r]);
-                            t[r] = s[r] * vscale;
-                        }
+                        for (int r = 0; r < 8; ++r) s[r] = at_exp2(s[r] - tref[r]);
+                        at_lds8(s_lift[b] + c, t);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) t[r] = s[r] * t[r] * vscale;
                         if (edge) {
 #pragma unroll
                             for (int r = 0; r < 8; ++r)
@@ -950,7 +957,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                             word.y = at_plane<PL, G>(p, t[4], t[5], t[6], t[7]);
                             *reinterpret_cast<uint2 *>(pb + p % Sh::kSteps * Sh::kPStep + ((p / Sh::kSteps * R + c) ^ turn)) = word;
                         }
-                        const float sum = at_butterfly<8>(s, lane, [](float x, float y) { return x + y; });
+                        float sum = at_butterfly(s, lane, [](float x, float y) { return x + y; });
+                        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
                         if (owner) den[c + own] = fmaf(den[c + own], s_lc[g][c + own], sum * s_lf[g][c + own]);
                     }
                     if constexpr (R > 8) release();
@@ -1048,7 +1056,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         const float tref = s_tref[b][dt], now = fmaxf(ref, tref);
                         raised = now > ref;
                         s_corr[dt] = at_exp2(ref - now);
-                        s_of[dt] = at_exp2(tref - now) * s_vf[b];
+                        s_of[dt] = at_exp2(tref - now) * __uint_as_float(s_top[b] - __float_as_uint(s_lift[b][dt]));
                         ref = now;
                     }
                     const bool moved = at_bar_or(3, raised);

@@ -1,0 +1,58 @@
+"""GPU tests of fp8blk_kv_attn where the value scales of one tile of 128 tokens lie far apart.
+
+The bound is check's (test_kv_attn_gpu.py).  It is relative to sum_t p_t |v_t| of the row itself, so a block that the row
+does not attend to may not cost it anything, whatever that block's scale."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import _step_ref as ref
+from test_kv_attn_gpu import Case, check, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ops():
+    from fp8_block_scaled_fp8blk_gb300 import ops as o
+    yield o
+    assert o.fp8blk_device_status(clear=True) == 0
+
+
+def quiet_block(e, block, heads, rows, dim, seed):
+    """In each tile one block has value scales 2^-e of the others' and all of the rows' weight: its scores are the others'
+    and a gap of e ln 2 + 12, so the others keep e^-12 of the output."""
+    c = Case([300], [rows], heads, 1, dim, block, seed=seed, spread=0)
+    rng = np.random.default_rng(seed)
+    c.q = (0.5 + 0.1 * rng.standard_normal(c.q.shape)).astype(np.float32)
+    gap = e * math.log(2.0) + 12.0
+    for j, b in enumerate(c.table[0]):
+        c.vs[b] = 1.0
+        if j % (128 // block) == 1:
+            c.vs[b] = 2.0 ** -e
+            c.kc[b] = ref.e4m3_encode(64.0 * (1.0 + 0.1 * rng.standard_normal(c.kc[b].shape)))
+            c.ks[b] = gap / (64.0 * 0.5 * dim * c.scale)
+    return c
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heads,rows,dim", [(4, 2, 64), (8, 2, 64), (8, 4, 64), (16, 4, 128), (4, 2, 256), (8, 2, 192)])
+@pytest.mark.parametrize("block", [16, 32, 64])
+@pytest.mark.parametrize("e", [4, 8, 12, 16, 20, 40, 100])
+def test_weight_on_a_block_of_small_scale(ops, dtype, heads, rows, dim, block, e):
+    check(ops, quiet_block(e, block, heads, rows, dim, seed=e + block + dim), dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scale", [2.0 ** 30, 2.0 ** 100, 2.0 ** -60, 0.0])
+def test_scale_of_a_block_that_rows_do_not_see(ops, dtype, scale):
+    """Rows before a block are the same bits whatever its scale."""
+    c = Case([114], [4], 8, 2, 64, 16, seed=33, spread=0)  # rows at 110 .. 113, the last block begins at 112
+    c.vs[c.table[0]] = 1.0
+    want, lse, _ = run(ops, c, dtype)
+    c.vs[c.table[0, 7]] = scale
+    out, lse2, _ = run(ops, c, dtype)
+    assert torch.equal(out[:2], want[:2]) and torch.equal(lse2, lse)
+    check(ops, c, dtype)
