@@ -14,21 +14,22 @@
 // (all subtractions exact).  Planes of one weight add up in the same columns of
 // tensor memory (an MMA each), planes of another weight lie beside them.
 //   f32 queries and outputs: four planes of weight 1, 1, 2^-8, 2^-8; a value keeps
-//     2^-16 of itself at worst (rms 5e-7), which leaves the result at the error
-//     of an f32 computation.
-//   bf16: two planes of weight 1, 1 (eight rows: 1, 2^-4, as an MMA has 16 columns
-//     at least).  bf16's 8 bits fit two planes, so q is exact to 2^-18 of its
-//     row's largest; p keeps 2^-8 at worst (rms 5e-4), a third of the rounding
-//     of the bf16 output.
+//     2^-16 of itself (rms 5e-7) and 2^-24 of its row's largest, which leaves the
+//     result at the error of an f32 computation.
+//   bf16: two planes of weight 1, 2^-4; a value keeps 2^-8 of itself and 2^-20 of
+//     its row's largest.  bf16's 8 bits fit two planes, so q loses only the
+//     2^-21 of its row's largest; p's 2^-8 (rms 5e-4) is a third of the rounding
+//     of the bf16 output.  (Two planes of weight 1 would keep 2^-16 of the largest
+//     only, which shows in elements where the largest weight meets a small value.
+//     Four planes here: 64 requests of 8 rows 128 us instead of 103.)
 // Scores, statistics and output sums are f32; the softmax denominator is
 // summed from the f32 weights.
 //
 // p is relative to the maximum over its own tile and row, not to the running
 // one, and p s_v is brought by a power of two of the row's own, 2^-k, under
 // the row's largest p |s_v| of the tile: every row's weights fill e4m3's range,
-// whatever the scales of blocks that the row does not attend to, so what a
-// weight loses is 2^-16 (bf16) or 2^-24 (f32) of its own row's largest in the
-// tile at worst, and a long tail of small weights keeps its share.  (k comes
+// whatever the scales of blocks that the row does not attend to, and a long
+// tail of small weights keeps its share.  (k comes
 // from the maxima of sixteen tokens, which share a scale, and their scales'
 // exponents, so it costs no second maximum.)  Each tile's product is read back
 // and added to f32 sums in registers with its factor 2^(m_r - running maximum)
@@ -103,7 +104,7 @@ __device__ float g_attn_nan = __builtin_nanf("");  // what a block outside the p
 
 template <int PL, int R, int ND>
 struct AttnShape {
-    static constexpr int kGroups = PL == 4 || R == 8 ? 2 : 1; // weights, each a group of R columns
+    static constexpr int kGroups = 2;                         // weights, each a group of R columns
     static constexpr int kSteps = PL / kGroups;               // planes of one weight, an MMA each
     static constexpr int N = kGroups * R;                     // columns of a product
     static constexpr int kTileBytes = ND * kAtTile * 128;     // K or V codes of a tile
@@ -111,7 +112,7 @@ struct AttnShape {
     static constexpr int kQBytes = ND * kSteps * kQStep;      // query planes of a unit
     static constexpr int kPStep = kAtTile * N;                // weight planes of one step
     static constexpr int kPBytes = kSteps * kPStep;           // weight planes of a tile
-    static constexpr int kPDeep = N == 64 || ND == 2 ? 2 : kAtDeep;  // tiles whose weights are held
+    static constexpr int kPDeep = (PL == 4 && N == 64) || ND == 2 ? 2 : kAtDeep;  // tiles whose weights are held
     static constexpr int kFixed = 1024 + 2 * kQBytes + kPDeep * kPBytes;
     static constexpr int kRoom = (227 - 10) * 1024;           // dynamic shared memory beside the static arrays
     static constexpr int kTiles = (kRoom - kFixed) / kTileBytes;
@@ -175,19 +176,16 @@ __device__ __forceinline__ void at_minus(uint32_t h, float &a, float &b) {
 // What is left after a plane is scaled up where the next one has another weight,
 // so that it does not end in e4m3's subnormals.  Plane p lies in step p % steps,
 // column group p / steps.
-template <int PL, int GROUPS>
-__device__ __forceinline__ float at_join(const float (&d)[GROUPS]) {
-    if constexpr (GROUPS == 1) return d[0];
-    else return fmaf(d[GROUPS - 1], PL == 2 ? 1.f / 16.f : 1.f / 256.f, d[0]);
-}
+template <int PL>
+__device__ __forceinline__ float at_join(const float (&d)[2]) { return fmaf(d[1], PL == 2 ? 1.f / 16.f : 1.f / 256.f, d[0]); }
 // The four values' plane p as a word of codes; the values become what it leaves.
-template <int PL, int GROUPS>
+template <int PL>
 __device__ __forceinline__ uint32_t at_plane(int p, float &a, float &b, float &c, float &d) {
     const uint32_t lo = t8_to_e4m3x2(a, b), hi = t8_to_e4m3x2(c, d);
     if (p + 1 < PL) {
         at_minus(at_e4m3x2_f16x2(lo), a, b);
         at_minus(at_e4m3x2_f16x2(hi), c, d);
-        if (GROUPS == 2 && p + 1 == PL / 2) {
+        if (p + 1 == PL / 2) {
             const float gain = PL == 2 ? 16.f : 256.f;
             a *= gain;
             b *= gain;
@@ -435,7 +433,7 @@ __device__ __forceinline__ void at_build_queries(const AttnArgs &a, const AttnWa
                 for (int p = 0; p < PL; ++p) {
                     const int n = p / Sh::kSteps * R + r;
                     *reinterpret_cast<uint32_t *>(dst + (h * Sh::kSteps + p % Sh::kSteps) * Sh::kQStep + at_swizzle<128>(n * 128 + k * 32 + 4 * l8)) =
-                        at_plane<PL, Sh::kGroups>(p, t0, t1, t2, t3);
+                        at_plane<PL>(p, t0, t1, t2, t3);
                 }
             }
     }
@@ -953,8 +951,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
 #pragma unroll
                         for (int p = 0; p < PL; ++p) {
                             uint2 word;
-                            word.x = at_plane<PL, G>(p, t[0], t[1], t[2], t[3]);
-                            word.y = at_plane<PL, G>(p, t[4], t[5], t[6], t[7]);
+                            word.x = at_plane<PL>(p, t[0], t[1], t[2], t[3]);
+                            word.y = at_plane<PL>(p, t[4], t[5], t[6], t[7]);
                             *reinterpret_cast<uint2 *>(pb + p % Sh::kSteps * Sh::kPStep + ((p / Sh::kSteps * R + c) ^ turn)) = word;
                         }
                         float sum = at_butterfly(s, lane, [](float x, float y) { return x + y; });

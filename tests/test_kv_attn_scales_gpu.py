@@ -46,6 +46,17 @@ def test_weight_on_a_block_of_small_scale(ops, dtype, heads, rows, dim, block, e
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("heads", [4, 16])
+def test_every_sixteen_tokens_their_own_scale(ops, dtype, heads):
+    """Rows that attend to different blocks of one tile, each of another scale."""
+    c = Case([384], [8], heads, 2, 64, 16, seed=31, spread=0)
+    rng = np.random.default_rng(32)
+    c.vs[c.table[0]] = (2.0 ** rng.integers(-45, 45, (24, 2))).astype(np.float32)
+    c.q *= 8.0
+    check(ops, c, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("scale", [2.0 ** 30, 2.0 ** 100, 2.0 ** -60, 0.0])
 def test_scale_of_a_block_that_rows_do_not_see(ops, dtype, scale):
     """Rows before a block are the same bits whatever its scale."""
