@@ -817,6 +817,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         } else if (warp < kAtOutWarp) {
             // ---------------- softmax: group g takes the tiles g, g + 2, ...; thread = token of the tile
             const int g = warp >> 2, wg = warp & 3, tg = tid & 127, bar = 1 + g;
+            const float nanf = __int_as_float(0x7FC00000);
             const uint32_t lanes = static_cast<uint32_t>(wg * 32) << 16;
             int st = 0, ub = 0;
             uint32_t ph = 0;
@@ -860,14 +861,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         if (p <= blocks && x < INFINITY) vtop = fmaxf(vtop, x);
                     }
                     const int ve = max(__float_as_int(vtop) >> 23, 127 + kAtMinScale);  // biased exponent
-                    const float vscale = sc[cs][1][tg >> a.block_log2] * __int_as_float(ve == 254 ? 0x00400000 : (254 - ve) << 23);
+                    // (A scale that is not finite counts as NaN: as a factor of codes it would saturate in the planes.)
+                    const float sv = sc[cs][1][tg >> a.block_log2], sk = sc[cs][0][tg >> a.block_log2];
+                    const float vscale = fabsf(sv) < INFINITY ? sv * __int_as_float(ve == 254 ? 0x00400000 : (254 - ve) << 23) : nanf;
+                    const float ks = fabsf(sk) < INFINITY ? sk : nanf;
                     if (tg < 8) {
                         const float x = fabsf(sc[cs][1][tg * 16 >> a.block_log2]);
                         s_ve[g][tg] = static_cast<float>(max((__float_as_int(x) >> 23) - 127, kAtMinScale));
                     }
                     ok = ok && at_warp_wait(smem_addr(&s_full[b]), bp, &s_abort);
                     const bool edge = (j + 1) * kAtTile - 1 > seen_by_all;  // some row does not see the whole tile
-                    const float ks = sc[cs][0][tg >> a.block_log2];
                     // Scores of rows c .. c + 7, in base 2; what a row does not see is -inf.
                     auto scores = [&](int c, float (&s)[8]) {
                         float d[G][8], qs[8];

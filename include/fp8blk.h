@@ -290,7 +290,8 @@ int mxfp4_expert_gemv(const uint8_t *codes, const uint8_t *scales, int n_experts
  *                       head_dim], 16-byte aligned
  *   k_scales, v_scales  device, f32 [n_blocks, kv_heads]; value = e4m3(code) *
  *                       scale.  fp8blk_kv_append writes powers of two;
- *                       fp8blk_kv_attn takes any f32.
+ *                       fp8blk_kv_attn takes any f32; one that is not finite
+ *                       counts as NaN.
  *   block_table         device, int32 [n_seqs, max_blocks]: token p of request
  *                       s is row p % block_tokens of block
  *                       block_table[s][p / block_tokens].

@@ -67,3 +67,29 @@ def test_scale_of_a_block_that_rows_do_not_see(ops, dtype, scale):
     out, lse2, _ = run(ops, c, dtype)
     assert torch.equal(out[:2], want[:2]) and torch.equal(lse2, lse)
     check(ops, c, dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("heads,block", [(4, 16), (16, 64), (16, 128)])
+def test_scales_that_are_not_finite(ops, dtype, value, heads, block):
+    """They count as NaN: the rows that see the block are NaN in that cache head, all others the same bits."""
+    c = Case([258, 40], [4, 1], heads, 2, 64, block, seed=41)  # rows at 254 .. 257; a block begins at 256
+    want, lse, _ = run(ops, c, dtype)
+    page = 256 // block
+    for scales in (c.ks, c.vs):
+        for j, first in ((0, 0), (page, 2)):                    # a block that every row sees; one that two rows see
+            b = c.table[0, j]
+            kept = scales[b, 1]
+            scales[b, 1] = value
+            out, lse2, _ = run(ops, c, dtype)
+            scales[b, 1] = kept
+            bad = out[first:4, heads // 2:]
+            assert torch.isnan(bad).all()
+            bad.copy_(want[first:4, heads // 2:])
+            assert torch.equal(out, want)
+            if scales is c.ks:
+                assert torch.isnan(lse2[first:4, heads // 2:]).all()
+                lse2[first:4, heads // 2:] = lse[first:4, heads // 2:]
+            assert torch.equal(lse2, lse)
+    assert ops.fp8blk_device_status(clear=True) == 0
