@@ -125,6 +125,7 @@ extern "C" int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, 
     a.counters = static_cast<uint32_t *>(ws);
     a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + kAtHeaderBytes);
     a.status = dev.status;
+    a.wait_limit_ns = tuning().wait_limit_ns;
     a.q_stride = q_stride;
     a.out_stride = out_stride;
     a.n_blocks = n_blocks;

@@ -61,9 +61,9 @@
 // third softmax group (140), the planes as a loop over their weights (123);
 // redux.sync for the maxima, both products of a tile from one issuer in order,
 // the join as a function of its own (most cases by 1 to 7 us).
-//   Every wait is bounded; a timeout raises a CTA-wide flag, the outputs become
-// NaN, the join still counts, copies and MMAs in flight are waited for, and the
-// status word records it.
+//   Every wait is bounded; a timeout raises a CTA-wide flag, the rows' outputs and
+// lse become NaN, the join still counts, copies and MMAs in flight are waited for,
+// and the status word records it.
 #pragma once
 
 #include "tc8_gemv.cuh"
@@ -94,6 +94,7 @@ struct AttnArgs {
     uint32_t *counters;               // [2][kAtMaxGrid] of the joins' first and second steps, zero between calls
     float *partials;                  // [grid][2][R x (ND * 128) sums | R references | R denominators]
     unsigned int *status;
+    uint64_t wait_limit_ns;           // of the roles' waits (drains keep kWaitLimitNs)
     int64_t q_stride, out_stride, n_blocks;
     int n_seqs, max_m, total_rows, kv_heads, group, head_dim, block_log2, width;
     int max_tiles;                    // a table's tiles and one more
@@ -207,24 +208,24 @@ __device__ __forceinline__ float at_exp2(float x) {
     return y;
 }
 
-// Waits of the roles in the tile loop: no suspend hint, every lane polls.  Same
-// bound and abort flag as t8_wait.
-__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, int *abort_flag) {
+// Waits of the roles in the tile loop: no suspend hint, every lane polls.  For at
+// most limit_ns, or until another role has raised the abort flag.
+__device__ __forceinline__ bool at_wait(uint32_t bar, uint32_t parity, int *abort_flag, uint64_t limit_ns) {
     if (mbar_try_wait_short(bar, parity)) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait_short(bar, parity)) return true;
         if (*reinterpret_cast<volatile int *>(abort_flag)) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (global_timer_ns() - t0 >= limit_ns) {
             *reinterpret_cast<volatile int *>(abort_flag) = 1;
             return false;
         }
     }
 }
 // The same for a whole warp: one outcome for all lanes.
-__device__ __forceinline__ bool at_warp_wait(uint32_t bar, uint32_t parity, int *abort_flag) {
-    const bool ok = at_wait(bar, parity, abort_flag);
+__device__ __forceinline__ bool at_warp_wait(uint32_t bar, uint32_t parity, int *abort_flag, uint64_t limit_ns) {
+    const bool ok = at_wait(bar, parity, abort_flag, limit_ns);
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             do {
                 if (n.none()) continue;
                 // The unit before last is written out: nothing reads this buffer, its scales or its limits any more.
-                if (iu >= 2 && !at_warp_wait(smem_addr(&ml_free[ub]), static_cast<uint32_t>((iu >> 1) - 1) & 1u, &s_abort)) break;
+                if (iu >= 2 && !at_warp_wait(smem_addr(&ml_free[ub]), static_cast<uint32_t>((iu >> 1) - 1) & 1u, &s_abort, a.wait_limit_ns)) break;
                 at_build_queries<T, PL, R, ND>(a, n, sQ + ub * Sh::kQBytes, s_qs[ub], s_lim[ub], all ? warp : warp - kAtQueryWarp,
                                                all ? kAtKWarp : 4, lane);
                 if (all) asm volatile("bar.sync 4, %0;" ::"n"(kAtKWarp * 32) : "memory");
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const bool mine = lane < pages, good = id >= 0 && id < a.n_blocks;
                     if (mine && !good) atomicOr(a.status, 4u);
                     const int64_t bh = static_cast<int64_t>(good ? id : 0) * a.kv_heads + head;
-                    if (it >= S && !at_warp_wait(smem_addr(&free[st]), ph ^ 1u, &s_abort)) {
+                    if (it >= S && !at_warp_wait(smem_addr(&free[st]), ph ^ 1u, &s_abort, a.wait_limit_ns)) {
                         ok = false;
                         break;
                     }
@@ -732,6 +733,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 bool more = true;           // false: unit_end is the end of the range
                 uint64_t t0 = 0;
                 int spins = 0;
+                // The clock is read every 32 polls, or every poll under a shorter limit: these polls do not suspend, so
+                // that a limit of 0 ends at the first one that finds nothing.
+                const int every = a.wait_limit_ns < kWaitLimitNs ? 1 : 32;
                 while (more || pt < unit_end) {
                     bool went = false;
                     {
@@ -801,11 +805,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     }
                     if (went) {
                         spins = 0;
-                    } else if ((++spins & 31) == 0) {  // bounded, as at_wait
+                    } else if ((++spins & (every - 1)) == 0) {  // bounded, as at_wait
                         if (*reinterpret_cast<volatile int *>(&s_abort)) break;
                         const uint64_t now = global_timer_ns();
-                        if (spins == 32) t0 = now;
-                        else if (now - t0 > kWaitLimitNs) {
+                        if (spins == every && a.wait_limit_ns != 0) t0 = now;
+                        else if (now - t0 >= a.wait_limit_ns) {
                             *reinterpret_cast<volatile int *>(&s_abort) = 1;
                             break;
                         }
@@ -826,8 +830,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             do {
                 if (w.none()) continue;
                 const uint32_t uph = static_cast<uint32_t>((iu >> 1) & 1);
-                ok = ok && at_warp_wait(smem_addr(&q_full[ub]), uph, &s_abort) &&
-                     (iu < 2 || at_warp_wait(smem_addr(&ml_free[ub]), uph ^ 1u, &s_abort));
+                ok = ok && at_warp_wait(smem_addr(&q_full[ub]), uph, &s_abort, a.wait_limit_ns) &&
+                     (iu < 2 || at_warp_wait(smem_addr(&ml_free[ub]), uph ^ 1u, &s_abort, a.wait_limit_ns));
                 float ref = kAtNoRef;  // running maximum of row `tg` (threads below R)
                 float *den = s_l[ub][warp];  // this warp's denominators; lane l looks after its own of every eight rows
                 const int own = at_owned(lane);
@@ -850,7 +854,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     const int b = static_cast<int>(it & (kAtDeep - 1));
                     const int cs = static_cast<int>(it & (kAtScaleDeep - 1));  // the scales' slot
                     const int pos = j * kAtTile + tg;
-                    ok = ok && at_warp_wait(smem_addr(&sc_full[cs]), static_cast<uint32_t>(it / kAtScaleDeep) & 1u, &s_abort);
+                    ok = ok && at_warp_wait(smem_addr(&sc_full[cs]), static_cast<uint32_t>(it / kAtScaleDeep) & 1u, &s_abort, a.wait_limit_ns);
                     // This token's value scale, relative to the power of two under the tile's largest.
                     const int blocks = (min(w.q.len - j * kAtTile, kAtTile) - 1) >> a.block_log2;  // the last one's number
                     float vs[8], vtop = 0.f;
@@ -869,7 +873,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                         const float x = fabsf(sc[cs][1][tg * 16 >> a.block_log2]);
                         s_ve[g][tg] = static_cast<float>(max((__float_as_int(x) >> 23) - 127, kAtMinScale));
                     }
-                    ok = ok && at_warp_wait(smem_addr(&s_full[b]), bp, &s_abort);
+                    ok = ok && at_warp_wait(smem_addr(&s_full[b]), bp, &s_abort, a.wait_limit_ns);
                     const bool edge = (j + 1) * kAtTile - 1 > seen_by_all;  // some row does not see the whole tile
                     // Scores of rows c .. c + 7, in base 2; what a row does not see is -inf.
                     auto scores = [&](int c, float (&s)[8]) {
@@ -907,10 +911,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     if constexpr (R == 8) release();
                     // One warp waits until the output sums have read what the tile kAtDeep ago left in this slot, another until
                     // the second MMA has read its weights.
-                    if (wg == 1 && it >= kAtDeep) ok = at_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort) && ok;
+                    if (wg == 1 && it >= kAtDeep) ok = at_wait(smem_addr(&o_free[b]), bp ^ 1u, &s_abort, a.wait_limit_ns) && ok;
                     at_bar(bar);
                     if (PD < kAtDeep && wg == 2 && it >= PD)
-                        ok = at_wait(smem_addr(&o_full[(it - PD) & (kAtDeep - 1)]), static_cast<uint32_t>((it - PD) / kAtDeep) & 1u, &s_abort) && ok;
+                        ok = at_wait(smem_addr(&o_full[(it - PD) & (kAtDeep - 1)]), static_cast<uint32_t>((it - PD) / kAtDeep) & 1u, &s_abort, a.wait_limit_ns) && ok;
                     if (tg < rows) {
                         float exps[8], tref = kAtNoRef, most = -INFINITY;
                         at_lds8(s_ve[g], exps);
@@ -966,7 +970,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     if (edge) {
                         // This token's row of V: zeros where the request ends (what is there is no token's), and NaN
                         // codes that only later rows see leave the tile and mark the element for those rows.
-                        ok = ok && at_warp_wait(smem_addr(&v_full[vs_st]), v_ph, &s_abort);
+                        ok = ok && at_warp_wait(smem_addr(&v_full[vs_st]), v_ph, &s_abort, a.wait_limit_ns);
                         if (ok && pos > seen_by_all) {
 #pragma unroll
                             for (int h = 0; h < ND; ++h) {
@@ -1048,8 +1052,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 for (int j = w.j0; j < w.j1; ++j) {
                     const int b = static_cast<int>(it & (kAtDeep - 1));
                     const uint32_t bp = static_cast<uint32_t>(it / kAtDeep) & 1u;
-                    ok = ok && at_warp_wait(smem_addr(&o_full[b]), bp, &s_abort) &&
-                         at_warp_wait(smem_addr(&p_full[b]), bp, &s_abort);  // long complete: orders the softmax's words
+                    ok = ok && at_warp_wait(smem_addr(&o_full[b]), bp, &s_abort, a.wait_limit_ns) &&
+                         at_warp_wait(smem_addr(&p_full[b]), bp, &s_abort, a.wait_limit_ns);  // long complete: orders the softmax's words
                     t8_fence_after();
                     bool raised = false;
                     at_bar(3);  // every warp has read the last tile's factors
@@ -1095,7 +1099,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     if (lane == 0) mbar_arrive(smem_addr(&o_free[b]));
                     ++it;
                 }
-                ok = ok && at_warp_wait(smem_addr(&ml_full[ub]), static_cast<uint32_t>((iu >> 1) & 1), &s_abort);
+                ok = ok && at_warp_wait(smem_addr(&ml_full[ub]), static_cast<uint32_t>((iu >> 1) & 1), &s_abort, a.wait_limit_ns);
+                // One outcome for the group, and no result out of weights that a softmax group gave up on (it raised the flag
+                // before it reported the unit).
+                ok = !at_bar_or(3, !ok || *reinterpret_cast<volatile int *>(&s_abort) != 0);
                 if (!ok) {
 #pragma unroll
                     for (int h = 0; h < ND; ++h)
@@ -1118,6 +1125,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     for (int g = 0; g < 2; ++g)
                         l += at_exp2(s_mref[ub][g][dt] - ref) * ((s_l[ub][4 * g][dt] + s_l[ub][4 * g + 1][dt]) +
                                                                  (s_l[ub][4 * g + 2][dt] + s_l[ub][4 * g + 3][dt]));
+                    if (!ok) l = nanf;
                 }
                 if (whole) {
                     if (dt < rows) {

@@ -25,7 +25,7 @@ struct Tuning {
     int tc_min_m = 1;                    // tensor-core kernel for m >= this (9 = never)
     int64_t tc_min_bytes = 0;            // ... and at least this many weight bytes (0 = by m, below)
     int64_t m1_rowwarp_min_bytes = 96ll << 20;  // by size: row-per-warp from this many weight bytes
-    uint64_t wait_limit_ns = kWaitLimitNs;      // consumer waits of the CUDA-core kernels
+    uint64_t wait_limit_ns = kWaitLimitNs;      // consumer waits of the CUDA-core kernels, role waits of kv_attn
     int fp4_kernel = 0;                  // NVFP4 experts: 0 = by shape, 1 = CUDA cores, 2 = tensor cores
 };
 Tuning &tuning();

@@ -522,7 +522,7 @@ WAIT_LIMIT_DEFAULT_NS = 1_000_000_000
 
 
 def set_wait_limit(limit_ns: int = WAIT_LIMIT_DEFAULT_NS) -> None:
-    """How long a CUDA-core GEMV thread waits for a weight tile before giving
+    """How long a CUDA-core GEMV thread waits for a weight tile (or a role of fp8blk_kv_attn for its operands) before giving
     up (status FP8BLK_STATUS_WAIT_TIMEOUT); the default is about one second."""
     _check(_lib.fp8blk_set_wait_limit(int(limit_ns)), "fp8blk_set_wait_limit")
 

@@ -397,6 +397,8 @@ size_t fp8blk_kv_attn_ws_bytes(int n_seqs, int max_m, int q_heads, int kv_heads,
  * A block id outside the pool (or a length past max_blocks) makes the rows
  * that see it NaN; a request with more than max_m rows, or rows outside
  * total_rows, is skipped; each sets FP8BLK_STATUS_BAD_KV.
+ * Rows of a CTA that gave up on a wait are NaN in out and lse (see
+ * fp8blk_set_wait_limit).
  * Errors: EINVAL, EALIGN, EWS, ERANGE (a size past the limits above, or more
  * than about 2^28 tiles of 128 tokens over all requests, heads and groups of 32
  * rows at max_blocks each), ECUDA.
@@ -460,14 +462,16 @@ int fp8blk_set_launch_tuning(int target_stage_bytes, int ctas_per_sm, int use_pd
  * FP8BLK_WAIT_LIMIT_DEFAULT_NS) on how long a kernel thread of the CUDA-core
  * GEMVs (fp8blk_gemv / fp8blk_gemv_argmax below the tensor-core thresholds,
  * fp8blk_bf16_gemv, nvfp4_expert_gemv, mxfp4_expert_gemv) waits for a weight
- * tile before it gives up, sets FP8BLK_STATUS_WAIT_TIMEOUT and returns.  The
+ * tile, or a role of fp8blk_kv_attn for its operands, before it gives up,
+ * sets FP8BLK_STATUS_WAIT_TIMEOUT and returns.  The
  * default is about one second; a healthy tile lands in microseconds, so any
  * shorter limit is for exercising the failure path (0 gives up on the first
  * tile that has not landed yet).  After a give-up the CTA still waits, with
  * the fixed one-second bound, for the copies it has in flight before it
- * exits, and still takes part in the argmax hand-off, so the workspace stays
- * consistent; the outputs of that call are invalid.  The tensor-core kernel
- * and the dequant kernel keep the fixed bound.  Not thread-safe against
+ * exits, and still takes part in the argmax hand-off or the join of parts, so
+ * the workspace stays consistent; the outputs of that call are invalid (those
+ * of fp8blk_kv_attn NaN).  The tensor-core GEMV kernels and the dequant kernel
+ * keep the fixed bound.  Not thread-safe against
  * concurrent calls of the other entry points.  Errors: EINVAL.
  */
 #define FP8BLK_WAIT_LIMIT_DEFAULT_NS 1000000000ll
