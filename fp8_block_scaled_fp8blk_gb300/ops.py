@@ -299,21 +299,26 @@ def _dtype(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _typed(t: torch.Tensor, dtype: torch.dtype, what: str) -> int:
-    """Data pointer of a contiguous tensor of exactly this type."""
-    if t.dtype is not dtype or not t.is_contiguous():
-        _refuse(t, dtype, what)
+def _typed(t: torch.Tensor, dtype: torch.dtype, what: str, device: int) -> int:
+    """Data pointer of a contiguous tensor of exactly this type on this device (as get_device() counts; the host is -1).
+    The stream's tensor gives the device, so a pointer that the kernel could not follow never reaches it."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, dtype, what, device)
     return t.data_ptr()
 
 
-def _refuse(t: torch.Tensor, dtype: torch.dtype, what: str) -> None:
+def _refuse(t: torch.Tensor, dtype: torch.dtype, what: str, device: int) -> None:
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{what} is on {t.device}, the call's other tensors are not")
     raise ValueError(f"{what} must be contiguous")
 
 
-def _rows3(t: torch.Tensor, what: str) -> int:
-    """Row stride of a [rows, heads, head_dim] tensor whose rows are dense."""
+def _rows3(t: torch.Tensor, what: str, device: int) -> int:
+    """Row stride of a [rows, heads, head_dim] tensor on this device whose rows are dense."""
+    if t.get_device() != device:
+        _refuse(t, t.dtype, what, device)
     if t.dim() != 3:
         raise ValueError(f"{what} must have 3 dimensions [rows, heads, head_dim]")
     rows, heads, dim = t.shape
@@ -326,7 +331,7 @@ def _rows3(t: torch.Tensor, what: str) -> int:
 _U8, _F32, _I32, _I64T = torch.uint8, torch.float32, torch.int32, torch.int64
 
 
-def _cache(k_codes, k_scales, v_codes, v_scales):
+def _cache(k_codes, k_scales, v_codes, v_scales, device):
     """Shape and data pointers of a cache: (n_blocks, kv_heads, block_tokens, head_dim), (k_codes, k_scales, ...)."""
     shape = k_codes.shape
     if len(shape) != 4 or v_codes.shape != shape:
@@ -334,8 +339,8 @@ def _cache(k_codes, k_scales, v_codes, v_scales):
     pairs = shape[:2]
     if k_scales.shape != pairs or v_scales.shape != pairs:
         raise ValueError("k_scales and v_scales must both be [n_blocks, kv_heads]")
-    return shape, (_typed(k_codes, _U8, "k_codes"), _typed(k_scales, _F32, "k_scales"), _typed(v_codes, _U8, "v_codes"),
-                   _typed(v_scales, _F32, "v_scales"))
+    return shape, (_typed(k_codes, _U8, "k_codes", device), _typed(k_scales, _F32, "k_scales", device),
+                   _typed(v_codes, _U8, "v_codes", device), _typed(v_scales, _F32, "v_scales", device))
 
 
 class KvMap(NamedTuple):
@@ -366,12 +371,12 @@ def fp8blk_kv_map(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     if (out.seq_lens.numel() != n or out.q_starts.numel() != n + 1 or out.slots.numel() != max_tokens
             or out.positions.numel() != max_tokens or out.free_head.numel() != 1):
         raise ValueError("out does not fit (see kv_map_buffers)")
-    i32 = torch.int32
-    _check(_lib.fp8blk_kv_map(_typed(ctx_lens, i32, "ctx_lens"), _typed(new_lens, i32, "new_lens"),
-                              _typed(block_table, i32, "block_table"), _typed(free_blocks, i32, "free_blocks"),
-                              _typed(free_head, i32, "free_head"), _typed(out.seq_lens, i32, "out.seq_lens"),
-                              _typed(out.q_starts, i32, "out.q_starts"), _typed(out.slots, torch.int64, "out.slots"),
-                              _typed(out.positions, i32, "out.positions"), _typed(out.free_head, i32, "out.free_head"),
+    i32, dev = torch.int32, block_table.get_device()
+    _check(_lib.fp8blk_kv_map(_typed(ctx_lens, i32, "ctx_lens", dev), _typed(new_lens, i32, "new_lens", dev),
+                              _typed(block_table, i32, "block_table", dev), _typed(free_blocks, i32, "free_blocks", dev),
+                              _typed(free_head, i32, "free_head", dev), _typed(out.seq_lens, i32, "out.seq_lens", dev),
+                              _typed(out.q_starts, i32, "out.q_starts", dev), _typed(out.slots, _I64T, "out.slots", dev),
+                              _typed(out.positions, i32, "out.positions", dev), _typed(out.free_head, i32, "out.free_head", dev),
                               n, width, free_blocks.numel(), block_tokens, max_tokens, _stream(block_table)),
            "fp8blk_kv_map")
     return out
@@ -380,7 +385,8 @@ def fp8blk_kv_map(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
 def fp8blk_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
                      v_codes: torch.Tensor, v_scales: torch.Tensor) -> None:
     """Write keys and values [n, kv_heads, head_dim] (float32 or bfloat16; rows may be strided) into the cache at `slots`."""
-    (blocks, heads, block, dim), cache = _cache(k_codes, k_scales, v_codes, v_scales)
+    dev = k_codes.get_device()
+    (blocks, heads, block, dim), cache = _cache(k_codes, k_scales, v_codes, v_scales, dev)
     n = slots.numel()
     if k.shape != (n, heads, dim) or v.shape != (n, heads, dim):
         raise ValueError("k and v must both be [len(slots), kv_heads, head_dim] of the cache")
@@ -388,8 +394,8 @@ def fp8blk_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_co
         raise TypeError("k and v must have the same type")
     if n == 0:
         return
-    rc = _lib.fp8blk_kv_append(k.data_ptr(), v.data_ptr(), _dtype(k, "k"), _typed(slots, _I64T, "slots"), *cache, n,
-                               _rows3(k, "k"), _rows3(v, "v"), blocks, heads, block, dim, _stream(k_codes))
+    rc = _lib.fp8blk_kv_append(k.data_ptr(), v.data_ptr(), _dtype(k, "k"), _typed(slots, _I64T, "slots", dev), *cache, n,
+                               _rows3(k, "k", dev), _rows3(v, "v", dev), blocks, heads, block, dim, _stream(k_codes))
     if rc:
         _check(rc, "fp8blk_kv_append")
 
@@ -412,9 +418,10 @@ def fp8blk_kv_attn(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tenso
                    lse: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of q [rows, q_heads, head_dim] (float32 or bfloat16; rows may be strided) over the paged cache; up to
     max_m rows per request.  `lse` (float32 [rows, q_heads]) is written when given."""
-    (blocks, kv_heads, block, dim), cache = _cache(k_codes, k_scales, v_codes, v_scales)
+    dev = q.get_device()
+    (blocks, kv_heads, block, dim), cache = _cache(k_codes, k_scales, v_codes, v_scales, dev)
     n, width = block_table.shape
-    q_stride = _rows3(q, "q")
+    q_stride = _rows3(q, "q", dev)
     rows, q_heads, q_dim = q.shape
     if q_dim != dim:
         raise ValueError("q must be [rows, q_heads, head_dim] of the cache")
@@ -428,10 +435,11 @@ def fp8blk_kv_attn(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tenso
         raise ValueError("lse must be [rows, q_heads]")
     if rows == 0:
         return out
-    rc = _lib.fp8blk_kv_attn(q.data_ptr(), _dtype(q, "q"), *cache, _typed(block_table, _I32, "block_table"),
-                             _typed(seq_lens, _I32, "seq_lens"), _typed(q_starts, _I32, "q_starts"), out.data_ptr(),
-                             None if lse is None else _typed(lse, _F32, "lse"), ws.data_ptr(), ws.nbytes, n, max_m, rows,
-                             q_heads, kv_heads, dim, block, blocks, width, q_stride, _rows3(out, "out"), sm_scale, _stream(q))
+    rc = _lib.fp8blk_kv_attn(q.data_ptr(), _dtype(q, "q"), *cache, _typed(block_table, _I32, "block_table", dev),
+                             _typed(seq_lens, _I32, "seq_lens", dev), _typed(q_starts, _I32, "q_starts", dev), out.data_ptr(),
+                             None if lse is None else _typed(lse, _F32, "lse", dev), _typed(ws, ws.dtype, "ws", dev), ws.nbytes,
+                             n, max_m, rows, q_heads, kv_heads, dim, block, blocks, width, q_stride, _rows3(out, "out", dev),
+                             sm_scale, _stream(q))
     if rc:
         _check(rc, "fp8blk_kv_attn")
     return out
@@ -470,11 +478,11 @@ def fp8blk_token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int 
         raise ValueError("out does not fit (see token_logprobs_buffers)")
     if n == 0:
         return out
-    f32, i32 = torch.float32, torch.int32
-    _check(_lib.fp8blk_token_logprobs(logits.data_ptr(), _dtype(logits, "logits"), _typed(targets, i32, "targets"),
-                                      _typed(out.logprob, f32, "out.logprob"), _typed(out.rank, i32, "out.rank"),
-                                      _typed(out.entropy, f32, "out.entropy"), _typed(out.top_ids, i32, "out.top_ids"),
-                                      _typed(out.top_logprobs, f32, "out.top_logprobs"), n, vocab,
+    f32, i32, dev = torch.float32, torch.int32, logits.get_device()
+    _check(_lib.fp8blk_token_logprobs(logits.data_ptr(), _dtype(logits, "logits"), _typed(targets, i32, "targets", dev),
+                                      _typed(out.logprob, f32, "out.logprob", dev), _typed(out.rank, i32, "out.rank", dev),
+                                      _typed(out.entropy, f32, "out.entropy", dev), _typed(out.top_ids, i32, "out.top_ids", dev),
+                                      _typed(out.top_logprobs, f32, "out.top_logprobs", dev), n, vocab,
                                       logits.stride(0) if n > 1 else vocab, top, _stream(logits)),
            "fp8blk_token_logprobs")
     return out
