@@ -102,11 +102,20 @@ def _check(rc: int, where: str) -> None:
         raise Fp8BlkError(rc, where)
 
 
-def _ptr(t: torch.Tensor | None) -> int | None:
+def _elsewhere(t: torch.Tensor, device: int, what: str = "a tensor") -> None:
+    """Refuse a tensor that is not on the device (get_device() of the stream's tensor; the host is -1), unless it is pinned
+    host memory, which kernels reach too: no pointer that a kernel could not follow is passed on."""
+    if t.get_device() != device and not (t.device.type == "cpu" and t.is_pinned()):
+        raise ValueError(f"{what} is on {t.device}, the call's other tensors are not")
+
+
+def _ptr(t: torch.Tensor | None, device: int) -> int | None:
     if t is None:
         return None
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
+    if t.get_device() != device:
+        _elsewhere(t, device)
     return t.data_ptr()
 
 
@@ -148,7 +157,8 @@ def fp8blk_gemv(w_codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
     m = x2.shape[0]
     if y is None:
         y = torch.empty((m, rows), dtype=torch.float32, device=x.device)
-    _check(_lib.fp8blk_gemv(_ptr(w_codes), _ptr(scales), _ptr(x2), _ptr(y), m, rows, cols,
+    dev = x.get_device()
+    _check(_lib.fp8blk_gemv(_ptr(w_codes, dev), _ptr(scales, dev), _ptr(x2, dev), _ptr(y, dev), m, rows, cols,
                             _stream(x)), "fp8blk_gemv")
     return y
 
@@ -174,8 +184,9 @@ def fp8blk_gemv_argmax(w_codes: torch.Tensor, scales: torch.Tensor, x: torch.Ten
     m = x2.shape[0]
     if tokens is None:
         tokens = torch.empty(m, dtype=torch.int32, device=x.device)
-    _check(_lib.fp8blk_gemv_argmax(_ptr(w_codes), _ptr(scales), _ptr(x2), _ptr(logits),
-                                   _ptr(tokens), _ptr(ws), ws.numel() * ws.element_size(), m,
+    dev = x.get_device()
+    _check(_lib.fp8blk_gemv_argmax(_ptr(w_codes, dev), _ptr(scales, dev), _ptr(x2, dev), _ptr(logits, dev),
+                                   _ptr(tokens, dev), _ptr(ws, dev), ws.numel() * ws.element_size(), m,
                                    rows, cols, _stream(x)), "fp8blk_gemv_argmax")
     return tokens
 
@@ -192,8 +203,9 @@ def fp8blk_gemv_argmax_noalloc(w_codes: torch.Tensor, scales: torch.Tensor, x: t
     m = x2.shape[0]
     if tokens is None:
         tokens = torch.empty(m, dtype=torch.int32, device=x.device)
-    _check(_lib.fp8blk_gemv_argmax_noalloc(_ptr(w_codes), _ptr(scales), _ptr(x2), _ptr(logits),
-                                           _ptr(tokens), m, rows, cols, _stream(x)),
+    dev = x.get_device()
+    _check(_lib.fp8blk_gemv_argmax_noalloc(_ptr(w_codes, dev), _ptr(scales, dev), _ptr(x2, dev), _ptr(logits, dev),
+                                           _ptr(tokens, dev), m, rows, cols, _stream(x)),
            "fp8blk_gemv_argmax_noalloc")
     return tokens
 
@@ -205,7 +217,8 @@ def fp8blk_bf16_gemv(w_bf16: torch.Tensor, x: torch.Tensor,
     m = x2.shape[0]
     if y is None:
         y = torch.empty((m, rows), dtype=torch.float32, device=x.device)
-    _check(_lib.fp8blk_bf16_gemv(_ptr(w_bf16), _ptr(x2), _ptr(y), m, rows, cols, _stream(x)),
+    dev = x.get_device()
+    _check(_lib.fp8blk_bf16_gemv(_ptr(w_bf16, dev), _ptr(x2, dev), _ptr(y, dev), m, rows, cols, _stream(x)),
            "fp8blk_bf16_gemv")
     return y
 
@@ -231,8 +244,9 @@ def nvfp4_expert_dequant(codes: torch.Tensor, scales: torch.Tensor, gscale, expe
     g = _host_f32(gscale)
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.int16, device=codes.device)
-    _check(_lib.nvfp4_expert_dequant(_ptr(codes), _ptr(scales), g.ctypes.data, n_experts,
-                                     int(expert_id), _ptr(out), rows, cols, _stream(codes)),
+    dev = codes.get_device()
+    _check(_lib.nvfp4_expert_dequant(_ptr(codes, dev), _ptr(scales, dev), g.ctypes.data, n_experts,
+                                     int(expert_id), _ptr(out, dev), rows, cols, _stream(codes)),
            "nvfp4_expert_dequant")
     return out
 
@@ -247,9 +261,10 @@ def nvfp4_expert_dequant_gemv(codes: torch.Tensor, scales: torch.Tensor, gscale,
     ids_h = _host_i32(ids)
     if y is None:
         y = torch.empty((ids_h.size, rows), dtype=torch.float32, device=x.device)
-    _check(_lib.nvfp4_expert_dequant_gemv(_ptr(codes), _ptr(scales), g.ctypes.data, n_experts,
-                                          ids_h.ctypes.data, ids_h.size, _ptr(x), _ptr(y),
-                                          _ptr(scratch), rows, cols, _stream(x)),
+    dev = x.get_device()
+    _check(_lib.nvfp4_expert_dequant_gemv(_ptr(codes, dev), _ptr(scales, dev), g.ctypes.data, n_experts,
+                                          ids_h.ctypes.data, ids_h.size, _ptr(x, dev), _ptr(y, dev),
+                                          _ptr(scratch, dev), rows, cols, _stream(x)),
            "nvfp4_expert_dequant_gemv")
     return y
 
@@ -266,8 +281,9 @@ def nvfp4_expert_gemv(codes: torch.Tensor, scales: torch.Tensor, gscale: torch.T
     n_active = ids.numel()
     if y is None:
         y = torch.empty((n_active, rows), dtype=torch.float32, device=x.device)
-    _check(_lib.nvfp4_expert_gemv(_ptr(codes), _ptr(scales), _ptr(gscale), n_experts, _ptr(ids), n_active,
-                                  _ptr(x), _ptr(y), rows, cols, _stream(x)), "nvfp4_expert_gemv")
+    dev = x.get_device()
+    _check(_lib.nvfp4_expert_gemv(_ptr(codes, dev), _ptr(scales, dev), _ptr(gscale, dev), n_experts, _ptr(ids, dev), n_active,
+                                  _ptr(x, dev), _ptr(y, dev), rows, cols, _stream(x)), "nvfp4_expert_gemv")
     return y
 
 
@@ -283,7 +299,8 @@ def mxfp4_expert_gemv(codes: torch.Tensor, scales: torch.Tensor, ids: torch.Tens
     n_active = ids.numel()
     if y is None:
         y = torch.empty((n_active, rows), dtype=torch.float32, device=x.device)
-    _check(_lib.mxfp4_expert_gemv(_ptr(codes), _ptr(scales), n_experts, _ptr(ids), n_active, _ptr(x), _ptr(y),
+    dev = x.get_device()
+    _check(_lib.mxfp4_expert_gemv(_ptr(codes, dev), _ptr(scales, dev), n_experts, _ptr(ids, dev), n_active, _ptr(x, dev), _ptr(y, dev),
                                   rows, cols, _stream(x)), "mxfp4_expert_gemv")
     return y
 
@@ -300,8 +317,7 @@ def _dtype(t: torch.Tensor, what: str) -> int:
 
 
 def _typed(t: torch.Tensor, dtype: torch.dtype, what: str, device: int) -> int:
-    """Data pointer of a contiguous tensor of exactly this type on this device (as get_device() counts; the host is -1).
-    The stream's tensor gives the device, so a pointer that the kernel could not follow never reaches it."""
+    """Data pointer of a contiguous tensor of exactly this type on this device (see _elsewhere)."""
     if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
         _refuse(t, dtype, what, device)
     return t.data_ptr()
@@ -310,15 +326,15 @@ def _typed(t: torch.Tensor, dtype: torch.dtype, what: str, device: int) -> int:
 def _refuse(t: torch.Tensor, dtype: torch.dtype, what: str, device: int) -> None:
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.get_device() != device:
-        raise ValueError(f"{what} is on {t.device}, the call's other tensors are not")
-    raise ValueError(f"{what} must be contiguous")
+    _elsewhere(t, device, what)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
 
 
 def _rows3(t: torch.Tensor, what: str, device: int) -> int:
     """Row stride of a [rows, heads, head_dim] tensor on this device whose rows are dense."""
     if t.get_device() != device:
-        _refuse(t, t.dtype, what, device)
+        _elsewhere(t, device, what)
     if t.dim() != 3:
         raise ValueError(f"{what} must have 3 dimensions [rows, heads, head_dim]")
     rows, heads, dim = t.shape

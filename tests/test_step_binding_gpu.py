@@ -68,3 +68,37 @@ def test_token_logprobs(ops):
     x = torch.zeros((3, 50), device=DEV)
     out = ops.token_logprobs_buffers(3, 2, DEV)
     refuses_host_tensors(lambda a, t, o: ops.fp8blk_token_logprobs(a, t, 2, out=o), (x, i32(0, 1, 2), out))
+
+
+def test_gemv_and_experts(ops):
+    from _helpers import scales_dev, to_dev
+    from fp8_block_scaled_fp8blk_gb300 import synth
+    c = synth.fp8blk_case(256, 256, 1, seed=1)
+    w, s, x = to_dev(c.codes), scales_dev(c.scale_e8m0), to_dev(c.x)
+    y = torch.full((1, 256), 3.0, device=DEV)
+    refuses_host_tensors(ops.fp8blk_gemv, (w, s, x, y))
+    ws, tok = ops.argmax_workspace(1, 256, 256, DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    refuses_host_tensors(ops.fp8blk_gemv_argmax, (w, s, x, ws, tok, y))
+    refuses_host_tensors(ops.fp8blk_gemv_argmax_noalloc, (w, s, x, tok, y))
+    refuses_host_tensors(ops.fp8blk_bf16_gemv, (torch.zeros((256, 256), dtype=torch.bfloat16, device=DEV), x, y))
+    e = synth.nvfp4_case(2, 128, 512, 1, seed=2)
+    codes, scales, g, ex = to_dev(e.codes), to_dev(e.scales), to_dev(e.gscale), to_dev(e.x)
+    ye = torch.full((1, 128), 3.0, device=DEV)
+    refuses_host_tensors(ops.nvfp4_expert_gemv, (codes, scales, g, i32(0), ex, ye))
+    refuses_host_tensors(ops.mxfp4_expert_gemv, (codes, scales, i32(0), ex, ye))
+    scratch = torch.zeros((128, 512), dtype=torch.int16, device=DEV)
+    refuses_host_tensors(lambda a, b, o: ops.nvfp4_expert_dequant(a, b, e.gscale, 0, out=o), (codes, scales, scratch))
+    refuses_host_tensors(lambda a, b, v, t, o: ops.nvfp4_expert_dequant_gemv(a, b, e.gscale, [0], v, t, y=o),
+                         (codes, scales, ex, scratch, ye))
+    torch.cuda.synchronize()
+    assert (y == 3).all() and (ye == 3).all()
+
+
+def test_pinned_host_memory_is_taken(ops):
+    """The device reaches it: a token written straight to the host."""
+    x = torch.randn((2, 1000), device=DEV)
+    out = ops.token_logprobs_buffers(2, 1, DEV)
+    pinned = out._replace(top_ids=torch.zeros((2, 1), dtype=torch.int32).pin_memory())
+    ops.fp8blk_token_logprobs(x, i32(1, 2), 1, out=pinned)
+    torch.cuda.synchronize()
+    assert torch.equal(pinned.top_ids[:, 0], x.argmax(1).int().cpu())
