@@ -56,6 +56,14 @@ class Cache:
         self.table = torch.full((n_seqs, max_blocks), -1, dtype=torch.int32, device=d)
         self.free_blocks = torch.arange(n_blocks, dtype=torch.int32, device=d)
         self.free_head = torch.zeros(1, dtype=torch.int32, device=d)
+        self.held, self._spare = (torch.zeros(n_seqs, dtype=torch.int32, device=d) for _ in range(2))
+
+    def map(self, ctx_lens, new_lens, max_tokens: int):
+        """Blocks and slots for new tokens; blocks of rejected ones stay their request's for the next."""
+        step = ops.fp8blk_kv_map(ctx_lens, new_lens, self.table, self.free_blocks, self.free_head, self.block_tokens, max_tokens,
+                                 held=self.held, held_out=self._spare)
+        self.free_head, self.held, self._spare = step.free_head, self._spare, self.held
+        return step
 
     @property
     def pools(self):
@@ -73,9 +81,7 @@ def linear(weight, x):
 
 def fill(model: Model, cache: Cache, lens: torch.Tensor, hidden: torch.Tensor) -> None:
     """Prompts: keys and values of all their tokens in one call."""
-    step = ops.fp8blk_kv_map(torch.zeros_like(lens), lens, cache.table, cache.free_blocks, cache.free_head, cache.block_tokens,
-                             hidden.shape[0])
-    cache.free_head = step.free_head
+    step = cache.map(torch.zeros_like(lens), lens, hidden.shape[0])
     qkv = linear(model.qkv, hidden).view(hidden.shape[0], -1, model.head_dim)
     k, v = qkv[:, model.q_heads: model.q_heads + model.kv_heads], qkv[:, model.q_heads + model.kv_heads:]
     ops.fp8blk_kv_append(k, v, step.slots, *cache.pools)
@@ -84,8 +90,7 @@ def fill(model: Model, cache: Cache, lens: torch.Tensor, hidden: torch.Tensor) -
 def verify(model: Model, cache: Cache, ctx_lens, new_lens, hidden, drafts, ws, top=4):
     """One step: hidden [rows, hidden], drafts [rows] (the token each row is asked about; -1 = none)."""
     rows, d = hidden.shape[0], model.head_dim
-    step = ops.fp8blk_kv_map(ctx_lens, new_lens, cache.table, cache.free_blocks, cache.free_head, cache.block_tokens, rows)
-    cache.free_head = step.free_head
+    step = cache.map(ctx_lens, new_lens, rows)
     qkv = linear(model.qkv, hidden).view(rows, -1, d)
     q = qkv[:, : model.q_heads]
     k, v = qkv[:, model.q_heads: model.q_heads + model.kv_heads], qkv[:, model.q_heads + model.kv_heads:]
@@ -137,5 +142,35 @@ def main(seed: int = 0) -> dict:
                 scores=scores, lens=lens, new=new)
 
 
+def loop(steps: int = 6, seed: int = 1):
+    """Verify steps in a row: each request's context grows by its accepted rows only, the rejected ones' slots are written
+    again, and the host is asked nothing in between."""
+    model, n = Model(), 3
+    gen = torch.Generator(device=model.device)
+    gen.manual_seed(seed)
+    lens = torch.tensor([30, 47, 64], dtype=torch.int32, device=model.device)
+    cache = Cache(model, n, n_blocks=40, block_tokens=16, max_blocks=10)
+    fill(model, cache, lens, torch.randn((int(lens.sum()), model.hidden), device=model.device, generator=gen))
+    new = torch.full((n,), ops.MAX_M, dtype=torch.int32, device=model.device)
+    rows = n * ops.MAX_M
+    ws = ops.kv_attn_workspace(n, ops.MAX_M, model.q_heads, model.kv_heads, model.head_dim, model.device)
+    accepted = torch.zeros((steps, n), dtype=torch.int32, device=model.device)
+    for i in range(steps):
+        hidden = torch.randn((rows, model.hidden), device=model.device, generator=gen)
+        drafts = torch.randint(0, model.vocab, (n, ops.MAX_M), device=model.device, generator=gen, dtype=torch.int32)
+        drafts[:, -1] = -1  # the last row has no draft after it
+        tokens = verify(model, cache, lens, new, hidden, drafts.flatten(), ws)[3].view(n, -1)
+        drafts[:, 0] = torch.where(torch.rand(n, device=model.device, generator=gen) < 0.5, tokens[:, 0], drafts[:, 0])
+        accepted[i] = 1 + torch.cumprod((tokens == drafts).int(), 1).sum(1).int()
+        lens = lens + accepted[i]
+    counts = accepted.cpu()
+    print(f"{steps} steps of {n} x {ops.MAX_M} rows: {counts.tolist()} rows accepted, {cache.held.tolist()} blocks held, "
+          f"{int(cache.free_head)} taken")
+    if ops.fp8blk_device_status(clear=True):
+        raise RuntimeError("a kernel reported a problem")
+    return cache, lens, counts
+
+
 if __name__ == "__main__":
     main()
+    loop()

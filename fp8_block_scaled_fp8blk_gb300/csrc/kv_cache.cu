@@ -15,6 +15,8 @@ namespace fp8blk {
 // ------------------------------------------------------------------ kv_map
 struct MapArgs {
     const int32_t *ctx_lens, *new_lens;  // [n]
+    const int32_t *held_blocks;          // [n] or null: blocks that a request has beside those of its context
+    int32_t *held_out;                   // [n], with held_blocks
     int32_t *table;                      // [n, width]
     const int32_t *free_blocks;          // [n_free]
     const int32_t *free_head;            // [1]
@@ -32,7 +34,8 @@ constexpr int kMapPerThread = 4;  // consecutive tokens of one thread: 32-byte s
 
 // One request's lengths, bounded: negative lengths count as zero, a sum past
 // 2^31 - 1 stops there.  `held` and `wanted` are its blocks before and after,
-// never more than the table is wide.
+// never more than the table is wide.  A request whose last rows were rejected
+// holds more blocks than its context needs.
 struct MapRequest {
     int32_t ctx, fresh, held, wanted;
     bool bad;
@@ -47,8 +50,13 @@ __device__ __forceinline__ MapRequest map_request(const MapArgs &a, int r) {
     const int64_t up = (1 << a.block_log2) - 1;
     const int32_t need = static_cast<int32_t>((len + up) >> a.block_log2);
     q.held = min(static_cast<int32_t>((q.ctx + up) >> a.block_log2), a.width);
-    q.wanted = min(need, a.width);
     q.bad = c < 0 || f < 0 || need > a.width;
+    if (a.held_blocks) {
+        const int32_t h = a.held_blocks[r];
+        q.held = max(q.held, min(h, a.width));
+        q.bad |= h < 0 || h > a.width;
+    }
+    q.wanted = max(min(need, a.width), q.held);
     return q;
 }
 
@@ -108,12 +116,15 @@ __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const MapArgs a) {
     const int64_t head = max(head_in, 0);
 
     if (blockIdx.x == 0) {  // per-request outputs, the new head and the status
-        int64_t at = s_tok[tid];
+        int64_t at = s_tok[tid], left = a.n_free - head - s_blk[tid];  // ids left for the request
         for (int r = r0; r < r1; ++r) {
             const MapRequest m = map_request(a, r);
             a.seq_lens[r] = m.ctx + m.fresh;
             a.q_starts[r] = static_cast<int32_t>(min(at, a.max_tokens));
             at += m.fresh;
+            const int32_t need = m.wanted - m.held;
+            if (a.held_out) a.held_out[r] = m.held + static_cast<int32_t>(min(max(left, int64_t(0)), static_cast<int64_t>(need)));
+            left -= need;
         }
         if (tid == 0) {
             a.q_starts[a.n] = static_cast<int32_t>(min(total, a.max_tokens));
@@ -484,29 +495,40 @@ __global__ void __launch_bounds__(kAppendThreads, WHOLE ? 6 : 2) kv_append_kerne
 
 using namespace fp8blk;
 
-extern "C" int fp8blk_kv_map(const int32_t *ctx_lens, const int32_t *new_lens, int32_t *block_table,
-                             const int32_t *free_blocks, const int32_t *free_head, int32_t *seq_lens, int32_t *q_starts,
-                             int64_t *slots, int32_t *positions, int32_t *free_head_out, int n_seqs, int max_blocks,
-                             int n_free, int block_tokens, int64_t max_tokens, void *stream) {
+extern "C" int fp8blk_kv_map_held(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *held_blocks,
+                                  int32_t *block_table, const int32_t *free_blocks, const int32_t *free_head,
+                                  int32_t *seq_lens, int32_t *q_starts, int64_t *slots, int32_t *positions,
+                                  int32_t *free_head_out, int32_t *held_out, int n_seqs, int max_blocks, int n_free,
+                                  int block_tokens, int64_t max_tokens, void *stream) {
     if (!ctx_lens || !new_lens || !block_table || !free_blocks || !free_head || !seq_lens || !q_starts || !slots ||
-        !positions || !free_head_out)
+        !positions || !free_head_out || !held_blocks != !held_out)
         return FP8BLK_EINVAL;
     if (n_seqs < 1 || max_blocks < 1 || n_free < 0 || !step_block_ok(block_tokens) || max_tokens < 1) return FP8BLK_EINVAL;
     if (n_seqs > 65536 || max_tokens > kStepMaxIndex) return FP8BLK_ERANGE;
     if (!step_aligned(ctx_lens, 4) || !step_aligned(new_lens, 4) || !step_aligned(block_table, 4) ||
         !step_aligned(free_blocks, 4) || !step_aligned(free_head, 4) || !step_aligned(seq_lens, 4) ||
-        !step_aligned(q_starts, 4) || !step_aligned(free_head_out, 4) || !step_aligned(slots, 16) ||
-        !step_aligned(positions, 16))
+        !step_aligned(q_starts, 4) || !step_aligned(free_head_out, 4) || !step_aligned(held_blocks, 4) ||
+        !step_aligned(held_out, 4) || !step_aligned(slots, 16) || !step_aligned(positions, 16))
         return FP8BLK_EALIGN;
-    if (free_head == free_head_out || seq_lens == ctx_lens || seq_lens == new_lens) return FP8BLK_EINVAL;
+    if (free_head == free_head_out || seq_lens == ctx_lens || seq_lens == new_lens ||
+        (held_out && (held_out == held_blocks || held_out == ctx_lens || held_out == new_lens)))
+        return FP8BLK_EINVAL;
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
-    MapArgs a = {ctx_lens, new_lens, block_table, free_blocks, free_head, seq_lens, q_starts, slots, positions,
-                 free_head_out, dev.status, n_seqs, max_blocks, n_free, step_log2(block_tokens), max_tokens};
+    MapArgs a = {ctx_lens, new_lens, held_blocks, held_out, block_table, free_blocks, free_head, seq_lens, q_starts, slots,
+                 positions, free_head_out, dev.status, n_seqs, max_blocks, n_free, step_log2(block_tokens), max_tokens};
     int64_t grid = (max_tokens + kMapThreads * kMapPerThread - 1) / (kMapThreads * kMapPerThread);
     if (grid > 3 * dev.sms) grid = 3 * dev.sms;
     return step_from_cuda(step_launch(kv_map_kernel, dim3(static_cast<unsigned>(grid)), kMapThreads, 0,
                                       static_cast<cudaStream_t>(stream), a));
+}
+
+extern "C" int fp8blk_kv_map(const int32_t *ctx_lens, const int32_t *new_lens, int32_t *block_table,
+                             const int32_t *free_blocks, const int32_t *free_head, int32_t *seq_lens, int32_t *q_starts,
+                             int64_t *slots, int32_t *positions, int32_t *free_head_out, int n_seqs, int max_blocks,
+                             int n_free, int block_tokens, int64_t max_tokens, void *stream) {
+    return fp8blk_kv_map_held(ctx_lens, new_lens, nullptr, block_table, free_blocks, free_head, seq_lens, q_starts, slots,
+                              positions, free_head_out, nullptr, n_seqs, max_blocks, n_free, block_tokens, max_tokens, stream);
 }
 
 extern "C" int fp8blk_kv_append(const void *k, const void *v, int dtype, const int64_t *slots, uint8_t *k_codes,

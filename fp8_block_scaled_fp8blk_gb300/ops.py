@@ -57,6 +57,8 @@ _lib.mxfp4_expert_gemv.restype = _INT
 _lib.mxfp4_expert_gemv.argtypes = [_P, _P, _INT, _P, _INT, _P, _P, _I64, _I64, _P]
 _lib.fp8blk_kv_map.restype = _INT
 _lib.fp8blk_kv_map.argtypes = [_P] * 10 + [_INT] * 4 + [_I64, _P]
+_lib.fp8blk_kv_map_held.restype = _INT
+_lib.fp8blk_kv_map_held.argtypes = [_P] * 12 + [_INT] * 4 + [_I64, _P]
 _lib.fp8blk_kv_append.restype = _INT
 _lib.fp8blk_kv_append.argtypes = [_P, _P, _INT, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _INT, _INT, _INT, _P]
 _lib.fp8blk_kv_attn_ws_bytes.restype = ctypes.c_size_t
@@ -377,8 +379,12 @@ def kv_map_buffers(n: int, max_tokens: int, device) -> KvMap:
 
 
 def fp8blk_kv_map(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_blocks: torch.Tensor,
-                  free_head: torch.Tensor, block_tokens: int, max_tokens: int, out: KvMap | None = None) -> KvMap:
-    """Block tables (updated in place), slots and positions of one step, from the requests' lengths on the device."""
+                  free_head: torch.Tensor, block_tokens: int, max_tokens: int, out: KvMap | None = None,
+                  held: torch.Tensor | None = None, held_out: torch.Tensor | None = None) -> KvMap:
+    """Block tables (updated in place), slots and positions of one step, from the requests' lengths on the device.
+
+    Where tokens of earlier steps may have been rejected, `held` [n] counts the blocks that each request has (0 at first) and
+    `held_out` [n], another tensor, receives the next step's counts, so that no block is taken twice."""
     n, width = block_table.shape
     if out is None:
         out = kv_map_buffers(n, max_tokens, block_table.device)
@@ -387,14 +393,20 @@ def fp8blk_kv_map(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     if (out.seq_lens.numel() != n or out.q_starts.numel() != n + 1 or out.slots.numel() != max_tokens
             or out.positions.numel() != max_tokens or out.free_head.numel() != 1):
         raise ValueError("out does not fit (see kv_map_buffers)")
+    if (held is None) != (held_out is None) or (held is not None and (held.numel() != n or held_out.numel() != n)):
+        raise ValueError("held and held_out go together, one entry each per row of block_table")
     i32, dev = torch.int32, block_table.get_device()
-    _check(_lib.fp8blk_kv_map(_typed(ctx_lens, i32, "ctx_lens", dev), _typed(new_lens, i32, "new_lens", dev),
-                              _typed(block_table, i32, "block_table", dev), _typed(free_blocks, i32, "free_blocks", dev),
-                              _typed(free_head, i32, "free_head", dev), _typed(out.seq_lens, i32, "out.seq_lens", dev),
-                              _typed(out.q_starts, i32, "out.q_starts", dev), _typed(out.slots, _I64T, "out.slots", dev),
-                              _typed(out.positions, i32, "out.positions", dev), _typed(out.free_head, i32, "out.free_head", dev),
-                              n, width, free_blocks.numel(), block_tokens, max_tokens, _stream(block_table)),
-           "fp8blk_kv_map")
+    rc = _lib.fp8blk_kv_map_held(_typed(ctx_lens, i32, "ctx_lens", dev), _typed(new_lens, i32, "new_lens", dev),
+                                 None if held is None else _typed(held, i32, "held", dev),
+                                 _typed(block_table, i32, "block_table", dev), _typed(free_blocks, i32, "free_blocks", dev),
+                                 _typed(free_head, i32, "free_head", dev), _typed(out.seq_lens, i32, "out.seq_lens", dev),
+                                 _typed(out.q_starts, i32, "out.q_starts", dev), _typed(out.slots, _I64T, "out.slots", dev),
+                                 _typed(out.positions, i32, "out.positions", dev),
+                                 _typed(out.free_head, i32, "out.free_head", dev),
+                                 None if held_out is None else _typed(held_out, i32, "held_out", dev),
+                                 n, width, free_blocks.numel(), block_tokens, max_tokens, _stream(block_table))
+    if rc:
+        _check(rc, "fp8blk_kv_map")
     return out
 
 

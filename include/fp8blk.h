@@ -320,8 +320,10 @@ int mxfp4_expert_gemv(const uint8_t *codes, const uint8_t *scales, int n_experts
  *   *free_head_out = *free_head + the number of ids taken.
  * Entries i of slots and positions past the last new token are -1, so a step
  * captured once with max_tokens rows serves every batch that fits.
- * A pass that only appends needs no copy between calls: *free_head_out is the
- * next call's *free_head (the two must not be the same address).
+ * *free_head_out is the next call's *free_head (the two must not be the same
+ * address).  Blocks are taken for all new tokens; where some of them may be
+ * rejected afterwards (a verify step), the next call would take a rejected
+ * token's block once more: such a loop calls fp8blk_kv_map_held.
  * When the free list runs out, the missing blocks' table entries and slots are
  * -1 and FP8BLK_STATUS_KV_EXHAUSTED is set.  Tokens beyond the table's width
  * get slot -1, starts beyond max_tokens stop there, negative lengths count as
@@ -342,6 +344,26 @@ int fp8blk_kv_map(const int32_t *ctx_lens, const int32_t *new_lens, int32_t *blo
                   const int32_t *free_head, int32_t *seq_lens, int32_t *q_starts, int64_t *slots, int32_t *positions,
                   int32_t *free_head_out, int n_seqs, int max_blocks, int n_free, int block_tokens, int64_t max_tokens,
                   void *stream);
+
+/*
+ * fp8blk_kv_map_held -- the same for requests that may hold more blocks than
+ * their context needs, because tokens of earlier steps were rejected.  Request
+ * s holds the blocks of its table entries [0, h), h = max(held_blocks[s],
+ * ceil(ctx / B)): these entries are read and kept, and [h, ceil((ctx + new) / B))
+ * are filled.  held_out[s] is the number it holds afterwards, without those that
+ * the free list could not give, and the next call's held_blocks[s]: every id of
+ * the free list then lies in one table entry or in the rest of the list.
+ * (A finished request's ids are its table's entries [0, held_out[s]).)
+ *   held_blocks  device, int32 [n_seqs]; 0 for a new request.  A negative count
+ *                is 0, one past max_blocks is max_blocks; both set
+ *                FP8BLK_STATUS_BAD_KV
+ *   held_out     device, int32 [n_seqs], not held_blocks itself
+ * Both may be NULL: then this is fp8blk_kv_map.
+ */
+int fp8blk_kv_map_held(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *held_blocks, int32_t *block_table,
+                       const int32_t *free_blocks, const int32_t *free_head, int32_t *seq_lens, int32_t *q_starts,
+                       int64_t *slots, int32_t *positions, int32_t *free_head_out, int32_t *held_out, int n_seqs,
+                       int max_blocks, int n_free, int block_tokens, int64_t max_tokens, void *stream);
 
 /*
  * fp8blk_kv_append -- write new keys and values into the cache.  A run is a
