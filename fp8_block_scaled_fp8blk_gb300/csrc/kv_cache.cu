@@ -500,8 +500,8 @@ extern "C" int fp8blk_kv_map_held(const int32_t *ctx_lens, const int32_t *new_le
                                   int32_t *seq_lens, int32_t *q_starts, int64_t *slots, int32_t *positions,
                                   int32_t *free_head_out, int32_t *held_out, int n_seqs, int max_blocks, int n_free,
                                   int block_tokens, int64_t max_tokens, void *stream) {
-    if (!ctx_lens || !new_lens || !block_table || !free_blocks || !free_head || !seq_lens || !q_starts || !slots ||
-        !positions || !free_head_out || !held_blocks != !held_out)
+    if (!ctx_lens || !new_lens || !block_table || (!free_blocks && n_free != 0) || !free_head || !seq_lens || !q_starts ||
+        !slots || !positions || !free_head_out || !held_blocks != !held_out)
         return FP8BLK_EINVAL;
     if (n_seqs < 1 || max_blocks < 1 || n_free < 0 || !step_block_ok(block_tokens) || max_tokens < 1) return FP8BLK_EINVAL;
     if (n_seqs > 65536 || max_tokens > kStepMaxIndex) return FP8BLK_ERANGE;

@@ -331,6 +331,7 @@ int mxfp4_expert_gemv(const uint8_t *codes, const uint8_t *scales, int n_experts
  *   ctx_lens, new_lens   device, int32 [n_seqs]
  *   block_table          device, int32 [n_seqs, max_blocks], updated in place
  *   free_blocks          device, int32 [n_free]: ids in the order they are taken
+ *                        (may be NULL if n_free is 0)
  *   free_head            device, int32 [1]: ids of free_blocks already taken
  *   seq_lens, q_starts   device, int32 [n_seqs], [n_seqs + 1]
  *   slots                device, int64 [max_tokens], 16-byte aligned

@@ -140,3 +140,17 @@ def test_verify_loop_example(ops):
     assert np.array_equal(np.sort(owned), np.arange(len(owned))) and len(owned) == cache.k_codes.shape[0]
     assert (h >= ceil(lens.cpu().numpy(), cache.block_tokens)).all()
     assert accepted.min() >= 1 and accepted.sum() < 6 * 3 * 8
+
+
+def test_an_empty_free_list(ops):
+    """A step whose tokens all fit in blocks that the requests have; then one that needs a block."""
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    table = torch.tensor([[5, -1], [2, 9]], dtype=torch.int32, device=DEV)
+    head = torch.zeros(1, dtype=torch.int32, device=DEV)
+    one = torch.ones(2, dtype=torch.int32, device=DEV)
+    got = ops.fp8blk_kv_map(to_dev(np.array([3, 20], np.int32)), one, table, none, head, 16, 4)
+    assert ops.fp8blk_device_status(clear=True) == 0
+    assert got.slots.tolist() == [5 * 16 + 3, 9 * 16 + 4, -1, -1] and int(got.free_head) == 0
+    got = ops.fp8blk_kv_map(to_dev(np.array([16, 20], np.int32)), one, table, none, head, 16, 4)
+    assert ops.fp8blk_device_status(clear=True) == ops.STATUS_KV_EXHAUSTED
+    assert got.slots.tolist() == [-1, 9 * 16 + 4, -1, -1] and table.tolist() == [[5, -1], [2, 9]]

@@ -35,3 +35,14 @@ def test_binding(ops):
             ops.fp8blk_kv_map(lens, lens, table, lens, lens, 16, 8, **kw)
     with pytest.raises(TypeError):
         ops.fp8blk_kv_map(lens, lens, table, lens, lens, 16, 8, held=lens.long(), held_out=lens)
+
+
+def test_an_empty_free_list_may_be_null(ops):
+    """Refused for another reason only (a launch would need a GPU)."""
+    lib = ops.raw_library()
+
+    def call(free, n_free, most=64):
+        return lib.fp8blk_kv_map(A4, A8, A4, free, A4, A16, A4, A16, A16, A8, 4, 8, n_free, 16, most, None)
+
+    assert call(None, 10) == ops.EINVAL
+    assert call(None, 0, most=1 << 31) == ops.ERANGE
