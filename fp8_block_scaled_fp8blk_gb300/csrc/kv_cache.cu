@@ -230,6 +230,7 @@ struct AppendArgs {
     int64_t n_slots;                       // n_blocks * block_tokens
     int kv_heads, head_dim, block_log2;
     int chunk;                             // tokens a CTA looks after
+    int checks, check_words;               // CTAs that look for blocks with two runs, words of their bitmaps
     int staged;                            // values of one run that shared memory holds (0: none)
     uint32_t per_inverse;                  // ceil(2^32 / (head_dim / 8)): divides group numbers below 2^16
 };
@@ -302,6 +303,8 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int kAppendHeld = 4;       // groups of eight values a thread keeps between its two passes
 constexpr int kAppendMaxChunk = 64;  // tokens a CTA looks after
+constexpr int kCheckWords = 1024;    // words of a bitmap of blocks, at most (more would take L1 from the CTAs that write)
+constexpr int kCheckAhead = 8;       // slots of a thread in flight
 
 // The token of group i of a run (i < 128 x 32): i / (head_dim / 8) by its inverse,
 // exact (the excess, i x (head_dim / 8) / 2^32, is below one group).
@@ -412,6 +415,38 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
     if (tid == 0) *scale = s;
 }
 
+// Two runs in one block would be written by two CTAs at once.  CTA c of the first
+// few marks the blocks of its range in a bitmap, run by run, and flags what is
+// marked twice: one pass over the slots beside the CTAs that write (no time of its
+// own with 64 tokens, 16.7 k or 131 k of 8 heads; 131 k of one head in a pool of
+// two million blocks wait for it, 80 us instead of 32).
+__device__ __noinline__ void append_check(const int64_t *slots, int64_t n_tokens, int64_t n_slots, int block_log2,
+                                          int check_words, unsigned int *status, uint32_t *bitmap, int c) {
+    const int tid = threadIdx.x, lane = tid & 31, block = 1 << block_log2;
+    const int64_t base = static_cast<int64_t>(c) * check_words * 32;
+    for (int i = tid; i < check_words; i += kAppendThreads) bitmap[i] = 0;
+    __syncthreads();
+    bool twice = false;
+    // A warp takes 32 x kCheckAhead consecutive slots at a time.
+    for (int64_t t0 = (tid >> 5) * 32 * kCheckAhead; t0 < n_tokens; t0 += kAppendThreads * kCheckAhead) {
+        int64_t mine[kCheckAhead], before = t0 > 0 ? slots[t0 - 1] : -1;
+#pragma unroll
+        for (int j = 0; j < kCheckAhead; ++j) mine[j] = t0 + 32 * j + lane < n_tokens ? slots[t0 + 32 * j + lane] : -1;
+#pragma unroll
+        for (int j = 0; j < kCheckAhead; ++j) {
+            const int64_t left = __shfl_up_sync(0xFFFFFFFFu, mine[j], 1), b = (mine[j] >> block_log2) - base;
+            if (lane > 0) before = left;
+            if (mine[j] >= 0 && mine[j] < n_slots && ((mine[j] & (block - 1)) == 0 || before != mine[j] - 1) && b >= 0 &&
+                b < static_cast<int64_t>(check_words) * 32) {
+                const uint32_t bit = 1u << (b & 31);
+                twice |= (atomicOr(bitmap + (b >> 5), bit) & bit) != 0;
+            }
+            before = __shfl_sync(0xFFFFFFFFu, mine[j], 31);
+        }
+    }
+    if (twice) atomicOr(status, FP8BLK_STATUS_BAD_KV);
+}
+
 // A run is a maximal group of consecutive tokens with consecutive slots of one
 // block; its first token leads it, and the CTA whose chunk holds that token
 // writes it.  Chunks with few leaders (prompts) take one run at a time with the
@@ -428,10 +463,16 @@ __global__ void __launch_bounds__(kAppendThreads, WHOLE ? 6 : 2) kv_append_kerne
     __shared__ uint32_t red[kAppendWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int h = blockIdx.y;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * a.chunk;
+    const int64_t t0 = (static_cast<int64_t>(blockIdx.x) - a.checks) * a.chunk;
     const int block = 1 << a.block_log2;
     grid_dependency_wait();
     grid_launch_dependents();
+    if (t0 < 0) {
+        if (h == 0 && blockIdx.z == 0)
+            append_check(a.slots, a.n_tokens, a.n_slots, a.block_log2, a.check_words, a.status,
+                         reinterpret_cast<uint32_t *>(append_smem), static_cast<int>(blockIdx.x));
+        return;
+    }
     // Where runs start, in the chunk and as far past it as its last run can reach (chunk + block <= 192 tokens).
     const int64_t mine = t0 + tid < a.n_tokens ? a.slots[t0 + tid] : -1;
     const int64_t before = t0 + tid > 0 && t0 + tid < a.n_tokens ? a.slots[t0 + tid - 1] : -1;
@@ -546,7 +587,7 @@ extern "C" int fp8blk_kv_append(const void *k, const void *v, int dtype, const i
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
     AppendArgs a = {k, v, slots, k_codes, v_codes, k_scales, v_scales, dev.status, n_tokens, k_stride, v_stride,
-                    n_blocks * block_tokens, kv_heads, head_dim, step_log2(block_tokens), 4, 0,
+                    n_blocks * block_tokens, kv_heads, head_dim, step_log2(block_tokens), 4, 0, 0, 0,
                     static_cast<uint32_t>(((uint64_t(1) << 32) + head_dim / 8 - 1) / (head_dim / 8))};
     // Tokens per CTA: about one run of a prompt when there are tokens enough to fill the SMs, down to a few tokens (a
     // warp each) for a decode step.
@@ -554,9 +595,11 @@ extern "C" int fp8blk_kv_append(const void *k, const void *v, int dtype, const i
     // K and V by the same CTA where it takes whole runs, by CTAs of their own where a warp does.  Runs are staged in
     // shared memory up to 32 KiB (three CTAs per SM or more).
     const bool whole = a.chunk > 8;
-    const dim3 grid(static_cast<unsigned>((n_tokens + a.chunk - 1) / a.chunk), static_cast<unsigned>(kv_heads), whole ? 1 : 2);
     if (whole) a.staged = std::min(block_tokens * head_dim, 32768 / es);
-    const size_t smem = static_cast<size_t>(a.staged) * 2 * es;
+    a.check_words = static_cast<int>(std::min<int64_t>((n_blocks + 31) / 32, kCheckWords));
+    a.checks = static_cast<int>((n_blocks + a.check_words * 32ll - 1) / (a.check_words * 32ll));
+    const dim3 grid(static_cast<unsigned>(a.checks + (n_tokens + a.chunk - 1) / a.chunk), static_cast<unsigned>(kv_heads), whole ? 1 : 2);
+    const size_t smem = std::max(static_cast<size_t>(a.staged) * 2 * es, a.check_words * sizeof(uint32_t));
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto launch = [&](auto kernel) {
         int per_sm = 0;

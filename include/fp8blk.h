@@ -383,7 +383,9 @@ int fp8blk_kv_map_held(const int32_t *ctx_lens, const int32_t *new_lens, const i
  *              fused projection), 16-byte aligned rows
  *   dtype      FP8BLK_F32 or FP8BLK_BF16, of k and v
  *   slots      device, int64 [n_tokens]; negative = skip the token
- * In one call, no two runs may lie in the same block.
+ * In one call, no two runs may lie in the same block (tokens of two requests
+ * in turn, rows out of order, or a token skipped inside a block make two): what
+ * such a block holds afterwards is undefined, and FP8BLK_STATUS_BAD_KV is set.
  * A slot at or past n_blocks * block_tokens is skipped and sets
  * FP8BLK_STATUS_BAD_KV.
  * Errors: EINVAL (also a stride that is no multiple of 16 bytes, or shorter

@@ -109,3 +109,27 @@ def test_few_tokens_that_are_not_finite(ops, dtype):
     for y, gc, gs in ((d, dev[0], dev[1]), (-d, dev[2], dev[3])):
         wc, ws = ref.kv_append(y.float().cpu().numpy().astype(np.float64), slots, kc, ks, 16)
         assert np.array_equal(gs.cpu().numpy().astype(np.float64), ws) and ref.same_codes(gc.cpu().numpy(), wc)
+
+
+@pytest.mark.parametrize("n,heads,block,blocks", [(4, 1, 16, 3), (64, 8, 64, 70), (3000, 8, 16, 700), (3000, 1, 128, 20),
+                                                  (200, 2, 16, 600000)])
+def test_two_runs_in_one_block_are_flagged(ops, n, heads, block, blocks):
+    """Rows out of order, tokens of two requests in turn, a token skipped inside a block, one slot twice; near and far apart,
+    in the first and the last blocks of a pool.  The same tokens in order raise nothing."""
+    shape = (blocks, heads, block, 16)
+    dev = [torch.zeros(shape, dtype=torch.uint8, device="cuda:0"), torch.zeros(shape[:2], device="cuda:0")]
+    dev += [torch.zeros_like(t) for t in dev]
+    x = torch.ones((n, heads, 16), device="cuda:0")
+    span = min(n, blocks * block)
+    good = np.full(n, -1, np.int64)
+    good[:span] = np.arange(span) + (blocks * block - span)  # the pool's last blocks
+    swapped, turns, twice, hole = good.copy(), good.copy(), good.copy(), good.copy()
+    at = next(t for t in range(span - 1) if good[t] % block == block - 3) if span >= block else 0
+    swapped[[at, at + 1]] = swapped[[at + 1, at]]
+    half = span // 2
+    turns[0: 2 * half: 2], turns[1: 2 * half: 2] = good[:half], good[half: 2 * half]
+    twice[span - 1] = twice[0]
+    hole[at + 1] = -1
+    for slots, bad in ((good, False), (swapped, True), (turns, True), (twice, True), (hole, True), (good, False)):
+        ops.fp8blk_kv_append(x, x, to_dev(slots), *dev)
+        assert ops.fp8blk_device_status(clear=True) == (ops.STATUS_BAD_KV if bad else 0)
