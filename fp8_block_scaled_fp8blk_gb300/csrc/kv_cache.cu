@@ -256,6 +256,30 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// Scales written here are powers of two, and products and quotients by them exact; one that was there may be any number.
+// q, the f32 next to a result, and the sign of what it leaves of it: rounded to odd instead, so that rounding q to e4m3
+// rounds the result once.
+__device__ __forceinline__ float round_to_odd(float q, float left) {
+    const uint32_t u = __float_as_uint(q);
+    if (left == 0.f || q == 0.f || (u & 1u)) return q;
+    return __uint_as_float((left > 0.f) == (q > 0.f) ? u + 1u : u - 1u);
+}
+__device__ __forceinline__ float times_to_odd(float a, float b) {
+    const float p = a * b;
+    return round_to_odd(p, fmaf(a, b, -p));
+}
+// x / s from inv = 1 / s and one correction of the quotient by its remainder (Markstein); all brought up where a
+// remainder would be too small for an f32.
+__device__ __forceinline__ float over_to_odd(float x, float s, float inv) {
+    const bool small = s < 0x1p-60f;
+    x = small ? x * 0x1p60f : x;
+    s = small ? s * 0x1p60f : s;
+    inv = small ? inv * 0x1p-60f : inv;
+    float q = x * inv;
+    q = fmaf(fmaf(-q, s, x), inv, q);
+    return round_to_odd(q, fmaf(-q, s, x));
+}
+__device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7FFFFFu) == 0; }
 __device__ __forceinline__ float poison_inf(float v) { return isfinite(v) ? v : __int_as_float(0x7FC00000); }
 
 // Eight consecutive values as they lie in memory: two or one 16-byte words.
@@ -384,14 +408,15 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
     }
     float s = __uint_as_float(static_cast<uint32_t>(scale_exponent(amax)) << 23);
     if (off > 0) {
-        if (old < s) {  // the codes that were there follow the larger scale: a product by a power of two, rounded once
+        if (old < s) {  // the codes that were there follow the larger scale
             const float ratio = old / s;
             uint32_t *w = reinterpret_cast<uint32_t *>(codes);
 #pragma unroll 1
             for (int i = tid; i < off * per * 2; i += THREADS) {
                 float2 lo, hi;
                 e4m3x4_to_f32(w[i], lo, hi);
-                w[i] = to_e4m3x2(lo.x * ratio, lo.y * ratio) | (to_e4m3x2(hi.x * ratio, hi.y * ratio) << 16);
+                w[i] = to_e4m3x2(times_to_odd(lo.x, ratio), times_to_odd(lo.y, ratio)) |
+                       (to_e4m3x2(times_to_odd(hi.x, ratio), times_to_odd(hi.y, ratio)) << 16);
             }
         } else {
             s = old;
@@ -399,17 +424,33 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
     }
     const float inv = 1.0f / s;
     uint2 *w = reinterpret_cast<uint2 *>(codes + static_cast<int64_t>(off) * D);
-    over_run([&](const Eight<T> &e, int i) {
-        float f[8];
-        e.get(f);
-        if (infinite) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = poison_inf(f[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= inv;
+    auto encode = [&](const float (&f)[8], int i) {
         w[i] = make_uint2(to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16), to_e4m3x2(f[4], f[5]) | (to_e4m3x2(f[6], f[7]) << 16));
-    });
+    };
+    if (power_of_two(s)) {
+        over_run([&](const Eight<T> &e, int i) {
+            float f[8];
+            e.get(f);
+            if (infinite) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = poison_inf(f[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= inv;
+            encode(f, i);
+        });
+    } else {  // (a loop of its own: as a branch in the other one it cost prompts 4%)
+#pragma unroll 1
+        for (int i = tid; i < total; i += THREADS) {
+            Eight<T> e;
+            float f[8];
+            e.load(at(i));
+            e.get(f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = over_to_odd(poison_inf(f[j]), s, inv);
+            encode(f, i);
+        }
+    }
     if constexpr (THREADS > 32) __syncthreads();  // red, the staged values and the old scale have been read
     else __syncwarp();
     if (tid == 0) *scale = s;

@@ -375,7 +375,8 @@ int fp8blk_kv_map_held(const int32_t *ctx_lens, const int32_t *new_lens, const i
  *       earlier tokens (the run does not start at row 0), s = max(s, old scale);
  *   code = e4m3(x / s), nearest even; NaN and infinities become the NaN code;
  *   if s is larger than the old scale, the codes of the block's earlier rows
- *   become e4m3(e4m3(code) * old / s).
+ *   become e4m3(e4m3(code) * old / s).  Each is rounded once, also where the
+ *   old scale is no power of two.
  * So a block's scale never shrinks while it fills, and row 0 starts it afresh
  * (a block that is reused, or rolled back to empty, needs no clearing).
  *   k, v       device, f32 or bf16 [n_tokens, kv_heads, head_dim], tokens
