@@ -51,12 +51,13 @@
 // from tensor memory twice rather than kept: unrolled over 32 rows, the roles'
 // code did not fit the instruction caches, and that was the largest stall.
 //   Bound: HBM for few query rows, the softmax groups for many (a tile of 32
-// rows of f32 takes a group about 7000 cycles: 1500 for the maxima, 3500 for
-// weights, planes and sums, the rest waits and barriers; of eight rows of bf16,
-// 2400).  Measured in a graph, 8 cache heads of 128: 64 requests of 4.2 k tokens
-// on average, eight bf16 rows a head, 101 us (82% of the copy rate); one of
-// 131072 tokens 54 us (74%: start-up and join take the rest); 16 of 8.4 k with
-// 4..32 f32 rows a head 107 us (39%).
+// rows of f32 took a group about 7000 cycles when references were the tile's:
+// 1500 for the maxima, 3500 for weights, planes and sums, the rest waits and
+// barriers; of eight rows of bf16, 2400).  Measured in a graph, 8 cache heads of
+// 128: 64 requests of 4.2 k tokens on average, eight bf16 rows a head, 105 us
+// (79% of the copy rate); one of 131072 tokens 54 us (74%: start-up and join take
+// the rest); 16 of 8.4 k with 4..32 f32 rows a head 111 us (37%).  With one
+// reference per tile, less exact, these were 101, 54 and 108 us.
 //   Measured slower (the last case, then at 119 us): 16 rows at a time (141), a
 // third softmax group (140), the planes as a loop over their weights (123);
 // redux.sync for the maxima, both products of a tile from one issuer in order,
@@ -291,7 +292,8 @@ __device__ __forceinline__ AttnSeq at_seq(const AttnArgs &a, int s) {
     // A length past the table ends in a tile past it, whose scales are NaN: every row sees some of it.
     q.tiles = min((q.len >> 7) + ((q.len & 127) != 0), a.max_tiles);
     q.groups = (q.rows * a.group + R - 1) / R;
-    // Measured on f32 tiles of 8, 16 and 32 rows: 1.1, 1.5 and 1.9 us, about (3 + eighths) x 0.28.
+    // Measured on f32 tiles of 8, 16 and 32 rows: 1.1, 1.5 and 1.9 us, about (3 + eighths) x 0.28.  (Lists of bf16 are
+    // cut by the same figures, which were not measured for them.)
     q.weight = R == 8 ? 1 : 3 + min(R, q.rows * a.group + 7) / 8;
     return q;
 }

@@ -65,8 +65,8 @@ __device__ __forceinline__ MapRequest map_request(const MapArgs &a, int r) {
 // outputs: tokens and fresh table entries, each found by a search in the scan.
 // Thread i scans requests [i q, (i + 1) q), q = ceil(n / 512).
 //   Bound: latency (the scan, then a search of nine dependent steps).  Measured
-// in a graph: 64 requests of one token 4.9 us; 512 requests with 2.1 M new
-// tokens 12.8 us, 3.9 of them what the bytes take.
+// in a graph: 64 requests of one token 5.1 us; 512 requests with 2.1 M new
+// tokens 12.7 us, 3.9 of them what the bytes take.
 __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const MapArgs a) {
     __shared__ int64_t s_tok[kMapThreads + 1], s_blk[kMapThreads + 1];  // exclusive prefixes per thread
     __shared__ int64_t w_tok[kMapThreads / 32], w_blk[kMapThreads / 32];
@@ -493,10 +493,10 @@ __device__ __noinline__ void append_check(const int64_t *slots, int64_t n_tokens
 // writes it.  Chunks with few leaders (prompts) take one run at a time with the
 // whole CTA, chunks with many (decode) a warp per run.
 //   Bound: HBM for prompts (es bytes in, 1 out per value), latency for decode.
-// Measured in a graph: 16.7 k bf16 tokens of 16 prompts, 8 heads of 128, 24.0 us
-// (64% of the copy rate; ncu: 52% of the ALU pipe's issue and 36% of DRAM's
-// cycles busy, so what is left is the two passes over a run one after the
-// other); 64 tokens of f32, one a request, 2.7 us.
+// Measured in a graph: 16.7 k bf16 tokens of 16 prompts, 8 heads of 128, 24.2 us
+// (64% of the copy rate; ncu: 81% of the issue slots busy while an SM has work,
+// 35% of DRAM's throughput, and 2104 CTAs of 912 at a time leave the last wave a
+// third full); 64 tokens of f32, one a request, 2.8 us.
 template <typename T, bool WHOLE>
 __global__ void __launch_bounds__(kAppendThreads, WHOLE ? 6 : 2) kv_append_kernel(const AppendArgs a) {
     extern __shared__ __align__(16) uint8_t append_smem[];  // a run's values, K's and V's
@@ -630,8 +630,9 @@ extern "C" int fp8blk_kv_append(const void *k, const void *v, int dtype, const i
     AppendArgs a = {k, v, slots, k_codes, v_codes, k_scales, v_scales, dev.status, n_tokens, k_stride, v_stride,
                     n_blocks * block_tokens, kv_heads, head_dim, step_log2(block_tokens), 4, 0, 0, 0,
                     static_cast<uint32_t>(((uint64_t(1) << 32) + head_dim / 8 - 1) / (head_dim / 8))};
-    // Tokens per CTA: about one run of a prompt when there are tokens enough to fill the SMs, down to a few tokens (a
-    // warp each) for a decode step.
+    // Tokens per CTA: four, for a decode step, and twice as many again while that leaves eight chunks an SM.  From 16 on
+    // (9728 (token, head) pairs on 152 SMs) a CTA takes whole runs.  The rule goes by the total: one prompt of 1000 tokens
+    // and 8 heads is below it, and a warp writes each of its runs (15.5 us).
     while (a.chunk < kAppendMaxChunk && n_tokens * kv_heads * 2 / (2 * a.chunk) >= 8 * dev.sms) a.chunk *= 2;
     // K and V by the same CTA where it takes whole runs, by CTAs of their own where a warp does.  Runs are staged in
     // shared memory up to 32 KiB (three CTAs per SM or more).

@@ -148,7 +148,9 @@ struct LpSlice {
 // slice from below.  Only segments (a thread's four words, or more in a long
 // row) whose own maximum reaches it hold candidates: some 20 segments are read
 // again, out of L2, and the few candidates are ranked by counting.  Rows where
-// too many values tie with the bound are selected one by one.
+// too many values tie with the bound are selected one by one, a pass over the slice
+// each: rows of -inf with 5 or 100 other values take 71 us instead of 7.7 (8 rows),
+// 7.5 ms instead of 0.18 (2048).
 //   Bound: HBM (4 or 2 bytes a logit) for many rows of f32, at about 9
 // instructions a logit; instructions for bf16; the chain of joins for few rows.
 // Measured, top 20 and 131072 logits: 2048 rows of f32 187 us (86% of the copy
