@@ -918,17 +918,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     if (PD < kAtDeep && wg == 2 && it >= PD)
                         ok = at_wait(smem_addr(&o_full[(it - PD) & (kAtDeep - 1)]), static_cast<uint32_t>((it - PD) / kAtDeep) & 1u, &s_abort, a.wait_limit_ns) && ok;
                     if (tg < rows) {
-                        float exps[8], tref = kAtNoRef, most = -INFINITY;
-                        at_lds8(s_ve[g], exps);
+                        float part[8], exps[8], tref = kAtNoRef, most = -INFINITY;
 #pragma unroll
                         for (int x = 0; x < 8; ++x) {
-                            const float part = s_wmax[g][x][tg];
-                            tref = fmaxf(tref, part);
-                            most = fmaxf(most, part + exps[x]);
+                            part[x] = s_wmax[g][x][tg];
+                            tref = fmaxf(tref, part[x]);
                         }
                         const float now = fmaxf(ref, tref);
-                        // k: the largest p |s_v| is below 2^(k + 1).
-                        const int k = min(max(__float2int_ru(most - tref), max(ve - 127 - kAtSpread, kAtMinScale)), ve - 127);
+                        // k: the largest p |s_v| is below 2^(k + 1).  (The difference first: it is exact for scores of any size.)
+                        at_lds8(s_ve[g], exps);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) most = fmaxf(most, (part[x] - tref) + exps[x]);
+                        const int k = min(max(__float2int_ru(most), max(ve - 127 - kAtSpread, kAtMinScale)), ve - 127);
                         s_lift[b][tg] = __int_as_float((kAtPeakLog2 + ve - k) << 23);
                         s_lf[g][tg] = at_exp2(tref - now);
                         s_lc[g][tg] = at_exp2(ref - now);

@@ -93,3 +93,36 @@ def test_scales_that_are_not_finite(ops, dtype, value, heads, block):
                 lse2[first:4, heads // 2:] = lse[first:4, heads // 2:]
             assert torch.equal(lse2, lse)
     assert ops.fp8blk_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [1e3, 1e8, 1e14])
+@pytest.mark.parametrize("e", [12, 30, 90])
+@pytest.mark.parametrize("heads,block", [(4, 16), (16, 64)])
+def test_huge_scores_on_a_block_of_small_scale(ops, dtype, size, e, heads, block):
+    """Scores of up to 1e14: one token of a block of value scale 2^-e has all the weight, so the output is its value, to what
+    a weight of one keeps (a power of two: both planes hold it, 2^-20 of the sums)."""
+    c = Case([200], [2], heads, 1, 64, block, seed=61, spread=0)
+    rng = np.random.default_rng(62)
+    at = {0: 37, 1: 171}                                    # the token of each tile that can win; the second one does
+    c.vs[c.table[0]] = 1.0
+    for tile, t in at.items():
+        b, r = c.table[0, t // block], t % block
+        c.vs[b] = 2.0 ** -e
+        c.kc[b, 0, r] = ref.e4m3_encode(np.full(64, 448.0 if tile else 352.0))
+        c.ks[b] = c.ks[c.table[0]].max()
+    for b in c.table[0]:                                    # all others: below a quarter of it
+        keep = c.kc[b, 0].copy()
+        low = ref.E4M3[keep] * 0.2
+        for t in at.values():
+            if b == c.table[0, t // block]:
+                low[t % block] = ref.E4M3[keep[t % block]]
+        c.kc[b, 0] = np.where(keep & 0x7F == 0x7F, keep, ref.e4m3_encode(low))
+    c.ks[c.table[0]] = c.ks[c.table[0]].max()
+    c.q[:] = size / (448.0 * c.ks[c.table[0, 0], 0] * 64 * c.scale) * (1.0 + 0.02 * rng.standard_normal(c.q.shape))
+    out, lse, q = run(ops, c, dtype)
+    b, r = c.table[0, 171 // block], 171 % block
+    want = ref.E4M3[c.vc[b, 0, r]] * 2.0 ** -e
+    got = out.float().cpu().numpy().astype(np.float64)
+    bound = (2.0 ** -8 if dtype is torch.bfloat16 else 2.0 ** -16) * np.abs(want) + 2.0 ** -20 * 448.0 * 2.0 ** -e
+    assert (np.abs(got - want) <= bound).all(), float((np.abs(got - want) / bound).max())
