@@ -11,8 +11,9 @@ through one attention layer and the vocab head:
   fp8blk_gemv_argmax     vocab head: the greedy token and the logits of every row
   fp8blk_token_logprobs  each draft's log probability and rank, the entropy, and the likeliest alternatives
 
-A draft is accepted while it is the greedy token of the row before it.  Weights are random; a real engine runs the
-middle part once per layer.  Run: python examples/verify_step.py
+A draft is accepted while it is the greedy token of the row before it.  Then loop() runs steps in a row: rejected rows'
+slots are written again, and a block that only they had reached stays their request's.  Weights are random; a real engine
+runs the middle part once per layer.  Run: python examples/verify_step.py
 """
 from __future__ import annotations
 
