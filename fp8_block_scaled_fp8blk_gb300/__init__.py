@@ -11,6 +11,7 @@ _BINDING_NAMES = (
     "nvfp4_expert_dequant", "nvfp4_expert_dequant_gemv", "nvfp4_expert_gemv", "mxfp4_expert_gemv",
     "fp8blk_scales_from_e8m0",
     "fp8blk_device_status", "Fp8BlkError", "library_path", "argmax_workspace",
+    "rope_frequencies", "rope_turns", "fp8blk_rope_table", "fp8blk_rope", "fp8blk_kv_append_rope",
     "fp8blk_kv_map", "kv_map_buffers", "KvMap", "fp8blk_kv_append", "fp8blk_kv_attn", "fp8blk_kv_attn_ws_bytes",
     "kv_attn_workspace", "fp8blk_token_logprobs", "token_logprobs_buffers", "TokenLogprobs",
     "set_launch_tuning", "abi_version",

@@ -1,14 +1,17 @@
 // kv_cache.cu -- the paged e4m3 cache of a decode / verify step: block tables
 // and slots from request lengths (fp8blk_kv_map), and keys and values written
-// with one power-of-two scale per (block of tokens, head) (fp8blk_kv_append).
+// with one power-of-two scale per (block of tokens, head) (fp8blk_kv_append),
+// the keys rotated on their way there (fp8blk_kv_append_rope).
 //
 // A pool holds uint8 e4m3 codes [n_blocks, kv_heads, block_tokens, head_dim]
 // and f32 scales [n_blocks, kv_heads].  Head-major inside a block: what one
 // head reads of one block is a single run of block_tokens x head_dim bytes
 // under one scale.
+#include "rope.cuh"
 #include "step.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace fp8blk {
 
@@ -234,6 +237,13 @@ struct AppendArgs {
     int staged;                            // values of one run that shared memory holds (0: none)
     uint32_t per_inverse;                  // ceil(2^32 / (head_dim / 8)): divides group numbers below 2^16
 };
+// ... with keys that are rotated first, and queries that are rotated beside them.
+struct AppendRopeArgs : AppendArgs {
+    RopeArgs rope;       // the keys' (x, out and strides unused)
+    RopeArgs q;          // the queries'
+    uint32_t q_items;    // 0: no queries
+    int q_first;         // from this blockIdx.x on CTAs take the queries' items, kAppendThreads each
+};
 
 // |v| for a block's maximum: what is not finite does not count.
 __device__ __forceinline__ uint32_t finite_abs_bits(float v) {
@@ -288,6 +298,10 @@ struct Eight;
 template <>
 struct Eight<float> {
     float4 a, b;
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+        a = make_float4(v[0], v[1], v[2], v[3]);
+        b = make_float4(v[4], v[5], v[6], v[7]);
+    }
     __device__ __forceinline__ void load(const float *p) {
         a = *reinterpret_cast<const float4 *>(p);
         b = *reinterpret_cast<const float4 *>(p + 4);
@@ -342,9 +356,12 @@ __device__ __forceinline__ int append_row(const AppendArgs &a, int i) {
 // rest comes from L1 again); the CTA takes them from shared memory, where they
 // were copied for K and V at once, so that V's are on their way while K's are
 // encoded.  staged: null if the run does not fit there.  red: a word per warp.
-template <typename T, int THREADS, int kHeld>
-__device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64_t slot, int run, int h, bool is_v, int tid,
-                                           const T *staged, uint32_t *red) {
+// ROPE: keys, rotated in f32 as they are read (staged ones have been); the scale
+// and the codes go by the rotated values, unrounded.
+template <typename T, int THREADS, int kHeld, bool ROPE, typename A>
+__device__ __forceinline__ void append_run(const A &a, int64_t t, int64_t slot, int run, int h, bool is_v, int tid,
+                                           const std::conditional_t<ROPE, float, T> *staged, uint32_t *red) {
+    using Group = Eight<std::conditional_t<ROPE, float, T>>;
     const int D = a.head_dim, block = 1 << a.block_log2, off = static_cast<int>(slot & (block - 1));
     const int64_t stride = is_v ? a.v_stride : a.k_stride;
     const T *x = static_cast<const T *>(is_v ? a.v : a.k) + t * stride + static_cast<int64_t>(h) * D;
@@ -356,10 +373,20 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
         const int row = append_row(a, i);
         return x + row * stride + 8 * (i - row * per);
     };
-    Eight<T> held[kHeld + 1];
+    auto fetch = [&](Group &e, int i) {
+        if constexpr (ROPE) {
+            const int row = append_row(a, i);
+            float f[8];
+            rope_eight(a.rope, x + row * stride, a.rope.cos_sin + (t + row) * a.rope.rot, 8 * (i - row * per), f);
+            e.set(f);
+        } else {
+            e.load(at(i));
+        }
+    };
+    Group held[kHeld + 1];
 #pragma unroll
     for (int k = 0; k < kHeld; ++k)
-        if (tid + k * THREADS < total) held[k].load(at(tid + k * THREADS));
+        if (tid + k * THREADS < total) fetch(held[k], tid + k * THREADS);
     const float old = off > 0 ? *scale : 0.f;
     // Over all the run's groups, and over the threads.  (Magnitudes are not negative: their bits order as they do.)
     auto over_run = [&](auto f) {
@@ -369,15 +396,15 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
         if (THREADS > 32 && staged) {
 #pragma unroll 4
             for (int i = tid; i < total; i += THREADS) {
-                Eight<T> e;
+                Group e;
                 e.load(staged + 8 * i);
                 f(e, i);
             }
         } else {
 #pragma unroll 1
             for (int i = tid + kHeld * THREADS; i < total; i += THREADS) {
-                Eight<T> e;
-                e.load(at(i));
+                Group e;
+                fetch(e, i);
                 f(e, i);
             }
         }
@@ -392,13 +419,13 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
         return m;
     };
     float peak = 0.f;
-    over_run([&](const Eight<T> &e, int) { peak = e.peak(peak); });
+    over_run([&](const Group &e, int) { peak = e.peak(peak); });
     uint32_t amax = over_threads(__float_as_uint(peak));
     const bool infinite = amax >= 0x7F800000u;
     if (infinite) {  // not often: once more, infinities left out (NaN already are)
         if constexpr (THREADS > 32) __syncthreads();
         uint32_t m = 0;
-        over_run([&](const Eight<T> &e, int) {
+        over_run([&](const Group &e, int) {
             float f[8];
             e.get(f);
 #pragma unroll
@@ -428,7 +455,7 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
         w[i] = make_uint2(to_e4m3x2(f[0], f[1]) | (to_e4m3x2(f[2], f[3]) << 16), to_e4m3x2(f[4], f[5]) | (to_e4m3x2(f[6], f[7]) << 16));
     };
     if (power_of_two(s)) {
-        over_run([&](const Eight<T> &e, int i) {
+        over_run([&](const Group &e, int i) {
             float f[8];
             e.get(f);
             if (infinite) {
@@ -442,9 +469,9 @@ __device__ __forceinline__ void append_run(const AppendArgs &a, int64_t t, int64
     } else {  // (a loop of its own: as a branch in the other one it cost prompts 4%)
 #pragma unroll 1
         for (int i = tid; i < total; i += THREADS) {
-            Eight<T> e;
+            Group e;
             float f[8];
-            e.load(at(i));
+            fetch(e, i);
             e.get(f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = over_to_odd(poison_inf(f[j]), s, inv);
@@ -497,8 +524,11 @@ __device__ __noinline__ void append_check(const int64_t *slots, int64_t n_tokens
 // (64% of the copy rate; ncu: 81% of the issue slots busy while an SM has work,
 // 35% of DRAM's throughput, and 2104 CTAs of 912 at a time leave the last wave a
 // third full); 64 tokens of f32, one a request, 2.8 us.
-template <typename T, bool WHOLE>
-__global__ void __launch_bounds__(kAppendThreads, WHOLE ? 6 : 2) kv_append_kernel(const AppendArgs a) {
+//   With rotated keys (A = AppendRopeArgs) the CTA stages K as rotated f32, and
+// CTAs behind the cache's rotate the queries of the same rows.
+template <typename T, bool WHOLE, typename A>
+__global__ void __launch_bounds__(kAppendThreads, !WHOLE ? 2 : std::is_same_v<A, AppendArgs> ? 6 : 4) kv_append_kernel(const A a) {
+    constexpr bool ROPE = std::is_same_v<A, AppendRopeArgs>;
     extern __shared__ __align__(16) uint8_t append_smem[];  // a run's values, K's and V's
     __shared__ uint32_t s_starts[kAppendWarps], s_leads[kAppendWarps];  // a bit per token from the chunk's first on
     __shared__ uint32_t red[kAppendWarps];
@@ -508,6 +538,14 @@ __global__ void __launch_bounds__(kAppendThreads, WHOLE ? 6 : 2) kv_append_kerne
     const int block = 1 << a.block_log2;
     grid_dependency_wait();
     grid_launch_dependents();
+    if constexpr (ROPE) {
+        if (static_cast<int>(blockIdx.x) >= a.q_first) {
+            const uint32_t cta = ((blockIdx.x - a.q_first) * gridDim.y + blockIdx.y) * gridDim.z + blockIdx.z;
+            const uint32_t item = cta * kAppendThreads + tid;
+            if (item < a.q_items) rope_item<T, 1>(a.q, item);
+            return;
+        }
+    }
     if (t0 < 0) {
         if (h == 0 && blockIdx.z == 0)
             append_check(a.slots, a.n_tokens, a.n_slots, a.block_log2, a.check_words, a.status,
@@ -539,16 +577,17 @@ __global__ void __launch_bounds__(kAppendThreads, WHOLE ? 6 : 2) kv_append_kerne
         if constexpr (WHOLE) if (whole) {
             const int per = a.head_dim / 8, total = (end - i) * per;
             const bool fits = total * 8 <= a.staged;
-            T *buffer = reinterpret_cast<T *>(append_smem);
+            // K's values (rotated ones as f32), then V's.
+            using Key = std::conditional_t<ROPE, float, T>;
+            Key *k_staged = reinterpret_cast<Key *>(append_smem);
+            T *v_staged = reinterpret_cast<T *>(k_staged + a.staged);
             if (fits) {
-#pragma unroll 1
-                for (int v = 0; v < 2; ++v) {
-                    const int64_t stride = v ? a.v_stride : a.k_stride;
-                    const T *x = static_cast<const T *>(v ? a.v : a.k) + (t0 + i) * stride + static_cast<int64_t>(h) * a.head_dim;
+                auto copy = [&](const void *from, int64_t stride, T *to) {
+                    const T *x = static_cast<const T *>(from) + (t0 + i) * stride + static_cast<int64_t>(h) * a.head_dim;
                     for (int g = tid; g < total; g += kAppendThreads) {
                         const int row = append_row(a, g);
                         const T *src = x + row * stride + 8 * (g - row * per);
-                        const uint32_t dst = smem_addr(buffer + v * a.staged + 8 * g);
+                        const uint32_t dst = smem_addr(to + 8 * g);
 #pragma unroll
                         for (int y = 0; y < static_cast<int>(sizeof(T)) / 2; ++y)
                             asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + 16 * y),
@@ -556,19 +595,46 @@ __global__ void __launch_bounds__(kAppendThreads, WHOLE ? 6 : 2) kv_append_kerne
                                          : "memory");
                     }
                     asm volatile("cp.async.commit_group;" ::: "memory");
+                };
+                if constexpr (ROPE) {
+                    copy(a.v, a.v_stride, v_staged);
+                    const T *x = static_cast<const T *>(a.k) + (t0 + i) * a.k_stride + static_cast<int64_t>(h) * a.head_dim;
+#pragma unroll 2
+                    for (int g = tid; g < total; g += kAppendThreads) {
+                        const int row = append_row(a, g);
+                        float f[8];
+                        rope_eight(a.rope, x + row * a.k_stride, a.rope.cos_sin + (t0 + i + row) * a.rope.rot, 8 * (g - row * per), f);
+                        rope_store8(k_staged + 8 * g, f);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int v = 0; v < 2; ++v)
+                        copy(v ? a.v : a.k, v ? a.v_stride : a.k_stride, v ? v_staged : reinterpret_cast<T *>(k_staged));
                 }
             }
-#pragma unroll 1
-            for (int v = 0; v < 2; ++v) {
-                if (v == 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
-                else asm volatile("cp.async.wait_group 0;" ::: "memory");
+            if constexpr (ROPE) {
                 __syncthreads();
-                append_run<T, kAppendThreads, 0>(a, t0 + i, slot, end - i, h, v != 0, tid, fits ? buffer + v * a.staged : nullptr, red);
+                append_run<T, kAppendThreads, 0, true>(a, t0 + i, slot, end - i, h, false, tid, fits ? k_staged : nullptr, red);
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+                __syncthreads();
+                append_run<T, kAppendThreads, 0, false>(a, t0 + i, slot, end - i, h, true, tid, fits ? v_staged : nullptr, red);
+            } else {
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    if (v == 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    __syncthreads();
+                    append_run<T, kAppendThreads, 0, false>(a, t0 + i, slot, end - i, h, v != 0, tid,
+                                                            fits ? (v ? v_staged : reinterpret_cast<T *>(k_staged)) : nullptr, red);
+                }
             }
         }
         if (!whole) {
 #pragma unroll 1
-            for (int v = blockIdx.z; v < 2; v += gridDim.z) append_run<T, 32, WHOLE ? 0 : kAppendHeld>(a, t0 + i, slot, end - i, h, v != 0, lane, nullptr, nullptr);
+            for (int v = blockIdx.z; v < 2; v += gridDim.z) {
+                if (ROPE && v == 0) append_run<T, 32, WHOLE ? 0 : kAppendHeld, ROPE>(a, t0 + i, slot, end - i, h, false, lane, nullptr, nullptr);
+                else append_run<T, 32, WHOLE ? 0 : kAppendHeld, false>(a, t0 + i, slot, end - i, h, v != 0, lane, nullptr, nullptr);
+            }
         }
     }
 }
@@ -613,10 +679,9 @@ extern "C" int fp8blk_kv_map(const int32_t *ctx_lens, const int32_t *new_lens, i
                               positions, free_head_out, nullptr, n_seqs, max_blocks, n_free, block_tokens, max_tokens, stream);
 }
 
-extern "C" int fp8blk_kv_append(const void *k, const void *v, int dtype, const int64_t *slots, uint8_t *k_codes,
-                                float *k_scales, uint8_t *v_codes, float *v_scales, int64_t n_tokens, int64_t k_stride,
-                                int64_t v_stride, int64_t n_blocks, int kv_heads, int block_tokens, int head_dim,
-                                void *stream) {
+static int append_check_args(const void *k, const void *v, int dtype, const int64_t *slots, const uint8_t *k_codes, const float *k_scales,
+                             const uint8_t *v_codes, const float *v_scales, int64_t n_tokens, int64_t k_stride, int64_t v_stride,
+                             int64_t n_blocks, int kv_heads, int block_tokens, int head_dim) {
     if (!k || !v || !slots || (dtype != FP8BLK_F32 && dtype != FP8BLK_BF16) || n_tokens < 1) return FP8BLK_EINVAL;
     const int rc = step_check_cache(k_codes, k_scales, v_codes, v_scales, n_blocks, kv_heads, block_tokens, head_dim);
     if (rc != FP8BLK_OK) return rc;
@@ -625,24 +690,30 @@ extern "C" int fp8blk_kv_append(const void *k, const void *v, int dtype, const i
     if (k_stride < row || v_stride < row || k_stride * es % 16 != 0 || v_stride * es % 16 != 0) return FP8BLK_EINVAL;
     if (n_tokens > kStepMaxIndex || k_stride > kStepMaxIndex || v_stride > kStepMaxIndex) return FP8BLK_ERANGE;
     if (!step_aligned(k, 16) || !step_aligned(v, 16) || !step_aligned(slots, 8)) return FP8BLK_EALIGN;
-    DeviceInfo dev;
-    if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
-    AppendArgs a = {k, v, slots, k_codes, v_codes, k_scales, v_scales, dev.status, n_tokens, k_stride, v_stride,
-                    n_blocks * block_tokens, kv_heads, head_dim, step_log2(block_tokens), 4, 0, 0, 0,
-                    static_cast<uint32_t>(((uint64_t(1) << 32) + head_dim / 8 - 1) / (head_dim / 8))};
+    return FP8BLK_OK;
+}
+
+template <typename A>
+static int append_launch(A a, int dtype, int64_t n_blocks, int block_tokens, const DeviceInfo &dev, cudaStream_t s) {
+    constexpr bool kRope = std::is_same_v<A, AppendRopeArgs>;
+    const int es = dtype == FP8BLK_F32 ? 4 : 2;
     // Tokens per CTA: four, for a decode step, and twice as many again while that leaves eight chunks an SM.  From 16 on
     // (9728 (token, head) pairs on 152 SMs) a CTA takes whole runs.  The rule goes by the total: one prompt of 1000 tokens
     // and 8 heads is below it, and a warp writes each of its runs (15.5 us).
-    while (a.chunk < kAppendMaxChunk && n_tokens * kv_heads * 2 / (2 * a.chunk) >= 8 * dev.sms) a.chunk *= 2;
+    while (a.chunk < kAppendMaxChunk && a.n_tokens * a.kv_heads * 2 / (2 * a.chunk) >= 8 * dev.sms) a.chunk *= 2;
     // K and V by the same CTA where it takes whole runs, by CTAs of their own where a warp does.  Runs are staged in
-    // shared memory up to 32 KiB (three CTAs per SM or more).
+    // shared memory up to 32 KiB (three CTAs per SM or more); rotated keys take four bytes a value.
     const bool whole = a.chunk > 8;
-    if (whole) a.staged = std::min(block_tokens * head_dim, 32768 / es);
+    if (whole) a.staged = std::min(block_tokens * a.head_dim, 32768 / es);
     a.check_words = static_cast<int>(std::min<int64_t>((n_blocks + 31) / 32, kCheckWords));
     a.checks = static_cast<int>((n_blocks + a.check_words * 32ll - 1) / (a.check_words * 32ll));
-    const dim3 grid(static_cast<unsigned>(a.checks + (n_tokens + a.chunk - 1) / a.chunk), static_cast<unsigned>(kv_heads), whole ? 1 : 2);
-    const size_t smem = std::max(static_cast<size_t>(a.staged) * 2 * es, a.check_words * sizeof(uint32_t));
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    dim3 grid(static_cast<unsigned>(a.checks + (a.n_tokens + a.chunk - 1) / a.chunk), static_cast<unsigned>(a.kv_heads), whole ? 1 : 2);
+    if constexpr (kRope) {
+        a.q_first = static_cast<int>(grid.x);
+        const int64_t slice = static_cast<int64_t>(kAppendThreads) * grid.y * grid.z;
+        grid.x += static_cast<unsigned>((a.q_items + slice - 1) / slice);
+    }
+    const size_t smem = std::max(static_cast<size_t>(a.staged) * ((kRope ? 4 : es) + es), a.check_words * sizeof(uint32_t));
     auto launch = [&](auto kernel) {
         int per_sm = 0;
         const cudaError_t err = kernel_occupancy(reinterpret_cast<const void *>(kernel), kAppendThreads, smem, &per_sm);
@@ -650,6 +721,49 @@ extern "C" int fp8blk_kv_append(const void *k, const void *v, int dtype, const i
         if (per_sm < 1) return cudaErrorInvalidConfiguration;
         return step_launch(kernel, grid, kAppendThreads, smem, s, a);
     };
-    if (dtype == FP8BLK_F32) return step_from_cuda(whole ? launch(kv_append_kernel<float, true>) : launch(kv_append_kernel<float, false>));
-    return step_from_cuda(whole ? launch(kv_append_kernel<__nv_bfloat16, true>) : launch(kv_append_kernel<__nv_bfloat16, false>));
+    if (dtype == FP8BLK_F32) return step_from_cuda(whole ? launch(kv_append_kernel<float, true, A>) : launch(kv_append_kernel<float, false, A>));
+    return step_from_cuda(whole ? launch(kv_append_kernel<__nv_bfloat16, true, A>) : launch(kv_append_kernel<__nv_bfloat16, false, A>));
+}
+
+extern "C" int fp8blk_kv_append(const void *k, const void *v, int dtype, const int64_t *slots, uint8_t *k_codes,
+                                float *k_scales, uint8_t *v_codes, float *v_scales, int64_t n_tokens, int64_t k_stride,
+                                int64_t v_stride, int64_t n_blocks, int kv_heads, int block_tokens, int head_dim,
+                                void *stream) {
+    const int rc = append_check_args(k, v, dtype, slots, k_codes, k_scales, v_codes, v_scales, n_tokens, k_stride, v_stride,
+                                     n_blocks, kv_heads, block_tokens, head_dim);
+    if (rc != FP8BLK_OK) return rc;
+    DeviceInfo dev;
+    if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
+    const AppendArgs a = {k, v, slots, k_codes, v_codes, k_scales, v_scales, dev.status, n_tokens, k_stride, v_stride,
+                          n_blocks * block_tokens, kv_heads, head_dim, step_log2(block_tokens), 4, 0, 0, 0,
+                          static_cast<uint32_t>(((uint64_t(1) << 32) + head_dim / 8 - 1) / (head_dim / 8))};
+    return append_launch(a, dtype, n_blocks, block_tokens, dev, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int fp8blk_kv_append_rope(const void *k, const void *v, int dtype, const int64_t *slots, const float *cos_sin,
+                                     uint8_t *k_codes, float *k_scales, uint8_t *v_codes, float *v_scales, const void *q, void *q_out,
+                                     int64_t n_tokens, int64_t k_stride, int64_t v_stride, int64_t q_stride, int64_t q_out_stride,
+                                     int64_t n_blocks, int kv_heads, int q_heads, int block_tokens, int head_dim, int rot_dim,
+                                     int rot_start, int interleaved, void *stream) {
+    const int rc = append_check_args(k, v, dtype, slots, k_codes, k_scales, v_codes, v_scales, n_tokens, k_stride, v_stride,
+                                     n_blocks, kv_heads, block_tokens, head_dim);
+    if (rc != FP8BLK_OK) return rc;
+    if (!q != !q_out) return FP8BLK_EINVAL;
+    AppendRopeArgs a = {};
+    uint32_t items = 0;
+    // (The keys' rotation has no output of its own: the checks and the layout are those of one in place.)
+    int plan = rope_plan(k, const_cast<void *>(k), cos_sin, dtype, n_tokens, kv_heads, head_dim, rot_dim, rot_start, interleaved,
+                         k_stride, k_stride, 1, &a.rope, &items);
+    if (plan != FP8BLK_OK) return plan;
+    if (q) {
+        plan = rope_plan(q, q_out, cos_sin, dtype, n_tokens, q_heads, head_dim, rot_dim, rot_start, interleaved, q_stride, q_out_stride,
+                         1, &a.q, &a.q_items);
+        if (plan != FP8BLK_OK) return plan;
+    }
+    DeviceInfo dev;
+    if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
+    static_cast<AppendArgs &>(a) = {k, v, slots, k_codes, v_codes, k_scales, v_scales, dev.status, n_tokens, k_stride, v_stride,
+                                    n_blocks * block_tokens, kv_heads, head_dim, step_log2(block_tokens), 4, 0, 0, 0,
+                                    static_cast<uint32_t>(((uint64_t(1) << 32) + head_dim / 8 - 1) / (head_dim / 8))};
+    return append_launch(a, dtype, n_blocks, block_tokens, dev, static_cast<cudaStream_t>(stream));
 }

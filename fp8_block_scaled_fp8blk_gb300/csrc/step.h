@@ -1,9 +1,11 @@
 // step.h -- host-side pieces shared by the entry points of the cache,
-// attention and scoring calls (kv_cache.cu, kv_attn.cu, token_logprobs.cu).
+// attention, rotation and scoring calls (kv_cache.cu, kv_attn.cu, rope.cu,
+// token_logprobs.cu).
 #pragma once
 
 #include "fp8blk.h"
 #include "launch.h"
+#include "rope.cuh"
 
 namespace fp8blk {
 
@@ -39,6 +41,10 @@ inline int step_check_cache(const uint8_t *k_codes, const float *k_scales, const
         return FP8BLK_EALIGN;
     return FP8BLK_OK;
 }
+
+// Checks and geometry of a rotation with `heads_each` heads a thread (rope.cu).
+int rope_plan(const void *x, void *out, const float *cos_sin, int dtype, int64_t n, int heads, int dim, int rot, int start, int interleaved,
+              int64_t x_stride, int64_t out_stride, int heads_each, RopeArgs *r, uint32_t *items);
 
 // Launch with programmatic dependent launch: every kernel of these files
 // waits on the grid dependency before it touches global memory.

@@ -55,12 +55,22 @@ _lib.nvfp4_expert_gemv.restype = _INT
 _lib.nvfp4_expert_gemv.argtypes = [_P, _P, _P, _INT, _P, _INT, _P, _P, _I64, _I64, _P]
 _lib.mxfp4_expert_gemv.restype = _INT
 _lib.mxfp4_expert_gemv.argtypes = [_P, _P, _INT, _P, _INT, _P, _P, _I64, _I64, _P]
+_lib.fp8blk_rope_frequencies.restype = _INT
+_lib.fp8blk_rope_frequencies.argtypes = [_INT, _INT] + [ctypes.c_double] * 5 + [_P, ctypes.POINTER(ctypes.c_float)]
+_lib.fp8blk_rope_turns.restype = _INT
+_lib.fp8blk_rope_turns.argtypes = [_P, _INT, _P]
+_lib.fp8blk_rope_table.restype = _INT
+_lib.fp8blk_rope_table.argtypes = [_P, _P, ctypes.c_float, _P, _I64, _INT, _P]
+_lib.fp8blk_rope.restype = _INT
+_lib.fp8blk_rope.argtypes = [_P, _INT, _P, _P, _I64, _INT, _INT, _INT, _INT, _INT, _I64, _I64, _P]
 _lib.fp8blk_kv_map.restype = _INT
 _lib.fp8blk_kv_map.argtypes = [_P] * 10 + [_INT] * 4 + [_I64, _P]
 _lib.fp8blk_kv_map_held.restype = _INT
 _lib.fp8blk_kv_map_held.argtypes = [_P] * 12 + [_INT] * 4 + [_I64, _P]
 _lib.fp8blk_kv_append.restype = _INT
 _lib.fp8blk_kv_append.argtypes = [_P, _P, _INT, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _INT, _INT, _INT, _P]
+_lib.fp8blk_kv_append_rope.restype = _INT
+_lib.fp8blk_kv_append_rope.argtypes = [_P, _P, _INT] + [_P] * 8 + [_I64] * 6 + [_INT] * 7 + [_P]
 _lib.fp8blk_kv_attn_ws_bytes.restype = ctypes.c_size_t
 _lib.fp8blk_kv_attn_ws_bytes.argtypes = [_INT] * 5
 _lib.fp8blk_kv_attn.restype = _INT
@@ -90,7 +100,7 @@ STATUS_BAD_EXPERT = 2
 STATUS_BAD_KV = 4
 STATUS_KV_EXHAUSTED = 8
 STATUS_BAD_TARGET = 16
-MAX_M, MAX_HEAD_DIM, MAX_TOP, MAX_VOCAB = 8, 256, 32, 262144
+MAX_M, MAX_HEAD_DIM, MAX_TOP, MAX_VOCAB, MAX_ROT = 8, 256, 32, 262144, 1024
 
 
 class Fp8BlkError(RuntimeError):
@@ -307,7 +317,8 @@ def mxfp4_expert_gemv(codes: torch.Tensor, scales: torch.Tensor, ids: torch.Tens
     return y
 
 
-# ---------------------------------------------------------------- paged cache
+# ---------------------------------------------------------------- arguments of the step's calls
+_U8, _F32, _I32, _I64T = torch.uint8, torch.float32, torch.int32, torch.int64
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
@@ -346,9 +357,82 @@ def _rows3(t: torch.Tensor, what: str, device: int) -> int:
     return s0 if rows > 1 else heads * dim
 
 
-_U8, _F32, _I32, _I64T = torch.uint8, torch.float32, torch.int32, torch.int64
+# ---------------------------------------------------------------- rotary positions
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "bands": 4}
 
 
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, original_len: float = 0.0,
+                     low: float = 1.0, high: float = 32.0) -> tuple[np.ndarray, float]:
+    """Radians a token of each pair (float64 [rot_dim / 2]) and the factor of cosines and sines, on the host.
+
+    `scaling` stretches positions for contexts longer than original_len: "plain", "linear", "base", "ramp" or "bands"."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(ROPE_SCALINGS)}, not {scaling!r}")
+    freqs, scale = np.empty(max(1, int(rot_dim) // 2), dtype=np.float64), ctypes.c_float(0)
+    _check(_lib.fp8blk_rope_frequencies(ROPE_SCALINGS[scaling], int(rot_dim), base, factor, original_len, low, high,
+                                        freqs.ctypes.data, ctypes.byref(scale)), "fp8blk_rope_frequencies")
+    return freqs, float(scale.value)
+
+
+def rope_turns(freqs, device) -> torch.Tensor:
+    """Frequencies (radians a token: an array, tensor or list) as 64-bit fractions of a turn (int64 storage) on the device."""
+    if isinstance(freqs, torch.Tensor):
+        freqs = freqs.cpu().double().numpy()
+    freqs = np.ascontiguousarray(freqs, dtype=np.float64)
+    if freqs.ndim != 1:
+        raise ValueError("freqs must have one dimension")
+    turns = np.empty(freqs.shape, dtype=np.int64)
+    _check(_lib.fp8blk_rope_turns(freqs.ctypes.data, freqs.size, turns.ctypes.data), "fp8blk_rope_turns")
+    return torch.from_numpy(turns).to(device)
+
+
+def fp8blk_rope_table(positions: torch.Tensor, turns: torch.Tensor, scale: float = 1.0,
+                      out: torch.Tensor | None = None) -> torch.Tensor:
+    """Cosines and sines [n, 2, rot_dim / 2] of a step's rows, for all its layers, from their positions (int32 [n])."""
+    n, half, dev = positions.numel(), turns.numel(), positions.get_device()
+    if out is None:
+        out = torch.empty((n, 2, half), dtype=torch.float32, device=positions.device)
+    elif out.shape != (n, 2, half):
+        raise ValueError("out must be [len(positions), 2, len(turns)]")
+    if n == 0:
+        return out
+    rc = _lib.fp8blk_rope_table(_typed(positions, _I32, "positions", dev), _typed(turns, _I64T, "turns", dev), scale,
+                                _typed(out, _F32, "out", dev), n, 2 * half, _stream(positions))
+    if rc:
+        _check(rc, "fp8blk_rope_table")
+    return out
+
+
+def _cos_sin(cos_sin: torch.Tensor, rows: int, device: int):
+    """Data pointer and rot_dim of a step's table for `rows` rows."""
+    shape = cos_sin.shape
+    if len(shape) != 3 or shape[0] != rows or shape[1] != 2:
+        raise ValueError("cos_sin must be [rows, 2, rot_dim / 2] with x's rows")
+    return _typed(cos_sin, _F32, "cos_sin", device), 2 * shape[2]
+
+
+def fp8blk_rope(x: torch.Tensor, cos_sin: torch.Tensor, interleaved: bool = False, start: int = 0,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """x [n, heads, head_dim] (float32 or bfloat16; rows may be strided) with values [start, start + rot_dim) of every head
+    turned by the row's cosines and sines; `out` may be x."""
+    dev = x.get_device()
+    x_stride = _rows3(x, "x", dev)
+    n, heads, dim = x.shape
+    table, rot = _cos_sin(cos_sin, n, dev)
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype is not x.dtype:
+        raise ValueError("out must have x's shape and type")
+    if n == 0:
+        return out
+    rc = _lib.fp8blk_rope(x.data_ptr(), _dtype(x, "x"), table, out.data_ptr(), n, heads, dim, rot, start, int(interleaved), x_stride,
+                          _rows3(out, "out", dev), _stream(x))
+    if rc:
+        _check(rc, "fp8blk_rope")
+    return out
+
+
+# ---------------------------------------------------------------- paged cache
 def _cache(k_codes, k_scales, v_codes, v_scales, device):
     """Shape and data pointers of a cache: (n_blocks, kv_heads, block_tokens, head_dim), (k_codes, k_scales, ...)."""
     shape = k_codes.shape
@@ -426,6 +510,41 @@ def fp8blk_kv_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_co
                                _rows3(k, "k", dev), _rows3(v, "v", dev), blocks, heads, block, dim, _stream(k_codes))
     if rc:
         _check(rc, "fp8blk_kv_append")
+
+
+def fp8blk_kv_append_rope(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cos_sin: torch.Tensor, k_codes: torch.Tensor,
+                          k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor, interleaved: bool = False,
+                          start: int = 0, q: torch.Tensor | None = None, q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """fp8blk_kv_append with the keys turned on their way (see fp8blk_rope); `q` [n, q_heads, head_dim], the queries of the
+    same rows, is turned beside them into `q_out` (made when not given; may be q), which is returned."""
+    dev = k_codes.get_device()
+    (blocks, heads, block, dim), cache = _cache(k_codes, k_scales, v_codes, v_scales, dev)
+    n = slots.numel()
+    if k.shape != (n, heads, dim) or v.shape != (n, heads, dim):
+        raise ValueError("k and v must both be [len(slots), kv_heads, head_dim] of the cache")
+    if v.dtype is not k.dtype:
+        raise TypeError("k and v must have the same type")
+    table, rot = _cos_sin(cos_sin, n, dev)
+    q_heads = q_stride = out_stride = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != dim or q.dtype is not k.dtype:
+            raise ValueError("q must be [len(slots), q_heads, head_dim] of k's type")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape or q_out.dtype is not q.dtype:
+            raise ValueError("q_out must have q's shape and type")
+        q_heads, q_stride, out_stride = q.shape[1], _rows3(q, "q", dev), _rows3(q_out, "q_out", dev)
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    if n == 0:
+        return q_out
+    rc = _lib.fp8blk_kv_append_rope(k.data_ptr(), v.data_ptr(), _dtype(k, "k"), _typed(slots, _I64T, "slots", dev), table, *cache,
+                                    None if q is None else q.data_ptr(), None if q is None else q_out.data_ptr(), n,
+                                    _rows3(k, "k", dev), _rows3(v, "v", dev), q_stride, out_stride, blocks, heads, q_heads, block,
+                                    dim, rot, start, int(interleaved), _stream(k_codes))
+    if rc:
+        _check(rc, "fp8blk_kv_append_rope")
+    return q_out
 
 
 def fp8blk_kv_attn_ws_bytes(n_seqs: int, max_m: int, q_heads: int, kv_heads: int, head_dim: int) -> int:

@@ -57,6 +57,14 @@ extern "C" {
 #define FP8BLK_MAX_HEAD_DIM 256  /* widest attention head of the paged cache */
 #define FP8BLK_MAX_TOP 32        /* most alternatives per row of fp8blk_token_logprobs */
 #define FP8BLK_MAX_VOCAB 262144  /* most logits per row of fp8blk_token_logprobs */
+#define FP8BLK_MAX_ROT 1024      /* widest head of fp8blk_rope, and widest rotated part of one */
+
+/* Scalings of fp8blk_rope_frequencies. */
+#define FP8BLK_ROPE_PLAIN 0
+#define FP8BLK_ROPE_LINEAR 1
+#define FP8BLK_ROPE_BASE 2
+#define FP8BLK_ROPE_RAMP 3
+#define FP8BLK_ROPE_BANDS 4
 
 /* Element types of activations and logits (the `dtype` arguments). */
 #define FP8BLK_F32 0
@@ -283,7 +291,87 @@ int mxfp4_expert_gemv(const uint8_t *codes, const uint8_t *scales, int n_experts
                       int n_active, const float *x, float *y, int64_t rows, int64_t cols, void *stream);
 
 /*
- * The paged e4m3 cache (fp8blk_kv_map, fp8blk_kv_append, fp8blk_kv_attn).
+ * Rotary positions.  The rotated part of a head is its values [rot_start,
+ * rot_start + rot_dim); pair i of it, i < rot_dim / 2, turns by the angle
+ * position * frequency[i]:
+ *   half layout      a = part[i],      b = part[i + rot_dim / 2]
+ *   interleaved      a = part[2 i],    b = part[2 i + 1]
+ *   a' = a cos - b sin,   b' = b cos + a sin
+ * Frequencies are made once per model (host), cosines and sines once per step
+ * for all its layers (fp8blk_rope_table), and each layer rotates by those:
+ * fp8blk_rope, or fp8blk_kv_append_rope on the way into the cache.
+ */
+
+/*
+ * fp8blk_rope_frequencies -- HOST function: radians a token of each pair,
+ * f_i = base^(-2 i / rot_dim), scaled for contexts longer than the original:
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor
+ *   BASE    with base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *   RAMP    f_i / factor * r_i + f_i * (1 - r_i), r_i = (i - a) / (b - a) in
+ *           [0, 1]; a = floor, b = ceil of the pair index at which a frequency
+ *           makes `high`, `low` turns over original_len tokens (kept in
+ *           [0, rot_dim - 1]); pairs that turn often keep their frequency
+ *   BANDS   the same mixture with 1 - r_i = (n_i - low) / (high - low) in
+ *           [0, 1], n_i the turns of pair i over original_len tokens
+ *   rot_dim     even, 2 .. FP8BLK_MAX_ROT (BASE: from 4)
+ *   base        > 1;  factor >= 1 (not read by PLAIN)
+ *   original_len, low, high   RAMP and BANDS only: >= 1, 0 < low < high
+ *   freqs       host, rot_dim / 2 doubles
+ *   attn_scale  host, optional: what cosines and sines are multiplied by
+ *               (fp8blk_rope_table's scale): 0.1 ln(factor) + 1 for RAMP, else 1
+ * Errors: EINVAL.
+ */
+int fp8blk_rope_frequencies(int scaling, int rot_dim, double base, double factor, double original_len, double low,
+                            double high, double *freqs, float *attn_scale);
+
+/*
+ * fp8blk_rope_turns -- HOST function: frequencies (radians a token, of any
+ * origin; negative ones turn back) as fractions of a turn,
+ *   turns[i] = round(2^64 * (freqs[i] / 2 pi)) mod 2^64,
+ * the form fp8blk_rope_table reads on the device.
+ *   freqs, turns  host, n entries, 1 <= n <= FP8BLK_MAX_ROT / 2
+ * Errors: EINVAL (also a frequency that is not finite or beyond 10^6).
+ */
+int fp8blk_rope_turns(const double *freqs, int n, uint64_t *turns);
+
+/*
+ * fp8blk_rope_table -- cosines and sines of a step's rows:
+ *   cos_sin[r][0][i] = scale * cos(2 pi positions[r] turns[i] / 2^64),
+ *   cos_sin[r][1][i] = scale * sin(...),   i < rot_dim / 2.
+ * The product wraps in 64-bit integers where the circle does, so positions of
+ * any size keep f32 precision.  A negative position (a row without a token, as
+ * fp8blk_kv_map marks them) gives 1 and 0: its row is not turned.
+ *   positions  device, int32 [n_rows]
+ *   turns      device, uint64 [rot_dim / 2], 8-byte aligned
+ *   cos_sin    device, f32 [n_rows, 2, rot_dim / 2], 16-byte aligned
+ *   rot_dim    even, 2 .. FP8BLK_MAX_ROT;  n_rows * rot_dim / 2 < 2^31
+ * Errors: EINVAL, EALIGN, ERANGE, ECUDA.
+ */
+int fp8blk_rope_table(const int32_t *positions, const uint64_t *turns, float scale, float *cos_sin, int64_t n_rows,
+                      int rot_dim, void *stream);
+
+/*
+ * fp8blk_rope -- rotate every head of x: row r by the row r of cos_sin.  The
+ * arithmetic is f32, rounded once to x's type; what is outside the rotated
+ * part is copied.
+ *   x, out    device, f32 or bf16 (`dtype`) [n_rows, heads, head_dim], rows
+ *             x_stride / out_stride elements apart, aligned to one element
+ *             (16-byte aligned rows, head_dim and rot_start multiples of 8 and
+ *             rot_dim of 16 take the fast path).  out may be x itself, with the
+ *             same stride; any other overlap is not allowed
+ *   cos_sin   as fp8blk_rope_table writes it
+ *   head_dim  2 .. FP8BLK_MAX_ROT; rot_dim even, rot_start + rot_dim <= head_dim
+ *   interleaved  0 half layout, 1 neighbours
+ * Errors: EINVAL, EALIGN, ERANGE (also more than 2^31 items of work: at least
+ * 16 million values), ECUDA.
+ */
+int fp8blk_rope(const void *x, int dtype, const float *cos_sin, void *out, int64_t n_rows, int heads, int head_dim,
+                int rot_dim, int rot_start, int interleaved, int64_t x_stride, int64_t out_stride, void *stream);
+
+/*
+ * The paged e4m3 cache (fp8blk_kv_map, fp8blk_kv_append, fp8blk_kv_attn,
+ * fp8blk_kv_append_rope, fp8blk_kv_attn_chunk).
  * Keys and values of past tokens are kept in blocks of block_tokens tokens
  * (16, 32, 64 or 128) out of two pools, with one scale for each (block, head):
  *   k_codes, v_codes    device, uint8 e4m3 [n_blocks, kv_heads, block_tokens,
@@ -395,6 +483,27 @@ int fp8blk_kv_map_held(const int32_t *ctx_lens, const int32_t *new_lens, const i
 int fp8blk_kv_append(const void *k, const void *v, int dtype, const int64_t *slots, uint8_t *k_codes, float *k_scales,
                      uint8_t *v_codes, float *v_scales, int64_t n_tokens, int64_t k_stride, int64_t v_stride,
                      int64_t n_blocks, int kv_heads, int block_tokens, int head_dim, void *stream);
+
+/*
+ * fp8blk_kv_append_rope -- fp8blk_kv_append with the keys rotated first (as
+ * fp8blk_rope does, by the row of cos_sin that has the token's number; the
+ * rotated f32 values, unrounded, give scale and codes), and, where q is given,
+ * with the queries of the same rows rotated into q_out by the same launch.
+ *   cos_sin    device, f32 [n_tokens, 2, rot_dim / 2], 16-byte aligned
+ *   q, q_out   device, optional (both NULL = none): [n_tokens, q_heads,
+ *              head_dim] of the same type, rows q_stride / q_out_stride
+ *              elements apart; q_out may be q itself.  Rows whose slot is
+ *              negative are rotated too
+ *   rot_dim, rot_start, interleaved  as fp8blk_rope, the same for k and q
+ *   others     as fp8blk_kv_append
+ * q_out must not overlap k or v.
+ * Errors: as fp8blk_kv_append and fp8blk_rope.
+ */
+int fp8blk_kv_append_rope(const void *k, const void *v, int dtype, const int64_t *slots, const float *cos_sin,
+                          uint8_t *k_codes, float *k_scales, uint8_t *v_codes, float *v_scales, const void *q, void *q_out,
+                          int64_t n_tokens, int64_t k_stride, int64_t v_stride, int64_t q_stride, int64_t q_out_stride,
+                          int64_t n_blocks, int kv_heads, int q_heads, int block_tokens, int head_dim, int rot_dim,
+                          int rot_start, int interleaved, void *stream);
 
 /* Workspace size (bytes) of fp8blk_kv_attn; 0 for invalid shapes. */
 size_t fp8blk_kv_attn_ws_bytes(int n_seqs, int max_m, int q_heads, int kv_heads, int head_dim);
