@@ -13,7 +13,8 @@ _BINDING_NAMES = (
     "fp8blk_device_status", "Fp8BlkError", "library_path", "argmax_workspace",
     "rope_frequencies", "rope_turns", "fp8blk_rope_table", "fp8blk_rope", "fp8blk_kv_append_rope",
     "fp8blk_kv_map", "kv_map_buffers", "KvMap", "fp8blk_kv_append", "fp8blk_kv_attn", "fp8blk_kv_attn_ws_bytes",
-    "kv_attn_workspace", "fp8blk_token_logprobs", "token_logprobs_buffers", "TokenLogprobs",
+    "kv_attn_workspace", "fp8blk_kv_attn_chunk", "fp8blk_kv_attn_chunk_ws_bytes", "kv_attn_chunk_workspace",
+    "fp8blk_token_logprobs", "token_logprobs_buffers", "TokenLogprobs",
     "set_launch_tuning", "abi_version",
 )
 

@@ -76,6 +76,11 @@ _lib.fp8blk_kv_attn_ws_bytes.argtypes = [_INT] * 5
 _lib.fp8blk_kv_attn.restype = _INT
 _lib.fp8blk_kv_attn.argtypes = [_P, _INT] + [_P] * 10 + [ctypes.c_size_t, _INT, _INT, _I64, _INT, _INT, _INT, _INT, _I64,
                                                        _INT, _I64, _I64, ctypes.c_float, _P]
+_lib.fp8blk_kv_attn_chunk_ws_bytes.restype = ctypes.c_size_t
+_lib.fp8blk_kv_attn_chunk_ws_bytes.argtypes = [_INT] * 3
+_lib.fp8blk_kv_attn_chunk.restype = _INT
+_lib.fp8blk_kv_attn_chunk.argtypes = [_P, _INT] + [_P] * 10 + [ctypes.c_size_t, _INT, _I64, _INT, _INT, _INT, _INT, _I64, _INT,
+                                                             _I64, _I64, ctypes.c_float, _P]
 _lib.fp8blk_token_logprobs.restype = _INT
 _lib.fp8blk_token_logprobs.argtypes = [_P, _INT] + [_P] * 6 + [_I64, _I64, _I64, _INT, _P]
 _lib.fp8blk_set_launch_tuning.restype = _INT
@@ -589,6 +594,51 @@ def fp8blk_kv_attn(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tenso
                              sm_scale, _stream(q))
     if rc:
         _check(rc, "fp8blk_kv_attn")
+    return out
+
+
+def fp8blk_kv_attn_chunk_ws_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(_lib.fp8blk_kv_attn_chunk_ws_bytes(q_heads, kv_heads, head_dim))
+
+
+def kv_attn_chunk_workspace(q_heads: int, kv_heads: int, head_dim: int, device) -> torch.Tensor:
+    """A workspace of the size fp8blk_kv_attn_chunk needs, whatever the batch."""
+    n = fp8blk_kv_attn_chunk_ws_bytes(q_heads, kv_heads, head_dim)
+    if n == 0:
+        raise Fp8BlkError(EINVAL, "fp8blk_kv_attn_chunk_ws_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def fp8blk_kv_attn_chunk(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                         v_scales: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, q_starts: torch.Tensor,
+                         sm_scale: float, ws: torch.Tensor, out: torch.Tensor | None = None,
+                         lse: torch.Tensor | None = None) -> torch.Tensor:
+    """fp8blk_kv_attn for any number of rows per request (prompts and chunks of them): q [rows, q_heads, head_dim] (float32
+    or bfloat16; rows may be strided).  `lse` (float32 [rows, q_heads]) is written when given."""
+    dev = q.get_device()
+    (blocks, kv_heads, block, dim), cache = _cache(k_codes, k_scales, v_codes, v_scales, dev)
+    n, width = block_table.shape
+    q_stride = _rows3(q, "q", dev)
+    rows, q_heads, q_dim = q.shape
+    if q_dim != dim:
+        raise ValueError("q must be [rows, q_heads, head_dim] of the cache")
+    if out is None:
+        out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype is not q.dtype:
+        raise ValueError("out must have q's shape and type")
+    if seq_lens.numel() != n or q_starts.numel() != n + 1:
+        raise ValueError("seq_lens must have one entry per row of block_table, q_starts one more")
+    if lse is not None and lse.shape != (rows, q_heads):
+        raise ValueError("lse must be [rows, q_heads]")
+    if rows == 0:
+        return out
+    rc = _lib.fp8blk_kv_attn_chunk(q.data_ptr(), _dtype(q, "q"), *cache, _typed(block_table, _I32, "block_table", dev),
+                                   _typed(seq_lens, _I32, "seq_lens", dev), _typed(q_starts, _I32, "q_starts", dev), out.data_ptr(),
+                                   None if lse is None else _typed(lse, _F32, "lse", dev), _typed(ws, ws.dtype, "ws", dev), ws.nbytes,
+                                   n, rows, q_heads, kv_heads, dim, block, blocks, width, q_stride, _rows3(out, "out", dev),
+                                   sm_scale, _stream(q))
+    if rc:
+        _check(rc, "fp8blk_kv_attn_chunk")
     return out
 
 

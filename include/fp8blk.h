@@ -549,6 +549,41 @@ int fp8blk_kv_attn(const void *q, int dtype, const uint8_t *k_codes, const float
                    int q_heads, int kv_heads, int head_dim, int block_tokens, int64_t n_blocks, int max_blocks,
                    int64_t q_stride, int64_t out_stride, float sm_scale, void *stream);
 
+/* Workspace size (bytes) of fp8blk_kv_attn_chunk; 0 for invalid shapes. */
+size_t fp8blk_kv_attn_chunk_ws_bytes(int q_heads, int kv_heads, int head_dim);
+
+/*
+ * fp8blk_kv_attn_chunk -- fp8blk_kv_attn for any number of rows a request:
+ * prompts, and chunks of prompts behind what the cache holds already (their own
+ * keys and values included: fp8blk_kv_append comes first).  The same definition:
+ * row i of the r rows of request s sits at position p = seq_lens[s] - r + i and
+ * sees the positions 0 .. p; a row that sees nothing gives out = 0 and
+ * lse = -inf; what a row does not see has no part in it.
+ * Scores, softmax statistics and sums are f32.  The codes are exact; q and the
+ * weights p s_v are f16 values under a power of two of their row's own: with
+ * bf16, q keeps all its bits down to 2^-39 of its row's largest, a weight 2^-11
+ * of itself and 2^-30 of its row's largest p |s_v|; with f32, each is a sum of
+ * two f16 values and keeps 2^-22 of itself.  A k or v scale that is not finite
+ * counts as NaN.
+ *   q, out, lse, seq_lens, q_starts  as fp8blk_kv_attn; a request may have any
+ *              number of rows, none among them
+ *   ws         device workspace of at least fp8blk_kv_attn_chunk_ws_bytes()
+ *              bytes, 16-byte aligned; nothing is kept in it between calls, and
+ *              it need not be cleared.  Calls that share it must be ordered
+ * A block id outside the pool (or a length past max_blocks) makes the rows that
+ * see it NaN; rows outside total_rows are skipped; each sets
+ * FP8BLK_STATUS_BAD_KV.  Rows of a CTA that gave up on a wait are NaN in out
+ * and lse (see fp8blk_set_wait_limit).
+ * For up to FP8BLK_MAX_M rows a request fp8blk_kv_attn is faster.
+ * Errors: EINVAL, EALIGN, EWS, ERANGE (as fp8blk_kv_attn, and 2^31 (row, query
+ * head of a cache head) pairs), ECUDA.
+ */
+int fp8blk_kv_attn_chunk(const void *q, int dtype, const uint8_t *k_codes, const float *k_scales, const uint8_t *v_codes,
+                         const float *v_scales, const int32_t *block_table, const int32_t *seq_lens, const int32_t *q_starts,
+                         void *out, float *lse, void *ws, size_t ws_bytes, int n_seqs, int64_t total_rows, int q_heads,
+                         int kv_heads, int head_dim, int block_tokens, int64_t n_blocks, int max_blocks, int64_t q_stride,
+                         int64_t out_stride, float sm_scale, void *stream);
+
 /*
  * fp8blk_token_logprobs -- score given tokens under rows of logits: for row i
  * with x = logits[i], t = targets[i], lse = log sum_v exp(x_v)
