@@ -32,7 +32,7 @@ static bool chunk_shape_ok(int q_heads, int kv_heads, int head_dim) {
 
 extern "C" size_t fp8blk_kv_attn_chunk_ws_bytes(int q_heads, int kv_heads, int head_dim) {
     if (!chunk_shape_ok(q_heads, kv_heads, head_dim)) return 0;
-    const size_t rows = head_dim > 128 ? ChunkShape<1, true>::U : ChunkShape<1, false>::U;
+    const size_t rows = head_dim > 128 ? ChunkShape<1, true>::U : ChunkShape<1, false>::U;  // of bf16, f32 has no more
     return kChHeaderBytes + static_cast<size_t>(kChMaxGrid) * 2 * rows * (head_dim + 2) * sizeof(float);
 }
 
@@ -57,7 +57,11 @@ extern "C" int fp8blk_kv_attn_chunk(const void *q, int dtype, const uint8_t *k_c
     if (!ws || ws_bytes < fp8blk_kv_attn_chunk_ws_bytes(q_heads, kv_heads, head_dim)) return FP8BLK_EWS;
     if (!step_aligned(ws, 16)) return FP8BLK_EALIGN;
     const bool wide = head_dim > 128;
-    const int rows = wide ? ChunkShape<1, true>::U : ChunkShape<1, false>::U, tile = rows / 2, group = q_heads / kv_heads;
+    const int rows = wide || dtype == FP8BLK_F32 ? 128 : 256, tile = wide ? 64 : 128, group = q_heads / kv_heads;
+    static_assert(ChunkShape<1, false>::U == 256 && ChunkShape<1, true>::U == 128 && ChunkShape<2, false>::U == 128 &&
+                      ChunkShape<2, true>::U == 128 && ChunkShape<1, false>::T == 128 && ChunkShape<2, false>::T == 128 &&
+                      ChunkShape<1, true>::T == 64 && ChunkShape<2, true>::T == 64,
+                  "row tiles and tiles");
     // What the kernel counts in 32 bits: rows times heads of a group, row tiles and tiles on one line, list entries.
     const int64_t tiles = (static_cast<int64_t>(max_blocks) * block_tokens + tile - 1) / tile + 1;
     const int64_t flat = total_rows * group, units = (flat + rows - 1) / rows + n_seqs;

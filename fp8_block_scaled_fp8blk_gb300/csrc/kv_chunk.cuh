@@ -28,29 +28,40 @@
 // scale that is not finite, or in a block outside the pool) is replaced by zero
 // in the tile and makes the rows that see it NaN at the end.
 //
+// The tensor cores cut sums to f32 instead of rounding them, which shows in f32
+// results (a systematic 2e-6 over 1024 tokens).  So with f32 each tile's product
+// starts anew, its second planes first, and is added to the sums by a group of
+// warps of its own; one such product shrinks by 2e-7.
+//
 // Work: all (request, row tile, cache head, token tile) quadruples in one list,
 // cut into one contiguous range per CTA, so ragged and causal lengths balance.
 // Row tiles are 256 rows (two products' rows, whose softmax and MMAs take turns)
-// for head_dim <= 128, else 128.  A unit (request, row tile, head) that lies
-// across CTAs leaves partial sums in the workspace, which a second kernel joins,
-// in CTA order (deterministic, no counters).
+// for bf16 with head_dim <= 128, else 128 (scores of the next tile beside the
+// softmax of this one).  A unit (request, row tile, head) that lies across CTAs
+// leaves partial sums in the workspace, which a second kernel joins, in CTA order
+// (deterministic, no counters).
 //
-// Roles (544 threads, one CTA per SM): warps 0-3 and 4-7 softmax of the unit's
-// first and second 128 rows (TMEM lane = row), warps 8-15 convert q, K and V,
-// warp 16 issues the MMAs.  Every wait is bounded; a timeout raises a CTA-wide
-// flag, the outputs and lse of the CTA's rows become NaN, MMAs in flight are
-// waited for, and the status word records it.
+// Roles (640 threads, one CTA per SM): warps 0-3 softmax (TMEM lane = row), warps
+// 4-7 softmax of the unit's second 128 rows, or f32's sums, warps 8-15 convert q, K
+// and V, warp 16 issues the MMAs.  Every wait is bounded; a timeout raises a
+// CTA-wide flag, the outputs and lse of the CTA's rows become NaN, MMAs in flight
+// are waited for, and the status word records it.
 #pragma once
 
 #include "kv_attn.cuh"
 #include "rope.cuh"
 
+#include <type_traits>
+
 namespace fp8blk {
 
-constexpr int kChThreads = 544;
+constexpr int kChThreads = 640;
 constexpr int kChConvertWarp = 8, kChConvertWarps = 8, kChMmaWarp = 16;
 constexpr int kChMaxGrid = 160;          // bound on CTAs: partial sums in the workspace
-constexpr int kChInfo = 4;               // tiles whose scales are held
+constexpr int kChInfo = 4;               // tiles whose scales (and sums' factors) are held
+// Registers a thread of each role (of the 96 of the launch).
+constexpr int kChSoftmaxRegs = 136, kChConvertRegs = 80, kChIssueRegs = 40;
+static_assert(256 * kChSoftmaxRegs + 256 * kChConvertRegs + 128 * kChIssueRegs <= kChThreads * 96, "registers");
 constexpr int kChLift = 6;               // K: a row's largest weight is below 2^6 when R moves, below 2^15 at most
 constexpr int kChSlack = 8;              // ... which it does when a tile passes it by more than 2^8
 constexpr float kChNone = -3.0e38f;      // maximum of a row that has seen nothing
@@ -81,28 +92,34 @@ template <int PL_, bool WIDE_>
 struct ChunkShape {
     static constexpr int PL = PL_;
     static constexpr bool WIDE = WIDE_;
-    static constexpr int NS = WIDE ? 1 : 2;             // 128-row products of a unit
+    static constexpr bool SUMS = PL == 2;               // products of a tile are added to the sums outside the tensor cores
+    static constexpr int NS = WIDE || SUMS ? 1 : 2;     // 128-row products of a unit
     static constexpr int U = NS * 128;                  // rows of a unit
     static constexpr int T = WIDE ? 64 : 128;           // tokens of a tile
     static constexpr int kBlocks = WIDE ? 4 : 2;        // 64-wide column blocks of a head
     static constexpr int kSlot = T * kBlocks * 128;     // K or V of a tile as f16: 32 KiB
-    static constexpr int kSlots = PL == 1 ? 4 : 2;
+    static constexpr int kSlots = PL == 2 && WIDE ? 2 : 4;
     static constexpr int kQPlane = 128 * kBlocks * 128;  // one plane of 128 rows
     static constexpr int kQ = NS * PL * kQPlane;
     static constexpr size_t kSmem = 1024 + kQ + kSlots * kSlot;
     static constexpr int kGranules = T / 16;            // scales of a tile
-    // Tensor memory: scores (and the weights, in their place), then sums.
-    static constexpr int kSDeep = WIDE ? 2 : 1;         // score buffers of a product
-    static constexpr int kOCol = 256;
+    // Tensor memory, in columns: scores (and the weights, in their place; two buffers of one product, or one of each of
+    // two), f32's product of a tile (half of a wide head at a time), the sums.
+    static constexpr int kProductCol = WIDE ? 128 : 256;
+    static constexpr int kSumCol = SUMS && !WIDE ? 384 : 256;
+    static constexpr int kHalves = SUMS && WIDE ? 2 : 1;
 };
 
 struct ChunkShared {
-    // Whoever waits on a barrier is never a whole turn of it behind: of the next phase but one a wait could not tell the
-    // one it is for.  So what a softmax product may skip or be late for goes by the unit's parity.
+    // Whoever waits on a barrier is never a whole turn of it behind: a wait could not tell the next phase but one from
+    // its own.  So what a role may skip or be late for goes by the unit's or the score buffer's parity.
     uint64_t slot_full[4], slot_free[4], s_full[2], p_full[2], o_done[2], info_full[kChInfo];
     uint64_t q_full[2], values_done[2], unit_done[2], q_free, mma_done;
+    uint64_t factor_full[kChInfo], last_full[2], product_free;  // f32's sums
     float4 info[kChInfo][8];     // per sixteen tokens: |k scale|, exponent of the v scale, its mantissa
     float qs[2][256];            // per row: what a score is times |s_k| of
+    float factor[kChInfo][128];  // f32: what the sums so far are times, per row of a tile
+    float last[2][3][128];       // f32: a unit's maxima, references and denominators
     int vnan[2][256];            // first position whose value is NaN, per element
     int any_nan[2];
     int64_t scan[kChThreads / 32];
@@ -113,46 +130,50 @@ struct ChunkShared {
 };
 
 // ------------------------------------------------------------------ the list
-// sum of floor((a + 2 i) / g) over i < n.  The floors of all integers from a to
-// a + 2 n add up in closed form; of two neighbours x, x + 1 the second's is one
-// more only where g divides x + 1, and those are counted.
+// sum of floor((a + step i) / g) over i < n, step 1 or 2.  The floors of all
+// integers from a to a + n add up in closed form.  For every other one of a to
+// a + 2 n: of two neighbours x, x + 1 the second's floor is one more only where g
+// divides x + 1, and those are counted.
 __host__ __device__ inline int64_t ch_floors_below(uint32_t x, uint32_t g) {
     const uint32_t q = x / g, r = x - q * g;
     return static_cast<int64_t>(g) * (static_cast<int64_t>(q) * (static_cast<int64_t>(q) - 1) / 2) + static_cast<int64_t>(q) * r;
 }
-__host__ __device__ inline int64_t ch_floor_sum(uint32_t a, uint32_t g, uint32_t n) {
+__host__ __device__ inline int64_t ch_floor_sum(uint32_t a, uint32_t g, uint32_t n, int step) {
     if (n == 0) return 0;
-    const uint32_t hi = a + 2 * n;
-    int64_t steps = 0;
+    const uint32_t hi = a + step * n;
+    const int64_t all = ch_floors_below(hi, g) - ch_floors_below(a, g);
+    if (step == 1) return all;
+    int64_t more = 0;
     if (g % 2 == 0) {
-        if (a % 2 == 1) steps = static_cast<int64_t>((hi - 1) / g) - a / g;
+        if (a % 2 == 1) more = static_cast<int64_t>((hi - 1) / g) - a / g;
     } else if (a % 2 == 1) {
-        steps = static_cast<int64_t>((hi - 1) / (2 * g)) - a / (2 * g);
+        more = static_cast<int64_t>((hi - 1) / (2 * g)) - a / (2 * g);
     } else {
-        steps = static_cast<int64_t>((hi - 1 + g) / (2 * g)) - (a + g) / (2 * g);
+        more = static_cast<int64_t>((hi - 1 + g) / (2 * g)) - (a + g) / (2 * g);
     }
-    return (ch_floors_below(hi, g) - ch_floors_below(a, g) - steps) / 2;
+    return (all - more) / 2;
 }
 
 // One request as the kernel takes it.  Row tile i's last row sees the tiles
-// 0 .. floor((a + 2 i) / g), as far as there are any: T is half a row tile.
+// 0 .. floor((a + step i) / g), as far as there are any; a row tile's rows are
+// step tiles' tokens.
 struct ChunkSeq {
     int first, rows, len;  // rows 0: nothing to do
     int tiles;             // of the whole cache
     int row_tiles;
-    int a, g, kv_heads;
+    int a, g, step, kv_heads;
     int full, last;        // list entries of a tile: of a row tile, of the last one
     bool bad;
     __host__ __device__ int seen(int i) const {  // tiles of row tile i
-        const int t = (a + 2 * i) / g + 1;
+        const int t = (a + step * i) / g + 1;
         return t < tiles ? t : tiles;
     }
     __host__ __device__ int weight(int i) const { return i + 1 == row_tiles ? last : full; }
     // Entries of the row tiles below i, i < row_tiles: each unit has one slot for its set-up and one per tile.
     __host__ __device__ int64_t before(int i) const {
-        const int64_t lack = static_cast<int64_t>(tiles - 1) * g - a;  // from row tile ceil(lack / 2) on all tiles are seen
-        const int64_t some = lack <= 0 ? 0 : (lack + 1) / 2 < i ? (lack + 1) / 2 : i;
-        const int64_t slots = ch_floor_sum(static_cast<uint32_t>(a), static_cast<uint32_t>(g), static_cast<uint32_t>(some)) + some +
+        const int64_t lack = static_cast<int64_t>(tiles - 1) * g - a;  // from row tile ceil(lack / step) on all tiles are seen
+        const int64_t all = lack <= 0 ? 0 : (lack + step - 1) / step, some = all < i ? all : i;
+        const int64_t slots = ch_floor_sum(static_cast<uint32_t>(a), static_cast<uint32_t>(g), static_cast<uint32_t>(some), step) + some +
                               (i - some) * tiles + i;
         return slots * full * kv_heads;
     }
@@ -180,6 +201,7 @@ __host__ __device__ inline ChunkSeq ch_seq_of(int first, int64_t rows, int len, 
     p = p < 0 ? 0 : p < end ? p : end;
     q.a = static_cast<int>((p * group + unit_rows - 1) / tile);
     q.g = group;
+    q.step = unit_rows / tile;
     q.kv_heads = kv_heads;
     q.full = unit_rows / 128;
     q.last = flat - static_cast<int64_t>(q.row_tiles - 1) * unit_rows > 128 ? q.full : 1;
@@ -318,14 +340,25 @@ __device__ __forceinline__ uint32_t ch_pack_f16(float lo, float hi) {
     return r;
 }
 __device__ __forceinline__ float2 ch_unpack_f16(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
+// Two f32 at a time.
+__device__ __forceinline__ uint64_t ch_pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void ch_unpair(uint64_t p, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ uint64_t ch_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t ch_add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float ch_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
-// x 2^e for a whole e that may leave the range of one power.
-__device__ __forceinline__ float ch_scale(float x, float e) {
-    const float a = fminf(fmaxf(e, -120.f), 120.f);
-    return x * at_exp2(a) * at_exp2(fminf(fmaxf(e - a, -120.f), 120.f));
-}
-
 template <typename Sh, typename T>
 __device__ __forceinline__ void ch_queries(const ChunkArgs &a, const ChunkWalk<Sh> &w, uint8_t *sq, float *qs, int warp, int lane) {
     // A warp takes two rows at a time (one of a wide head), sixteen (32) lanes a row, eight values a lane.
@@ -565,7 +598,6 @@ template <typename Sh>
 __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkWalk<Sh> w, ChunkShared &sh, uint32_t tmem, uint32_t sq, uint32_t slots) {
     constexpr int PL = Sh::PL, T = Sh::T;
     constexpr uint32_t qk_idesc = ch_idesc(T, false);
-    const uint32_t pv_idesc = ch_idesc(a.head_dim, true);
     const uint64_t q_desc = ch_desc(sq, 16), k_desc = ch_desc(slots, 16), v_desc = ch_desc(slots, T * 128);
     const int steps = a.head_dim / 16;
     bool any = false;
@@ -574,35 +606,44 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkWalk<Sh> w, Ch
         t8_fence_after();
         return ok;
     };
-    int n = 0, it = 0, unit = 0;       // slots consumed in order K, V, K, V ..; tiles; units
+    int n = 0, unit = 0;               // slots consumed in order K, V, K, V ..; units
     int done[2] = {0, 0};              // tiles of each product whose weights have been taken
     int begun[2] = {0, 0};             // ... whose scores have been issued
-    auto scores = [&](int i, int slot) {  // product i's scores against K in the slot
-        const uint32_t d = tmem + static_cast<uint32_t>(Sh::WIDE ? (begun[0] & 1) * T : i * 128);
+    int products = 0;                  // f32: products of a tile (of half a wide head) issued
+    auto scores = [&](int i, int slot) {  // product i's scores against K in the slot, the second plane's first
+        const uint32_t d = tmem + static_cast<uint32_t>(Sh::NS == 1 ? (begun[0] & 1) * T : i * 128);
         const uint64_t k = k_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
 #pragma unroll 1
-        for (int p = 0; p < PL; ++p) {
+        for (int p = PL - 1; p >= 0; --p) {
             const uint64_t q = q_desc + static_cast<uint32_t>(i * PL + p) * (Sh::kQPlane / 16);
 #pragma unroll 4
             for (int s = 0; s < steps; ++s)
-                ch_mma_ss(d, q + (s >> 2) * (128 * 128 / 16) + (s & 3) * 2, k + (s >> 2) * (T * 128 / 16) + (s & 3) * 2, qk_idesc, p + s > 0);
+                ch_mma_ss(d, q + (s >> 2) * (128 * 128 / 16) + (s & 3) * 2, k + (s >> 2) * (T * 128 / 16) + (s & 3) * 2, qk_idesc,
+                          p + 1 < PL || s > 0);
         }
-        t8_commit(smem_addr(&sh.s_full[Sh::WIDE ? (begun[0] & 1) : i]));
+        t8_commit(smem_addr(&sh.s_full[Sh::NS == 1 ? (begun[0] & 1) : i]));
         ++begun[i];
         any = true;
     };
     auto sums = [&](int i, int slot, bool acc) {  // product i's weights times V in the slot
-        const uint32_t d = tmem + static_cast<uint32_t>(Sh::kOCol + i * 128);
-        const uint32_t p0 = tmem + static_cast<uint32_t>(Sh::WIDE ? (done[0] & 1) * T : i * 128);
+        const uint32_t p0 = tmem + static_cast<uint32_t>(Sh::NS == 1 ? (done[0] & 1) * T : i * 128);
         const uint64_t v = v_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
+#pragma unroll 1
+        for (int h = 0; h < Sh::kHalves; ++h) {
+            if (Sh::SUMS && products > 0 && !wait(sh.product_free, static_cast<uint32_t>(products - 1) & 1u)) return false;
+            const uint32_t d = tmem + static_cast<uint32_t>(Sh::SUMS ? Sh::kProductCol : Sh::kSumCol + i * 128);
+            const uint32_t idesc = ch_idesc(Sh::kHalves == 1 ? a.head_dim : h == 0 ? 128 : a.head_dim - 128, true);
 #pragma unroll
-        for (int p = 0; p < PL; ++p)
+            for (int p = PL - 1; p >= 0; --p)
 #pragma unroll
-            for (int s = 0; s < T / 16; ++s)
-                ch_mma_ts(d, p0 + (PL == 1 ? 8 * s : 32 * (s >> 1) + 16 * p + 8 * (s & 1)), v + s * (16 * 128 / 16), pv_idesc,
-                          acc || p + s > 0);
-        t8_commit(smem_addr(&sh.o_done[i]));
+                for (int s = 0; s < T / 16; ++s)
+                    ch_mma_ts(d, p0 + (PL == 1 ? 8 * s : 32 * (s >> 1) + 16 * p + 8 * (s & 1)),
+                              v + h * (2 * T * 128 / 16) + s * (16 * 128 / 16), idesc, (!Sh::SUMS && acc) || p + 1 < PL || s > 0);
+            t8_commit(smem_addr(&sh.o_done[i]));
+            ++products;
+        }
         ++done[i];
+        return true;
     };
     auto slot_ready = [&](int m) { return wait(sh.slot_full[m % Sh::kSlots], static_cast<uint32_t>(m / Sh::kSlots) & 1u); };
     bool more = !w.none();
@@ -614,9 +655,9 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkWalk<Sh> w, Ch
         for (int i = 0; i < np; ++i) scores(i, n % Sh::kSlots);
         t8_commit(smem_addr(&sh.slot_free[n % Sh::kSlots]));
         if (tiles == 1) t8_commit(smem_addr(&sh.q_free));
-        for (int j = 0; j < tiles; ++j, n += 2, ++it) {
+        for (int j = 0; j < tiles; ++j, n += 2) {
             const bool next = j + 1 < tiles;
-            if (Sh::WIDE && next) {  // the next scores have a buffer of their own
+            if (Sh::NS == 1 && next) {  // the next scores have a buffer of their own
                 if (!slot_ready(n + 2)) return any;
                 scores(0, (n + 2) % Sh::kSlots);
                 t8_commit(smem_addr(&sh.slot_free[(n + 2) % Sh::kSlots]));
@@ -624,11 +665,11 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkWalk<Sh> w, Ch
             }
             if (!slot_ready(n + 1)) return any;
             for (int i = 0; i < np; ++i) {
-                if (!wait(sh.p_full[i], static_cast<uint32_t>(done[i]) & 1u)) return any;
-                sums(i, (n + 1) % Sh::kSlots, j > 0);
+                if (!wait(sh.p_full[Sh::NS == 1 ? done[0] & 1 : i], static_cast<uint32_t>(Sh::NS == 1 ? done[0] >> 1 : done[i]) & 1u)) return any;
+                if (!sums(i, (n + 1) % Sh::kSlots, j > 0)) return any;
                 if (i + 1 == np) t8_commit(smem_addr(&sh.slot_free[(n + 1) % Sh::kSlots]));
                 // The weights lay where these scores go: MMAs of one thread run in the order of their issue.
-                if (!Sh::WIDE && next) {
+                if (Sh::NS == 2 && next) {
                     if (i == 0 && !slot_ready(n + 2)) return any;
                     scores(i, (n + 2) % Sh::kSlots);
                     if (i + 1 == np) {
@@ -646,35 +687,151 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkWalk<Sh> w, Ch
 }
 
 // ------------------------------------------------------------------ softmax
+// A row of the unit: where it lies, and what it sees.
+struct ChunkRow {
+    int64_t out, lse;
+    int last;    // last position it sees
+    bool valid;
+    template <typename Sh>
+    __device__ __forceinline__ ChunkRow(const ChunkArgs &a, const ChunkWalk<Sh> &w, int local) {
+        const int r = w.row0() + local, token = r / a.group;
+        const int64_t row = w.q.first + token, head = static_cast<int64_t>(w.head) * a.group + (r - token * a.group);
+        valid = r < w.q.rows * a.group;
+        last = valid ? w.q.len - w.q.rows + token : 0x7FFFFFFF;  // (rows that are not there: zeros, stored nowhere)
+        out = row * a.out_stride + head * a.head_dim;
+        lse = row * (static_cast<int64_t>(a.kv_heads) * a.group) + head;
+    }
+};
+
+// Writes a unit's row out: its outputs, or its part of them.
+template <typename Sh, typename T>
+__device__ __forceinline__ void ch_finish(const ChunkArgs &a, const ChunkWalk<Sh> &w, ChunkShared &sh, int unit, const ChunkRow &row, int local,
+                                          uint32_t o_col, float M, float R, float l, bool ok) {
+    const float nanf = __int_as_float(0x7FC00000);
+    const int ub = unit & 1;
+    // The converters' word on what is NaN.
+    ok = ok && at_warp_wait(smem_addr(&sh.values_done[ub]), static_cast<uint32_t>(unit >> 1) & 1u, &sh.abort, a.wait_limit_ns);
+    const bool whole = w.starts() && w.ends();
+    const float up = R > kChNone ? R - static_cast<float>(kChLift) : 0.f;  // sums are 2^-up times what they stand for
+    float f = 1.f;
+    if (!ok) l = nanf;
+    if (whole) {
+        f = l == 0.f ? 0.f : 1.f / l;
+        if (row.valid && a.lse) a.lse[row.lse] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+    }
+    float *part = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + w.starts()) * (static_cast<int64_t>(Sh::U) * (a.head_dim + 2));
+    if (!whole) {
+        __stcg(part + static_cast<int64_t>(Sh::U) * a.head_dim + local, M);
+        __stcg(part + static_cast<int64_t>(Sh::U) * (a.head_dim + 1) + local, l);
+    }
+    T *out = static_cast<T *>(a.out) + row.out;
+    const bool nans = ok && sh.any_nan[ub] != 0;
+    // 2^up in two factors, since it may leave the range of one.
+    const float u1 = at_exp2(fminf(fmaxf(up, -120.f), 120.f)), u2 = at_exp2(fminf(fmaxf(up - fminf(fmaxf(up, -120.f), 120.f), -120.f), 120.f)) * f;
+#pragma unroll 1
+    for (int c = 0; c < a.head_dim; c += 16) {
+        float v[16];
+        if (ok) {
+            t8_ld16(o_col + c, v);
+            at_wait_ld();
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+            v[x] = ok ? v[x] * u1 * u2 : nanf;
+            if (nans && sh.vnan[ub][c + x] <= row.last) v[x] = nanf;
+        }
+        float lo[8], hi[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) lo[x] = v[x], hi[x] = v[8 + x];
+        if (whole) {
+            if (row.valid) {
+                rope_store8(out + c, lo);
+                rope_store8(out + c + 8, hi);
+            }
+        } else {
+            float *p = part + static_cast<int64_t>(local) * a.head_dim + c;
+            rope_store8(p, lo);
+            rope_store8(p + 8, hi);
+        }
+    }
+}
+// ... of a unit over an empty cache.
+template <typename T>
+__device__ __forceinline__ void ch_nothing(const ChunkArgs &a, const ChunkRow &row) {
+    if (!row.valid) return;
+    const float zero[8] = {};
+    for (int d = 0; d < a.head_dim; d += 8) rope_store8(static_cast<T *>(a.out) + row.out + d, zero);
+    if (a.lse) a.lse[row.lse] = -INFINITY;
+}
+
+// The weights of sixteen columns, from their scores, as f16 words (PL = 2: and
+// what those leave), their sum at the row's maximum added to l.
+// CAREFUL: columns past `rel` are not seen, and product and difference round one
+// by one, as the maxima did, so that no weight is above its reference (past 2^20
+// the rounding of a score shows beside that).
+template <int PL, bool CAREFUL>
+__device__ __forceinline__ void ch_weights(const float *v, int col, int rel, float k, float base, float log, float mantissa, float &l,
+                                           uint32_t *hi, uint32_t *lo) {
+    const uint64_t k2 = ch_pair(k, k), off2 = ch_pair(log - base, log - base);
+    uint64_t sum = 0;
+    float w[16];
+#pragma unroll
+    for (int x = 0; x < 16; x += 2) {
+        float t0, t1;
+        if (CAREFUL) {
+            t0 = __fadd_rn(__fmul_rn(v[x], k), -base) + log;
+            t1 = __fadd_rn(__fmul_rn(v[x + 1], k), -base) + log;
+            t0 = col + x <= rel ? t0 : -INFINITY;
+            t1 = col + x + 1 <= rel ? t1 : -INFINITY;
+        } else {
+            ch_unpair(ch_fma2(ch_pair(v[x], v[x + 1]), k2, off2), t0, t1);
+        }
+        w[x] = at_exp2(t0);
+        w[x + 1] = at_exp2(t1);
+        sum = ch_add2(sum, ch_pair(w[x], w[x + 1]));
+    }
+    float s0, s1;
+    ch_unpair(sum, s0, s1);
+    l = fmaf(s0 + s1, at_exp2(-log), l);
+    if (mantissa != 1.f) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) w[x] *= mantissa;
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+        hi[x] = ch_pack_f16(w[2 * x], w[2 * x + 1]);
+        if (PL == 2) {
+            const float2 b = ch_unpack_f16(hi[x]);
+            lo[x] = ch_pack_f16(w[2 * x] - b.x, w[2 * x + 1] - b.y);
+        }
+    }
+}
+
+// The scores of a tile in turn, 32 columns at a time, the next ones on their way.
+template <int T, typename F>
+__device__ __forceinline__ void ch_columns(uint32_t s_col, F f) {
+    float v[2][32];
+    ch_ld32(s_col, v[0]);
+#pragma unroll
+    for (int c = 0; c < T; c += 32) {
+        at_wait_ld();
+        if (c + 32 < T) ch_ld32(s_col + c + 32, v[(c / 32 + 1) & 1]);
+        f(c, v[(c / 32) & 1]);
+    }
+}
+
 template <typename Sh, typename T>
 __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, ChunkShared &sh, uint32_t tmem, int product, int wq, int lane) {
     constexpr int PL = Sh::PL, kTile = Sh::T;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t o_col = tmem + lanes + static_cast<uint32_t>(Sh::kOCol + product * 128);
+    const uint32_t o_col = tmem + lanes + static_cast<uint32_t>(Sh::kSumCol + product * 128);
     const int local = product * 128 + wq * 32 + lane;
-    const float nanf = __int_as_float(0x7FC00000);
-    T *out = static_cast<T *>(a.out);
     int it = 0, unit = 0;   // all tiles of the CTA; units with tiles
     int mine = 0;           // tiles of this product
     bool ok = true;
     do {
-        const int r = w.row0() + local;
-        const bool valid = r < w.q.rows * a.group;
-        const int token = r / a.group;
-        const int lim = valid ? w.q.len - w.q.rows + token : 0x7FFFFFFF;  // (rows that are not there: zeros, stored nowhere)
-        const int64_t row = w.q.first + token;
-        const int64_t at = row * a.out_stride + (static_cast<int64_t>(w.head) * a.group + (r - token * a.group)) * a.head_dim;
-        const int64_t lse_at = row * (static_cast<int64_t>(a.kv_heads) * a.group) + static_cast<int64_t>(w.head) * a.group + (r - token * a.group);
-        if (w.tiles == 0) {  // nothing in the cache
-            if (valid) {
-                for (int d = 0; d < a.head_dim; d += 8) {
-                    const float zero[8] = {};
-                    rope_store8(out + at + d, zero);
-                }
-                if (a.lse) a.lse[lse_at] = -INFINITY;
-            }
-            continue;
-        }
+        const ChunkRow row(a, w, local);
+        if (w.tiles == 0 && !Sh::SUMS) ch_nothing<T>(a, row);
         if (w.none()) continue;
         const int ub = unit & 1, tiles = w.j1 - w.j0;
         // (Also without rows: no product's report runs ahead of the unit.)
@@ -688,24 +845,20 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, 
         const float qs = sh.qs[ub][local];
         float M = kChNone, R = kChNone, l = 0.f;  // maximum, the weights' reference less M, denominator
         for (int j = 0; ok && j < tiles; ++j, ++it, ++mine) {
-            const int sb = Sh::WIDE ? mine & 1 : 0;
-            const uint32_t s_col = tmem + lanes + static_cast<uint32_t>(Sh::WIDE ? sb * kTile : product * 128);
-            ok = at_warp_wait(smem_addr(&sh.s_full[Sh::WIDE ? sb : product]), static_cast<uint32_t>(Sh::WIDE ? mine >> 1 : mine) & 1u, &sh.abort,
-                              a.wait_limit_ns) &&
+            const int sb = Sh::NS == 1 ? mine & 1 : 0;
+            const uint32_t s_col = tmem + lanes + static_cast<uint32_t>(Sh::NS == 1 ? sb * kTile : product * 128);
+            ok = at_warp_wait(smem_addr(&sh.s_full[Sh::NS == 1 ? sb : product]), static_cast<uint32_t>(Sh::NS == 1 ? mine >> 1 : mine) & 1u,
+                              &sh.abort, a.wait_limit_ns) &&
                  at_warp_wait(smem_addr(&sh.info_full[it & (kChInfo - 1)]), static_cast<uint32_t>(it / kChInfo) & 1u, &sh.abort, a.wait_limit_ns);
             if (!ok) break;
             t8_fence_after();
             const float4 *info = sh.info[it & (kChInfo - 1)];
             const int64_t t0 = static_cast<int64_t>(w.j0 + j) * kTile;
-            const int rel = t0 > lim ? -1 : static_cast<int>(lim - t0 < kTile ? lim - t0 : kTile);  // last column this row sees
+            const int rel = t0 > row.last ? -1 : static_cast<int>(row.last - t0 < kTile ? row.last - t0 : kTile);  // last column this row sees
             const bool masked = __any_sync(0xFFFFFFFFu, rel < kTile - 1);
             // Maxima of sixteens, then the row's.
             float top = M, m16[kTile / 16];
-#pragma unroll
-            for (int c = 0; c < kTile; c += 32) {
-                float v[32];
-                ch_ld32(s_col + c, v);
-                at_wait_ld();
+            ch_columns<kTile>(s_col, [&](int c, float (&v)[32]) {
                 if (masked) {
 #pragma unroll
                     for (int x = 0; x < 32; ++x) v[x] = c + x <= rel ? v[x] : -INFINITY;
@@ -719,7 +872,7 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, 
                     top = fmaxf(top, m);
                     m16[c / 16 + g] = m;
                 }
-            }
+            });
             if (top > M) {
                 l *= at_exp2(M - top);
                 R = R > kChNone ? R - (top - M) : R;
@@ -729,126 +882,113 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, 
 #pragma unroll
             for (int g = 0; g < kTile / 16; ++g) ref = fmaxf(ref, (m16[g] - M) + info[g].y);
             const bool move = ref > R + kChSlack;
-            if (__any_sync(0xFFFFFFFFu, move)) {
-                if (j > 0) {
-                    // The sums so far follow the larger reference.
-                    ok = at_warp_wait(smem_addr(&sh.o_done[product]), static_cast<uint32_t>(mine - 1) & 1u, &sh.abort, a.wait_limit_ns);
-                    if (!ok) break;
-                    t8_fence_after();
-                    const float f = move && R > kChNone ? at_exp2(R - ref) : 1.f;
+            const float factor = move && R > kChNone ? at_exp2(R - ref) : 1.f;  // of the sums so far
+            if (Sh::SUMS) {
+                sh.factor[it & (kChInfo - 1)][local] = factor;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.factor_full[it & (kChInfo - 1)]));
+            } else if (j > 0 && __any_sync(0xFFFFFFFFu, move)) {
+                ok = at_warp_wait(smem_addr(&sh.o_done[product]), static_cast<uint32_t>(mine - 1) & 1u, &sh.abort, a.wait_limit_ns);
+                if (!ok) break;
+                t8_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < a.head_dim; c += 16) {
-                        float v[16];
-                        t8_ld16(o_col + c, v);
-                        at_wait_ld();
-                        uint32_t u[16];
+                for (int c = 0; c < a.head_dim; c += 16) {
+                    float v[16];
+                    t8_ld16(o_col + c, v);
+                    at_wait_ld();
+                    uint32_t u[16];
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(v[x] * f);
-                        ch_st16(o_col + c, u);
-                    }
-                    ch_wait_st();
+                    for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(v[x] * factor);
+                    ch_st16(o_col + c, u);
                 }
-                if (move) R = ref;
+                ch_wait_st();
             }
+            if (move) R = ref;
             const float base = M > kChNone ? M : 0.f, lift = R > kChNone ? static_cast<float>(kChLift) - R : 0.f;
-            // Past 2^20 the rounding of a score shows beside the reference: product and difference round one by one there, as
-            // the maxima did, so that none is above its reference.
-            const bool careful = masked || __any_sync(0xFFFFFFFFu, fabsf(base) >= 0x1p20f);
+            auto weights = [&](auto careful) {
+                ch_columns<kTile>(s_col, [&](int c, float (&v)[32]) {
+                    uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int c = 0; c < kTile; c += 32) {
-                float v[32];
-                ch_ld32(s_col + c, v);
-                at_wait_ld();
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float4 f = info[c / 16 + g];
-                    const float k = f.x * qs, log = fmaxf(f.y + lift, kChMinLog), off = log - base;
-                    float sum = 0.f;
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        float t;
-                        if (careful) {
-                            t = __fadd_rn(__fmul_rn(v[16 * g + x], k), -base) + log;
-                            t = c + 16 * g + x <= rel ? t : -INFINITY;
-                        } else {
-                            t = fmaf(v[16 * g + x], k, off);
-                        }
-                        v[16 * g + x] = at_exp2(t);
-                        sum += v[16 * g + x];
+                    for (int g = 0; g < 2; ++g) {
+                        const float4 f = info[c / 16 + g];
+                        ch_weights<PL, decltype(careful)::value>(v + 16 * g, c + 16 * g, rel, f.x * qs, base, fmaxf(f.y + lift, kChMinLog), f.z, l,
+                                                                 hi + 8 * g, lo + 8 * g);
                     }
-                    l = fmaf(sum, at_exp2(-log), l);
-                    if (f.z != 1.f) {
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) v[16 * g + x] *= f.z;
+                    if (PL == 1) {
+                        ch_st16(s_col + c / 2, hi);
+                    } else {
+                        ch_st16(s_col + c, hi);
+                        ch_st16(s_col + c + 16, lo);
                     }
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const float u0 = v[16 * g + 2 * x], u1 = v[16 * g + 2 * x + 1];
-                        hi[8 * g + x] = ch_pack_f16(u0, u1);
-                        if (PL == 2) {
-                            const float2 b = ch_unpack_f16(hi[8 * g + x]);
-                            lo[8 * g + x] = ch_pack_f16(u0 - b.x, u1 - b.y);
-                        }
-                    }
-                }
-                if (PL == 1) {
-                    ch_st16(s_col + c / 2, hi);
-                } else {
-                    ch_st16(s_col + c, hi);
-                    ch_st16(s_col + c + 16, lo);
-                }
-            }
+                });
+            };
+            if (masked || __any_sync(0xFFFFFFFFu, fabsf(base) >= 0x1p20f)) weights(std::true_type{});
+            else weights(std::false_type{});
             ch_wait_st();
             t8_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[product]));
+            if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[Sh::NS == 1 ? sb : product]));
         }
-        // The last product, and the converters' word on what is NaN.
-        ok = ok && at_warp_wait(smem_addr(&sh.o_done[product]), static_cast<uint32_t>(mine - 1) & 1u, &sh.abort, a.wait_limit_ns) &&
-             at_warp_wait(smem_addr(&sh.values_done[ub]), static_cast<uint32_t>(unit >> 1) & 1u, &sh.abort, a.wait_limit_ns);
-        t8_fence_after();
-        const bool whole = w.starts() && w.ends();
-        const float up = R > kChNone ? R - static_cast<float>(kChLift) : 0.f;  // sums are 2^-up times what they stand for
-        float f = 1.f;
-        if (!ok) l = nanf;
-        if (whole) {
-            f = l == 0.f ? 0.f : 1.f / l;
-            if (valid && a.lse) a.lse[lse_at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+        if (Sh::SUMS) {
+            sh.last[ub][0][local] = M;
+            sh.last[ub][1][local] = R;
+            sh.last[ub][2][local] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.last_full[ub]));
+        } else {
+            ok = ok && at_warp_wait(smem_addr(&sh.o_done[product]), static_cast<uint32_t>(mine - 1) & 1u, &sh.abort, a.wait_limit_ns);
+            t8_fence_after();
+            ch_finish<Sh, T>(a, w, sh, unit, row, local, o_col, M, R, l, ok);
+            t8_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.unit_done[ub]));
         }
-        float *part = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + w.starts()) * (static_cast<int64_t>(Sh::U) * (a.head_dim + 2));
-        if (!whole) {
-            __stcg(part + static_cast<int64_t>(Sh::U) * a.head_dim + local, M);
-            __stcg(part + static_cast<int64_t>(Sh::U) * (a.head_dim + 1) + local, l);
-        }
-        const bool nans = ok && sh.any_nan[ub] != 0;
+        ++unit;
+    } while (w.next());
+}
+
+// f32's sums: each tile's product, out of tensor memory, onto the sums there,
+// rounded; at a unit's end its rows are written out.
+template <typename Sh, typename T>
+__device__ __forceinline__ void ch_sums(const ChunkArgs &a, ChunkWalk<Sh> w, ChunkShared &sh, uint32_t tmem, int wq, int lane) {
+    const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t p_col = tmem + lanes + static_cast<uint32_t>(Sh::kProductCol), o_col = tmem + lanes + static_cast<uint32_t>(Sh::kSumCol);
+    const int local = wq * 32 + lane;
+    int it = 0, unit = 0, products = 0;
+    bool ok = true;
+    do {
+        const ChunkRow row(a, w, local);
+        if (w.tiles == 0) ch_nothing<T>(a, row);
+        if (w.none()) continue;
+        const int ub = unit & 1, tiles = w.j1 - w.j0;
+        for (int j = 0; ok && j < tiles; ++j, ++it) {
+            ok = at_warp_wait(smem_addr(&sh.factor_full[it & (kChInfo - 1)]), static_cast<uint32_t>(it / kChInfo) & 1u, &sh.abort, a.wait_limit_ns);
+            const float factor = sh.factor[it & (kChInfo - 1)][local];
 #pragma unroll 1
-        for (int c = 0; c < a.head_dim; c += 16) {
-            float v[16];
-            if (ok) {
-                t8_ld16(o_col + c, v);
-                at_wait_ld();
-            }
+            for (int h = 0; ok && h < Sh::kHalves; ++h, ++products) {
+                ok = at_warp_wait(smem_addr(&sh.o_done[0]), static_cast<uint32_t>(products) & 1u, &sh.abort, a.wait_limit_ns);
+                if (!ok) break;
+                t8_fence_after();
+                const int c0 = 128 * h, c1 = min(a.head_dim, c0 + 128);
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 16) {
+                    float p[16], o[16];
+                    t8_ld16(p_col + c - c0, p);
+                    if (j > 0) t8_ld16(o_col + c, o);
+                    at_wait_ld();
+                    uint32_t u[16];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                v[x] = ok ? ch_scale(v[x], up) * f : nanf;
-                if (nans && sh.vnan[ub][c + x] <= lim) v[x] = nanf;
-            }
-            float lo[8], hi[8];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) lo[x] = v[x], hi[x] = v[8 + x];
-            if (whole) {
-                if (valid) {
-                    rope_store8(out + at + c, lo);
-                    rope_store8(out + at + c + 8, hi);
+                    for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(j > 0 ? fmaf(o[x], factor, p[x]) : p[x]);
+                    ch_st16(o_col + c, u);
                 }
-            } else {
-                float *p = part + static_cast<int64_t>(local) * a.head_dim + c;
-                rope_store8(p, lo);
-                rope_store8(p + 8, hi);
+                t8_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.product_free));
             }
         }
-        t8_fence_before();
+        ch_wait_st();
+        ok = ok && at_warp_wait(smem_addr(&sh.last_full[ub]), static_cast<uint32_t>(unit >> 1) & 1u, &sh.abort, a.wait_limit_ns);
+        ch_finish<Sh, T>(a, w, sh, unit, row, local, o_col, sh.last[ub][0][local], sh.last[ub][1][local], sh.last[ub][2][local], ok);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.unit_done[ub]));
         ++unit;
@@ -877,7 +1017,13 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
             mbar_init(smem_addr(&sh.values_done[i]), kChConvertWarps);
             mbar_init(smem_addr(&sh.unit_done[i]), 4 * Sh::NS);
         }
-        for (int i = 0; i < kChInfo; ++i) mbar_init(smem_addr(&sh.info_full[i]), 1);
+        for (int i = 0; i < kChInfo; ++i) {
+            mbar_init(smem_addr(&sh.info_full[i]), 1);
+            mbar_init(smem_addr(&sh.factor_full[i]), 4);
+        }
+        mbar_init(smem_addr(&sh.last_full[0]), 4);
+        mbar_init(smem_addr(&sh.last_full[1]), 4);
+        mbar_init(smem_addr(&sh.product_free), 4);
         mbar_init(smem_addr(&sh.q_free), 1);
         mbar_init(smem_addr(&sh.mma_done), 1);
         mbar_init_fence();
@@ -965,11 +1111,16 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
     if (busy) {
         ChunkWalk<Sh> w(a, sh.at, sh.cut[1] - sh.cut[0]);
         if (warp < kChConvertWarp) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChSoftmaxRegs));
             if (warp < 4 * Sh::NS) ch_softmax<Sh, T>(a, w, sh, tmem, warp >> 2, warp & 3, lane);
+            else if (Sh::SUMS) ch_sums<Sh, T>(a, w, sh, tmem, warp & 3, lane);
         } else if (warp < kChMmaWarp) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChConvertRegs));
             ch_convert<Sh, T>(a, w, sh, sq, slots, tid - kChConvertWarp * 32);
         } else {
-            if (lane == 0) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChIssueRegs));
+            if (warp != kChMmaWarp) {
+            } else if (lane == 0) {
                 issued = ch_issue<Sh>(a, w, sh, tmem, smem_addr(sq), smem_addr(slots));
                 if (issued) {  // also after a wait that ran out: nothing is in flight at the end
                     t8_commit(smem_addr(&sh.mma_done));
