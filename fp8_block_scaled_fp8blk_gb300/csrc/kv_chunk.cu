@@ -97,6 +97,7 @@ extern "C" int fp8blk_kv_attn_chunk(const void *q, int dtype, const uint8_t *k_c
     a.block_log2 = step_log2(block_tokens);
     a.width = max_blocks;
     a.max_tiles = static_cast<int>(tiles);
+    a.group_inverse = 0xFFFFFFFFu / static_cast<uint32_t>(group);
     a.c = static_cast<float>(c);
     a.c_low = static_cast<float>(c - static_cast<double>(a.c));
     const int grid = static_cast<int>(std::min<int64_t>(std::min(dev.sms, kChMaxGrid), entries));

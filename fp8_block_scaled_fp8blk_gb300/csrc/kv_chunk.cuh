@@ -43,7 +43,8 @@
 //
 // Roles (640 threads, one CTA per SM): warps 0-3 softmax (TMEM lane = row), warps
 // 4-7 softmax of the unit's second 128 rows, or f32's sums, warps 8-15 convert q, K
-// and V, warp 16 issues the MMAs.  Every wait is bounded; a timeout raises a
+// and V, warps 16 and 17 issue the MMAs (of the first and second 128 rows), warp 18
+// walks the list and lays out the units to come.  Every wait is bounded; a timeout raises a
 // CTA-wide flag, the outputs and lse of the CTA's rows become NaN, MMAs in flight
 // are waited for, and the status word records it.
 #pragma once
@@ -56,11 +57,12 @@
 namespace fp8blk {
 
 constexpr int kChThreads = 640;
-constexpr int kChConvertWarp = 8, kChConvertWarps = 8, kChMmaWarp = 16;
+constexpr int kChConvertWarp = 8, kChConvertWarps = 8, kChMmaWarp = 16, kChPlanWarp = 18;
 constexpr int kChMaxGrid = 160;          // bound on CTAs: partial sums in the workspace
 constexpr int kChInfo = 4;               // tiles whose scales (and sums' factors) are held
+constexpr int kChUnits = 4;              // units that are laid out ahead
 // Registers a thread of each role (of the 96 of the launch).
-constexpr int kChSoftmaxRegs = 136, kChConvertRegs = 80, kChIssueRegs = 40;
+constexpr int kChSoftmaxRegs = 112, kChConvertRegs = 104, kChIssueRegs = 48;
 static_assert(256 * kChSoftmaxRegs + 256 * kChConvertRegs + 128 * kChIssueRegs <= kChThreads * 96, "registers");
 constexpr int kChLift = 6;               // K: a row's largest weight is below 2^6 when R moves, below 2^15 at most
 constexpr int kChSlack = 8;              // ... which it does when a tile passes it by more than 2^8
@@ -84,6 +86,7 @@ struct ChunkArgs {
     int64_t q_stride, out_stride, n_blocks;
     int n_seqs, total_rows, kv_heads, group, head_dim, block_log2, width;
     int max_tiles;                    // a table's tiles and one more
+    uint32_t group_inverse;           // floor((2^32 - 1) / group)
     float c, c_low;                   // softmax scale x log2 e, and what c leaves of it
 };
 
@@ -108,50 +111,70 @@ struct ChunkShape {
     static constexpr int kProductCol = WIDE ? 128 : 256;
     static constexpr int kSumCol = SUMS && !WIDE ? 384 : 256;
     static constexpr int kHalves = SUMS && WIDE ? 2 : 1;
+    static constexpr int kIssuers = NS;                 // warps that issue MMAs, one a product
+    // The weights of buffer (or product) b.  The next scores' MMAs are issued right behind those that read the weights, and
+    // only MMAs of one shape are sure to run in their order.  So the weights take the scores' place only where both have 128
+    // columns (sums of 64 < head_dim <= 128 have them all, whatever lies past head_dim), or where the issuer waits in
+    // between (f32); otherwise they have columns of their own.
+    __device__ static uint32_t weights_col(int b, int head_dim) {
+        return SUMS ? b * T : WIDE ? 128 + b * (T / 2) : head_dim <= 64 ? kSumCol + b * 128 + 64 : b * 128;
+    }
+    __device__ static int sum_cols(int head_dim) { return SUMS || WIDE || head_dim <= 64 ? head_dim : 128; }
 };
+
+// One unit's tiles in a CTA's range.
+struct ChunkUnit {
+    int first, rows, len;   // its request: first row, rows, tokens
+    int s, row0, head;      // request, first of the flat rows (row x query head of the group), cache head
+    int j0, tiles;          // its tiles here (none: the cache is empty)
+    int flags;              // below
+};
+constexpr int kChStarts = 1, kChEnds = 2, kChTwo = 4, kChStop = 8;  // first and last tile are here; two products have rows; no unit
 
 struct ChunkShared {
     // Whoever waits on a barrier is never a whole turn of it behind: a wait could not tell the next phase but one from
     // its own.  So what a role may skip or be late for goes by the unit's or the score buffer's parity.
     uint64_t slot_full[4], slot_free[4], s_full[2], p_full[2], o_done[2], info_full[kChInfo];
-    uint64_t q_full[2], values_done[2], unit_done[2], q_free, mma_done;
+    uint64_t q_full[2], values_done[2], unit_done[2], q_free, mma_done[2];
     uint64_t factor_full[kChInfo], last_full[2], product_free;  // f32's sums
-    float4 info[kChInfo][8];     // per sixteen tokens: |k scale|, exponent of the v scale, its mantissa
+    uint64_t unit_full[kChUnits], unit_free[kChUnits];
+    float4 info[kChInfo][8];     // per sixteen tokens: k scale (NaN if not finite), exponent of the v scale, its signed mantissa
+    int info_minus[kChInfo];     // whether a k scale of the tile is negative
+    ChunkUnit units[kChUnits];
     float qs[2][256];            // per row: what a score is times |s_k| of
     float factor[kChInfo][128];  // f32: what the sums so far are times, per row of a tile
     float last[2][3][128];       // f32: a unit's maxima, references and denominators
     int vnan[2][256];            // first position whose value is NaN, per element
     int any_nan[2];
-    int64_t scan[kChThreads / 32];
-    int64_t cut[2];              // this CTA's range
+    int scan[kChThreads / 32];
+    int cut[2];                  // this CTA's range
     int at[4];                   // its first request, row tile, head and slot
     int abort;
     uint32_t tmem;
 };
 
 // ------------------------------------------------------------------ the list
+// (Entries are counted in 32 bits: the host sees to it.)
 // sum of floor((a + step i) / g) over i < n, step 1 or 2.  The floors of all
 // integers from a to a + n add up in closed form.  For every other one of a to
 // a + 2 n: of two neighbours x, x + 1 the second's floor is one more only where g
 // divides x + 1, and those are counted.
-__host__ __device__ inline int64_t ch_floors_below(uint32_t x, uint32_t g) {
+__device__ __forceinline__ int64_t ch_floors_below(uint32_t x, uint32_t g) {
     const uint32_t q = x / g, r = x - q * g;
     return static_cast<int64_t>(g) * (static_cast<int64_t>(q) * (static_cast<int64_t>(q) - 1) / 2) + static_cast<int64_t>(q) * r;
 }
-__host__ __device__ inline int64_t ch_floor_sum(uint32_t a, uint32_t g, uint32_t n, int step) {
+__device__ __noinline__ int ch_floor_sum(uint32_t a, uint32_t g, uint32_t n, int step) {
     if (n == 0) return 0;
     const uint32_t hi = a + step * n;
-    const int64_t all = ch_floors_below(hi, g) - ch_floors_below(a, g);
-    if (step == 1) return all;
-    int64_t more = 0;
-    if (g % 2 == 0) {
-        if (a % 2 == 1) more = static_cast<int64_t>((hi - 1) / g) - a / g;
-    } else if (a % 2 == 1) {
-        more = static_cast<int64_t>((hi - 1) / (2 * g)) - a / (2 * g);
-    } else {
-        more = static_cast<int64_t>((hi - 1 + g) / (2 * g)) - (a + g) / (2 * g);
+    int64_t all = ch_floors_below(hi, g) - ch_floors_below(a, g);
+    if (step == 2) {
+        // Multiples of g among a + 1, a + 3, .., hi - 1: of even g all in between, of odd g every other one.
+        const bool odd = g & 1u;
+        const uint32_t m = odd ? 2 * g : g, shift = odd && a % 2 == 0 ? g : 0;
+        if (odd || a % 2 == 1) all -= (hi - 1 + shift) / m - (a + shift) / m;
+        all /= 2;
     }
-    return (all - more) / 2;
+    return static_cast<int>(all);
 }
 
 // One request as the kernel takes it.  Row tile i's last row sees the tiles
@@ -161,128 +184,123 @@ struct ChunkSeq {
     int first, rows, len;  // rows 0: nothing to do
     int tiles;             // of the whole cache
     int row_tiles;
-    int a, g, step, kv_heads;
-    int full, last;        // list entries of a tile: of a row tile, of the last one
+    int a, last;           // last: list entries of a tile of the last row tile
     bool bad;
-    __host__ __device__ int seen(int i) const {  // tiles of row tile i
-        const int t = (a + step * i) / g + 1;
-        return t < tiles ? t : tiles;
-    }
-    __host__ __device__ int weight(int i) const { return i + 1 == row_tiles ? last : full; }
-    // Entries of the row tiles below i, i < row_tiles: each unit has one slot for its set-up and one per tile.
-    __host__ __device__ int64_t before(int i) const {
-        const int64_t lack = static_cast<int64_t>(tiles - 1) * g - a;  // from row tile ceil(lack / step) on all tiles are seen
-        const int64_t all = lack <= 0 ? 0 : (lack + step - 1) / step, some = all < i ? all : i;
-        const int64_t slots = ch_floor_sum(static_cast<uint32_t>(a), static_cast<uint32_t>(g), static_cast<uint32_t>(some), step) + some +
-                              (i - some) * tiles + i;
-        return slots * full * kv_heads;
-    }
-    __host__ __device__ int64_t entries() const {
-        if (row_tiles == 0) return 0;
-        return before(row_tiles - 1) + static_cast<int64_t>(kv_heads) * last * (seen(row_tiles - 1) + 1);
-    }
 };
-
-__host__ __device__ inline ChunkSeq ch_seq_of(int first, int64_t rows, int len, int total_rows, int group, int kv_heads, int max_tiles,
-                                              int unit_rows, int tile) {
-    ChunkSeq q;
-    q.first = first;
-    const bool off = first < 0 || rows < 0 || first + rows > total_rows;
-    q.bad = off || len < 0;
-    q.rows = off ? 0 : static_cast<int>(rows);
-    q.len = len < 0 ? 0 : len;
-    const int all = q.len / tile + (q.len % tile != 0);
-    q.tiles = all < max_tiles ? all : max_tiles;
-    const int64_t flat = static_cast<int64_t>(q.rows) * group;
-    q.row_tiles = static_cast<int>((flat + unit_rows - 1) / unit_rows);
-    // The first row's position, no further than the table's end (all tiles are seen from there on).
-    int64_t p = static_cast<int64_t>(q.len) - q.rows;
-    const int64_t end = static_cast<int64_t>(max_tiles) * tile;
-    p = p < 0 ? 0 : p < end ? p : end;
-    q.a = static_cast<int>((p * group + unit_rows - 1) / tile);
-    q.g = group;
-    q.step = unit_rows / tile;
-    q.kv_heads = kv_heads;
-    q.full = unit_rows / 128;
-    q.last = flat - static_cast<int64_t>(q.row_tiles - 1) * unit_rows > 128 ? q.full : 1;
-    return q;
-}
 template <typename Sh>
-__device__ __forceinline__ ChunkSeq ch_seq(const ChunkArgs &a, int s) {
-    const int first = a.q_starts[s];
-    return ch_seq_of(first, static_cast<int64_t>(a.q_starts[s + 1]) - first, a.seq_lens[s], a.total_rows, a.group, a.kv_heads, a.max_tiles,
-                     Sh::U, Sh::T);
-}
-
-// The place of entry x of a request: its row tile, head and slot, by `search`
-// (the number of row tiles i > 0 whose entries begin at or below x), and the
-// entry moved back to the slot's start.  A cut in a unit's set-up or first two
-// tiles goes to the unit's start: joining parts costs more than they do.
-constexpr int kChSmallCut = 2;
-struct ChunkPlace {
-    int row_tile, head, slot;
-    int64_t at;
-};
-template <typename Search>
-__host__ __device__ inline ChunkPlace ch_place(const ChunkSeq &q, int64_t x, Search search) {
-    ChunkPlace p;
-    p.row_tile = search(q, x);
-    const int64_t base = q.before(p.row_tile);
-    const int w = q.weight(p.row_tile), unit = w * (q.seen(p.row_tile) + 1);
-    const int off = static_cast<int>(x - base);  // within a row tile's units: kv_heads x unit < 2^31
-    p.head = off / unit;
-    p.slot = (off - p.head * unit) / w;
-    if (p.slot <= kChSmallCut) p.slot = 0;
-    p.at = base + static_cast<int64_t>(p.head) * unit + p.slot * w;
-    return p;
-}
-
-// A position in a CTA's range of the list: request, row tile and head, the
-// unit's slots from e0 on (slot 0 is the set-up, slot j + 1 tile j), tiles
-// [j0, j1), and the list entries left after them.
-template <typename Sh>
-struct ChunkWalk {
+struct ChunkList {
+    static constexpr int kStep = Sh::U / Sh::T, kFull = Sh::U / 128;  // kFull: list entries of a tile of a full row tile
     const ChunkArgs &a;
-    ChunkSeq q;
-    int s, row_tile, head, tiles, weight, e0, j0, j1;
-    int64_t left;
-    __device__ __forceinline__ ChunkWalk(const ChunkArgs &args, const int (&at)[4], int64_t count) : a(args), left(count) {
-        s = at[0];
-        row_tile = at[1];
-        head = at[2];
-        e0 = at[3];
-        q = ch_seq<Sh>(a, s);
-        unit();
+    __device__ __noinline__ ChunkSeq seq(int s) const {
+        ChunkSeq q;
+        q.first = a.q_starts[s];
+        const int64_t rows = static_cast<int64_t>(a.q_starts[s + 1]) - q.first;
+        const int len = a.seq_lens[s];
+        const bool off = q.first < 0 || rows < 0 || q.first + rows > a.total_rows;
+        q.bad = off || len < 0;
+        q.rows = off ? 0 : static_cast<int>(rows);
+        q.len = max(len, 0);
+        q.tiles = min(q.len / Sh::T + (q.len % Sh::T != 0), a.max_tiles);
+        const int flat = q.rows * a.group;
+        q.row_tiles = flat / Sh::U + (flat % Sh::U != 0);
+        // The first row's position, no further than the table's end (all tiles are seen from there on).
+        const int p = min(max(q.len - q.rows, 0), a.max_tiles * Sh::T);
+        q.a = static_cast<int>((static_cast<int64_t>(p) * a.group + Sh::U - 1) / Sh::T);
+        q.last = flat - (q.row_tiles - 1) * Sh::U > 128 ? kFull : 1;
+        return q;
     }
-    __device__ __forceinline__ void unit() {
-        tiles = q.seen(row_tile);
-        weight = q.weight(row_tile);
-        const int64_t room = left / weight;
-        const int e1 = e0 + room < tiles + 1 ? static_cast<int>(e0 + room) : tiles + 1;
-        left -= static_cast<int64_t>(e1 - e0) * weight;
-        j0 = max(e0 - 1, 0);
-        j1 = e1 - 1;
+    __device__ __forceinline__ int seen(const ChunkSeq &q, int i) const { return min((q.a + kStep * i) / a.group + 1, q.tiles); }
+    __device__ __forceinline__ int weight(const ChunkSeq &q, int i) const { return i + 1 == q.row_tiles ? q.last : kFull; }
+    // Entries of the row tiles below i, i < row_tiles: each unit has one slot for its set-up and one per tile.
+    __device__ __noinline__ int before(const ChunkSeq &q, int i) const {
+        const int64_t lack = static_cast<int64_t>(q.tiles - 1) * a.group - q.a;  // from row tile ceil(lack / step) on all tiles are seen
+        const int some = lack <= 0 ? 0 : static_cast<int>(min((lack + kStep - 1) / kStep, static_cast<int64_t>(i)));
+        const int slots = ch_floor_sum(q.a, a.group, some, kStep) + some + (i - some) * q.tiles + i;
+        return slots * kFull * a.kv_heads;
     }
-    __device__ __forceinline__ bool none() const { return j1 <= j0; }
-    __device__ __forceinline__ bool starts() const { return e0 == 0; }
-    __device__ __forceinline__ bool ends() const { return j1 == tiles; }
-    __device__ __forceinline__ int row0() const { return row_tile * Sh::U; }
-    __device__ __forceinline__ int products() const { return Sh::NS == 1 ? 1 : weight; }  // 128-row products with rows
-    __device__ __forceinline__ bool next() {
-        if (left <= 0) return false;
-        if (++head == a.kv_heads) {
+    __device__ __forceinline__ int entries(const ChunkSeq &q) const {
+        return q.row_tiles == 0 ? 0 : before(q, q.row_tiles - 1) + a.kv_heads * q.last * (seen(q, q.row_tiles - 1) + 1);
+    }
+};
+
+// A cut in a unit's set-up or first two tiles goes to the unit's start: joining
+// parts costs more than they do.
+constexpr int kChSmallCut = 2;
+
+// Lays out the CTA's units (one thread).  What the join needs goes to a.heads: the
+// last unit, whether it is cut and begins here (1), and whether the whole range is
+// the middle of one unit (2).
+template <typename Sh>
+__device__ __forceinline__ void ch_plan(const ChunkArgs &a, ChunkShared &sh) {
+    const ChunkList<Sh> list{a};
+    int s = sh.at[0], row_tile = sh.at[1], head = sh.at[2], e0 = sh.at[3], left = sh.cut[1] - sh.cut[0];
+    ChunkSeq q = list.seq(s);
+    const bool first_cut = e0 != 0;
+    for (int u = 0;; ++u) {
+        const int slot = u & (kChUnits - 1);
+        // (Not one of the role's waits: after one of those ran out the units still go round.)
+        if (u >= kChUnits && !mbar_wait_bounded(smem_addr(&sh.unit_free[slot]), static_cast<uint32_t>(u / kChUnits - 1) & 1u)) return;
+        ChunkUnit &x = sh.units[slot];
+        if (left <= 0) {
+            x.flags = kChStop;
+            mbar_arrive(smem_addr(&sh.unit_full[slot]));
+            return;
+        }
+        const int tiles = list.seen(q, row_tile), weight = list.weight(q, row_tile);
+        const int e1 = min(tiles + 1, e0 + (weight == 2 ? left >> 1 : left));
+        left -= (e1 - e0) * weight;
+        x.first = q.first;
+        x.rows = q.rows;
+        x.len = q.len;
+        x.s = s;
+        x.row0 = row_tile * Sh::U;
+        x.head = head;
+        x.j0 = max(e0 - 1, 0);
+        x.tiles = e1 - 1 - x.j0;
+        x.flags = (e0 == 0 ? kChStarts : 0) | (e1 == tiles + 1 ? kChEnds : 0) | (weight == 2 ? kChTwo : 0);
+        mbar_arrive(smem_addr(&sh.unit_full[slot]));
+        if (left <= 0) {
+            const bool last_cut = e1 != tiles + 1;
+            a.heads[2 * blockIdx.x] = make_int4(s, row_tile, head, (last_cut && e0 == 0 ? 1 : 0) | (u == 0 && first_cut && last_cut ? 2 : 0));
+            a.heads[2 * blockIdx.x + 1] = make_int4(q.first, q.rows, 0, 0);
+        } else if (++head == a.kv_heads) {
             head = 0;
             if (++row_tile == q.row_tiles) {
                 row_tile = 0;
-                do q = ch_seq<Sh>(a, ++s);
+                do q = list.seq(++s);
                 while (q.rows == 0);
             }
         }
         e0 = 0;
-        unit();
-        return true;
     }
-};
+}
+
+// A role's wait, for a whole warp: for at most the limit, or until another role has
+// raised the abort flag.  (A short loop: the waits are inlined in every role.)
+__device__ __forceinline__ bool ch_wait(const ChunkArgs &a, ChunkShared &sh, uint64_t &bar, uint32_t parity) {
+    const uint32_t at = smem_addr(&bar);
+    uint64_t t0 = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (int n = 1; ok && !mbar_try_wait_short(at, parity); ++n) {
+        if ((n & 15) != 0) continue;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 >= a.wait_limit_ns) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+        ok = *reinterpret_cast<volatile int *>(&sh.abort) == 0;
+    }
+    return __all_sync(0xFFFFFFFFu, ok);
+}
+
+// The u-th unit, for a warp; false after the last one.
+__device__ __forceinline__ bool ch_unit(ChunkShared &sh, int u, int lane, ChunkUnit &x) {
+    const int slot = u & (kChUnits - 1);
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded<false>(smem_addr(&sh.unit_full[slot]), static_cast<uint32_t>(u / kChUnits) & 1u))) return false;
+    x = sh.units[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&sh.unit_free[slot]));
+    return (x.flags & kChStop) == 0;
+}
 
 // ------------------------------------------------------------------ pieces
 // kind::f16 instruction descriptor: f16 A and B, f32 D; B K-major or MN-major.
@@ -357,331 +375,388 @@ __device__ __forceinline__ uint64_t ch_add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// r / group and the remainder, r < 2^31 (the estimate is at most one too small).
+__device__ __forceinline__ int ch_token(const ChunkArgs &a, int r, int &head) {
+    int t = static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.group_inverse));
+    head = r - t * a.group;
+    if (head >= a.group) {
+        ++t;
+        head -= a.group;
+    }
+    return t;
+}
+// The largest of three.
+__device__ __forceinline__ float ch_max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float ch_max16(const float *v) {
+    float m = ch_max3(v[0], v[1], v[2]), n = ch_max3(v[3], v[4], v[5]);
+#pragma unroll
+    for (int x = 6; x < 14; x += 4) {
+        m = ch_max3(m, v[x], v[x + 1]);
+        n = ch_max3(n, v[x + 2], v[x + 3]);
+    }
+    m = ch_max3(m, v[14], v[15]);
+    return fmaxf(m, n);
+}
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float ch_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// A unit's queries.  They are copied as they are to where their f16 planes will
+// lie (all copies in flight at once; a bf16 row is as long as one plane, an f32 row
+// as two), and converted in place: a warp takes two rows at a time (one of a wide
+// head), sixteen (32) lanes a row, eight values a lane.  (Short loops: this code
+// runs once a unit, and unrolled its instructions took longer to come than the
+// queries: 13 us a unit.)
 template <typename Sh, typename T>
-__device__ __forceinline__ void ch_queries(const ChunkArgs &a, const ChunkWalk<Sh> &w, uint8_t *sq, float *qs, int warp, int lane) {
-    // A warp takes two rows at a time (one of a wide head), sixteen (32) lanes a row, eight values a lane.
-    constexpr int L = Sh::WIDE ? 32 : 16, RW = 32 / L, PL = Sh::PL;
-    const int sub = lane / L, d0 = (lane % L) * 8, rows = w.products() * 128;
-    const int flat = w.q.rows * a.group - w.row0();  // rows of the unit that exist
-    const bool negative = a.c < 0.f;
-    const T *q = static_cast<const T *>(a.q) + w.q.first * a.q_stride + static_cast<int64_t>(w.head) * a.group * a.head_dim;
-    constexpr int kBatch = 4;
+__device__ __forceinline__ void ch_queries(const ChunkArgs &a, const ChunkUnit &w, uint8_t *sq, float *qs, int warp, int lane) {
+    constexpr int L = Sh::WIDE ? 32 : 16, RW = 32 / L, PL = Sh::PL, kStride = kChConvertWarps * RW;
+    const int d0 = (lane % L) * 8, rows = w.flags & kChTwo ? 256 : 128;
+    const int flat = w.rows * a.group - w.row0;  // rows of the unit that exist
+    const T *q = static_cast<const T *>(a.q) + w.first * a.q_stride + static_cast<int64_t>(w.head) * a.group * a.head_dim + d0;
+    const int r0 = warp * RW + lane / L;
+    auto place = [&](int r) {
+        return sq + (r >> 7) * (PL * Sh::kQPlane) + (d0 >> 6) * (128 * 128) + (r & 127) * 128 + ((((d0 >> 3) & 7) ^ (r & 7)) << 4);
+    };
 #pragma unroll 1
-    for (int r0 = warp * RW + sub; r0 < rows; r0 += kChConvertWarps * RW * kBatch) {
-        float x[kBatch][8];
+    for (int r = r0; r < rows; r += kStride) {
+        int head;
+        const int token = ch_token(a, w.row0 + r, head);
+        const T *x = q + token * a.q_stride + head * a.head_dim;
+        const uint32_t dst = smem_addr(place(r)), bytes = r < flat && d0 < a.head_dim ? 16 : 0;  // the rest is filled with zeros
+        if (bytes == 0) x = static_cast<const T *>(a.q);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(x), "r"(bytes) : "memory");
+        if (PL == 2) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + Sh::kQPlane), "l"(x + (bytes ? 4 : 0)), "r"(bytes) : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+    for (int r = r0; r < rows; r += kStride) {
+        uint8_t *at = place(r);
+        float x[8];
+        if constexpr (PL == 2) {
+            const float4 u = *reinterpret_cast<const float4 *>(at), v = *reinterpret_cast<const float4 *>(at + Sh::kQPlane);
+            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+        } else {
+            rope_load8(reinterpret_cast<const __nv_bfloat16 *>(at), x);
+        }
+        uint32_t top = 0;
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + b * kChConvertWarps * RW;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[b][i] = 0.f;
-            if (r < rows && r < flat && d0 < a.head_dim) {
-                const int token = (w.row0() + r) / a.group;
-                rope_load8(q + token * a.q_stride + (w.row0() + r - token * a.group) * a.head_dim + d0, x[b]);
-            }
+        for (int i = 0; i < 8; ++i) {
+            if (PL == 2) x[i] = fmaf(x[i], a.c, x[i] * a.c_low);  // the scale per value, rounded at random
+            top = max(top, __float_as_uint(fabsf(x[i])));
         }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + b * kChConvertWarps * RW;
-            uint32_t top = 0;
+        for (int d = L / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        const bool good = top < 0x7F800000u;
+        int e = 0;  // the row's largest times 2^e is in [2^14, 2^15)
+        if (good && top != 0) e = top >= 0x800000u ? 14 + 127 - static_cast<int>(top >> 23) : 14 + 149 - (31 - __clz(top));
+        const int e1 = e >> 1, e2 = e - e1;
+        if (lane % L == 0)
+            qs[r] = good ? ch_pow2(-e1) * (PL == 2 ? 1.f : fabsf(a.c)) * ch_pow2(-e2) : __int_as_float(0x7FC00000);
+        // (bf16: the sign of the softmax scale goes here.)
+        const float f1 = good ? ch_pow2(e1) : 0.f, f2 = PL == 1 && a.c < 0.f ? -ch_pow2(e2) : ch_pow2(e2);
+        uint32_t h[4], l[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (PL == 2) x[b][i] = fmaf(x[b][i], a.c, x[b][i] * a.c_low);  // the scale per value, rounded at random
-                else if (negative) x[b][i] = -x[b][i];
-                top = max(top, __float_as_uint(fabsf(x[b][i])));
-            }
-#pragma unroll
-            for (int d = L / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-            const bool good = top < 0x7F800000u;
-            int e = 0;  // the row's largest times 2^e is in [2^14, 2^15)
-            if (good && top != 0) e = top >= 0x800000u ? 14 + 127 - static_cast<int>(top >> 23) : 14 + 149 - (31 - __clz(top));
-            const float f1 = ch_pow2(e >> 1), f2 = ch_pow2(e - (e >> 1));
-            if (r >= rows) continue;
-            if (lane % L == 0) {
-                const float back = ch_pow2(-(e >> 1)) * (PL == 2 ? 1.f : fabsf(a.c)) * ch_pow2(-(e - (e >> 1)));
-                qs[r] = good ? back : __int_as_float(0x7FC00000);
-            }
-            uint32_t h[4], l[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = good ? x[b][2 * i] * f1 * f2 : 0.f, v = good ? x[b][2 * i + 1] * f1 * f2 : 0.f;
-                h[i] = ch_pack_f16(u, v);
-                if (PL == 2) {
-                    const float2 f = ch_unpack_f16(h[i]);
-                    l[i] = ch_pack_f16(u - f.x, v - f.y);
-                }
-            }
-            uint8_t *dst = sq + (r >> 7) * (PL * Sh::kQPlane) + (d0 >> 6) * (128 * 128) + (r & 127) * 128 + ((((d0 >> 3) & 7) ^ (r & 7)) << 4);
-            if (d0 < Sh::kBlocks * 64) {
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(h[0], h[1], h[2], h[3]);
-                if (PL == 2) *reinterpret_cast<uint4 *>(dst + Sh::kQPlane) = make_uint4(l[0], l[1], l[2], l[3]);
+        for (int i = 0; i < 4; ++i) {
+            const float u = good ? x[2 * i] * f1 * f2 : 0.f, v = good ? x[2 * i + 1] * f1 * f2 : 0.f;
+            h[i] = ch_pack_f16(u, v);
+            if (PL == 2) {
+                const float2 f = ch_unpack_f16(h[i]);
+                l[i] = ch_pack_f16(u - f.x, v - f.y);
             }
         }
+        *reinterpret_cast<uint4 *>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (PL == 2) *reinterpret_cast<uint4 *>(at + Sh::kQPlane) = make_uint4(l[0], l[1], l[2], l[3]);
     }
 }
 
 // ------------------------------------------------------------------ converters
+__device__ uint4 g_chunk_zeros;  // what tokens that are not there have for codes
+
 // Warps 8-15: q of each unit, then K and V of its tiles.  A thread has up to
 // four groups of sixteen codes of a tile; the next tile's codes are on their way
 // while this one's are converted, their block ids a tile earlier.
 template <typename Sh, typename T>
-__device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkWalk<Sh> w, ChunkShared &sh, uint8_t *sq, uint8_t *slots, int tid) {
+__device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, uint8_t *sq, uint8_t *slots, int tid) {
     constexpr int kEach = 4, kThreads = kChConvertWarps * 32;
     const int warp = tid >> 5, lane = tid & 31, per = a.head_dim / 16, total = Sh::T * per, block = 1 << a.block_log2;
-    int token[kEach], col[kEach];  // of the thread's groups in a tile
+    int token[kEach], from[kEach];  // of the thread's groups: token of a tile (T: none), place in the block of its first tile
     uint32_t dst[kEach];
+    auto group = [&](int i, int &t, int &c) {
+        const int g = tid + i * kThreads;
+        t = g < total ? g / per : Sh::T;
+        c = g < total ? g - t * per : 0;
+        return (c >> 2) * (Sh::T * 128) + t * 128 + (((2 * (c & 3)) ^ (t & 7)) << 4);
+    };
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const int g = tid + i * kThreads;
-        token[i] = g < total ? g / per : Sh::T;  // T: none
-        col[i] = g < total ? g - token[i] * per : 0;
-        dst[i] = (col[i] >> 2) * (Sh::T * 128) + token[i] * 128 + (((2 * (col[i] & 3)) ^ (token[i] & 7)) << 4);
+        int c;
+        dst[i] = group(i, token[i], c);
+        from[i] = (token[i] & (block - 1)) * a.head_dim + 16 * c;
     }
-    int n = 0;        // slots filled so far
-    int it = 0;       // tiles
-    int unit = 0;
-    bool more = !w.none();
-    while (!more && w.next()) more = !w.none();
-    const float nanf = __int_as_float(0x7FC00000);
-    while (more) {
-        const int ub = unit & 1, len = w.q.len, j1 = w.j1;
+    const int64_t id_bytes = static_cast<int64_t>(a.kv_heads) * block * a.head_dim;
+    const uint32_t n_blocks = static_cast<uint32_t>(a.n_blocks);
+    int n = 0, it = 0, unit = 0;  // slots filled so far, tiles, units with tiles
+    bool ok = true;
+    ChunkUnit w;
+    for (int u = 0; ch_unit(sh, u, lane, w); ++u) {
+        if (w.tiles == 0 || !ok) continue;
+        const int ub = unit & 1, j1 = w.j0 + w.tiles;
         const int32_t *row = a.table + static_cast<int64_t>(w.s) * a.width;
-        // A group's block: its id, -1 for one that is not there, -2 for tokens past the end.
-        auto ids_of = [&](int j, int (&id)[kEach]) {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const int64_t t = static_cast<int64_t>(j) * Sh::T + token[i];
-                id[i] = -2;
-                if (j < j1 && token[i] < Sh::T && t < len) {
-                    const int page = static_cast<int>(t >> a.block_log2);
-                    id[i] = page < a.width ? row[page] : -1;
-                }
-            }
+        const uint8_t *k_codes = a.k_codes + static_cast<int64_t>(w.head) * block * a.head_dim, *v_codes = a.v_codes + (k_codes - a.k_codes);
+        // Tiles below this have all their tokens, and the table has their blocks.
+        const int full = min(min(w.len, static_cast<int>(min(static_cast<int64_t>(a.width) << a.block_log2, static_cast<int64_t>(0x7FFFFFFF)))) / Sh::T, j1);
+        // The block of a token of a tile: its id (maybe one outside the pool), -1 where the table ends before it, -2 past the
+        // request's end.
+        auto id_of = [&](int j, int tok) {
+            const int t = j * Sh::T + tok;
+            if (j < full) return row[t >> a.block_log2];
+            if (j >= j1 || static_cast<int64_t>(j) * Sh::T + tok >= w.len) return -2;
+            return (t >> a.block_log2) < a.width ? row[t >> a.block_log2] : -1;
         };
-        auto fetch = [&](int j, const int (&id)[kEach], const uint8_t *codes, const float *scales, uint4 (&x)[kEach], float (&sc)[kEach]) {
+        auto ids = [&](int j, int (&id)[kEach]) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) id[i] = token[i] < Sh::T ? id_of(j, token[i]) : -2;
+        };
+        auto fetch = [&](int j, const int (&id)[kEach], const uint8_t *codes, uint4 (&x)[kEach]) {
+            // A block of more tokens than a tile: its tiles in turn.
+            const int more = block > Sh::T ? (j * Sh::T & (block - 1)) * a.head_dim : 0;
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                x[i] = make_uint4(0, 0, 0, 0);
-                sc[i] = 1.f;
-                if (id[i] == -2) continue;
-                if (id[i] < 0 || id[i] >= a.n_blocks) {
-                    sc[i] = nanf;
-                    atomicOr(a.status, 4u);
-                    continue;
-                }
-                const int64_t bh = static_cast<int64_t>(id[i]) * a.kv_heads + w.head;
+                const uint4 *p = reinterpret_cast<const uint4 *>(codes + id[i] * id_bytes + (from[i] + more));
                 // (Plain loads: the kernel before this one may have written the cache after this one had begun.)
-                x[i] = *reinterpret_cast<const uint4 *>(codes + ((bh << a.block_log2) + ((j * Sh::T + token[i]) & (block - 1))) * a.head_dim +
-                                                        16 * col[i]);
-                sc[i] = scales[bh];
+                x[i] = *(static_cast<uint32_t>(id[i]) < n_blocks ? p : &g_chunk_zeros);
             }
         };
-        int id[kEach], id_next[kEach];
+        int id[kEach];
         uint4 kx[kEach], vx[kEach];
-        float ks[kEach], vs[kEach];
-        ids_of(w.j0, id);
-        ids_of(w.j0 + 1, id_next);
-        fetch(w.j0, id, a.k_codes, a.k_scales, kx, ks);
-        fetch(w.j0, id, a.v_codes, a.v_scales, vx, vs);
+        ids(w.j0, id);
+        fetch(w.j0, id, k_codes, kx);
+        fetch(w.j0, id, v_codes, vx);
+        ids(w.j0 + 1, id);
         // The unit's queries, once the MMAs have read the last one's, and the softmax has written out the one before that.
-        if (unit >= 1 && !at_warp_wait(smem_addr(&sh.q_free), static_cast<uint32_t>(unit - 1) & 1u, &sh.abort, a.wait_limit_ns)) return;
-        if (unit >= 2 && !at_warp_wait(smem_addr(&sh.unit_done[ub]), static_cast<uint32_t>((unit >> 1) - 1) & 1u, &sh.abort, a.wait_limit_ns)) return;
+        ok = (unit < 1 || ch_wait(a, sh, sh.q_free, static_cast<uint32_t>(unit - 1) & 1u)) &&
+             (unit < 2 || ch_wait(a, sh, sh.unit_done[ub], static_cast<uint32_t>((unit >> 1) - 1) & 1u));
         sh.vnan[ub][tid] = kChNoNan;
         if (tid == 0) sh.any_nan[ub] = 0;
         asm volatile("bar.sync 4, %0;" ::"n"(kThreads) : "memory");
+        if (!ok) continue;
         ch_queries<Sh, T>(a, w, sq, sh.qs[ub], warp, lane);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[ub]));
-        for (int j = w.j0; j < j1; ++j, ++it) {
+        // One slot: groups of codes as f16 into shared memory.
+        auto slot_begin = [&]() {
+            ok = n < Sh::kSlots || ch_wait(a, sh, sh.slot_free[n % Sh::kSlots], (static_cast<uint32_t>(n / Sh::kSlots) & 1u) ^ 1u);
+            return ok;
+        };
+        auto slot_end = [&]() {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic stores -> the MMA
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.slot_full[n % Sh::kSlots]));
+            ++n;
+        };
+        auto store = [&](uint8_t *to, int i, const uint4 &c, uint32_t (&h)[8]) {
+            const uint32_t x[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                h[2 * y] = at_e4m3x2_f16x2(x[y]);
+                h[2 * y + 1] = at_e4m3x2_f16x2(x[y] >> 16);
+            }
+            if (token[i] < Sh::T) {
+                *reinterpret_cast<uint4 *>(to + dst[i]) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(to + (dst[i] ^ 16u)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+        };
 #pragma unroll 1
-            for (int is_v = 0; is_v < 2; ++is_v, ++n) {
-                const int slot = n % Sh::kSlots;
-                const uint32_t ph = static_cast<uint32_t>(n / Sh::kSlots) & 1u;
-                if (n >= Sh::kSlots && !at_warp_wait(smem_addr(&sh.slot_free[slot]), ph ^ 1u, &sh.abort, a.wait_limit_ns)) return;
-                uint8_t *to = slots + slot * Sh::kSlot;
+        for (int j = w.j0; ok && j < j1; ++j, ++it) {
+            if (!slot_begin()) break;
+            uint8_t *to = slots + (n % Sh::kSlots) * Sh::kSlot;
 #pragma unroll
-                for (int i = 0; i < kEach; ++i) {
-                    if (token[i] >= Sh::T) continue;
-                    const float scale = is_v ? vs[i] : ks[i];
-                    const uint4 c = is_v ? vx[i] : kx[i];
-                    uint32_t x[4] = {c.x, c.y, c.z, c.w};
-                    const bool finite = fabsf(scale) < INFINITY;
-                    const uint32_t sign = scale < 0.f ? 0x80808080u : 0u;  // the scale's magnitude is what the softmax uses
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) x[y] ^= sign;
-                    if (is_v) {
-                        uint32_t bad = 0;
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) bad |= (x[y] & 0x7F7F7F7Fu) + 0x01010101u;
-                        if ((bad & 0x80808080u) != 0 || !finite) {  // seldom: which elements, from which position on
-                            const int p = j * Sh::T + token[i];
+            for (int i = 0; i < kEach; ++i) {
+                uint32_t h[8];
+                store(to, i, kx[i], h);
+            }
+            if (warp == 0) {
+                // Scales of the tile's sixteens, and a flag for blocks outside the pool.
+                float k1 = 1.f;
+                if (lane < Sh::kGranules) {
+                    const int b = id_of(j, 16 * lane);
+                    const int64_t bh = static_cast<int64_t>(b) * a.kv_heads + w.head;
+                    float v1 = 1.f;
+                    if (b != -2) {
+                        const bool there = static_cast<uint32_t>(b) < n_blocks;
+                        k1 = there ? a.k_scales[bh] : INFINITY;
+                        v1 = there ? a.v_scales[bh] : INFINITY;
+                        if (!there) atomicOr(a.status, 4u);
+                        if (!(fabsf(k1) < INFINITY)) k1 = __int_as_float(0x7FC00000);
+                        if (!(fabsf(v1) < INFINITY)) {  // every element, from here on
                             sh.any_nan[ub] = 1;
 #pragma unroll 1
-                            for (int y = 0; y < 16; ++y) {
-                                const uint32_t word = y < 8 ? (y < 4 ? x[0] : x[1]) : (y < 12 ? x[2] : x[3]);
-                                const uint32_t code = (word >> (8 * (y & 3))) & 0x7Fu;
-                                if (!finite || code == 0x7Fu) {
-                                    atomicMin(&sh.vnan[ub][16 * col[i] + y], p);
-                                    const uint32_t keep = ~(0xFFu << (8 * (y & 3)));
-#pragma unroll
-                                    for (int z = 0; z < 4; ++z)
-                                        if (z == y >> 2) x[z] &= keep;
-                                }
-                            }
+                            for (int d = 0; d < a.head_dim; ++d) atomicMin(&sh.vnan[ub][d], j * Sh::T + 16 * lane);
+                            v1 = 1.f;
                         }
-                    } else if (!finite) {
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) x[y] = 0x7F7F7F7Fu;
                     }
-                    uint32_t h[8];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        h[2 * y] = at_e4m3x2_f16x2(x[y]);
-                        h[2 * y + 1] = at_e4m3x2_f16x2(x[y] >> 16);
-                    }
-                    *reinterpret_cast<uint4 *>(to + dst[i]) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4 *>(to + (dst[i] ^ 16u)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    const bool small = fabsf(v1) < 0x1p-126f;
+                    const uint32_t bits = __float_as_uint(small ? v1 * 0x1p64f : v1), e = bits >> 23 & 0xFFu;
+                    sh.info[it & (kChInfo - 1)][lane] =
+                        v1 == 0.f ? make_float4(k1, -1000.f, 1.f, 0.f)
+                                  : make_float4(k1, static_cast<float>(static_cast<int>(e) - (small ? 191 : 127)),
+                                                __uint_as_float((bits & 0x807FFFFFu) | 0x3F800000u), 0.f);
                 }
-                if (!is_v && warp == 0) {
-                    // Scales of the tile's sixteens (both, for the softmax).
-                    if (lane < Sh::kGranules) {
-                        const int64_t t = static_cast<int64_t>(j) * Sh::T + 16 * lane;
-                        float k1 = 1.f, v1 = 1.f;
-                        if (t < len && (t >> a.block_log2) < a.width) {
-                            const int b = row[t >> a.block_log2];
-                            if (b >= 0 && b < a.n_blocks) {
-                                k1 = fabsf(a.k_scales[static_cast<int64_t>(b) * a.kv_heads + w.head]);
-                                v1 = fabsf(a.v_scales[static_cast<int64_t>(b) * a.kv_heads + w.head]);
-                            }
-                        }
-                        if (!(k1 < INFINITY)) k1 = 1.f;  // K's codes are NaN there
-                        if (!(v1 < INFINITY)) v1 = 1.f;  // V's are zero
-                        float e = 0.f, m = 1.f;
-                        const bool small = v1 < 0x1p-126f;
-                        const uint32_t u = __float_as_uint(small ? v1 * 0x1p64f : v1);
-                        if (v1 == 0.f) {
-                            e = -1000.f;
-                        } else {
-                            e = static_cast<float>(static_cast<int>(u >> 23) - 127 - (small ? 64 : 0));
-                            m = __uint_as_float((u & 0x7FFFFFu) | 0x3F800000u);
-                        }
-                        sh.info[it & (kChInfo - 1)][lane] = make_float4(k1, e, m, 0.f);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sh.info_full[it & (kChInfo - 1)]));
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic stores -> the MMA
+                const bool minus = __any_sync(0xFFFFFFFFu, k1 < 0.f);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.slot_full[slot]));
-                if (is_v) {
-                    fetch(j + 1, id_next, a.v_codes, a.v_scales, vx, vs);
-#pragma unroll
-                    for (int i = 0; i < kEach; ++i) id[i] = id_next[i];
-                    ids_of(j + 2, id_next);
-                } else {
-                    fetch(j + 1, id_next, a.k_codes, a.k_scales, kx, ks);
+                if (lane == 0) {
+                    sh.info_minus[it & (kChInfo - 1)] = minus;
+                    mbar_arrive(smem_addr(&sh.info_full[it & (kChInfo - 1)]));
                 }
             }
+            slot_end();
+            fetch(j + 1, id, k_codes, kx);
+            if (!slot_begin()) break;
+            to = slots + (n % Sh::kSlots) * Sh::kSlot;
+            __half2 sum = __half2(__ushort_as_half(0), __ushort_as_half(0));  // of the values (at most 32 x 448): a NaN shows in it
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                uint32_t h[8];
+                store(to, i, vx[i], h);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) sum = __hadd2(sum, *reinterpret_cast<const __half2 *>(h + y));
+            }
+            if (__hisnan(sum.x) || __hisnan(sum.y)) {  // seldom: zeros in their places, and from which position on each element has one
+                sh.any_nan[ub] = 1;
+#pragma unroll 1
+                for (int i = 0; i < kEach; ++i) {
+                    int t, c;
+                    const uint32_t at = group(i, t, c);
+                    if (t >= Sh::T) break;
+#pragma unroll 1
+                    for (int y = 0; y < 16; ++y) {
+                        uint16_t *h = reinterpret_cast<uint16_t *>(to + (y < 8 ? at : at ^ 16u)) + (y & 7);
+                        if ((*h & 0x7C00u) != 0x7C00u) continue;
+                        *h = 0;
+                        atomicMin(&sh.vnan[ub][16 * c + y], j * Sh::T + t);
+                    }
+                }
+            }
+            slot_end();
+            fetch(j + 1, id, v_codes, vx);
+            ids(j + 2, id);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.values_done[ub]));
         ++unit;
-        do more = w.next();
-        while (more && w.none());
     }
 }
 
 // ------------------------------------------------------------------ MMAs
+// One thread of the (converged) warp.
+__device__ __forceinline__ bool ch_elect() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
+// The MMAs of product `i`.  The warp goes through the tiles together; one thread
+// issues.  Returns whether anything was issued.
 template <typename Sh>
-__device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkWalk<Sh> w, ChunkShared &sh, uint32_t tmem, uint32_t sq, uint32_t slots) {
+__device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, uint32_t tmem_base, uint32_t sq, uint32_t slots, int product,
+                                         int lane) {
     constexpr int PL = Sh::PL, T = Sh::T;
     constexpr uint32_t qk_idesc = ch_idesc(T, false);
-    const uint64_t q_desc = ch_desc(sq, 16), k_desc = ch_desc(slots, 16), v_desc = ch_desc(slots, T * 128);
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
+    const int i = Sh::NS == 1 ? 0 : __shfl_sync(0xFFFFFFFFu, product, 0);
+    const uint64_t q_desc = ch_desc(sq + i * PL * Sh::kQPlane, 16), k_desc = ch_desc(slots, 16), v_desc = ch_desc(slots, T * 128);
     const int steps = a.head_dim / 16;
-    bool any = false;
+    bool any = false, ok = true;
     auto wait = [&](uint64_t &bar, uint32_t parity) {
-        const bool ok = at_wait(smem_addr(&bar), parity, &sh.abort, a.wait_limit_ns);
+        ok = ok && ch_wait(a, sh, bar, parity);
         t8_fence_after();
         return ok;
     };
-    int n = 0, unit = 0;               // slots consumed in order K, V, K, V ..; units
-    int done[2] = {0, 0};              // tiles of each product whose weights have been taken
-    int begun[2] = {0, 0};             // ... whose scores have been issued
-    int products = 0;                  // f32: products of a tile (of half a wide head) issued
-    auto scores = [&](int i, int slot) {  // product i's scores against K in the slot, the second plane's first
-        const uint32_t d = tmem + static_cast<uint32_t>(Sh::NS == 1 ? (begun[0] & 1) * T : i * 128);
-        const uint64_t k = k_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
+    int n = 0, unit = 0;      // slots consumed in order K, V, K, V ..; units with tiles
+    int done = 0, begun = 0;  // tiles whose weights have been taken, whose scores have been issued
+    int products = 0;         // f32: products of a tile (of half a wide head) issued
+    // Scores against K in the slot, the second plane's first.  end: q is read.
+    auto scores = [&](int slot, bool end) {
+        const int buf = Sh::NS == 1 ? begun & 1 : i;
+        if (ch_elect()) {
+            const uint32_t d = tmem + static_cast<uint32_t>(buf * (Sh::NS == 1 ? T : 128));
+            const uint64_t k = k_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
 #pragma unroll 1
-        for (int p = PL - 1; p >= 0; --p) {
-            const uint64_t q = q_desc + static_cast<uint32_t>(i * PL + p) * (Sh::kQPlane / 16);
-#pragma unroll 4
-            for (int s = 0; s < steps; ++s)
-                ch_mma_ss(d, q + (s >> 2) * (128 * 128 / 16) + (s & 3) * 2, k + (s >> 2) * (T * 128 / 16) + (s & 3) * 2, qk_idesc,
-                          p + 1 < PL || s > 0);
+            for (int p = PL - 1; p >= 0; --p) {
+                const uint64_t q = q_desc + static_cast<uint32_t>(p) * (Sh::kQPlane / 16);
+#pragma unroll 1
+                for (int s = 0; s < steps; ++s)
+                    ch_mma_ss(d, q + (s >> 2) * (128 * 128 / 16) + (s & 3) * 2, k + (s >> 2) * (T * 128 / 16) + (s & 3) * 2, qk_idesc,
+                              p + 1 < PL || s > 0);
+            }
+            t8_commit(smem_addr(&sh.s_full[buf]));
+            t8_commit(smem_addr(&sh.slot_free[slot]));
+            if (end) t8_commit(smem_addr(&sh.q_free));
         }
-        t8_commit(smem_addr(&sh.s_full[Sh::NS == 1 ? (begun[0] & 1) : i]));
-        ++begun[i];
+        __syncwarp();
+        ++begun;
         any = true;
     };
-    auto sums = [&](int i, int slot, bool acc) {  // product i's weights times V in the slot
-        const uint32_t p0 = tmem + static_cast<uint32_t>(Sh::NS == 1 ? (done[0] & 1) * T : i * 128);
+    auto sums = [&](int slot, bool acc) {  // the weights times V in the slot
+        const uint32_t p0 = tmem + Sh::weights_col(Sh::NS == 1 ? done & 1 : i, a.head_dim);
         const uint64_t v = v_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
 #pragma unroll 1
         for (int h = 0; h < Sh::kHalves; ++h) {
-            if (Sh::SUMS && products > 0 && !wait(sh.product_free, static_cast<uint32_t>(products - 1) & 1u)) return false;
-            const uint32_t d = tmem + static_cast<uint32_t>(Sh::SUMS ? Sh::kProductCol : Sh::kSumCol + i * 128);
-            const uint32_t idesc = ch_idesc(Sh::kHalves == 1 ? a.head_dim : h == 0 ? 128 : a.head_dim - 128, true);
-#pragma unroll
-            for (int p = PL - 1; p >= 0; --p)
-#pragma unroll
-                for (int s = 0; s < T / 16; ++s)
-                    ch_mma_ts(d, p0 + (PL == 1 ? 8 * s : 32 * (s >> 1) + 16 * p + 8 * (s & 1)),
-                              v + h * (2 * T * 128 / 16) + s * (16 * 128 / 16), idesc, (!Sh::SUMS && acc) || p + 1 < PL || s > 0);
-            t8_commit(smem_addr(&sh.o_done[i]));
+            if (Sh::SUMS && products > 0 && !wait(sh.product_free, static_cast<uint32_t>(products - 1) & 1u)) return;
+            if (ch_elect()) {
+                const uint32_t d = tmem + static_cast<uint32_t>(Sh::SUMS ? Sh::kProductCol : Sh::kSumCol + i * 128);
+                const int cols = Sh::sum_cols(a.head_dim);
+                const uint32_t idesc = ch_idesc(Sh::kHalves == 1 ? cols : h == 0 ? 128 : cols - 128, true);
+#pragma unroll 1
+                for (int p = PL - 1; p >= 0; --p)
+#pragma unroll 1
+                    for (int s = 0; s < T / 16; ++s)
+                        ch_mma_ts(d, p0 + (PL == 1 ? 8 * s : 32 * (s >> 1) + 16 * p + 8 * (s & 1)),
+                                  v + h * (2 * T * 128 / 16) + s * (16 * 128 / 16), idesc, (!Sh::SUMS && acc) || p + 1 < PL || s > 0);
+                t8_commit(smem_addr(&sh.o_done[i]));
+                if (h + 1 == Sh::kHalves) t8_commit(smem_addr(&sh.slot_free[slot]));
+            }
+            __syncwarp();
             ++products;
         }
-        ++done[i];
-        return true;
+        ++done;
     };
     auto slot_ready = [&](int m) { return wait(sh.slot_full[m % Sh::kSlots], static_cast<uint32_t>(m / Sh::kSlots) & 1u); };
-    bool more = !w.none();
-    while (!more && w.next()) more = !w.none();
-    while (more) {
-        const int np = w.products(), tiles = w.j1 - w.j0;
-        if (!wait(sh.q_full[unit & 1], static_cast<uint32_t>(unit >> 1) & 1u)) return any;
-        if (!slot_ready(n)) return any;
-        for (int i = 0; i < np; ++i) scores(i, n % Sh::kSlots);
-        t8_commit(smem_addr(&sh.slot_free[n % Sh::kSlots]));
-        if (tiles == 1) t8_commit(smem_addr(&sh.q_free));
-        for (int j = 0; j < tiles; ++j, n += 2) {
-            const bool next = j + 1 < tiles;
-            if (Sh::NS == 1 && next) {  // the next scores have a buffer of their own
-                if (!slot_ready(n + 2)) return any;
-                scores(0, (n + 2) % Sh::kSlots);
-                t8_commit(smem_addr(&sh.slot_free[(n + 2) % Sh::kSlots]));
-                if (j + 2 == tiles) t8_commit(smem_addr(&sh.q_free));
-            }
-            if (!slot_ready(n + 1)) return any;
-            for (int i = 0; i < np; ++i) {
-                if (!wait(sh.p_full[Sh::NS == 1 ? done[0] & 1 : i], static_cast<uint32_t>(Sh::NS == 1 ? done[0] >> 1 : done[i]) & 1u)) return any;
-                if (!sums(i, (n + 1) % Sh::kSlots, j > 0)) return any;
-                if (i + 1 == np) t8_commit(smem_addr(&sh.slot_free[(n + 1) % Sh::kSlots]));
-                // The weights lay where these scores go: MMAs of one thread run in the order of their issue.
-                if (Sh::NS == 2 && next) {
-                    if (i == 0 && !slot_ready(n + 2)) return any;
-                    scores(i, (n + 2) % Sh::kSlots);
-                    if (i + 1 == np) {
-                        t8_commit(smem_addr(&sh.slot_free[(n + 2) % Sh::kSlots]));
-                        if (j + 2 == tiles) t8_commit(smem_addr(&sh.q_free));
-                    }
-                }
-            }
+    ChunkUnit w;
+    for (int u = 0; ch_unit(sh, u, lane, w); ++u) {
+        // (Broadcasts: so the compiler knows these, and what is counted by them, to be one value a warp, and descriptors and
+        // addresses are made by the uniform units.)
+        const int two = __shfl_sync(0xFFFFFFFFu, w.flags & kChTwo, 0), tiles = __shfl_sync(0xFFFFFFFFu, w.tiles, 0);
+        if (tiles == 0 || !ok) continue;
+        if (!wait(sh.q_full[unit & 1], static_cast<uint32_t>(unit >> 1) & 1u)) continue;
+        if (i == 1 && !two) {
+            // No rows: each slot is given back once it has been filled.
+#pragma unroll 1
+            for (int j = 0; j < 2 * tiles && slot_ready(n); ++j, ++n)
+                if (lane == 0) mbar_arrive(smem_addr(&sh.slot_free[n % Sh::kSlots]));
+            if (lane == 0) mbar_arrive(smem_addr(&sh.q_free));
+            ++unit;
+            continue;
+        }
+        if (!slot_ready(n)) continue;
+        scores(n % Sh::kSlots, tiles == 1);
+#pragma unroll 1
+        for (int j = 0; ok && j < tiles; ++j, n += 2) {
+            const bool next = j + 1 < tiles, end = j + 2 == tiles;
+            // One product: the next scores have a buffer of their own.  (f32: the weights in it have been taken once their
+            // product is in the sums.)
+            if (Sh::NS == 1 && next && slot_ready(n + 2) &&
+                (!Sh::SUMS || products == 0 || wait(sh.product_free, static_cast<uint32_t>(products - 1) & 1u)))
+                scores((n + 2) % Sh::kSlots, end);
+            if (!slot_ready(n + 1)) break;
+            if (!wait(sh.p_full[Sh::NS == 1 ? done & 1 : i], static_cast<uint32_t>(Sh::NS == 1 ? done >> 1 : done) & 1u)) break;
+            sums((n + 1) % Sh::kSlots, j > 0);
+            if (Sh::NS == 2 && next && slot_ready(n + 2)) scores((n + 2) % Sh::kSlots, end);
         }
         ++unit;
-        do more = w.next();
-        while (more && w.none());
     }
     return any;
 }
@@ -692,12 +767,12 @@ struct ChunkRow {
     int64_t out, lse;
     int last;    // last position it sees
     bool valid;
-    template <typename Sh>
-    __device__ __forceinline__ ChunkRow(const ChunkArgs &a, const ChunkWalk<Sh> &w, int local) {
-        const int r = w.row0() + local, token = r / a.group;
-        const int64_t row = w.q.first + token, head = static_cast<int64_t>(w.head) * a.group + (r - token * a.group);
-        valid = r < w.q.rows * a.group;
-        last = valid ? w.q.len - w.q.rows + token : 0x7FFFFFFF;  // (rows that are not there: zeros, stored nowhere)
+    __device__ __forceinline__ ChunkRow(const ChunkArgs &a, const ChunkUnit &w, int local) {
+        int in_group;
+        const int r = w.row0 + local, token = ch_token(a, r, in_group);
+        const int64_t row = w.first + token, head = static_cast<int64_t>(w.head) * a.group + in_group;
+        valid = r < w.rows * a.group;
+        last = valid ? w.len - w.rows + token : 0x7FFFFFFF;  // (rows that are not there: zeros, stored nowhere)
         out = row * a.out_stride + head * a.head_dim;
         lse = row * (static_cast<int64_t>(a.kv_heads) * a.group) + head;
     }
@@ -705,13 +780,13 @@ struct ChunkRow {
 
 // Writes a unit's row out: its outputs, or its part of them.
 template <typename Sh, typename T>
-__device__ __forceinline__ void ch_finish(const ChunkArgs &a, const ChunkWalk<Sh> &w, ChunkShared &sh, int unit, const ChunkRow &row, int local,
+__device__ __forceinline__ void ch_finish(const ChunkArgs &a, const ChunkUnit &w, ChunkShared &sh, int unit, const ChunkRow &row, int local,
                                           uint32_t o_col, float M, float R, float l, bool ok) {
     const float nanf = __int_as_float(0x7FC00000);
     const int ub = unit & 1;
     // The converters' word on what is NaN.
-    ok = ok && at_warp_wait(smem_addr(&sh.values_done[ub]), static_cast<uint32_t>(unit >> 1) & 1u, &sh.abort, a.wait_limit_ns);
-    const bool whole = w.starts() && w.ends();
+    ok = ok && ch_wait(a, sh, sh.values_done[ub], static_cast<uint32_t>(unit >> 1) & 1u);
+    const bool starts = w.flags & kChStarts, whole = starts && (w.flags & kChEnds);
     const float up = R > kChNone ? R - static_cast<float>(kChLift) : 0.f;  // sums are 2^-up times what they stand for
     float f = 1.f;
     if (!ok) l = nanf;
@@ -719,7 +794,7 @@ __device__ __forceinline__ void ch_finish(const ChunkArgs &a, const ChunkWalk<Sh
         f = l == 0.f ? 0.f : 1.f / l;
         if (row.valid && a.lse) a.lse[row.lse] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
     }
-    float *part = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + w.starts()) * (static_cast<int64_t>(Sh::U) * (a.head_dim + 2));
+    float *part = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + starts) * (static_cast<int64_t>(Sh::U) * (a.head_dim + 2));
     if (!whole) {
         __stcg(part + static_cast<int64_t>(Sh::U) * a.head_dim + local, M);
         __stcg(part + static_cast<int64_t>(Sh::U) * (a.head_dim + 1) + local, l);
@@ -727,31 +802,29 @@ __device__ __forceinline__ void ch_finish(const ChunkArgs &a, const ChunkWalk<Sh
     T *out = static_cast<T *>(a.out) + row.out;
     const bool nans = ok && sh.any_nan[ub] != 0;
     // 2^up in two factors, since it may leave the range of one.
-    const float u1 = at_exp2(fminf(fmaxf(up, -120.f), 120.f)), u2 = at_exp2(fminf(fmaxf(up - fminf(fmaxf(up, -120.f), 120.f), -120.f), 120.f)) * f;
+    const float up1 = fminf(fmaxf(up, -120.f), 120.f);
+    const float u1 = at_exp2(up1), u2 = ok ? at_exp2(fminf(fmaxf(up - up1, -120.f), 120.f)) * f : nanf;
+    part += static_cast<int64_t>(local) * a.head_dim;
 #pragma unroll 1
     for (int c = 0; c < a.head_dim; c += 16) {
         float v[16];
-        if (ok) {
-            t8_ld16(o_col + c, v);
-            at_wait_ld();
-        }
+        t8_ld16(o_col + c, v);
+        at_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            v[x] = ok ? v[x] * u1 * u2 : nanf;
-            if (nans && sh.vnan[ub][c + x] <= row.last) v[x] = nanf;
+        for (int x = 0; x < 16; ++x) v[x] = v[x] * u1 * u2;
+        if (nans) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[x] = sh.vnan[ub][c + x] <= row.last ? nanf : v[x];
         }
         float lo[8], hi[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) lo[x] = v[x], hi[x] = v[8 + x];
-        if (whole) {
-            if (row.valid) {
-                rope_store8(out + c, lo);
-                rope_store8(out + c + 8, hi);
-            }
-        } else {
-            float *p = part + static_cast<int64_t>(local) * a.head_dim + c;
-            rope_store8(p, lo);
-            rope_store8(p + 8, hi);
+        if (!whole) {
+            rope_store8(part + c, lo);
+            rope_store8(part + c + 8, hi);
+        } else if (row.valid) {
+            rope_store8(out + c, lo);
+            rope_store8(out + c + 8, hi);
         }
     }
 }
@@ -807,21 +880,32 @@ __device__ __forceinline__ void ch_weights(const float *v, int col, int rel, flo
     }
 }
 
-// The scores of a tile in turn, 32 columns at a time, the next ones on their way.
-template <int T, typename F>
+// The scores of a tile in turn, 32 columns at a time.  LOOP: what is seldom needed
+// stays a loop, for the sake of the instruction caches (with every pass unrolled
+// and every role's walk its own, all roles ran three times slower).
+template <int T, bool LOOP, typename F>
 __device__ __forceinline__ void ch_columns(uint32_t s_col, F f) {
-    float v[2][32];
-    ch_ld32(s_col, v[0]);
+    if constexpr (LOOP) {
+#pragma unroll 1
+        for (int c = 0; c < T; c += 32) {
+            float v[32];
+            ch_ld32(s_col + c, v);
+            at_wait_ld();
+            f(c, v);
+        }
+    } else {
 #pragma unroll
-    for (int c = 0; c < T; c += 32) {
-        at_wait_ld();
-        if (c + 32 < T) ch_ld32(s_col + c + 32, v[(c / 32 + 1) & 1]);
-        f(c, v[(c / 32) & 1]);
+        for (int c = 0; c < T; c += 32) {
+            float v[32];
+            ch_ld32(s_col + c, v);
+            at_wait_ld();
+            f(c, v);
+        }
     }
 }
 
 template <typename Sh, typename T>
-__device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, ChunkShared &sh, uint32_t tmem, int product, int wq, int lane) {
+__device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, uint32_t tmem, int product, int wq, int lane) {
     constexpr int PL = Sh::PL, kTile = Sh::T;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t o_col = tmem + lanes + static_cast<uint32_t>(Sh::kSumCol + product * 128);
@@ -829,14 +913,17 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, 
     int it = 0, unit = 0;   // all tiles of the CTA; units with tiles
     int mine = 0;           // tiles of this product
     bool ok = true;
-    do {
+    ChunkUnit w;
+    for (int u = 0; ch_unit(sh, u, lane, w); ++u) {
         const ChunkRow row(a, w, local);
-        if (w.tiles == 0 && !Sh::SUMS) ch_nothing<T>(a, row);
-        if (w.none()) continue;
-        const int ub = unit & 1, tiles = w.j1 - w.j0;
+        const int ub = unit & 1, tiles = w.tiles;
+        if (tiles == 0) {
+            if (!Sh::SUMS) ch_nothing<T>(a, row);
+            continue;
+        }
         // (Also without rows: no product's report runs ahead of the unit.)
-        ok = ok && at_warp_wait(smem_addr(&sh.q_full[ub]), static_cast<uint32_t>(unit >> 1) & 1u, &sh.abort, a.wait_limit_ns);
-        if (product >= w.products()) {  // no rows
+        ok = ok && ch_wait(a, sh, sh.q_full[ub], static_cast<uint32_t>(unit >> 1) & 1u);
+        if (product == 1 && (w.flags & kChTwo) == 0) {  // no rows
             it += tiles;
             if (lane == 0) mbar_arrive(smem_addr(&sh.unit_done[ub]));
             ++unit;
@@ -847,40 +934,51 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, 
         for (int j = 0; ok && j < tiles; ++j, ++it, ++mine) {
             const int sb = Sh::NS == 1 ? mine & 1 : 0;
             const uint32_t s_col = tmem + lanes + static_cast<uint32_t>(Sh::NS == 1 ? sb * kTile : product * 128);
-            ok = at_warp_wait(smem_addr(&sh.s_full[Sh::NS == 1 ? sb : product]), static_cast<uint32_t>(Sh::NS == 1 ? mine >> 1 : mine) & 1u,
-                              &sh.abort, a.wait_limit_ns) &&
-                 at_warp_wait(smem_addr(&sh.info_full[it & (kChInfo - 1)]), static_cast<uint32_t>(it / kChInfo) & 1u, &sh.abort, a.wait_limit_ns);
-            if (!ok) break;
-            t8_fence_after();
+            ok = ch_wait(a, sh, sh.info_full[it & (kChInfo - 1)], static_cast<uint32_t>(it / kChInfo) & 1u);
             const float4 *info = sh.info[it & (kChInfo - 1)];
             const int64_t t0 = static_cast<int64_t>(w.j0 + j) * kTile;
             const int rel = t0 > row.last ? -1 : static_cast<int>(row.last - t0 < kTile ? row.last - t0 : kTile);  // last column this row sees
-            const bool masked = __any_sync(0xFFFFFFFFu, rel < kTile - 1);
-            // Maxima of sixteens, then the row's.
-            float top = M, m16[kTile / 16];
-            ch_columns<kTile>(s_col, [&](int c, float (&v)[32]) {
-                if (masked) {
+            const bool careful = __any_sync(0xFFFFFFFFu, rel < kTile - 1 || fabsf(M) >= 0x1p19f) || sh.info_minus[it & (kChInfo - 1)] != 0;
+            ok = ok && ch_wait(a, sh, sh.s_full[Sh::NS == 1 ? sb : product], static_cast<uint32_t>(Sh::NS == 1 ? mine >> 1 : mine) & 1u);
+            if (!ok) break;
+            t8_fence_after();
+            // The row's maximum, and the largest of the sixteens' maxima times their value scales, relative to the former.
+            // Both as whole powers of two.
+            float top = M, ref = kChNone;
+            if (!careful) {
+                float m16[kTile / 16];
+                ch_columns<kTile, false>(s_col, [&](int c, float (&v)[32]) {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) v[x] = c + x <= rel ? v[x] : -INFINITY;
+                    for (int g = 0; g < 2; ++g) m16[c / 16 + g] = ch_max16(v + 16 * g);
+                });
+#pragma unroll
+                for (int g = 0; g < kTile / 16; ++g) {
+                    m16[g] = ceilf(m16[g] * (info[g].x * qs));
+                    top = fmaxf(top, m16[g]);
                 }
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float m = v[16 * g];
+                for (int g = 0; g < kTile / 16; ++g) ref = fmaxf(ref, (m16[g] - top) + info[g].y);
+            } else {
+                ch_columns<kTile, true>(s_col, [&](int c, float (&v)[32]) {
 #pragma unroll
-                    for (int x = 1; x < 16; ++x) m = fmaxf(m, v[16 * g + x]);
-                    m = m == -INFINITY ? m : ceilf(m * (info[c / 16 + g].x * qs));
-                    top = fmaxf(top, m);
-                    m16[c / 16 + g] = m;
-                }
-            });
+                    for (int g = 0; g < 2; ++g) {
+                        const float4 f = info[c / 16 + g];
+                        const float k = f.x * qs;
+                        float m = -INFINITY;
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) m = c + 16 * g + x <= rel ? fmaxf(m, v[16 * g + x] * k) : m;
+                        m = m == -INFINITY ? m : ceilf(m);
+                        const float now = fmaxf(top, m);
+                        ref = fmaxf(now > top && ref > kChNone ? ref - (now - top) : ref, (m - now) + f.y);
+                        top = now;
+                    }
+                });
+            }
             if (top > M) {
                 l *= at_exp2(M - top);
                 R = R > kChNone ? R - (top - M) : R;
                 M = top;
             }
-            float ref = kChNone;
-#pragma unroll
-            for (int g = 0; g < kTile / 16; ++g) ref = fmaxf(ref, (m16[g] - M) + info[g].y);
             const bool move = ref > R + kChSlack;
             const float factor = move && R > kChNone ? at_exp2(R - ref) : 1.f;  // of the sums so far
             if (Sh::SUMS) {
@@ -888,7 +986,7 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.factor_full[it & (kChInfo - 1)]));
             } else if (j > 0 && __any_sync(0xFFFFFFFFu, move)) {
-                ok = at_warp_wait(smem_addr(&sh.o_done[product]), static_cast<uint32_t>(mine - 1) & 1u, &sh.abort, a.wait_limit_ns);
+                ok = ch_wait(a, sh, sh.o_done[product], static_cast<uint32_t>(mine - 1) & 1u);
                 if (!ok) break;
                 t8_fence_after();
 #pragma unroll 1
@@ -905,26 +1003,33 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, 
             }
             if (move) R = ref;
             const float base = M > kChNone ? M : 0.f, lift = R > kChNone ? static_cast<float>(kChLift) - R : 0.f;
-            auto weights = [&](auto careful) {
-                ch_columns<kTile>(s_col, [&](int c, float (&v)[32]) {
+            const uint32_t w_col = tmem + lanes + Sh::weights_col(Sh::NS == 1 ? sb : product, a.head_dim);
+            auto weights = [&](auto slow) {
+                ch_columns<kTile, decltype(slow)::value>(s_col, [&](int c, float (&v)[32]) {
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const float4 f = info[c / 16 + g];
-                        ch_weights<PL, decltype(careful)::value>(v + 16 * g, c + 16 * g, rel, f.x * qs, base, fmaxf(f.y + lift, kChMinLog), f.z, l,
-                                                                 hi + 8 * g, lo + 8 * g);
+                        ch_weights<PL, decltype(slow)::value>(v + 16 * g, c + 16 * g, rel, f.x * qs, base, fmaxf(f.y + lift, kChMinLog), f.z, l,
+                                                              hi + 8 * g, lo + 8 * g);
                     }
                     if (PL == 1) {
-                        ch_st16(s_col + c / 2, hi);
+                        ch_st16(w_col + c / 2, hi);
                     } else {
-                        ch_st16(s_col + c, hi);
-                        ch_st16(s_col + c + 16, lo);
+                        ch_st16(w_col + c, hi);
+                        ch_st16(w_col + c + 16, lo);
                     }
                 });
             };
-            if (masked || __any_sync(0xFFFFFFFFu, fabsf(base) >= 0x1p20f)) weights(std::true_type{});
+            if (careful || __any_sync(0xFFFFFFFFu, fabsf(base) >= 0x1p20f)) weights(std::true_type{});
             else weights(std::false_type{});
             ch_wait_st();
+            // With scores issued ahead, the sums of the tile before may still be under way: each phase is waited for, so that
+            // the last one cannot be taken for the one before it.
+            if (Sh::NS == 1 && !Sh::SUMS && j > 0) {
+                ok = ch_wait(a, sh, sh.o_done[0], static_cast<uint32_t>(mine - 1) & 1u);
+                if (!ok) break;
+            }
             t8_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[Sh::NS == 1 ? sb : product]));
@@ -936,7 +1041,7 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, 
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.last_full[ub]));
         } else {
-            ok = ok && at_warp_wait(smem_addr(&sh.o_done[product]), static_cast<uint32_t>(mine - 1) & 1u, &sh.abort, a.wait_limit_ns);
+            ok = ok && ch_wait(a, sh, sh.o_done[product], static_cast<uint32_t>(mine - 1) & 1u);
             t8_fence_after();
             ch_finish<Sh, T>(a, w, sh, unit, row, local, o_col, M, R, l, ok);
             t8_fence_before();
@@ -944,29 +1049,32 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkWalk<Sh> w, 
             if (lane == 0) mbar_arrive(smem_addr(&sh.unit_done[ub]));
         }
         ++unit;
-    } while (w.next());
+    }
 }
 
 // f32's sums: each tile's product, out of tensor memory, onto the sums there,
 // rounded; at a unit's end its rows are written out.
 template <typename Sh, typename T>
-__device__ __forceinline__ void ch_sums(const ChunkArgs &a, ChunkWalk<Sh> w, ChunkShared &sh, uint32_t tmem, int wq, int lane) {
+__device__ __forceinline__ void ch_sums(const ChunkArgs &a, ChunkShared &sh, uint32_t tmem, int wq, int lane) {
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t p_col = tmem + lanes + static_cast<uint32_t>(Sh::kProductCol), o_col = tmem + lanes + static_cast<uint32_t>(Sh::kSumCol);
     const int local = wq * 32 + lane;
     int it = 0, unit = 0, products = 0;
     bool ok = true;
-    do {
+    ChunkUnit w;
+    for (int u = 0; ch_unit(sh, u, lane, w); ++u) {
         const ChunkRow row(a, w, local);
-        if (w.tiles == 0) ch_nothing<T>(a, row);
-        if (w.none()) continue;
-        const int ub = unit & 1, tiles = w.j1 - w.j0;
+        const int ub = unit & 1, tiles = w.tiles;
+        if (tiles == 0) {
+            ch_nothing<T>(a, row);
+            continue;
+        }
         for (int j = 0; ok && j < tiles; ++j, ++it) {
-            ok = at_warp_wait(smem_addr(&sh.factor_full[it & (kChInfo - 1)]), static_cast<uint32_t>(it / kChInfo) & 1u, &sh.abort, a.wait_limit_ns);
+            ok = ch_wait(a, sh, sh.factor_full[it & (kChInfo - 1)], static_cast<uint32_t>(it / kChInfo) & 1u);
             const float factor = sh.factor[it & (kChInfo - 1)][local];
 #pragma unroll 1
             for (int h = 0; ok && h < Sh::kHalves; ++h, ++products) {
-                ok = at_warp_wait(smem_addr(&sh.o_done[0]), static_cast<uint32_t>(products) & 1u, &sh.abort, a.wait_limit_ns);
+                ok = ch_wait(a, sh, sh.o_done[0], static_cast<uint32_t>(products) & 1u);
                 if (!ok) break;
                 t8_fence_after();
                 const int c0 = 128 * h, c1 = min(a.head_dim, c0 + 128);
@@ -987,12 +1095,12 @@ __device__ __forceinline__ void ch_sums(const ChunkArgs &a, ChunkWalk<Sh> w, Chu
             }
         }
         ch_wait_st();
-        ok = ok && at_warp_wait(smem_addr(&sh.last_full[ub]), static_cast<uint32_t>(unit >> 1) & 1u, &sh.abort, a.wait_limit_ns);
+        ok = ok && ch_wait(a, sh, sh.last_full[ub], static_cast<uint32_t>(unit >> 1) & 1u);
         ch_finish<Sh, T>(a, w, sh, unit, row, local, o_col, sh.last[ub][0][local], sh.last[ub][1][local], sh.last[ub][2][local], ok);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.unit_done[ub]));
         ++unit;
-    } while (w.next());
+    }
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -1007,7 +1115,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
     if (tid == 0) {
         for (int i = 0; i < Sh::kSlots; ++i) {
             mbar_init(smem_addr(&sh.slot_full[i]), kChConvertWarps);
-            mbar_init(smem_addr(&sh.slot_free[i]), 1);
+            mbar_init(smem_addr(&sh.slot_free[i]), Sh::kIssuers);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.s_full[i]), 1);
@@ -1024,8 +1132,13 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
         mbar_init(smem_addr(&sh.last_full[0]), 4);
         mbar_init(smem_addr(&sh.last_full[1]), 4);
         mbar_init(smem_addr(&sh.product_free), 4);
-        mbar_init(smem_addr(&sh.q_free), 1);
-        mbar_init(smem_addr(&sh.mma_done), 1);
+        for (int i = 0; i < kChUnits; ++i) {
+            mbar_init(smem_addr(&sh.unit_full[i]), 1);
+            mbar_init(smem_addr(&sh.unit_free[i]), (Sh::NS == 2 || Sh::SUMS ? 8 : 4) + kChConvertWarps + Sh::kIssuers);  // every warp that takes units
+        }
+        mbar_init(smem_addr(&sh.q_free), Sh::kIssuers);
+        mbar_init(smem_addr(&sh.mma_done[0]), 1);
+        mbar_init(smem_addr(&sh.mma_done[1]), 1);
         mbar_init_fence();
         sh.abort = 0;
     }
@@ -1041,100 +1154,94 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
     grid_launch_dependents();
 
     // ---- the list, scanned by every CTA: thread i sums requests [i each, (i + 1) each).
-    int64_t total = 0;
-    int grid = 0;
+    bool busy;
     {
+        const ChunkList<Sh> list{a};
         const int each = (a.n_seqs + kChThreads - 1) / kChThreads;
         const int r0 = min(tid * each, a.n_seqs), r1 = min(r0 + each, a.n_seqs);
-        int64_t sum = 0;
+        int sum = 0;
         bool bad = false;
+#pragma unroll 1
         for (int s = r0; s < r1; ++s) {
-            const ChunkSeq q = ch_seq<Sh>(a, s);
-            sum += q.entries();
+            const ChunkSeq q = list.seq(s);
+            sum += list.entries(q);
             bad |= q.bad;
         }
         if (bad && blockIdx.x == 0) atomicOr(a.status, 4u);
-        int64_t pre = sum;
+        int pre = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, pre, d);
+            const int u = __shfl_up_sync(0xFFFFFFFFu, pre, d);
             if (lane >= d) pre += u;
         }
         if (lane == 31) sh.scan[warp] = pre;
         __syncthreads();
-        int64_t base = 0;
-        for (int i = 0; i < kChThreads / 32; ++i) {
-            const int64_t u = sh.scan[i];
-            if (i < warp) base += u;
-            total += u;
-        }
+        const int part = sh.scan[min(lane, kChThreads / 32 - 1)];  // each warp's sum, in the lanes of its number
+        const int total = __reduce_add_sync(0xFFFFFFFFu, lane < kChThreads / 32 ? part : 0);
+        const int from = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? part : 0) + pre - sum;
         // Every CTA's share is a few entries, so no two cuts inside a unit meet.
-        grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(total / 8, min(total, int64_t(1)))));
-        const int64_t from = base + pre - sum;
-        if (static_cast<int>(blockIdx.x) < grid) {
+        const int grid = min(static_cast<int>(gridDim.x), max(total / 8, min(total, 1)));
+        busy = static_cast<int>(blockIdx.x) < grid;
+        if (busy) {
+            const AttnSplit split(total, grid);
+#pragma unroll 1
             for (int e = 0; e < 2; ++e) {
-                const int64_t share = total / grid, rest = total - share * grid, b = blockIdx.x + e;
-                const int64_t x = b * share + min(b, rest);
-                if (e == 1 && x == total) {
-                    if (tid == 0) sh.cut[1] = total;
+                const int x = split.begin(blockIdx.x + e);
+                if (x == total) {
+                    if (tid == 0) sh.cut[e] = total;
                 } else if (from <= x && x < from + sum) {
-                    int64_t here = from;
-                    int s = r0;
-                    ChunkSeq q = ch_seq<Sh>(a, s);
-                    while (x >= here + q.entries()) {
-                        here += q.entries();
-                        q = ch_seq<Sh>(a, ++s);
+                    int here = from, s = r0;
+                    ChunkSeq q = list.seq(s);
+#pragma unroll 1
+                    for (int n = list.entries(q); x >= here + n; n = list.entries(q)) {
+                        here += n;
+                        q = list.seq(++s);
                     }
-                    const ChunkPlace p = ch_place(q, x - here, [](const ChunkSeq &q, int64_t x) {
-                        int lo = 0, hi = q.row_tiles - 1;
-                        while (lo < hi) {
-                            const int mid = (lo + hi + 1) >> 1;
-                            if (q.before(mid) <= x) lo = mid;
-                            else hi = mid - 1;
-                        }
-                        return lo;
-                    });
-                    sh.cut[e] = here + p.at;
+                    int lo = 0, hi = q.row_tiles - 1;  // the row tile: the last one whose entries begin at or below x
+#pragma unroll 1
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (list.before(q, mid) <= x - here) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    here += list.before(q, lo);
+                    const int weight = list.weight(q, lo), slots = list.seen(q, lo) + 1;
+                    const int head = (x - here) / (weight * slots);
+                    int slot = ((x - here) - head * weight * slots) / weight;
+                    if (slot <= kChSmallCut) slot = 0;
+                    sh.cut[e] = here + (head * slots + slot) * weight;
                     if (e == 0) {
                         sh.at[0] = s;
-                        sh.at[1] = p.row_tile;
-                        sh.at[2] = p.head;
-                        sh.at[3] = p.slot;
+                        sh.at[1] = lo;
+                        sh.at[2] = head;
+                        sh.at[3] = slot;
                     }
                 }
             }
         }
         __syncthreads();
+        busy = busy && sh.cut[0] < sh.cut[1];
     }
-    const bool busy = static_cast<int>(blockIdx.x) < grid && sh.cut[0] < sh.cut[1];
-    bool issued = false;
     if (busy) {
-        ChunkWalk<Sh> w(a, sh.at, sh.cut[1] - sh.cut[0]);
         if (warp < kChConvertWarp) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChSoftmaxRegs));
-            if (warp < 4 * Sh::NS) ch_softmax<Sh, T>(a, w, sh, tmem, warp >> 2, warp & 3, lane);
-            else if (Sh::SUMS) ch_sums<Sh, T>(a, w, sh, tmem, warp & 3, lane);
+            if (warp < 4 * Sh::NS) ch_softmax<Sh, T>(a, sh, tmem, warp >> 2, warp & 3, lane);
+            else if (Sh::SUMS) ch_sums<Sh, T>(a, sh, tmem, warp & 3, lane);
         } else if (warp < kChMmaWarp) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChConvertRegs));
-            ch_convert<Sh, T>(a, w, sh, sq, slots, tid - kChConvertWarp * 32);
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChConvertRegs));
+            ch_convert<Sh, T>(a, sh, sq, slots, tid - kChConvertWarp * 32);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChIssueRegs));
-            if (warp != kChMmaWarp) {
-            } else if (lane == 0) {
-                issued = ch_issue<Sh>(a, w, sh, tmem, smem_addr(sq), smem_addr(slots));
-                if (issued) {  // also after a wait that ran out: nothing is in flight at the end
-                    t8_commit(smem_addr(&sh.mma_done));
-                    (void)mbar_wait_bounded(smem_addr(&sh.mma_done), 0);
+            if (warp < kChMmaWarp + Sh::kIssuers) {
+                // Also after a wait that ran out: nothing is in flight at the end.
+                const int i = warp - kChMmaWarp;
+                if (ch_issue<Sh>(a, sh, tmem, smem_addr(sq), smem_addr(slots), i, lane)) {
+                    if (ch_elect()) t8_commit(smem_addr(&sh.mma_done[i]));
+                    __syncwarp();
+                    (void)mbar_wait_bounded(smem_addr(&sh.mma_done[i]), 0);
                 }
-            } else if (lane == 1) {
-                // What the join needs: the last unit, and which ends of the range are cuts.
-                const bool first_cut = !w.starts();
-                bool alone = true;
-                while (w.next()) alone = false;
-                const bool last_cut = !w.ends();
-                a.heads[2 * blockIdx.x] = make_int4(w.s, w.row_tile, w.head,
-                                                    (last_cut && (w.starts() || !alone) ? 1 : 0) | (alone && first_cut && last_cut ? 2 : 0));
-                a.heads[2 * blockIdx.x + 1] = make_int4(w.q.first, w.q.rows, 0, 0);
+            } else if (warp == kChPlanWarp && lane == 0) {
+                ch_plan<Sh>(a, sh);
             }
         }
     } else if (tid == 0) {
@@ -1187,8 +1294,9 @@ __global__ void __launch_bounds__(kChJoinRows * 32) kv_chunk_join_kernel(const C
     nan = __any_sync(0xFFFFFFFFu, nan);
     if (nan) l = __int_as_float(0x7FC00000);
     __syncwarp();
-    const int token = r / a.group;
-    const int64_t row = rows.x + token, head = static_cast<int64_t>(h.z) * a.group + (r - token * a.group);
+    int in_group;
+    const int token = ch_token(a, r, in_group);
+    const int64_t row = rows.x + token, head = static_cast<int64_t>(h.z) * a.group + in_group;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     if (lane == 0 && a.lse) a.lse[row * (static_cast<int64_t>(a.kv_heads) * a.group) + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
     T *out = static_cast<T *>(a.out) + row * a.out_stride + head * a.head_dim;

@@ -310,6 +310,22 @@ def test_same_result_every_time_captured_and_on_two_streams(ops):
     assert torch.equal(out[:320], ops.fp8blk_kv_attn_chunk(qa, *da, a.scale, wa)[:320])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lens,rows,heads,kv,dim,block", [([300], [40], 8, 8, 256, 128), ([129, 500], [70, 90], 10, 2, 192, 128),
+                                                          ([513, 40, 900], [100, 3, 250], 15, 3, 80, 16), ([40] * 200, [8] * 200, 2, 1, 32, 16)])
+def test_a_hundred_calls_in_a_row(ops, lens, rows, heads, kv, dim, block, dtype):
+    """The same bits from calls back to back, with warm and with cold caches."""
+    c = Case(lens, rows, heads, kv, dim, block, seed=20)
+    dev, q = c.dev(), to_dev(c.q).to(dtype)
+    ws, junk = ops.kv_attn_chunk_workspace(heads, kv, dim, DEV), torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    outs = []
+    for i in range(100):
+        if i % 3 == 0:
+            junk.fill_(i)
+        outs.append(ops.fp8blk_kv_attn_chunk(q, *dev, c.scale, ws))
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
 def test_offsets_past_32_bits(ops):
     """A pool of more than 2^32 bytes, its last blocks in use."""
     kv, block, dim, blocks = 8, 128, 256, 16500
