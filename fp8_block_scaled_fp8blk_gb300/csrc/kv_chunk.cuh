@@ -3,7 +3,7 @@
 // cores.
 //
 // For one request and cache head, a tile of 128 query rows (row = new token x
-// query head of the group) against a tile of T tokens:
+// query head of the group) against a tile of 64 tokens:
 //   S[r][t] = sum_d q[r][d] k[t][d]                    (first MMA, kind::f16)
 //   a = S s_k(t) c_r,   w = 2^(a + e_t + K - R_r)      (e_t: exponent of s_v(t))
 //   O[r][d] += sum_t w[r][t] v[t][d]                   (second MMA, w out of tensor memory)
@@ -35,18 +35,22 @@
 //
 // Work: all (request, row tile, cache head, token tile) quadruples in one list,
 // cut into one contiguous range per CTA, so ragged and causal lengths balance.
-// Row tiles are 256 rows (two products' rows, whose softmax and MMAs take turns)
-// for bf16 with head_dim <= 128, else 128 (scores of the next tile beside the
-// softmax of this one).  A unit (request, row tile, head) that lies across CTAs
-// leaves partial sums in the workspace, which a second kernel joins, in CTA order
-// (deterministic, no counters).
+// Row tiles are 256 rows (two products' rows) for bf16 with head_dim <= 128, else
+// 128.  A unit (request, row tile, head) that lies across CTAs leaves partial sums
+// in the workspace, which a second kernel joins, in CTA order (deterministic, no
+// counters).
+//
+// Each product has two score buffers: the next tile's scores are there when a
+// tile's softmax ends, and its sums and the scores after the next run beside the
+// next softmax.  (With tiles of 128 tokens and one buffer each product waited for
+// its own two MMAs: 6400 cycles a pair of tiles, 2600 of them softmax.)
 //
 // Roles (640 threads, one CTA per SM): warps 0-3 softmax (TMEM lane = row), warps
 // 4-7 softmax of the unit's second 128 rows, or f32's sums, warps 8-15 convert q, K
 // and V, warps 16 and 17 issue the MMAs (of the first and second 128 rows), warp 18
-// walks the list and lays out the units to come.  Every wait is bounded; a timeout raises a
-// CTA-wide flag, the outputs and lse of the CTA's rows become NaN, MMAs in flight
-// are waited for, and the status word records it.
+// walks the list and lays out the units to come.  Every wait is bounded; a timeout
+// raises a CTA-wide flag, the outputs and lse of the CTA's rows become NaN, MMAs in
+// flight are waited for, and the status word records it.
 #pragma once
 
 #include "kv_attn.cuh"
@@ -59,7 +63,7 @@ namespace fp8blk {
 constexpr int kChThreads = 640;
 constexpr int kChConvertWarp = 8, kChConvertWarps = 8, kChMmaWarp = 16, kChPlanWarp = 18;
 constexpr int kChMaxGrid = 160;          // bound on CTAs: partial sums in the workspace
-constexpr int kChInfo = 4;               // tiles whose scales (and sums' factors) are held
+constexpr int kChInfo = 8;               // tiles whose scales (and sums' factors) are held: more than K is ahead of the softmax
 constexpr int kChUnits = 4;              // units that are laid out ahead
 // Registers a thread of each role (of the 96 of the launch).
 constexpr int kChSoftmaxRegs = 112, kChConvertRegs = 104, kChIssueRegs = 48;
@@ -98,28 +102,24 @@ struct ChunkShape {
     static constexpr bool SUMS = PL == 2;               // products of a tile are added to the sums outside the tensor cores
     static constexpr int NS = WIDE || SUMS ? 1 : 2;     // 128-row products of a unit
     static constexpr int U = NS * 128;                  // rows of a unit
-    static constexpr int T = WIDE ? 64 : 128;           // tokens of a tile
+    static constexpr int T = 64;                        // tokens of a tile
+    static constexpr int TL = U / 2, kPer = TL / T;     // tokens of a tile of the list, tiles of those
     static constexpr int kBlocks = WIDE ? 4 : 2;        // 64-wide column blocks of a head
-    static constexpr int kSlot = T * kBlocks * 128;     // K or V of a tile as f16: 32 KiB
-    static constexpr int kSlots = PL == 2 && WIDE ? 2 : 4;
+    static constexpr int kSlot = T * kBlocks * 128;     // K or V of a tile as f16: 16 or 32 KiB
+    static constexpr int kSlots = WIDE ? 1 : 3;         // of K, and as many of V
+    static constexpr int kRaw = kSlot / 2;              // ... of the codes as they are: copied ahead
+    static constexpr int kRaws = !WIDE ? 6 : PL == 1 ? 4 : 1;  // of K and V in turn
+    static constexpr int kEach = kSlot / (32 * 256);    // groups of sixteen codes of a converting thread
     static constexpr int kQPlane = 128 * kBlocks * 128;  // one plane of 128 rows
     static constexpr int kQ = NS * PL * kQPlane;
-    static constexpr size_t kSmem = 1024 + kQ + kSlots * kSlot;
+    static constexpr size_t kSmem = 1024 + kQ + 2 * kSlots * kSlot + kRaws * kRaw;
     static constexpr int kGranules = T / 16;            // scales of a tile
-    // Tensor memory, in columns: scores (and the weights, in their place; two buffers of one product, or one of each of
-    // two), f32's product of a tile (half of a wide head at a time), the sums.
-    static constexpr int kProductCol = WIDE ? 128 : 256;
-    static constexpr int kSumCol = SUMS && !WIDE ? 384 : 256;
+    // Tensor memory, in columns: scores (and the weights, in their place), two buffers of a product; f32's product of a
+    // tile (half of a wide head at a time); the sums.
+    static constexpr int kProductCol = 128, kSumCol = 256;
     static constexpr int kHalves = SUMS && WIDE ? 2 : 1;
     static constexpr int kIssuers = NS;                 // warps that issue MMAs, one a product
-    // The weights of buffer (or product) b.  The next scores' MMAs are issued right behind those that read the weights, and
-    // only MMAs of one shape are sure to run in their order.  So the weights take the scores' place only where both have 128
-    // columns (sums of 64 < head_dim <= 128 have them all, whatever lies past head_dim), or where the issuer waits in
-    // between (f32); otherwise they have columns of their own.
-    __device__ static uint32_t weights_col(int b, int head_dim) {
-        return SUMS ? b * T : WIDE ? 128 + b * (T / 2) : head_dim <= 64 ? kSumCol + b * 128 + 64 : b * 128;
-    }
-    __device__ static int sum_cols(int head_dim) { return SUMS || WIDE || head_dim <= 64 ? head_dim : 128; }
+    static_assert(NS * 2 * T <= 256, "tensor memory");
 };
 
 // One unit's tiles in a CTA's range.
@@ -134,12 +134,12 @@ constexpr int kChStarts = 1, kChEnds = 2, kChTwo = 4, kChStop = 8;  // first and
 struct ChunkShared {
     // Whoever waits on a barrier is never a whole turn of it behind: a wait could not tell the next phase but one from
     // its own.  So what a role may skip or be late for goes by the unit's or the score buffer's parity.
-    uint64_t slot_full[4], slot_free[4], s_full[2], p_full[2], o_done[2], info_full[kChInfo];
+    uint64_t k_full[4], k_free[4], v_full[4], v_free[4], s_full[4], p_full[4], o_done[2], info_full[kChInfo];
     uint64_t q_full[2], values_done[2], unit_done[2], q_free, mma_done[2];
     uint64_t factor_full[kChInfo], last_full[2], product_free;  // f32's sums
     uint64_t unit_full[kChUnits], unit_free[kChUnits];
-    float4 info[kChInfo][8];     // per sixteen tokens: k scale (NaN if not finite), exponent of the v scale, its signed mantissa
-    int info_minus[kChInfo];     // whether a k scale of the tile is negative
+    float4 info[kChInfo][4];     // per sixteen tokens: k scale (NaN if not finite), exponent of the v scale, its signed mantissa
+    int info_odd[kChInfo];       // whether a k scale of the tile is negative, or a v scale no (positive) power of two
     ChunkUnit units[kChUnits];
     float qs[2][256];            // per row: what a score is times |s_k| of
     float factor[kChInfo][128];  // f32: what the sums so far are times, per row of a tile
@@ -155,31 +155,27 @@ struct ChunkShared {
 
 // ------------------------------------------------------------------ the list
 // (Entries are counted in 32 bits: the host sees to it.)
-// sum of floor((a + step i) / g) over i < n, step 1 or 2.  The floors of all
-// integers from a to a + n add up in closed form.  For every other one of a to
-// a + 2 n: of two neighbours x, x + 1 the second's floor is one more only where g
-// divides x + 1, and those are counted.
+// sum of floor((a + 2 i) / g) over i < n.  The floors of all integers from a to
+// a + 2 n add up in closed form; of two neighbours x, x + 1 the second's is one more
+// only where g divides x + 1, and those are counted.
 __device__ __forceinline__ int64_t ch_floors_below(uint32_t x, uint32_t g) {
     const uint32_t q = x / g, r = x - q * g;
     return static_cast<int64_t>(g) * (static_cast<int64_t>(q) * (static_cast<int64_t>(q) - 1) / 2) + static_cast<int64_t>(q) * r;
 }
-__device__ __noinline__ int ch_floor_sum(uint32_t a, uint32_t g, uint32_t n, int step) {
+__device__ __noinline__ int ch_floor_sum(uint32_t a, uint32_t g, uint32_t n) {
     if (n == 0) return 0;
-    const uint32_t hi = a + step * n;
+    const uint32_t hi = a + 2 * n;
     int64_t all = ch_floors_below(hi, g) - ch_floors_below(a, g);
-    if (step == 2) {
-        // Multiples of g among a + 1, a + 3, .., hi - 1: of even g all in between, of odd g every other one.
-        const bool odd = g & 1u;
-        const uint32_t m = odd ? 2 * g : g, shift = odd && a % 2 == 0 ? g : 0;
-        if (odd || a % 2 == 1) all -= (hi - 1 + shift) / m - (a + shift) / m;
-        all /= 2;
-    }
-    return static_cast<int>(all);
+    // Multiples of g among a + 1, a + 3, .., hi - 1: of even g all in between, of odd g every other one.
+    const bool odd = g & 1u;
+    const uint32_t m = odd ? 2 * g : g, shift = odd && a % 2 == 0 ? g : 0;
+    if (odd || a % 2 == 1) all -= (hi - 1 + shift) / m - (a + shift) / m;
+    return static_cast<int>(all / 2);
 }
 
-// One request as the kernel takes it.  Row tile i's last row sees the tiles
-// 0 .. floor((a + step i) / g), as far as there are any; a row tile's rows are
-// step tiles' tokens.
+// One request as the kernel takes it.  Tiles of the list are half as many tokens
+// as a row tile has rows, so row tile i's last row sees the tiles
+// 0 .. floor((a + 2 i) / g), as far as there are any.
 struct ChunkSeq {
     int first, rows, len;  // rows 0: nothing to do
     int tiles;             // of the whole cache
@@ -189,7 +185,7 @@ struct ChunkSeq {
 };
 template <typename Sh>
 struct ChunkList {
-    static constexpr int kStep = Sh::U / Sh::T, kFull = Sh::U / 128;  // kFull: list entries of a tile of a full row tile
+    static constexpr int kFull = Sh::U / 128;  // list entries of a tile of a full row tile
     const ChunkArgs &a;
     __device__ __noinline__ ChunkSeq seq(int s) const {
         ChunkSeq q;
@@ -200,22 +196,22 @@ struct ChunkList {
         q.bad = off || len < 0;
         q.rows = off ? 0 : static_cast<int>(rows);
         q.len = max(len, 0);
-        q.tiles = min(q.len / Sh::T + (q.len % Sh::T != 0), a.max_tiles);
+        q.tiles = min(q.len / Sh::TL + (q.len % Sh::TL != 0), a.max_tiles);
         const int flat = q.rows * a.group;
         q.row_tiles = flat / Sh::U + (flat % Sh::U != 0);
         // The first row's position, no further than the table's end (all tiles are seen from there on).
-        const int p = min(max(q.len - q.rows, 0), a.max_tiles * Sh::T);
-        q.a = static_cast<int>((static_cast<int64_t>(p) * a.group + Sh::U - 1) / Sh::T);
+        const int p = min(max(q.len - q.rows, 0), a.max_tiles * Sh::TL);
+        q.a = static_cast<int>((static_cast<int64_t>(p) * a.group + Sh::U - 1) / Sh::TL);
         q.last = flat - (q.row_tiles - 1) * Sh::U > 128 ? kFull : 1;
         return q;
     }
-    __device__ __forceinline__ int seen(const ChunkSeq &q, int i) const { return min((q.a + kStep * i) / a.group + 1, q.tiles); }
+    __device__ __forceinline__ int seen(const ChunkSeq &q, int i) const { return min((q.a + 2 * i) / a.group + 1, q.tiles); }
     __device__ __forceinline__ int weight(const ChunkSeq &q, int i) const { return i + 1 == q.row_tiles ? q.last : kFull; }
     // Entries of the row tiles below i, i < row_tiles: each unit has one slot for its set-up and one per tile.
     __device__ __noinline__ int before(const ChunkSeq &q, int i) const {
-        const int64_t lack = static_cast<int64_t>(q.tiles - 1) * a.group - q.a;  // from row tile ceil(lack / step) on all tiles are seen
-        const int some = lack <= 0 ? 0 : static_cast<int>(min((lack + kStep - 1) / kStep, static_cast<int64_t>(i)));
-        const int slots = ch_floor_sum(q.a, a.group, some, kStep) + some + (i - some) * q.tiles + i;
+        const int64_t lack = static_cast<int64_t>(q.tiles - 1) * a.group - q.a;  // from row tile ceil(lack / 2) on all tiles are seen
+        const int some = lack <= 0 ? 0 : static_cast<int>(min((lack + 1) / 2, static_cast<int64_t>(i)));
+        const int slots = ch_floor_sum(q.a, a.group, some) + some + (i - some) * q.tiles + i;
         return slots * kFull * a.kv_heads;
     }
     __device__ __forceinline__ int entries(const ChunkSeq &q) const {
@@ -255,8 +251,9 @@ __device__ __forceinline__ void ch_plan(const ChunkArgs &a, ChunkShared &sh) {
         x.s = s;
         x.row0 = row_tile * Sh::U;
         x.head = head;
-        x.j0 = max(e0 - 1, 0);
-        x.tiles = e1 - 1 - x.j0;
+        // (In tiles of the kernel; the list's last one may lie past the request's end with its second half.)
+        x.j0 = max(e0 - 1, 0) * Sh::kPer;
+        x.tiles = min((e1 - 1) * Sh::kPer, q.len / Sh::T + (q.len % Sh::T != 0)) - x.j0;
         x.flags = (e0 == 0 ? kChStarts : 0) | (e1 == tiles + 1 ? kChEnds : 0) | (weight == 2 ? kChTwo : 0);
         mbar_arrive(smem_addr(&sh.unit_full[slot]));
         if (left <= 0) {
@@ -472,14 +469,16 @@ __device__ __forceinline__ void ch_queries(const ChunkArgs &a, const ChunkUnit &
 }
 
 // ------------------------------------------------------------------ converters
-__device__ uint4 g_chunk_zeros;  // what tokens that are not there have for codes
-
-// Warps 8-15: q of each unit, then K and V of its tiles.  A thread has up to
-// four groups of sixteen codes of a tile; the next tile's codes are on their way
-// while this one's are converted, their block ids a tile earlier.
+// Warps 8-15: q of each unit, then K and V of its tiles.  A thread has two groups
+// of sixteen codes of a tile (four of a wide head): it copies them to shared memory
+// several tiles ahead, and converts them there when they have come.  (Asynchronous
+// copies, because the barriers' releases wait for loads under way: with the codes
+// ahead in registers a tile cost 6000 cycles.)  Block ids and scales come eight
+// tiles at a time, a lane for each sixteen tokens, one and two such windows ahead.
 template <typename Sh, typename T>
-__device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, uint8_t *sq, uint8_t *slots, int tid) {
-    constexpr int kEach = 4, kThreads = kChConvertWarps * 32;
+__device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, uint8_t *sq, uint8_t *k_slots, uint8_t *v_slots, uint8_t *raw,
+                                           int tid) {
+    constexpr int kEach = Sh::kEach, kThreads = kChConvertWarps * 32, kSlots = Sh::kSlots, G = Sh::kGranules, kWindow = 32 / G;
     const int warp = tid >> 5, lane = tid & 31, per = a.head_dim / 16, total = Sh::T * per, block = 1 << a.block_log2;
     int token[kEach], from[kEach];  // of the thread's groups: token of a tile (T: none), place in the block of its first tile
     uint32_t dst[kEach];
@@ -495,46 +494,62 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
         dst[i] = group(i, token[i], c);
         from[i] = (token[i] & (block - 1)) * a.head_dim + 16 * c;
     }
+    const uint8_t *mine = raw + tid * 16;  // the thread's groups of a raw slot lie 16 x threads apart
     const int64_t id_bytes = static_cast<int64_t>(a.kv_heads) * block * a.head_dim;
     const uint32_t n_blocks = static_cast<uint32_t>(a.n_blocks);
-    int n = 0, it = 0, unit = 0;  // slots filled so far, tiles, units with tiles
+    int nt = 0, unit = 0;  // tiles so far; units with tiles
     bool ok = true;
     ChunkUnit w;
     for (int u = 0; ch_unit(sh, u, lane, w); ++u) {
         if (w.tiles == 0 || !ok) continue;
         const int ub = unit & 1, j1 = w.j0 + w.tiles;
         const int32_t *row = a.table + static_cast<int64_t>(w.s) * a.width;
-        const uint8_t *k_codes = a.k_codes + static_cast<int64_t>(w.head) * block * a.head_dim, *v_codes = a.v_codes + (k_codes - a.k_codes);
-        // Tiles below this have all their tokens, and the table has their blocks.
-        const int full = min(min(w.len, static_cast<int>(min(static_cast<int64_t>(a.width) << a.block_log2, static_cast<int64_t>(0x7FFFFFFF)))) / Sh::T, j1);
-        // The block of a token of a tile: its id (maybe one outside the pool), -1 where the table ends before it, -2 past the
-        // request's end.
-        auto id_of = [&](int j, int tok) {
-            const int t = j * Sh::T + tok;
-            if (j < full) return row[t >> a.block_log2];
-            if (j >= j1 || static_cast<int64_t>(j) * Sh::T + tok >= w.len) return -2;
-            return (t >> a.block_log2) < a.width ? row[t >> a.block_log2] : -1;
+        const int64_t head = static_cast<int64_t>(w.head) * block * a.head_dim;
+        // Lane: tile lane / G of the window from tile j on, its sixteen tokens lane % G.  The block's id (maybe one outside the
+        // pool), -1 where the table ends before it, -2 past the request's end.
+        auto window = [&](int j) {
+            const int64_t t = static_cast<int64_t>(j + lane / G) * Sh::T + 16 * (lane % G);
+            const int64_t page = t >> a.block_log2;
+            return j + lane / G >= j1 || t >= w.len ? -2 : page < a.width ? row[page] : -1;
         };
-        auto ids = [&](int j, int (&id)[kEach]) {
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) id[i] = token[i] < Sh::T ? id_of(j, token[i]) : -2;
+        // The scales of the block in hand.  One that is not finite, and one of a block outside the pool, counts as NaN.
+        auto scales = [&](int b, float &k1, float &v1) {
+            k1 = v1 = 1.f;
+            if (b == -2) return;
+            const bool there = static_cast<uint32_t>(b) < n_blocks;
+            const int64_t bh = static_cast<int64_t>(b) * a.kv_heads + w.head;
+            k1 = there ? a.k_scales[bh] : INFINITY;
+            v1 = there ? a.v_scales[bh] : INFINITY;
+            if (!there) atomicOr(a.status, 4u);
         };
-        auto fetch = [&](int j, const int (&id)[kEach], const uint8_t *codes, uint4 (&x)[kEach]) {
-            // A block of more tokens than a tile: its tiles in turn.
-            const int more = block > Sh::T ? (j * Sh::T & (block - 1)) * a.head_dim : 0;
+        int id0 = window(w.j0), id1 = window(w.j0 + kWindow), id2 = 0, first = w.j0;  // windows from tile `first` on
+        float k0 = 1.f, v0 = 1.f, k1 = 1.f, v1 = 1.f;
+        // Copies of slot n of the unit (K and V of its tiles in turn), into the raw slot n % kRaws.
+        auto copy = [&](int n) {
+            const int j = w.j0 + (n >> 1), at = (j - first) * G;
+            const uint8_t *codes = n & 1 ? a.v_codes : a.k_codes;
+            const int64_t more = head + (j * Sh::T & (block - 1)) * a.head_dim;  // (a block of 128 tokens is two tiles)
+            const uint32_t to = smem_addr(mine) + (n % Sh::kRaws) * Sh::kRaw;
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                const uint4 *p = reinterpret_cast<const uint4 *>(codes + id[i] * id_bytes + (from[i] + more));
-                // (Plain loads: the kernel before this one may have written the cache after this one had begun.)
-                x[i] = *(static_cast<uint32_t>(id[i]) < n_blocks ? p : &g_chunk_zeros);
+                const int lane_of = at + (token[i] >> 4);
+                const int a0 = __shfl_sync(0xFFFFFFFFu, id0, lane_of & 31), a1 = __shfl_sync(0xFFFFFFFFu, id1, lane_of & 31);
+                const int id = lane_of < 32 ? a0 : a1;
+                const bool there = static_cast<uint32_t>(id) < n_blocks && j < j1 && static_cast<int64_t>(j) * Sh::T + token[i] < w.len;
+                const uint8_t *p = there ? codes + id * id_bytes + (from[i] + more) : codes;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * kThreads * 16), "l"(p), "r"(there ? 16 : 0) : "memory");
             }
         };
-        int id[kEach];
-        uint4 kx[kEach], vx[kEach];
-        ids(w.j0, id);
-        fetch(w.j0, id, k_codes, kx);
-        fetch(w.j0, id, v_codes, vx);
-        ids(w.j0 + 1, id);
+#pragma unroll 1
+        for (int n = 0; n < Sh::kRaws; ++n) {
+            copy(n);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        if (warp == 0) {
+            scales(id0, k0, v0);
+            scales(id1, k1, v1);
+        }
+        id2 = window(w.j0 + 2 * kWindow);
         // The unit's queries, once the MMAs have read the last one's, and the softmax has written out the one before that.
         ok = (unit < 1 || ch_wait(a, sh, sh.q_free, static_cast<uint32_t>(unit - 1) & 1u)) &&
              (unit < 2 || ch_wait(a, sh, sh.unit_done[ub], static_cast<uint32_t>((unit >> 1) - 1) & 1u));
@@ -543,87 +558,86 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
         asm volatile("bar.sync 4, %0;" ::"n"(kThreads) : "memory");
         if (!ok) continue;
         ch_queries<Sh, T>(a, w, sq, sh.qs[ub], warp, lane);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[ub]));
-        // One slot: groups of codes as f16 into shared memory.
-        auto slot_begin = [&]() {
-            ok = n < Sh::kSlots || ch_wait(a, sh, sh.slot_free[n % Sh::kSlots], (static_cast<uint32_t>(n / Sh::kSlots) & 1u) ^ 1u);
-            return ok;
-        };
-        auto slot_end = [&]() {
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // generic stores -> the MMA
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.slot_full[n % Sh::kSlots]));
-            ++n;
-        };
-        auto store = [&](uint8_t *to, int i, const uint4 &c, uint32_t (&h)[8]) {
-            const uint32_t x[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                h[2 * y] = at_e4m3x2_f16x2(x[y]);
-                h[2 * y + 1] = at_e4m3x2_f16x2(x[y] >> 16);
-            }
-            if (token[i] < Sh::T) {
-                *reinterpret_cast<uint4 *>(to + dst[i]) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4 *>(to + (dst[i] ^ 16u)) = make_uint4(h[4], h[5], h[6], h[7]);
-            }
-        };
-#pragma unroll 1
-        for (int j = w.j0; ok && j < j1; ++j, ++it) {
-            if (!slot_begin()) break;
-            uint8_t *to = slots + (n % Sh::kSlots) * Sh::kSlot;
+        // One raw slot, which has come, as f16; then the copies that take its place.  The sum of V's values (at most 32 x 448)
+        // is not finite where one is a NaN.
+        auto convert = [&](int n, uint8_t *to, auto is_v) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(Sh::kRaws - 1) : "memory");
+            const uint8_t *x = mine + (n % Sh::kRaws) * Sh::kRaw;
+            __half2 sum = __half2(__ushort_as_half(0), __ushort_as_half(0));
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
+                const uint4 c = *reinterpret_cast<const uint4 *>(x + i * kThreads * 16);
+                const uint32_t y[4] = {c.x, c.y, c.z, c.w};
                 uint32_t h[8];
-                store(to, i, kx[i], h);
-            }
-            if (warp == 0) {
-                // Scales of the tile's sixteens, and a flag for blocks outside the pool.
-                float k1 = 1.f;
-                if (lane < Sh::kGranules) {
-                    const int b = id_of(j, 16 * lane);
-                    const int64_t bh = static_cast<int64_t>(b) * a.kv_heads + w.head;
-                    float v1 = 1.f;
-                    if (b != -2) {
-                        const bool there = static_cast<uint32_t>(b) < n_blocks;
-                        k1 = there ? a.k_scales[bh] : INFINITY;
-                        v1 = there ? a.v_scales[bh] : INFINITY;
-                        if (!there) atomicOr(a.status, 4u);
-                        if (!(fabsf(k1) < INFINITY)) k1 = __int_as_float(0x7FC00000);
-                        if (!(fabsf(v1) < INFINITY)) {  // every element, from here on
-                            sh.any_nan[ub] = 1;
-#pragma unroll 1
-                            for (int d = 0; d < a.head_dim; ++d) atomicMin(&sh.vnan[ub][d], j * Sh::T + 16 * lane);
-                            v1 = 1.f;
-                        }
-                    }
-                    const bool small = fabsf(v1) < 0x1p-126f;
-                    const uint32_t bits = __float_as_uint(small ? v1 * 0x1p64f : v1), e = bits >> 23 & 0xFFu;
-                    sh.info[it & (kChInfo - 1)][lane] =
-                        v1 == 0.f ? make_float4(k1, -1000.f, 1.f, 0.f)
-                                  : make_float4(k1, static_cast<float>(static_cast<int>(e) - (small ? 191 : 127)),
-                                                __uint_as_float((bits & 0x807FFFFFu) | 0x3F800000u), 0.f);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    h[2 * z] = at_e4m3x2_f16x2(y[z]);
+                    h[2 * z + 1] = at_e4m3x2_f16x2(y[z] >> 16);
                 }
-                const bool minus = __any_sync(0xFFFFFFFFu, k1 < 0.f);
+                if (token[i] < Sh::T) {
+                    *reinterpret_cast<uint4 *>(to + dst[i]) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4 *>(to + (dst[i] ^ 16u)) = make_uint4(h[4], h[5], h[6], h[7]);
+                }
+                if (decltype(is_v)::value) {
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) sum = __hadd2(sum, *reinterpret_cast<const __half2 *>(h + z));
+                }
+            }
+            copy(n + Sh::kRaws);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            return sum;
+        };
+#pragma unroll 1
+        for (int j = w.j0; j < j1; ++j, ++nt) {
+            const int slot = nt % kSlots, n = 2 * (j - w.j0);
+            const uint32_t free = (static_cast<uint32_t>(nt / kSlots) & 1u) ^ 1u;
+            if (j == first + kWindow) {  // (the copies ahead are in this window or the next)
+                first = j;
+                id0 = id1;
+                id1 = id2;
+                k0 = k1;
+                v0 = v1;
+                id2 = window(j + 2 * kWindow);
+                if (warp == 0) scales(id1, k1, v1);
+            }
+            ok = nt < kSlots || ch_wait(a, sh, sh.k_free[slot], free);
+            if (!ok) break;
+            (void)convert(n, k_slots + slot * Sh::kSlot, std::false_type{});
+            if (warp == 0) {
+                const int at = nt & (kChInfo - 1);
+                bool odd = false;
+                if (lane / G == j - first) {
+                    const float k = fabsf(k0) < INFINITY ? k0 : __int_as_float(0x7FC00000);
+                    float v = v0;
+                    if (!(fabsf(v) < INFINITY)) {  // every element, from here on
+                        sh.any_nan[ub] = 1;
+#pragma unroll 1
+                        for (int d = 0; d < a.head_dim; ++d) atomicMin(&sh.vnan[ub][d], j * Sh::T + 16 * (lane % G));
+                        v = 1.f;
+                    }
+                    const bool small = fabsf(v) < 0x1p-126f;
+                    const uint32_t bits = __float_as_uint(small ? v * 0x1p64f : v), e = bits >> 23 & 0xFFu;
+                    const float4 f = v == 0.f ? make_float4(k, -1000.f, 1.f, 0.f)
+                                              : make_float4(k, static_cast<float>(static_cast<int>(e) - (small ? 191 : 127)),
+                                                            __uint_as_float((bits & 0x807FFFFFu) | 0x3F800000u), 0.f);
+                    odd = k < 0.f || f.z != 1.f;
+                    sh.info[at][lane % G] = f;
+                }
+                odd = __any_sync(0xFFFFFFFFu, odd);
                 __syncwarp();
                 if (lane == 0) {
-                    sh.info_minus[it & (kChInfo - 1)] = minus;
-                    mbar_arrive(smem_addr(&sh.info_full[it & (kChInfo - 1)]));
+                    sh.info_odd[at] = odd;
+                    mbar_arrive(smem_addr(&sh.info_full[at]));
                 }
             }
-            slot_end();
-            fetch(j + 1, id, k_codes, kx);
-            if (!slot_begin()) break;
-            to = slots + (n % Sh::kSlots) * Sh::kSlot;
-            __half2 sum = __half2(__ushort_as_half(0), __ushort_as_half(0));  // of the values (at most 32 x 448): a NaN shows in it
-#pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                uint32_t h[8];
-                store(to, i, vx[i], h);
-#pragma unroll
-                for (int y = 0; y < 8; ++y) sum = __hadd2(sum, *reinterpret_cast<const __half2 *>(h + y));
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.k_full[slot]));
+            ok = nt < kSlots || ch_wait(a, sh, sh.v_free[slot], free);
+            if (!ok) break;
+            uint8_t *to = v_slots + slot * Sh::kSlot;
+            const __half2 sum = convert(n + 1, to, std::true_type{});
             if (__hisnan(sum.x) || __hisnan(sum.y)) {  // seldom: zeros in their places, and from which position on each element has one
                 sh.any_nan[ub] = 1;
 #pragma unroll 1
@@ -640,14 +654,15 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
                     }
                 }
             }
-            slot_end();
-            fetch(j + 1, id, v_codes, vx);
-            ids(j + 2, id);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.v_full[slot]));
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.values_done[ub]));
         ++unit;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ MMAs
@@ -658,16 +673,18 @@ __device__ __forceinline__ bool ch_elect() {
     return one != 0;
 }
 
-// The MMAs of product `i`.  The warp goes through the tiles together; one thread
+// The MMAs of a product.  The warp goes through the tiles together; one thread
 // issues.  Returns whether anything was issued.
 template <typename Sh>
-__device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, uint32_t tmem_base, uint32_t sq, uint32_t slots, int product,
-                                         int lane) {
-    constexpr int PL = Sh::PL, T = Sh::T;
+__device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, uint32_t tmem_base, uint32_t sq, uint32_t k_slots,
+                                         uint32_t v_slots, int product, int lane) {
+    constexpr int PL = Sh::PL, T = Sh::T, kSlots = Sh::kSlots;
     constexpr uint32_t qk_idesc = ch_idesc(T, false);
+    // (Broadcasts, here and below: so the compiler knows these, and what is counted by them, to be one value a warp, and
+    // descriptors and addresses are made by the uniform units.)
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
     const int i = Sh::NS == 1 ? 0 : __shfl_sync(0xFFFFFFFFu, product, 0);
-    const uint64_t q_desc = ch_desc(sq + i * PL * Sh::kQPlane, 16), k_desc = ch_desc(slots, 16), v_desc = ch_desc(slots, T * 128);
+    const uint64_t q_desc = ch_desc(sq + i * PL * Sh::kQPlane, 16), k_desc = ch_desc(k_slots, 16), v_desc = ch_desc(v_slots, T * 128);
     const int steps = a.head_dim / 16;
     bool any = false, ok = true;
     auto wait = [&](uint64_t &bar, uint32_t parity) {
@@ -675,14 +692,19 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
         t8_fence_after();
         return ok;
     };
-    int n = 0, unit = 0;      // slots consumed in order K, V, K, V ..; units with tiles
-    int done = 0, begun = 0;  // tiles whose weights have been taken, whose scores have been issued
-    int products = 0;         // f32: products of a tile (of half a wide head) issued
-    // Scores against K in the slot, the second plane's first.  end: q is read.
-    auto scores = [&](int slot, bool end) {
-        const int buf = Sh::NS == 1 ? begun & 1 : i;
+    // The converters' stores, seen through their barriers, before the MMAs' reads.  (The fence is here and not behind the
+    // stores: there it waited for the thread's loads of the tiles to come as well, 2000 cycles a tile.)
+    auto stores_seen = [&]() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); };
+    int nk = 0, nv = 0, unit = 0;  // tiles of K, of V that have gone by; units with tiles
+    int ms = 0, mv = 0;            // tiles whose scores, whose sums have been issued
+    int products = 0;              // products of the second kind (f32, wide: two a tile)
+    // Scores of the next tile against K, the second plane's first.  end: q is read.
+    auto scores = [&](bool end) {
+        const int slot = nk % kSlots, buf = 2 * i + (ms & 1);
+        if (!wait(sh.k_full[slot], static_cast<uint32_t>(nk / kSlots) & 1u)) return;
+        stores_seen();
         if (ch_elect()) {
-            const uint32_t d = tmem + static_cast<uint32_t>(buf * (Sh::NS == 1 ? T : 128));
+            const uint32_t d = tmem + static_cast<uint32_t>(buf * T);
             const uint64_t k = k_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
 #pragma unroll 1
             for (int p = PL - 1; p >= 0; --p) {
@@ -693,23 +715,28 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
                               p + 1 < PL || s > 0);
             }
             t8_commit(smem_addr(&sh.s_full[buf]));
-            t8_commit(smem_addr(&sh.slot_free[slot]));
+            t8_commit(smem_addr(&sh.k_free[slot]));
             if (end) t8_commit(smem_addr(&sh.q_free));
         }
         __syncwarp();
-        ++begun;
+        ++nk;
+        ++ms;
         any = true;
     };
-    auto sums = [&](int slot, bool acc) {  // the weights times V in the slot
-        const uint32_t p0 = tmem + Sh::weights_col(Sh::NS == 1 ? done & 1 : i, a.head_dim);
+    // The next tile's weights times V.  They lie where its scores were and the scores after the next will be: only MMAs of
+    // one shape are sure to run in the order of their issue, so the end of these is waited for.
+    auto sums = [&](bool acc) {
+        const int slot = nv % kSlots, buf = 2 * i + (mv & 1);
+        if (!wait(sh.v_full[slot], static_cast<uint32_t>(nv / kSlots) & 1u) || !wait(sh.p_full[buf], static_cast<uint32_t>(mv >> 1) & 1u)) return;
+        stores_seen();
+        const uint32_t p0 = tmem + static_cast<uint32_t>(buf * T);
         const uint64_t v = v_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
 #pragma unroll 1
         for (int h = 0; h < Sh::kHalves; ++h) {
             if (Sh::SUMS && products > 0 && !wait(sh.product_free, static_cast<uint32_t>(products - 1) & 1u)) return;
             if (ch_elect()) {
                 const uint32_t d = tmem + static_cast<uint32_t>(Sh::SUMS ? Sh::kProductCol : Sh::kSumCol + i * 128);
-                const int cols = Sh::sum_cols(a.head_dim);
-                const uint32_t idesc = ch_idesc(Sh::kHalves == 1 ? cols : h == 0 ? 128 : cols - 128, true);
+                const uint32_t idesc = ch_idesc(Sh::kHalves == 1 ? a.head_dim : h == 0 ? 128 : a.head_dim - 128, true);
 #pragma unroll 1
                 for (int p = PL - 1; p >= 0; --p)
 #pragma unroll 1
@@ -717,44 +744,36 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
                         ch_mma_ts(d, p0 + (PL == 1 ? 8 * s : 32 * (s >> 1) + 16 * p + 8 * (s & 1)),
                                   v + h * (2 * T * 128 / 16) + s * (16 * 128 / 16), idesc, (!Sh::SUMS && acc) || p + 1 < PL || s > 0);
                 t8_commit(smem_addr(&sh.o_done[i]));
-                if (h + 1 == Sh::kHalves) t8_commit(smem_addr(&sh.slot_free[slot]));
+                if (h + 1 == Sh::kHalves) t8_commit(smem_addr(&sh.v_free[slot]));
             }
             __syncwarp();
-            ++products;
+            if (!wait(sh.o_done[i], static_cast<uint32_t>(products++) & 1u)) return;
         }
-        ++done;
+        ++nv;
+        ++mv;
     };
-    auto slot_ready = [&](int m) { return wait(sh.slot_full[m % Sh::kSlots], static_cast<uint32_t>(m / Sh::kSlots) & 1u); };
     ChunkUnit w;
     for (int u = 0; ch_unit(sh, u, lane, w); ++u) {
-        // (Broadcasts: so the compiler knows these, and what is counted by them, to be one value a warp, and descriptors and
-        // addresses are made by the uniform units.)
         const int two = __shfl_sync(0xFFFFFFFFu, w.flags & kChTwo, 0), tiles = __shfl_sync(0xFFFFFFFFu, w.tiles, 0);
         if (tiles == 0 || !ok) continue;
         if (!wait(sh.q_full[unit & 1], static_cast<uint32_t>(unit >> 1) & 1u)) continue;
         if (i == 1 && !two) {
             // No rows: each slot is given back once it has been filled.
 #pragma unroll 1
-            for (int j = 0; j < 2 * tiles && slot_ready(n); ++j, ++n)
-                if (lane == 0) mbar_arrive(smem_addr(&sh.slot_free[n % Sh::kSlots]));
+            for (int j = 0; j < tiles && wait(sh.k_full[nk % kSlots], static_cast<uint32_t>(nk / kSlots) & 1u); ++j, ++nk) {
+                if (lane == 0) mbar_arrive(smem_addr(&sh.k_free[nk % kSlots]));
+                if (!wait(sh.v_full[nv % kSlots], static_cast<uint32_t>(nv / kSlots) & 1u)) break;
+                if (lane == 0) mbar_arrive(smem_addr(&sh.v_free[nv % kSlots]));
+                ++nv;
+            }
             if (lane == 0) mbar_arrive(smem_addr(&sh.q_free));
             ++unit;
             continue;
         }
-        if (!slot_ready(n)) continue;
-        scores(n % Sh::kSlots, tiles == 1);
 #pragma unroll 1
-        for (int j = 0; ok && j < tiles; ++j, n += 2) {
-            const bool next = j + 1 < tiles, end = j + 2 == tiles;
-            // One product: the next scores have a buffer of their own.  (f32: the weights in it have been taken once their
-            // product is in the sums.)
-            if (Sh::NS == 1 && next && slot_ready(n + 2) &&
-                (!Sh::SUMS || products == 0 || wait(sh.product_free, static_cast<uint32_t>(products - 1) & 1u)))
-                scores((n + 2) % Sh::kSlots, end);
-            if (!slot_ready(n + 1)) break;
-            if (!wait(sh.p_full[Sh::NS == 1 ? done & 1 : i], static_cast<uint32_t>(Sh::NS == 1 ? done >> 1 : done) & 1u)) break;
-            sums((n + 1) % Sh::kSlots, j > 0);
-            if (Sh::NS == 2 && next && slot_ready(n + 2)) scores((n + 2) % Sh::kSlots, end);
+        for (int j = -2; ok && j < tiles; ++j) {
+            if (j >= 0) sums(j > 0);
+            if (ok && j + 2 < tiles) scores(j + 3 == tiles);
         }
         ++unit;
     }
@@ -839,7 +858,8 @@ __device__ __forceinline__ void ch_nothing(const ChunkArgs &a, const ChunkRow &r
 
 // The weights of sixteen columns, from their scores, as f16 words (PL = 2: and
 // what those leave), their sum at the row's maximum added to l.
-// CAREFUL: columns past `rel` are not seen, and product and difference round one
+// CAREFUL: columns past `rel` are not seen, the value scale has a mantissa (or a
+// sign), and product and difference round one
 // by one, as the maxima did, so that no weight is above its reference (past 2^20
 // the rounding of a score shows beside that).
 template <int PL, bool CAREFUL>
@@ -866,7 +886,7 @@ __device__ __forceinline__ void ch_weights(const float *v, int col, int rel, flo
     float s0, s1;
     ch_unpair(sum, s0, s1);
     l = fmaf(s0 + s1, at_exp2(-log), l);
-    if (mantissa != 1.f) {
+    if (CAREFUL) {
 #pragma unroll
         for (int x = 0; x < 16; ++x) w[x] *= mantissa;
     }
@@ -911,7 +931,7 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
     const uint32_t o_col = tmem + lanes + static_cast<uint32_t>(Sh::kSumCol + product * 128);
     const int local = product * 128 + wq * 32 + lane;
     int it = 0, unit = 0;   // all tiles of the CTA; units with tiles
-    int mine = 0;           // tiles of this product
+    int mine = 0;           // tiles of this product (the buffers of a product go by its own count)
     bool ok = true;
     ChunkUnit w;
     for (int u = 0; ch_unit(sh, u, lane, w); ++u) {
@@ -932,14 +952,16 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
         const float qs = sh.qs[ub][local];
         float M = kChNone, R = kChNone, l = 0.f;  // maximum, the weights' reference less M, denominator
         for (int j = 0; ok && j < tiles; ++j, ++it, ++mine) {
-            const int sb = Sh::NS == 1 ? mine & 1 : 0;
-            const uint32_t s_col = tmem + lanes + static_cast<uint32_t>(Sh::NS == 1 ? sb * kTile : product * 128);
-            ok = ch_wait(a, sh, sh.info_full[it & (kChInfo - 1)], static_cast<uint32_t>(it / kChInfo) & 1u);
-            const float4 *info = sh.info[it & (kChInfo - 1)];
+            const int at = it & (kChInfo - 1), buf = 2 * product + (mine & 1);
+            const uint32_t s_col = tmem + lanes + static_cast<uint32_t>(buf * kTile);
+            ok = ch_wait(a, sh, sh.info_full[at], static_cast<uint32_t>(it / kChInfo) & 1u);
+            const float4 *info = sh.info[at];
             const int64_t t0 = static_cast<int64_t>(w.j0 + j) * kTile;
             const int rel = t0 > row.last ? -1 : static_cast<int>(row.last - t0 < kTile ? row.last - t0 : kTile);  // last column this row sees
-            const bool careful = __any_sync(0xFFFFFFFFu, rel < kTile - 1 || fabsf(M) >= 0x1p19f) || sh.info_minus[it & (kChInfo - 1)] != 0;
-            ok = ok && ch_wait(a, sh, sh.s_full[Sh::NS == 1 ? sb : product], static_cast<uint32_t>(Sh::NS == 1 ? mine >> 1 : mine) & 1u);
+            // Tiles that are not seen whole, odd scales, and scores past 2^19, where the rounding of a score shows beside its
+            // row's reference.
+            const bool careful = __any_sync(0xFFFFFFFFu, rel < kTile - 1 || fabsf(M) >= 0x1p19f) || sh.info_odd[at] != 0;
+            ok = ok && ch_wait(a, sh, sh.s_full[buf], static_cast<uint32_t>(mine >> 1) & 1u);
             if (!ok) break;
             t8_fence_after();
             // The row's maximum, and the largest of the sixteens' maxima times their value scales, relative to the former.
@@ -1003,36 +1025,36 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
             }
             if (move) R = ref;
             const float base = M > kChNone ? M : 0.f, lift = R > kChNone ? static_cast<float>(kChLift) - R : 0.f;
-            const uint32_t w_col = tmem + lanes + Sh::weights_col(Sh::NS == 1 ? sb : product, a.head_dim);
             auto weights = [&](auto slow) {
-                ch_columns<kTile, decltype(slow)::value>(s_col, [&](int c, float (&v)[32]) {
+                constexpr bool kSlow = decltype(slow)::value;
+                ch_columns<kTile, kSlow>(s_col, [&](int c, float (&v)[32]) {
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const float4 f = info[c / 16 + g];
-                        ch_weights<PL, decltype(slow)::value>(v + 16 * g, c + 16 * g, rel, f.x * qs, base, fmaxf(f.y + lift, kChMinLog), f.z, l,
-                                                              hi + 8 * g, lo + 8 * g);
+                        ch_weights<PL, kSlow>(v + 16 * g, c + 16 * g, rel, f.x * qs, base, fmaxf(f.y + lift, kChMinLog), f.z, l, hi + 8 * g,
+                                              lo + 8 * g);
                     }
                     if (PL == 1) {
-                        ch_st16(w_col + c / 2, hi);
+                        ch_st16(s_col + c / 2, hi);
                     } else {
-                        ch_st16(w_col + c, hi);
-                        ch_st16(w_col + c + 16, lo);
+                        ch_st16(s_col + c, hi);
+                        ch_st16(s_col + c + 16, lo);
                     }
                 });
             };
             if (careful || __any_sync(0xFFFFFFFFu, fabsf(base) >= 0x1p20f)) weights(std::true_type{});
             else weights(std::false_type{});
             ch_wait_st();
-            // With scores issued ahead, the sums of the tile before may still be under way: each phase is waited for, so that
-            // the last one cannot be taken for the one before it.
-            if (Sh::NS == 1 && !Sh::SUMS && j > 0) {
-                ok = ch_wait(a, sh, sh.o_done[0], static_cast<uint32_t>(mine - 1) & 1u);
+            // The sums of the tile before may still be under way: each phase is waited for, so that the last one cannot be
+            // taken for the one before it.
+            if (!Sh::SUMS && j > 0) {
+                ok = ch_wait(a, sh, sh.o_done[product], static_cast<uint32_t>(mine - 1) & 1u);
                 if (!ok) break;
             }
             t8_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[Sh::NS == 1 ? sb : product]));
+            if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[buf]));
         }
         if (Sh::SUMS) {
             sh.last[ub][0][local] = M;
@@ -1111,15 +1133,17 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
     __shared__ __align__(16) ChunkShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t *sq = ch_smem + ((1024u - (smem_addr(ch_smem) & 1023u)) & 1023u);
-    uint8_t *slots = sq + Sh::kQ;
+    uint8_t *k_slots = sq + Sh::kQ, *v_slots = k_slots + Sh::kSlots * Sh::kSlot, *raw = v_slots + Sh::kSlots * Sh::kSlot;
     if (tid == 0) {
-        for (int i = 0; i < Sh::kSlots; ++i) {
-            mbar_init(smem_addr(&sh.slot_full[i]), kChConvertWarps);
-            mbar_init(smem_addr(&sh.slot_free[i]), Sh::kIssuers);
-        }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_addr(&sh.k_full[i]), kChConvertWarps);
+            mbar_init(smem_addr(&sh.k_free[i]), Sh::kIssuers);
+            mbar_init(smem_addr(&sh.v_full[i]), kChConvertWarps);
+            mbar_init(smem_addr(&sh.v_free[i]), Sh::kIssuers);
             mbar_init(smem_addr(&sh.s_full[i]), 1);
             mbar_init(smem_addr(&sh.p_full[i]), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.o_done[i]), 1);
             mbar_init(smem_addr(&sh.q_full[i]), kChConvertWarps);
             mbar_init(smem_addr(&sh.values_done[i]), kChConvertWarps);
@@ -1229,13 +1253,13 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
             else if (Sh::SUMS) ch_sums<Sh, T>(a, sh, tmem, warp & 3, lane);
         } else if (warp < kChMmaWarp) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kChConvertRegs));
-            ch_convert<Sh, T>(a, sh, sq, slots, tid - kChConvertWarp * 32);
+            ch_convert<Sh, T>(a, sh, sq, k_slots, v_slots, raw, tid - kChConvertWarp * 32);
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kChIssueRegs));
             if (warp < kChMmaWarp + Sh::kIssuers) {
                 // Also after a wait that ran out: nothing is in flight at the end.
                 const int i = warp - kChMmaWarp;
-                if (ch_issue<Sh>(a, sh, tmem, smem_addr(sq), smem_addr(slots), i, lane)) {
+                if (ch_issue<Sh>(a, sh, tmem, smem_addr(sq), smem_addr(k_slots), smem_addr(v_slots), i, lane)) {
                     if (ch_elect()) t8_commit(smem_addr(&sh.mma_done[i]));
                     __syncwarp();
                     (void)mbar_wait_bounded(smem_addr(&sh.mma_done[i]), 0);
