@@ -139,7 +139,7 @@ struct ChunkShared {
     uint64_t factor_full[kChInfo], last_full[2], product_free;  // f32's sums
     uint64_t unit_full[kChUnits], unit_free[kChUnits];
     float4 info[kChInfo][4];     // per sixteen tokens: k scale (NaN if not finite), exponent of the v scale, its signed mantissa
-    int info_odd[kChInfo];       // whether a k scale of the tile is negative, or a v scale no (positive) power of two
+    int info_kind[kChInfo];      // of a tile's scales: 0 all the same, 1 several, 2 a negative k scale, or a v scale that is no (positive) power of two
     ChunkUnit units[kChUnits];
     float qs[2][256];            // per row: what a score is times |s_k| of
     float factor[kChInfo][128];  // f32: what the sums so far are times, per row of a tile
@@ -273,20 +273,20 @@ __device__ __forceinline__ void ch_plan(const ChunkArgs &a, ChunkShared &sh) {
 }
 
 // A role's wait, for a whole warp: for at most the limit, or until another role has
-// raised the abort flag.  (A short loop: the waits are inlined in every role.)
+// raised the abort flag.
 __device__ __forceinline__ bool ch_wait(const ChunkArgs &a, ChunkShared &sh, uint64_t &bar, uint32_t parity) {
     const uint32_t at = smem_addr(&bar);
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait_short(at, parity))) return true;
     uint64_t t0 = 0;
-    bool ok = true;
 #pragma unroll 1
-    for (int n = 1; ok && !mbar_try_wait_short(at, parity); ++n) {
+    for (int n = 1; !__all_sync(0xFFFFFFFFu, mbar_try_wait_short(at, parity)); ++n) {
         if ((n & 15) != 0) continue;
         const uint64_t now = global_timer_ns();
         if (t0 == 0) t0 = now;
         if (now - t0 >= a.wait_limit_ns) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
-        ok = *reinterpret_cast<volatile int *>(&sh.abort) == 0;
+        if (__any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int *>(&sh.abort) != 0)) return false;
     }
-    return __all_sync(0xFFFFFFFFu, ok);
+    return true;
 }
 
 // The u-th unit, for a warp; false after the last one.
@@ -480,7 +480,7 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
                                            int tid) {
     constexpr int kEach = Sh::kEach, kThreads = kChConvertWarps * 32, kSlots = Sh::kSlots, G = Sh::kGranules, kWindow = 32 / G;
     const int warp = tid >> 5, lane = tid & 31, per = a.head_dim / 16, total = Sh::T * per, block = 1 << a.block_log2;
-    int token[kEach], from[kEach];  // of the thread's groups: token of a tile (T: none), place in the block of its first tile
+    int token[kEach];  // of the thread's groups, in a tile (T: none)
     uint32_t dst[kEach];
     auto group = [&](int i, int &t, int &c) {
         const int g = tid + i * kThreads;
@@ -488,6 +488,7 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
         c = g < total ? g - t * per : 0;
         return (c >> 2) * (Sh::T * 128) + t * 128 + (((2 * (c & 3)) ^ (t & 7)) << 4);
     };
+    int from[kEach];   // ... their places in the block of a request's first tile
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
         int c;
@@ -522,34 +523,42 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
             v1 = there ? a.v_scales[bh] : INFINITY;
             if (!there) atomicOr(a.status, 4u);
         };
-        int id0 = window(w.j0), id1 = window(w.j0 + kWindow), id2 = 0, first = w.j0;  // windows from tile `first` on
+        // Ids of the window from tile `ahead` on, which the copies have come to, and of the next; scales of the window from tile
+        // `first` on (warp 0), and ids and scales of the next.
+        int id = window(w.j0), id_next = window(w.j0 + kWindow), ahead = w.j0, first = w.j0, id_scales = id_next;
         float k0 = 1.f, v0 = 1.f, k1 = 1.f, v1 = 1.f;
         // Copies of slot n of the unit (K and V of its tiles in turn), into the raw slot n % kRaws.
-        auto copy = [&](int n) {
-            const int j = w.j0 + (n >> 1), at = (j - first) * G;
-            const uint8_t *codes = n & 1 ? a.v_codes : a.k_codes;
-            const int64_t more = head + (j * Sh::T & (block - 1)) * a.head_dim;  // (a block of 128 tokens is two tiles)
-            const uint32_t to = smem_addr(mine) + (n % Sh::kRaws) * Sh::kRaw;
+        const uint8_t *k_head = a.k_codes + head, *v_head = a.v_codes + head;
+        int n_copy = 0, j_copy = w.j0;
+        uint32_t to_copy = smem_addr(mine);
+        auto copy = [&]() {
+            if (j_copy == ahead + kWindow) {
+                ahead = j_copy;
+                id = id_next;
+                id_next = window(j_copy + kWindow);
+            }
+            const uint8_t *codes = (n_copy & 1 ? v_head : k_head) + (j_copy * Sh::T & (block - 1)) * a.head_dim;  // (a block of 128 tokens is two tiles)
+            const int left = w.len - j_copy * Sh::T;  // (past the unit's last tile the ids say so)
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-                const int lane_of = at + (token[i] >> 4);
-                const int a0 = __shfl_sync(0xFFFFFFFFu, id0, lane_of & 31), a1 = __shfl_sync(0xFFFFFFFFu, id1, lane_of & 31);
-                const int id = lane_of < 32 ? a0 : a1;
-                const bool there = static_cast<uint32_t>(id) < n_blocks && j < j1 && static_cast<int64_t>(j) * Sh::T + token[i] < w.len;
-                const uint8_t *p = there ? codes + id * id_bytes + (from[i] + more) : codes;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + i * kThreads * 16), "l"(p), "r"(there ? 16 : 0) : "memory");
+                const int b = __shfl_sync(0xFFFFFFFFu, id, (j_copy - ahead) * G + (token[i] >> 4));
+                const bool there = static_cast<uint32_t>(b) < n_blocks && token[i] < left;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to_copy + i * kThreads * 16),
+                             "l"(codes + (there ? b : 0) * id_bytes + from[i]), "r"(there ? 16 : 0)
+                             : "memory");
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            j_copy += n_copy & 1;
+            ++n_copy;
+            to_copy = n_copy % Sh::kRaws == 0 ? smem_addr(mine) : to_copy + Sh::kRaw;
         };
 #pragma unroll 1
-        for (int n = 0; n < Sh::kRaws; ++n) {
-            copy(n);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
+        for (int n = 0; n < Sh::kRaws; ++n) copy();
         if (warp == 0) {
-            scales(id0, k0, v0);
-            scales(id1, k1, v1);
+            scales(id, k0, v0);
+            scales(id_scales, k1, v1);
+            id_scales = window(w.j0 + 2 * kWindow);
         }
-        id2 = window(w.j0 + 2 * kWindow);
         // The unit's queries, once the MMAs have read the last one's, and the softmax has written out the one before that.
         ok = (unit < 1 || ch_wait(a, sh, sh.q_free, static_cast<uint32_t>(unit - 1) & 1u)) &&
              (unit < 2 || ch_wait(a, sh, sh.unit_done[ub], static_cast<uint32_t>((unit >> 1) - 1) & 1u));
@@ -572,10 +581,10 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
                 const uint32_t y[4] = {c.x, c.y, c.z, c.w};
                 uint32_t h[8];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    h[2 * z] = at_e4m3x2_f16x2(y[z]);
-                    h[2 * z + 1] = at_e4m3x2_f16x2(y[z] >> 16);
-                }
+                for (int z = 0; z < 4; ++z)
+                    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+                        : "=r"(h[2 * z]), "=r"(h[2 * z + 1])
+                        : "r"(y[z]));
                 if (token[i] < Sh::T) {
                     *reinterpret_cast<uint4 *>(to + dst[i]) = make_uint4(h[0], h[1], h[2], h[3]);
                     *reinterpret_cast<uint4 *>(to + (dst[i] ^ 16u)) = make_uint4(h[4], h[5], h[6], h[7]);
@@ -585,31 +594,29 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
                     for (int z = 0; z < 8; ++z) sum = __hadd2(sum, *reinterpret_cast<const __half2 *>(h + z));
                 }
             }
-            copy(n + Sh::kRaws);
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            copy();
             return sum;
         };
 #pragma unroll 1
         for (int j = w.j0; j < j1; ++j, ++nt) {
-            const int slot = nt % kSlots, n = 2 * (j - w.j0);
+            const int slot = nt % kSlots, n = 2 * (j - w.j0);  // (a slot of each ring, and K's place among the raw ones)
             const uint32_t free = (static_cast<uint32_t>(nt / kSlots) & 1u) ^ 1u;
-            if (j == first + kWindow) {  // (the copies ahead are in this window or the next)
+            if (warp == 0 && j == first + kWindow) {
                 first = j;
-                id0 = id1;
-                id1 = id2;
                 k0 = k1;
                 v0 = v1;
-                id2 = window(j + 2 * kWindow);
-                if (warp == 0) scales(id1, k1, v1);
+                scales(id_scales, k1, v1);
+                id_scales = window(j + 2 * kWindow);
             }
             ok = nt < kSlots || ch_wait(a, sh, sh.k_free[slot], free);
             if (!ok) break;
             (void)convert(n, k_slots + slot * Sh::kSlot, std::false_type{});
             if (warp == 0) {
                 const int at = nt & (kChInfo - 1);
-                bool odd = false;
-                if (lane / G == j - first) {
-                    const float k = fabsf(k0) < INFINITY ? k0 : __int_as_float(0x7FC00000);
+                float4 f = make_float4(1.f, 0.f, 1.f, 0.f);
+                const bool here = lane / G == j - first;
+                if (here) {
+                    f.x = fabsf(k0) < INFINITY ? k0 : __int_as_float(0x7FC00000);
                     float v = v0;
                     if (!(fabsf(v) < INFINITY)) {  // every element, from here on
                         sh.any_nan[ub] = 1;
@@ -619,16 +626,17 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
                     }
                     const bool small = fabsf(v) < 0x1p-126f;
                     const uint32_t bits = __float_as_uint(small ? v * 0x1p64f : v), e = bits >> 23 & 0xFFu;
-                    const float4 f = v == 0.f ? make_float4(k, -1000.f, 1.f, 0.f)
-                                              : make_float4(k, static_cast<float>(static_cast<int>(e) - (small ? 191 : 127)),
-                                                            __uint_as_float((bits & 0x807FFFFFu) | 0x3F800000u), 0.f);
-                    odd = k < 0.f || f.z != 1.f;
+                    f.y = v == 0.f ? -1000.f : static_cast<float>(static_cast<int>(e) - (small ? 191 : 127));
+                    f.z = v == 0.f ? 1.f : __uint_as_float((bits & 0x807FFFFFu) | 0x3F800000u);
                     sh.info[at][lane % G] = f;
                 }
-                odd = __any_sync(0xFFFFFFFFu, odd);
+                // (Tokens past the request's end take any scale.)
+                const bool odd = __any_sync(0xFFFFFFFFu, here && (f.x < 0.f || f.z != 1.f));
+                const float kf = __shfl_sync(0xFFFFFFFFu, f.x, (j - first) * G), vf = __shfl_sync(0xFFFFFFFFu, f.y, (j - first) * G);
+                const bool same = __all_sync(0xFFFFFFFFu, !here || (f.x == kf && f.y == vf));
                 __syncwarp();
                 if (lane == 0) {
-                    sh.info_odd[at] = odd;
+                    sh.info_kind[at] = odd ? 2 : same ? 0 : 1;
                     mbar_arrive(smem_addr(&sh.info_full[at]));
                 }
             }
@@ -856,20 +864,20 @@ __device__ __forceinline__ void ch_nothing(const ChunkArgs &a, const ChunkRow &r
     if (a.lse) a.lse[row.lse] = -INFINITY;
 }
 
-// The weights of sixteen columns, from their scores, as f16 words (PL = 2: and
-// what those leave), their sum at the row's maximum added to l.
+// The weights of N columns, from their scores, as f16 words (PL = 2: and what those
+// leave); their sum is the answer.
 // CAREFUL: columns past `rel` are not seen, the value scale has a mantissa (or a
 // sign), and product and difference round one
 // by one, as the maxima did, so that no weight is above its reference (past 2^20
 // the rounding of a score shows beside that).
-template <int PL, bool CAREFUL>
-__device__ __forceinline__ void ch_weights(const float *v, int col, int rel, float k, float base, float log, float mantissa, float &l,
-                                           uint32_t *hi, uint32_t *lo) {
+template <int PL, bool CAREFUL, int N>
+__device__ __forceinline__ float ch_weights(const float *v, int col, int rel, float k, float base, float log, float mantissa, uint32_t *hi,
+                                            uint32_t *lo) {
     const uint64_t k2 = ch_pair(k, k), off2 = ch_pair(log - base, log - base);
-    uint64_t sum = 0;
-    float w[16];
+    uint64_t sum[2] = {0, 0};
+    float w[N];
 #pragma unroll
-    for (int x = 0; x < 16; x += 2) {
+    for (int x = 0; x < N; x += 2) {
         float t0, t1;
         if (CAREFUL) {
             t0 = __fadd_rn(__fmul_rn(v[x], k), -base) + log;
@@ -881,23 +889,23 @@ __device__ __forceinline__ void ch_weights(const float *v, int col, int rel, flo
         }
         w[x] = at_exp2(t0);
         w[x + 1] = at_exp2(t1);
-        sum = ch_add2(sum, ch_pair(w[x], w[x + 1]));
+        sum[(x >> 1) & 1] = ch_add2(sum[(x >> 1) & 1], ch_pair(w[x], w[x + 1]));
     }
-    float s0, s1;
-    ch_unpair(sum, s0, s1);
-    l = fmaf(s0 + s1, at_exp2(-log), l);
     if (CAREFUL) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) w[x] *= mantissa;
+        for (int x = 0; x < N; ++x) w[x] *= mantissa;
     }
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
+    for (int x = 0; x < N / 2; ++x) {
         hi[x] = ch_pack_f16(w[2 * x], w[2 * x + 1]);
         if (PL == 2) {
             const float2 b = ch_unpack_f16(hi[x]);
             lo[x] = ch_pack_f16(w[2 * x] - b.x, w[2 * x + 1] - b.y);
         }
     }
+    float s0, s1;
+    ch_unpair(ch_add2(sum[0], sum[1]), s0, s1);
+    return s0 + s1;
 }
 
 // The scores of a tile in turn, 32 columns at a time.  LOOP: what is seldom needed
@@ -958,9 +966,12 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
             const float4 *info = sh.info[at];
             const int64_t t0 = static_cast<int64_t>(w.j0 + j) * kTile;
             const int rel = t0 > row.last ? -1 : static_cast<int>(row.last - t0 < kTile ? row.last - t0 : kTile);  // last column this row sees
-            // Tiles that are not seen whole, odd scales, and scores past 2^19, where the rounding of a score shows beside its
-            // row's reference.
-            const bool careful = __any_sync(0xFFFFFFFFu, rel < kTile - 1 || fabsf(M) >= 0x1p19f) || sh.info_odd[at] != 0;
+            // Careful: tiles that are not seen whole, odd scales, and scores past 2^19, where the rounding of a score shows
+            // beside its row's reference.
+            const int kind = ok ? sh.info_kind[at] : 0;
+            const bool careful = __any_sync(0xFFFFFFFFu, rel < kTile - 1 || fabsf(M) >= 0x1p19f) || kind == 2;
+            const float4 f0 = info[0];
+            const float k0 = f0.x * qs;
             ok = ok && ch_wait(a, sh, sh.s_full[buf], static_cast<uint32_t>(mine >> 1) & 1u);
             if (!ok) break;
             t8_fence_after();
@@ -973,13 +984,19 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
 #pragma unroll
                     for (int g = 0; g < 2; ++g) m16[c / 16 + g] = ch_max16(v + 16 * g);
                 });
+                if (kind == 0) {
+                    const float m = ceilf(fmaxf(ch_max3(m16[0], m16[1], m16[2]), m16[3]) * k0);
+                    top = fmaxf(top, m);
+                    ref = fmaxf(ref, (m - top) + f0.y);
+                } else {
 #pragma unroll
-                for (int g = 0; g < kTile / 16; ++g) {
-                    m16[g] = ceilf(m16[g] * (info[g].x * qs));
-                    top = fmaxf(top, m16[g]);
+                    for (int g = 0; g < kTile / 16; ++g) {
+                        m16[g] = ceilf(m16[g] * (info[g].x * qs));
+                        top = fmaxf(top, m16[g]);
+                    }
+#pragma unroll
+                    for (int g = 0; g < kTile / 16; ++g) ref = fmaxf(ref, (m16[g] - top) + info[g].y);
                 }
-#pragma unroll
-                for (int g = 0; g < kTile / 16; ++g) ref = fmaxf(ref, (m16[g] - top) + info[g].y);
             } else {
                 ch_columns<kTile, true>(s_col, [&](int c, float (&v)[32]) {
 #pragma unroll
@@ -1025,26 +1042,42 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
             }
             if (move) R = ref;
             const float base = M > kChNone ? M : 0.f, lift = R > kChNone ? static_cast<float>(kChLift) - R : 0.f;
-            auto weights = [&](auto slow) {
+            auto put = [&](int c, const uint32_t (&hi)[16], const uint32_t (&lo)[16]) {
+                if (PL == 1) {
+                    ch_st16(s_col + c / 2, hi);
+                } else {
+                    ch_st16(s_col + c, hi);
+                    ch_st16(s_col + c + 16, lo);
+                }
+            };
+            auto by_sixteens = [&](auto slow) {
                 constexpr bool kSlow = decltype(slow)::value;
-                ch_columns<kTile, kSlow>(s_col, [&](int c, float (&v)[32]) {
+                ch_columns<kTile, true>(s_col, [&](int c, float (&v)[32]) {
                     uint32_t hi[16], lo[16];
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const float4 f = info[c / 16 + g];
-                        ch_weights<PL, kSlow>(v + 16 * g, c + 16 * g, rel, f.x * qs, base, fmaxf(f.y + lift, kChMinLog), f.z, l, hi + 8 * g,
-                                              lo + 8 * g);
+                        const float log = fmaxf(f.y + lift, kChMinLog);
+                        l = fmaf(ch_weights<PL, kSlow, 16>(v + 16 * g, c + 16 * g, rel, f.x * qs, base, log, f.z, hi + 8 * g, lo + 8 * g),
+                                 at_exp2(-log), l);
                     }
-                    if (PL == 1) {
-                        ch_st16(s_col + c / 2, hi);
-                    } else {
-                        ch_st16(s_col + c, hi);
-                        ch_st16(s_col + c + 16, lo);
-                    }
+                    put(c, hi, lo);
                 });
             };
-            if (careful || __any_sync(0xFFFFFFFFu, fabsf(base) >= 0x1p20f)) weights(std::true_type{});
-            else weights(std::false_type{});
+            if (careful || __any_sync(0xFFFFFFFFu, fabsf(base) >= 0x1p20f)) {
+                by_sixteens(std::true_type{});
+            } else if (kind == 1) {
+                by_sixteens(std::false_type{});
+            } else {
+                const float log = fmaxf(f0.y + lift, kChMinLog);
+                float sum = 0.f;
+                ch_columns<kTile, false>(s_col, [&](int c, float (&v)[32]) {
+                    uint32_t hi[16], lo[16];
+                    sum += ch_weights<PL, false, 32>(v, c, rel, k0, base, log, 1.f, hi, lo);
+                    put(c, hi, lo);
+                });
+                l = fmaf(sum, at_exp2(-log), l);
+            }
             ch_wait_st();
             // The sums of the tile before may still be under way: each phase is waited for, so that the last one cannot be
             // taken for the one before it.
