@@ -59,7 +59,7 @@ extern "C" int fp8blk_kv_attn_chunk(const void *q, int dtype, const uint8_t *k_c
     const bool wide = head_dim > 128;
     const int rows = wide || dtype == FP8BLK_F32 ? 128 : 256, tile = rows / 2, group = q_heads / kv_heads;
     static_assert(ChunkShape<1, false>::U == 256 && ChunkShape<1, true>::U == 128 && ChunkShape<2, false>::U == 128 &&
-                      ChunkShape<2, true>::U == 128 && ChunkShape<1, false>::TL == 128 && ChunkShape<2, false>::TL == 64,
+                      ChunkShape<2, true>::U == 128 && ChunkShape<1, false>::T == 128 && ChunkShape<2, false>::T == 64,
                   "row tiles and tiles");
     // What the kernel counts in 32 bits: rows times heads of a group, row tiles and tiles on one line, list entries.
     const int64_t tiles = (static_cast<int64_t>(max_blocks) * block_tokens + tile - 1) / tile + 1;

@@ -3,7 +3,8 @@
 // cores.
 //
 // For one request and cache head, a tile of 128 query rows (row = new token x
-// query head of the group) against a tile of 64 tokens:
+// query head of the group) against a tile of T = 128 tokens (64 where there is one
+// product only):
 //   S[r][t] = sum_d q[r][d] k[t][d]                    (first MMA, kind::f16)
 //   a = S s_k(t) c_r,   w = 2^(a + e_t + K - R_r)      (e_t: exponent of s_v(t))
 //   O[r][d] += sum_t w[r][t] v[t][d]                   (second MMA, w out of tensor memory)
@@ -40,10 +41,11 @@
 // in the workspace, which a second kernel joins, in CTA order (deterministic, no
 // counters).
 //
-// Each product has two score buffers: the next tile's scores are there when a
-// tile's softmax ends, and its sums and the scores after the next run beside the
-// next softmax.  (With tiles of 128 tokens and one buffer each product waited for
-// its own two MMAs: 6400 cycles a pair of tiles, 2600 of them softmax.)
+// Two products take turns: while one's softmax runs, the other's MMAs do.  The
+// second MMA starts on the first half of a tile's weights.  (Tiles of 64 tokens and
+// two score buffers a product cost more instructions than they hid latency: 2.3 ms
+// for the last case below.)  One product has two score buffers of 64 tokens: the
+// next scores are there when a softmax ends.
 //
 // Roles (640 threads, one CTA per SM): warps 0-3 softmax (TMEM lane = row), warps
 // 4-7 softmax of the unit's second 128 rows, or f32's sums, warps 8-15 convert q, K
@@ -102,24 +104,24 @@ struct ChunkShape {
     static constexpr bool SUMS = PL == 2;               // products of a tile are added to the sums outside the tensor cores
     static constexpr int NS = WIDE || SUMS ? 1 : 2;     // 128-row products of a unit
     static constexpr int U = NS * 128;                  // rows of a unit
-    static constexpr int T = 64;                        // tokens of a tile
-    static constexpr int TL = U / 2, kPer = TL / T;     // tokens of a tile of the list, tiles of those
+    static constexpr int T = U / 2;                     // tokens of a tile
+    static constexpr int kDeep = NS == 1 ? 2 : 1;       // score buffers of a product
     static constexpr int kBlocks = WIDE ? 4 : 2;        // 64-wide column blocks of a head
     static constexpr int kSlot = T * kBlocks * 128;     // K or V of a tile as f16: 16 or 32 KiB
-    static constexpr int kSlots = WIDE ? 1 : 3;         // of K, and as many of V
+    static constexpr int kSlots = WIDE ? 1 : NS == 2 ? 2 : 3;  // of K, and as many of V
     static constexpr int kRaw = kSlot / 2;              // ... of the codes as they are: copied ahead
-    static constexpr int kRaws = !WIDE ? 6 : PL == 1 ? 4 : 1;  // of K and V in turn
+    static constexpr int kRaws = NS == 2 ? 1 : !WIDE ? 6 : PL == 1 ? 4 : 1;  // of K and V in turn
     static constexpr int kEach = kSlot / (32 * 256);    // groups of sixteen codes of a converting thread
     static constexpr int kQPlane = 128 * kBlocks * 128;  // one plane of 128 rows
     static constexpr int kQ = NS * PL * kQPlane;
     static constexpr size_t kSmem = 1024 + kQ + 2 * kSlots * kSlot + kRaws * kRaw;
     static constexpr int kGranules = T / 16;            // scales of a tile
-    // Tensor memory, in columns: scores (and the weights, in their place), two buffers of a product; f32's product of a
-    // tile (half of a wide head at a time); the sums.
+    // Tensor memory, in columns: scores (and the weights, in their place), of two products or in two buffers of one; f32's
+    // product of a tile (half of a wide head at a time); the sums.
     static constexpr int kProductCol = 128, kSumCol = 256;
     static constexpr int kHalves = SUMS && WIDE ? 2 : 1;
     static constexpr int kIssuers = NS;                 // warps that issue MMAs, one a product
-    static_assert(NS * 2 * T <= 256, "tensor memory");
+    static_assert(NS * kDeep * T <= 256, "tensor memory");
 };
 
 // One unit's tiles in a CTA's range.
@@ -134,12 +136,12 @@ constexpr int kChStarts = 1, kChEnds = 2, kChTwo = 4, kChStop = 8;  // first and
 struct ChunkShared {
     // Whoever waits on a barrier is never a whole turn of it behind: a wait could not tell the next phase but one from
     // its own.  So what a role may skip or be late for goes by the unit's or the score buffer's parity.
-    uint64_t k_full[4], k_free[4], v_full[4], v_free[4], s_full[4], p_full[4], o_done[2], info_full[kChInfo];
+    uint64_t k_full[4], k_free[4], v_full[4], v_free[4], s_full[2], p_half[2], p_full[2], o_done[2], info_full[kChInfo];
     uint64_t q_full[2], values_done[2], unit_done[2], q_free, mma_done[2];
     uint64_t factor_full[kChInfo], last_full[2], product_free;  // f32's sums
     uint64_t unit_full[kChUnits], unit_free[kChUnits];
-    float4 info[kChInfo][4];     // per sixteen tokens: k scale (NaN if not finite), exponent of the v scale, its signed mantissa
-    int info_kind[kChInfo];      // of a tile's scales: 0 all the same, 1 several, 2 a negative k scale, or a v scale that is no (positive) power of two
+    float4 info[kChInfo][8];     // per sixteen tokens: k scale (NaN if not finite), exponent of the v scale, its signed mantissa
+    int info_kind[kChInfo];      // of a tile's scales: 0 one per 64 tokens, 1 several, 2 a negative k scale, or a v scale that is no (positive) power of two
     ChunkUnit units[kChUnits];
     float qs[2][256];            // per row: what a score is times |s_k| of
     float factor[kChInfo][128];  // f32: what the sums so far are times, per row of a tile
@@ -196,12 +198,12 @@ struct ChunkList {
         q.bad = off || len < 0;
         q.rows = off ? 0 : static_cast<int>(rows);
         q.len = max(len, 0);
-        q.tiles = min(q.len / Sh::TL + (q.len % Sh::TL != 0), a.max_tiles);
+        q.tiles = min(q.len / Sh::T + (q.len % Sh::T != 0), a.max_tiles);
         const int flat = q.rows * a.group;
         q.row_tiles = flat / Sh::U + (flat % Sh::U != 0);
         // The first row's position, no further than the table's end (all tiles are seen from there on).
-        const int p = min(max(q.len - q.rows, 0), a.max_tiles * Sh::TL);
-        q.a = static_cast<int>((static_cast<int64_t>(p) * a.group + Sh::U - 1) / Sh::TL);
+        const int p = min(max(q.len - q.rows, 0), a.max_tiles * Sh::T);
+        q.a = static_cast<int>((static_cast<int64_t>(p) * a.group + Sh::U - 1) / Sh::T);
         q.last = flat - (q.row_tiles - 1) * Sh::U > 128 ? kFull : 1;
         return q;
     }
@@ -251,9 +253,8 @@ __device__ __forceinline__ void ch_plan(const ChunkArgs &a, ChunkShared &sh) {
         x.s = s;
         x.row0 = row_tile * Sh::U;
         x.head = head;
-        // (In tiles of the kernel; the list's last one may lie past the request's end with its second half.)
-        x.j0 = max(e0 - 1, 0) * Sh::kPer;
-        x.tiles = min((e1 - 1) * Sh::kPer, q.len / Sh::T + (q.len % Sh::T != 0)) - x.j0;
+        x.j0 = max(e0 - 1, 0);
+        x.tiles = e1 - 1 - x.j0;
         x.flags = (e0 == 0 ? kChStarts : 0) | (e1 == tiles + 1 ? kChEnds : 0) | (weight == 2 ? kChTwo : 0);
         mbar_arrive(smem_addr(&sh.unit_full[slot]));
         if (left <= 0) {
@@ -632,7 +633,7 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
                 }
                 // (Tokens past the request's end take any scale.)
                 const bool odd = __any_sync(0xFFFFFFFFu, here && (f.x < 0.f || f.z != 1.f));
-                const float kf = __shfl_sync(0xFFFFFFFFu, f.x, (j - first) * G), vf = __shfl_sync(0xFFFFFFFFu, f.y, (j - first) * G);
+                const float kf = __shfl_sync(0xFFFFFFFFu, f.x, lane & ~3), vf = __shfl_sync(0xFFFFFFFFu, f.y, lane & ~3);  // of the 64 tokens
                 const bool same = __all_sync(0xFFFFFFFFu, !here || (f.x == kf && f.y == vf));
                 __syncwarp();
                 if (lane == 0) {
@@ -708,7 +709,7 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
     int products = 0;              // products of the second kind (f32, wide: two a tile)
     // Scores of the next tile against K, the second plane's first.  end: q is read.
     auto scores = [&](bool end) {
-        const int slot = nk % kSlots, buf = 2 * i + (ms & 1);
+        const int slot = nk % kSlots, buf = Sh::NS == 1 ? ms & 1 : i;
         if (!wait(sh.k_full[slot], static_cast<uint32_t>(nk / kSlots) & 1u)) return;
         stores_seen();
         if (ch_elect()) {
@@ -731,31 +732,52 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
         ++ms;
         any = true;
     };
-    // The next tile's weights times V.  They lie where its scores were and the scores after the next will be: only MMAs of
-    // one shape are sure to run in the order of their issue, so the end of these is waited for.
+    // The next tile's weights times V.  They lie where its scores were and other scores will be: only MMAs of one shape are
+    // sure to run in the order of their issue.  So with two products the sums have 128 columns as the scores do (whatever
+    // lies past head_dim), and with one, whose next scores go elsewhere, the end of these is waited for.
     auto sums = [&](bool acc) {
-        const int slot = nv % kSlots, buf = 2 * i + (mv & 1);
-        if (!wait(sh.v_full[slot], static_cast<uint32_t>(nv / kSlots) & 1u) || !wait(sh.p_full[buf], static_cast<uint32_t>(mv >> 1) & 1u)) return;
+        const int slot = nv % kSlots, buf = Sh::NS == 1 ? mv & 1 : i;
+        const uint32_t ph = static_cast<uint32_t>(Sh::NS == 1 ? mv >> 1 : mv) & 1u;
+        if (!wait(sh.v_full[slot], static_cast<uint32_t>(nv / kSlots) & 1u)) return;
+        if (!(Sh::NS == 2 ? wait(sh.p_half[buf], ph) : wait(sh.p_full[buf], ph))) return;
         stores_seen();
         const uint32_t p0 = tmem + static_cast<uint32_t>(buf * T);
         const uint64_t v = v_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
+        if constexpr (Sh::NS == 2) {
+            const uint32_t d = tmem + static_cast<uint32_t>(Sh::kSumCol + i * 128);
 #pragma unroll 1
-        for (int h = 0; h < Sh::kHalves; ++h) {
-            if (Sh::SUMS && products > 0 && !wait(sh.product_free, static_cast<uint32_t>(products - 1) & 1u)) return;
-            if (ch_elect()) {
-                const uint32_t d = tmem + static_cast<uint32_t>(Sh::SUMS ? Sh::kProductCol : Sh::kSumCol + i * 128);
-                const uint32_t idesc = ch_idesc(Sh::kHalves == 1 ? a.head_dim : h == 0 ? 128 : a.head_dim - 128, true);
+            for (int h = 0; h < 2; ++h) {
+                if (h == 1 && !wait(sh.p_full[buf], ph)) return;
+                if (ch_elect()) {
 #pragma unroll 1
-                for (int p = PL - 1; p >= 0; --p)
-#pragma unroll 1
-                    for (int s = 0; s < T / 16; ++s)
-                        ch_mma_ts(d, p0 + (PL == 1 ? 8 * s : 32 * (s >> 1) + 16 * p + 8 * (s & 1)),
-                                  v + h * (2 * T * 128 / 16) + s * (16 * 128 / 16), idesc, (!Sh::SUMS && acc) || p + 1 < PL || s > 0);
-                t8_commit(smem_addr(&sh.o_done[i]));
-                if (h + 1 == Sh::kHalves) t8_commit(smem_addr(&sh.v_free[slot]));
+                    for (int s = 4 * h; s < 4 * h + 4; ++s)
+                        ch_mma_ts(d, p0 + 8 * s, v + s * (16 * 128 / 16), ch_idesc(128, true), acc || s > 0);
+                    if (h == 1) {
+                        t8_commit(smem_addr(&sh.o_done[i]));
+                        t8_commit(smem_addr(&sh.v_free[slot]));
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            if (!wait(sh.o_done[i], static_cast<uint32_t>(products++) & 1u)) return;
+        } else {
+#pragma unroll 1
+            for (int h = 0; h < Sh::kHalves; ++h) {
+                if (Sh::SUMS && products > 0 && !wait(sh.product_free, static_cast<uint32_t>(products - 1) & 1u)) return;
+                if (ch_elect()) {
+                    const uint32_t d = tmem + static_cast<uint32_t>(Sh::SUMS ? Sh::kProductCol : Sh::kSumCol);
+                    const uint32_t idesc = ch_idesc(Sh::kHalves == 1 ? a.head_dim : h == 0 ? 128 : a.head_dim - 128, true);
+#pragma unroll 1
+                    for (int p = PL - 1; p >= 0; --p)
+#pragma unroll 1
+                        for (int s = 0; s < T / 16; ++s)
+                            ch_mma_ts(d, p0 + (PL == 1 ? 8 * s : 32 * (s >> 1) + 16 * p + 8 * (s & 1)),
+                                      v + h * (2 * T * 128 / 16) + s * (16 * 128 / 16), idesc, (!Sh::SUMS && acc) || p + 1 < PL || s > 0);
+                    t8_commit(smem_addr(&sh.o_done[0]));
+                    if (h + 1 == Sh::kHalves) t8_commit(smem_addr(&sh.v_free[slot]));
+                }
+                __syncwarp();
+                if (!wait(sh.o_done[0], static_cast<uint32_t>(products++) & 1u)) return;
+            }
         }
         ++nv;
         ++mv;
@@ -779,9 +801,9 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
             continue;
         }
 #pragma unroll 1
-        for (int j = -2; ok && j < tiles; ++j) {
+        for (int j = -Sh::kDeep; ok && j < tiles; ++j) {
             if (j >= 0) sums(j > 0);
-            if (ok && j + 2 < tiles) scores(j + 3 == tiles);
+            if (ok && j + Sh::kDeep < tiles) scores(j + Sh::kDeep + 1 == tiles);
         }
         ++unit;
     }
@@ -960,7 +982,8 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
         const float qs = sh.qs[ub][local];
         float M = kChNone, R = kChNone, l = 0.f;  // maximum, the weights' reference less M, denominator
         for (int j = 0; ok && j < tiles; ++j, ++it, ++mine) {
-            const int at = it & (kChInfo - 1), buf = 2 * product + (mine & 1);
+            const int at = it & (kChInfo - 1), buf = Sh::NS == 1 ? mine & 1 : product;
+            const uint32_t ph = static_cast<uint32_t>(Sh::NS == 1 ? mine >> 1 : mine) & 1u;
             const uint32_t s_col = tmem + lanes + static_cast<uint32_t>(buf * kTile);
             ok = ch_wait(a, sh, sh.info_full[at], static_cast<uint32_t>(it / kChInfo) & 1u);
             const float4 *info = sh.info[at];
@@ -970,9 +993,7 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
             // beside its row's reference.
             const int kind = ok ? sh.info_kind[at] : 0;
             const bool careful = __any_sync(0xFFFFFFFFu, rel < kTile - 1 || fabsf(M) >= 0x1p19f) || kind == 2;
-            const float4 f0 = info[0];
-            const float k0 = f0.x * qs;
-            ok = ok && ch_wait(a, sh, sh.s_full[buf], static_cast<uint32_t>(mine >> 1) & 1u);
+            ok = ok && ch_wait(a, sh, sh.s_full[buf], ph);
             if (!ok) break;
             t8_fence_after();
             // The row's maximum, and the largest of the sixteens' maxima times their value scales, relative to the former.
@@ -985,9 +1006,14 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
                     for (int g = 0; g < 2; ++g) m16[c / 16 + g] = ch_max16(v + 16 * g);
                 });
                 if (kind == 0) {
-                    const float m = ceilf(fmaxf(ch_max3(m16[0], m16[1], m16[2]), m16[3]) * k0);
-                    top = fmaxf(top, m);
-                    ref = fmaxf(ref, (m - top) + f0.y);
+                    float m[kTile / 64];
+#pragma unroll
+                    for (int h = 0; h < kTile / 64; ++h) {
+                        m[h] = ceilf(fmaxf(ch_max3(m16[4 * h], m16[4 * h + 1], m16[4 * h + 2]), m16[4 * h + 3]) * (info[4 * h].x * qs));
+                        top = fmaxf(top, m[h]);
+                    }
+#pragma unroll
+                    for (int h = 0; h < kTile / 64; ++h) ref = fmaxf(ref, (m[h] - top) + info[4 * h].y);
                 } else {
 #pragma unroll
                     for (int g = 0; g < kTile / 16; ++g) {
@@ -1049,6 +1075,12 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
                     ch_st16(s_col + c, hi);
                     ch_st16(s_col + c + 16, lo);
                 }
+                if (Sh::NS == 2 && c == 32) {  // the first half is there
+                    ch_wait_st();
+                    t8_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.p_half[buf]));
+                }
             };
             auto by_sixteens = [&](auto slow) {
                 constexpr bool kSlow = decltype(slow)::value;
@@ -1069,19 +1101,18 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
             } else if (kind == 1) {
                 by_sixteens(std::false_type{});
             } else {
-                const float log = fmaxf(f0.y + lift, kChMinLog);
-                float sum = 0.f;
                 ch_columns<kTile, false>(s_col, [&](int c, float (&v)[32]) {
                     uint32_t hi[16], lo[16];
-                    sum += ch_weights<PL, false, 32>(v, c, rel, k0, base, log, 1.f, hi, lo);
+                    const float4 f = info[c / 64 * 4];
+                    const float log = fmaxf(f.y + lift, kChMinLog);
+                    l = fmaf(ch_weights<PL, false, 32>(v, c, rel, f.x * qs, base, log, 1.f, hi, lo), at_exp2(-log), l);
                     put(c, hi, lo);
                 });
-                l = fmaf(sum, at_exp2(-log), l);
             }
             ch_wait_st();
             // The sums of the tile before may still be under way: each phase is waited for, so that the last one cannot be
             // taken for the one before it.
-            if (!Sh::SUMS && j > 0) {
+            if (Sh::NS == 1 && !Sh::SUMS && j > 0) {
                 ok = ch_wait(a, sh, sh.o_done[product], static_cast<uint32_t>(mine - 1) & 1u);
                 if (!ok) break;
             }
@@ -1173,10 +1204,11 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
             mbar_init(smem_addr(&sh.k_free[i]), Sh::kIssuers);
             mbar_init(smem_addr(&sh.v_full[i]), kChConvertWarps);
             mbar_init(smem_addr(&sh.v_free[i]), Sh::kIssuers);
-            mbar_init(smem_addr(&sh.s_full[i]), 1);
-            mbar_init(smem_addr(&sh.p_full[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sh.s_full[i]), 1);
+            mbar_init(smem_addr(&sh.p_half[i]), 4);
+            mbar_init(smem_addr(&sh.p_full[i]), 4);
             mbar_init(smem_addr(&sh.o_done[i]), 1);
             mbar_init(smem_addr(&sh.q_full[i]), kChConvertWarps);
             mbar_init(smem_addr(&sh.values_done[i]), kChConvertWarps);
