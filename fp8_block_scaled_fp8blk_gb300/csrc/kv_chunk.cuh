@@ -305,27 +305,32 @@ __device__ __forceinline__ bool ch_unit(ChunkShared &sh, int u, int lane, ChunkU
 __host__ __device__ constexpr uint32_t ch_idesc(int n, bool mn_major) {
     return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24) | (mn_major ? 1u << 16 : 0u);
 }
-// 128-byte swizzle, 8-row groups 1024 bytes apart; `lead`: bytes between 64-element blocks along N of an MN-major operand.
-__device__ __forceinline__ uint64_t ch_desc(uint32_t saddr, uint32_t lead) {
-    uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-    d |= static_cast<uint64_t>(lead >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= 1ull << 46;
-    d |= 2ull << 61;
-    return d;
-}
-__device__ __forceinline__ void ch_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// Shared-memory descriptors, as two words: 128-byte swizzle, 8-row groups 1024 bytes apart.  `lead`: bytes between
+// 64-element blocks along N of an MN-major operand.  An offset inside shared memory adds to the low word, in 16 bytes.
+__device__ __forceinline__ uint32_t ch_desc(uint32_t saddr, uint32_t lead) { return ((saddr >> 4) & 0x3FFFu) | (lead >> 4) << 16; }
+constexpr uint32_t kChDescHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+// The MMAs, and the commit, of a converged warp: one thread issues, by a predicate
+// inside, so that operands are made once a warp, by the uniform units.  (Alone on an
+// SM an MMA takes 42 cycles to issue so, unrolled, 58 in a branch that one thread
+// takes, 86 there in a loop.)
+__device__ __forceinline__ void ch_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(kChDescHigh)
         : "memory");
 }
-__device__ __forceinline__ void ch_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void ch_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+        "{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xFFFFFFFF;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc)), "r"(kChDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ void ch_commit(uint64_t &bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(&bar))
         : "memory");
 }
 // 32 or 16 consecutive columns of this warp's lanes.
@@ -675,15 +680,8 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
 }
 
 // ------------------------------------------------------------------ MMAs
-// One thread of the (converged) warp.
-__device__ __forceinline__ bool ch_elect() {
-    uint32_t one;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-    return one != 0;
-}
-
-// The MMAs of a product.  The warp goes through the tiles together; one thread
-// issues.  Returns whether anything was issued.
+// The MMAs of a product.  The warp goes through the tiles together.  Returns
+// whether anything was issued.
 template <typename Sh>
 __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, uint32_t tmem_base, uint32_t sq, uint32_t k_slots,
                                          uint32_t v_slots, int product, int lane) {
@@ -693,7 +691,7 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
     // descriptors and addresses are made by the uniform units.)
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
     const int i = Sh::NS == 1 ? 0 : __shfl_sync(0xFFFFFFFFu, product, 0);
-    const uint64_t q_desc = ch_desc(sq + i * PL * Sh::kQPlane, 16), k_desc = ch_desc(k_slots, 16), v_desc = ch_desc(v_slots, T * 128);
+    const uint32_t q_desc = ch_desc(sq + i * PL * Sh::kQPlane, 16), k_desc = ch_desc(k_slots, 16), v_desc = ch_desc(v_slots, T * 128);
     const int steps = a.head_dim / 16;
     bool any = false, ok = true;
     auto wait = [&](uint64_t &bar, uint32_t parity) {
@@ -712,22 +710,32 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
         const int slot = nk % kSlots, buf = Sh::NS == 1 ? ms & 1 : i;
         if (!wait(sh.k_full[slot], static_cast<uint32_t>(nk / kSlots) & 1u)) return;
         stores_seen();
-        if (ch_elect()) {
-            const uint32_t d = tmem + static_cast<uint32_t>(buf * T);
-            const uint64_t k = k_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
+        const uint32_t d = tmem + static_cast<uint32_t>(buf * T);
 #pragma unroll 1
-            for (int p = PL - 1; p >= 0; --p) {
-                const uint64_t q = q_desc + static_cast<uint32_t>(p) * (Sh::kQPlane / 16);
+        for (int p = PL - 1; p >= 0; --p) {
+            uint32_t q = q_desc + static_cast<uint32_t>(p) * (Sh::kQPlane / 16), k = k_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
+            bool acc = p + 1 < PL;
 #pragma unroll 1
-                for (int s = 0; s < steps; ++s)
-                    ch_mma_ss(d, q + (s >> 2) * (128 * 128 / 16) + (s & 3) * 2, k + (s >> 2) * (T * 128 / 16) + (s & 3) * 2, qk_idesc,
-                              p + 1 < PL || s > 0);
+            for (int s = 0; s + 4 <= steps; s += 4) {  // 64 columns of a head
+                ch_mma_ss(d, q, k, qk_idesc, acc);
+                ch_mma_ss(d, q + 2, k + 2, qk_idesc, true);
+                ch_mma_ss(d, q + 4, k + 4, qk_idesc, true);
+                ch_mma_ss(d, q + 6, k + 6, qk_idesc, true);
+                acc = true;
+                q += 128 * 128 / 16;
+                k += T * 128 / 16;
             }
-            t8_commit(smem_addr(&sh.s_full[buf]));
-            t8_commit(smem_addr(&sh.k_free[slot]));
-            if (end) t8_commit(smem_addr(&sh.q_free));
+#pragma unroll 1
+            for (int s = steps & ~3; s < steps; ++s) {
+                ch_mma_ss(d, q, k, qk_idesc, acc);
+                acc = true;
+                q += 2;
+                k += 2;
+            }
         }
-        __syncwarp();
+        ch_commit(sh.s_full[buf]);
+        ch_commit(sh.k_free[slot]);
+        if (end) ch_commit(sh.q_free);
         ++nk;
         ++ms;
         any = true;
@@ -742,40 +750,39 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
         if (!(Sh::NS == 2 ? wait(sh.p_half[buf], ph) : wait(sh.p_full[buf], ph))) return;
         stores_seen();
         const uint32_t p0 = tmem + static_cast<uint32_t>(buf * T);
-        const uint64_t v = v_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16);
+        uint32_t v = v_desc + static_cast<uint32_t>(slot) * (Sh::kSlot / 16), p = p0;
         if constexpr (Sh::NS == 2) {
             const uint32_t d = tmem + static_cast<uint32_t>(Sh::kSumCol + i * 128);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 if (h == 1 && !wait(sh.p_full[buf], ph)) return;
-                if (ch_elect()) {
-#pragma unroll 1
-                    for (int s = 4 * h; s < 4 * h + 4; ++s)
-                        ch_mma_ts(d, p0 + 8 * s, v + s * (16 * 128 / 16), ch_idesc(128, true), acc || s > 0);
-                    if (h == 1) {
-                        t8_commit(smem_addr(&sh.o_done[i]));
-                        t8_commit(smem_addr(&sh.v_free[slot]));
-                    }
-                }
-                __syncwarp();
+                ch_mma_ts(d, p, v, ch_idesc(128, true), acc || h > 0);
+                ch_mma_ts(d, p + 8, v + 16 * 128 / 16, ch_idesc(128, true), true);
+                ch_mma_ts(d, p + 16, v + 32 * 128 / 16, ch_idesc(128, true), true);
+                ch_mma_ts(d, p + 24, v + 48 * 128 / 16, ch_idesc(128, true), true);
+                p += 32;
+                v += 64 * 128 / 16;
             }
+            ch_commit(sh.o_done[i]);
+            ch_commit(sh.v_free[slot]);
         } else {
 #pragma unroll 1
             for (int h = 0; h < Sh::kHalves; ++h) {
                 if (Sh::SUMS && products > 0 && !wait(sh.product_free, static_cast<uint32_t>(products - 1) & 1u)) return;
-                if (ch_elect()) {
-                    const uint32_t d = tmem + static_cast<uint32_t>(Sh::SUMS ? Sh::kProductCol : Sh::kSumCol);
-                    const uint32_t idesc = ch_idesc(Sh::kHalves == 1 ? a.head_dim : h == 0 ? 128 : a.head_dim - 128, true);
+                const uint32_t d = tmem + static_cast<uint32_t>(Sh::SUMS ? Sh::kProductCol : Sh::kSumCol);
+                const uint32_t idesc = ch_idesc(Sh::kHalves == 1 ? a.head_dim : h == 0 ? 128 : a.head_dim - 128, true);
 #pragma unroll 1
-                    for (int p = PL - 1; p >= 0; --p)
-#pragma unroll 1
-                        for (int s = 0; s < T / 16; ++s)
-                            ch_mma_ts(d, p0 + (PL == 1 ? 8 * s : 32 * (s >> 1) + 16 * p + 8 * (s & 1)),
-                                      v + h * (2 * T * 128 / 16) + s * (16 * 128 / 16), idesc, (!Sh::SUMS && acc) || p + 1 < PL || s > 0);
-                    t8_commit(smem_addr(&sh.o_done[0]));
-                    if (h + 1 == Sh::kHalves) t8_commit(smem_addr(&sh.v_free[slot]));
+                for (int x = PL - 1; x >= 0; --x) {  // the second plane's first
+                    constexpr uint32_t kStep = PL == 1 ? 16 : 32;  // columns of 32 tokens' weights; with two planes the second's follow the first's
+                    const uint32_t at = p + 16 * x;
+                    ch_mma_ts(d, at, v, idesc, (!Sh::SUMS && acc) || x + 1 < PL);
+                    ch_mma_ts(d, at + 8, v + 16 * 128 / 16, idesc, true);
+                    ch_mma_ts(d, at + kStep, v + 32 * 128 / 16, idesc, true);
+                    ch_mma_ts(d, at + kStep + 8, v + 48 * 128 / 16, idesc, true);
                 }
-                __syncwarp();
+                v += 2 * T * 128 / 16;
+                ch_commit(sh.o_done[0]);
+                if (h + 1 == Sh::kHalves) ch_commit(sh.v_free[slot]);
                 if (!wait(sh.o_done[0], static_cast<uint32_t>(products++) & 1u)) return;
             }
         }
@@ -1325,8 +1332,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
                 // Also after a wait that ran out: nothing is in flight at the end.
                 const int i = warp - kChMmaWarp;
                 if (ch_issue<Sh>(a, sh, tmem, smem_addr(sq), smem_addr(k_slots), smem_addr(v_slots), i, lane)) {
-                    if (ch_elect()) t8_commit(smem_addr(&sh.mma_done[i]));
-                    __syncwarp();
+                    ch_commit(sh.mma_done[i]);
                     (void)mbar_wait_bounded(smem_addr(&sh.mma_done[i]), 0);
                 }
             } else if (warp == kChPlanWarp && lane == 0) {
