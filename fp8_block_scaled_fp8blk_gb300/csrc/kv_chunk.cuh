@@ -47,6 +47,10 @@
 // for the last case below.)  One product has two score buffers of 64 tokens: the
 // next scores are there when a softmax ends.
 //
+// A unit with 128 rows or fewer gives every other of its tiles to the second
+// product, and the two are added up at its end (16 rows of 65536 tokens: 89 us with
+// one product at work).
+//
 // Roles (640 threads, one CTA per SM): warps 0-3 softmax (TMEM lane = row), warps
 // 4-7 softmax of the unit's second 128 rows, or f32's sums, warps 8-15 convert q, K
 // and V, warps 16 and 17 issue the MMAs (of the first and second 128 rows), warp 18
@@ -139,13 +143,14 @@ struct ChunkShared {
     uint64_t k_full[4], k_free[4], v_full[4], v_free[4], s_full[2], p_half[2], p_full[2], o_done[2], info_full[kChInfo];
     uint64_t q_full[2], values_done[2], unit_done[2], q_free, mma_done[2];
     uint64_t factor_full[kChInfo], last_full[2], product_free;  // f32's sums
+    uint64_t merged;             // the first product has taken the second's share of a unit
     uint64_t unit_full[kChUnits], unit_free[kChUnits];
     float4 info[kChInfo][8];     // per sixteen tokens: k scale (NaN if not finite), exponent of the v scale, its signed mantissa
     int info_kind[kChInfo];      // of a tile's scales: 0 one per 64 tokens, 1 several, 2 a negative k scale, or a v scale that is no (positive) power of two
     ChunkUnit units[kChUnits];
     float qs[2][256];            // per row: what a score is times |s_k| of
     float factor[kChInfo][128];  // f32: what the sums so far are times, per row of a tile
-    float last[2][3][128];       // f32: a unit's maxima, references and denominators
+    float last[2][3][128];       // f32, and a second product's share: a unit's maxima, references and denominators
     int vnan[2][256];            // first position whose value is NaN, per element
     int any_nan[2];
     int scan[kChThreads / 32];
@@ -489,9 +494,11 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
     int token[kEach];  // of the thread's groups, in a tile (T: none)
     uint32_t dst[kEach];
     auto group = [&](int i, int &t, int &c) {
-        const int g = tid + i * kThreads;
-        t = g < total ? g / per : Sh::T;
-        c = g < total ? g - t * per : 0;
+        // (Where a token has a multiple of four groups, four of them and the same of the next token go to eight lanes: their
+        // stores then meet no bank twice.)
+        const int g = tid + i * kThreads, four = per & 3 ? 0 : per >> 2;
+        t = g >= total ? Sh::T : four ? (g / (2 * per) << 1) + (g >> 2 & 1) : g / per;
+        c = g >= total ? 0 : four ? (g & 3) + (g / 8 % four << 2) : g - t * per;
         return (c >> 2) * (Sh::T * 128) + t * 128 + (((2 * (c & 3)) ^ (t & 7)) << 4);
     };
     int from[kEach];   // ... their places in the block of a request's first tile
@@ -554,6 +561,15 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
                              : "memory");
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
+            if (warp == 1 && (n_copy & 1) == 0) {
+                // Into L2: the blocks of the tile four further on, a lane for each sixteen tokens.
+                const int of = (j_copy + 4 - ahead) * G + lane % G;
+                const int b0 = __shfl_sync(0xFFFFFFFFu, id, of & 31), b1 = __shfl_sync(0xFFFFFFFFu, id_next, of & 31), b = of < 32 ? b0 : b1;
+                if (lane < G && (16 * lane & (block - 1)) == 0 && static_cast<uint32_t>(b) < n_blocks) {
+                    bulk_prefetch_l2(k_head + b * id_bytes, static_cast<uint32_t>(block * a.head_dim));
+                    bulk_prefetch_l2(v_head + b * id_bytes, static_cast<uint32_t>(block * a.head_dim));
+                }
+            }
             j_copy += n_copy & 1;
             ++n_copy;
             to_copy = n_copy % Sh::kRaws == 0 ? smem_addr(mine) : to_copy + Sh::kRaw;
@@ -691,7 +707,8 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
     // descriptors and addresses are made by the uniform units.)
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
     const int i = Sh::NS == 1 ? 0 : __shfl_sync(0xFFFFFFFFu, product, 0);
-    const uint32_t q_desc = ch_desc(sq + i * PL * Sh::kQPlane, 16), k_desc = ch_desc(k_slots, 16), v_desc = ch_desc(v_slots, T * 128);
+    uint32_t q_desc = 0;
+    const uint32_t k_desc = ch_desc(k_slots, 16), v_desc = ch_desc(v_slots, T * 128);
     const int steps = a.head_dim / 16;
     bool any = false, ok = true;
     auto wait = [&](uint64_t &bar, uint32_t parity) {
@@ -794,19 +811,32 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
         const int two = __shfl_sync(0xFFFFFFFFu, w.flags & kChTwo, 0), tiles = __shfl_sync(0xFFFFFFFFu, w.tiles, 0);
         if (tiles == 0 || !ok) continue;
         if (!wait(sh.q_full[unit & 1], static_cast<uint32_t>(unit >> 1) & 1u)) continue;
-        if (i == 1 && !two) {
-            // No rows: each slot is given back once it has been filled.
-#pragma unroll 1
-            for (int j = 0; j < tiles && wait(sh.k_full[nk % kSlots], static_cast<uint32_t>(nk / kSlots) & 1u); ++j, ++nk) {
+        if (Sh::NS == 2 && !two) {
+            // Every other tile; the slots of the others are given back once they have been filled.
+            q_desc = ch_desc(sq, 16);
+            auto skip = [&]() {
+                if (!wait(sh.k_full[nk % kSlots], static_cast<uint32_t>(nk / kSlots) & 1u)) return;
                 if (lane == 0) mbar_arrive(smem_addr(&sh.k_free[nk % kSlots]));
-                if (!wait(sh.v_full[nv % kSlots], static_cast<uint32_t>(nv / kSlots) & 1u)) break;
+                ++nk;
+                if (!wait(sh.v_full[nv % kSlots], static_cast<uint32_t>(nv / kSlots) & 1u)) return;
                 if (lane == 0) mbar_arrive(smem_addr(&sh.v_free[nv % kSlots]));
                 ++nv;
+            };
+            if (i == 1) {
+                skip();
+                if (tiles == 1 && lane == 0) mbar_arrive(smem_addr(&sh.q_free));
             }
-            if (lane == 0) mbar_arrive(smem_addr(&sh.q_free));
+            if (ok && i < tiles) scores(i + 2 >= tiles);
+#pragma unroll 1
+            for (int j = i; ok && j < tiles; j += 2) {
+                sums(j >= 2);
+                if (ok && j + 1 < tiles) skip();
+                if (ok && j + 2 < tiles) scores(j + 4 >= tiles);
+            }
             ++unit;
             continue;
         }
+        q_desc = ch_desc(sq + i * PL * Sh::kQPlane, 16);
 #pragma unroll 1
         for (int j = -Sh::kDeep; ok && j < tiles; ++j) {
             if (j >= 0) sums(j > 0);
@@ -834,17 +864,32 @@ struct ChunkRow {
     }
 };
 
-// Writes a unit's row out: its outputs, or its part of them.
+// What a product has of a row: the sums' columns, their maximum, reference and
+// denominator.
+struct ChunkSums {
+    uint32_t col;
+    float M, R, l;
+    // The sums are 2^-up times what they stand for, relative to 2^top: that, in two factors, since it may leave the range
+    // of one.
+    __device__ __forceinline__ void factors(float top, float &u1, float &u2) const {
+        const float up = R > kChNone ? R - static_cast<float>(kChLift) + (M - top) : 0.f, up1 = fminf(fmaxf(up, -120.f), 120.f);
+        u1 = at_exp2(up1);
+        u2 = at_exp2(fminf(fmaxf(up - up1, -120.f), 120.f));
+    }
+};
+
+// Writes a unit's row out: its outputs, or its part of them; of both products'
+// sums if `both`.
 template <typename Sh, typename T>
 __device__ __forceinline__ void ch_finish(const ChunkArgs &a, const ChunkUnit &w, ChunkShared &sh, int unit, const ChunkRow &row, int local,
-                                          uint32_t o_col, float M, float R, float l, bool ok) {
+                                          const ChunkSums &x, const ChunkSums &y, bool both, bool ok) {
     const float nanf = __int_as_float(0x7FC00000);
     const int ub = unit & 1;
     // The converters' word on what is NaN.
     ok = ok && ch_wait(a, sh, sh.values_done[ub], static_cast<uint32_t>(unit >> 1) & 1u);
     const bool starts = w.flags & kChStarts, whole = starts && (w.flags & kChEnds);
-    const float up = R > kChNone ? R - static_cast<float>(kChLift) : 0.f;  // sums are 2^-up times what they stand for
-    float f = 1.f;
+    const float M = both ? fmaxf(x.M, y.M) : x.M;
+    float l = both ? x.l * at_exp2(x.M - M) + y.l * at_exp2(y.M - M) : x.l, f = 1.f;
     if (!ok) l = nanf;
     if (whole) {
         f = l == 0.f ? 0.f : 1.f / l;
@@ -857,24 +902,33 @@ __device__ __forceinline__ void ch_finish(const ChunkArgs &a, const ChunkUnit &w
     }
     T *out = static_cast<T *>(a.out) + row.out;
     const bool nans = ok && sh.any_nan[ub] != 0;
-    // 2^up in two factors, since it may leave the range of one.
-    const float up1 = fminf(fmaxf(up, -120.f), 120.f);
-    const float u1 = at_exp2(up1), u2 = ok ? at_exp2(fminf(fmaxf(up - up1, -120.f), 120.f)) * f : nanf;
+    float u1, u2, t1, t2;
+    x.factors(M, u1, u2);
+    y.factors(M, t1, t2);
+    u2 *= ok ? f : nanf;
+    t2 *= f;
     part += static_cast<int64_t>(local) * a.head_dim;
 #pragma unroll 1
     for (int c = 0; c < a.head_dim; c += 16) {
         float v[16];
-        t8_ld16(o_col + c, v);
+        t8_ld16(x.col + c, v);
         at_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 16; ++x) v[x] = v[x] * u1 * u2;
+        for (int i = 0; i < 16; ++i) v[i] = v[i] * u1 * u2;
+        if (both) {
+            float z[16];
+            t8_ld16(y.col + c, z);
+            at_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = fmaf(z[i] * t1, t2, v[i]);
+        }
         if (nans) {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) v[x] = sh.vnan[ub][c + x] <= row.last ? nanf : v[x];
+            for (int i = 0; i < 16; ++i) v[i] = sh.vnan[ub][c + i] <= row.last ? nanf : v[i];
         }
         float lo[8], hi[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) lo[x] = v[x], hi[x] = v[8 + x];
+        for (int i = 0; i < 8; ++i) lo[i] = v[i], hi[i] = v[8 + i];
         if (!whole) {
             rope_store8(part + c, lo);
             rope_store8(part + c + 8, hi);
@@ -966,33 +1020,29 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
     constexpr int PL = Sh::PL, kTile = Sh::T;
     const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t o_col = tmem + lanes + static_cast<uint32_t>(Sh::kSumCol + product * 128);
-    const int local = product * 128 + wq * 32 + lane;
     int it = 0, unit = 0;   // all tiles of the CTA; units with tiles
     int mine = 0;           // tiles of this product (the buffers of a product go by its own count)
+    int shared = 0, shared0 = 0, shared1 = 0;  // units shared with the other product: all, and by parity
     bool ok = true;
     ChunkUnit w;
     for (int u = 0; ch_unit(sh, u, lane, w); ++u) {
+        const bool alone = Sh::NS == 1 || (w.flags & kChTwo) != 0;  // else the products share the rows and take every other tile
+        const int local = (alone ? product * 128 : 0) + wq * 32 + lane, step = alone ? 1 : 2;
         const ChunkRow row(a, w, local);
         const int ub = unit & 1, tiles = w.tiles;
         if (tiles == 0) {
-            if (!Sh::SUMS) ch_nothing<T>(a, row);
+            if (!Sh::SUMS && (alone || product == 0)) ch_nothing<T>(a, row);
             continue;
         }
-        // (Also without rows: no product's report runs ahead of the unit.)
         ok = ok && ch_wait(a, sh, sh.q_full[ub], static_cast<uint32_t>(unit >> 1) & 1u);
-        if (product == 1 && (w.flags & kChTwo) == 0) {  // no rows
-            it += tiles;
-            if (lane == 0) mbar_arrive(smem_addr(&sh.unit_done[ub]));
-            ++unit;
-            continue;
-        }
         const float qs = sh.qs[ub][local];
         float M = kChNone, R = kChNone, l = 0.f;  // maximum, the weights' reference less M, denominator
-        for (int j = 0; ok && j < tiles; ++j, ++it, ++mine) {
-            const int at = it & (kChInfo - 1), buf = Sh::NS == 1 ? mine & 1 : product;
+        const int j_first = alone ? 0 : product;
+        for (int j = j_first; ok && j < tiles; j += step, ++mine) {
+            const int at = (it + j) & (kChInfo - 1), buf = Sh::NS == 1 ? mine & 1 : product;
             const uint32_t ph = static_cast<uint32_t>(Sh::NS == 1 ? mine >> 1 : mine) & 1u;
             const uint32_t s_col = tmem + lanes + static_cast<uint32_t>(buf * kTile);
-            ok = ch_wait(a, sh, sh.info_full[at], static_cast<uint32_t>(it / kChInfo) & 1u);
+            ok = ch_wait(a, sh, sh.info_full[at], static_cast<uint32_t>((it + j) / kChInfo) & 1u);
             const float4 *info = sh.info[at];
             const int64_t t0 = static_cast<int64_t>(w.j0 + j) * kTile;
             const int rel = t0 > row.last ? -1 : static_cast<int>(row.last - t0 < kTile ? row.last - t0 : kTile);  // last column this row sees
@@ -1054,10 +1104,10 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
             const bool move = ref > R + kChSlack;
             const float factor = move && R > kChNone ? at_exp2(R - ref) : 1.f;  // of the sums so far
             if (Sh::SUMS) {
-                sh.factor[it & (kChInfo - 1)][local] = factor;
+                sh.factor[at][local] = factor;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.factor_full[it & (kChInfo - 1)]));
-            } else if (j > 0 && __any_sync(0xFFFFFFFFu, move)) {
+                if (lane == 0) mbar_arrive(smem_addr(&sh.factor_full[at]));
+            } else if (j > j_first && __any_sync(0xFFFFFFFFu, move)) {
                 ok = ch_wait(a, sh, sh.o_done[product], static_cast<uint32_t>(mine - 1) & 1u);
                 if (!ok) break;
                 t8_fence_after();
@@ -1127,20 +1177,36 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[buf]));
         }
-        if (Sh::SUMS) {
-            sh.last[ub][0][local] = M;
-            sh.last[ub][1][local] = R;
-            sh.last[ub][2][local] = l;
+        it += tiles;
+        if (!Sh::SUMS && j_first < tiles) ok = ok && ch_wait(a, sh, sh.o_done[product], static_cast<uint32_t>(mine - 1) & 1u);
+        t8_fence_after();
+        ChunkSums x = {o_col, M, R, ok ? l : __int_as_float(0x7FC00000)}, y = x;
+        if (Sh::SUMS || (!alone && product == 1)) {
+            const int r = wq * 32 + lane;
+            sh.last[ub][0][r] = x.M;
+            sh.last[ub][1][r] = x.R;
+            sh.last[ub][2][r] = x.l;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.last_full[ub]));
+            // The sums stay as they are until the first product has taken them.
+            if (!Sh::SUMS) ok = ok && ch_wait(a, sh, sh.merged, static_cast<uint32_t>(shared) & 1u);
         } else {
-            ok = ok && ch_wait(a, sh, sh.o_done[product], static_cast<uint32_t>(mine - 1) & 1u);
-            t8_fence_after();
-            ch_finish<Sh, T>(a, w, sh, unit, row, local, o_col, M, R, l, ok);
+            if (!alone) {
+                ok = ok && ch_wait(a, sh, sh.last_full[ub], static_cast<uint32_t>((ub == 0 ? shared0 : shared1)) & 1u);
+                y = {o_col + 128, sh.last[ub][0][wq * 32 + lane], sh.last[ub][1][wq * 32 + lane], sh.last[ub][2][wq * 32 + lane]};
+            }
+            ch_finish<Sh, T>(a, w, sh, unit, row, local, x, y, !alone && tiles > 1, ok);
             t8_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sh.unit_done[ub]));
+            if (!alone && lane == 0) mbar_arrive(smem_addr(&sh.merged));
         }
+        if (!alone) {
+            ++shared;
+            if (ub == 0) ++shared0;
+            else ++shared1;
+        }
+        __syncwarp();
+        if (!Sh::SUMS && lane == 0) mbar_arrive(smem_addr(&sh.unit_done[ub]));
         ++unit;
     }
 }
@@ -1189,7 +1255,8 @@ __device__ __forceinline__ void ch_sums(const ChunkArgs &a, ChunkShared &sh, uin
         }
         ch_wait_st();
         ok = ok && ch_wait(a, sh, sh.last_full[ub], static_cast<uint32_t>(unit >> 1) & 1u);
-        ch_finish<Sh, T>(a, w, sh, unit, row, local, o_col, sh.last[ub][0][local], sh.last[ub][1][local], sh.last[ub][2][local], ok);
+        const ChunkSums x = {o_col, sh.last[ub][0][local], sh.last[ub][1][local], sh.last[ub][2][local]};
+        ch_finish<Sh, T>(a, w, sh, unit, row, local, x, x, false, ok);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.unit_done[ub]));
         ++unit;
@@ -1228,6 +1295,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
         mbar_init(smem_addr(&sh.last_full[0]), 4);
         mbar_init(smem_addr(&sh.last_full[1]), 4);
         mbar_init(smem_addr(&sh.product_free), 4);
+        mbar_init(smem_addr(&sh.merged), 4);
         for (int i = 0; i < kChUnits; ++i) {
             mbar_init(smem_addr(&sh.unit_full[i]), 1);
             mbar_init(smem_addr(&sh.unit_free[i]), (Sh::NS == 2 || Sh::SUMS ? 8 : 4) + kChConvertWarps + Sh::kIssuers);  // every warp that takes units
@@ -1363,8 +1431,13 @@ __global__ void __launch_bounds__(kChJoinRows * 32) kv_chunk_join_kernel(const C
     const int4 rows = a.heads[2 * b + 1];
     const int local = blockIdx.y * kChJoinRows + warp, r = h.y * U + local;
     if (r >= rows.y * a.group) return;  // (warps go their own ways from here on)
-    int parts = 2;
-    while (b + parts < grid && (a.heads[2 * (b + parts - 1)].w & 2) != 0) ++parts;
+    int parts = 2;  // x + 1, and on as long as a CTA's whole range is the unit's middle
+    for (bool on = true; on;) {
+        const int c = b + parts - 1 + lane;
+        const unsigned middle = __ballot_sync(0xFFFFFFFFu, c < grid - 1 && (a.heads[2 * c].w & 2) != 0);
+        on = middle == 0xFFFFFFFFu;
+        parts += on ? 32 : __ffs(~middle) - 1;
+    }
     const int64_t size = static_cast<int64_t>(U) * (a.head_dim + 2);
     auto part = [&](int p) { return a.partials + (static_cast<int64_t>(b + p) * 2 + (p == 0)) * size; };
     float M = kChNone;
