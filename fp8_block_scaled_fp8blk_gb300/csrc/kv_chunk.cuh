@@ -78,7 +78,6 @@ constexpr int kChLift = 6;               // K: a row's largest weight is below 2
 constexpr int kChSlack = 8;              // ... which it does when a tile passes it by more than 2^8
 constexpr float kChNone = -3.0e38f;      // maximum of a row that has seen nothing
 constexpr float kChMinLog = -60.f;       // weights under value scales smaller than 2^-60 of their row's are zero in f16 anyway
-constexpr int kChJoinRows = 8;           // rows a CTA of the join takes
 constexpr size_t kChHeaderBytes = kChMaxGrid * 2 * sizeof(int4);
 constexpr int kChNoNan = 0x7FFFFFFF;
 
@@ -137,6 +136,17 @@ struct ChunkUnit {
 };
 constexpr int kChStarts = 1, kChEnds = 2, kChTwo = 4, kChStop = 8;  // first and last tile are here; two products have rows; no unit
 
+// One request as the kernel takes it.  Tiles of the list are half as many tokens
+// as a row tile has rows, so row tile i's last row sees the tiles
+// 0 .. floor((a + 2 i) / g), as far as there are any.
+struct ChunkSeq {
+    int first, rows, len;  // rows 0: nothing to do
+    int tiles;             // of the whole cache
+    int row_tiles;
+    int a, last;           // last: list entries of a tile of the last row tile
+    bool bad;
+};
+
 struct ChunkShared {
     // Whoever waits on a barrier is never a whole turn of it behind: a wait could not tell the next phase but one from
     // its own.  So what a role may skip or be late for goes by the unit's or the score buffer's parity.
@@ -155,7 +165,8 @@ struct ChunkShared {
     int any_nan[2];
     int scan[kChThreads / 32];
     int cut[2];                  // this CTA's range
-    int at[4];                   // its first request, row tile, head and slot
+    int at[2][4];                // where its cuts lie: request (the first cut also: row tile, head and slot)
+    ChunkSeq seq;                // the first one's request
     int abort;
     uint32_t tmem;
 };
@@ -180,16 +191,6 @@ __device__ __noinline__ int ch_floor_sum(uint32_t a, uint32_t g, uint32_t n) {
     return static_cast<int>(all / 2);
 }
 
-// One request as the kernel takes it.  Tiles of the list are half as many tokens
-// as a row tile has rows, so row tile i's last row sees the tiles
-// 0 .. floor((a + 2 i) / g), as far as there are any.
-struct ChunkSeq {
-    int first, rows, len;  // rows 0: nothing to do
-    int tiles;             // of the whole cache
-    int row_tiles;
-    int a, last;           // last: list entries of a tile of the last row tile
-    bool bad;
-};
 template <typename Sh>
 struct ChunkList {
     static constexpr int kFull = Sh::U / 128;  // list entries of a tile of a full row tile
@@ -236,8 +237,8 @@ constexpr int kChSmallCut = 2;
 template <typename Sh>
 __device__ __forceinline__ void ch_plan(const ChunkArgs &a, ChunkShared &sh) {
     const ChunkList<Sh> list{a};
-    int s = sh.at[0], row_tile = sh.at[1], head = sh.at[2], e0 = sh.at[3], left = sh.cut[1] - sh.cut[0];
-    ChunkSeq q = list.seq(s);
+    int s = sh.at[0][0], row_tile = sh.at[0][1], head = sh.at[0][2], e0 = sh.at[0][3], left = sh.cut[1] - sh.cut[0];
+    ChunkSeq q = sh.seq;
     const bool first_cut = e0 != 0;
     for (int u = 0;; ++u) {
         const int slot = u & (kChUnits - 1);
@@ -423,7 +424,7 @@ __device__ __forceinline__ void ch_queries(const ChunkArgs &a, const ChunkUnit &
     const int d0 = (lane % L) * 8, rows = w.flags & kChTwo ? 256 : 128;
     const int flat = w.rows * a.group - w.row0;  // rows of the unit that exist
     const T *q = static_cast<const T *>(a.q) + w.first * a.q_stride + static_cast<int64_t>(w.head) * a.group * a.head_dim + d0;
-    const int r0 = warp * RW + lane / L;
+    const int r0 = warp * RW + lane / L, here = min(rows, flat);
     auto place = [&](int r) {
         return sq + (r >> 7) * (PL * Sh::kQPlane) + (d0 >> 6) * (128 * 128) + (r & 127) * 128 + ((((d0 >> 3) & 7) ^ (r & 7)) << 4);
     };
@@ -434,48 +435,61 @@ __device__ __forceinline__ void ch_queries(const ChunkArgs &a, const ChunkUnit &
         const T *x = q + token * a.q_stride + head * a.head_dim;
         const uint32_t dst = smem_addr(place(r)), bytes = r < flat && d0 < a.head_dim ? 16 : 0;  // the rest is filled with zeros
         if (bytes == 0) x = static_cast<const T *>(a.q);
+        if (r >= flat && lane % L == 0) qs[r] = 1.f;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(x), "r"(bytes) : "memory");
         if (PL == 2) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + Sh::kQPlane), "l"(x + (bytes ? 4 : 0)), "r"(bytes) : "memory");
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    // (Two of a warp's turns in one, so that one's loads and reductions cover the other's.)
 #pragma unroll 1
-    for (int r = r0; r < rows; r += kStride) {
-        uint8_t *at = place(r);
-        float x[8];
-        if constexpr (PL == 2) {
-            const float4 u = *reinterpret_cast<const float4 *>(at), v = *reinterpret_cast<const float4 *>(at + Sh::kQPlane);
-            x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-        } else {
-            rope_load8(reinterpret_cast<const __nv_bfloat16 *>(at), x);
-        }
-        uint32_t top = 0;
+    for (int rb = warp * RW; rb < here; rb += 2 * kStride) {
+        float x[2][8];
+        uint32_t top[2] = {0, 0};
+        uint8_t *const at[2] = {place(rb + lane / L), place(rb + lane / L + kStride)};
+        const bool two = rb + kStride < here;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (PL == 2) x[i] = fmaf(x[i], a.c, x[i] * a.c_low);  // the scale per value, rounded at random
-            top = max(top, __float_as_uint(fabsf(x[i])));
-        }
+        for (int b = 0; b < 2; ++b) {
+            if constexpr (PL == 2) {
+                const float4 u = *reinterpret_cast<const float4 *>(at[b & two]), v = *reinterpret_cast<const float4 *>(at[b & two] + Sh::kQPlane);
+                x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w, x[b][4] = v.x, x[b][5] = v.y, x[b][6] = v.z, x[b][7] = v.w;
+            } else {
+                rope_load8(reinterpret_cast<const __nv_bfloat16 *>(at[b & two]), x[b]);
+            }
 #pragma unroll
-        for (int d = L / 2; d; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        const bool good = top < 0x7F800000u;
-        int e = 0;  // the row's largest times 2^e is in [2^14, 2^15)
-        if (good && top != 0) e = top >= 0x800000u ? 14 + 127 - static_cast<int>(top >> 23) : 14 + 149 - (31 - __clz(top));
-        const int e1 = e >> 1, e2 = e - e1;
-        if (lane % L == 0)
-            qs[r] = good ? ch_pow2(-e1) * (PL == 2 ? 1.f : fabsf(a.c)) * ch_pow2(-e2) : __int_as_float(0x7FC00000);
-        // (bf16: the sign of the softmax scale goes here.)
-        const float f1 = good ? ch_pow2(e1) : 0.f, f2 = PL == 1 && a.c < 0.f ? -ch_pow2(e2) : ch_pow2(e2);
-        uint32_t h[4], l[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float u = good ? x[2 * i] * f1 * f2 : 0.f, v = good ? x[2 * i + 1] * f1 * f2 : 0.f;
-            h[i] = ch_pack_f16(u, v);
-            if (PL == 2) {
-                const float2 f = ch_unpack_f16(h[i]);
-                l[i] = ch_pack_f16(u - f.x, v - f.y);
+            for (int i = 0; i < 8; ++i) {
+                if (PL == 2) x[b][i] = fmaf(x[b][i], a.c, x[b][i] * a.c_low);  // the scale per value, rounded at random
+                top[b] = max(top[b], __float_as_uint(fabsf(x[b][i])));
             }
         }
-        *reinterpret_cast<uint4 *>(at) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (PL == 2) *reinterpret_cast<uint4 *>(at + Sh::kQPlane) = make_uint4(l[0], l[1], l[2], l[3]);
+#pragma unroll
+        for (int d = L / 2; d; d >>= 1) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) top[b] = max(top[b], __shfl_xor_sync(0xFFFFFFFFu, top[b], d));
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const bool good = top[b] < 0x7F800000u;
+            int e = 0;  // the row's largest times 2^e is in [2^14, 2^15)
+            if (good && top[b] != 0) e = top[b] >= 0x800000u ? 14 + 127 - static_cast<int>(top[b] >> 23) : 14 + 149 - (31 - __clz(top[b]));
+            const int e1 = e >> 1, e2 = e - e1;
+            // (bf16: the sign of the softmax scale goes here.)
+            const float f1 = good ? ch_pow2(e1) : 0.f, f2 = PL == 1 && a.c < 0.f ? -ch_pow2(e2) : ch_pow2(e2);
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u = good ? x[b][2 * i] * f1 * f2 : 0.f, v = good ? x[b][2 * i + 1] * f1 * f2 : 0.f;
+                h[i] = ch_pack_f16(u, v);
+                if (PL == 2) {
+                    const float2 f = ch_unpack_f16(h[i]);
+                    l[i] = ch_pack_f16(u - f.x, v - f.y);
+                }
+            }
+            if (b == 1 && !two) continue;
+            if (lane % L == 0)
+                qs[rb + lane / L + b * kStride] = good ? ch_pow2(-e1) * (PL == 2 ? 1.f : fabsf(a.c)) * ch_pow2(-e2) : __int_as_float(0x7FC00000);
+            *reinterpret_cast<uint4 *>(at[b]) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (PL == 2) *reinterpret_cast<uint4 *>(at[b] + Sh::kQPlane) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
     }
 }
 
@@ -907,7 +921,7 @@ __device__ __forceinline__ void ch_finish(const ChunkArgs &a, const ChunkUnit &w
     y.factors(M, t1, t2);
     u2 *= ok ? f : nanf;
     t2 *= f;
-    part += static_cast<int64_t>(local) * a.head_dim;
+    part += local;  // (column by column: the warp's rows lie together)
 #pragma unroll 1
     for (int c = 0; c < a.head_dim; c += 16) {
         float v[16];
@@ -926,13 +940,13 @@ __device__ __forceinline__ void ch_finish(const ChunkArgs &a, const ChunkUnit &w
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = sh.vnan[ub][c + i] <= row.last ? nanf : v[i];
         }
-        float lo[8], hi[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) lo[i] = v[i], hi[i] = v[8 + i];
         if (!whole) {
-            rope_store8(part + c, lo);
-            rope_store8(part + c + 8, hi);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) __stcg(part + static_cast<int64_t>(c + i) * Sh::U, v[i]);
         } else if (row.valid) {
+            float lo[8], hi[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) lo[i] = v[i], hi[i] = v[8 + i];
             rope_store8(out + c, lo);
             rope_store8(out + c + 8, hi);
         }
@@ -1346,39 +1360,50 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
         // Every CTA's share is a few entries, so no two cuts inside a unit meet.
         const int grid = min(static_cast<int>(gridDim.x), max(total / 8, min(total, 1)));
         busy = static_cast<int>(blockIdx.x) < grid;
-        if (busy) {
-            const AttnSplit split(total, grid);
+        const AttnSplit split(total, max(grid, 1));
+        if (busy) {  // the requests that the two cuts lie in
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {
                 const int x = split.begin(blockIdx.x + e);
-                if (x == total) {
-                    if (tid == 0) sh.cut[e] = total;
-                } else if (from <= x && x < from + sum) {
-                    int here = from, s = r0;
-                    ChunkSeq q = list.seq(s);
+                if (from > x || x >= from + sum) continue;
+                int here = from, s = r0;
 #pragma unroll 1
-                    for (int n = list.entries(q); x >= here + n; n = list.entries(q)) {
-                        here += n;
-                        q = list.seq(++s);
-                    }
-                    int lo = 0, hi = q.row_tiles - 1;  // the row tile: the last one whose entries begin at or below x
+                for (int n = each == 1 ? sum : list.entries(list.seq(s)); x >= here + n; n = list.entries(list.seq(s))) {
+                    here += n;
+                    ++s;
+                }
+                sh.at[e][0] = s;
+                sh.at[e][1] = here;
+            }
+        }
+        __syncthreads();
+        if (busy && warp < 2) {  // warp e: cut e
+            const int x = split.begin(blockIdx.x + warp);
+            if (x == total) {
+                if (lane == 0) sh.cut[warp] = total;
+            } else {
+                const int s = sh.at[warp][0];
+                const ChunkSeq q = list.seq(s);
+                int here = sh.at[warp][1], lo = 0;  // the row tile: the last one whose entries begin at or below x
 #pragma unroll 1
-                    while (lo < hi) {
-                        const int mid = (lo + hi + 1) >> 1;
-                        if (list.before(q, mid) <= x - here) lo = mid;
-                        else hi = mid - 1;
-                    }
-                    here += list.before(q, lo);
-                    const int weight = list.weight(q, lo), slots = list.seen(q, lo) + 1;
-                    const int head = (x - here) / (weight * slots);
-                    int slot = ((x - here) - head * weight * slots) / weight;
-                    if (slot <= kChSmallCut) slot = 0;
-                    sh.cut[e] = here + (head * slots + slot) * weight;
-                    if (e == 0) {
-                        sh.at[0] = s;
-                        sh.at[1] = lo;
-                        sh.at[2] = head;
-                        sh.at[3] = slot;
+                for (int n = q.row_tiles; n > 1;) {
+                    const int step = (n + 31) / 32, i = lane * step;
+                    const int k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, i < n && list.before(q, lo + min(i, n - 1)) <= x - here));
+                    lo += k * step;
+                    n = min(step, n - k * step);
+                }
+                here += list.before(q, lo);
+                const int weight = list.weight(q, lo), slots = list.seen(q, lo) + 1;
+                const int head = (x - here) / (weight * slots);
+                int slot = ((x - here) - head * weight * slots) / weight;
+                if (slot <= kChSmallCut) slot = 0;
+                if (lane == 0) {
+                    sh.cut[warp] = here + (head * slots + slot) * weight;
+                    if (warp == 0) {
+                        sh.seq = q;
+                        sh.at[0][1] = lo;
+                        sh.at[0][2] = head;
+                        sh.at[0][3] = slot;
                     }
                 }
             }
@@ -1416,71 +1441,53 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Joins the parts of units that lie across CTAs.  CTA (x, y): rows [8 y, 8 y + 8)
-// of the unit that CTA x of the first kernel began and did not end (if there is
-// one); its parts lie with x, x + 1, .. as far as their ranges go on.  Warp r
-// weighs the parts of row r, then takes four elements a lane of its sums.
+// Joins the parts of units that lie across CTAs.  CTA (x, y): 32 rows and 64
+// columns of the unit that CTA x of the first kernel began and did not end (if there
+// is one); its parts lie with x, x + 1, .. as far as their ranges go on.  A warp has
+// eight columns, a lane a row: it weighs the row's parts, then adds up its columns',
+// in the parts' order.
 template <typename T, int U>
-__global__ void __launch_bounds__(kChJoinRows * 32) kv_chunk_join_kernel(const ChunkArgs a, int grid) {
-    __shared__ float weight[kChJoinRows][kChMaxGrid];
+__global__ void __launch_bounds__(256) kv_chunk_join_kernel(const ChunkArgs a, int grid) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
+    const int local = static_cast<int>(blockIdx.y) % (U / 32) * 32 + lane, c = static_cast<int>(blockIdx.y) / (U / 32) * 64 + warp * 8;
     grid_dependency_wait();
     grid_launch_dependents();
     const int4 h = a.heads[2 * b];
     if ((h.w & 1) == 0) return;
     const int4 rows = a.heads[2 * b + 1];
-    const int local = blockIdx.y * kChJoinRows + warp, r = h.y * U + local;
-    if (r >= rows.y * a.group) return;  // (warps go their own ways from here on)
+    const int r = h.y * U + local;
+    if (r - lane >= rows.y * a.group || c >= a.head_dim) return;  // (warps go their own ways from here on)
     int parts = 2;  // x + 1, and on as long as a CTA's whole range is the unit's middle
     for (bool on = true; on;) {
-        const int c = b + parts - 1 + lane;
-        const unsigned middle = __ballot_sync(0xFFFFFFFFu, c < grid - 1 && (a.heads[2 * c].w & 2) != 0);
+        const int x = b + parts - 1 + lane;
+        const unsigned middle = __ballot_sync(0xFFFFFFFFu, x < grid - 1 && (a.heads[2 * x].w & 2) != 0);
         on = middle == 0xFFFFFFFFu;
         parts += on ? 32 : __ffs(~middle) - 1;
     }
     const int64_t size = static_cast<int64_t>(U) * (a.head_dim + 2);
-    auto part = [&](int p) { return a.partials + (static_cast<int64_t>(b + p) * 2 + (p == 0)) * size; };
-    float M = kChNone;
-    bool nan = false;
-    for (int p = lane; p < parts; p += 32) M = fmaxf(M, __ldcg(part(p) + static_cast<int64_t>(U) * a.head_dim + local));
+    auto part = [&](int p) { return a.partials + (static_cast<int64_t>(b + p) * 2 + (p == 0)) * size + local; };
+    const int64_t at_m = static_cast<int64_t>(U) * a.head_dim;
+    float M = kChNone, l = 0.f, o[8] = {};
+#pragma unroll 8
+    for (int p = 0; p < parts; ++p) M = fmaxf(M, part(p)[at_m]);
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        const float *x = part(p);
+        const float f = at_exp2(x[at_m] - M);
+        l = fmaf(x[at_m + U], f, l);
+        x += static_cast<int64_t>(c) * U;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
-    float l = 0.f;
-    for (int p = lane; p < parts; p += 32) {
-        const float f = at_exp2(__ldcg(part(p) + static_cast<int64_t>(U) * a.head_dim + local) - M);
-        const float pl = __ldcg(part(p) + static_cast<int64_t>(U) * (a.head_dim + 1) + local);
-        weight[warp][p] = f;
-        l = fmaf(pl, f, l);
-        nan |= pl != pl;
+        for (int i = 0; i < 8; ++i) o[i] = fmaf(x[i * U], f, o[i]);
     }
-    // One order, one result.
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const float o = __shfl_xor_sync(0xFFFFFFFFu, l, d);
-        l = lane & d ? o + l : l + o;
-    }
-    nan = __any_sync(0xFFFFFFFFu, nan);
-    if (nan) l = __int_as_float(0x7FC00000);
-    __syncwarp();
+    if (r >= rows.y * a.group) return;
     int in_group;
     const int token = ch_token(a, r, in_group);
     const int64_t row = rows.x + token, head = static_cast<int64_t>(h.z) * a.group + in_group;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (lane == 0 && a.lse) a.lse[row * (static_cast<int64_t>(a.kv_heads) * a.group) + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
-    T *out = static_cast<T *>(a.out) + row * a.out_stride + head * a.head_dim;
-    for (int d = 4 * lane; d < a.head_dim; d += 128) {
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int p = 0; p < parts; ++p) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(part(p) + static_cast<int64_t>(local) * a.head_dim + d));
-            const float f = weight[warp][p];
-            o.x = fmaf(x.x, f, o.x);
-            o.y = fmaf(x.y, f, o.y);
-            o.z = fmaf(x.z, f, o.z);
-            o.w = fmaf(x.w, f, o.w);
-        }
-        at_store4(out + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    }
+    if (c == 0 && a.lse) a.lse[row * (static_cast<int64_t>(a.kv_heads) * a.group) + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= inv;
+    rope_store8(static_cast<T *>(a.out) + row * a.out_stride + head * a.head_dim + c, o);
 }
 
 }  // namespace fp8blk
