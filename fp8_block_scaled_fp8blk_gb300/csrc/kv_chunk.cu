@@ -17,7 +17,7 @@ static cudaError_t launch_chunk(const ChunkArgs &a, int grid, cudaStream_t strea
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     err = step_launch(kernel, dim3(static_cast<unsigned>(grid)), kChThreads, Sh::kSmem, stream, a);
     if (err != cudaSuccess) return err;
-    return step_launch(kv_chunk_join_kernel<T, Sh::U>, dim3(static_cast<unsigned>(grid), Sh::U / 32 * ((a.head_dim + 63) / 64)), 256, 0, stream,
+    return step_launch(kv_chunk_join_kernel<T, Sh::U>, dim3(static_cast<unsigned>(grid), kChJoinCtas), 256, 0, stream,
                        a, grid);
 }
 

@@ -69,6 +69,7 @@ namespace fp8blk {
 constexpr int kChThreads = 640;
 constexpr int kChConvertWarp = 8, kChConvertWarps = 8, kChMmaWarp = 16, kChPlanWarp = 18;
 constexpr int kChMaxGrid = 160;          // bound on CTAs: partial sums in the workspace
+constexpr int kChJoinCtas = 8;           // CTAs of the join for one of the first kernel
 constexpr int kChInfo = 8;               // tiles whose scales (and sums' factors) are held: more than K is ahead of the softmax
 constexpr int kChUnits = 4;              // units that are laid out ahead
 // Registers a thread of each role (of the 96 of the launch).
@@ -529,7 +530,11 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
     bool ok = true;
     ChunkUnit w;
     for (int u = 0; ch_unit(sh, u, lane, w); ++u) {
-        if (w.tiles == 0 || !ok) continue;
+        if (w.tiles == 0) continue;
+        if (!ok) {  // (nobody is left behind at the set-up's barrier)
+            asm volatile("bar.sync 4, %0;" ::"n"(kThreads) : "memory");
+            continue;
+        }
         const int ub = unit & 1, j1 = w.j0 + w.tiles;
         const int32_t *row = a.table + static_cast<int64_t>(w.s) * a.width;
         const int64_t head = static_cast<int64_t>(w.head) * block * a.head_dim;
@@ -605,7 +610,7 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
         ch_queries<Sh, T>(a, w, sq, sh.qs[ub], warp, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[ub]));
-        // One raw slot, which has come, as f16; then the copies that take its place.  The sum of V's values (at most 32 x 448)
+        // One raw slot, which has come, as f16 (the copies that take its place come behind the barrier's release).  The sum of V's values (at most 32 x 448)
         // is not finite where one is a NaN.
         auto convert = [&](int n, uint8_t *to, auto is_v) {
             asm volatile("cp.async.wait_group %0;" ::"n"(Sh::kRaws - 1) : "memory");
@@ -630,7 +635,6 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
                     for (int z = 0; z < 8; ++z) sum = __hadd2(sum, *reinterpret_cast<const __half2 *>(h + z));
                 }
             }
-            copy();
             return sum;
         };
 #pragma unroll 1
@@ -678,6 +682,7 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.k_full[slot]));
+            copy();
             ok = nt < kSlots || ch_wait(a, sh, sh.v_free[slot], free);
             if (!ok) break;
             uint8_t *to = v_slots + slot * Sh::kSlot;
@@ -700,6 +705,7 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.v_full[slot]));
+            copy();
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
@@ -1441,22 +1447,21 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Joins the parts of units that lie across CTAs.  CTA (x, y): 32 rows and 64
-// columns of the unit that CTA x of the first kernel began and did not end (if there
-// is one); its parts lie with x, x + 1, .. as far as their ranges go on.  A warp has
-// eight columns, a lane a row: it weighs the row's parts, then adds up its columns',
-// in the parts' order.
+// Joins the parts of units that lie across CTAs.  CTAs (x, ..): the unit that CTA x of
+// the first kernel began and did not end (if there is one), in turns of 32 rows and
+// 64 columns; its parts lie with x, x + 1, .. as far as their ranges go on.  The
+// warps weigh the rows' parts; then a warp adds up eight columns', a lane two of
+// four rows, in the parts' order.  Bound by the way of its loads: few rows in many
+// parts are few warps, so eight parts are under way at a time, and by its start: with
+// a CTA for every turn there might be, 2432, the empty ones alone took 10 us.
 template <typename T, int U>
 __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const ChunkArgs a, int grid) {
+    __shared__ __align__(16) float weights[kChMaxGrid][32], sums[kChMaxGrid][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, b = blockIdx.x;
-    const int local = static_cast<int>(blockIdx.y) % (U / 32) * 32 + lane, c = static_cast<int>(blockIdx.y) / (U / 32) * 64 + warp * 8;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int4 h = a.heads[2 * b];
+    const int4 h = a.heads[2 * b], rows = a.heads[2 * b + 1];
     if ((h.w & 1) == 0) return;
-    const int4 rows = a.heads[2 * b + 1];
-    const int r = h.y * U + local;
-    if (r - lane >= rows.y * a.group || c >= a.head_dim) return;  // (warps go their own ways from here on)
     int parts = 2;  // x + 1, and on as long as a CTA's whole range is the unit's middle
     for (bool on = true; on;) {
         const int x = b + parts - 1 + lane;
@@ -1464,30 +1469,67 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const ChunkArgs a, i
         on = middle == 0xFFFFFFFFu;
         parts += on ? 32 : __ffs(~middle) - 1;
     }
-    const int64_t size = static_cast<int64_t>(U) * (a.head_dim + 2);
-    auto part = [&](int p) { return a.partials + (static_cast<int64_t>(b + p) * 2 + (p == 0)) * size + local; };
-    const int64_t at_m = static_cast<int64_t>(U) * a.head_dim;
-    float M = kChNone, l = 0.f, o[8] = {};
+    const int64_t size = static_cast<int64_t>(U) * (a.head_dim + 2), at_m = static_cast<int64_t>(U) * a.head_dim;
+    const int flat = rows.y * a.group - h.y * U, row_turns = (min(flat, U) + 31) / 32, turns = row_turns * ((a.head_dim + 63) / 64);
+#pragma unroll 1
+    for (int turn = blockIdx.y; turn < turns; turn += kChJoinCtas) {
+        const int row0 = turn % row_turns * 32, r = h.y * U + row0;
+        auto part = [&](int p) { return a.partials + (static_cast<int64_t>(b + p) * 2 + (p == 0)) * size + row0; };
+        __syncthreads();  // (the turn before is done with the weights)
+        for (int p = warp; p < parts; p += 8) {
+            weights[p][lane] = part(p)[at_m + lane];
+            sums[p][lane] = part(p)[at_m + U + lane];
+        }
+        __syncthreads();
+        float M = kChNone, l = 0.f;
 #pragma unroll 8
-    for (int p = 0; p < parts; ++p) M = fmaxf(M, part(p)[at_m]);
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-        const float *x = part(p);
-        const float f = at_exp2(x[at_m] - M);
-        l = fmaf(x[at_m + U], f, l);
-        x += static_cast<int64_t>(c) * U;
+        for (int p = 0; p < parts; ++p) M = fmaxf(M, weights[p][lane]);
+#pragma unroll 8
+        for (int p = 0; p < parts; ++p) l = fmaf(sums[p][lane], at_exp2(weights[p][lane] - M), l);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        __syncthreads();
+        for (int p = warp; p < parts; p += 8) weights[p][lane] = at_exp2(weights[p][lane] - M) * inv;
+        if (turn < row_turns && warp == 0 && a.lse && r + lane < rows.y * a.group) {
+            int in_group;
+            const int token = ch_token(a, r + lane, in_group);
+            a.lse[(static_cast<int64_t>(rows.x) + token) * (static_cast<int64_t>(a.kv_heads) * a.group) + static_cast<int64_t>(h.z) * a.group + in_group] =
+                l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
+        }
+        __syncthreads();
+        const int c = turn / row_turns * 64 + warp * 8 + 2 * (lane >> 3), q = 4 * (lane & 7);
+        float o[2][4] = {};
+        for (int p0 = c < a.head_dim ? 0 : parts; p0 < parts; p0 += 8) {
+            float4 x[8][2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = fmaf(x[i * U], f, o[i]);
+            for (int p = 0; p < 8; ++p) {
+                const float *at = part(min(p0 + p, parts - 1)) + static_cast<int64_t>(c) * U + q;
+                x[p][0] = *reinterpret_cast<const float4 *>(at);
+                x[p][1] = *reinterpret_cast<const float4 *>(at + U);
+            }
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                if (p0 + p >= parts) break;
+                const float4 f = *reinterpret_cast<const float4 *>(&weights[p0 + p][q]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    o[i][0] = fmaf(x[p][i].x, f.x, o[i][0]);
+                    o[i][1] = fmaf(x[p][i].y, f.y, o[i][1]);
+                    o[i][2] = fmaf(x[p][i].z, f.z, o[i][2]);
+                    o[i][3] = fmaf(x[p][i].w, f.w, o[i][3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (c >= a.head_dim || r + q + i >= rows.y * a.group) break;
+            int in_group;
+            const int token = ch_token(a, r + q + i, in_group);
+            T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(rows.x) + token) * a.out_stride +
+                     (static_cast<int64_t>(h.z) * a.group + in_group) * a.head_dim + c;
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<float2 *>(out) = make_float2(o[0][i], o[1][i]);
+            else *reinterpret_cast<__nv_bfloat162 *>(out) = __floats2bfloat162_rn(o[0][i], o[1][i]);
+        }
     }
-    if (r >= rows.y * a.group) return;
-    int in_group;
-    const int token = ch_token(a, r, in_group);
-    const int64_t row = rows.x + token, head = static_cast<int64_t>(h.z) * a.group + in_group;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (c == 0 && a.lse) a.lse[row * (static_cast<int64_t>(a.kv_heads) * a.group) + head] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= inv;
-    rope_store8(static_cast<T *>(a.out) + row * a.out_stride + head * a.head_dim + c, o);
 }
 
 }  // namespace fp8blk
