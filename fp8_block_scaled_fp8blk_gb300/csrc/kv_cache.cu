@@ -753,11 +753,11 @@ extern "C" int fp8blk_kv_append_rope(const void *k, const void *v, int dtype, co
     uint32_t items = 0;
     // (The keys' rotation has no output of its own: the checks and the layout are those of one in place.)
     int plan = rope_plan(k, const_cast<void *>(k), cos_sin, dtype, n_tokens, kv_heads, head_dim, rot_dim, rot_start, interleaved,
-                         k_stride, k_stride, 1, &a.rope, &items);
+                         k_stride, k_stride, &a.rope, &items);
     if (plan != FP8BLK_OK) return plan;
     if (q) {
         plan = rope_plan(q, q_out, cos_sin, dtype, n_tokens, q_heads, head_dim, rot_dim, rot_start, interleaved, q_stride, q_out_stride,
-                         1, &a.q, &a.q_items);
+                         &a.q, &a.q_items);
         if (plan != FP8BLK_OK) return plan;
     }
     DeviceInfo dev;

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs r, ui
     const uint32_t item = blockIdx.x * kRopeThreads + threadIdx.x;
     grid_dependency_wait();
     grid_launch_dependents();
-    if (item < items) rope_item<T, kRopeHeads>(r, item);
+    if (item < items) rope_item<T, kRopeHeads<T>>(r, item);
 }
 
 }  // namespace fp8blk
@@ -156,9 +156,9 @@ extern "C" int fp8blk_rope_table(const int32_t *positions, const uint64_t *turns
 
 namespace fp8blk {
 
-// Checks and geometry of a rotation; `heads_each` heads a thread.
+// Checks and geometry of a rotation, a head a thread.
 int rope_plan(const void *x, void *out, const float *cos_sin, int dtype, int64_t n, int heads, int dim, int rot, int start, int interleaved,
-              int64_t x_stride, int64_t out_stride, int heads_each, RopeArgs *r, uint32_t *items) {
+              int64_t x_stride, int64_t out_stride, RopeArgs *r, uint32_t *items) {
     if (!x || !out || !cos_sin || (dtype != FP8BLK_F32 && dtype != FP8BLK_BF16) || n < 1 || heads < 1 || dim < 2) return FP8BLK_EINVAL;
     if (rot < 2 || rot % 2 != 0 || start < 0 || rot > dim || start > dim - rot || (interleaved != 0 && interleaved != 1)) return FP8BLK_EINVAL;
     if (dim > FP8BLK_MAX_ROT || heads > 65535 || n > kStepMaxIndex) return FP8BLK_ERANGE;
@@ -174,11 +174,21 @@ int rope_plan(const void *x, void *out, const float *cos_sin, int dtype, int64_t
     const int per = r->fast ? 8 : 1;
     // In place there is nothing to do outside the rotated part.
     r->units = rot / 2 / per + (x == out ? 0 : (dim - rot) / per);
-    r->chunks = (heads + heads_each - 1) / heads_each;
+    r->chunks = heads;
     const int64_t a_row = static_cast<int64_t>(r->units) * r->chunks;
     if (n > (int64_t(1) << 31) / a_row) return FP8BLK_ERANGE;
     *items = static_cast<uint32_t>(n * a_row);
     return FP8BLK_OK;
+}
+
+// A planned rotation by a kernel of its own.
+cudaError_t rope_launch(RopeArgs r, int dtype, cudaStream_t stream) {
+    const int each = dtype == FP8BLK_F32 ? kRopeHeads<float> : kRopeHeads<__nv_bfloat16>;
+    r.chunks = (r.heads + each - 1) / each;
+    const uint32_t items = static_cast<uint32_t>(r.n * r.units * r.chunks);
+    const dim3 grid((items + kRopeThreads - 1) / kRopeThreads);
+    return dtype == FP8BLK_F32 ? step_launch(rope_kernel<float>, grid, kRopeThreads, 0, stream, r, items)
+                               : step_launch(rope_kernel<__nv_bfloat16>, grid, kRopeThreads, 0, stream, r, items);
 }
 
 }  // namespace fp8blk
@@ -188,10 +198,6 @@ extern "C" int fp8blk_rope(const void *x, int dtype, const float *cos_sin, void 
     RopeArgs r;
     uint32_t items = 0;
     const int rc = rope_plan(x, out, cos_sin, dtype, n_rows, heads, head_dim, rot_dim, rot_start, interleaved, x_stride, out_stride,
-                             kRopeHeads, &r, &items);
-    if (rc != FP8BLK_OK) return rc;
-    const dim3 grid((items + kRopeThreads - 1) / kRopeThreads);
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return step_from_cuda(dtype == FP8BLK_F32 ? step_launch(rope_kernel<float>, grid, kRopeThreads, 0, s, r, items)
-                                              : step_launch(rope_kernel<__nv_bfloat16>, grid, kRopeThreads, 0, s, r, items));
+                             &r, &items);
+    return rc != FP8BLK_OK ? rc : step_from_cuda(rope_launch(r, dtype, static_cast<cudaStream_t>(stream)));
 }

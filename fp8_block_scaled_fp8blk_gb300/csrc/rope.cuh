@@ -23,7 +23,12 @@ struct RopeArgs {
     int units, chunks;      // threads of a chunk of heads (units of pairs, then groups to copy), chunks of heads a row
 };
 
-constexpr int kRopeHeads = 4;  // heads a thread takes: their loads are in flight together, the row's cosines are read once
+// Heads a thread takes: their loads are in flight together, the row's cosines are
+// read once.  With 1, 2, 4 and 8 of them 16384 bf16 rows of 64 heads took 87, 90, 119
+// and 194 us (the registers of more leave too few threads), and 1001 f32 rows of 24
+// heads, a third of each rotated, 8.2, 7.4, 8.7 and 9.9 us.
+template <typename T>
+constexpr int kRopeHeads = sizeof(T) == 2 ? 1 : 2;
 
 // Eight values as f32, from and to memory (16-byte aligned).
 __device__ __forceinline__ void rope_load8(const float *p, float (&v)[8]) {
