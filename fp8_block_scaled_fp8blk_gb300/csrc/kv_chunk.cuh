@@ -297,6 +297,20 @@ __device__ __forceinline__ bool ch_wait(const ChunkArgs &a, ChunkShared &sh, uin
     return true;
 }
 
+// ... with a limit shorter than the usual one, looked at from the first poll on: the
+// polls above sleep in between.  (The MMAs' wait for a unit's queries alone takes it,
+// and the other roles hear of it by the flag.  Code in every wait costs all roles
+// instruction cache: this one in all of them, 3% of a long call.)
+__device__ __noinline__ bool ch_wait_brief(uint32_t at, uint32_t parity, uint64_t limit_ns, volatile int *abort) {
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    while (!__all_sync(0xFFFFFFFFu, mbar_test_wait(at, parity))) {
+        if (global_timer_ns() - t0 >= limit_ns) *abort = 1;
+        if (__any_sync(0xFFFFFFFFu, *abort != 0)) return false;
+    }
+    return true;
+}
+
 // The u-th unit, for a warp; false after the last one.
 __device__ __forceinline__ bool ch_unit(ChunkShared &sh, int u, int lane, ChunkUnit &x) {
     const int slot = u & (kChUnits - 1);
@@ -830,6 +844,8 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
     for (int u = 0; ch_unit(sh, u, lane, w); ++u) {
         const int two = __shfl_sync(0xFFFFFFFFu, w.flags & kChTwo, 0), tiles = __shfl_sync(0xFFFFFFFFu, w.tiles, 0);
         if (tiles == 0 || !ok) continue;
+        if (a.wait_limit_ns < kWaitLimitNs)
+            ok = ch_wait_brief(smem_addr(&sh.q_full[unit & 1]), static_cast<uint32_t>(unit >> 1) & 1u, a.wait_limit_ns, &sh.abort);
         if (!wait(sh.q_full[unit & 1], static_cast<uint32_t>(unit >> 1) & 1u)) continue;
         if (Sh::NS == 2 && !two) {
             // Every other tile; the slots of the others are given back once they have been filled.
