@@ -594,7 +594,7 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
                              : "memory");
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
-            if (warp == 1 && (n_copy & 1) == 0) {
+            if (Sh::kRaws == 1 && warp == 1 && (n_copy & 1) == 0) {
                 // Into L2: the blocks of the tile four further on, a lane for each sixteen tokens.
                 const int of = (j_copy + 4 - ahead) * G + lane % G;
                 const int b0 = __shfl_sync(0xFFFFFFFFu, id, of & 31), b1 = __shfl_sync(0xFFFFFFFFu, id_next, of & 31), b = of < 32 ? b0 : b1;
