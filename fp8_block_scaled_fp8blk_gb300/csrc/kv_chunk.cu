@@ -65,8 +65,9 @@ extern "C" int fp8blk_kv_attn_chunk(const void *q, int dtype, const uint8_t *k_c
     const int64_t tiles = (static_cast<int64_t>(max_blocks) * block_tokens + tile - 1) / tile + 1;
     const int64_t flat = total_rows * group, units = (flat + rows - 1) / rows + n_seqs;
     if (flat > kStepMaxIndex || tiles > kStepMaxIndex / 256 || tiles * group + 2 * units > kStepMaxIndex / 2) return FP8BLK_ERANGE;
-    if (units * kv_heads > kStepMaxIndex / (rows / 128) / (tiles + 1)) return FP8BLK_ERANGE;
-    const int64_t entries = units * kv_heads * (rows / 128) * (tiles + 1);
+    const int64_t slots = tiles + kChSetUp;
+    if (units * kv_heads > kStepMaxIndex / (rows / 128) / slots) return FP8BLK_ERANGE;
+    const int64_t entries = units * kv_heads * (rows / 128) * slots;
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
     const double c = static_cast<double>(sm_scale) * 1.4426950408889634073599246810019;

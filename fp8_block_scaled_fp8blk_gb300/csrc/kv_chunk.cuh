@@ -44,12 +44,25 @@
 // Two products take turns: while one's softmax runs, the other's MMAs do.  The
 // second MMA starts on the first half of a tile's weights.  (Tiles of 64 tokens and
 // two score buffers a product cost more instructions than they hid latency: 2.3 ms
-// for the last case below.)  One product has two score buffers of 64 tokens: the
+// for the first call below.)  One product has two score buffers of 64 tokens: the
 // next scores are there when a softmax ends.
 //
 // A unit with 128 rows or fewer gives every other of its tiles to the second
-// product, and the two are added up at its end (16 rows of 65536 tokens: 89 us with
+// product, and the two are added up at its end (the third call below took 89 us with
 // one product at work).
+//
+// Measured, calls in a row, the cache not in L2:
+//   4096 rows at the end of 16384 tokens, 64 / 8 heads of 128, bf16    2.02 ms, 950 TFLOP/s, 49% of the matrix rate
+//   512 rows of 8192 tokens, the same heads                            180 us, 740 TFLOP/s, 38%
+//   16 rows of 65536 tokens, 32 / 8 heads, bf16                        82 us, 1.64 TB/s, 24% of the copy rate
+//   8 ragged prompts of up to 1024 tokens, 32 / 8 heads, f32           314 us
+//   9 requests of up to 2001 tokens, 15 / 3 heads of 80, bf16          62 us
+// Long calls are bound by a tile's chain: scores, softmax, weights' MMA.  256 rows x
+// 128 tokens take 5100 cycles, 2048 of them MMAs; a softmax group is at work for
+// 3500, its 700 instructions a warp slowed by the other roles' and by instruction
+// caches (141 KiB of code).  Short calls are bound by what comes before and
+// after their tiles, about 45 us: 7 us up to the first unit, 5 for its first tiles,
+// 3 for queries, 4 for writing a unit out, the join (12 in the third call).
 //
 // Roles (640 threads, one CTA per SM): warps 0-3 softmax (TMEM lane = row), warps
 // 4-7 softmax of the unit's second 128 rows, or f32's sums, warps 8-15 convert q, K
@@ -69,8 +82,12 @@ namespace fp8blk {
 constexpr int kChThreads = 640;
 constexpr int kChConvertWarp = 8, kChConvertWarps = 8, kChMmaWarp = 16, kChPlanWarp = 18;
 constexpr int kChMaxGrid = 160;          // bound on CTAs: partial sums in the workspace
-constexpr int kChJoinCtas = 8;           // CTAs of the join for one of the first kernel
+// CTAs of the join for one of the first kernel: with 4, 8 and 16 of them 9 requests of up to 2001 tokens took 67, 62 and 62 us.
+constexpr int kChJoinCtas = 8;
 constexpr int kChInfo = 8;               // tiles whose scales (and sums' factors) are held: more than K is ahead of the softmax
+// Tiles that a unit costs beside its own: queries, first tiles, writing out.  With 1, 2, 4 and 8 the 8 ragged prompts of f32 rows
+// took 316, 264, 234 and 241 us; 8 of 1024 bf16 rows, 32 / 8 heads, 245, 207 and 191 us with 1, 2 and 4.
+constexpr int kChSetUp = 4;
 constexpr int kChUnits = 4;              // units that are laid out ahead
 // Registers a thread of each role (of the 96 of the launch).
 constexpr int kChSoftmaxRegs = 112, kChConvertRegs = 104, kChIssueRegs = 48;
@@ -165,6 +182,7 @@ struct ChunkShared {
     int vnan[2][256];            // first position whose value is NaN, per element
     int any_nan[2];
     int scan[kChThreads / 32];
+    uint32_t scan_rows[kChThreads / 32];
     int cut[2];                  // this CTA's range
     int at[2][4];                // where its cuts lie: request (the first cut also: row tile, head and slot)
     ChunkSeq seq;                // the first one's request
@@ -216,15 +234,15 @@ struct ChunkList {
     }
     __device__ __forceinline__ int seen(const ChunkSeq &q, int i) const { return min((q.a + 2 * i) / a.group + 1, q.tiles); }
     __device__ __forceinline__ int weight(const ChunkSeq &q, int i) const { return i + 1 == q.row_tiles ? q.last : kFull; }
-    // Entries of the row tiles below i, i < row_tiles: each unit has one slot for its set-up and one per tile.
+    // Entries of the row tiles below i, i < row_tiles: each unit has kChSetUp slots for what it costs beside its tiles, and one per tile.
     __device__ __noinline__ int before(const ChunkSeq &q, int i) const {
         const int64_t lack = static_cast<int64_t>(q.tiles - 1) * a.group - q.a;  // from row tile ceil(lack / 2) on all tiles are seen
         const int some = lack <= 0 ? 0 : static_cast<int>(min((lack + 1) / 2, static_cast<int64_t>(i)));
-        const int slots = ch_floor_sum(q.a, a.group, some) + some + (i - some) * q.tiles + i;
+        const int slots = ch_floor_sum(q.a, a.group, some) + some + (i - some) * q.tiles + i * kChSetUp;
         return slots * kFull * a.kv_heads;
     }
     __device__ __forceinline__ int entries(const ChunkSeq &q) const {
-        return q.row_tiles == 0 ? 0 : before(q, q.row_tiles - 1) + a.kv_heads * q.last * (seen(q, q.row_tiles - 1) + 1);
+        return q.row_tiles == 0 ? 0 : before(q, q.row_tiles - 1) + a.kv_heads * q.last * (seen(q, q.row_tiles - 1) + kChSetUp);
     }
 };
 
@@ -252,7 +270,7 @@ __device__ __forceinline__ void ch_plan(const ChunkArgs &a, ChunkShared &sh) {
             return;
         }
         const int tiles = list.seen(q, row_tile), weight = list.weight(q, row_tile);
-        const int e1 = min(tiles + 1, e0 + (weight == 2 ? left >> 1 : left));
+        const int e1 = min(tiles + kChSetUp, e0 + (weight == 2 ? left >> 1 : left));
         left -= (e1 - e0) * weight;
         x.first = q.first;
         x.rows = q.rows;
@@ -260,12 +278,12 @@ __device__ __forceinline__ void ch_plan(const ChunkArgs &a, ChunkShared &sh) {
         x.s = s;
         x.row0 = row_tile * Sh::U;
         x.head = head;
-        x.j0 = max(e0 - 1, 0);
-        x.tiles = e1 - 1 - x.j0;
-        x.flags = (e0 == 0 ? kChStarts : 0) | (e1 == tiles + 1 ? kChEnds : 0) | (weight == 2 ? kChTwo : 0);
+        x.j0 = max(e0 - kChSetUp, 0);
+        x.tiles = e1 - kChSetUp - x.j0;
+        x.flags = (e0 == 0 ? kChStarts : 0) | (e1 == tiles + kChSetUp ? kChEnds : 0) | (weight == 2 ? kChTwo : 0);
         mbar_arrive(smem_addr(&sh.unit_full[slot]));
         if (left <= 0) {
-            const bool last_cut = e1 != tiles + 1;
+            const bool last_cut = e1 != tiles + kChSetUp;
             a.heads[2 * blockIdx.x] = make_int4(s, row_tile, head, (last_cut && e0 == 0 ? 1 : 0) | (u == 0 && first_cut && last_cut ? 2 : 0));
             a.heads[2 * blockIdx.x + 1] = make_int4(q.first, q.rows, 0, 0);
         } else if (++head == a.kv_heads) {
@@ -434,79 +452,89 @@ __device__ __forceinline__ float ch_pow2(int e) { return __uint_as_float(static_
 // runs once a unit, and unrolled its instructions took longer to come than the
 // queries: 13 us a unit.)
 template <typename Sh, typename T>
-__device__ __forceinline__ void ch_queries(const ChunkArgs &a, const ChunkUnit &w, uint8_t *sq, float *qs, int warp, int lane) {
-    constexpr int L = Sh::WIDE ? 32 : 16, RW = 32 / L, PL = Sh::PL, kStride = kChConvertWarps * RW;
-    const int d0 = (lane % L) * 8, rows = w.flags & kChTwo ? 256 : 128;
-    const int flat = w.rows * a.group - w.row0;  // rows of the unit that exist
-    const T *q = static_cast<const T *>(a.q) + w.first * a.q_stride + static_cast<int64_t>(w.head) * a.group * a.head_dim + d0;
-    const int r0 = warp * RW + lane / L, here = min(rows, flat);
-    auto place = [&](int r) {
+struct ChunkQueries {
+    static constexpr int L = Sh::WIDE ? 32 : 16, RW = 32 / L, PL = Sh::PL, kStride = kChConvertWarps * RW;
+    const ChunkArgs &a;
+    uint8_t *sq;
+    float *qs;
+    int warp, lane, d0, rows, flat, row0, here;
+    const T *q;
+    __device__ __forceinline__ ChunkQueries(const ChunkArgs &a, const ChunkUnit &w, uint8_t *sq, float *qs, int warp, int lane)
+        : a(a), sq(sq), qs(qs), warp(warp), lane(lane), d0((lane % L) * 8), rows(w.flags & kChTwo ? 256 : 128),
+          flat(w.rows * a.group - w.row0),  // rows of the unit that exist
+          row0(w.row0), here(min(rows, flat)),
+          q(static_cast<const T *>(a.q) + w.first * a.q_stride + static_cast<int64_t>(w.head) * a.group * a.head_dim + d0) {}
+    __device__ __forceinline__ uint8_t *place(int r) const {
         return sq + (r >> 7) * (PL * Sh::kQPlane) + (d0 >> 6) * (128 * 128) + (r & 127) * 128 + ((((d0 >> 3) & 7) ^ (r & 7)) << 4);
-    };
-#pragma unroll 1
-    for (int r = r0; r < rows; r += kStride) {
-        int head;
-        const int token = ch_token(a, w.row0 + r, head);
-        const T *x = q + token * a.q_stride + head * a.head_dim;
-        const uint32_t dst = smem_addr(place(r)), bytes = r < flat && d0 < a.head_dim ? 16 : 0;  // the rest is filled with zeros
-        if (bytes == 0) x = static_cast<const T *>(a.q);
-        if (r >= flat && lane % L == 0) qs[r] = 1.f;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(x), "r"(bytes) : "memory");
-        if (PL == 2) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + Sh::kQPlane), "l"(x + (bytes ? 4 : 0)), "r"(bytes) : "memory");
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    // (Two of a warp's turns in one, so that one's loads and reductions cover the other's.)
+    __device__ __forceinline__ void copy() const {
 #pragma unroll 1
-    for (int rb = warp * RW; rb < here; rb += 2 * kStride) {
-        float x[2][8];
-        uint32_t top[2] = {0, 0};
-        uint8_t *const at[2] = {place(rb + lane / L), place(rb + lane / L + kStride)};
-        const bool two = rb + kStride < here;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            if constexpr (PL == 2) {
-                const float4 u = *reinterpret_cast<const float4 *>(at[b & two]), v = *reinterpret_cast<const float4 *>(at[b & two] + Sh::kQPlane);
-                x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w, x[b][4] = v.x, x[b][5] = v.y, x[b][6] = v.z, x[b][7] = v.w;
-            } else {
-                rope_load8(reinterpret_cast<const __nv_bfloat16 *>(at[b & two]), x[b]);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (PL == 2) x[b][i] = fmaf(x[b][i], a.c, x[b][i] * a.c_low);  // the scale per value, rounded at random
-                top[b] = max(top[b], __float_as_uint(fabsf(x[b][i])));
-            }
+        for (int r = warp * RW + lane / L; r < rows; r += kStride) {
+            int head;
+            const int token = ch_token(a, row0 + r, head);
+            const T *x = q + token * a.q_stride + head * a.head_dim;
+            const uint32_t dst = smem_addr(place(r)), bytes = r < flat && d0 < a.head_dim ? 16 : 0;  // the rest is filled with zeros
+            if (bytes == 0) x = static_cast<const T *>(a.q);
+            if (r >= flat && lane % L == 0) qs[r] = 1.f;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(x), "r"(bytes) : "memory");
+            if (PL == 2) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + Sh::kQPlane), "l"(x + (bytes ? 4 : 0)), "r"(bytes) : "memory");
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void convert() const {
+        // (Two of a warp's turns in one, so that one's loads and reductions cover the other's.)
+#pragma unroll 1
+        for (int rb = warp * RW; rb < here; rb += 2 * kStride) {
+            float x[2][8];
+            uint32_t top[2] = {0, 0};
+            uint8_t *const at[2] = {place(rb + lane / L), place(rb + lane / L + kStride)};
+            const bool two = rb + kStride < here;
 #pragma unroll
-        for (int d = L / 2; d; d >>= 1) {
+            for (int b = 0; b < 2; ++b) {
+                if constexpr (PL == 2) {
+                    const float4 u = *reinterpret_cast<const float4 *>(at[b & two]), v = *reinterpret_cast<const float4 *>(at[b & two] + Sh::kQPlane);
+                    x[b][0] = u.x, x[b][1] = u.y, x[b][2] = u.z, x[b][3] = u.w, x[b][4] = v.x, x[b][5] = v.y, x[b][6] = v.z, x[b][7] = v.w;
+                } else {
+                    rope_load8(reinterpret_cast<const __nv_bfloat16 *>(at[b & two]), x[b]);
+                }
 #pragma unroll
-            for (int b = 0; b < 2; ++b) top[b] = max(top[b], __shfl_xor_sync(0xFFFFFFFFu, top[b], d));
-        }
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const bool good = top[b] < 0x7F800000u;
-            int e = 0;  // the row's largest times 2^e is in [2^14, 2^15)
-            if (good && top[b] != 0) e = top[b] >= 0x800000u ? 14 + 127 - static_cast<int>(top[b] >> 23) : 14 + 149 - (31 - __clz(top[b]));
-            const int e1 = e >> 1, e2 = e - e1;
-            // (bf16: the sign of the softmax scale goes here.)
-            const float f1 = good ? ch_pow2(e1) : 0.f, f2 = PL == 1 && a.c < 0.f ? -ch_pow2(e2) : ch_pow2(e2);
-            uint32_t h[4], l[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = good ? x[b][2 * i] * f1 * f2 : 0.f, v = good ? x[b][2 * i + 1] * f1 * f2 : 0.f;
-                h[i] = ch_pack_f16(u, v);
-                if (PL == 2) {
-                    const float2 f = ch_unpack_f16(h[i]);
-                    l[i] = ch_pack_f16(u - f.x, v - f.y);
+                for (int i = 0; i < 8; ++i) {
+                    if (PL == 2) x[b][i] = fmaf(x[b][i], a.c, x[b][i] * a.c_low);  // the scale per value, rounded at random
+                    top[b] = max(top[b], __float_as_uint(fabsf(x[b][i])));
                 }
             }
-            if (b == 1 && !two) continue;
-            if (lane % L == 0)
-                qs[rb + lane / L + b * kStride] = good ? ch_pow2(-e1) * (PL == 2 ? 1.f : fabsf(a.c)) * ch_pow2(-e2) : __int_as_float(0x7FC00000);
-            *reinterpret_cast<uint4 *>(at[b]) = make_uint4(h[0], h[1], h[2], h[3]);
-            if (PL == 2) *reinterpret_cast<uint4 *>(at[b] + Sh::kQPlane) = make_uint4(l[0], l[1], l[2], l[3]);
+#pragma unroll
+            for (int d = L / 2; d; d >>= 1) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) top[b] = max(top[b], __shfl_xor_sync(0xFFFFFFFFu, top[b], d));
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const bool good = top[b] < 0x7F800000u;
+                int e = 0;  // the row's largest times 2^e is in [2^14, 2^15)
+                if (good && top[b] != 0) e = top[b] >= 0x800000u ? 14 + 127 - static_cast<int>(top[b] >> 23) : 14 + 149 - (31 - __clz(top[b]));
+                const int e1 = e >> 1, e2 = e - e1;
+                // (bf16: the sign of the softmax scale goes here.)
+                const float f1 = good ? ch_pow2(e1) : 0.f, f2 = PL == 1 && a.c < 0.f ? -ch_pow2(e2) : ch_pow2(e2);
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float u = good ? x[b][2 * i] * f1 * f2 : 0.f, v = good ? x[b][2 * i + 1] * f1 * f2 : 0.f;
+                    h[i] = ch_pack_f16(u, v);
+                    if (PL == 2) {
+                        const float2 f = ch_unpack_f16(h[i]);
+                        l[i] = ch_pack_f16(u - f.x, v - f.y);
+                    }
+                }
+                if (b == 1 && !two) continue;
+                if (lane % L == 0)
+                    qs[rb + lane / L + b * kStride] = good ? ch_pow2(-e1) * (PL == 2 ? 1.f : fabsf(a.c)) * ch_pow2(-e2) : __int_as_float(0x7FC00000);
+                *reinterpret_cast<uint4 *>(at[b]) = make_uint4(h[0], h[1], h[2], h[3]);
+                if (PL == 2) *reinterpret_cast<uint4 *>(at[b] + Sh::kQPlane) = make_uint4(l[0], l[1], l[2], l[3]);
+            }
         }
     }
-}
+};
 
 // ------------------------------------------------------------------ converters
 // Warps 8-15: q of each unit, then K and V of its tiles.  A thread has two groups
@@ -615,13 +643,16 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
             id_scales = window(w.j0 + 2 * kWindow);
         }
         // The unit's queries, once the MMAs have read the last one's, and the softmax has written out the one before that.
+        const ChunkQueries<Sh, T> queries(a, w, sq, sh.qs[ub], warp, lane);
         ok = (unit < 1 || ch_wait(a, sh, sh.q_free, static_cast<uint32_t>(unit - 1) & 1u)) &&
              (unit < 2 || ch_wait(a, sh, sh.unit_done[ub], static_cast<uint32_t>((unit >> 1) - 1) & 1u));
+        if (ok) queries.copy();
         sh.vnan[ub][tid] = kChNoNan;
         if (tid == 0) sh.any_nan[ub] = 0;
         asm volatile("bar.sync 4, %0;" ::"n"(kThreads) : "memory");
         if (!ok) continue;
-        ch_queries<Sh, T>(a, w, sq, sh.qs[ub], warp, lane);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        queries.convert();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&sh.q_full[ub]));
         // One raw slot, which has come, as f16 (the copies that take its place come behind the barrier's release).  The sum of V's values (at most 32 x 448)
@@ -1360,13 +1391,20 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
         const int each = (a.n_seqs + kChThreads - 1) / kChThreads;
         const int r0 = min(tid * each, a.n_seqs), r1 = min(r0 + each, a.n_seqs);
         int sum = 0;
+        int64_t rows = 0;
         bool bad = false;
 #pragma unroll 1
         for (int s = r0; s < r1; ++s) {
             const ChunkSeq q = list.seq(s);
             sum += list.entries(q);
+            rows += q.rows;
             bad |= q.bad;
         }
+        // More rows than there are (starts that go back): nothing is done, and no sum below has passed 32 bits otherwise.
+        auto add_up = [](uint32_t x) {
+            return static_cast<int64_t>(__reduce_add_sync(0xFFFFFFFFu, x & 0xFFFFu)) + (static_cast<int64_t>(__reduce_add_sync(0xFFFFFFFFu, x >> 16)) << 16);
+        };
+        rows = add_up(static_cast<uint32_t>(min(rows, static_cast<int64_t>(0x7FFFFFFF))));
         if (bad && blockIdx.x == 0) atomicOr(a.status, 4u);
         int pre = sum;
 #pragma unroll
@@ -1374,14 +1412,19 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
             const int u = __shfl_up_sync(0xFFFFFFFFu, pre, d);
             if (lane >= d) pre += u;
         }
-        if (lane == 31) sh.scan[warp] = pre;
+        if (lane == 31) {
+            sh.scan[warp] = pre;
+            sh.scan_rows[warp] = static_cast<uint32_t>(min(rows, static_cast<int64_t>(0x7FFFFFFF)));
+        }
         __syncthreads();
+        const bool over = add_up(lane < kChThreads / 32 ? sh.scan_rows[lane] : 0) > a.total_rows;
+        if (over && tid == 0) atomicOr(a.status, 4u);
         const int part = sh.scan[min(lane, kChThreads / 32 - 1)];  // each warp's sum, in the lanes of its number
         const int total = __reduce_add_sync(0xFFFFFFFFu, lane < kChThreads / 32 ? part : 0);
         const int from = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? part : 0) + pre - sum;
         // Every CTA's share is a few entries, so no two cuts inside a unit meet.
         const int grid = min(static_cast<int>(gridDim.x), max(total / 8, min(total, 1)));
-        busy = static_cast<int>(blockIdx.x) < grid;
+        busy = static_cast<int>(blockIdx.x) < grid && !over;
         const AttnSplit split(total, max(grid, 1));
         if (busy) {  // the requests that the two cuts lie in
 #pragma unroll 1
@@ -1415,10 +1458,10 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
                     n = min(step, n - k * step);
                 }
                 here += list.before(q, lo);
-                const int weight = list.weight(q, lo), slots = list.seen(q, lo) + 1;
+                const int weight = list.weight(q, lo), slots = list.seen(q, lo) + kChSetUp;
                 const int head = (x - here) / (weight * slots);
                 int slot = ((x - here) - head * weight * slots) / weight;
-                if (slot <= kChSmallCut) slot = 0;
+                if (slot < kChSetUp + kChSmallCut) slot = 0;
                 if (lane == 0) {
                     sh.cut[warp] = here + (head * slots + slot) * weight;
                     if (warp == 0) {
@@ -1468,8 +1511,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
 // 64 columns; its parts lie with x, x + 1, .. as far as their ranges go on.  The
 // warps weigh the rows' parts; then a warp adds up eight columns', a lane two of
 // four rows, in the parts' order.  Bound by the way of its loads: few rows in many
-// parts are few warps, so eight parts are under way at a time, and by its start: with
-// a CTA for every turn there might be, 2432, the empty ones alone took 10 us.
+// parts are few warps, so eight parts are under way at a time.
 template <typename T, int U>
 __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const ChunkArgs a, int grid) {
     __shared__ __align__(16) float weights[kChMaxGrid][32], sums[kChMaxGrid][32];

