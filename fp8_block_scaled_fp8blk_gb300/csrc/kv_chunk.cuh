@@ -52,17 +52,18 @@
 // one product at work).
 //
 // Measured, calls in a row, the cache not in L2:
-//   4096 rows at the end of 16384 tokens, 64 / 8 heads of 128, bf16    2.02 ms, 950 TFLOP/s, 49% of the matrix rate
+//   4096 rows at the end of 16384 tokens, 64 / 8 heads of 128, bf16    2.03 ms, 947 TFLOP/s, 49% of the matrix rate
 //   512 rows of 8192 tokens, the same heads                            180 us, 740 TFLOP/s, 38%
-//   16 rows of 65536 tokens, 32 / 8 heads, bf16                        82 us, 1.64 TB/s, 24% of the copy rate
-//   8 ragged prompts of up to 1024 tokens, 32 / 8 heads, f32           314 us
-//   9 requests of up to 2001 tokens, 15 / 3 heads of 80, bf16          62 us
+//   16 rows of 65536 tokens, 32 / 8 heads, bf16                        86 us, 1.56 TB/s, 23% of the copy rate
+//   8 ragged prompts of up to 1024 tokens, 32 / 8 heads, f32           235 us
+//   9 requests of up to 2001 tokens, 15 / 3 heads of 80, bf16          58 us
 // Long calls are bound by a tile's chain: scores, softmax, weights' MMA.  256 rows x
 // 128 tokens take 5100 cycles, 2048 of them MMAs; a softmax group is at work for
 // 3500, its 700 instructions a warp slowed by the other roles' and by instruction
 // caches (141 KiB of code).  Short calls are bound by what comes before and
 // after their tiles, about 45 us: 7 us up to the first unit, 5 for its first tiles,
-// 3 for queries, 4 for writing a unit out, the join (12 in the third call).
+// 3 for queries, 4 for writing a unit out, the join (12 in the third call).  That a unit
+// costs so much beside its tiles is in the list's weights.
 //
 // Roles (640 threads, one CTA per SM): warps 0-3 softmax (TMEM lane = row), warps
 // 4-7 softmax of the unit's second 128 rows, or f32's sums, warps 8-15 convert q, K
@@ -249,6 +250,14 @@ struct ChunkList {
 // A cut in a unit's set-up or first two tiles goes to the unit's start: joining
 // parts costs more than they do.
 constexpr int kChSmallCut = 2;
+
+// CTA b's share of the list begins at entry floor(b total / grid), so that equal
+// units whose number divides the grid are cut at their ends.
+struct ChunkSplit {
+    int each, more, grid;
+    __device__ __forceinline__ ChunkSplit(int total, int grid) : each(total / grid), more(total - each * grid), grid(grid) {}
+    __device__ __forceinline__ int begin(int b) const { return b * each + b * more / grid; }
+};
 
 // Lays out the CTA's units (one thread).  What the join needs goes to a.heads: the
 // last unit, whether it is cut and begins here (1), and whether the whole range is
@@ -1425,7 +1434,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
         // Every CTA's share is a few entries, so no two cuts inside a unit meet.
         const int grid = min(static_cast<int>(gridDim.x), max(total / 8, min(total, 1)));
         busy = static_cast<int>(blockIdx.x) < grid && !over;
-        const AttnSplit split(total, max(grid, 1));
+        const ChunkSplit split(total, max(grid, 1));
         if (busy) {  // the requests that the two cuts lie in
 #pragma unroll 1
             for (int e = 0; e < 2; ++e) {

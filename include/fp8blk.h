@@ -575,7 +575,9 @@ size_t fp8blk_kv_attn_chunk_ws_bytes(int q_heads, int kv_heads, int head_dim);
  * have more of them together than total_rows; each sets FP8BLK_STATUS_BAD_KV.
  * Rows of a CTA that gave up on a wait are NaN in out and lse (see
  * fp8blk_set_wait_limit).
- * For up to FP8BLK_MAX_M rows a request fp8blk_kv_attn is faster.
+ * For up to FP8BLK_MAX_M rows a request fp8blk_kv_attn is the faster one (64
+ * requests of 8192 tokens, one row: 169 against 507 us), but for 8 rows of bf16
+ * with 8 query heads a cache head (16 requests of 8192: 183 against 148 us).
  * Errors: EINVAL, EALIGN, EWS, ERANGE (as fp8blk_kv_attn, and 2^31 (row, query
  * head of a cache head) pairs), ECUDA.
  */
