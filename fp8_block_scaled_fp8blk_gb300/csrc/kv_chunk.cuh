@@ -546,12 +546,13 @@ struct ChunkQueries {
 };
 
 // ------------------------------------------------------------------ converters
-// Warps 8-15: q of each unit, then K and V of its tiles.  A thread has two groups
-// of sixteen codes of a tile (four of a wide head): it copies them to shared memory
-// several tiles ahead, and converts them there when they have come.  (Asynchronous
-// copies, because the barriers' releases wait for loads under way: with the codes
-// ahead in registers a tile cost 6000 cycles.)  Block ids and scales come eight
-// tiles at a time, a lane for each sixteen tokens, one and two such windows ahead.
+// Warps 8-15: q of each unit, then K and V of its tiles.  A thread has two or four
+// groups of sixteen codes of a tile: it copies them to shared memory several tiles
+// ahead (one slot, where there is no room for more, and into L2 four tiles ahead),
+// and converts them there when they have come.  (Asynchronous copies, because the
+// barriers' releases wait for loads under way: with the codes ahead in registers a
+// tile cost 6000 cycles.)  Block ids and scales come four or eight tiles at a time, a
+// lane for each sixteen tokens, one and two such windows ahead.
 template <typename Sh, typename T>
 __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, uint8_t *sq, uint8_t *k_slots, uint8_t *v_slots, uint8_t *raw,
                                            int tid) {
