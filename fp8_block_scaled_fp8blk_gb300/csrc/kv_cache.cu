@@ -237,6 +237,8 @@ struct AppendArgs {
     int staged;                            // values of one run that shared memory holds (0: none)
     uint32_t per_inverse;                  // ceil(2^32 / (head_dim / 8)): divides group numbers below 2^16
 };
+// Query heads a thread takes beside the cache's CTAs: with 1, 2 and 4 the 16.7 k tokens below took 96, 91 and 98 us (f32: 152 and 142).
+constexpr int kAppendQueryHeads = 2;
 // ... with keys that are rotated first, and queries that are rotated beside them.
 struct AppendRopeArgs : AppendArgs {
     RopeArgs rope;       // the keys' (x, out and strides unused)
@@ -526,11 +528,11 @@ __device__ __noinline__ void append_check(const int64_t *slots, int64_t n_tokens
 // third full); 64 tokens of f32, one a request, 2.8 us.
 //   With rotated keys (A = AppendRopeArgs) the CTA stages K as rotated f32, and
 // CTAs behind the cache's rotate the queries of the same rows.  The 16.7 k tokens
-// with 32 query heads: 96 us, 59% of the copy rate, half for the queries (whose CTAs
-// have the staging's share of an SM: four at a time) and half for the cache, where
-// 64 registers and 48 KiB leave four CTAs waiting on loads one after the other.
-// Measured and not kept: the queries by a kernel of their own or spread among the
-// cache's CTAs (96 and 97 us), both halves of a head by one thread (96).  64 tokens
+// with 32 query heads: 91 us, 62% of the copy rate, about half for the queries (whose
+// CTAs have the staging's share of an SM: four at a time) and half for the cache,
+// where 64 registers and 48 KiB leave four CTAs waiting on loads one after the other.
+// Measured and not kept: the queries by a kernel of their own (96 us) or spread among
+// the cache's CTAs (90), both halves of a head by one thread (no gain).  64 tokens
 // of f32: 19 us a call from the host, 8.6 alone on the device with cold caches.
 template <typename T, bool WHOLE, typename A>
 __global__ void __launch_bounds__(kAppendThreads, !WHOLE ? 2 : std::is_same_v<A, AppendArgs> ? 6 : 4) kv_append_kernel(const A a) {
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kAppendThreads, !WHOLE ? 2 : std::is_same_v<A,
         if (static_cast<int>(blockIdx.x) >= a.q_first) {
             const uint32_t cta = ((blockIdx.x - a.q_first) * gridDim.y + blockIdx.y) * gridDim.z + blockIdx.z;
             const uint32_t item = cta * kAppendThreads + tid;
-            if (item < a.q_items) rope_item<T, 1>(a.q, item);
+            if (item < a.q_items) rope_item<T, kAppendQueryHeads>(a.q, item);
             return;
         }
     }
@@ -765,6 +767,8 @@ extern "C" int fp8blk_kv_append_rope(const void *k, const void *v, int dtype, co
         plan = rope_plan(q, q_out, cos_sin, dtype, n_tokens, q_heads, head_dim, rot_dim, rot_start, interleaved, q_stride, q_out_stride,
                          &a.q, &a.q_items);
         if (plan != FP8BLK_OK) return plan;
+        a.q.chunks = (q_heads + kAppendQueryHeads - 1) / kAppendQueryHeads;
+        a.q_items = static_cast<uint32_t>(n_tokens * a.q.units * a.q.chunks);
     }
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
