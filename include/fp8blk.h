@@ -363,8 +363,8 @@ int fp8blk_rope_table(const int32_t *positions, const uint64_t *turns, float sca
  *   cos_sin   as fp8blk_rope_table writes it
  *   head_dim  2 .. FP8BLK_MAX_ROT; rot_dim even, rot_start + rot_dim <= head_dim
  *   interleaved  0 half layout, 1 neighbours
- * Errors: EINVAL, EALIGN, ERANGE (also more than 2^31 items of work: at least
- * 16 million values), ECUDA.
+ * Errors: EINVAL, EALIGN, ERANGE (also more than 2^31 items of work: pairs and
+ * values outside the rotated part, eight of either on the fast path), ECUDA.
  */
 int fp8blk_rope(const void *x, int dtype, const float *cos_sin, void *out, int64_t n_rows, int heads, int head_dim,
                 int rot_dim, int rot_start, int interleaved, int64_t x_stride, int64_t out_stride, void *stream);
