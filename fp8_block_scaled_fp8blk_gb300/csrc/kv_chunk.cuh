@@ -53,16 +53,16 @@
 //
 // Measured, calls in a row, the cache not in L2:
 //   4096 rows at the end of 16384 tokens, 64 / 8 heads of 128, bf16    2.03 ms, 947 TFLOP/s, 49% of the matrix rate
-//   512 rows of 8192 tokens, the same heads                            180 us, 740 TFLOP/s, 38%
-//   16 rows of 65536 tokens, 32 / 8 heads, bf16                        86 us, 1.56 TB/s, 23% of the copy rate
+//   512 rows of 8192 tokens, the same heads                            179 us, 745 TFLOP/s, 38%
+//   16 rows of 65536 tokens, 32 / 8 heads, bf16                        83 us, 1.62 TB/s, 24% of the copy rate
 //   8 ragged prompts of up to 1024 tokens, 32 / 8 heads, f32           235 us
-//   9 requests of up to 2001 tokens, 15 / 3 heads of 80, bf16          58 us
+//   9 requests of up to 2001 tokens, 15 / 3 heads of 80, bf16          57 us
 // Long calls are bound by a tile's chain: scores, softmax, weights' MMA.  256 rows x
 // 128 tokens take 5100 cycles, 2048 of them MMAs; a softmax group is at work for
 // 3500, its 700 instructions a warp slowed by the other roles' and by instruction
 // caches (141 KiB of code).  Short calls are bound by what comes before and
 // after their tiles, about 45 us: 7 us up to the first unit, 5 for its first tiles,
-// 3 for queries, 4 for writing a unit out, the join (12 in the third call).  That a unit
+// 3 for queries, 4 for writing a unit out, the join (9 in the third call).  That a unit
 // costs so much beside its tiles is in the list's weights.
 //
 // Roles (640 threads, one CTA per SM): warps 0-3 softmax (TMEM lane = row), warps
@@ -1521,7 +1521,10 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
 // 64 columns; its parts lie with x, x + 1, .. as far as their ranges go on.  The
 // warps weigh the rows' parts; then a warp adds up eight columns', a lane two of
 // four rows, in the parts' order.  Bound by the way of its loads: few rows in many
-// parts are few warps, so eight parts are under way at a time.
+// parts are few warps, so four parts are under way at a time, the first four while
+// the parts are weighed (16 rows in 19 parts: 86 us a call without that, 84 with eight
+// parts, 83 with four or two; with eight, whose registers leave two CTAs an SM, 512
+// rows of 8192 tokens 185 for 179).
 template <typename T, int U>
 __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const ChunkArgs a, int grid) {
     __shared__ __align__(16) float weights[kChMaxGrid][32], sums[kChMaxGrid][32];
@@ -1529,11 +1532,13 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const ChunkArgs a, i
     grid_dependency_wait();
     grid_launch_dependents();
     const int4 h = a.heads[2 * b], rows = a.heads[2 * b + 1];
+    int middle_of = a.heads[2 * min(b + 1 + lane, grid - 1)].w;  // (asked for at once)
     if ((h.w & 1) == 0) return;
     int parts = 2;  // x + 1, and on as long as a CTA's whole range is the unit's middle
     for (bool on = true; on;) {
         const int x = b + parts - 1 + lane;
-        const unsigned middle = __ballot_sync(0xFFFFFFFFu, x < grid - 1 && (a.heads[2 * x].w & 2) != 0);
+        if (parts > 2) middle_of = a.heads[2 * min(x, grid - 1)].w;
+        const unsigned middle = __ballot_sync(0xFFFFFFFFu, x < grid - 1 && (middle_of & 2) != 0);
         on = middle == 0xFFFFFFFFu;
         parts += on ? 32 : __ffs(~middle) - 1;
     }
@@ -1543,6 +1548,18 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const ChunkArgs a, i
     for (int turn = blockIdx.y; turn < turns; turn += kChJoinCtas) {
         const int row0 = turn % row_turns * 32, r = h.y * U + row0;
         auto part = [&](int p) { return a.partials + (static_cast<int64_t>(b + p) * 2 + (p == 0)) * size + row0; };
+        const int c = turn / row_turns * 64 + warp * 8 + 2 * (lane >> 3), q = 4 * (lane & 7);
+        const bool has = c < a.head_dim;
+        float4 x[4][2];
+        auto load = [&](int p0) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float *at = part(min(p0 + p, parts - 1)) + static_cast<int64_t>(has ? c : 0) * U + q;
+                x[p][0] = *reinterpret_cast<const float4 *>(at);
+                x[p][1] = *reinterpret_cast<const float4 *>(at + U);
+            }
+        };
+        load(0);  // (on their way while the parts are weighed)
         __syncthreads();  // (the turn before is done with the weights)
         for (int p = warp; p < parts; p += 8) {
             weights[p][lane] = part(p)[at_m + lane];
@@ -1564,18 +1581,11 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const ChunkArgs a, i
                 l == 0.f ? -INFINITY : (M + log2f(l)) * 0.6931471805599453f;
         }
         __syncthreads();
-        const int c = turn / row_turns * 64 + warp * 8 + 2 * (lane >> 3), q = 4 * (lane & 7);
         float o[2][4] = {};
-        for (int p0 = c < a.head_dim ? 0 : parts; p0 < parts; p0 += 8) {
-            float4 x[8][2];
+        for (int p0 = has ? 0 : parts; p0 < parts; p0 += 4) {
+            if (p0 > 0) load(p0);
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const float *at = part(min(p0 + p, parts - 1)) + static_cast<int64_t>(c) * U + q;
-                x[p][0] = *reinterpret_cast<const float4 *>(at);
-                x[p][1] = *reinterpret_cast<const float4 *>(at + U);
-            }
-#pragma unroll
-            for (int p = 0; p < 8; ++p) {
+            for (int p = 0; p < 4; ++p) {
                 if (p0 + p >= parts) break;
                 const float4 f = *reinterpret_cast<const float4 *>(&weights[p0 + p][q]);
 #pragma unroll
@@ -1589,7 +1599,7 @@ __global__ void __launch_bounds__(256) kv_chunk_join_kernel(const ChunkArgs a, i
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (c >= a.head_dim || r + q + i >= rows.y * a.group) break;
+            if (!has || r + q + i >= rows.y * a.group) break;
             int in_group;
             const int token = ch_token(a, r + q + i, in_group);
             T *out = static_cast<T *>(a.out) + (static_cast<int64_t>(rows.x) + token) * a.out_stride +
