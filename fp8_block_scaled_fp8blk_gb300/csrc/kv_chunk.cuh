@@ -74,6 +74,7 @@
 #pragma once
 
 #include "kv_attn.cuh"
+#include "kv_chunk_copy.h"
 #include "rope.cuh"
 
 #include <type_traits>
@@ -557,15 +558,13 @@ template <typename Sh, typename T>
 __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, uint8_t *sq, uint8_t *k_slots, uint8_t *v_slots, uint8_t *raw,
                                            int tid) {
     constexpr int kEach = Sh::kEach, kThreads = kChConvertWarps * 32, kSlots = Sh::kSlots, G = Sh::kGranules, kWindow = 32 / G;
-    const int warp = tid >> 5, lane = tid & 31, per = a.head_dim / 16, total = Sh::T * per, block = 1 << a.block_log2;
+    const int warp = tid >> 5, lane = tid & 31, per = a.head_dim / 16, block = 1 << a.block_log2;
     int token[kEach];  // of the thread's groups, in a tile (T: none)
     uint32_t dst[kEach];
     auto group = [&](int i, int &t, int &c) {
-        // (Where a token has a multiple of four groups, four of them and the same of the next token go to eight lanes: their
-        // stores then meet no bank twice.)
-        const int g = tid + i * kThreads, four = per & 3 ? 0 : per >> 2;
-        t = g >= total ? Sh::T : four ? (g / (2 * per) << 1) + (g >> 2 & 1) : g / per;
-        c = g >= total ? 0 : four ? (g & 3) + (g / 8 % four << 2) : g - t * per;
+        const ChunkGroup x = ch_group(tid + i * kThreads, Sh::T, per);
+        t = x.token;
+        c = x.part;
         return (c >> 2) * (Sh::T * 128) + t * 128 + (((2 * (c & 3)) ^ (t & 7)) << 4);
     };
     int from[kEach];   // ... their places in the block of a request's first tile
@@ -573,7 +572,7 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
     for (int i = 0; i < kEach; ++i) {
         int c;
         dst[i] = group(i, token[i], c);
-        from[i] = (token[i] & (block - 1)) * a.head_dim + 16 * c;
+        from[i] = ch_group_from({token[i], c}, Sh::T, block, a.head_dim);
     }
     const uint8_t *mine = raw + tid * 16;  // the thread's groups of a raw slot lie 16 x threads apart
     const int64_t id_bytes = static_cast<int64_t>(a.kv_heads) * block * a.head_dim;
@@ -621,12 +620,12 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
                 id = id_next;
                 id_next = window(j_copy + kWindow);
             }
-            const uint8_t *codes = (n_copy & 1 ? v_head : k_head) + (j_copy * Sh::T & (block - 1)) * a.head_dim;  // (a block of 128 tokens is two tiles)
-            const int left = w.len - j_copy * Sh::T;  // (past the unit's last tile the ids say so)
+            const uint8_t *codes = (n_copy & 1 ? v_head : k_head) + ch_tile_from(j_copy, Sh::T, block, a.head_dim);
+            const int left = ch_tile_left(w.len, j_copy, Sh::T);  // (past the unit's last tile the ids say so)
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 const int b = __shfl_sync(0xFFFFFFFFu, id, (j_copy - ahead) * G + (token[i] >> 4));
-                const bool there = static_cast<uint32_t>(b) < n_blocks && token[i] < left;
+                const bool there = ch_group_copied(token[i], left, static_cast<uint32_t>(b), n_blocks);
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to_copy + i * kThreads * 16),
                              "l"(codes + (there ? b : 0) * id_bytes + from[i]), "r"(there ? 16 : 0)
                              : "memory");
