@@ -1324,12 +1324,12 @@ __device__ __forceinline__ void ch_sums(const ChunkArgs &a, ChunkShared &sh, uin
                     for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(j > 0 ? fmaf(o[x], factor, p[x]) : p[x]);
                     ch_st16(o_col + c, u);
                 }
+                ch_wait_st();  // (the next tile loads them: nothing else orders a load behind a store)
                 t8_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.product_free));
             }
         }
-        ch_wait_st();
         ok = ok && ch_wait(a, sh, sh.last_full[ub], static_cast<uint32_t>(unit >> 1) & 1u);
         const ChunkSums x = {o_col, sh.last[ub][0][local], sh.last[ub][1][local], sh.last[ub][2][local]};
         ch_finish<Sh, T>(a, w, sh, unit, row, local, x, x, false, ok);
