@@ -69,8 +69,9 @@
 // 4-7 softmax of the unit's second 128 rows, or f32's sums, warps 8-15 convert q, K
 // and V, warps 16 and 17 issue the MMAs (of the first and second 128 rows), warp 18
 // walks the list and lays out the units to come.  Every wait is bounded; a timeout
-// raises a CTA-wide flag, the outputs and lse of the CTA's rows become NaN, MMAs in
-// flight are waited for, and the status word records it.
+// raises a CTA-wide flag, the outputs and lse of the CTA's rows become NaN (also
+// those of units that were not laid out any more), MMAs in flight are waited for,
+// and the status word records it.
 #pragma once
 
 #include "kv_attn.cuh"
@@ -189,10 +190,37 @@ struct ChunkShared {
     int at[2][4];                // where its cuts lie: request (the first cut also: row tile, head and slot)
     ChunkSeq seq;                // the first one's request
     int abort;
+    ChunkUnit lost;              // one that the layout does not hand on any more
     uint32_t tmem;
 };
 
 // ------------------------------------------------------------------ the list
+// r / group and the remainder, r < 2^31 (the estimate is at most one too small).
+__device__ __forceinline__ int ch_token(const ChunkArgs &a, int r, int &head) {
+    int t = static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.group_inverse));
+    head = r - t * a.group;
+    if (head >= a.group) {
+        ++t;
+        head -= a.group;
+    }
+    return t;
+}
+// A row of the unit: where it lies, and what it sees.
+struct ChunkRow {
+    int64_t out, lse;
+    int last;    // last position it sees
+    bool valid;
+    __device__ __forceinline__ ChunkRow(const ChunkArgs &a, const ChunkUnit &w, int local) {
+        int in_group;
+        const int r = w.row0 + local, token = ch_token(a, r, in_group);
+        const int64_t row = w.first + token, head = static_cast<int64_t>(w.head) * a.group + in_group;
+        valid = r < w.rows * a.group;
+        last = valid ? w.len - w.rows + token : 0x7FFFFFFF;  // (rows that are not there: zeros, stored nowhere)
+        out = row * a.out_stride + head * a.head_dim;
+        lse = row * (static_cast<int64_t>(a.kv_heads) * a.group) + head;
+    }
+};
+
 // (Entries are counted in 32 bits: the host sees to it.)
 // sum of floor((a + 2 i) / g) over i < n.  The floors of all integers from a to
 // a + 2 n add up in closed form; of two neighbours x, x + 1 the second's is one more
@@ -260,25 +288,80 @@ struct ChunkSplit {
     __device__ __forceinline__ int begin(int b) const { return b * each + b * more / grid; }
 };
 
-// Lays out the CTA's units (one thread).  What the join needs goes to a.heads: the
-// last unit, whether it is cut and begins here (1), and whether the whole range is
-// the middle of one unit (2).
-template <typename Sh>
+// Waits of the ring of units.  They end because all others do: whoever has given up goes on taking units, so a unit's
+// place is free at last, and the layout goes on to the end.  (No limit of a second for them: a unit may be a second's
+// work, and the layout's wait begins before that of a role that stalls.)  What bounds them nevertheless is counted by
+// their polls, so that a GPU that stood still in between does not end them.  The layout's: 16 s, a poll for a
+// millisecond at most.
+constexpr uint64_t kChLayoutLimitNs = 16 * kWaitLimitNs;
+__device__ __forceinline__ bool ch_layout_wait(uint32_t at, uint32_t parity) {
+    uint64_t last = global_timer_ns(), spent = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(at, parity)) {
+        const uint64_t now = global_timer_ns(), step = now - last;
+        spent += step < 1000000 ? step : 1000000;
+        if (spent >= kChLayoutLimitNs) return false;
+        last = now;
+    }
+    return true;
+}
+// The roles': a minute or more (a poll takes 40 ns to 1.5 us), longer than any silence of the layout.
+constexpr uint32_t kChRolePolls = 1u << 30;
+__device__ __forceinline__ bool ch_role_wait(uint32_t at, uint32_t parity) {
+#pragma unroll 1
+    for (uint32_t n = 0; n < kChRolePolls; ++n)
+        if (mbar_try_wait_short(at, parity)) return true;
+    return false;
+}
+
+// The rows of a unit that no role will see: NaN, as where other waits ran out.  (One thread.)
+template <typename Sh, typename T>
+__device__ __forceinline__ void ch_lose(const ChunkArgs &a, const ChunkUnit &x) {
+    const float nanf = __int_as_float(0x7FC00000);
+    if ((x.flags & (kChStarts | kChEnds)) != (kChStarts | kChEnds)) {  // a part: by its denominators
+        float *l = a.partials + (static_cast<int64_t>(blockIdx.x) * 2 + (x.flags & kChStarts)) * (static_cast<int64_t>(Sh::U) * (a.head_dim + 2)) +
+                   static_cast<int64_t>(Sh::U) * (a.head_dim + 1);
+#pragma unroll 1
+        for (int r = 0; r < Sh::U; ++r) __stcg(l + r, nanf);
+        return;
+    }
+#pragma unroll 1
+    for (int r = 0; r < Sh::U; ++r) {
+        const ChunkRow row(a, x, r);
+        if (!row.valid) return;
+#pragma unroll 1
+        for (int d = 0; d < a.head_dim; ++d) static_cast<T *>(a.out)[row.out + d] = static_cast<T>(nanf);
+        if (a.lse) a.lse[row.lse] = nanf;
+    }
+}
+
+// Lays out the CTA's units (one thread), each in the place of the one kChUnits
+// before it.  What the join needs goes to a.heads: the last unit, whether it is cut
+// and begins here (1), and whether the whole range is the middle of one unit (2).
+//   After a wait that ran out the rest goes round without the roles, which hear of
+// it by the flag, and of the end by a stop in the place that was waited for.  (A
+// limit shorter than the usual one holds here too: a test comes by such units so.)
+template <typename Sh, typename T>
 __device__ __forceinline__ void ch_plan(const ChunkArgs &a, ChunkShared &sh) {
     const ChunkList<Sh> list{a};
     int s = sh.at[0][0], row_tile = sh.at[0][1], head = sh.at[0][2], e0 = sh.at[0][3], left = sh.cut[1] - sh.cut[0];
     ChunkSeq q = sh.seq;
     const bool first_cut = e0 != 0;
-    for (int u = 0;; ++u) {
+    bool lost = false;
+    for (int u = 0;;) {
         const int slot = u & (kChUnits - 1);
-        // (Not one of the role's waits: after one of those ran out the units still go round.)
-        if (u >= kChUnits && !mbar_wait_bounded(smem_addr(&sh.unit_free[slot]), static_cast<uint32_t>(u / kChUnits - 1) & 1u)) return;
-        ChunkUnit &x = sh.units[slot];
+        if (u >= kChUnits && !lost) {
+            const uint32_t at = smem_addr(&sh.unit_free[slot]), parity = static_cast<uint32_t>(u / kChUnits - 1) & 1u;
+            lost = !(a.wait_limit_ns < kWaitLimitNs ? mbar_wait_limit(at, parity, a.wait_limit_ns) : ch_layout_wait(at, parity));
+            if (lost) *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+        }
         if (left <= 0) {
-            x.flags = kChStop;
+            if (lost && !ch_layout_wait(smem_addr(&sh.unit_free[slot]), static_cast<uint32_t>(u / kChUnits - 1) & 1u)) return;
+            sh.units[slot].flags = kChStop;
             mbar_arrive(smem_addr(&sh.unit_full[slot]));
             return;
         }
+        ChunkUnit &x = lost ? sh.lost : sh.units[slot];
         const int tiles = list.seen(q, row_tile), weight = list.weight(q, row_tile);
         const int e1 = min(tiles + kChSetUp, e0 + (weight == 2 ? left >> 1 : left));
         left -= (e1 - e0) * weight;
@@ -291,7 +374,8 @@ __device__ __forceinline__ void ch_plan(const ChunkArgs &a, ChunkShared &sh) {
         x.j0 = max(e0 - kChSetUp, 0);
         x.tiles = e1 - kChSetUp - x.j0;
         x.flags = (e0 == 0 ? kChStarts : 0) | (e1 == tiles + kChSetUp ? kChEnds : 0) | (weight == 2 ? kChTwo : 0);
-        mbar_arrive(smem_addr(&sh.unit_full[slot]));
+        if (lost) ch_lose<Sh, T>(a, x);
+        else mbar_arrive(smem_addr(&sh.unit_full[slot]));
         if (left <= 0) {
             const bool last_cut = e1 != tiles + kChSetUp;
             a.heads[2 * blockIdx.x] = make_int4(s, row_tile, head, (last_cut && e0 == 0 ? 1 : 0) | (u == 0 && first_cut && last_cut ? 2 : 0));
@@ -305,6 +389,7 @@ __device__ __forceinline__ void ch_plan(const ChunkArgs &a, ChunkShared &sh) {
             }
         }
         e0 = 0;
+        u += !lost;
     }
 }
 
@@ -342,7 +427,10 @@ __device__ __noinline__ bool ch_wait_brief(uint32_t at, uint32_t parity, uint64_
 // The u-th unit, for a warp; false after the last one.
 __device__ __forceinline__ bool ch_unit(ChunkShared &sh, int u, int lane, ChunkUnit &x) {
     const int slot = u & (kChUnits - 1);
-    if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded<false>(smem_addr(&sh.unit_full[slot]), static_cast<uint32_t>(u / kChUnits) & 1u))) return false;
+    if (!__all_sync(0xFFFFFFFFu, ch_role_wait(smem_addr(&sh.unit_full[slot]), static_cast<uint32_t>(u / kChUnits) & 1u))) {
+        *reinterpret_cast<volatile int *>(&sh.abort) = 1;
+        return false;
+    }
     x = sh.units[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&sh.unit_free[slot]));
@@ -426,16 +514,6 @@ __device__ __forceinline__ uint64_t ch_add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
-}
-// r / group and the remainder, r < 2^31 (the estimate is at most one too small).
-__device__ __forceinline__ int ch_token(const ChunkArgs &a, int r, int &head) {
-    int t = static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.group_inverse));
-    head = r - t * a.group;
-    if (head >= a.group) {
-        ++t;
-        head -= a.group;
-    }
-    return t;
 }
 // The largest of three.
 __device__ __forceinline__ float ch_max3(float a, float b, float c) {
@@ -924,22 +1002,6 @@ __device__ __forceinline__ bool ch_issue(const ChunkArgs &a, ChunkShared &sh, ui
 }
 
 // ------------------------------------------------------------------ softmax
-// A row of the unit: where it lies, and what it sees.
-struct ChunkRow {
-    int64_t out, lse;
-    int last;    // last position it sees
-    bool valid;
-    __device__ __forceinline__ ChunkRow(const ChunkArgs &a, const ChunkUnit &w, int local) {
-        int in_group;
-        const int r = w.row0 + local, token = ch_token(a, r, in_group);
-        const int64_t row = w.first + token, head = static_cast<int64_t>(w.head) * a.group + in_group;
-        valid = r < w.rows * a.group;
-        last = valid ? w.len - w.rows + token : 0x7FFFFFFF;  // (rows that are not there: zeros, stored nowhere)
-        out = row * a.out_stride + head * a.head_dim;
-        lse = row * (static_cast<int64_t>(a.kv_heads) * a.group) + head;
-    }
-};
-
 // What a product has of a row: the sums' columns, their maximum, reference and
 // denominator.
 struct ChunkSums {
@@ -1503,7 +1565,7 @@ __global__ void __launch_bounds__(kChThreads, 1) kv_chunk_kernel(const ChunkArgs
                     (void)mbar_wait_bounded(smem_addr(&sh.mma_done[i]), 0);
                 }
             } else if (warp == kChPlanWarp && lane == 0) {
-                ch_plan<Sh>(a, sh);
+                ch_plan<Sh, T>(a, sh);
             }
         }
     } else if (tid == 0) {

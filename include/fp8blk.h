@@ -647,14 +647,16 @@ int fp8blk_set_launch_tuning(int target_stage_bytes, int ctas_per_sm, int use_pd
  * fp8blk_bf16_gemv, nvfp4_expert_gemv, mxfp4_expert_gemv) waits for a weight
  * tile, or a role of fp8blk_kv_attn or fp8blk_kv_attn_chunk for its operands,
  * before it gives up, sets FP8BLK_STATUS_WAIT_TIMEOUT and returns (the latter's
- * roles look at a limit at a unit's start, and between polls that may sleep).  The
- * default is about one second; a healthy tile lands in microseconds, so any
+ * roles look at a limit at a unit's start, and between polls that may sleep; the
+ * layout of its units goes by one below the default, and else ends with its
+ * roles, or 16 s after the last unit that was taken).  The default is about one
+ * second; a healthy tile lands in microseconds, so any
  * shorter limit is for exercising the failure path (0 gives up on the first
  * tile that has not landed yet).  After a give-up the CTA still waits, with
  * the fixed one-second bound, for the copies it has in flight before it
  * exits, and still takes part in the argmax hand-off or the join of parts, so
- * the workspace stays consistent; the outputs of that call are invalid (those
- * of fp8blk_kv_attn NaN).  The tensor-core GEMV kernels and the dequant kernel
+ * the workspace stays consistent; the outputs of that call are invalid (rows of
+ * fp8blk_kv_attn and fp8blk_kv_attn_chunk that are lost are NaN).  The tensor-core GEMV kernels and the dequant kernel
  * keep the fixed bound.  Not thread-safe against
  * concurrent calls of the other entry points.  Errors: EINVAL.
  */
