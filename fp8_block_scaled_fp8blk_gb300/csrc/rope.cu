@@ -51,8 +51,8 @@ __device__ __forceinline__ void rope_cos_sin(uint64_t phase, float &c, float &s)
 // A step's table once for all layers: bound by its launch (64 rows of 128: 4.6 us a
 // call from the host; 16384 rows, 8.5 MB, 5.1 us, 24% of the copy rate).
 // Angles are fractions of a turn in 64 bits: position x frequency wraps where
-// the circle does, so a far position costs no precision (2^31 x the frequency's
-// 2^-65 of a turn is 2^-34 of one).
+// the circle does, so a far position costs no precision (2^31 x the 2^-65 of a turn
+// that the frequency is rounded by are 2^-34 of one).
 __global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(const RopeTableArgs a) {
     const uint32_t item = blockIdx.x * kRopeThreads + threadIdx.x;
     grid_dependency_wait();
@@ -134,15 +134,21 @@ extern "C" int fp8blk_rope_frequencies(int scaling, int rot_dim, double base, do
     return FP8BLK_OK;
 }
 
+// 1 / 2 pi as the sum of two doubles (what they leave is 2^-110).
+static constexpr double kInvTwoPi = 0x1.45f306dc9c883p-3, kInvTwoPiLow = -0x1.6b01ec5417056p-57;
+
+// |f| / 2 pi as hi + rest, hi the f64 product and rest what it leaves of the exact one (2^-106 of it); then the fraction
+// of a turn in units of 2^-64, whole ones and the rest's apart.  Off by half a unit and 2^-25 of one (f <= 10^6).
 extern "C" int fp8blk_rope_turns(const double *freqs, int n, uint64_t *turns) {
     if (!freqs || !turns || n < 1 || n > FP8BLK_MAX_ROT / 2) return FP8BLK_EINVAL;
     for (int i = 0; i < n; ++i) {
         if (!(std::fabs(freqs[i]) <= 1e6)) return FP8BLK_EINVAL;
-        const double t = freqs[i] / kTwoPi, part = t - std::floor(t);  // in [0, 1]: a tiny negative t gives 1
-        // As two halves of 32 bits (either may round up to 2^32, and the sum wraps as the circle does).
-        const double up = std::floor(part * 0x1p32);
-        const double low = std::floor((part * 0x1p32 - up) * 0x1p32 + 0.5);
-        turns[i] = (static_cast<uint64_t>(up) << 32) + static_cast<uint64_t>(low);
+        const double f = std::fabs(freqs[i]);
+        const volatile double product = f * kInvTwoPi;  // (rounded, whatever the host's compiler would fuse it with)
+        const double hi = product, rest = std::fma(f, kInvTwoPi, -hi) + f * kInvTwoPiLow;
+        const double units = (hi - std::floor(hi)) * 0x1p64, whole = std::floor(units);  // exact
+        const uint64_t t = static_cast<uint64_t>(whole) + static_cast<uint64_t>(static_cast<int64_t>(std::floor((units - whole) + rest * 0x1p64 + 0.5)));
+        turns[i] = freqs[i] < 0 ? 0 - t : t;
     }
     return FP8BLK_OK;
 }

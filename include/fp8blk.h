@@ -328,8 +328,9 @@ int fp8blk_rope_frequencies(int scaling, int rot_dim, double base, double factor
 /*
  * fp8blk_rope_turns -- HOST function: frequencies (radians a token, of any
  * origin; negative ones turn back) as fractions of a turn,
- *   turns[i] = round(2^64 * (freqs[i] / 2 pi)) mod 2^64,
- * the form fp8blk_rope_table reads on the device.
+ *   turns[i] = round(2^64 * (freqs[i] / 2 pi)) mod 2^64
+ * (of the double as it is, to 2^-25 of a unit beside the rounding), the form
+ * fp8blk_rope_table reads on the device.
  *   freqs, turns  host, n entries, 1 <= n <= FP8BLK_MAX_ROT / 2
  * Errors: EINVAL (also a frequency that is not finite or beyond 10^6).
  */
