@@ -7,6 +7,7 @@
 // and f32 scales [n_blocks, kv_heads].  Head-major inside a block: what one
 // head reads of one block is a single run of block_tokens x head_dim bytes
 // under one scale.
+#include "overlap.h"
 #include "rope.cuh"
 #include "step.h"
 
@@ -767,6 +768,11 @@ extern "C" int fp8blk_kv_append_rope(const void *k, const void *v, int dtype, co
         plan = rope_plan(q, q_out, cos_sin, dtype, n_tokens, q_heads, head_dim, rot_dim, rot_start, interleaved, q_stride, q_out_stride,
                          &a.q, &a.q_items);
         if (plan != FP8BLK_OK) return plan;
+        // Some CTAs turn the queries while others read keys and values.
+        const int64_t es = dtype == FP8BLK_F32 ? 4 : 2, row = es * kv_heads * head_dim, q_row = es * q_heads * head_dim;
+        if (rows_overlap(q_out, q_out_stride * es, q_row, k, k_stride * es, row, n_tokens) ||
+            rows_overlap(q_out, q_out_stride * es, q_row, v, v_stride * es, row, n_tokens))
+            return FP8BLK_EINVAL;
         a.q.chunks = (q_heads + kAppendQueryHeads - 1) / kAppendQueryHeads;
         a.q_items = static_cast<uint32_t>(n_tokens * a.q.units * a.q.chunks);
     }

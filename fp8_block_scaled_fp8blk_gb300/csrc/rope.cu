@@ -1,6 +1,7 @@
 // rope.cu -- rotary positions: frequencies on the host (fp8blk_rope_frequencies,
 // fp8blk_rope_turns), a step's cosines and sines (fp8blk_rope_table), and the
 // rotation of queries and keys by them (fp8blk_rope).
+#include "overlap.h"
 #include "rope.cuh"
 #include "step.h"
 
@@ -188,6 +189,7 @@ int rope_plan(const void *x, void *out, const float *cos_sin, int dtype, int64_t
     r->chunks = heads;
     const int64_t a_row = static_cast<int64_t>(r->units) * r->chunks;
     if (n > (int64_t(1) << 31) / a_row) return FP8BLK_ERANGE;
+    if (x != out && rows_overlap(x, x_stride * es, row * es, out, out_stride * es, row * es, n)) return FP8BLK_EINVAL;
     *items = static_cast<uint32_t>(n * a_row);
     return FP8BLK_OK;
 }

@@ -360,7 +360,8 @@ int fp8blk_rope_table(const int32_t *positions, const uint64_t *turns, float sca
  *             x_stride / out_stride elements apart, aligned to one element
  *             (16-byte aligned rows, head_dim and rot_start multiples of 8 and
  *             rot_dim of 16 take the fast path).  out may be x itself, with the
- *             same stride; any other overlap is not allowed
+ *             same stride; any other overlap of their rows is refused (slices
+ *             of one wider tensor are none)
  *   cos_sin   as fp8blk_rope_table writes it
  *   head_dim  2 .. FP8BLK_MAX_ROT; rot_dim even, rot_start + rot_dim <= head_dim
  *   interleaved  0 half layout, 1 neighbours
@@ -497,7 +498,7 @@ int fp8blk_kv_append(const void *k, const void *v, int dtype, const int64_t *slo
  *              negative are rotated too
  *   rot_dim, rot_start, interleaved  as fp8blk_rope, the same for k and q
  *   others     as fp8blk_kv_append
- * q_out must not overlap k or v.
+ * q_out must not overlap k or v (EINVAL; slices of one fused projection do not).
  * Errors: as fp8blk_kv_append and fp8blk_rope.
  */
 int fp8blk_kv_append_rope(const void *k, const void *v, int dtype, const int64_t *slots, const float *cos_sin,
