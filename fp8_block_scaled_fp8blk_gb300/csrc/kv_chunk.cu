@@ -1,6 +1,7 @@
 // kv_chunk.cu -- attention of any number of new rows per request over the paged
 // e4m3 cache (fp8blk_kv_attn_chunk): entry point and launch.
 #include "kv_chunk.cuh"
+#include "overlap.h"
 #include "step.h"
 
 #include <algorithm>
@@ -68,6 +69,10 @@ extern "C" int fp8blk_kv_attn_chunk(const void *q, int dtype, const uint8_t *k_c
     const int64_t slots = tiles + kChSetUp;
     if (units * kv_heads > kStepMaxIndex / (rows / 128) / slots) return FP8BLK_ERANGE;
     const int64_t entries = units * kv_heads * (rows / 128) * slots;
+    // A row of a head is read by the units that write it, before they do (a unit in parts: before the join), so out may be q.
+    if (q != out || q_stride != out_stride) {
+        if (rows_overlap(q, q_stride * es, row * es, out, out_stride * es, row * es, total_rows)) return FP8BLK_EINVAL;
+    }
     DeviceInfo dev;
     if (current_device_info(&dev) != cudaSuccess) return step_from_cuda(cudaErrorUnknown);
     const double c = static_cast<double>(sm_scale) * 1.4426950408889634073599246810019;

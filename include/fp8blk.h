@@ -568,7 +568,8 @@ size_t fp8blk_kv_attn_chunk_ws_bytes(int q_heads, int kv_heads, int head_dim);
  * two f16 values and keeps 2^-22 of itself.  A k or v scale that is not finite
  * counts as NaN.
  *   q, out, lse, seq_lens, q_starts  as fp8blk_kv_attn; a request may have any
- *              number of rows, none among them
+ *              number of rows, none among them.  out may be q itself, with the
+ *              same stride; any other overlap of their rows is refused
  *   ws         device workspace of at least fp8blk_kv_attn_chunk_ws_bytes()
  *              bytes, 16-byte aligned; nothing is kept in it between calls, and
  *              it need not be cleared.  Calls that share it must be ordered
