@@ -1185,9 +1185,10 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
             const int64_t t0 = static_cast<int64_t>(w.j0 + j) * kTile;
             const int rel = t0 > row.last ? -1 : static_cast<int>(row.last - t0 < kTile ? row.last - t0 : kTile);  // last column this row sees
             // Careful: tiles that are not seen whole, odd scales, and scores past 2^19, where the rounding of a score shows
-            // beside its row's reference.
+            // beside its row's reference.  (A unit's first tile has no maximum yet: it is not careful for that, its maxima are
+            // rounded the same either way, and its weights go by `base` below.)
             const int kind = ok ? sh.info_kind[at] : 0;
-            const bool careful = __any_sync(0xFFFFFFFFu, rel < kTile - 1 || fabsf(M) >= 0x1p19f) || kind == 2;
+            const bool careful = __any_sync(0xFFFFFFFFu, rel < kTile - 1 || (M > kChNone && fabsf(M) >= 0x1p19f)) || kind == 2;
             ok = ok && ch_wait(a, sh, sh.s_full[buf], ph);
             if (!ok) break;
             t8_fence_after();
