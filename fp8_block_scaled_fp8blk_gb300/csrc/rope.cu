@@ -195,7 +195,7 @@ int rope_plan(const void *x, void *out, const float *cos_sin, int dtype, int64_t
 }
 
 // A planned rotation by a kernel of its own.
-cudaError_t rope_launch(RopeArgs r, int dtype, cudaStream_t stream) {
+static cudaError_t rope_launch(RopeArgs r, int dtype, cudaStream_t stream) {
     const int each = dtype == FP8BLK_F32 ? kRopeHeads<float> : kRopeHeads<__nv_bfloat16>;
     r.chunks = (r.heads + each - 1) / each;
     const uint32_t items = static_cast<uint32_t>(r.n * r.units * r.chunks);

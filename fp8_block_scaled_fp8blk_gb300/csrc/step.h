@@ -42,10 +42,9 @@ inline int step_check_cache(const uint8_t *k_codes, const float *k_scales, const
     return FP8BLK_OK;
 }
 
-// Checks and geometry of a rotation, a head a thread; and its launch (rope.cu).
+// Checks and geometry of a rotation, a head a thread (rope.cu).
 int rope_plan(const void *x, void *out, const float *cos_sin, int dtype, int64_t n, int heads, int dim, int rot, int start, int interleaved,
               int64_t x_stride, int64_t out_stride, RopeArgs *r, uint32_t *items);
-cudaError_t rope_launch(RopeArgs r, int dtype, cudaStream_t stream);
 
 // Launch with programmatic dependent launch: every kernel of these files
 // waits on the grid dependency before it touches global memory.
