@@ -533,8 +533,9 @@ __device__ __noinline__ void append_check(const int64_t *slots, int64_t n_tokens
 // CTAs have the staging's share of an SM: four at a time) and half for the cache,
 // where 64 registers and 48 KiB leave four CTAs waiting on loads one after the other.
 // Measured and not kept: the queries by a kernel of their own (96 us) or spread among
-// the cache's CTAs (90), both halves of a head by one thread (no gain).  64 tokens
-// of f32: 19 us a call from the host, 8.6 alone on the device with cold caches.
+// the cache's CTAs (90), both halves of a head by one thread (no gain).  The same of
+// f32: 138 us, 78% of the copy rate.  64 tokens of f32: 19 us a call from the host,
+// 4.4 in a graph, 8.6 alone on the device with cold caches.
 template <typename T, bool WHOLE, typename A>
 __global__ void __launch_bounds__(kAppendThreads, !WHOLE ? 2 : std::is_same_v<A, AppendArgs> ? 6 : 4) kv_append_kernel(const A a) {
     constexpr bool ROPE = std::is_same_v<A, AppendRopeArgs>;

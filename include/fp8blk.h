@@ -359,7 +359,8 @@ int fp8blk_rope_table(const int32_t *positions, const uint64_t *turns, float sca
  *   x, out    device, f32 or bf16 (`dtype`) [n_rows, heads, head_dim], rows
  *             x_stride / out_stride elements apart, aligned to one element
  *             (16-byte aligned rows, head_dim and rot_start multiples of 8 and
- *             rot_dim of 16 take the fast path).  out may be x itself, with the
+ *             rot_dim of 16 take the fast path; others a pair a thread, at an
+ *             eighth to a fifth of the copy rate).  out may be x itself, with the
  *             same stride; any other overlap of their rows is refused (slices
  *             of one wider tensor are none)
  *   cos_sin   as fp8blk_rope_table writes it
@@ -579,8 +580,11 @@ size_t fp8blk_kv_attn_chunk_ws_bytes(int q_heads, int kv_heads, int head_dim);
  * Rows of a CTA that gave up on a wait are NaN in out and lse (see
  * fp8blk_set_wait_limit).
  * For up to FP8BLK_MAX_M rows a request fp8blk_kv_attn is the faster one (64
- * requests of 8192 tokens, one row: 169 against 507 us), but for 8 rows of bf16
- * with 8 query heads a cache head (16 requests of 8192: 183 against 148 us).
+ * requests of 8192 tokens, one row: 164 against 484 us), but for 8 rows of bf16
+ * with 8 query heads a cache head (16 requests of 8192: 183 against 144 us).  So
+ * a step of decoded rows and a chunk is best two calls, by slices of q, out,
+ * block_table and seq_lens (63 requests of one row and one of 512, 8192 tokens
+ * each: 356 us, 778 in one call).
  * Errors: EINVAL, EALIGN, EWS, ERANGE (as fp8blk_kv_attn, and 2^31 (row, query
  * head of a cache head) pairs), ECUDA.
  */
@@ -653,15 +657,15 @@ int fp8blk_set_launch_tuning(int target_stage_bytes, int ctas_per_sm, int use_pd
  * roles look at a limit at a unit's start, and between polls that may sleep; the
  * layout of its units goes by one below the default, and else ends with its
  * roles, or 16 s after the last unit that was taken).  The default is about one
- * second; a healthy tile lands in microseconds, so any
- * shorter limit is for exercising the failure path (0 gives up on the first
- * tile that has not landed yet).  After a give-up the CTA still waits, with
- * the fixed one-second bound, for the copies it has in flight before it
- * exits, and still takes part in the argmax hand-off or the join of parts, so
- * the workspace stays consistent; the outputs of that call are invalid (rows of
- * fp8blk_kv_attn and fp8blk_kv_attn_chunk that are lost are NaN).  The tensor-core GEMV kernels and the dequant kernel
- * keep the fixed bound.  Not thread-safe against
- * concurrent calls of the other entry points.  Errors: EINVAL.
+ * second; a healthy tile lands in microseconds, so any shorter limit is for
+ * exercising the failure path (0 gives up on the first tile that has not landed
+ * yet).  After a give-up the CTA still waits, with the fixed one-second bound,
+ * for the copies it has in flight before it exits, and still takes part in the
+ * argmax hand-off or the join of parts, so the workspace stays consistent; the
+ * outputs of that call are invalid (rows of fp8blk_kv_attn and
+ * fp8blk_kv_attn_chunk that are lost are NaN).  The tensor-core GEMV kernels and
+ * the dequant kernel keep the fixed bound.  Not thread-safe against concurrent
+ * calls of the other entry points.  Errors: EINVAL.
  */
 #define FP8BLK_WAIT_LIMIT_DEFAULT_NS 1000000000ll
 int fp8blk_set_wait_limit(int64_t limit_ns);
