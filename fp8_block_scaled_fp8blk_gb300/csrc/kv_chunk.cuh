@@ -426,6 +426,12 @@ __device__ __noinline__ bool ch_wait_brief(uint32_t at, uint32_t parity, uint64_
     return true;
 }
 
+// Whether no role has given up.  One that has goes on arriving at the barriers that are a unit's (unit_done, last_full,
+// merged), so after a wait at one of those a whole warp asks here: what it waited for may be an arrival of a later unit.
+__device__ __forceinline__ bool ch_alive(const ChunkShared &sh) {
+    return __all_sync(0xFFFFFFFFu, *reinterpret_cast<const volatile int *>(&sh.abort) == 0);
+}
+
 // The u-th unit, for a warp; false after the last one.
 __device__ __forceinline__ bool ch_unit(ChunkShared &sh, int u, int lane, ChunkUnit &x) {
     const int slot = u & (kChUnits - 1);
@@ -734,10 +740,12 @@ __device__ __forceinline__ void ch_convert(const ChunkArgs &a, ChunkShared &sh, 
         // The unit's queries, once the MMAs have read the last one's, and the softmax has written out the one before that.
         const ChunkQueries<Sh, T> queries(a, w, sq, sh.qs[ub], warp, lane);
         ok = (unit < 1 || ch_wait(a, sh, sh.q_free, static_cast<uint32_t>(unit - 1) & 1u)) &&
-             (unit < 2 || ch_wait(a, sh, sh.unit_done[ub], static_cast<uint32_t>((unit >> 1) - 1) & 1u));
-        if (ok) queries.copy();
-        sh.vnan[ub][tid] = kChNoNan;
-        if (tid == 0) sh.any_nan[ub] = 0;
+             (unit < 2 || (ch_wait(a, sh, sh.unit_done[ub], static_cast<uint32_t>((unit >> 1) - 1) & 1u) && ch_alive(sh)));
+        if (ok) {
+            queries.copy();
+            sh.vnan[ub][tid] = kChNoNan;
+            if (tid == 0) sh.any_nan[ub] = 0;
+        }
         asm volatile("bar.sync 4, %0;" ::"n"(kThreads) : "memory");
         if (!ok) continue;
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -1026,7 +1034,7 @@ __device__ __forceinline__ void ch_finish(const ChunkArgs &a, const ChunkUnit &w
     const float nanf = __int_as_float(0x7FC00000);
     const int ub = unit & 1;
     // The converters' word on what is NaN.
-    ok = ok && ch_wait(a, sh, sh.values_done[ub], static_cast<uint32_t>(unit >> 1) & 1u);
+    ok = ok && ch_wait(a, sh, sh.values_done[ub], static_cast<uint32_t>(unit >> 1) & 1u) && ch_alive(sh);
     const bool starts = w.flags & kChStarts, whole = starts && (w.flags & kChEnds);
     const float M = both ? fmaxf(x.M, y.M) : x.M;
     float l = both ? x.l * at_exp2(x.M - M) + y.l * at_exp2(y.M - M) : x.l, f = 1.f;
@@ -1330,7 +1338,7 @@ __device__ __forceinline__ void ch_softmax(const ChunkArgs &a, ChunkShared &sh, 
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&sh.last_full[ub]));
             // The sums stay as they are until the first product has taken them.
-            if (!Sh::SUMS) ok = ok && ch_wait(a, sh, sh.merged, static_cast<uint32_t>(shared) & 1u);
+            if (!Sh::SUMS) ok = ok && ch_wait(a, sh, sh.merged, static_cast<uint32_t>(shared) & 1u) && ch_alive(sh);
         } else {
             if (!alone) {
                 ok = ok && ch_wait(a, sh, sh.last_full[ub], static_cast<uint32_t>((ub == 0 ? shared0 : shared1)) & 1u);
