@@ -52,11 +52,11 @@
 // one product at work).
 //
 // Measured, calls in a row, the cache not in L2:
-//   4096 rows at the end of 16384 tokens, 64 / 8 heads of 128, bf16    2.06 ms, 935 TFLOP/s, 48% of the matrix rate
-//   512 rows of 8192 tokens, the same heads                            180 us, 740 TFLOP/s, 38%
+//   4096 rows at the end of 16384 tokens, 64 / 8 heads of 128, bf16    2.04 ms, 944 TFLOP/s, 49% of the matrix rate
+//   512 rows of 8192 tokens, the same heads                            178 us, 748 TFLOP/s, 39%
 //   16 rows of 65536 tokens, 32 / 8 heads, bf16                        82 us, 1.64 TB/s, 24% of the copy rate
-//   8 ragged prompts of up to 1024 tokens, 32 / 8 heads, f32           229 us, 133 TFLOP/s, 14% of the rate at two planes
-//   8 prompts of 1024, the same heads, bf16; f32                       185 us, 19%; 442 us, 16%
+//   8 ragged prompts of up to 1024 tokens, 32 / 8 heads, f32           231 us, 132 TFLOP/s, 14% of the rate at two planes
+//   8 prompts of 1024, the same heads, bf16; f32                       183 us, 19%; 447 us, 16%
 //   16 prompts of 700, 8 / 2 heads of 256, bf16; f32                   138 us, 12%; 224 us, 15%
 //   9 requests of up to 2001 tokens, 15 / 3 heads of 80, bf16          55 us
 // Long calls are bound by a tile's chain: scores, softmax, weights' MMA.  256 rows x

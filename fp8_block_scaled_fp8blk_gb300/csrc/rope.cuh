@@ -123,8 +123,8 @@ __device__ __forceinline__ void rope_item(const RopeArgs &r, uint32_t item) {
         return;
     }
     // Any start, part and alignment: a pair, or a value outside the part.  (Bound by its narrow loads and stores: 16384 bf16
-    // rows of 64 heads of 80, 40 of each rotated, 347 us, 14% of the copy rate, and 75 us with 48, by the units above; 24 of
-    // 96 452 us, 13%; f32, 32 heads of 80, 40 of each, 237 us, 21%.)
+    // rows of 64 heads of 80, 40 of each rotated, 342 us, 15% of the copy rate, and 74 us with 48, by the units above; 24 of
+    // 96 444 us, 13%; f32, 32 heads of 80, 40 of each, 228 us, 22%.)
     for (int h = 0; h < HEADS && h0 + h < r.heads; ++h, x += r.dim, out += r.dim) {
         if (u < half) {
             const int at = r.start + (r.interleaved ? 2 * u : u), bt = r.interleaved ? at + 1 : at + half;

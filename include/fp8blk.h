@@ -580,11 +580,11 @@ size_t fp8blk_kv_attn_chunk_ws_bytes(int q_heads, int kv_heads, int head_dim);
  * Rows of a CTA that gave up on a wait are NaN in out and lse (see
  * fp8blk_set_wait_limit).
  * For up to FP8BLK_MAX_M rows a request fp8blk_kv_attn is the faster one (64
- * requests of 8192 tokens, one row: 164 against 484 us), but for 8 rows of bf16
- * with 8 query heads a cache head (16 requests of 8192: 183 against 144 us).  So
+ * requests of 8192 tokens, one row: 167 against 495 us), but for 8 rows of bf16
+ * with 8 query heads a cache head (16 requests of 8192: 183 against 145 us).  So
  * a step of decoded rows and a chunk is best two calls, by slices of q, out,
  * block_table and seq_lens (63 requests of one row and one of 512, 8192 tokens
- * each: 356 us, 778 in one call).
+ * each: 356 us, 790 in one call).
  * Errors: EINVAL, EALIGN, EWS, ERANGE (as fp8blk_kv_attn, and 2^31 (row, query
  * head of a cache head) pairs), ECUDA.
  */
